@@ -244,3 +244,15 @@ def decompress(comp, dtype, n: int, stream=None, out=None, status=None, check: b
         if st != UZIP_OK:
             raise UzipError(st, "uzip_decompress (device)")
     return out
+
+
+# ---- matrix products over these tensors -------------------------------------
+
+from .ops import (  # noqa: E402
+    cross_entropy,
+    cross_entropy_backward,
+    grouped_linear,
+    grouped_linear_backward,
+    linear,
+    linear_backward,
+)

@@ -31,6 +31,10 @@ AddrRangeFn addr_range_fn() {
     return fn;
 }
 
+}  // namespace
+
+namespace uzip {
+
 // [p, p + bytes) must be device-accessible memory.  Device allocations are
 // checked against the allocation that holds p; mapped host memory is accepted
 // by type (its extent is not known to the driver query).
@@ -53,9 +57,6 @@ bool device_range_ok(const void* p, uint64_t bytes) {
     return start <= size && bytes <= size - start;
 }
 
-}  // namespace
-
-namespace uzip {
 namespace {
 struct ShapeEntry {
     int dev;

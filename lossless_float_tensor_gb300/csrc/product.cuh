@@ -1,0 +1,176 @@
+// Definitions shared by the matrix-product sources: the description of one
+// product C = A B^T (sums in 32 bits) with its epilogue, and the element-wise
+// arithmetic of the epilogues.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "../../include/uzip_ops.h"
+#include "uzip_internal.cuh"
+
+namespace uzip {
+
+// ---- one product ------------------------------------------------------------
+
+// An operand of `rows` x `depth` values (depth is the summed dimension).
+// depth_major: a row's values are contiguous and rows are ld apart; else the
+// rows of one depth index are contiguous and depths are ld apart.  Group g
+// starts group * g elements further.
+struct Operand {
+    const void* p;
+    uint64_t ld, group;
+    uint32_t depth_major;
+};
+
+enum Schedule : uint32_t {
+    kDense = 0,  // one product
+    kRows = 1,   // the rows of A and C are cut by the offsets, B belongs to the group
+    kDepth = 2   // the depth is cut by the offsets, C[group] = A_g B_g^T
+};
+
+enum EpilogueKind : uint32_t {
+    kStore = 0,      // C = act(alpha acc + bias) + residual + sum so far, 16- or 32-bit
+    kLossStats = 1,  // running maximum and sum of exponentials of each row, target logits
+    kLossGrad = 2    // C = g (softmax - [target])
+};
+
+struct StoreEpilogue {
+    void* out;
+    uint64_t ldo, out_group;
+    const void* bias;  // dtype, [groups, n]
+    const void* residual;
+    uint64_t ldr;
+    void* z;
+    uint64_t ldz;
+    const float* sum_in;  // fp32 partial results to add, nullable
+    uint64_t ld_sum;
+    const float* alpha;  // device scalar on the products' sum, nullable
+    uint32_t act;
+    uint32_t out_fp32;
+};
+
+struct LossEpilogue {
+    const int64_t* targets;
+    int64_t ignore;
+    uint64_t col0;     // class of column 0
+    float2* part;      // kLossStats: [column tiles][rows] maximum, sum
+    float* hit;        // kLossStats: [rows] logit of the target
+    const float* lse;  // kLossGrad
+    const float* g;    // kLossGrad: [rows], scaled
+    void* out;         // kLossGrad: dtype [rows, ldo]
+    uint64_t ldo;
+};
+
+struct Product {
+    Operand a, b;
+    uint64_t m, n, depth;  // kRows: m over all groups; kDepth: depth over all groups
+    uint32_t schedule, epilogue;
+    uint32_t groups;  // 1 for kDense
+    const int64_t* offsets;
+    // kDense: bit i of word j set = depth 64 j + i adds nothing, whatever the operands hold there (nullable)
+    const uint64_t* skip_depth;
+    StoreEpilogue st;
+    LossEpilogue ls;
+    int dtype;
+    int32_t* status;
+};
+
+// columns of the tiles in which launch_product takes p (kLossStats partials)
+uint32_t product_tile_columns(const Product& p, int sms);
+cudaError_t launch_product(const Product& p, cudaStream_t s);
+
+// ---- steps around the products (product_steps.cu) ---------------------------
+
+// rows x cols values of each of `groups` matrices copied to rows ld_to apart
+cudaError_t launch_pack_rows(const void* from, uint64_t ld, uint64_t group, void* to, uint64_t ld_to, uint64_t rows,
+                             uint64_t cols, uint64_t groups, cudaStream_t s);
+
+// dz = dy act'(z) into dz (nullable) and its column sums into db (nullable)
+struct ActGrad {
+    const void* dy;
+    uint64_t lddy;
+    const void* z;
+    uint64_t ldz;
+    void* dz;
+    uint64_t lddz;
+    void* db;
+    float* part;  // [groups][splits][n] where splits > 1
+    uint64_t m, n;
+    uint32_t groups, splits;
+    const int64_t* offsets;  // nullable: one group of all rows
+    uint32_t act;
+    int dtype;
+};
+uint32_t act_grad_splits(uint64_t m, uint64_t n, uint64_t groups);
+cudaError_t launch_act_grad(const ActGrad& a, cudaStream_t s);
+
+// status and NaN outputs for offsets that do not cut [0, m)
+struct OffsetCheck {
+    const int64_t* offsets;
+    uint64_t groups, m;
+    void* out[4];
+    uint64_t rows[4], cols[4], ld[4], group[4], count[4];
+    int dtype;
+    int32_t* status;
+};
+cudaError_t launch_offset_check(const OffsetCheck& c, cudaStream_t s);
+
+cudaError_t launch_loss_join(const LossEpilogue& e, uint64_t t, uint64_t v, uint32_t tiles, float* loss, float* lse,
+                             int32_t* status, cudaStream_t s);
+// scale[0] = a power of two that brings the largest |dloss| to [2^10, 2^11),
+// scale[1] = its reciprocal; g = scaled dloss, 0 for ignored tokens
+cudaError_t launch_loss_weights(const float* dloss, const int64_t* targets, int64_t ignore, uint64_t t, uint64_t v,
+                                float* scale, float* g, int32_t* status, cudaStream_t s);
+// skip word per 64 tokens: ignored tokens whose h row is not finite
+cudaError_t launch_skip_words(const void* h, uint64_t ldh, const int64_t* targets, int64_t ignore, uint64_t t,
+                              uint64_t d, int dtype, uint64_t* words, cudaStream_t s);
+cudaError_t launch_fill(void* p, uint64_t ld, uint64_t rows, uint64_t cols, uint32_t elem, cudaStream_t s);
+
+// ---- arithmetic ---------------------------------------------------------------
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kSqrtHalf = 0.70710678118654752f;
+constexpr float kInvSqrt2Pi = 0.39894228040143268f;
+
+__device__ __forceinline__ float from16(uint16_t b, int dtype) {
+    return dtype == UZIP_BF16 ? __uint_as_float(uint32_t(b) << 16) : __half2float(__ushort_as_half(b));
+}
+__device__ __forceinline__ uint16_t to16(float v, int dtype) {
+    return dtype == UZIP_BF16 ? __bfloat16_as_ushort(__float2bfloat16_rn(v)) : __half_as_ushort(__float2half_rn(v));
+}
+// two values in one word, the first in the low half
+__device__ __forceinline__ float2 from16x2(uint32_t w, int dtype) {
+    if (dtype == UZIP_BF16) return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+    return __half22float2(*reinterpret_cast<const __half2*>(&w));
+}
+__device__ __forceinline__ uint32_t to16x2(float lo, float hi, int dtype) {
+    if (dtype == UZIP_BF16) {
+        const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+        return *reinterpret_cast<const uint32_t*>(&v);
+    }
+    const __half2 v = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+__device__ __forceinline__ float act_value(float z, uint32_t act) {
+    switch (act) {
+        case UZIP_ACT_RELU: return z > 0.f || z != z ? z : 0.f;
+        case UZIP_ACT_GELU: return 0.5f * z * (1.f + erff(z * kSqrtHalf));
+        case UZIP_ACT_SILU: return __fdividef(z, 1.f + __expf(-z));
+        default: return z;
+    }
+}
+__device__ __forceinline__ float act_slope(float z, uint32_t act) {
+    switch (act) {
+        case UZIP_ACT_RELU: return z > 0.f ? 1.f : (z != z ? z : 0.f);
+        case UZIP_ACT_GELU: return 0.5f * (1.f + erff(z * kSqrtHalf)) + z * __expf(-0.5f * z * z) * kInvSqrt2Pi;
+        case UZIP_ACT_SILU: {
+            const float q = __fdividef(1.f, 1.f + __expf(-z));
+            return q * (1.f + z * (1.f - q));
+        }
+        default: return 1.f;
+    }
+}
+
+}  // namespace uzip

@@ -1,0 +1,312 @@
+// The element-wise steps around the matrix products: row packing, the
+// activation's gradient with the bias gradient, the checks of offsets and
+// targets, and the joining of the loss statistics.  All of them read and
+// write each value once and are bound by memory bandwidth or launch latency.
+#include <algorithm>
+
+#include "product.cuh"
+
+namespace uzip {
+namespace {
+
+constexpr uint32_t kThreads = 256;
+
+uint32_t blocks_for(uint64_t items, uint64_t most) {
+    return uint32_t(std::max<uint64_t>(1, std::min<uint64_t>((items + kThreads - 1) / kThreads, most)));
+}
+
+// Rows copied to rows on 16-byte boundaries; the last values of a padded row
+// are zero.  One thread makes one 16-byte store from eight 2-byte loads.
+__global__ void __launch_bounds__(kThreads) pack_kernel(const uint16_t* from, uint64_t ld, uint64_t group, uint4* to,
+                                                        uint64_t vecs, uint64_t rows, uint64_t cols, uint64_t total) {
+    for (uint64_t i = blockIdx.x * uint64_t(kThreads) + threadIdx.x; i < total; i += uint64_t(gridDim.x) * kThreads) {
+        const uint64_t v = i % vecs, r = i / vecs, g = r / rows, row = r - g * rows;
+        const uint16_t* src = from + g * group + row * ld + 8 * v;
+        uint32_t w[4];
+#pragma unroll
+        for (uint32_t j = 0; j < 4; ++j) {
+            const uint32_t lo = 8 * v + 2 * j < cols ? src[2 * j] : 0u;
+            const uint32_t hi = 8 * v + 2 * j + 1 < cols ? src[2 * j + 1] : 0u;
+            w[j] = lo | hi << 16;
+        }
+        to[i] = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads) fill_kernel(T* p, uint64_t ld, uint64_t cols, uint64_t total, T value) {
+    for (uint64_t i = blockIdx.x * uint64_t(kThreads) + threadIdx.x; i < total; i += uint64_t(gridDim.x) * kThreads)
+        p[i / cols * ld + i % cols] = value;
+}
+
+// Block (x, y, z): 128 columns, a share of the rows, one group.  A thread
+// holds 8 columns and walks every 16th row; the 16 partial column sums meet in
+// shared memory in a fixed order.
+constexpr uint32_t kGradCols = 128, kGradRows = 16;
+
+__device__ __forceinline__ void load8(const uint16_t* p, bool vec, uint32_t cols, int dtype, float v[8]) {
+    uint32_t w[4] = {};
+    if (vec) {
+        const uint4 q = *reinterpret_cast<const uint4*>(p);
+        w[0] = q.x, w[1] = q.y, w[2] = q.z, w[3] = q.w;
+    } else {
+#pragma unroll
+        for (uint32_t j = 0; j < 8; ++j)
+            if (j < cols) w[j / 2] |= uint32_t(p[j]) << (j % 2 * 16);
+    }
+#pragma unroll
+    for (uint32_t j = 0; j < 4; ++j) {
+        const float2 f = from16x2(w[j], dtype);
+        v[2 * j] = f.x, v[2 * j + 1] = f.y;
+    }
+}
+
+__global__ void __launch_bounds__(kThreads) act_grad_kernel(const __grid_constant__ ActGrad a) {
+    __shared__ float sums[kGradRows][kGradCols + 4];
+    const uint32_t tx = threadIdx.x % 16, ty = threadIdx.x / 16, g = blockIdx.z;
+    const uint64_t col = uint64_t(blockIdx.x) * kGradCols + 8 * tx;
+    uint64_t r0 = 0, r1 = a.m;
+    if (a.offsets) {
+        const int64_t lo = a.offsets[g], hi = a.offsets[g + 1];
+        const bool good = lo >= 0 && lo <= hi && hi <= int64_t(a.m);  // else reported by the offset check
+        r0 = good ? lo : 0, r1 = good ? hi : 0;
+    }
+    const uint64_t share = (r1 - r0 + a.splits - 1) / a.splits;
+    r0 = min(r0 + blockIdx.y * share, r1);
+    r1 = min(r0 + share, r1);
+    float sum[8] = {};
+    if (col < a.n) {
+        const uint32_t cols = uint32_t(min(uint64_t(8), a.n - col));
+        const uint16_t* dy = static_cast<const uint16_t*>(a.dy) + col;
+        const uint16_t* z = static_cast<const uint16_t*>(a.z) + col;
+        uint16_t* dz = static_cast<uint16_t*>(a.dz) + col;
+        const bool vy = cols == 8 && a.lddy % 8 == 0 && reinterpret_cast<uintptr_t>(a.dy) % 16 == 0;
+        const bool vz = cols == 8 && a.ldz % 8 == 0 && reinterpret_cast<uintptr_t>(a.z) % 16 == 0;
+        for (uint64_t r = r0 + ty; r < r1; r += kGradRows) {
+            float d[8], f[8];
+            load8(dy + r * a.lddy, vy, cols, a.dtype, d);
+            if (a.act != UZIP_ACT_NONE) {
+                load8(z + r * a.ldz, vz, cols, a.dtype, f);
+#pragma unroll
+                for (uint32_t j = 0; j < 8; ++j) d[j] *= act_slope(f[j], a.act);
+            }
+#pragma unroll
+            for (uint32_t j = 0; j < 8; ++j) sum[j] += d[j];
+            if (a.dz) {  // rows of the work area: padded to 16 bytes
+                uint4 q;
+                q.x = to16x2(d[0], d[1], a.dtype), q.y = to16x2(d[2], d[3], a.dtype);
+                q.z = to16x2(d[4], d[5], a.dtype), q.w = to16x2(d[6], d[7], a.dtype);
+                *reinterpret_cast<uint4*>(dz + r * a.lddz) = q;
+            }
+        }
+    }
+    if (!a.db) return;
+#pragma unroll
+    for (uint32_t j = 0; j < 8; ++j) sums[ty][8 * tx + j] = sum[j];
+    __syncthreads();
+    const uint64_t c = uint64_t(blockIdx.x) * kGradCols + threadIdx.x;
+    if (threadIdx.x < kGradCols && c < a.n) {
+        float total = 0.f;
+#pragma unroll
+        for (uint32_t i = 0; i < kGradRows; ++i) total += sums[i][threadIdx.x];
+        if (a.splits > 1) a.part[(uint64_t(g) * a.splits + blockIdx.y) * a.n + c] = total;
+        else static_cast<uint16_t*>(a.db)[g * a.n + c] = to16(total, a.dtype);
+    }
+}
+
+__global__ void __launch_bounds__(kThreads) join_columns_kernel(const float* part, uint32_t splits, uint64_t n,
+                                                                uint64_t total, uint16_t* db, int dtype) {
+    const uint64_t i = blockIdx.x * uint64_t(kThreads) + threadIdx.x;
+    if (i >= total) return;
+    const uint64_t g = i / n, c = i - g * n;
+    float v = 0.f;
+    for (uint32_t s = 0; s < splits; ++s) v += part[(g * splits + s) * n + c];
+    db[i] = to16(v, dtype);
+}
+
+// Every block reads the offsets (8 KiB at most); all of them fill the outputs
+// with NaN where the offsets do not cut [0, m).
+__global__ void __launch_bounds__(kThreads) offset_check_kernel(const __grid_constant__ OffsetCheck c) {
+    bool bad = false;
+    for (uint64_t i = threadIdx.x; i <= c.groups; i += kThreads) {
+        const int64_t v = c.offsets[i];
+        bad |= v < 0 || v > int64_t(c.m) || (i == 0 && v != 0) || (i == c.groups ? v != int64_t(c.m) : v > c.offsets[i + 1]);
+    }
+    if (!__syncthreads_or(bad)) return;
+    if (blockIdx.x == 0 && threadIdx.x == 0 && c.status) atomicCAS(c.status, 0, int(UZIP_ERR_INVALID_ARG));
+    const uint16_t nan = c.dtype == UZIP_BF16 ? 0x7FC0 : 0x7E00;
+    for (uint32_t k = 0; k < 4; ++k) {
+        if (!c.out[k]) continue;
+        const uint64_t total = c.count[k] * c.rows[k] * c.cols[k];
+        for (uint64_t i = blockIdx.x * uint64_t(kThreads) + threadIdx.x; i < total; i += uint64_t(gridDim.x) * kThreads) {
+            const uint64_t r = i / c.cols[k], col = i % c.cols[k], g = r / c.rows[k];
+            static_cast<uint16_t*>(c.out[k])[g * c.group[k] + (r - g * c.rows[k]) * c.ld[k] + col] = nan;
+        }
+    }
+}
+
+// One row's tile maxima and sums joined in tile order: 32 rows x 8 threads
+// each, thread (x, y) takes tiles y, y + 8, ...
+__global__ void __launch_bounds__(kThreads) loss_join_kernel(LossEpilogue e, uint64_t t, uint64_t v, uint32_t tiles,
+                                                             float* loss, float* lse, int32_t* status) {
+    __shared__ float2 s[8][32];
+    const uint32_t x = threadIdx.x % 32, y = threadIdx.x / 32;
+    const uint64_t row = uint64_t(blockIdx.x) * 32 + x;
+    float top = -INFINITY, sum = 0.f;
+    bool nan = false;
+    if (row < t)
+        for (uint32_t i = y; i < tiles; i += 8) {
+            const float2 q = e.part[uint64_t(i) * t + row];
+            nan |= q.y != q.y;
+            const float next = fmaxf(top, q.x);
+            if (next == -INFINITY) continue;
+            sum = sum * exp2f((top - next) * kLog2e) + q.y * exp2f((q.x - next) * kLog2e);
+            top = next;
+        }
+    s[y][x] = make_float2(top, nan ? NAN : sum);
+    __syncthreads();
+    if (y != 0 || row >= t) return;
+    for (uint32_t i = 1; i < 8; ++i) {
+        const float2 q = s[i][x];
+        const float next = fmaxf(top, q.x);
+        nan |= q.y != q.y;
+        if (next == -INFINITY) continue;
+        sum = sum * exp2f((top - next) * kLog2e) + q.y * exp2f((q.x - next) * kLog2e);
+        top = next;
+    }
+    const int64_t target = e.targets[row];
+    const float l = nan ? NAN : top + logf(sum);
+    if (target == e.ignore) {
+        loss[row] = 0.f;
+        lse[row] = 0.f;
+        return;
+    }
+    lse[row] = l;
+    if (target < 0 || target >= int64_t(v)) {
+        loss[row] = NAN;
+        if (status) atomicCAS(status, 0, int(UZIP_ERR_INVALID_ARG));
+        return;
+    }
+    loss[row] = l - e.hit[row];
+}
+
+// One block: the largest finite weight, then its power of two.
+__global__ void __launch_bounds__(1024) loss_weights_kernel(const float* dloss, const int64_t* targets, int64_t ignore,
+                                                            uint64_t t, uint64_t v, float* scale, float* g,
+                                                            int32_t* status) {
+    __shared__ float tops[32];
+    float top = 0.f;
+    for (uint64_t i = threadIdx.x; i < t; i += 1024)
+        if (targets[i] != ignore && fabsf(dloss[i]) < INFINITY) top = fmaxf(top, fabsf(dloss[i]));
+#pragma unroll
+    for (uint32_t o = 16; o; o /= 2) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+    if (threadIdx.x % 32 == 0) tops[threadIdx.x / 32] = top;
+    __syncthreads();
+    top = tops[threadIdx.x % 32];
+#pragma unroll
+    for (uint32_t o = 16; o; o /= 2) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+    int power = top > 0.f ? 10 - ilogbf(top) : 0;
+    power = max(-110, min(110, power));
+    const float up = exp2f(float(power));
+    if (threadIdx.x == 0) {
+        scale[0] = up;
+        scale[1] = exp2f(float(-power));
+    }
+    for (uint64_t i = threadIdx.x; i < t; i += 1024) {
+        const int64_t target = targets[i];
+        float w = target == ignore ? 0.f : dloss[i] * up;
+        if (target != ignore && (target < 0 || target >= int64_t(v))) {
+            w = NAN;
+            if (status) atomicCAS(status, 0, int(UZIP_ERR_INVALID_ARG));
+        }
+        g[i] = w;
+    }
+}
+
+// One block for each word of 64 tokens; a warp reads one ignored row at a time.
+__global__ void __launch_bounds__(kThreads) skip_words_kernel(const uint16_t* h, uint64_t ldh, const int64_t* targets,
+                                                              int64_t ignore, uint64_t t, uint64_t d, int dtype,
+                                                              uint64_t* words) {
+    __shared__ uint32_t half[2];
+    if (threadIdx.x < 2) half[threadIdx.x] = 0;
+    __syncthreads();
+    const uint32_t lane = threadIdx.x % 32;
+    const uint16_t infinite = dtype == UZIP_BF16 ? 0x7F80 : 0x7C00;
+    for (uint32_t i = threadIdx.x / 32; i < 64; i += kThreads / 32) {
+        const uint64_t row = uint64_t(blockIdx.x) * 64 + i;
+        if (row >= t || targets[row] != ignore) continue;
+        bool odd = false;
+        for (uint64_t c = lane; c < d; c += 32) odd |= (h[row * ldh + c] & infinite) == infinite;
+        if (__any_sync(0xFFFFFFFFu, odd) && lane == 0) atomicOr(&half[i / 32], 1u << (i % 32));
+    }
+    __syncthreads();
+    if (threadIdx.x == 0) words[blockIdx.x] = uint64_t(half[0]) | uint64_t(half[1]) << 32;
+}
+
+}  // namespace
+
+cudaError_t launch_pack_rows(const void* from, uint64_t ld, uint64_t group, void* to, uint64_t ld_to, uint64_t rows,
+                             uint64_t cols, uint64_t groups, cudaStream_t s) {
+    const uint64_t vecs = ld_to / 8, total = vecs * rows * groups;
+    if (total == 0) return cudaSuccess;
+    pack_kernel<<<blocks_for(total, 152 * 32), kThreads, 0, s>>>(static_cast<const uint16_t*>(from), ld, group,
+                                                                 static_cast<uint4*>(to), vecs, rows, cols, total);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_fill(void* p, uint64_t ld, uint64_t rows, uint64_t cols, uint32_t elem, cudaStream_t s) {
+    const uint64_t total = rows * cols;
+    if (total == 0) return cudaSuccess;
+    if (elem == 2)
+        fill_kernel<<<blocks_for(total, 152 * 32), kThreads, 0, s>>>(static_cast<uint16_t*>(p), ld, cols, total, uint16_t(0));
+    else
+        fill_kernel<<<blocks_for(total, 152 * 32), kThreads, 0, s>>>(static_cast<float*>(p), ld, cols, total, 0.f);
+    return cudaGetLastError();
+}
+
+// Blocks enough to fill the GPU four times over, a share of at least 64 rows.
+uint32_t act_grad_splits(uint64_t m, uint64_t n, uint64_t groups) {
+    const uint64_t have = (n + kGradCols - 1) / kGradCols * groups;
+    const uint64_t want = std::max<uint64_t>(1, 152 * 4 / std::max<uint64_t>(1, have));
+    return uint32_t(std::max<uint64_t>(1, std::min(want, m / groups / 64)));
+}
+
+cudaError_t launch_act_grad(const ActGrad& a, cudaStream_t s) {
+    if (a.n == 0) return cudaSuccess;
+    const dim3 grid(uint32_t((a.n + kGradCols - 1) / kGradCols), a.splits, a.groups);
+    act_grad_kernel<<<grid, kThreads, 0, s>>>(a);
+    cudaError_t err = cudaGetLastError();
+    if (err == cudaSuccess && a.db && a.splits > 1) {
+        const uint64_t total = uint64_t(a.groups) * a.n;
+        join_columns_kernel<<<uint32_t((total + kThreads - 1) / kThreads), kThreads, 0, s>>>(
+            a.part, a.splits, a.n, total, static_cast<uint16_t*>(a.db), a.dtype);
+        err = cudaGetLastError();
+    }
+    return err;
+}
+
+cudaError_t launch_offset_check(const OffsetCheck& c, cudaStream_t s) {
+    offset_check_kernel<<<152, kThreads, 0, s>>>(c);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_loss_join(const LossEpilogue& e, uint64_t t, uint64_t v, uint32_t tiles, float* loss, float* lse,
+                             int32_t* status, cudaStream_t s) {
+    loss_join_kernel<<<uint32_t((t + 31) / 32), kThreads, 0, s>>>(e, t, v, tiles, loss, lse, status);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_loss_weights(const float* dloss, const int64_t* targets, int64_t ignore, uint64_t t, uint64_t v,
+                                float* scale, float* g, int32_t* status, cudaStream_t s) {
+    loss_weights_kernel<<<1, 1024, 0, s>>>(dloss, targets, ignore, t, v, scale, g, status);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_skip_words(const void* h, uint64_t ldh, const int64_t* targets, int64_t ignore, uint64_t t,
+                              uint64_t d, int dtype, uint64_t* words, cudaStream_t s) {
+    skip_words_kernel<<<uint32_t((t + 63) / 64), kThreads, 0, s>>>(static_cast<const uint16_t*>(h), ldh, targets,
+                                                                   ignore, t, d, dtype, words);
+    return cudaGetLastError();
+}
+
+}  // namespace uzip
