@@ -1,109 +1,735 @@
-// C = A B^T with a fused epilogue, the plain way: 64 x 64 tiles of C per
-// block, 4 x 4 values per thread, operands staged through shared memory and
-// multiplied in 32 bits.
+// C = A B^T on the tensor cores, with a fused epilogue.
+//
+// A block (or a pair of blocks on two SMs) owns one tile of C at a time and
+// walks the tiles of the launch.  Three roles run at once: one thread fetches
+// 64 depths of both operands at a time with TMA into a ring of shared-memory
+// stages, one thread multiplies them with tcgen05.mma into TMEM, and four
+// warps turn a finished accumulator (one TMEM lane per row) into the result
+// while the next tile is multiplied into the other half of TMEM.
+//
+// Operands may be contiguous along the depth or along the rows: the tensor
+// core reads both from the 128-byte swizzled layout that TMA writes, so the
+// transposed products of the gradients need no copy.
+#include <cuda.h>
+
+#include <algorithm>
+#include <atomic>
+#include <cmath>
+
 #include "product.cuh"
 
 namespace uzip {
 namespace {
 
-constexpr uint32_t kTile = 64, kStep = 16;
+constexpr uint32_t kRowsTile = 128;  // accumulator rows of a block: the TMEM lanes
+constexpr uint32_t kDepthTile = 64;  // depths of a stage: 128 bytes, the swizzle's span
+constexpr uint32_t kSliceBytes = kDepthTile * 128;  // 64 rows x 64 depths when rows are contiguous
+constexpr uint32_t kAStage = kRowsTile * kDepthTile * 2;
+constexpr uint32_t kMaxStages = 12;
+constexpr uint32_t kThreads = 192;  // TMA warp, MMA warp, four epilogue warps
+constexpr uint32_t kWaitLimit = 1u << 22;  // tries of a bounded wait (up to about 1 us each)
 
-__device__ __forceinline__ float load_value(const Operand& o, uint32_t g, uint64_t row, uint64_t depth, int dtype) {
-    const uint64_t at = g * o.group + (o.depth_major ? row * o.ld + depth : depth * o.ld + row);
-    return from16(static_cast<const uint16_t*>(o.p)[at], dtype);
+struct Tiling {
+    uint32_t bn;       // columns of a tile
+    uint32_t stages;
+    uint32_t stage_bytes;
+    uint32_t splits;   // blocks of a cluster that share a tile's depth
+    uint32_t pair;     // two blocks share a tile of 256 rows
+    uint32_t a_box;    // rows of one TMA box of A (depth-major)
+    uint32_t raster;   // row tiles taken together for the sake of L2
+    uint32_t tmem_cols;
+    uint32_t idesc;
+    uint32_t smem;
+    uint32_t vec;      // bit flags: 16-byte access to out 1, bias 2, residual 4, z 8, sums 16
+};
+
+// ---- PTX ------------------------------------------------------------------------
+
+__device__ __forceinline__ uint64_t matrix_descriptor(uint32_t addr, bool depth_major) {
+    // start, distance between 64-row slices (rows contiguous), distance between
+    // groups of 8 swizzled 128-byte lines, version 1, 128-byte swizzle
+    const uint64_t lead = depth_major ? 1 : kSliceBytes / 16;
+    return uint64_t((addr & 0x3FFFF) >> 4) | lead << 16 | uint64_t(1024 / 16) << 32 | uint64_t(1) << 46 | uint64_t(2) << 61;
+}
+__device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap* map, int c0, int c1, int c2, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];"
+        ::"r"(dst), "l"(map), "r"(c0), "r"(c1), "r"(c2), "r"(bar)
+        : "memory");
+}
+__device__ __forceinline__ void mma(uint32_t tmem, uint64_t a, uint64_t b, uint32_t idesc, uint32_t add) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
+        ::"r"(tmem), "l"(a), "l"(b), "r"(idesc), "r"(add)
+        : "memory");
+}
+__device__ __forceinline__ void mma_commit(uint32_t bar) {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void tmem_alloc(uint32_t to, uint32_t cols) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(to), "r"(cols) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+}
+__device__ __forceinline__ void tmem_free(uint32_t addr, uint32_t cols) {
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(cols) : "memory");
+}
+__device__ __forceinline__ void tmem_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tmem_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+// 32 columns of this warp's 32 lanes; each lane gets its row
+__device__ __forceinline__ void tmem_load32(uint32_t addr, float v[32]) {
+    uint32_t r[32];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+          "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(addr));
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+    for (uint32_t i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+}
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t cluster_address(uint32_t addr, uint32_t rank) {
+    uint32_t r;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+    return r;
+}
+__device__ __forceinline__ float4 cluster_load4(uint32_t addr) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr));
+    return v;
 }
 
-__device__ __forceinline__ void store_value(const Product& p, uint32_t g, uint64_t row, uint64_t col, float acc) {
-    const StoreEpilogue& e = p.st;
-    if (e.alpha) acc *= *e.alpha;
-    if (e.sum_in) acc += e.sum_in[row * e.ld_sum + col];
-    if (e.bias) acc += from16(static_cast<const uint16_t*>(e.bias)[g * p.n + col], p.dtype);
-    if (e.z) static_cast<uint16_t*>(e.z)[row * e.ldz + col] = to16(acc, p.dtype);
-    acc = act_value(acc, e.act);
-    if (e.residual) acc += from16(static_cast<const uint16_t*>(e.residual)[row * e.ldr + col], p.dtype);
-    const uint64_t at = g * e.out_group + row * e.ldo + col;
-    if (e.out_fp32) static_cast<float*>(e.out)[at] = acc;
-    else static_cast<uint16_t*>(e.out)[at] = to16(acc, p.dtype);
+// ---- the block's shared state ------------------------------------------------------
+
+struct Control {
+    uint64_t full[kMaxStages], empty[kMaxStages];
+    uint64_t acc_full[2], acc_empty[2];
+    uint64_t drain;
+    uint32_t tmem;
+    volatile uint32_t abort;
+};
+// behind it, for the grouped schedules: int32 offsets[groups + 1], then (kRows)
+// first row tile of each group, int32 [groups + 1]
+
+__device__ __forceinline__ bool wait(Control* c, uint64_t* bar, uint32_t parity, uint32_t limit = kWaitLimit) {
+    const uint32_t b = smem_u32(bar);
+    for (uint32_t i = 0; i < limit; ++i) {
+        if (mbar_try_wait(b, parity)) return true;
+        if (i % 64 == 63 && c->abort) return false;
+    }
+    c->abort = 1;
+    return false;
 }
 
-__global__ void __launch_bounds__(256) product_kernel(const __grid_constant__ Product p) {
-    __shared__ float sa[kStep][kTile + 1], sb[kStep][kTile + 1], sc[kTile][kTile + 1];
-    const uint32_t tid = threadIdx.x, tx = tid % 16, ty = tid / 16, g = blockIdx.z;
-    uint64_t row0 = uint64_t(blockIdx.y) * kTile, row_end = p.m, d0 = 0, d_end = p.depth;
-    const uint64_t col0 = uint64_t(blockIdx.x) * kTile;
-    if (p.schedule != kDense) {
-        int64_t lo = p.offsets[g], hi = p.offsets[g + 1];
-        const int64_t top = p.schedule == kRows ? p.m : p.depth;
-        if (lo < 0 || hi > top || lo > hi) return;  // reported by the offset check
+// A tile of C: its group, first row and column, the end of its rows, and its depths.
+struct Tile {
+    uint32_t group, row0, row_end, col0, col_tile;
+    uint32_t d0, blocks, depth_end;
+};
+
+struct Walk {
+    const Product& p;
+    const Tiling& t;
+    const int32_t *offsets, *first;  // shared memory
+    uint32_t tile_rows, row_tiles, col_tiles, total, step, next, group, split;
+
+    __device__ Walk(const Product& p, const Tiling& t, const int32_t* offsets, const int32_t* first)
+        : p(p), t(t), offsets(offsets), first(first) {
+        tile_rows = kRowsTile;
+        col_tiles = (uint32_t(p.n) + t.bn - 1) / t.bn;
+        row_tiles = p.schedule == kRows ? uint32_t(first[p.groups]) : (uint32_t(p.m) + tile_rows - 1) / tile_rows;
+        total = row_tiles * col_tiles * (p.schedule == kDepth ? p.groups : 1);
+        step = gridDim.x / t.splits;
+        next = blockIdx.x / t.splits;
+        split = blockIdx.x % t.splits;
+        group = 0;
+    }
+    __device__ __forceinline__ bool take(Tile& o) {
+        if (next >= total) return false;
+        uint32_t id = next;
+        next += step;
+        o.group = 0;
+        o.d0 = 0;
+        o.depth_end = uint32_t(p.depth);
         if (p.schedule == kRows) {
-            row0 += lo;
-            row_end = hi;
+            while (uint32_t(first[group + 1]) * col_tiles <= id) ++group;
+            const uint32_t rows = first[group + 1] - first[group];
+            id -= first[group] * col_tiles;
+            o.group = group;
+            o.col_tile = id / rows;
+            o.row0 = offsets[group] + id % rows * kRowsTile;
+            o.row_end = offsets[group + 1];
         } else {
-            d0 = lo;
-            d_end = hi;
+            if (p.schedule == kDepth) {
+                const uint32_t per = row_tiles * col_tiles;
+                o.group = id / per;
+                id -= o.group * per;
+                o.d0 = offsets[o.group];
+                o.depth_end = offsets[o.group + 1];
+            }
+            const uint32_t band = id / (t.raster * col_tiles), in = id - band * t.raster * col_tiles;
+            const uint32_t rows = min(t.raster, row_tiles - band * t.raster);
+            o.row0 = (band * t.raster + in % rows) * tile_rows;
+            o.col_tile = in / rows;
+            o.row_end = uint32_t(p.m);
+        }
+        o.col0 = o.col_tile * t.bn;
+        o.blocks = (o.depth_end - o.d0 + kDepthTile - 1) / kDepthTile;
+        if (t.splits > 1) {
+            const uint32_t lo = o.blocks * split / t.splits, hi = o.blocks * (split + 1) / t.splits;
+            o.d0 += lo * kDepthTile;
+            o.blocks = hi - lo;
+        }
+        return true;
+    }
+};
+
+// ---- epilogues ------------------------------------------------------------------------
+
+// Up to 8 values of a row from 16-bit memory; vec: one 16-byte load.
+__device__ __forceinline__ void read8(const void* base, uint64_t at, bool vec, uint32_t cols, int dtype, float v[8]) {
+    const uint16_t* p = static_cast<const uint16_t*>(base) + at;
+    uint32_t w[4] = {};
+    if (vec && cols == 8) {
+        const uint4 q = *reinterpret_cast<const uint4*>(p);
+        w[0] = q.x, w[1] = q.y, w[2] = q.z, w[3] = q.w;
+    } else {
+#pragma unroll
+        for (uint32_t j = 0; j < 8; ++j)
+            if (j < cols) w[j / 2] |= uint32_t(p[j]) << (j % 2 * 16);
+    }
+#pragma unroll
+    for (uint32_t j = 0; j < 4; ++j) {
+        const float2 f = from16x2(w[j], dtype);
+        v[2 * j] = f.x, v[2 * j + 1] = f.y;
+    }
+}
+__device__ __forceinline__ void write8(void* base, uint64_t at, bool vec, uint32_t cols, int dtype, const float v[8]) {
+    uint16_t* p = static_cast<uint16_t*>(base) + at;
+    uint32_t w[4];
+#pragma unroll
+    for (uint32_t j = 0; j < 4; ++j) w[j] = to16x2(v[2 * j], v[2 * j + 1], dtype);
+    if (vec && cols == 8) {
+        *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+    } else {
+#pragma unroll
+        for (uint32_t j = 0; j < 8; ++j)
+            if (j < cols) p[j] = uint16_t(w[j / 2] >> (j % 2 * 16));
+    }
+}
+
+// kStore for `cols` (1 to 8) neighbouring values of a row.
+__device__ __forceinline__ void store8(const Product& p, uint32_t vec, uint32_t g, uint64_t row, uint32_t col,
+                                       uint32_t cols, float alpha, float v[8]) {
+    const StoreEpilogue& e = p.st;
+    float q[8];
+    if (e.alpha) {
+#pragma unroll
+        for (uint32_t j = 0; j < 8; ++j) v[j] *= alpha;
+    }
+    if (e.sum_in) {
+        const float* s = e.sum_in + row * e.ld_sum + col;
+        if ((vec & 16) && cols == 8) {
+            const float4 lo = *reinterpret_cast<const float4*>(s), hi = *reinterpret_cast<const float4*>(s + 4);
+            v[0] += lo.x, v[1] += lo.y, v[2] += lo.z, v[3] += lo.w, v[4] += hi.x, v[5] += hi.y, v[6] += hi.z, v[7] += hi.w;
+        } else {
+#pragma unroll
+            for (uint32_t j = 0; j < 8; ++j)
+                if (j < cols) v[j] += s[j];
         }
     }
-    if (row0 >= row_end) return;
-    float acc[4][4] = {};
-    for (uint64_t d = d0; d < d_end; d += kStep) {
-        for (uint32_t i = tid; i < kTile * kStep; i += 256) {
-            const uint32_t r = i / kStep, c = i % kStep;
-            bool on = d + c < d_end;
-            if (on && p.skip_depth) on = !((p.skip_depth[(d + c) / 64] >> ((d + c) % 64)) & 1);
-            sa[c][r] = on && row0 + r < row_end ? load_value(p.a, p.schedule == kDepth ? 0 : 0, row0 + r, d + c, p.dtype) : 0.f;
-            sb[c][r] = on && col0 + r < p.n ? load_value(p.b, p.schedule == kRows ? g : 0, col0 + r, d + c, p.dtype) : 0.f;
+    if (e.bias) {
+        read8(e.bias, g * p.n + col, vec & 2, cols, p.dtype, q);
+#pragma unroll
+        for (uint32_t j = 0; j < 8; ++j) v[j] += q[j];
+    }
+    if (e.z) write8(e.z, row * e.ldz + col, vec & 8, cols, p.dtype, v);
+    if (e.act != UZIP_ACT_NONE) {
+#pragma unroll
+        for (uint32_t j = 0; j < 8; ++j) v[j] = act_value(v[j], e.act);
+    }
+    if (e.residual) {
+        read8(e.residual, row * e.ldr + col, vec & 4, cols, p.dtype, q);
+#pragma unroll
+        for (uint32_t j = 0; j < 8; ++j) v[j] += q[j];
+    }
+    const uint64_t at = g * e.out_group + row * e.ldo + col;
+    if (!e.out_fp32) {
+        write8(e.out, at, vec & 1, cols, p.dtype, v);
+        return;
+    }
+    float* o = static_cast<float*>(e.out) + at;
+    if ((vec & 1) && cols == 8) {
+        reinterpret_cast<float4*>(o)[0] = make_float4(v[0], v[1], v[2], v[3]);
+        reinterpret_cast<float4*>(o)[1] = make_float4(v[4], v[5], v[6], v[7]);
+    } else {
+#pragma unroll
+        for (uint32_t j = 0; j < 8; ++j)
+            if (j < cols) o[j] = v[j];
+    }
+}
+
+// One finished accumulator: every lane of the four warps holds a row.
+template <int EPI>
+__device__ __forceinline__ void finish_tile(const Product& p, const Tiling& t, const Tile& o, uint32_t acc, uint32_t lane_row,
+                                            bool empty, float alpha) {
+    const uint64_t row = uint64_t(o.row0) + lane_row;
+    const bool live = row < o.row_end;
+    const uint32_t cols = min(t.bn, uint32_t(p.n) - o.col0);
+    float top = -INFINITY, sum = 0.f;
+    int64_t target = -1;
+    float lse2 = 0.f, weight = 0.f;
+    if (EPI != kStore && live) {
+        target = p.ls.targets[row] - int64_t(p.ls.col0 + o.col0);
+        if (EPI == kLossGrad) {
+            lse2 = p.ls.lse[row] * kLog2e;
+            weight = p.ls.g[row];
         }
-        __syncthreads();
-        for (uint32_t c = 0; c < kStep; ++c)
-            for (uint32_t i = 0; i < 4; ++i)
-                for (uint32_t j = 0; j < 4; ++j) acc[i][j] += sa[c][ty + 16 * i] * sb[c][tx + 16 * j];
-        __syncthreads();
     }
-    if (p.epilogue == kStore) {
-        for (uint32_t i = 0; i < 4; ++i)
-            for (uint32_t j = 0; j < 4; ++j) {
-                const uint64_t r = row0 + ty + 16 * i, c = col0 + tx + 16 * j;
-                if (r < row_end && c < p.n) store_value(p, g, r, c, acc[i][j]);
+    for (uint32_t c = 0; c < cols; c += 32) {
+        float v[32];
+        __syncwarp();  // rows past the end skip the work below
+        if (!empty) {
+            tmem_load32(acc + c, v);
+        } else {
+#pragma unroll
+            for (uint32_t i = 0; i < 32; ++i) v[i] = 0.f;
+        }
+        if (!live) continue;
+        const uint32_t here = min(32u, cols - c);
+        if (EPI == kStore) {
+#pragma unroll
+            for (uint32_t j = 0; j < 4; ++j)
+                if (8 * j < here)
+                    store8(p, t.vec, o.group, row, o.col0 + c + 8 * j, min(8u, here - 8 * j), alpha, v + 8 * j);
+        } else if (EPI == kLossStats) {
+            if (here < 32) {
+#pragma unroll
+                for (uint32_t i = 0; i < 32; ++i)
+                    if (i >= here) v[i] = -INFINITY;
             }
-        return;
-    }
-    if (p.epilogue == kLossGrad) {
-        for (uint32_t i = 0; i < 4; ++i)
-            for (uint32_t j = 0; j < 4; ++j) {
-                const uint64_t r = row0 + ty + 16 * i, c = col0 + tx + 16 * j;
-                if (r >= row_end || c >= p.n) continue;
-                const float w = p.ls.g[r];
-                float v = exp2f((acc[i][j] - p.ls.lse[r]) * kLog2e);
-                if (p.ls.targets[r] == int64_t(p.ls.col0 + c)) v -= 1.f;
-                static_cast<uint16_t*>(p.ls.out)[r * p.ls.ldo + c] = to16(w == 0.f ? 0.f : w * v, p.dtype);
+            float most = v[0];
+#pragma unroll
+            for (uint32_t i = 1; i < 32; ++i) most = fmaxf(most, v[i]);
+            const float next = fmaxf(top, most), base = next == -INFINITY ? 0.f : next * kLog2e;
+            float add = 0.f;
+#pragma unroll
+            for (uint32_t i = 0; i < 32; ++i) add += exp2f(fmaf(v[i], kLog2e, -base));
+            sum = sum * exp2f(fmaf(top, kLog2e, -base)) + add;
+            top = next;
+            if (target >= c && target < int64_t(c + here)) {
+#pragma unroll
+                for (uint32_t i = 0; i < 32; ++i)
+                    if (target == int64_t(c + i)) p.ls.hit[row] = v[i];
             }
-        return;
+        } else {
+#pragma unroll
+            for (uint32_t i = 0; i < 32; ++i) {
+                float d = exp2f(fmaf(v[i], kLog2e, -lse2));
+                if (target == int64_t(c + i)) d -= 1.f;
+                v[i] = weight == 0.f ? 0.f : weight * d;
+            }
+#pragma unroll
+            for (uint32_t j = 0; j < 4; ++j)
+                if (8 * j < here)
+                    write8(p.ls.out, row * p.ls.ldo + o.col0 + c + 8 * j, true, min(8u, here - 8 * j), p.dtype, v + 8 * j);
+        }
     }
-    for (uint32_t i = 0; i < 4; ++i)
-        for (uint32_t j = 0; j < 4; ++j) sc[ty + 16 * i][tx + 16 * j] = acc[i][j];
+    if (EPI == kLossStats && live) p.ls.part[uint64_t(o.col_tile) * p.m + row] = make_float2(top, sum);
+}
+
+// ---- the kernel -------------------------------------------------------------------------
+
+template <int EPI, bool SPLIT>
+__global__ void __launch_bounds__(kThreads, 1)
+    product_kernel(const __grid_constant__ Product p, const __grid_constant__ Tiling t,
+                   const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b) {
+    extern __shared__ uint8_t raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
+    Control* ctl = reinterpret_cast<Control*>(smem + t.stages * t.stage_bytes);
+    int32_t* offsets = reinterpret_cast<int32_t*>(ctl + 1);
+    int32_t* first = offsets + p.groups + 1;
+    const uint32_t warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+
+    // the cut of the rows or depths, checked whole
+    if (p.schedule != kDense) {
+        const int64_t end = p.schedule == kRows ? p.m : p.depth;
+        bool bad = false;
+        for (uint32_t i = threadIdx.x; i <= p.groups; i += kThreads) {
+            const int64_t v = p.offsets[i];
+            bad |= v < 0 || v > end || (i == 0 && v != 0) || (i == p.groups ? v != end : v > p.offsets[i + 1]);
+            offsets[i] = int32_t(v);
+        }
+        if (__syncthreads_or(bad)) {
+            if (blockIdx.x == 0 && threadIdx.x == 0 && p.status) atomicCAS(p.status, 0, int(UZIP_ERR_INVALID_ARG));
+            const uint16_t nan = p.dtype == UZIP_BF16 ? 0x7FC0 : 0x7E00;
+            const uint64_t total = p.m * p.n * (p.schedule == kDepth ? p.groups : 1);
+            for (uint64_t i = blockIdx.x * uint64_t(kThreads) + threadIdx.x; i < total; i += uint64_t(gridDim.x) * kThreads) {
+                const uint64_t r = i / p.n, g = r / p.m;
+                static_cast<uint16_t*>(p.st.out)[g * p.st.out_group + (r - g * p.m) * p.st.ldo + i % p.n] = nan;
+                if (p.st.z) static_cast<uint16_t*>(p.st.z)[r * p.st.ldz + i % p.n] = nan;
+            }
+            return;
+        }
+        if (p.schedule == kRows && warp == 0) {
+            int32_t before = 0;
+            for (uint32_t i = 0; i < p.groups; i += 32) {
+                const uint32_t g = i + lane;
+                int32_t v = g < p.groups ? (offsets[g + 1] - offsets[g] + int32_t(kRowsTile) - 1) / int32_t(kRowsTile) : 0;
+#pragma unroll
+                for (uint32_t d = 1; d < 32; d *= 2) {
+                    const int32_t u = __shfl_up_sync(0xFFFFFFFFu, v, d);
+                    if (lane >= d) v += u;
+                }
+                if (g < p.groups) first[g + 1] = before + v;
+                before += __shfl_sync(0xFFFFFFFFu, v, 31);
+            }
+            if (lane == 0) first[0] = 0;
+        }
+    }
+    if (threadIdx.x == 0) {
+        for (uint32_t i = 0; i < t.stages; ++i) {
+            mbar_init(smem_u32(&ctl->full[i]), 1);
+            mbar_init(smem_u32(&ctl->empty[i]), 1);
+        }
+        for (uint32_t i = 0; i < 2; ++i) {
+            mbar_init(smem_u32(&ctl->acc_full[i]), 1);
+            mbar_init(smem_u32(&ctl->acc_empty[i]), 4);
+        }
+        mbar_init(smem_u32(&ctl->drain), 1);
+        ctl->abort = 0;
+        fence_mbar_init();
+    }
+    if (warp == 1) tmem_alloc(smem_u32(&ctl->tmem), t.tmem_cols);
+    tmem_fence_before();
     __syncthreads();
-    if (tid < kTile && row0 + tid < row_end) {
-        const uint64_t r = row0 + tid;
-        float top = -INFINITY, sum = 0.f;
-        const uint32_t cols = p.n - col0 < kTile ? uint32_t(p.n - col0) : kTile;
-        for (uint32_t c = 0; c < cols; ++c) top = fmaxf(top, sc[tid][c]);
-        const float base = top == -INFINITY ? 0.f : top;
-        for (uint32_t c = 0; c < cols; ++c) sum += exp2f((sc[tid][c] - base) * kLog2e);
-        p.ls.part[blockIdx.x * p.m + r] = make_float2(top, sum);
-        const int64_t t = p.ls.targets[r] - int64_t(p.ls.col0 + col0);
-        if (t >= 0 && t < int64_t(cols)) p.ls.hit[r] = sc[tid][t];
+    tmem_fence_after();
+    const uint32_t tmem = ctl->tmem;
+    const uint32_t buffer_cols = t.tmem_cols / 2;
+
+    if (warp == 0) {
+        if (lane == 0) {
+            Walk walk(p, t, offsets, first);
+            Tile o;
+            uint32_t n = 0;
+            bool ok = true;
+            const uint32_t b_slices = (t.bn + 63) / 64;
+            while (ok && walk.take(o)) {
+                const uint32_t a_rows = min(kRowsTile, (o.row_end - o.row0 + t.a_box - 1) / t.a_box * t.a_box);
+                for (uint32_t i = 0; i < o.blocks; ++i, ++n) {
+                    const uint32_t s = n % t.stages;
+                    if (!(ok = wait(ctl, &ctl->empty[s], (n / t.stages & 1) ^ 1))) break;
+                    const uint32_t bar = smem_u32(&ctl->full[s]), a = smem_u32(smem + s * t.stage_bytes), b = a + kAStage;
+                    const int d = int(o.d0 + i * kDepthTile);
+                    const uint32_t a_bytes = p.a.depth_major ? a_rows * 128 : kAStage;
+                    const uint32_t b_bytes = p.b.depth_major ? t.bn * 128 : b_slices * kSliceBytes;
+                    mbar_expect_tx(bar, a_bytes + b_bytes);
+                    const int ga = 0, gb = p.schedule == kRows ? int(o.group) : 0;
+                    if (p.a.depth_major) {
+                        for (uint32_t r = 0; r < a_rows; r += t.a_box) tma_load(a + r * 128, &map_a, d, int(o.row0 + r), ga, bar);
+                    } else {
+                        tma_load(a, &map_a, int(o.row0), d, ga, bar);
+                        tma_load(a + kSliceBytes, &map_a, int(o.row0 + 64), d, ga, bar);
+                    }
+                    if (p.b.depth_major) {
+                        tma_load(b, &map_b, d, int(o.col0), gb, bar);
+                    } else {
+                        for (uint32_t r = 0; r < b_slices; ++r)
+                            tma_load(b + r * kSliceBytes, &map_b, int(o.col0 + 64 * r), d, gb, bar);
+                    }
+                }
+            }
+            if (ctl->abort)  // copies in flight land before the block ends
+                for (uint32_t i = n > t.stages ? n - t.stages : 0; i < n; ++i)
+                    for (uint32_t k = 0; k < 1u << 16; ++k)
+                        if (mbar_try_wait(smem_u32(&ctl->full[i % t.stages]), i / t.stages & 1)) break;
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        Walk walk(p, t, offsets, first);
+        Tile o;
+        uint32_t n = 0, tiles = 0;
+        bool ok = true;
+        const uint32_t step_a = p.a.depth_major ? 2 : 128, step_b = p.b.depth_major ? 2 : 128;
+        const uint32_t slices = 2 + (t.bn + 63) / 64;
+        while (ok && walk.take(o)) {
+            const uint32_t buf = tiles & 1;
+            ok = __all_sync(0xFFFFFFFFu, wait(ctl, &ctl->acc_empty[buf], (tiles >> 1 & 1) ^ 1));
+            if (!ok) break;
+            tmem_fence_after();
+            const uint32_t acc = tmem + buf * buffer_cols;
+            for (uint32_t i = 0; i < o.blocks; ++i, ++n) {
+                const uint32_t s = n % t.stages;
+                ok = __all_sync(0xFFFFFFFFu, wait(ctl, &ctl->full[s], n / t.stages & 1));
+                if (!ok) break;
+                uint8_t* stage = smem + s * t.stage_bytes;
+                uint32_t steps = 4;
+                if (p.schedule == kDepth || p.skip_depth) {
+                    // depths past the group's end belong to its neighbour, and skipped ones may hold anything:
+                    // both operands' lines are cleared (rows are contiguous here, a depth is one line of each slice)
+                    const uint32_t left = o.depth_end - (o.d0 + i * kDepthTile);
+                    uint64_t clear = p.skip_depth ? p.skip_depth[(o.d0 + i * kDepthTile) / 64] : 0;
+                    if (left < kDepthTile) {
+                        steps = (left + 15) / 16;
+                        clear |= ~0ull << left;
+                        if (steps < 4) clear &= (1ull << 16 * steps) - 1;
+                    }
+                    if (clear) {
+                        for (uint64_t m = clear; m; m &= m - 1) {
+                            const uint32_t line = __ffsll(m) - 1;
+                            for (uint32_t q = lane; q < slices * 8; q += 32)
+                                *reinterpret_cast<uint4*>(stage + q / 8 * kSliceBytes + line * 128 + q % 8 * 16) =
+                                    make_uint4(0, 0, 0, 0);
+                        }
+                        fence_async_shared();
+                        __syncwarp();
+                    }
+                }
+                tmem_fence_after();
+                if (lane == 0) {
+                    const uint64_t a = matrix_descriptor(smem_u32(stage), p.a.depth_major);
+                    const uint64_t b = matrix_descriptor(smem_u32(stage + kAStage), p.b.depth_major);
+                    for (uint32_t k = 0; k < steps; ++k) mma(acc, a + k * step_a, b + k * step_b, t.idesc, i || k);
+                    mma_commit(smem_u32(&ctl->empty[s]));
+                    if (i + 1 == o.blocks) mma_commit(smem_u32(&ctl->acc_full[buf]));
+                }
+                __syncwarp();
+            }
+            if (o.blocks == 0 && lane == 0) mbar_arrive(smem_u32(&ctl->acc_full[buf]));
+            __syncwarp();
+            ++tiles;
+        }
+        if (ctl->abort && lane == 0) {  // products in flight end before TMEM is freed
+            mma_commit(smem_u32(&ctl->drain));
+            for (uint32_t k = 0; k < 1u << 16; ++k)
+                if (mbar_try_wait(smem_u32(&ctl->drain), 0)) break;
+        }
+        __syncwarp();
+    } else {
+        Walk walk(p, t, offsets, first);
+        Tile o;
+        uint32_t tiles = 0;
+        const uint32_t quarter = warp % 4;  // the TMEM lanes that this warp may read
+        const float alpha = EPI == kStore && p.st.alpha ? *p.st.alpha : 1.f;
+        while (walk.take(o)) {
+            const uint32_t buf = tiles & 1;
+            if (!__all_sync(0xFFFFFFFFu, wait(ctl, &ctl->acc_full[buf], tiles >> 1 & 1))) break;
+            tmem_fence_after();
+            const uint32_t acc = tmem + buf * buffer_cols + (quarter * 32 << 16);
+            const uint32_t lane_row = quarter * 32 + lane;
+            if (!SPLIT) {
+                finish_tile<EPI>(p, t, o, acc, lane_row, o.blocks == 0, alpha);
+            } else {
+                // partial sums to shared memory, rows bn + 4 floats apart (no bank conflicts for 16-byte access)
+                float* part = reinterpret_cast<float*>(smem) + lane_row * (t.bn + 4);
+                for (uint32_t c = 0; c < t.bn; c += 32) {
+                    float v[32];
+                    if (o.blocks) {
+                        tmem_load32(acc + c, v);
+                    } else {
+#pragma unroll
+                        for (uint32_t i = 0; i < 32; ++i) v[i] = 0.f;
+                    }
+#pragma unroll
+                    for (uint32_t i = 0; i < 32; i += 4)
+                        if (c + i < t.bn) *reinterpret_cast<float4*>(part + c + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+                }
+            }
+            tmem_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&ctl->acc_empty[buf]));
+            ++tiles;
+        }
     }
+    if (SPLIT) {
+        // every block of the cluster joins and finishes its share of the tile, in the order of the splits
+        __syncthreads();
+        cluster_sync();
+        Walk walk(p, t, offsets, first);
+        Tile o;
+        if (walk.take(o)) {
+            const float alpha = p.st.alpha ? *p.st.alpha : 1.f;
+            const uint32_t rows = min(kRowsTile, o.row_end - o.row0), wide = t.bn / 8, items = rows * wide;
+            const uint32_t base = smem_u32(smem);
+            for (uint32_t i = walk.split * kThreads + threadIdx.x; i < items; i += t.splits * kThreads) {
+                const uint32_t r = i / wide, c = i % wide * 8;
+                if (o.col0 + c >= p.n) continue;
+                const uint32_t at = base + (r * (t.bn + 4) + c) * 4;
+                float v[8] = {};
+                for (uint32_t s = 0; s < t.splits; ++s) {
+                    const uint32_t from = cluster_address(at, s);
+                    const float4 lo = cluster_load4(from), hi = cluster_load4(from + 16);
+                    v[0] += lo.x, v[1] += lo.y, v[2] += lo.z, v[3] += lo.w, v[4] += hi.x, v[5] += hi.y, v[6] += hi.z, v[7] += hi.w;
+                }
+                store8(p, t.vec, 0, uint64_t(o.row0) + r, o.col0 + c, min(8u, uint32_t(p.n) - o.col0 - c), alpha, v);
+            }
+        }
+        cluster_sync();
+    }
+    tmem_fence_before();
+    __syncthreads();
+    tmem_fence_after();
+    if (warp == 1) tmem_free(tmem, t.tmem_cols);
+    if (threadIdx.x == 0 && ctl->abort && p.status) atomicCAS(p.status, 0, int(UZIP_ERR_TIMEOUT));
+}
+
+// ---- host side ----------------------------------------------------------------------------
+
+typedef CUresult (*EncodeFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                             const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                             CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeFn encode_fn() {
+    static const EncodeFn fn = [] {
+        void* f = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+            q != cudaDriverEntryPointSuccess) {
+            cudaGetLastError();
+            f = nullptr;
+        }
+        return reinterpret_cast<EncodeFn>(f);
+    }();
+    return fn;
+}
+
+// rows x depth x groups of 16-bit values, read in swizzled boxes of 64 contiguous values
+cudaError_t make_map(CUtensorMap* map, const Operand& o, uint64_t rows, uint64_t depth, uint64_t groups, uint32_t box_rows,
+                     int dtype) {
+    const uint64_t inner = o.depth_major ? depth : rows, outer = o.depth_major ? rows : depth;
+    if (inner == 0 || outer == 0) {  // nothing to load
+        *map = CUtensorMap{};
+        return cudaSuccess;
+    }
+    EncodeFn fn = encode_fn();
+    if (!fn) return cudaErrorNotSupported;
+    const cuuint64_t dims[3] = {inner, outer, groups};
+    const uint64_t group = groups > 1 ? o.group * 2 : std::min<uint64_t>(o.ld * 2 * outer, uint64_t(1) << 39);
+    const cuuint64_t strides[2] = {o.ld * 2, group};
+    const cuuint32_t box[3] = {kDepthTile, o.depth_major ? box_rows : kDepthTile, 1}, ones[3] = {1, 1, 1};
+    const CUresult r = fn(map, dtype == UZIP_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,
+                          const_cast<void*>(o.p), dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                          CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+bool aligned16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
+
+constexpr uint32_t kSmemMost = 227 * 1024;
+
+// Tile width, split of the depth and stages for a product: the smallest
+// estimate in clock cycles.  A stage costs the longest of its multiplication
+// (2 cycles a column), its way into shared memory (about 64 bytes a cycle) and
+// the HBM share of the operand that is read once (about 3500 bytes a cycle
+// for the whole GPU); tiles come in waves of one block per SM.
+Tiling choose(const Product& p, int sms) {
+    Tiling best{};
+    double best_cost = 1e300;
+    const uint64_t rows = p.m, row_tiles = p.schedule == kRows ? rows / kRowsTile + p.groups : (rows + kRowsTile - 1) / kRowsTile;
+    const uint64_t groups = p.schedule == kDepth ? p.groups : 1;
+    const double blocks = std::max(1.0, double(p.depth) / (p.schedule == kDepth ? p.groups : 1) / kDepthTile);
+    const uint32_t low = uint32_t(std::min<uint64_t>(kRowsTile, (rows + 7) / 8 * 8));
+    const uint32_t unit = p.b.depth_major ? 16 : 64;  // whole slices where rows are contiguous
+    const uint32_t widest = uint32_t(std::min<uint64_t>(256, (p.n + unit - 1) / unit * unit));
+    const bool may_split = p.epilogue == kStore && p.schedule == kDense && rows <= 512;
+    for (uint32_t bn = widest; bn >= unit; bn -= unit) {
+        if (bn < 32 && bn < widest) break;
+        const uint64_t tiles = row_tiles * ((p.n + bn - 1) / bn) * groups;
+        for (uint32_t splits = 1; splits <= (may_split ? 8u : 1u); ++splits) {
+            if (splits > 1 && blocks / splits < 4) break;
+            const double running = double(std::min<uint64_t>(tiles * splits, sms));
+            const double waves = std::ceil(double(tiles) * splits / sms);
+            const double fill = (low * 128.0 + bn * 128.0) / 64;
+            const double hbm = p.schedule == kDense ? bn * 128.0 * running / 3500 / std::min<double>(16, double(row_tiles)) : 0;
+            const double stage = std::max({2.0 * bn, fill, hbm, 128.0});
+            const double cost = waves * (blocks / splits * stage + 4.0 * bn + (splits > 1 ? 1500 : 0)) + 2000;
+            if (cost < best_cost * 0.999) {
+                best_cost = cost;
+                best.bn = bn;
+                best.splits = splits;
+            }
+        }
+    }
+    Tiling& t = best;
+    const uint32_t b_bytes = p.b.depth_major ? t.bn * 128 : (t.bn + 63) / 64 * kSliceBytes;
+    t.stage_bytes = kAStage + b_bytes;
+    const uint32_t tables = p.schedule == kDense ? 0 : (2 * p.groups + 2) * 4;
+    const uint32_t rest = 1024 + sizeof(Control) + tables;
+    t.stages = std::min<uint32_t>(kMaxStages, (kSmemMost - rest) / t.stage_bytes);
+    // (with splits the partial sums, 512 bn + 2 KiB bytes, take the stages' place: always less)
+    t.smem = rest + t.stages * t.stage_bytes;
+    uint32_t cols = 32;
+    while (cols < 2 * ((t.bn + 31) / 32 * 32)) cols *= 2;
+    t.tmem_cols = cols;
+    t.raster = 16;
+    t.a_box = p.schedule == kRows ? (rows / std::max(1u, p.groups) >= 96 ? kRowsTile : 32) : low;
+    const uint32_t fmt = p.dtype == UZIP_BF16 ? 1 : 0;
+    t.idesc = 1u << 4 | fmt << 7 | fmt << 10 | (p.a.depth_major ? 0u : 1u << 15) | (p.b.depth_major ? 0u : 1u << 16) |
+              (t.bn >> 3) << 17 | (kRowsTile >> 4) << 24;
+    const StoreEpilogue& e = p.st;
+    const uint32_t out_unit = e.out_fp32 ? 4 : 8;
+    t.vec = (aligned16(e.out) && e.ldo % out_unit == 0 && e.out_group % out_unit == 0 ? 1 : 0) |
+            (aligned16(e.bias) && (p.n % 8 == 0 || p.groups == 1) ? 2 : 0) | (aligned16(e.residual) && e.ldr % 8 == 0 ? 4 : 0) |
+            (aligned16(e.z) && e.ldz % 8 == 0 ? 8 : 0) | (aligned16(e.sum_in) && e.ld_sum % 4 == 0 ? 16 : 0);
+    return t;
+}
+
+template <int EPI, bool SPLIT>
+cudaError_t launch(const Product& p, const Tiling& t, int sms, const CUtensorMap& a, const CUtensorMap& b, cudaStream_t s) {
+    auto kern = product_kernel<EPI, SPLIT>;
+    static std::atomic<uint64_t> ready{0};  // devices on which the kernel may use all of the shared memory
+    int dev = 0;
+    cudaError_t err = cudaGetDevice(&dev);
+    if (err != cudaSuccess) return err;
+    if (dev >= 64 || !(ready.load(std::memory_order_relaxed) >> dev & 1)) {
+        err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kSmemMost));
+        if (err != cudaSuccess) return err;
+        if (dev < 64) ready.fetch_or(uint64_t(1) << dev, std::memory_order_relaxed);
+    }
+    const uint64_t col_tiles = (p.n + t.bn - 1) / t.bn;
+    const uint64_t row_tiles = p.schedule == kRows ? p.m / kRowsTile + p.groups : (p.m + kRowsTile - 1) / kRowsTile;
+    const uint64_t tiles = row_tiles * col_tiles * (p.schedule == kDepth ? p.groups : 1);
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(uint32_t(SPLIT ? tiles * t.splits : std::min<uint64_t>(tiles, sms)));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = t.smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = t.splits;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = SPLIT ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, kern, p, t, a, b);
 }
 
 }  // namespace
 
-uint32_t product_tile_columns(const Product&, int) { return kTile; }
+uint32_t product_tile_columns(const Product& p, int sms) { return choose(p, sms).bn; }
 
-cudaError_t launch_product(const Product& p, cudaStream_t s) {
+cudaError_t launch_product(const Product& p, int sms, cudaStream_t s) {
     if (p.m == 0 || p.n == 0) return cudaSuccess;
-    const dim3 grid(uint32_t((p.n + kTile - 1) / kTile), uint32_t((p.m + kTile - 1) / kTile), p.groups);
-    product_kernel<<<grid, 256, 0, s>>>(p);
-    return cudaGetLastError();
+    const Tiling t = choose(p, sms);
+    CUtensorMap a, b;
+    cudaError_t err = make_map(&a, p.a, p.m, p.depth, 1, t.a_box, p.dtype);
+    if (err == cudaSuccess) err = make_map(&b, p.b, p.n, p.depth, p.schedule == kRows ? p.groups : 1, t.bn, p.dtype);
+    if (err != cudaSuccess) return err;
+    switch (p.epilogue) {
+        case kLossStats: return launch<kLossStats, false>(p, t, sms, a, b, s);
+        case kLossGrad: return launch<kLossGrad, false>(p, t, sms, a, b, s);
+        default: return t.splits > 1 ? launch<kStore, true>(p, t, sms, a, b, s) : launch<kStore, false>(p, t, sms, a, b, s);
+    }
 }
 
 }  // namespace uzip

@@ -78,7 +78,7 @@ struct Product {
 
 // columns of the tiles in which launch_product takes p (kLossStats partials)
 uint32_t product_tile_columns(const Product& p, int sms);
-cudaError_t launch_product(const Product& p, cudaStream_t s);
+cudaError_t launch_product(const Product& p, int sms, cudaStream_t s);
 
 // ---- steps around the products (product_steps.cu) ---------------------------
 
@@ -86,7 +86,8 @@ cudaError_t launch_product(const Product& p, cudaStream_t s);
 cudaError_t launch_pack_rows(const void* from, uint64_t ld, uint64_t group, void* to, uint64_t ld_to, uint64_t rows,
                              uint64_t cols, uint64_t groups, cudaStream_t s);
 
-// dz = dy act'(z) into dz (nullable) and its column sums into db (nullable)
+// dz = dy act'(z) into dz (nullable) and its column sums into db (nullable); db
+// is NaN where the offsets do not cut [0, m)
 struct ActGrad {
     const void* dy;
     uint64_t lddy;
@@ -101,20 +102,13 @@ struct ActGrad {
     const int64_t* offsets;  // nullable: one group of all rows
     uint32_t act;
     int dtype;
+    int32_t* status;
 };
 uint32_t act_grad_splits(uint64_t m, uint64_t n, uint64_t groups);
 cudaError_t launch_act_grad(const ActGrad& a, cudaStream_t s);
 
-// status and NaN outputs for offsets that do not cut [0, m)
-struct OffsetCheck {
-    const int64_t* offsets;
-    uint64_t groups, m;
-    void* out[4];
-    uint64_t rows[4], cols[4], ld[4], group[4], count[4];
-    int dtype;
-    int32_t* status;
-};
-cudaError_t launch_offset_check(const OffsetCheck& c, cudaStream_t s);
+// status only, for offsets that do not cut [0, m)
+cudaError_t launch_offset_check(const int64_t* offsets, uint64_t groups, uint64_t m, int32_t* status, cudaStream_t s);
 
 cudaError_t launch_loss_join(const LossEpilogue& e, uint64_t t, uint64_t v, uint32_t tiles, float* loss, float* lse,
                              int32_t* status, cudaStream_t s);

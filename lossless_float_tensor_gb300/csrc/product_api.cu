@@ -43,7 +43,7 @@ struct Matrix {
     }
     bool shape_ok() const {
         if (rows > 1 && (ld < cols || ld > (int64_t(1) << 36))) return false;
-        if (groups > 1 && (group < (rows - 1) * step() + cols || group > (int64_t(1) << 40))) return false;
+        if (groups > 1 && (group < (rows - 1) * step() + cols || group > (int64_t(1) << 38))) return false;
         return true;
     }
     bool ok() const { return empty() || (p && aligned(p, 2) && shape_ok() && device_range_ok(p, bytes())); }
@@ -71,6 +71,19 @@ cudaError_t run_pack(const Packed& p, cudaStream_t s) {
     if (!p.to) return cudaSuccess;
     return launch_pack_rows(p.from.p, p.from.step(), p.from.groups > 1 ? p.from.group : 0, p.to, p.ld, p.from.rows,
                             p.from.cols, p.from.groups, s);
+}
+
+int sm_count() {
+    static const int sms = [] {  // one kind of GPU in a process
+        int dev = 0, v = 0;
+        if (cudaGetDevice(&dev) != cudaSuccess ||
+            cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
+            cudaGetLastError();
+            return 152;
+        }
+        return v;
+    }();
+    return sms;
 }
 
 bool half_type(int dtype) { return dtype == UZIP_BF16 || dtype == UZIP_FP16; }
@@ -155,15 +168,9 @@ uzip_status forward(const uzip_linear_args* a, void* ws, uint64_t bytes, int32_t
     if (err == cudaSuccess && some) {
         err = run_pack(f.px, s);
         if (err == cudaSuccess) err = run_pack(f.pw, s);
-        if (err == cudaSuccess) err = launch_product(f.p, s);
-    }
-    if (err == cudaSuccess && grouped) {
-        OffsetCheck c{a->offsets, uint64_t(g), uint64_t(a->m)};
-        c.dtype = a->dtype, c.status = d_status;
-        c.out[0] = a->y, c.rows[0] = a->m, c.cols[0] = a->n, c.ld[0] = f.p.st.ldo, c.count[0] = 1;
-        c.out[1] = a->z, c.rows[1] = a->m, c.cols[1] = a->n, c.ld[1] = f.p.st.ldz, c.count[1] = 1;
-        err = launch_offset_check(c, s);
-    }
+        if (err == cudaSuccess) err = launch_product(f.p, sm_count(), s);
+    } else if (err == cudaSuccess && grouped)
+        err = launch_offset_check(a->offsets, g, a->m, d_status, s);
     return finish(err);
 }
 
@@ -186,7 +193,7 @@ Backward plan_backward(const uzip_linear_grad_args& a, Work& w, int32_t* d_statu
         q.dy = a.dy, q.lddy = dy.step();
         q.z = a.z, q.ldz = a.m > 1 ? a.ldz : a.n;
         q.m = a.m, q.n = a.n;
-        q.act = a.act, q.dtype = a.dtype;
+        q.act = a.act, q.dtype = a.dtype, q.status = d_status;
         const bool by_group = a.db && a.groups;
         q.groups = by_group ? groups : 1;
         q.offsets = by_group ? a.offsets : nullptr;
@@ -248,33 +255,15 @@ uzip_status backward(const uzip_linear_grad_args* a, void* ws, uint64_t bytes, i
     if (err == cudaSuccess && f.need_grad) err = launch_act_grad(f.grad, s);
     for (const Packed* p : {&f.pdy, &f.pw, &f.px})
         if (err == cudaSuccess) err = run_pack(*p, s);
-    if (err == cudaSuccess && a->dx) err = launch_product(f.dx, s);
-    if (err == cudaSuccess && a->dw) err = launch_product(f.dw, s);
-    if (err == cudaSuccess && grouped) {
-        OffsetCheck c{a->offsets, uint64_t(g), uint64_t(a->m)};
-        c.dtype = a->dtype, c.status = d_status;
-        c.out[0] = a->dx, c.rows[0] = a->m, c.cols[0] = a->k, c.ld[0] = f.dx.st.ldo, c.count[0] = 1;
-        c.out[1] = a->dw, c.rows[1] = a->n, c.cols[1] = a->k, c.ld[1] = f.dw.st.ldo, c.group[1] = a->dw_group, c.count[1] = g;
-        c.out[2] = a->db, c.rows[2] = g, c.cols[2] = a->n, c.ld[2] = a->n, c.count[2] = 1;
-        err = launch_offset_check(c, s);
-    }
+    if (err == cudaSuccess && a->dx) err = launch_product(f.dx, sm_count(), s);
+    if (err == cudaSuccess && a->dw) err = launch_product(f.dw, sm_count(), s);
+    // the products and the bias gradient check the offsets themselves
+    const bool checked = (a->dx && a->m && a->k) || (a->dw && a->n && a->k) || (a->db && a->n);
+    if (err == cudaSuccess && grouped && !checked) err = launch_offset_check(a->offsets, g, a->m, d_status, s);
     return finish(err);
 }
 
 // ---- cross entropy --------------------------------------------------------------
-
-int sm_count() {
-    static int sms = 0;  // one kind of GPU in a process
-    if (!sms) {
-        int dev = 0;
-        if (cudaGetDevice(&dev) != cudaSuccess ||
-            cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
-            cudaGetLastError();
-            return 152;
-        }
-    }
-    return sms;
-}
 
 struct Loss {
     Product p{};
@@ -348,7 +337,7 @@ cudaError_t run_loss_grad(const uzip_cross_entropy_grad_args& a, const LossGradP
         p.epilogue = kLossGrad;
         p.ls.targets = a.targets, p.ls.ignore = a.ignore_index, p.ls.col0 = col0;
         p.ls.lse = a.lse, p.ls.g = f.g, p.ls.out = f.dl, p.ls.ldo = f.ld_piece;
-        err = launch_product(p, s);
+        err = launch_product(p, sm_count(), s);
         if (err == cudaSuccess && a.dh) {
             Product q{};
             q.dtype = a.dtype, q.status = d_status, q.groups = 1;
@@ -363,7 +352,7 @@ cudaError_t run_loss_grad(const uzip_cross_entropy_grad_args& a, const LossGradP
                 q.st.out = a.dh, q.st.ldo = a.t > 1 ? a.lddh : a.d;
             }
             q.st.alpha = f.scale + 1;
-            err = launch_product(q, s);
+            err = launch_product(q, sm_count(), s);
         }
         if (err == cudaSuccess && a.dw) {
             Product q{};
@@ -376,7 +365,7 @@ cudaError_t run_loss_grad(const uzip_cross_entropy_grad_args& a, const LossGradP
             const uint64_t ldo = a.v > 1 ? a.lddw : a.d;
             q.st.out = static_cast<uint16_t*>(a.dw) + col0 * ldo, q.st.ldo = ldo;
             q.st.alpha = f.scale + 1;
-            err = launch_product(q, s);
+            err = launch_product(q, sm_count(), s);
         }
     }
     return err;
@@ -470,7 +459,7 @@ uzip_status uzip_cross_entropy(const uzip_cross_entropy_args* a, void* d_workspa
     const Loss f = plan_loss(*a, work, d_status);
     err = run_pack(f.ph, s);
     if (err == cudaSuccess) err = run_pack(f.pw, s);
-    if (err == cudaSuccess) err = launch_product(f.p, s);
+    if (err == cudaSuccess) err = launch_product(f.p, sm_count(), s);
     if (err == cudaSuccess) err = launch_loss_join(f.p.ls, a->t, a->v, f.tiles, a->loss, a->lse, d_status, s);
     return finish(err);
 }

@@ -61,15 +61,27 @@ __device__ __forceinline__ void load8(const uint16_t* p, bool vec, uint32_t cols
     }
 }
 
+// Whether this thread's share of the offsets breaks the rule: 0, never less, m.
+__device__ __forceinline__ bool offsets_bad(const int64_t* offsets, uint32_t groups, uint64_t m) {
+    bool bad = false;
+    for (uint32_t i = threadIdx.x; i <= groups; i += kThreads) {
+        const int64_t v = offsets[i];
+        bad |= v < 0 || v > int64_t(m) || (i == 0 && v != 0) || (i == groups ? v != int64_t(m) : v > offsets[i + 1]);
+    }
+    return bad;
+}
+
 __global__ void __launch_bounds__(kThreads) act_grad_kernel(const __grid_constant__ ActGrad a) {
     __shared__ float sums[kGradRows][kGradCols + 4];
     const uint32_t tx = threadIdx.x % 16, ty = threadIdx.x / 16, g = blockIdx.z;
     const uint64_t col = uint64_t(blockIdx.x) * kGradCols + 8 * tx;
     uint64_t r0 = 0, r1 = a.m;
+    bool bad = false;
     if (a.offsets) {
-        const int64_t lo = a.offsets[g], hi = a.offsets[g + 1];
-        const bool good = lo >= 0 && lo <= hi && hi <= int64_t(a.m);  // else reported by the offset check
-        r0 = good ? lo : 0, r1 = good ? hi : 0;
+        bad = __syncthreads_or(offsets_bad(a.offsets, a.groups, a.m));
+        if (bad && a.status && blockIdx.x + blockIdx.y + blockIdx.z + threadIdx.x == 0)
+            atomicCAS(a.status, 0, int(UZIP_ERR_INVALID_ARG));
+        r0 = bad ? 0 : a.offsets[g], r1 = bad ? 0 : a.offsets[g + 1];
     }
     const uint64_t share = (r1 - r0 + a.splits - 1) / a.splits;
     r0 = min(r0 + blockIdx.y * share, r1);
@@ -106,7 +118,7 @@ __global__ void __launch_bounds__(kThreads) act_grad_kernel(const __grid_constan
     __syncthreads();
     const uint64_t c = uint64_t(blockIdx.x) * kGradCols + threadIdx.x;
     if (threadIdx.x < kGradCols && c < a.n) {
-        float total = 0.f;
+        float total = bad ? NAN : 0.f;
 #pragma unroll
         for (uint32_t i = 0; i < kGradRows; ++i) total += sums[i][threadIdx.x];
         if (a.splits > 1) a.part[(uint64_t(g) * a.splits + blockIdx.y) * a.n + c] = total;
@@ -124,25 +136,9 @@ __global__ void __launch_bounds__(kThreads) join_columns_kernel(const float* par
     db[i] = to16(v, dtype);
 }
 
-// Every block reads the offsets (8 KiB at most); all of them fill the outputs
-// with NaN where the offsets do not cut [0, m).
-__global__ void __launch_bounds__(kThreads) offset_check_kernel(const __grid_constant__ OffsetCheck c) {
-    bool bad = false;
-    for (uint64_t i = threadIdx.x; i <= c.groups; i += kThreads) {
-        const int64_t v = c.offsets[i];
-        bad |= v < 0 || v > int64_t(c.m) || (i == 0 && v != 0) || (i == c.groups ? v != int64_t(c.m) : v > c.offsets[i + 1]);
-    }
-    if (!__syncthreads_or(bad)) return;
-    if (blockIdx.x == 0 && threadIdx.x == 0 && c.status) atomicCAS(c.status, 0, int(UZIP_ERR_INVALID_ARG));
-    const uint16_t nan = c.dtype == UZIP_BF16 ? 0x7FC0 : 0x7E00;
-    for (uint32_t k = 0; k < 4; ++k) {
-        if (!c.out[k]) continue;
-        const uint64_t total = c.count[k] * c.rows[k] * c.cols[k];
-        for (uint64_t i = blockIdx.x * uint64_t(kThreads) + threadIdx.x; i < total; i += uint64_t(gridDim.x) * kThreads) {
-            const uint64_t r = i / c.cols[k], col = i % c.cols[k], g = r / c.rows[k];
-            static_cast<uint16_t*>(c.out[k])[g * c.group[k] + (r - g * c.rows[k]) * c.ld[k] + col] = nan;
-        }
-    }
+__global__ void __launch_bounds__(kThreads) offset_check_kernel(const int64_t* offsets, uint32_t groups, uint64_t m,
+                                                                int32_t* status) {
+    if (__syncthreads_or(offsets_bad(offsets, groups, m)) && threadIdx.x == 0) *status = int(UZIP_ERR_INVALID_ARG);
 }
 
 // One row's tile maxima and sums joined in tile order: 32 rows x 8 threads
@@ -285,8 +281,9 @@ cudaError_t launch_act_grad(const ActGrad& a, cudaStream_t s) {
     return err;
 }
 
-cudaError_t launch_offset_check(const OffsetCheck& c, cudaStream_t s) {
-    offset_check_kernel<<<152, kThreads, 0, s>>>(c);
+cudaError_t launch_offset_check(const int64_t* offsets, uint64_t groups, uint64_t m, int32_t* status, cudaStream_t s) {
+    if (!status) return cudaSuccess;
+    offset_check_kernel<<<1, kThreads, 0, s>>>(offsets, uint32_t(groups), m, status);
     return cudaGetLastError();
 }
 
