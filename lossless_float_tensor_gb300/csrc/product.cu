@@ -10,6 +10,10 @@
 // Operands may be contiguous along the depth or along the rows: the tensor
 // core reads both from the 128-byte swizzled layout that TMA writes, so the
 // transposed products of the gradients need no copy.
+//
+// A pair of blocks (tcgen05 cta_group::2) multiplies 256 rows by up to 256
+// columns: each block holds its own 128 rows of A and half of the columns of
+// B, so a stage takes 32 KB instead of 48 KB and seven of them fit.
 #include <cuda.h>
 
 #include <algorithm>
@@ -27,14 +31,16 @@ constexpr uint32_t kSliceBytes = kDepthTile * 128;  // 64 rows x 64 depths when 
 constexpr uint32_t kAStage = kRowsTile * kDepthTile * 2;
 constexpr uint32_t kMaxStages = 12;
 constexpr uint32_t kThreads = 192;  // TMA warp, MMA warp, four epilogue warps
-constexpr uint32_t kWaitLimit = 1u << 22;  // tries of a bounded wait (up to about 1 us each)
+constexpr uint32_t kLines = 8;      // lines of the smaller boxes for depths that are cut
+constexpr uint64_t kWaitLimitNs = 4000000000;  // a wait gives up after four seconds,
+constexpr uint64_t kDrainLimitNs = 50000000;   // one for copies or products in flight then after 50 ms
 
 struct Tiling {
     uint32_t bn;       // columns of a tile
     uint32_t stages;
     uint32_t stage_bytes;
     uint32_t splits;   // blocks of a cluster that share a tile's depth
-    uint32_t pair;     // two blocks share a tile of 256 rows
+    uint32_t pair;     // 2: two blocks share a tile of 256 rows, else 1
     uint32_t a_box;    // rows of one TMA box of A (depth-major)
     uint32_t raster;   // row tiles taken together for the sake of L2
     uint32_t tmem_cols;
@@ -51,28 +57,62 @@ __device__ __forceinline__ uint64_t matrix_descriptor(uint32_t addr, bool depth_
     const uint64_t lead = depth_major ? 1 : kSliceBytes / 16;
     return uint64_t((addr & 0x3FFFF) >> 4) | lead << 16 | uint64_t(1024 / 16) << 32 | uint64_t(1) << 46 | uint64_t(2) << 61;
 }
+template <bool PAIR>
 __device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap* map, int c0, int c1, int c2, uint32_t bar) {
-    asm volatile(
+    if (PAIR)  // the barrier may be the other block's
+        asm volatile(
+            "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, "
+            "%3, %4}], [%5];" ::"r"(dst),
+            "l"(map), "r"(c0), "r"(c1), "r"(c2), "r"(bar)
+            : "memory");
+    else
+        asm volatile(
         "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];"
         ::"r"(dst), "l"(map), "r"(c0), "r"(c1), "r"(c2), "r"(bar)
         : "memory");
 }
+template <bool PAIR>
 __device__ __forceinline__ void mma(uint32_t tmem, uint64_t a, uint64_t b, uint32_t idesc, uint32_t add) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
-        ::"r"(tmem), "l"(a), "l"(b), "r"(idesc), "r"(add)
-        : "memory");
+    if (PAIR)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(tmem),
+            "l"(a), "l"(b), "r"(idesc), "r"(add)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(tmem),
+            "l"(a), "l"(b), "r"(idesc), "r"(add)
+            : "memory");
 }
+// one arrival once the products issued so far are done (a pair: on both blocks' barriers)
+template <bool PAIR>
 __device__ __forceinline__ void mma_commit(uint32_t bar) {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+    if (PAIR)
+        asm volatile(
+            "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+            "h"(uint16_t(3))
+            : "memory");
+    else
+        asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
 }
+template <bool PAIR>
 __device__ __forceinline__ void tmem_alloc(uint32_t to, uint32_t cols) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(to), "r"(cols) : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    if (PAIR) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(to), "r"(cols) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
+    } else {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(to), "r"(cols) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    }
 }
+template <bool PAIR>
 __device__ __forceinline__ void tmem_free(uint32_t addr, uint32_t cols) {
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(cols) : "memory");
+    if (PAIR)
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(cols) : "memory");
+    else
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(cols) : "memory");
 }
 __device__ __forceinline__ void tmem_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tmem_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
@@ -104,11 +144,46 @@ __device__ __forceinline__ uint32_t cluster_address(uint32_t addr, uint32_t rank
     asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
     return r;
 }
+__device__ __forceinline__ void cluster_arrive(uint32_t bar) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+// CLUSTER: arrivals may come from the other block of the pair
+template <bool CLUSTER>
+__device__ __forceinline__ bool try_wait(uint32_t bar, uint32_t parity) {
+    uint32_t done;
+    if (CLUSTER)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(done)
+            : "r"(bar), "r"(parity)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(done)
+            : "r"(bar), "r"(parity)
+            : "memory");
+    return done != 0;
+}
+__device__ __forceinline__ uint64_t now_ns() {
+    uint64_t v;
+    asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(v));
+    return v;
+}
 __device__ __forceinline__ float4 cluster_load4(uint32_t addr) {
     float4 v;
     asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr));
     return v;
 }
+
+// the operands in boxes of a whole stage, and of 8 lines and 1 line for cut depths
+struct Maps {
+    CUtensorMap a, b, a_lines, a_line, b_lines, b_line;
+};
 
 // ---- the block's shared state ------------------------------------------------------
 
@@ -122,15 +197,33 @@ struct Control {
 // behind it, for the grouped schedules: int32 offsets[groups + 1], then (kRows)
 // first row tile of each group, int32 [groups + 1]
 
-__device__ __forceinline__ bool wait(Control* c, uint64_t* bar, uint32_t parity, uint32_t limit = kWaitLimit) {
+template <bool PAIR>
+__device__ __forceinline__ bool wait(Control* c, uint64_t* bar, uint32_t parity) {
     const uint32_t b = smem_u32(bar);
-    for (uint32_t i = 0; i < limit; ++i) {
-        if (mbar_try_wait(b, parity)) return true;
-        if (i % 64 == 63 && c->abort) return false;
-    }
+    if (try_wait<PAIR>(b, parity)) return true;
+    const uint64_t end = now_ns() + kWaitLimitNs;
+    do {
+        for (uint32_t i = 0; i < 32; ++i)
+            if (try_wait<PAIR>(b, parity)) return true;
+        if (c->abort) return false;
+    } while (now_ns() < end);
     c->abort = 1;
     return false;
 }
+__device__ __forceinline__ void drain(uint64_t* bar, uint32_t parity) {
+    const uint64_t end = now_ns() + kDrainLimitNs;
+    while (!try_wait<true>(smem_u32(bar), parity) && now_ns() < end) {
+    }
+}
+
+// The next stage of the ring and the parity of its use.
+struct Ring {
+    uint32_t stages, s = 0, phase = 0, used = 0;
+    __device__ __forceinline__ void advance() {
+        ++used;
+        if (++s == stages) s = 0, phase ^= 1;
+    }
+};
 
 // A tile of C: its group, first row and column, the end of its rows, and its depths.
 struct Tile {
@@ -146,12 +239,13 @@ struct Walk {
 
     __device__ Walk(const Product& p, const Tiling& t, const int32_t* offsets, const int32_t* first)
         : p(p), t(t), offsets(offsets), first(first) {
-        tile_rows = kRowsTile;
+        tile_rows = kRowsTile * t.pair;
         col_tiles = (uint32_t(p.n) + t.bn - 1) / t.bn;
         row_tiles = p.schedule == kRows ? uint32_t(first[p.groups]) : (uint32_t(p.m) + tile_rows - 1) / tile_rows;
         total = row_tiles * col_tiles * (p.schedule == kDepth ? p.groups : 1);
-        step = gridDim.x / t.splits;
-        next = blockIdx.x / t.splits;
+        const uint32_t cluster = t.splits * t.pair;  // one of the two is 1
+        step = gridDim.x / cluster;
+        next = blockIdx.x / cluster;
         split = blockIdx.x % t.splits;
         group = 0;
     }
@@ -168,7 +262,7 @@ struct Walk {
             id -= first[group] * col_tiles;
             o.group = group;
             o.col_tile = id / rows;
-            o.row0 = offsets[group] + id % rows * kRowsTile;
+            o.row0 = offsets[group] + id % rows * tile_rows;
             o.row_end = offsets[group + 1];
         } else {
             if (p.schedule == kDepth) {
@@ -351,16 +445,19 @@ __device__ __forceinline__ void finish_tile(const Product& p, const Tiling& t, c
 
 // ---- the kernel -------------------------------------------------------------------------
 
-template <int EPI, bool SPLIT>
+// MODE: 0 a block by itself, 1 a cluster splits the depth, 2 a pair of blocks
+template <int EPI, int MODE>
 __global__ void __launch_bounds__(kThreads, 1)
     product_kernel(const __grid_constant__ Product p, const __grid_constant__ Tiling t,
-                   const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b) {
+                   const __grid_constant__ Maps maps) {
+    constexpr bool SPLIT = MODE == 1, PAIR = MODE == 2;
     extern __shared__ uint8_t raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
     Control* ctl = reinterpret_cast<Control*>(smem + t.stages * t.stage_bytes);
     int32_t* offsets = reinterpret_cast<int32_t*>(ctl + 1);
     int32_t* first = offsets + p.groups + 1;
     const uint32_t warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const uint32_t rank = PAIR ? cluster_rank() : 0;  // the pair's block 0 issues the products
 
     // the cut of the rows or depths, checked whole
     if (p.schedule != kDense) {
@@ -386,7 +483,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             int32_t before = 0;
             for (uint32_t i = 0; i < p.groups; i += 32) {
                 const uint32_t g = i + lane;
-                int32_t v = g < p.groups ? (offsets[g + 1] - offsets[g] + int32_t(kRowsTile) - 1) / int32_t(kRowsTile) : 0;
+                int32_t v = 0;
+                if (g < p.groups) v = int32_t((uint32_t(offsets[g + 1] - offsets[g]) + kRowsTile * t.pair - 1) / (kRowsTile * t.pair));
 #pragma unroll
                 for (uint32_t d = 1; d < 32; d *= 2) {
                     const int32_t u = __shfl_up_sync(0xFFFFFFFFu, v, d);
@@ -405,15 +503,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         for (uint32_t i = 0; i < 2; ++i) {
             mbar_init(smem_u32(&ctl->acc_full[i]), 1);
-            mbar_init(smem_u32(&ctl->acc_empty[i]), 4);
+            mbar_init(smem_u32(&ctl->acc_empty[i]), 4 * t.pair);
         }
         mbar_init(smem_u32(&ctl->drain), 1);
         ctl->abort = 0;
         fence_mbar_init();
     }
-    if (warp == 1) tmem_alloc(smem_u32(&ctl->tmem), t.tmem_cols);
+    if (warp == 1) tmem_alloc<PAIR>(smem_u32(&ctl->tmem), t.tmem_cols);
     tmem_fence_before();
     __syncthreads();
+    if (PAIR) cluster_sync();
     tmem_fence_after();
     const uint32_t tmem = ctl->tmem;
     const uint32_t buffer_cols = t.tmem_cols / 2;
@@ -422,98 +521,118 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) {
             Walk walk(p, t, offsets, first);
             Tile o;
-            uint32_t n = 0;
+            Ring ring{t.stages};
             bool ok = true;
-            const uint32_t b_slices = (t.bn + 63) / 64;
+            const uint32_t b_cols = t.bn / t.pair, b_slices = (b_cols + 63) / 64;
+            const bool cut = p.schedule == kDepth || p.skip_depth;
             while (ok && walk.take(o)) {
-                const uint32_t a_rows = min(kRowsTile, (o.row_end - o.row0 + t.a_box - 1) / t.a_box * t.a_box);
-                for (uint32_t i = 0; i < o.blocks; ++i, ++n) {
-                    const uint32_t s = n % t.stages;
-                    if (!(ok = wait(ctl, &ctl->empty[s], (n / t.stages & 1) ^ 1))) break;
-                    const uint32_t bar = smem_u32(&ctl->full[s]), a = smem_u32(smem + s * t.stage_bytes), b = a + kAStage;
-                    const int d = int(o.d0 + i * kDepthTile);
-                    const uint32_t a_bytes = p.a.depth_major ? a_rows * 128 : kAStage;
-                    const uint32_t b_bytes = p.b.depth_major ? t.bn * 128 : b_slices * kSliceBytes;
-                    mbar_expect_tx(bar, a_bytes + b_bytes);
-                    const int ga = 0, gb = p.schedule == kRows ? int(o.group) : 0;
+                const uint32_t row0 = o.row0 + rank * kRowsTile, col0 = o.col0 + rank * b_cols;
+                const uint32_t a_rows = PAIR ? kRowsTile : min(kRowsTile, (o.row_end - row0 + t.a_box - 1) / t.a_box * t.a_box);
+                const int gb = p.schedule == kRows ? int(o.group) : 0;
+                for (uint32_t i = 0; i < o.blocks; ++i, ring.advance()) {
+                    const uint32_t s = ring.s;
+                    if (!(ok = wait<PAIR>(ctl, &ctl->empty[s], ring.phase ^ 1))) break;
+                    uint32_t bar = smem_u32(&ctl->full[s]);
+                    const uint32_t a = smem_u32(smem + s * t.stage_bytes), b = a + kAStage;
+                    const uint32_t d = o.d0 + i * kDepthTile;
+                    uint32_t lines = kDepthTile;
+                    uint64_t keep = ~0ull;
+                    if (cut) {
+                        const uint32_t left = o.depth_end - d;
+                        if (left < kDepthTile) {
+                            lines = (left + 15) / 16 * 16;
+                            keep >>= 64 - left;
+                        }
+                        if (p.skip_depth) keep &= ~p.skip_depth[d / 64];
+                    }
+                    const uint32_t a_bytes = p.a.depth_major ? a_rows * 128 : 2 * 128 * lines;
+                    const uint32_t b_bytes = p.b.depth_major ? b_cols * 128 : b_slices * 128 * lines;
+                    if (rank == 0) mbar_expect_tx(bar, (a_bytes + b_bytes) * t.pair);
+                    if (PAIR) bar = cluster_address(bar, 0);
+                    if (~keep) {
+                        // Depths past the group's end belong to its neighbour, and skipped ones may hold anything: their
+                        // lines are read from beyond the tensor's end, where TMA gives zeros.  (Both operands have
+                        // contiguous rows here: a depth is one line of each slice.)
+                        for (uint32_t l = 0; l < lines; l += kLines) {
+                            const uint32_t some = uint32_t(keep >> l) & 0xFF;
+                            const uint32_t wide = some == 0xFF || some == 0 ? kLines : 1;
+                            for (uint32_t j = l; j < l + kLines; j += wide) {
+                                const int from = int((keep >> j) & 1 ? d + j : uint32_t(p.depth));
+                                for (uint32_t r = 0; r < 2; ++r)
+                                    tma_load<PAIR>(a + r * kSliceBytes + j * 128, wide > 1 ? &maps.a_lines : &maps.a_line,
+                                                   int(row0 + 64 * r), from, 0, bar);
+                                for (uint32_t r = 0; r < b_slices; ++r)
+                                    tma_load<PAIR>(b + r * kSliceBytes + j * 128, wide > 1 ? &maps.b_lines : &maps.b_line,
+                                                   int(col0 + 64 * r), from, 0, bar);
+                            }
+                        }
+                        continue;
+                    }
                     if (p.a.depth_major) {
-                        for (uint32_t r = 0; r < a_rows; r += t.a_box) tma_load(a + r * 128, &map_a, d, int(o.row0 + r), ga, bar);
+                        for (uint32_t r = 0; r < a_rows; r += t.a_box)
+                            tma_load<PAIR>(a + r * 128, &maps.a, int(d), int(row0 + r), 0, bar);
                     } else {
-                        tma_load(a, &map_a, int(o.row0), d, ga, bar);
-                        tma_load(a + kSliceBytes, &map_a, int(o.row0 + 64), d, ga, bar);
+                        tma_load<PAIR>(a, &maps.a, int(row0), int(d), 0, bar);
+                        tma_load<PAIR>(a + kSliceBytes, &maps.a, int(row0 + 64), int(d), 0, bar);
                     }
                     if (p.b.depth_major) {
-                        tma_load(b, &map_b, d, int(o.col0), gb, bar);
+                        tma_load<PAIR>(b, &maps.b, int(d), int(col0), gb, bar);
                     } else {
                         for (uint32_t r = 0; r < b_slices; ++r)
-                            tma_load(b + r * kSliceBytes, &map_b, int(o.col0 + 64 * r), d, gb, bar);
+                            tma_load<PAIR>(b + r * kSliceBytes, &maps.b, int(col0 + 64 * r), int(d), gb, bar);
                     }
                 }
             }
-            if (ctl->abort)  // copies in flight land before the block ends
-                for (uint32_t i = n > t.stages ? n - t.stages : 0; i < n; ++i)
-                    for (uint32_t k = 0; k < 1u << 16; ++k)
-                        if (mbar_try_wait(smem_u32(&ctl->full[i % t.stages]), i / t.stages & 1)) break;
+            if (ctl->abort && rank == 0)  // copies in flight (a pair's: both blocks') land before the block ends
+                for (uint32_t i = 0; i < min(ring.used, t.stages); ++i) {
+                    const uint32_t back = ring.s > i ? ring.s - 1 - i : ring.s + t.stages - 1 - i;
+                    drain(&ctl->full[back], ring.s > i ? ring.phase : ring.phase ^ 1);
+                }
         }
         __syncwarp();
     } else if (warp == 1) {
-        Walk walk(p, t, offsets, first);
-        Tile o;
-        uint32_t n = 0, tiles = 0;
-        bool ok = true;
-        const uint32_t step_a = p.a.depth_major ? 2 : 128, step_b = p.b.depth_major ? 2 : 128;
-        const uint32_t slices = 2 + (t.bn + 63) / 64;
-        while (ok && walk.take(o)) {
-            const uint32_t buf = tiles & 1;
-            ok = __all_sync(0xFFFFFFFFu, wait(ctl, &ctl->acc_empty[buf], (tiles >> 1 & 1) ^ 1));
-            if (!ok) break;
-            tmem_fence_after();
-            const uint32_t acc = tmem + buf * buffer_cols;
-            for (uint32_t i = 0; i < o.blocks; ++i, ++n) {
-                const uint32_t s = n % t.stages;
-                ok = __all_sync(0xFFFFFFFFu, wait(ctl, &ctl->full[s], n / t.stages & 1));
+        if (rank == 0) {
+            Walk walk(p, t, offsets, first);
+            Tile o;
+            Ring ring{t.stages};
+            uint32_t tiles = 0;
+            bool ok = true;
+            const uint32_t step_a = p.a.depth_major ? 2 : 128, step_b = p.b.depth_major ? 2 : 128;
+            const bool cut = p.schedule == kDepth || p.skip_depth;
+            while (ok && walk.take(o)) {
+                const uint32_t buf = tiles & 1;
+                ok = __all_sync(0xFFFFFFFFu, wait<PAIR>(ctl, &ctl->acc_empty[buf], (tiles >> 1 & 1) ^ 1));
                 if (!ok) break;
-                uint8_t* stage = smem + s * t.stage_bytes;
-                uint32_t steps = 4;
-                if (p.schedule == kDepth || p.skip_depth) {
-                    // depths past the group's end belong to its neighbour, and skipped ones may hold anything:
-                    // both operands' lines are cleared (rows are contiguous here, a depth is one line of each slice)
-                    const uint32_t left = o.depth_end - (o.d0 + i * kDepthTile);
-                    uint64_t clear = p.skip_depth ? p.skip_depth[(o.d0 + i * kDepthTile) / 64] : 0;
-                    if (left < kDepthTile) {
-                        steps = (left + 15) / 16;
-                        clear |= ~0ull << left;
-                        if (steps < 4) clear &= (1ull << 16 * steps) - 1;
-                    }
-                    if (clear) {
-                        for (uint64_t m = clear; m; m &= m - 1) {
-                            const uint32_t line = __ffsll(m) - 1;
-                            for (uint32_t q = lane; q < slices * 8; q += 32)
-                                *reinterpret_cast<uint4*>(stage + q / 8 * kSliceBytes + line * 128 + q % 8 * 16) =
-                                    make_uint4(0, 0, 0, 0);
-                        }
-                        fence_async_shared();
-                        __syncwarp();
-                    }
-                }
                 tmem_fence_after();
-                if (lane == 0) {
-                    const uint64_t a = matrix_descriptor(smem_u32(stage), p.a.depth_major);
-                    const uint64_t b = matrix_descriptor(smem_u32(stage + kAStage), p.b.depth_major);
-                    for (uint32_t k = 0; k < steps; ++k) mma(acc, a + k * step_a, b + k * step_b, t.idesc, i || k);
-                    mma_commit(smem_u32(&ctl->empty[s]));
-                    if (i + 1 == o.blocks) mma_commit(smem_u32(&ctl->acc_full[buf]));
+                const uint32_t acc = tmem + buf * buffer_cols;
+                for (uint32_t i = 0; i < o.blocks; ++i, ring.advance()) {
+                    const uint32_t s = ring.s;
+                    ok = __all_sync(0xFFFFFFFFu, wait<PAIR>(ctl, &ctl->full[s], ring.phase));
+                    if (!ok) break;
+                    tmem_fence_after();
+                    if (lane == 0) {
+                        uint32_t steps = 4;
+                        if (cut) steps = min(4u, (o.depth_end - (o.d0 + i * kDepthTile) + 15) / 16);
+                        const uint32_t stage = smem_u32(smem + s * t.stage_bytes);
+                        const uint64_t a = matrix_descriptor(stage, p.a.depth_major);
+                        const uint64_t b = matrix_descriptor(stage + kAStage, p.b.depth_major);
+                        for (uint32_t k = 0; k < steps; ++k) mma<PAIR>(acc, a + k * step_a, b + k * step_b, t.idesc, i || k);
+                        mma_commit<PAIR>(smem_u32(&ctl->empty[s]));
+                        if (i + 1 == o.blocks) mma_commit<PAIR>(smem_u32(&ctl->acc_full[buf]));
+                    }
+                    __syncwarp();
+                }
+                if (o.blocks == 0 && lane < t.pair) {  // nothing to add up: the epilogues take zeros
+                    if (PAIR) cluster_arrive(cluster_address(smem_u32(&ctl->acc_full[buf]), lane));
+                    else mbar_arrive(smem_u32(&ctl->acc_full[buf]));
                 }
                 __syncwarp();
+                ++tiles;
             }
-            if (o.blocks == 0 && lane == 0) mbar_arrive(smem_u32(&ctl->acc_full[buf]));
-            __syncwarp();
-            ++tiles;
-        }
-        if (ctl->abort && lane == 0) {  // products in flight end before TMEM is freed
-            mma_commit(smem_u32(&ctl->drain));
-            for (uint32_t k = 0; k < 1u << 16; ++k)
-                if (mbar_try_wait(smem_u32(&ctl->drain), 0)) break;
+            if (ctl->abort && lane == 0) {  // products in flight end before TMEM is freed
+                mma_commit<PAIR>(smem_u32(&ctl->drain));
+                drain(&ctl->drain, 0);
+            }
         }
         __syncwarp();
     } else {
@@ -524,11 +643,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float alpha = EPI == kStore && p.st.alpha ? *p.st.alpha : 1.f;
         while (walk.take(o)) {
             const uint32_t buf = tiles & 1;
-            if (!__all_sync(0xFFFFFFFFu, wait(ctl, &ctl->acc_full[buf], tiles >> 1 & 1))) break;
+            if (!__all_sync(0xFFFFFFFFu, wait<PAIR>(ctl, &ctl->acc_full[buf], tiles >> 1 & 1))) break;
             tmem_fence_after();
             const uint32_t acc = tmem + buf * buffer_cols + (quarter * 32 << 16);
             const uint32_t lane_row = quarter * 32 + lane;
             if (!SPLIT) {
+                o.row0 += rank * kRowsTile;
                 finish_tile<EPI>(p, t, o, acc, lane_row, o.blocks == 0, alpha);
             } else {
                 // partial sums to shared memory, rows bn + 4 floats apart (no bank conflicts for 16-byte access)
@@ -548,7 +668,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             tmem_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&ctl->acc_empty[buf]));
+            if (lane == 0) {
+                if (PAIR) cluster_arrive(cluster_address(smem_u32(&ctl->acc_empty[buf]), 0));
+                else mbar_arrive(smem_u32(&ctl->acc_empty[buf]));
+            }
             ++tiles;
         }
     }
@@ -579,8 +702,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     tmem_fence_before();
     __syncthreads();
+    if (PAIR) cluster_sync();  // no arrival reaches a block that has ended
     tmem_fence_after();
-    if (warp == 1) tmem_free(tmem, t.tmem_cols);
+    if (warp == 1) tmem_free<PAIR>(tmem, t.tmem_cols);
     if (threadIdx.x == 0 && ctl->abort && p.status) atomicCAS(p.status, 0, int(UZIP_ERR_TIMEOUT));
 }
 
@@ -605,7 +729,7 @@ EncodeFn encode_fn() {
 }
 
 // rows x depth x groups of 16-bit values, read in swizzled boxes of 64 contiguous values
-cudaError_t make_map(CUtensorMap* map, const Operand& o, uint64_t rows, uint64_t depth, uint64_t groups, uint32_t box_rows,
+cudaError_t make_map(CUtensorMap* map, const Operand& o, uint64_t rows, uint64_t depth, uint64_t groups, uint32_t box_outer,
                      int dtype) {
     const uint64_t inner = o.depth_major ? depth : rows, outer = o.depth_major ? rows : depth;
     if (inner == 0 || outer == 0) {  // nothing to load
@@ -617,7 +741,7 @@ cudaError_t make_map(CUtensorMap* map, const Operand& o, uint64_t rows, uint64_t
     const cuuint64_t dims[3] = {inner, outer, groups};
     const uint64_t group = groups > 1 ? o.group * 2 : std::min<uint64_t>(o.ld * 2 * outer, uint64_t(1) << 39);
     const cuuint64_t strides[2] = {o.ld * 2, group};
-    const cuuint32_t box[3] = {kDepthTile, o.depth_major ? box_rows : kDepthTile, 1}, ones[3] = {1, 1, 1};
+    const cuuint32_t box[3] = {64, box_outer, 1}, ones[3] = {1, 1, 1};
     const CUresult r = fn(map, dtype == UZIP_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,
                           const_cast<void*>(o.p), dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
                           CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
@@ -633,10 +757,19 @@ constexpr uint32_t kSmemMost = 227 * 1024;
 // (2 cycles a column), its way into shared memory (about 64 bytes a cycle) and
 // the HBM share of the operand that is read once (about 3500 bytes a cycle
 // for the whole GPU); tiles come in waves of one block per SM.
+uint64_t row_tiles_of(const Product& p, uint32_t pair) {
+    const uint64_t unit = kRowsTile * pair;
+    return p.schedule == kRows ? p.m / unit + p.groups : (p.m + unit - 1) / unit;  // grouped: at most
+}
+uint64_t most_tiles(const Product& p, const Tiling& t) {
+    return row_tiles_of(p, t.pair) * ((p.n + t.bn - 1) / t.bn) * (p.schedule == kDepth ? p.groups : 1);
+}
+
 Tiling choose(const Product& p, int sms) {
     Tiling best{};
     double best_cost = 1e300;
-    const uint64_t rows = p.m, row_tiles = p.schedule == kRows ? rows / kRowsTile + p.groups : (rows + kRowsTile - 1) / kRowsTile;
+    const uint64_t rows = p.m, row_tiles = row_tiles_of(p, 1);
+    best.pair = 1;
     const uint64_t groups = p.schedule == kDepth ? p.groups : 1;
     const double blocks = std::max(1.0, double(p.depth) / (p.schedule == kDepth ? p.groups : 1) / kDepthTile);
     const uint32_t low = uint32_t(std::min<uint64_t>(kRowsTile, (rows + 7) / 8 * 8));
@@ -661,8 +794,22 @@ Tiling choose(const Product& p, int sms) {
             }
         }
     }
+    // pairs: half of B's bytes a block, at full rate from 7 stages
+    if (p.m > kRowsTile)
+        for (uint32_t bn : {256u, 128u}) {
+            const uint64_t tiles = row_tiles_of(p, 2) * ((p.n + bn - 1) / bn) * groups;
+            const double waves = std::ceil(double(tiles) / (sms / 2));
+            const double cost = waves * (blocks * std::max(1.6 * bn, 300.0) + 4.0 * bn) + 2500;
+            if (cost < best_cost) {
+                best_cost = cost;
+                best.bn = bn;
+                best.splits = 1;
+                best.pair = 2;
+            }
+        }
     Tiling& t = best;
-    const uint32_t b_bytes = p.b.depth_major ? t.bn * 128 : (t.bn + 63) / 64 * kSliceBytes;
+    const uint32_t b_cols = t.bn / t.pair;
+    const uint32_t b_bytes = p.b.depth_major ? b_cols * 128 : (b_cols + 63) / 64 * kSliceBytes;
     t.stage_bytes = kAStage + b_bytes;
     const uint32_t tables = p.schedule == kDense ? 0 : (2 * p.groups + 2) * 4;
     const uint32_t rest = 1024 + sizeof(Control) + tables;
@@ -672,11 +819,11 @@ Tiling choose(const Product& p, int sms) {
     uint32_t cols = 32;
     while (cols < 2 * ((t.bn + 31) / 32 * 32)) cols *= 2;
     t.tmem_cols = cols;
-    t.raster = 16;
-    t.a_box = p.schedule == kRows ? (rows / std::max(1u, p.groups) >= 96 ? kRowsTile : 32) : low;
+    t.raster = 16 / t.pair;
+    t.a_box = t.pair == 2 ? kRowsTile : p.schedule == kRows ? (rows / std::max(1u, p.groups) >= 96 ? kRowsTile : 32) : low;
     const uint32_t fmt = p.dtype == UZIP_BF16 ? 1 : 0;
     t.idesc = 1u << 4 | fmt << 7 | fmt << 10 | (p.a.depth_major ? 0u : 1u << 15) | (p.b.depth_major ? 0u : 1u << 16) |
-              (t.bn >> 3) << 17 | (kRowsTile >> 4) << 24;
+              (t.bn >> 3) << 17 | (kRowsTile * t.pair >> 4) << 24;
     const StoreEpilogue& e = p.st;
     const uint32_t out_unit = e.out_fp32 ? 4 : 8;
     t.vec = (aligned16(e.out) && e.ldo % out_unit == 0 && e.out_group % out_unit == 0 ? 1 : 0) |
@@ -685,9 +832,9 @@ Tiling choose(const Product& p, int sms) {
     return t;
 }
 
-template <int EPI, bool SPLIT>
-cudaError_t launch(const Product& p, const Tiling& t, int sms, const CUtensorMap& a, const CUtensorMap& b, cudaStream_t s) {
-    auto kern = product_kernel<EPI, SPLIT>;
+template <int EPI, int MODE>
+cudaError_t launch(const Product& p, const Tiling& t, int sms, const Maps& maps, cudaStream_t s) {
+    auto kern = product_kernel<EPI, MODE>;
     static std::atomic<uint64_t> ready{0};  // devices on which the kernel may use all of the shared memory
     int dev = 0;
     cudaError_t err = cudaGetDevice(&dev);
@@ -697,21 +844,28 @@ cudaError_t launch(const Product& p, const Tiling& t, int sms, const CUtensorMap
         if (err != cudaSuccess) return err;
         if (dev < 64) ready.fetch_or(uint64_t(1) << dev, std::memory_order_relaxed);
     }
-    const uint64_t col_tiles = (p.n + t.bn - 1) / t.bn;
-    const uint64_t row_tiles = p.schedule == kRows ? p.m / kRowsTile + p.groups : (p.m + kRowsTile - 1) / kRowsTile;
-    const uint64_t tiles = row_tiles * col_tiles * (p.schedule == kDepth ? p.groups : 1);
+    const uint64_t tiles = most_tiles(p, t);
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(uint32_t(SPLIT ? tiles * t.splits : std::min<uint64_t>(tiles, sms)));
+    cfg.gridDim = dim3(uint32_t(MODE == 1   ? tiles * t.splits
+                                : MODE == 2 ? 2 * std::min<uint64_t>(tiles, sms / 2)
+                                            : std::min<uint64_t>(tiles, sms)));
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = t.smem;
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = t.splits;
+    attr[0].val.clusterDim.x = t.splits * t.pair;
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = SPLIT ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, kern, p, t, a, b);
+    cfg.numAttrs = MODE ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, kern, p, t, maps);
+}
+
+template <int EPI>
+cudaError_t launch_mode(const Product& p, const Tiling& t, int sms, const Maps& maps, cudaStream_t s) {
+    if (t.pair == 2) return launch<EPI, 2>(p, t, sms, maps, s);
+    if (EPI == kStore && t.splits > 1) return launch<EPI, EPI == kStore ? 1 : 0>(p, t, sms, maps, s);
+    return launch<EPI, 0>(p, t, sms, maps, s);
 }
 
 }  // namespace
@@ -721,14 +875,21 @@ uint32_t product_tile_columns(const Product& p, int sms) { return choose(p, sms)
 cudaError_t launch_product(const Product& p, int sms, cudaStream_t s) {
     if (p.m == 0 || p.n == 0) return cudaSuccess;
     const Tiling t = choose(p, sms);
-    CUtensorMap a, b;
-    cudaError_t err = make_map(&a, p.a, p.m, p.depth, 1, t.a_box, p.dtype);
-    if (err == cudaSuccess) err = make_map(&b, p.b, p.n, p.depth, p.schedule == kRows ? p.groups : 1, t.bn, p.dtype);
+    Maps maps;
+    const uint32_t bgroups = p.schedule == kRows ? p.groups : 1;
+    cudaError_t err = make_map(&maps.a, p.a, p.m, p.depth, 1, p.a.depth_major ? t.a_box : kDepthTile, p.dtype);
+    if (err == cudaSuccess) err = make_map(&maps.b, p.b, p.n, p.depth, bgroups, p.b.depth_major ? t.bn / t.pair : kDepthTile, p.dtype);
+    if (p.schedule == kDepth || p.skip_depth) {
+        if (err == cudaSuccess) err = make_map(&maps.a_lines, p.a, p.m, p.depth, 1, kLines, p.dtype);
+        if (err == cudaSuccess) err = make_map(&maps.a_line, p.a, p.m, p.depth, 1, 1, p.dtype);
+        if (err == cudaSuccess) err = make_map(&maps.b_lines, p.b, p.n, p.depth, 1, kLines, p.dtype);
+        if (err == cudaSuccess) err = make_map(&maps.b_line, p.b, p.n, p.depth, 1, 1, p.dtype);
+    }
     if (err != cudaSuccess) return err;
     switch (p.epilogue) {
-        case kLossStats: return launch<kLossStats, false>(p, t, sms, a, b, s);
-        case kLossGrad: return launch<kLossGrad, false>(p, t, sms, a, b, s);
-        default: return t.splits > 1 ? launch<kStore, true>(p, t, sms, a, b, s) : launch<kStore, false>(p, t, sms, a, b, s);
+        case kLossStats: return launch_mode<kLossStats>(p, t, sms, maps, s);
+        case kLossGrad: return launch_mode<kLossGrad>(p, t, sms, maps, s);
+        default: return launch_mode<kStore>(p, t, sms, maps, s);
     }
 }
 
