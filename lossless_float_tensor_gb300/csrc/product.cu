@@ -32,8 +32,8 @@ constexpr uint32_t kAStage = kRowsTile * kDepthTile * 2;
 constexpr uint32_t kMaxStages = 12;
 constexpr uint32_t kThreads = 192;  // TMA warp, MMA warp, four epilogue warps
 constexpr uint32_t kLines = 8;      // lines of the smaller boxes for depths that are cut
-constexpr uint64_t kWaitLimitNs = 4000000000;  // a wait gives up after four seconds,
-constexpr uint64_t kDrainLimitNs = 50000000;   // one for copies or products in flight then after 50 ms
+constexpr int64_t kWaitLimit = 8000000000;  // clock cycles: a wait gives up after about four seconds,
+constexpr int64_t kDrainLimit = 100000000;  // one for copies or products in flight then after 50 ms
 
 struct Tiling {
     uint32_t bn;       // columns of a tile
@@ -131,6 +131,16 @@ __device__ __forceinline__ void tmem_load32(uint32_t addr, float v[32]) {
 #pragma unroll
     for (uint32_t i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
 }
+// True in one lane of a converged warp.  The compiler knows that one lane is
+// left, so the TMA and MMA instructions behind it take their operands straight
+// from uniform registers; behind `lane == 0` each of them cost 100 cycles more.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t one;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(one));
+    return one != 0;
+}
 __device__ __forceinline__ uint32_t cluster_rank() {
     uint32_t r;
     asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
@@ -169,11 +179,6 @@ __device__ __forceinline__ bool try_wait(uint32_t bar, uint32_t parity) {
             : "memory");
     return done != 0;
 }
-__device__ __forceinline__ uint64_t now_ns() {
-    uint64_t v;
-    asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(v));
-    return v;
-}
 __device__ __forceinline__ float4 cluster_load4(uint32_t addr) {
     float4 v;
     asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr));
@@ -197,22 +202,24 @@ struct Control {
 // behind it, for the grouped schedules: int32 offsets[groups + 1], then (kRows)
 // first row tile of each group, int32 [groups + 1]
 
+// (the clock is read only after 64 tries: reading a timer costs more than most waits)
 template <bool PAIR>
 __device__ __forceinline__ bool wait(Control* c, uint64_t* bar, uint32_t parity) {
     const uint32_t b = smem_u32(bar);
-    if (try_wait<PAIR>(b, parity)) return true;
-    const uint64_t end = now_ns() + kWaitLimitNs;
+    for (uint32_t i = 0; i < 64; ++i)
+        if (try_wait<PAIR>(b, parity)) return true;
+    const int64_t start = clock64();
     do {
-        for (uint32_t i = 0; i < 32; ++i)
+        for (uint32_t i = 0; i < 64; ++i)
             if (try_wait<PAIR>(b, parity)) return true;
         if (c->abort) return false;
-    } while (now_ns() < end);
+    } while (clock64() - start < kWaitLimit);
     c->abort = 1;
     return false;
 }
 __device__ __forceinline__ void drain(uint64_t* bar, uint32_t parity) {
-    const uint64_t end = now_ns() + kDrainLimitNs;
-    while (!try_wait<true>(smem_u32(bar), parity) && now_ns() < end) {
+    const int64_t start = clock64();
+    while (!try_wait<true>(smem_u32(bar), parity) && clock64() - start < kDrainLimit) {
     }
 }
 
@@ -231,22 +238,24 @@ struct Tile {
     uint32_t d0, blocks, depth_end;
 };
 
+// The launch's tiles in the order in which this block takes them.  All of its
+// numbers are copies: the roles' loops touch no parameter memory.
 struct Walk {
-    const Product& p;
-    const Tiling& t;
     const int32_t *offsets, *first;  // shared memory
+    uint32_t schedule, rows, depth, bn, splits, raster;
     uint32_t tile_rows, row_tiles, col_tiles, total, step, next, group, split;
 
-    __device__ Walk(const Product& p, const Tiling& t, const int32_t* offsets, const int32_t* first)
-        : p(p), t(t), offsets(offsets), first(first) {
+    __device__ __forceinline__ Walk(const Product& p, const Tiling& t, const int32_t* offsets, const int32_t* first)
+        : offsets(offsets), first(first), schedule(p.schedule), rows(uint32_t(p.m)), depth(uint32_t(p.depth)), bn(t.bn),
+          splits(t.splits), raster(t.raster) {
         tile_rows = kRowsTile * t.pair;
-        col_tiles = (uint32_t(p.n) + t.bn - 1) / t.bn;
-        row_tiles = p.schedule == kRows ? uint32_t(first[p.groups]) : (uint32_t(p.m) + tile_rows - 1) / tile_rows;
-        total = row_tiles * col_tiles * (p.schedule == kDepth ? p.groups : 1);
-        const uint32_t cluster = t.splits * t.pair;  // one of the two is 1
+        col_tiles = (uint32_t(p.n) + bn - 1) / bn;
+        row_tiles = schedule == kRows ? uint32_t(first[p.groups]) : (rows + tile_rows - 1) / tile_rows;
+        total = row_tiles * col_tiles * (schedule == kDepth ? p.groups : 1);
+        const uint32_t cluster = splits * t.pair;  // one of the two is 1
         step = gridDim.x / cluster;
         next = blockIdx.x / cluster;
-        split = blockIdx.x % t.splits;
+        split = blockIdx.x % splits;
         group = 0;
     }
     __device__ __forceinline__ bool take(Tile& o) {
@@ -255,33 +264,33 @@ struct Walk {
         next += step;
         o.group = 0;
         o.d0 = 0;
-        o.depth_end = uint32_t(p.depth);
-        if (p.schedule == kRows) {
+        o.depth_end = depth;
+        if (schedule == kRows) {
             while (uint32_t(first[group + 1]) * col_tiles <= id) ++group;
-            const uint32_t rows = first[group + 1] - first[group];
+            const uint32_t some = first[group + 1] - first[group];
             id -= first[group] * col_tiles;
             o.group = group;
-            o.col_tile = id / rows;
-            o.row0 = offsets[group] + id % rows * tile_rows;
+            o.col_tile = id / some;
+            o.row0 = offsets[group] + id % some * tile_rows;
             o.row_end = offsets[group + 1];
         } else {
-            if (p.schedule == kDepth) {
+            if (schedule == kDepth) {
                 const uint32_t per = row_tiles * col_tiles;
                 o.group = id / per;
                 id -= o.group * per;
                 o.d0 = offsets[o.group];
                 o.depth_end = offsets[o.group + 1];
             }
-            const uint32_t band = id / (t.raster * col_tiles), in = id - band * t.raster * col_tiles;
-            const uint32_t rows = min(t.raster, row_tiles - band * t.raster);
-            o.row0 = (band * t.raster + in % rows) * tile_rows;
-            o.col_tile = in / rows;
-            o.row_end = uint32_t(p.m);
+            const uint32_t band = id / (raster * col_tiles), in = id - band * raster * col_tiles;
+            const uint32_t some = min(raster, row_tiles - band * raster);
+            o.row0 = (band * raster + in % some) * tile_rows;
+            o.col_tile = in / some;
+            o.row_end = rows;
         }
-        o.col0 = o.col_tile * t.bn;
+        o.col0 = o.col_tile * bn;
         o.blocks = (o.depth_end - o.d0 + kDepthTile - 1) / kDepthTile;
-        if (t.splits > 1) {
-            const uint32_t lo = o.blocks * split / t.splits, hi = o.blocks * (split + 1) / t.splits;
+        if (splits > 1) {
+            const uint32_t lo = o.blocks * split / splits, hi = o.blocks * (split + 1) / splits;
             o.d0 += lo * kDepthTile;
             o.blocks = hi - lo;
         }
@@ -456,7 +465,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     Control* ctl = reinterpret_cast<Control*>(smem + t.stages * t.stage_bytes);
     int32_t* offsets = reinterpret_cast<int32_t*>(ctl + 1);
     int32_t* first = offsets + p.groups + 1;
-    const uint32_t warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const uint32_t warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x / 32, 0), lane = threadIdx.x % 32;
     const uint32_t rank = PAIR ? cluster_rank() : 0;  // the pair's block 0 issues the products
 
     // the cut of the rows or depths, checked whole
@@ -518,22 +527,28 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t buffer_cols = t.tmem_cols / 2;
 
     if (warp == 0) {
-        if (lane == 0) {
+        {
             Walk walk(p, t, offsets, first);
             Tile o;
             Ring ring{t.stages};
             bool ok = true;
             const uint32_t b_cols = t.bn / t.pair, b_slices = (b_cols + 63) / 64;
-            const bool cut = p.schedule == kDepth || p.skip_depth;
+            const uint64_t* const skip = p.skip_depth;
+            const bool cut = walk.schedule == kDepth || skip, by_group = walk.schedule == kRows;
+            const bool a_deep = p.a.depth_major, b_deep = p.b.depth_major;
+            const uint32_t a_box = t.a_box, stage_bytes = t.stage_bytes, blocks_of_tile = t.pair, depth = walk.depth;
+            const uint32_t base = smem_u32(smem);
             while (ok && walk.take(o)) {
                 const uint32_t row0 = o.row0 + rank * kRowsTile, col0 = o.col0 + rank * b_cols;
-                const uint32_t a_rows = PAIR ? kRowsTile : min(kRowsTile, (o.row_end - row0 + t.a_box - 1) / t.a_box * t.a_box);
-                const int gb = p.schedule == kRows ? int(o.group) : 0;
+                const uint32_t a_rows = PAIR ? kRowsTile : min(kRowsTile, (o.row_end - row0 + a_box - 1) / a_box * a_box);
+                const int gb = by_group ? int(o.group) : 0;
                 for (uint32_t i = 0; i < o.blocks; ++i, ring.advance()) {
                     const uint32_t s = ring.s;
-                    if (!(ok = wait<PAIR>(ctl, &ctl->empty[s], ring.phase ^ 1))) break;
+                    ok = __all_sync(0xFFFFFFFFu, wait<PAIR>(ctl, &ctl->empty[s], ring.phase ^ 1));
+                    if (!ok) break;
+                    if (!elect_one()) continue;
                     uint32_t bar = smem_u32(&ctl->full[s]);
-                    const uint32_t a = smem_u32(smem + s * t.stage_bytes), b = a + kAStage;
+                    const uint32_t a = base + s * stage_bytes, b = a + kAStage;
                     const uint32_t d = o.d0 + i * kDepthTile;
                     uint32_t lines = kDepthTile;
                     uint64_t keep = ~0ull;
@@ -543,11 +558,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                             lines = (left + 15) / 16 * 16;
                             keep >>= 64 - left;
                         }
-                        if (p.skip_depth) keep &= ~p.skip_depth[d / 64];
+                        if (skip) keep &= ~skip[d / 64];
                     }
-                    const uint32_t a_bytes = p.a.depth_major ? a_rows * 128 : 2 * 128 * lines;
-                    const uint32_t b_bytes = p.b.depth_major ? b_cols * 128 : b_slices * 128 * lines;
-                    if (rank == 0) mbar_expect_tx(bar, (a_bytes + b_bytes) * t.pair);
+                    const uint32_t a_bytes = a_deep ? a_rows * 128 : 2 * 128 * lines;
+                    const uint32_t b_bytes = b_deep ? b_cols * 128 : b_slices * 128 * lines;
+                    if (rank == 0) mbar_expect_tx(bar, (a_bytes + b_bytes) * blocks_of_tile);
                     if (PAIR) bar = cluster_address(bar, 0);
                     if (~keep) {
                         // Depths past the group's end belong to its neighbour, and skipped ones may hold anything: their
@@ -557,7 +572,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             const uint32_t some = uint32_t(keep >> l) & 0xFF;
                             const uint32_t wide = some == 0xFF || some == 0 ? kLines : 1;
                             for (uint32_t j = l; j < l + kLines; j += wide) {
-                                const int from = int((keep >> j) & 1 ? d + j : uint32_t(p.depth));
+                                const int from = int((keep >> j) & 1 ? d + j : depth);
                                 for (uint32_t r = 0; r < 2; ++r)
                                     tma_load<PAIR>(a + r * kSliceBytes + j * 128, wide > 1 ? &maps.a_lines : &maps.a_line,
                                                    int(row0 + 64 * r), from, 0, bar);
@@ -568,14 +583,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                         continue;
                     }
-                    if (p.a.depth_major) {
-                        for (uint32_t r = 0; r < a_rows; r += t.a_box)
+                    if (a_deep) {
+                        for (uint32_t r = 0; r < a_rows; r += a_box)
                             tma_load<PAIR>(a + r * 128, &maps.a, int(d), int(row0 + r), 0, bar);
                     } else {
                         tma_load<PAIR>(a, &maps.a, int(row0), int(d), 0, bar);
                         tma_load<PAIR>(a + kSliceBytes, &maps.a, int(row0 + 64), int(d), 0, bar);
                     }
-                    if (p.b.depth_major) {
+                    if (b_deep) {
                         tma_load<PAIR>(b, &maps.b, int(d), int(col0), gb, bar);
                     } else {
                         for (uint32_t r = 0; r < b_slices; ++r)
@@ -583,7 +598,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
             }
-            if (ctl->abort && rank == 0)  // copies in flight (a pair's: both blocks') land before the block ends
+            if (ctl->abort && rank == 0 && lane == 0)  // copies in flight (a pair's: both blocks') land before the block ends
                 for (uint32_t i = 0; i < min(ring.used, t.stages); ++i) {
                     const uint32_t back = ring.s > i ? ring.s - 1 - i : ring.s + t.stages - 1 - i;
                     drain(&ctl->full[back], ring.s > i ? ring.phase : ring.phase ^ 1);
@@ -598,7 +613,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint32_t tiles = 0;
             bool ok = true;
             const uint32_t step_a = p.a.depth_major ? 2 : 128, step_b = p.b.depth_major ? 2 : 128;
-            const bool cut = p.schedule == kDepth || p.skip_depth;
+            const bool cut = walk.schedule == kDepth || p.skip_depth;
+            const uint32_t idesc = t.idesc, stage_bytes = t.stage_bytes, blocks_of_tile = t.pair;
+            const uint64_t desc_a = matrix_descriptor(smem_u32(smem), p.a.depth_major);
+            const uint64_t desc_b = matrix_descriptor(smem_u32(smem) + kAStage, p.b.depth_major);
             while (ok && walk.take(o)) {
                 const uint32_t buf = tiles & 1;
                 ok = __all_sync(0xFFFFFFFFu, wait<PAIR>(ctl, &ctl->acc_empty[buf], (tiles >> 1 & 1) ^ 1));
@@ -610,26 +628,25 @@ __global__ void __launch_bounds__(kThreads, 1)
                     ok = __all_sync(0xFFFFFFFFu, wait<PAIR>(ctl, &ctl->full[s], ring.phase));
                     if (!ok) break;
                     tmem_fence_after();
-                    if (lane == 0) {
+                    if (elect_one()) {
                         uint32_t steps = 4;
                         if (cut) steps = min(4u, (o.depth_end - (o.d0 + i * kDepthTile) + 15) / 16);
-                        const uint32_t stage = smem_u32(smem + s * t.stage_bytes);
-                        const uint64_t a = matrix_descriptor(stage, p.a.depth_major);
-                        const uint64_t b = matrix_descriptor(stage + kAStage, p.b.depth_major);
-                        for (uint32_t k = 0; k < steps; ++k) mma<PAIR>(acc, a + k * step_a, b + k * step_b, t.idesc, i || k);
+                        const uint64_t at = s * stage_bytes >> 4;
+                        for (uint32_t k = 0; k < steps; ++k)
+                            mma<PAIR>(acc, desc_a + at + k * step_a, desc_b + at + k * step_b, idesc, i || k);
                         mma_commit<PAIR>(smem_u32(&ctl->empty[s]));
                         if (i + 1 == o.blocks) mma_commit<PAIR>(smem_u32(&ctl->acc_full[buf]));
                     }
                     __syncwarp();
                 }
-                if (o.blocks == 0 && lane < t.pair) {  // nothing to add up: the epilogues take zeros
+                if (o.blocks == 0 && lane < blocks_of_tile) {  // nothing to add up: the epilogues take zeros
                     if (PAIR) cluster_arrive(cluster_address(smem_u32(&ctl->acc_full[buf]), lane));
                     else mbar_arrive(smem_u32(&ctl->acc_full[buf]));
                 }
                 __syncwarp();
                 ++tiles;
             }
-            if (ctl->abort && lane == 0) {  // products in flight end before TMEM is freed
+            if (ctl->abort && elect_one()) {  // products in flight end before TMEM is freed
                 mma_commit<PAIR>(smem_u32(&ctl->drain));
                 drain(&ctl->drain, 0);
             }
