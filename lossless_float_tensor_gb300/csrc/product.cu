@@ -454,12 +454,15 @@ __device__ __forceinline__ void finish_tile(const Product& p, const Tiling& t, c
 
 // ---- the kernel -------------------------------------------------------------------------
 
-// MODE: 0 a block by itself, 1 a cluster splits the depth, 2 a pair of blocks
-template <int EPI, int MODE>
+// MODE: 0 a block by itself, 1 a cluster splits the depth, 2 a pair of blocks.
+// LAYOUT: 0 both operands contiguous along the depth, 1 only A, 2 neither, 3
+// neither, with the depth cut by groups or skipped tokens.
+template <int EPI, int MODE, int LAYOUT>
 __global__ void __launch_bounds__(kThreads, 1)
     product_kernel(const __grid_constant__ Product p, const __grid_constant__ Tiling t,
                    const __grid_constant__ Maps maps) {
     constexpr bool SPLIT = MODE == 1, PAIR = MODE == 2;
+    constexpr bool A_DEEP = LAYOUT < 2, B_DEEP = LAYOUT == 0, CUT = LAYOUT == 3;
     extern __shared__ uint8_t raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
     Control* ctl = reinterpret_cast<Control*>(smem + t.stages * t.stage_bytes);
@@ -527,70 +530,68 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t buffer_cols = t.tmem_cols / 2;
 
     if (warp == 0) {
-        {
+        if (elect_one()) {
             Walk walk(p, t, offsets, first);
             Tile o;
             Ring ring{t.stages};
             bool ok = true;
-            const uint32_t b_cols = t.bn / t.pair, b_slices = (b_cols + 63) / 64;
+            const uint32_t b_cols = t.bn / (PAIR ? 2 : 1), b_slices = (b_cols + 63) / 64;
             const uint64_t* const skip = p.skip_depth;
-            const bool cut = walk.schedule == kDepth || skip, by_group = walk.schedule == kRows;
-            const bool a_deep = p.a.depth_major, b_deep = p.b.depth_major;
-            const uint32_t a_box = t.a_box, stage_bytes = t.stage_bytes, blocks_of_tile = t.pair, depth = walk.depth;
+            const bool by_group = walk.schedule == kRows;
+            const uint32_t a_box = t.a_box, stage_bytes = t.stage_bytes, depth = walk.depth;
             const uint32_t base = smem_u32(smem);
             while (ok && walk.take(o)) {
                 const uint32_t row0 = o.row0 + rank * kRowsTile, col0 = o.col0 + rank * b_cols;
                 const uint32_t a_rows = PAIR ? kRowsTile : min(kRowsTile, (o.row_end - row0 + a_box - 1) / a_box * a_box);
+                const uint32_t bytes = ((A_DEEP ? a_rows * 128 : kAStage) + (B_DEEP ? b_cols * 128 : b_slices * kSliceBytes)) *
+                                       (PAIR ? 2 : 1);
                 const int gb = by_group ? int(o.group) : 0;
-                for (uint32_t i = 0; i < o.blocks; ++i, ring.advance()) {
-                    const uint32_t s = ring.s;
-                    ok = __all_sync(0xFFFFFFFFu, wait<PAIR>(ctl, &ctl->empty[s], ring.phase ^ 1));
-                    if (!ok) break;
-                    if (!elect_one()) continue;
-                    uint32_t bar = smem_u32(&ctl->full[s]);
-                    const uint32_t a = base + s * stage_bytes, b = a + kAStage;
-                    const uint32_t d = o.d0 + i * kDepthTile;
-                    uint32_t lines = kDepthTile;
-                    uint64_t keep = ~0ull;
-                    if (cut) {
+                uint32_t d = o.d0;
+                for (uint32_t i = 0; i < o.blocks; ++i, d += kDepthTile, ring.advance()) {
+                    if (!(ok = wait<PAIR>(ctl, &ctl->empty[ring.s], ring.phase ^ 1))) break;
+                    uint32_t bar = smem_u32(&ctl->full[ring.s]);
+                    const uint32_t a = base + ring.s * stage_bytes, b = a + kAStage;
+                    if (CUT) {
                         const uint32_t left = o.depth_end - d;
+                        uint32_t lines = kDepthTile;
+                        uint64_t keep = ~0ull;
                         if (left < kDepthTile) {
                             lines = (left + 15) / 16 * 16;
                             keep >>= 64 - left;
                         }
                         if (skip) keep &= ~skip[d / 64];
-                    }
-                    const uint32_t a_bytes = a_deep ? a_rows * 128 : 2 * 128 * lines;
-                    const uint32_t b_bytes = b_deep ? b_cols * 128 : b_slices * 128 * lines;
-                    if (rank == 0) mbar_expect_tx(bar, (a_bytes + b_bytes) * blocks_of_tile);
-                    if (PAIR) bar = cluster_address(bar, 0);
-                    if (~keep) {
-                        // Depths past the group's end belong to its neighbour, and skipped ones may hold anything: their
-                        // lines are read from beyond the tensor's end, where TMA gives zeros.  (Both operands have
-                        // contiguous rows here: a depth is one line of each slice.)
-                        for (uint32_t l = 0; l < lines; l += kLines) {
-                            const uint32_t some = uint32_t(keep >> l) & 0xFF;
-                            const uint32_t wide = some == 0xFF || some == 0 ? kLines : 1;
-                            for (uint32_t j = l; j < l + kLines; j += wide) {
-                                const int from = int((keep >> j) & 1 ? d + j : depth);
-                                for (uint32_t r = 0; r < 2; ++r)
-                                    tma_load<PAIR>(a + r * kSliceBytes + j * 128, wide > 1 ? &maps.a_lines : &maps.a_line,
-                                                   int(row0 + 64 * r), from, 0, bar);
-                                for (uint32_t r = 0; r < b_slices; ++r)
-                                    tma_load<PAIR>(b + r * kSliceBytes + j * 128, wide > 1 ? &maps.b_lines : &maps.b_line,
-                                                   int(col0 + 64 * r), from, 0, bar);
+                        if (~keep) {
+                            // Depths past the group's end belong to its neighbour, and skipped ones may hold anything:
+                            // their lines are read from beyond the tensor's end, where TMA gives zeros.  (Both operands
+                            // have contiguous rows here: a depth is one line of each slice.)
+                            if (rank == 0) mbar_expect_tx(bar, (2 + b_slices) * 128 * lines * (PAIR ? 2 : 1));
+                            if (PAIR) bar = cluster_address(bar, 0);
+                            for (uint32_t l = 0; l < lines; l += kLines) {
+                                const uint32_t some = uint32_t(keep >> l) & 0xFF;
+                                const uint32_t wide = some == 0xFF || some == 0 ? kLines : 1;
+                                for (uint32_t j = l; j < l + kLines; j += wide) {
+                                    const int from = int((keep >> j) & 1 ? d + j : depth);
+                                    for (uint32_t r = 0; r < 2; ++r)
+                                        tma_load<PAIR>(a + r * kSliceBytes + j * 128, wide > 1 ? &maps.a_lines : &maps.a_line,
+                                                       int(row0 + 64 * r), from, 0, bar);
+                                    for (uint32_t r = 0; r < b_slices; ++r)
+                                        tma_load<PAIR>(b + r * kSliceBytes + j * 128, wide > 1 ? &maps.b_lines : &maps.b_line,
+                                                       int(col0 + 64 * r), from, 0, bar);
+                                }
                             }
+                            continue;
                         }
-                        continue;
                     }
-                    if (a_deep) {
+                    if (rank == 0) mbar_expect_tx(bar, bytes);
+                    if (PAIR) bar = cluster_address(bar, 0);
+                    if (A_DEEP) {
                         for (uint32_t r = 0; r < a_rows; r += a_box)
                             tma_load<PAIR>(a + r * 128, &maps.a, int(d), int(row0 + r), 0, bar);
                     } else {
                         tma_load<PAIR>(a, &maps.a, int(row0), int(d), 0, bar);
                         tma_load<PAIR>(a + kSliceBytes, &maps.a, int(row0 + 64), int(d), 0, bar);
                     }
-                    if (b_deep) {
+                    if (B_DEEP) {
                         tma_load<PAIR>(b, &maps.b, int(d), int(col0), gb, bar);
                     } else {
                         for (uint32_t r = 0; r < b_slices; ++r)
@@ -598,7 +599,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
             }
-            if (ctl->abort && rank == 0 && lane == 0)  // copies in flight (a pair's: both blocks') land before the block ends
+            if (ctl->abort && rank == 0)  // copies in flight (a pair's: both blocks') land before the block ends
                 for (uint32_t i = 0; i < min(ring.used, t.stages); ++i) {
                     const uint32_t back = ring.s > i ? ring.s - 1 - i : ring.s + t.stages - 1 - i;
                     drain(&ctl->full[back], ring.s > i ? ring.phase : ring.phase ^ 1);
@@ -606,47 +607,44 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         __syncwarp();
     } else if (warp == 1) {
-        if (rank == 0) {
+        if (rank == 0 && elect_one()) {
             Walk walk(p, t, offsets, first);
             Tile o;
             Ring ring{t.stages};
             uint32_t tiles = 0;
             bool ok = true;
-            const uint32_t step_a = p.a.depth_major ? 2 : 128, step_b = p.b.depth_major ? 2 : 128;
-            const bool cut = walk.schedule == kDepth || p.skip_depth;
-            const uint32_t idesc = t.idesc, stage_bytes = t.stage_bytes, blocks_of_tile = t.pair;
-            const uint64_t desc_a = matrix_descriptor(smem_u32(smem), p.a.depth_major);
-            const uint64_t desc_b = matrix_descriptor(smem_u32(smem) + kAStage, p.b.depth_major);
+            // 16 depths further: 32 bytes along the depth, or 16 lines
+            constexpr uint32_t kStepA = A_DEEP ? 2 : 128, kStepB = B_DEEP ? 2 : 128;
+            const uint32_t idesc = t.idesc, stage_step = t.stage_bytes >> 4;
+            const uint64_t desc_a = matrix_descriptor(smem_u32(smem), A_DEEP);
+            const uint64_t desc_b = matrix_descriptor(smem_u32(smem) + kAStage, B_DEEP);
             while (ok && walk.take(o)) {
                 const uint32_t buf = tiles & 1;
-                ok = __all_sync(0xFFFFFFFFu, wait<PAIR>(ctl, &ctl->acc_empty[buf], (tiles >> 1 & 1) ^ 1));
-                if (!ok) break;
+                if (!(ok = wait<PAIR>(ctl, &ctl->acc_empty[buf], (tiles >> 1 & 1) ^ 1))) break;
                 tmem_fence_after();
                 const uint32_t acc = tmem + buf * buffer_cols;
                 for (uint32_t i = 0; i < o.blocks; ++i, ring.advance()) {
-                    const uint32_t s = ring.s;
-                    ok = __all_sync(0xFFFFFFFFu, wait<PAIR>(ctl, &ctl->full[s], ring.phase));
-                    if (!ok) break;
+                    if (!(ok = wait<PAIR>(ctl, &ctl->full[ring.s], ring.phase))) break;
                     tmem_fence_after();
-                    if (elect_one()) {
-                        uint32_t steps = 4;
-                        if (cut) steps = min(4u, (o.depth_end - (o.d0 + i * kDepthTile) + 15) / 16);
-                        const uint64_t at = s * stage_bytes >> 4;
-                        for (uint32_t k = 0; k < steps; ++k)
-                            mma<PAIR>(acc, desc_a + at + k * step_a, desc_b + at + k * step_b, idesc, i || k);
-                        mma_commit<PAIR>(smem_u32(&ctl->empty[s]));
-                        if (i + 1 == o.blocks) mma_commit<PAIR>(smem_u32(&ctl->acc_full[buf]));
-                    }
-                    __syncwarp();
+                    const uint64_t a = desc_a + ring.s * stage_step, b = desc_b + ring.s * stage_step;
+                    const uint32_t steps = CUT ? (o.depth_end - (o.d0 + i * kDepthTile) + 15) / 16 : 4;
+                    mma<PAIR>(acc, a, b, idesc, i);
+                    if (!CUT || steps > 1) mma<PAIR>(acc, a + kStepA, b + kStepB, idesc, 1);
+                    if (!CUT || steps > 2) mma<PAIR>(acc, a + 2 * kStepA, b + 2 * kStepB, idesc, 1);
+                    if (!CUT || steps > 3) mma<PAIR>(acc, a + 3 * kStepA, b + 3 * kStepB, idesc, 1);
+                    mma_commit<PAIR>(smem_u32(&ctl->empty[ring.s]));
                 }
-                if (o.blocks == 0 && lane < blocks_of_tile) {  // nothing to add up: the epilogues take zeros
-                    if (PAIR) cluster_arrive(cluster_address(smem_u32(&ctl->acc_full[buf]), lane));
-                    else mbar_arrive(smem_u32(&ctl->acc_full[buf]));
+                if (o.blocks) {
+                    mma_commit<PAIR>(smem_u32(&ctl->acc_full[buf]));
+                } else if (PAIR) {  // nothing to add up: the epilogues take zeros
+                    cluster_arrive(cluster_address(smem_u32(&ctl->acc_full[buf]), 0));
+                    cluster_arrive(cluster_address(smem_u32(&ctl->acc_full[buf]), 1));
+                } else {
+                    mbar_arrive(smem_u32(&ctl->acc_full[buf]));
                 }
-                __syncwarp();
                 ++tiles;
             }
-            if (ctl->abort && elect_one()) {  // products in flight end before TMEM is freed
+            if (ctl->abort) {  // products in flight end before TMEM is freed
                 mma_commit<PAIR>(smem_u32(&ctl->drain));
                 drain(&ctl->drain, 0);
             }
@@ -774,6 +772,7 @@ constexpr uint32_t kSmemMost = 227 * 1024;
 // (2 cycles a column), its way into shared memory (about 64 bytes a cycle) and
 // the HBM share of the operand that is read once (about 3500 bytes a cycle
 // for the whole GPU); tiles come in waves of one block per SM.
+bool cut(const Product& p) { return p.schedule == kDepth || p.skip_depth; }  // depths left out, at a group's end or for skipped tokens
 uint64_t row_tiles_of(const Product& p, uint32_t pair) {
     const uint64_t unit = kRowsTile * pair;
     return p.schedule == kRows ? p.m / unit + p.groups : (p.m + unit - 1) / unit;  // grouped: at most
@@ -792,7 +791,7 @@ Tiling choose(const Product& p, int sms) {
     const uint32_t low = uint32_t(std::min<uint64_t>(kRowsTile, (rows + 7) / 8 * 8));
     const uint32_t unit = p.b.depth_major ? 16 : 64;  // whole slices where rows are contiguous
     const uint32_t widest = uint32_t(std::min<uint64_t>(256, (p.n + unit - 1) / unit * unit));
-    const bool may_split = p.epilogue == kStore && p.schedule == kDense && rows <= 512;
+    const bool may_split = p.epilogue == kStore && p.schedule == kDense && !p.skip_depth && rows <= 512;
     for (uint32_t bn = widest; bn >= unit; bn -= unit) {
         if (bn < 32 && bn < widest) break;
         const uint64_t tiles = row_tiles * ((p.n + bn - 1) / bn) * groups;
@@ -849,9 +848,9 @@ Tiling choose(const Product& p, int sms) {
     return t;
 }
 
-template <int EPI, int MODE>
+template <int EPI, int MODE, int LAYOUT>
 cudaError_t launch(const Product& p, const Tiling& t, int sms, const Maps& maps, cudaStream_t s) {
-    auto kern = product_kernel<EPI, MODE>;
+    auto kern = product_kernel<EPI, MODE, LAYOUT>;
     static std::atomic<uint64_t> ready{0};  // devices on which the kernel may use all of the shared memory
     int dev = 0;
     cudaError_t err = cudaGetDevice(&dev);
@@ -878,11 +877,12 @@ cudaError_t launch(const Product& p, const Tiling& t, int sms, const Maps& maps,
     return cudaLaunchKernelEx(&cfg, kern, p, t, maps);
 }
 
-template <int EPI>
+template <int EPI, int LAYOUT>
 cudaError_t launch_mode(const Product& p, const Tiling& t, int sms, const Maps& maps, cudaStream_t s) {
-    if (t.pair == 2) return launch<EPI, 2>(p, t, sms, maps, s);
-    if (EPI == kStore && t.splits > 1) return launch<EPI, EPI == kStore ? 1 : 0>(p, t, sms, maps, s);
-    return launch<EPI, 0>(p, t, sms, maps, s);
+    constexpr bool kMaySplit = EPI == kStore && LAYOUT != 3;
+    if (t.pair == 2) return launch<EPI, 2, LAYOUT>(p, t, sms, maps, s);
+    if (kMaySplit && t.splits > 1) return launch<EPI, kMaySplit ? 1 : 0, LAYOUT>(p, t, sms, maps, s);
+    return launch<EPI, 0, LAYOUT>(p, t, sms, maps, s);
 }
 
 }  // namespace
@@ -896,18 +896,18 @@ cudaError_t launch_product(const Product& p, int sms, cudaStream_t s) {
     const uint32_t bgroups = p.schedule == kRows ? p.groups : 1;
     cudaError_t err = make_map(&maps.a, p.a, p.m, p.depth, 1, p.a.depth_major ? t.a_box : kDepthTile, p.dtype);
     if (err == cudaSuccess) err = make_map(&maps.b, p.b, p.n, p.depth, bgroups, p.b.depth_major ? t.bn / t.pair : kDepthTile, p.dtype);
-    if (p.schedule == kDepth || p.skip_depth) {
+    if (cut(p)) {
         if (err == cudaSuccess) err = make_map(&maps.a_lines, p.a, p.m, p.depth, 1, kLines, p.dtype);
         if (err == cudaSuccess) err = make_map(&maps.a_line, p.a, p.m, p.depth, 1, 1, p.dtype);
         if (err == cudaSuccess) err = make_map(&maps.b_lines, p.b, p.n, p.depth, 1, kLines, p.dtype);
         if (err == cudaSuccess) err = make_map(&maps.b_line, p.b, p.n, p.depth, 1, 1, p.dtype);
     }
     if (err != cudaSuccess) return err;
-    switch (p.epilogue) {
-        case kLossStats: return launch_mode<kLossStats>(p, t, sms, maps, s);
-        case kLossGrad: return launch_mode<kLossGrad>(p, t, sms, maps, s);
-        default: return launch_mode<kStore>(p, t, sms, maps, s);
-    }
+    if (p.epilogue == kLossStats) return launch_mode<kLossStats, 0>(p, t, sms, maps, s);
+    if (p.epilogue == kLossGrad) return launch_mode<kLossGrad, 0>(p, t, sms, maps, s);
+    if (p.b.depth_major) return launch_mode<kStore, 0>(p, t, sms, maps, s);
+    if (p.a.depth_major) return launch_mode<kStore, 1>(p, t, sms, maps, s);
+    return cut(p) ? launch_mode<kStore, 3>(p, t, sms, maps, s) : launch_mode<kStore, 2>(p, t, sms, maps, s);
 }
 
 }  // namespace uzip
