@@ -31,6 +31,7 @@ constexpr uint32_t kSliceBytes = kDepthTile * 128;  // 64 rows x 64 depths when 
 constexpr uint32_t kAStage = kRowsTile * kDepthTile * 2;
 constexpr uint32_t kMaxStages = 12;
 constexpr uint32_t kThreads = 192;  // TMA warp, MMA warp, four epilogue warps
+constexpr uint32_t kPatchBytes = 32 * 128, kEpilogueBytes = kPatchBytes + 256 * 4;  // an epilogue warp's shared memory
 constexpr uint32_t kLines = 8;      // lines of the smaller boxes for depths that are cut
 constexpr int64_t kWaitLimit = 8000000000;  // clock cycles: a wait gives up after about four seconds,
 constexpr int64_t kDrainLimit = 100000000;  // one for copies or products in flight then after 50 ms
@@ -337,7 +338,7 @@ __device__ __forceinline__ void store8(const Product& p, uint32_t vec, uint32_t 
                                        uint32_t cols, float alpha, float v[8]) {
     const StoreEpilogue& e = p.st;
     float q[8];
-    if (e.alpha) {
+    {
 #pragma unroll
         for (uint32_t j = 0; j < 8; ++j) v[j] *= alpha;
     }
@@ -383,40 +384,105 @@ __device__ __forceinline__ void store8(const Product& p, uint32_t vec, uint32_t 
     }
 }
 
-// One finished accumulator: every lane of the four warps holds a row.
-template <int EPI>
-__device__ __forceinline__ void finish_tile(const Product& p, const Tiling& t, const Tile& o, uint32_t acc, uint32_t lane_row,
-                                            bool empty, float alpha) {
-    const uint64_t row = uint64_t(o.row0) + lane_row;
-    const bool live = row < o.row_end;
-    const uint32_t cols = min(t.bn, uint32_t(p.n) - o.col0);
-    float top = -INFINITY, sum = 0.f;
-    int64_t target = -1;
-    float lse2 = 0.f, weight = 0.f;
-    if (EPI != kStore && live) {
-        target = p.ls.targets[row] - int64_t(p.ls.col0 + o.col0);
-        if (EPI == kLossGrad) {
-            lse2 = p.ls.lse[row] * kLog2e;
-            weight = p.ls.g[row];
-        }
+__device__ __forceinline__ float fast_exp2(float v) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
+
+// An epilogue warp holds a row in each lane, which would read and write memory
+// 16 bytes a row apart.  32 rows x 64 columns of 16-bit values go through 4 KB
+// of shared memory instead (16-byte pieces swizzled by the row, free of bank
+// conflicts both ways), so that 8 lanes touch 128 contiguous bytes of a row.
+constexpr uint32_t kPatchCols = 64;
+struct Patch {
+    uint4* s;  // [32][8]
+    uint32_t lane;
+    __device__ __forceinline__ uint4& at(uint32_t row, uint32_t piece) const { return s[row * 8 + (piece ^ (row & 7))]; }
+    __device__ __forceinline__ void put_row(const uint32_t w[32]) const {
+        __syncwarp();
+#pragma unroll
+        for (uint32_t i = 0; i < 8; ++i) at(lane, i) = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+        __syncwarp();
     }
-    for (uint32_t c = 0; c < cols; c += 32) {
-        float v[32];
-        __syncwarp();  // rows past the end skip the work below
-        if (!empty) {
-            tmem_load32(acc + c, v);
+    __device__ __forceinline__ void take_row(uint32_t w[32]) const {
+        __syncwarp();
+#pragma unroll
+        for (uint32_t i = 0; i < 8; ++i) {
+            const uint4 q = at(lane, i);
+            w[4 * i] = q.x, w[4 * i + 1] = q.y, w[4 * i + 2] = q.z, w[4 * i + 3] = q.w;
+        }
+        __syncwarp();
+    }
+    // rows x cols values from (or to) p, rows ld apart; vec: 16-byte access
+    __device__ __forceinline__ void load(const uint16_t* p, uint64_t ld, uint32_t rows, uint32_t cols, bool vec, uint4 q[8]) const {
+        if (vec && cols % 8 == 0) {
+#pragma unroll
+            for (uint32_t i = 0; i < 8; ++i) {
+                const uint32_t r = 4 * i + lane / 8;
+                q[i] = make_uint4(0, 0, 0, 0);
+                if (r < rows && lane % 8 * 8 < cols) q[i] = *reinterpret_cast<const uint4*>(p + r * ld + lane % 8 * 8);
+            }
         } else {
 #pragma unroll
-            for (uint32_t i = 0; i < 32; ++i) v[i] = 0.f;
-        }
-        if (!live) continue;
-        const uint32_t here = min(32u, cols - c);
-        if (EPI == kStore) {
+            for (uint32_t i = 0; i < 8; ++i) {
+                const uint32_t r = 4 * i + lane / 8, c = lane % 8 * 8;
+                uint32_t w[4] = {};
 #pragma unroll
-            for (uint32_t j = 0; j < 4; ++j)
-                if (8 * j < here)
-                    store8(p, t.vec, o.group, row, o.col0 + c + 8 * j, min(8u, here - 8 * j), alpha, v + 8 * j);
-        } else if (EPI == kLossStats) {
+                for (uint32_t j = 0; j < 8; ++j)
+                    if (r < rows && c + j < cols) w[j / 2] |= uint32_t(p[r * ld + c + j]) << (j % 2 * 16);
+                q[i] = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+        }
+    }
+    __device__ __forceinline__ void put_loaded(const uint4 q[8]) const {
+        __syncwarp();
+#pragma unroll
+        for (uint32_t i = 0; i < 8; ++i) at(4 * i + lane / 8, lane % 8) = q[i];
+    }
+    __device__ __forceinline__ void store(uint16_t* p, uint64_t ld, uint32_t rows, uint32_t cols, bool vec) const {
+        if (vec && cols % 8 == 0) {
+#pragma unroll
+            for (uint32_t i = 0; i < 8; ++i) {
+                const uint32_t r = 4 * i + lane / 8;
+                if (r < rows && lane % 8 * 8 < cols) *reinterpret_cast<uint4*>(p + r * ld + lane % 8 * 8) = at(r, lane % 8);
+            }
+        } else {
+            for (uint32_t r = 0; r < rows; ++r)
+                for (uint32_t c = lane; c < cols; c += 32)
+                    p[r * ld + c] = reinterpret_cast<const uint16_t*>(&at(r, c / 8))[c % 8];
+        }
+    }
+};
+
+// One finished accumulator of a block: 128 rows, one in each lane of the four
+// warps.  `scratch` is this warp's patch, `bias` its copy of the tile's bias.
+template <int EPI>
+__device__ __forceinline__ void finish_tile(const Product& p, const Tiling& t, const Tile& o, uint32_t acc, uint32_t warp_row,
+                                            uint32_t lane, float alpha, uint4* scratch, const float* bias, const uint4 ahead[8]) {
+    const uint64_t row0 = uint64_t(o.row0) + warp_row, row = row0 + lane;
+    const bool live = row < o.row_end, empty = o.blocks == 0;
+    const uint32_t rows = row0 < o.row_end ? uint32_t(min(uint64_t(32), o.row_end - row0)) : 0;
+    const uint32_t cols = min(t.bn, uint32_t(p.n) - o.col0);
+    const Patch patch{scratch, lane};
+    const int dtype = p.dtype;
+    if (EPI == kLossStats) {
+        float top = -INFINITY, sum = 0.f;
+        const int64_t target = live ? p.ls.targets[row] - int64_t(o.col0) : -1;
+        for (uint32_t c = 0; c < cols; c += 32) {
+            float v[32];
+            if (empty) {
+#pragma unroll
+                for (uint32_t i = 0; i < 32; ++i) v[i] = 0.f;
+            } else {
+                tmem_load32(acc + c, v);
+            }
+            const uint32_t here = min(32u, cols - c);
+            if (target >= c && target < int64_t(c + here)) {
+#pragma unroll
+                for (uint32_t i = 0; i < 32; ++i)
+                    if (target == int64_t(c + i)) p.ls.hit[row] = v[i];
+            }
             if (here < 32) {
 #pragma unroll
                 for (uint32_t i = 0; i < 32; ++i)
@@ -426,30 +492,121 @@ __device__ __forceinline__ void finish_tile(const Product& p, const Tiling& t, c
 #pragma unroll
             for (uint32_t i = 1; i < 32; ++i) most = fmaxf(most, v[i]);
             const float next = fmaxf(top, most), base = next == -INFINITY ? 0.f : next * kLog2e;
-            float add = 0.f;
+            float add[4] = {};
 #pragma unroll
-            for (uint32_t i = 0; i < 32; ++i) add += exp2f(fmaf(v[i], kLog2e, -base));
-            sum = sum * exp2f(fmaf(top, kLog2e, -base)) + add;
+            for (uint32_t i = 0; i < 32; ++i) add[i % 4] += fast_exp2(fmaf(v[i], kLog2e, -base));
+            sum = sum * fast_exp2(fmaf(top, kLog2e, -base)) + ((add[0] + add[1]) + (add[2] + add[3]));
             top = next;
-            if (target >= c && target < int64_t(c + here)) {
+            __syncwarp();
+        }
+        if (live) p.ls.part[uint64_t(o.col_tile) * p.m + row] = make_float2(top, sum);
+        return;
+    }
+    if (EPI == kStore && (p.st.out_fp32 || p.st.sum_in)) {  // partial results in 32 bits: few, after long depths
+        for (uint32_t c = 0; c < cols; c += 32) {
+            float v[32];
+            __syncwarp();
+            if (empty) {
 #pragma unroll
-                for (uint32_t i = 0; i < 32; ++i)
-                    if (target == int64_t(c + i)) p.ls.hit[row] = v[i];
+                for (uint32_t i = 0; i < 32; ++i) v[i] = 0.f;
+            } else {
+                tmem_load32(acc + c, v);
             }
-        } else {
-#pragma unroll
-            for (uint32_t i = 0; i < 32; ++i) {
-                float d = exp2f(fmaf(v[i], kLog2e, -lse2));
-                if (target == int64_t(c + i)) d -= 1.f;
-                v[i] = weight == 0.f ? 0.f : weight * d;
-            }
+            if (!live) continue;
 #pragma unroll
             for (uint32_t j = 0; j < 4; ++j)
-                if (8 * j < here)
-                    write8(p.ls.out, row * p.ls.ldo + o.col0 + c + 8 * j, true, min(8u, here - 8 * j), p.dtype, v + 8 * j);
+                if (c + 8 * j < cols)
+                    store8(p, t.vec, o.group, row, o.col0 + c + 8 * j, min(8u, cols - c - 8 * j), alpha, v + 8 * j);
         }
+        __syncwarp();
+        return;
     }
-    if (EPI == kLossStats && live) p.ls.part[uint64_t(o.col_tile) * p.m + row] = make_float2(top, sum);
+    int64_t target = -1;
+    float lse2 = 0.f, weight = 0.f;
+    if (EPI == kLossGrad && live) {
+        target = p.ls.targets[row] - int64_t(p.ls.col0 + o.col0);
+        lse2 = p.ls.lse[row] * kLog2e;
+        weight = p.ls.g[row];
+    }
+    const StoreEpilogue& e = p.st;
+    const bool has_bias = EPI == kStore && e.bias, has_z = EPI == kStore && e.z, has_res = EPI == kStore && e.residual;
+    const uint32_t act = EPI == kStore ? e.act : uint32_t(UZIP_ACT_NONE);
+    uint16_t* const out = EPI == kStore ? static_cast<uint16_t*>(e.out) + o.group * e.out_group + row0 * e.ldo + o.col0
+                                        : static_cast<uint16_t*>(p.ls.out) + row0 * p.ls.ldo + o.col0;
+    const uint64_t ldo = EPI == kStore ? e.ldo : p.ls.ldo;
+    uint4 q[8];
+#pragma unroll
+    for (uint32_t i = 0; i < 8; ++i) q[i] = ahead[i];
+    for (uint32_t c = 0; c < cols; c += kPatchCols) {
+        const uint32_t here = min(kPatchCols, cols - c);
+        uint32_t res[32], zw[32], yw[32];
+        if (has_res) {
+            patch.put_loaded(q);
+            patch.take_row(res);
+            if (c + kPatchCols < cols)
+                patch.load(static_cast<const uint16_t*>(e.residual) + row0 * e.ldr + o.col0 + c + kPatchCols, e.ldr, rows,
+                           min(kPatchCols, cols - c - kPatchCols), t.vec & 4, q);
+        }
+#pragma unroll
+        for (uint32_t half = 0; half < 2; ++half) {
+            if (half && here <= 32) break;
+            float v[32];
+            if (empty) {
+#pragma unroll
+                for (uint32_t i = 0; i < 32; ++i) v[i] = 0.f;
+            } else {
+                tmem_load32(acc + c + 32 * half, v);
+            }
+            if (EPI == kLossGrad) {
+#pragma unroll
+                for (uint32_t i = 0; i < 32; ++i) {
+                    float d = fast_exp2(fmaf(v[i], kLog2e, -lse2));
+                    if (target == int64_t(c + 32 * half + i)) d -= 1.f;
+                    v[i] = weight == 0.f ? 0.f : weight * d;
+                }
+            } else {
+#pragma unroll
+                for (uint32_t i = 0; i < 32; ++i) v[i] *= alpha;
+                if (has_bias) {
+#pragma unroll
+                    for (uint32_t i = 0; i < 32; i += 4) {
+                        const float4 f = *reinterpret_cast<const float4*>(bias + c + 32 * half + i);
+                        v[i] += f.x, v[i + 1] += f.y, v[i + 2] += f.z, v[i + 3] += f.w;
+                    }
+                }
+                if (has_z) {
+#pragma unroll
+                    for (uint32_t i = 0; i < 16; ++i) zw[16 * half + i] = to16x2(v[2 * i], v[2 * i + 1], dtype);
+                }
+                if (act == UZIP_ACT_RELU) {
+#pragma unroll
+                    for (uint32_t i = 0; i < 32; ++i) v[i] = act_value(v[i], UZIP_ACT_RELU);
+                } else if (act == UZIP_ACT_GELU) {
+#pragma unroll
+                    for (uint32_t i = 0; i < 32; ++i) v[i] = act_value(v[i], UZIP_ACT_GELU);
+                } else if (act == UZIP_ACT_SILU) {
+#pragma unroll
+                    for (uint32_t i = 0; i < 32; ++i) v[i] = act_value(v[i], UZIP_ACT_SILU);
+                }
+                if (has_res) {
+#pragma unroll
+                    for (uint32_t i = 0; i < 16; ++i) {
+                        const float2 f = from16x2(res[16 * half + i], dtype);
+                        v[2 * i] += f.x, v[2 * i + 1] += f.y;
+                    }
+                }
+            }
+#pragma unroll
+            for (uint32_t i = 0; i < 16; ++i) yw[16 * half + i] = to16x2(v[2 * i], v[2 * i + 1], dtype);
+        }
+        if (has_z) {
+            patch.put_row(zw);
+            patch.store(static_cast<uint16_t*>(e.z) + row0 * e.ldz + o.col0 + c, e.ldz, rows, here, t.vec & 8);
+        }
+        patch.put_row(yw);
+        patch.store(out + c, ldo, rows, here, t.vec & 1);
+    }
+    __syncwarp();
 }
 
 // ---- the kernel -------------------------------------------------------------------------
@@ -465,7 +622,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr bool A_DEEP = LAYOUT < 2, B_DEEP = LAYOUT == 0, CUT = LAYOUT == 3;
     extern __shared__ uint8_t raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
-    Control* ctl = reinterpret_cast<Control*>(smem + t.stages * t.stage_bytes);
+    Control* ctl = reinterpret_cast<Control*>(smem + t.stages * t.stage_bytes + 4 * kEpilogueBytes);
     int32_t* offsets = reinterpret_cast<int32_t*>(ctl + 1);
     int32_t* first = offsets + p.groups + 1;
     const uint32_t warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x / 32, 0), lane = threadIdx.x % 32;
@@ -547,7 +704,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                                        (PAIR ? 2 : 1);
                 const int gb = by_group ? int(o.group) : 0;
                 uint32_t d = o.d0;
+                uint64_t skip_next = CUT && skip && o.blocks ? skip[d / 64] : 0;
                 for (uint32_t i = 0; i < o.blocks; ++i, d += kDepthTile, ring.advance()) {
+                    const uint64_t skip_now = skip_next;
+                    if (CUT && skip && i + 1 < o.blocks) skip_next = skip[d / 64 + 1];
                     if (!(ok = wait<PAIR>(ctl, &ctl->empty[ring.s], ring.phase ^ 1))) break;
                     uint32_t bar = smem_u32(&ctl->full[ring.s]);
                     const uint32_t a = base + ring.s * stage_bytes, b = a + kAStage;
@@ -559,7 +719,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             lines = (left + 15) / 16 * 16;
                             keep >>= 64 - left;
                         }
-                        if (skip) keep &= ~skip[d / 64];
+                        keep &= ~skip_now;
                         if (~keep) {
                             // Depths past the group's end belong to its neighbour, and skipped ones may hold anything:
                             // their lines are read from beyond the tensor's end, where TMA gives zeros.  (Both operands
@@ -656,16 +816,35 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t tiles = 0;
         const uint32_t quarter = warp % 4;  // the TMEM lanes that this warp may read
         const float alpha = EPI == kStore && p.st.alpha ? *p.st.alpha : 1.f;
+        uint8_t* const mine = reinterpret_cast<uint8_t*>(ctl) - (4 - quarter) * kEpilogueBytes;
+        uint4* const scratch = reinterpret_cast<uint4*>(mine);
+        float* const bias = reinterpret_cast<float*>(mine + kPatchBytes);
         while (walk.take(o)) {
             const uint32_t buf = tiles & 1;
+            uint4 ahead[8] = {};
+            if (!SPLIT) {
+                // what the epilogue reads besides the products is fetched while they run
+                o.row0 += rank * kRowsTile;
+                if (EPI == kStore && p.st.bias) {
+                    const uint16_t* from = static_cast<const uint16_t*>(p.st.bias) + o.group * p.n + o.col0;
+                    const uint32_t cols = min(t.bn, uint32_t(p.n) - o.col0);
+                    for (uint32_t c = lane; c < cols; c += 32) bias[c] = from16(from[c], p.dtype);
+                }
+                if (EPI == kStore && p.st.residual && !p.st.out_fp32) {
+                    const uint64_t row0 = uint64_t(o.row0) + quarter * 32;
+                    const uint32_t rows = row0 < o.row_end ? uint32_t(min(uint64_t(32), o.row_end - row0)) : 0;
+                    Patch{scratch, lane}.load(static_cast<const uint16_t*>(p.st.residual) + row0 * p.st.ldr + o.col0, p.st.ldr,
+                                              rows, min(min(kPatchCols, t.bn), uint32_t(p.n) - o.col0), t.vec & 4, ahead);
+                }
+                __syncwarp();
+            }
             if (!__all_sync(0xFFFFFFFFu, wait<PAIR>(ctl, &ctl->acc_full[buf], tiles >> 1 & 1))) break;
             tmem_fence_after();
             const uint32_t acc = tmem + buf * buffer_cols + (quarter * 32 << 16);
-            const uint32_t lane_row = quarter * 32 + lane;
             if (!SPLIT) {
-                o.row0 += rank * kRowsTile;
-                finish_tile<EPI>(p, t, o, acc, lane_row, o.blocks == 0, alpha);
+                finish_tile<EPI>(p, t, o, acc, quarter * 32, lane, alpha, scratch, bias, ahead);
             } else {
+                const uint32_t lane_row = quarter * 32 + lane;
                 // partial sums to shared memory, rows bn + 4 floats apart (no bank conflicts for 16-byte access)
                 float* part = reinterpret_cast<float*>(smem) + lane_row * (t.bn + 4);
                 for (uint32_t c = 0; c < t.bn; c += 32) {
@@ -828,7 +1007,7 @@ Tiling choose(const Product& p, int sms) {
     const uint32_t b_bytes = p.b.depth_major ? b_cols * 128 : (b_cols + 63) / 64 * kSliceBytes;
     t.stage_bytes = kAStage + b_bytes;
     const uint32_t tables = p.schedule == kDense ? 0 : (2 * p.groups + 2) * 4;
-    const uint32_t rest = 1024 + sizeof(Control) + tables;
+    const uint32_t rest = 1024 + 4 * kEpilogueBytes + sizeof(Control) + tables;
     t.stages = std::min<uint32_t>(kMaxStages, (kSmemMost - rest) / t.stage_bytes);
     // (with splits the partial sums, 512 bn + 2 KiB bytes, take the stages' place: always less)
     t.smem = rest + t.stages * t.stage_bytes;
