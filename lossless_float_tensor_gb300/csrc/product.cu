@@ -29,16 +29,17 @@ constexpr uint32_t kRowsTile = 128;  // accumulator rows of a block: the TMEM la
 constexpr uint32_t kDepthTile = 64;  // depths of a stage: 128 bytes, the swizzle's span
 constexpr uint32_t kSliceBytes = kDepthTile * 128;  // 64 rows x 64 depths when rows are contiguous
 constexpr uint32_t kAStage = kRowsTile * kDepthTile * 2;
-constexpr uint32_t kMaxStages = 12;
+constexpr uint32_t kMaxStages = 24;
 constexpr uint32_t kThreads = 192;  // TMA warp, MMA warp, four epilogue warps
 constexpr uint32_t kPatchBytes = 32 * 128, kEpilogueBytes = kPatchBytes + 256 * 4;  // an epilogue warp's shared memory
-constexpr uint32_t kLines = 8;      // lines of the smaller boxes for depths that are cut
+constexpr uint32_t kHeights = 6;    // boxes of 1 to 32 lines for depths that are cut
 constexpr int64_t kWaitLimit = 8000000000;  // clock cycles: a wait gives up after about four seconds,
 constexpr int64_t kDrainLimit = 100000000;  // one for copies or products in flight then after 50 ms
 
 struct Tiling {
     uint32_t bn;       // columns of a tile
     uint32_t stages;
+    uint32_t a_stage;  // bytes of A in a stage: fewer rows than 128 leave more stages
     uint32_t stage_bytes;
     uint32_t splits;   // blocks of a cluster that share a tile's depth
     uint32_t pair;     // 2: two blocks share a tile of 256 rows, else 1
@@ -186,9 +187,14 @@ __device__ __forceinline__ float4 cluster_load4(uint32_t addr) {
     return v;
 }
 
-// the operands in boxes of a whole stage, and of 8 lines and 1 line for cut depths
+// the operands in boxes of a whole stage, and of 1, 2, 4, ... 32 lines for cut depths
+template <bool CUT>
 struct Maps {
-    CUtensorMap a, b, a_lines, a_line, b_lines, b_line;
+    CUtensorMap a, b;
+};
+template <>
+struct Maps<true> : Maps<false> {
+    CUtensorMap a_lines[kHeights], b_lines[kHeights];
 };
 
 // ---- the block's shared state ------------------------------------------------------
@@ -448,9 +454,11 @@ struct Patch {
                 if (r < rows && lane % 8 * 8 < cols) *reinterpret_cast<uint4*>(p + r * ld + lane % 8 * 8) = at(r, lane % 8);
             }
         } else {
-            for (uint32_t r = 0; r < rows; ++r)
-                for (uint32_t c = lane; c < cols; c += 32)
-                    p[r * ld + c] = reinterpret_cast<const uint16_t*>(&at(r, c / 8))[c % 8];
+#pragma unroll 8
+            for (uint32_t r = 0; r < 32; ++r)
+#pragma unroll
+                for (uint32_t c = lane; c < kPatchCols; c += 32)
+                    if (r < rows && c < cols) p[r * ld + c] = reinterpret_cast<const uint16_t*>(&at(r, c / 8))[c % 8];
         }
     }
 };
@@ -499,7 +507,7 @@ __device__ __forceinline__ void finish_tile(const Product& p, const Tiling& t, c
             top = next;
             __syncwarp();
         }
-        if (live) p.ls.part[uint64_t(o.col_tile) * p.m + row] = make_float2(top, sum);
+        if (live) p.ls.part[row * p.ls.tiles + o.col_tile] = make_float2(top, sum);
         return;
     }
     if (EPI == kStore && (p.st.out_fp32 || p.st.sum_in)) {  // partial results in 32 bits: few, after long depths
@@ -617,7 +625,7 @@ __device__ __forceinline__ void finish_tile(const Product& p, const Tiling& t, c
 template <int EPI, int MODE, int LAYOUT>
 __global__ void __launch_bounds__(kThreads, 1)
     product_kernel(const __grid_constant__ Product p, const __grid_constant__ Tiling t,
-                   const __grid_constant__ Maps maps) {
+                   const __grid_constant__ Maps<LAYOUT == 3> maps) {
     constexpr bool SPLIT = MODE == 1, PAIR = MODE == 2;
     constexpr bool A_DEEP = LAYOUT < 2, B_DEEP = LAYOUT == 0, CUT = LAYOUT == 3;
     extern __shared__ uint8_t raw[];
@@ -695,7 +703,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t b_cols = t.bn / (PAIR ? 2 : 1), b_slices = (b_cols + 63) / 64;
             const uint64_t* const skip = p.skip_depth;
             const bool by_group = walk.schedule == kRows;
-            const uint32_t a_box = t.a_box, stage_bytes = t.stage_bytes, depth = walk.depth;
+            const uint32_t a_box = t.a_box, a_stage = t.a_stage, stage_bytes = t.stage_bytes, depth = walk.depth;
             const uint32_t base = smem_u32(smem);
             while (ok && walk.take(o)) {
                 const uint32_t row0 = o.row0 + rank * kRowsTile, col0 = o.col0 + rank * b_cols;
@@ -710,8 +718,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (CUT && skip && i + 1 < o.blocks) skip_next = skip[d / 64 + 1];
                     if (!(ok = wait<PAIR>(ctl, &ctl->empty[ring.s], ring.phase ^ 1))) break;
                     uint32_t bar = smem_u32(&ctl->full[ring.s]);
-                    const uint32_t a = base + ring.s * stage_bytes, b = a + kAStage;
-                    if (CUT) {
+                    const uint32_t a = base + ring.s * stage_bytes, b = a + a_stage;
+                    if constexpr (CUT) {
                         const uint32_t left = o.depth_end - d;
                         uint32_t lines = kDepthTile;
                         uint64_t keep = ~0ull;
@@ -726,18 +734,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                             // have contiguous rows here: a depth is one line of each slice.)
                             if (rank == 0) mbar_expect_tx(bar, (2 + b_slices) * 128 * lines * (PAIR ? 2 : 1));
                             if (PAIR) bar = cluster_address(bar, 0);
-                            for (uint32_t l = 0; l < lines; l += kLines) {
-                                const uint32_t some = uint32_t(keep >> l) & 0xFF;
-                                const uint32_t wide = some == 0xFF || some == 0 ? kLines : 1;
-                                for (uint32_t j = l; j < l + kLines; j += wide) {
-                                    const int from = int((keep >> j) & 1 ? d + j : depth);
-                                    for (uint32_t r = 0; r < 2; ++r)
-                                        tma_load<PAIR>(a + r * kSliceBytes + j * 128, wide > 1 ? &maps.a_lines : &maps.a_line,
-                                                       int(row0 + 64 * r), from, 0, bar);
-                                    for (uint32_t r = 0; r < b_slices; ++r)
-                                        tma_load<PAIR>(b + r * kSliceBytes + j * 128, wide > 1 ? &maps.b_lines : &maps.b_line,
-                                                       int(col0 + 64 * r), from, 0, bar);
-                                }
+                            for (uint32_t l = 0; l < lines;) {  // runs of kept or cleared lines, in powers of two
+                                const bool kept = keep >> l & 1;
+                                const uint64_t other = (kept ? ~keep : keep) >> l;
+                                const uint32_t run = min(other ? uint32_t(__ffsll(other)) - 1 : 64u, lines - l);
+                                const uint32_t h = min(31u - __clz(run), kHeights - 1);
+                                const int from = int(kept ? d + l : depth);
+                                for (uint32_t r = 0; r < 2; ++r)
+                                    tma_load<PAIR>(a + r * kSliceBytes + l * 128, &maps.a_lines[h], int(row0 + 64 * r), from, 0, bar);
+                                for (uint32_t r = 0; r < b_slices; ++r)
+                                    tma_load<PAIR>(b + r * kSliceBytes + l * 128, &maps.b_lines[h], int(col0 + 64 * r), from, 0, bar);
+                                l += 1u << h;
                             }
                             continue;
                         }
@@ -777,7 +784,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             constexpr uint32_t kStepA = A_DEEP ? 2 : 128, kStepB = B_DEEP ? 2 : 128;
             const uint32_t idesc = t.idesc, stage_step = t.stage_bytes >> 4;
             const uint64_t desc_a = matrix_descriptor(smem_u32(smem), A_DEEP);
-            const uint64_t desc_b = matrix_descriptor(smem_u32(smem) + kAStage, B_DEEP);
+            // (the tensor core reads 128 rows of A also where a stage holds fewer: those accumulator rows are never
+            // stored, and what lies there, the stage's B, later stages or the epilogue's patches, is shared memory of
+            // this block)
+            const uint64_t desc_b = matrix_descriptor(smem_u32(smem) + t.a_stage, B_DEEP);
             while (ok && walk.take(o)) {
                 const uint32_t buf = tiles & 1;
                 if (!(ok = wait<PAIR>(ctl, &ctl->acc_empty[buf], (tiles >> 1 & 1) ^ 1))) break;
@@ -857,7 +867,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
 #pragma unroll
                     for (uint32_t i = 0; i < 32; i += 4)
-                        if (c + i < t.bn) *reinterpret_cast<float4*>(part + c + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+                        if (c + i < t.bn && lane_row < o.row_end - o.row0)
+                            *reinterpret_cast<float4*>(part + c + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
                 }
             }
             tmem_fence_before();
@@ -956,6 +967,11 @@ uint64_t row_tiles_of(const Product& p, uint32_t pair) {
     const uint64_t unit = kRowsTile * pair;
     return p.schedule == kRows ? p.m / unit + p.groups : (p.m + unit - 1) / unit;  // grouped: at most
 }
+// grouped: what ragged groups take on average
+double mean_row_tiles(const Product& p, uint32_t pair) {
+    const uint64_t unit = kRowsTile * pair;
+    return p.schedule == kRows ? double(p.m) / unit + 0.5 * double(std::min<uint64_t>(p.groups, p.m)) : double((p.m + unit - 1) / unit);
+}
 uint64_t most_tiles(const Product& p, const Tiling& t) {
     return row_tiles_of(p, t.pair) * ((p.n + t.bn - 1) / t.bn) * (p.schedule == kDepth ? p.groups : 1);
 }
@@ -963,23 +979,24 @@ uint64_t most_tiles(const Product& p, const Tiling& t) {
 Tiling choose(const Product& p, int sms) {
     Tiling best{};
     double best_cost = 1e300;
-    const uint64_t rows = p.m, row_tiles = row_tiles_of(p, 1);
+    const uint64_t rows = p.m;
+    const double row_tiles = mean_row_tiles(p, 1);
     best.pair = 1;
     const uint64_t groups = p.schedule == kDepth ? p.groups : 1;
     const double blocks = std::max(1.0, double(p.depth) / (p.schedule == kDepth ? p.groups : 1) / kDepthTile);
     const uint32_t low = uint32_t(std::min<uint64_t>(kRowsTile, (rows + 7) / 8 * 8));
     const uint32_t unit = p.b.depth_major ? 16 : 64;  // whole slices where rows are contiguous
     const uint32_t widest = uint32_t(std::min<uint64_t>(256, (p.n + unit - 1) / unit * unit));
-    const bool may_split = p.epilogue == kStore && p.schedule == kDense && !p.skip_depth && rows <= 512;
+    const bool may_split = p.epilogue == kStore && p.schedule == kDense && !p.skip_depth;
     for (uint32_t bn = widest; bn >= unit; bn -= unit) {
         if (bn < 32 && bn < widest) break;
-        const uint64_t tiles = row_tiles * ((p.n + bn - 1) / bn) * groups;
+        const double tiles = row_tiles * double((p.n + bn - 1) / bn * groups);
         for (uint32_t splits = 1; splits <= (may_split ? 8u : 1u); ++splits) {
             if (splits > 1 && blocks / splits < 4) break;
-            const double running = double(std::min<uint64_t>(tiles * splits, sms));
-            const double waves = std::ceil(double(tiles) * splits / sms);
+            const double running = std::min<double>(tiles * splits, sms);
+            const double waves = std::ceil(tiles * splits / sms);
             const double fill = (low * 128.0 + bn * 128.0) / 64;
-            const double hbm = p.schedule == kDense ? bn * 128.0 * running / 3500 / std::min<double>(16, double(row_tiles)) : 0;
+            const double hbm = p.schedule == kDense ? bn * 128.0 * running / 3500 / std::min(16.0, row_tiles) : 0;
             const double stage = std::max({2.0 * bn, fill, hbm, 128.0});
             const double cost = waves * (blocks / splits * stage + 4.0 * bn + (splits > 1 ? 1500 : 0)) + 2000;
             if (cost < best_cost * 0.999) {
@@ -992,8 +1009,8 @@ Tiling choose(const Product& p, int sms) {
     // pairs: half of B's bytes a block, at full rate from 7 stages
     if (p.m > kRowsTile)
         for (uint32_t bn : {256u, 128u}) {
-            const uint64_t tiles = row_tiles_of(p, 2) * ((p.n + bn - 1) / bn) * groups;
-            const double waves = std::ceil(double(tiles) / (sms / 2));
+            const double tiles = mean_row_tiles(p, 2) * double((p.n + bn - 1) / bn * groups);
+            const double waves = std::ceil(tiles / (sms / 2));
             const double cost = waves * (blocks * std::max(1.6 * bn, 300.0) + 4.0 * bn) + 2500;
             if (cost < best_cost) {
                 best_cost = cost;
@@ -1005,7 +1022,10 @@ Tiling choose(const Product& p, int sms) {
     Tiling& t = best;
     const uint32_t b_cols = t.bn / t.pair;
     const uint32_t b_bytes = p.b.depth_major ? b_cols * 128 : (b_cols + 63) / 64 * kSliceBytes;
-    t.stage_bytes = kAStage + b_bytes;
+    const bool few = t.pair == 1 && p.a.depth_major;
+    t.a_box = !few ? kRowsTile : p.schedule != kRows || low < 32 ? low : rows / p.groups >= 96 ? kRowsTile : 32;
+    t.a_stage = few ? (low + t.a_box - 1) / t.a_box * t.a_box * 128 : kAStage;
+    t.stage_bytes = t.a_stage + b_bytes;
     const uint32_t tables = p.schedule == kDense ? 0 : (2 * p.groups + 2) * 4;
     const uint32_t rest = 1024 + 4 * kEpilogueBytes + sizeof(Control) + tables;
     t.stages = std::min<uint32_t>(kMaxStages, (kSmemMost - rest) / t.stage_bytes);
@@ -1015,7 +1035,6 @@ Tiling choose(const Product& p, int sms) {
     while (cols < 2 * ((t.bn + 31) / 32 * 32)) cols *= 2;
     t.tmem_cols = cols;
     t.raster = 16 / t.pair;
-    t.a_box = t.pair == 2 ? kRowsTile : p.schedule == kRows ? (rows / std::max(1u, p.groups) >= 96 ? kRowsTile : 32) : low;
     const uint32_t fmt = p.dtype == UZIP_BF16 ? 1 : 0;
     t.idesc = 1u << 4 | fmt << 7 | fmt << 10 | (p.a.depth_major ? 0u : 1u << 15) | (p.b.depth_major ? 0u : 1u << 16) |
               (t.bn >> 3) << 17 | (kRowsTile * t.pair >> 4) << 24;
@@ -1028,7 +1047,7 @@ Tiling choose(const Product& p, int sms) {
 }
 
 template <int EPI, int MODE, int LAYOUT>
-cudaError_t launch(const Product& p, const Tiling& t, int sms, const Maps& maps, cudaStream_t s) {
+cudaError_t launch(const Product& p, const Tiling& t, int sms, const Maps<LAYOUT == 3>& maps, cudaStream_t s) {
     auto kern = product_kernel<EPI, MODE, LAYOUT>;
     static std::atomic<uint64_t> ready{0};  // devices on which the kernel may use all of the shared memory
     int dev = 0;
@@ -1057,8 +1076,19 @@ cudaError_t launch(const Product& p, const Tiling& t, int sms, const Maps& maps,
 }
 
 template <int EPI, int LAYOUT>
-cudaError_t launch_mode(const Product& p, const Tiling& t, int sms, const Maps& maps, cudaStream_t s) {
-    constexpr bool kMaySplit = EPI == kStore && LAYOUT != 3;
+cudaError_t launch_layout(const Product& p, const Tiling& t, int sms, cudaStream_t s) {
+    constexpr bool kCut = LAYOUT == 3, kMaySplit = EPI == kStore && !kCut;
+    Maps<kCut> maps;
+    cudaError_t err = make_map(&maps.a, p.a, p.m, p.depth, 1, LAYOUT < 2 ? t.a_box : kDepthTile, p.dtype);
+    if (err == cudaSuccess)
+        err = make_map(&maps.b, p.b, p.n, p.depth, p.schedule == kRows ? p.groups : 1, LAYOUT ? kDepthTile : t.bn / t.pair, p.dtype);
+    if constexpr (kCut) {
+        for (uint32_t h = 0; h < kHeights && err == cudaSuccess; ++h) {
+            err = make_map(&maps.a_lines[h], p.a, p.m, p.depth, 1, 1u << h, p.dtype);
+            if (err == cudaSuccess) err = make_map(&maps.b_lines[h], p.b, p.n, p.depth, 1, 1u << h, p.dtype);
+        }
+    }
+    if (err != cudaSuccess) return err;
     if (t.pair == 2) return launch<EPI, 2, LAYOUT>(p, t, sms, maps, s);
     if (kMaySplit && t.splits > 1) return launch<EPI, kMaySplit ? 1 : 0, LAYOUT>(p, t, sms, maps, s);
     return launch<EPI, 0, LAYOUT>(p, t, sms, maps, s);
@@ -1071,22 +1101,11 @@ uint32_t product_tile_columns(const Product& p, int sms) { return choose(p, sms)
 cudaError_t launch_product(const Product& p, int sms, cudaStream_t s) {
     if (p.m == 0 || p.n == 0) return cudaSuccess;
     const Tiling t = choose(p, sms);
-    Maps maps;
-    const uint32_t bgroups = p.schedule == kRows ? p.groups : 1;
-    cudaError_t err = make_map(&maps.a, p.a, p.m, p.depth, 1, p.a.depth_major ? t.a_box : kDepthTile, p.dtype);
-    if (err == cudaSuccess) err = make_map(&maps.b, p.b, p.n, p.depth, bgroups, p.b.depth_major ? t.bn / t.pair : kDepthTile, p.dtype);
-    if (cut(p)) {
-        if (err == cudaSuccess) err = make_map(&maps.a_lines, p.a, p.m, p.depth, 1, kLines, p.dtype);
-        if (err == cudaSuccess) err = make_map(&maps.a_line, p.a, p.m, p.depth, 1, 1, p.dtype);
-        if (err == cudaSuccess) err = make_map(&maps.b_lines, p.b, p.n, p.depth, 1, kLines, p.dtype);
-        if (err == cudaSuccess) err = make_map(&maps.b_line, p.b, p.n, p.depth, 1, 1, p.dtype);
-    }
-    if (err != cudaSuccess) return err;
-    if (p.epilogue == kLossStats) return launch_mode<kLossStats, 0>(p, t, sms, maps, s);
-    if (p.epilogue == kLossGrad) return launch_mode<kLossGrad, 0>(p, t, sms, maps, s);
-    if (p.b.depth_major) return launch_mode<kStore, 0>(p, t, sms, maps, s);
-    if (p.a.depth_major) return launch_mode<kStore, 1>(p, t, sms, maps, s);
-    return cut(p) ? launch_mode<kStore, 3>(p, t, sms, maps, s) : launch_mode<kStore, 2>(p, t, sms, maps, s);
+    if (p.epilogue == kLossStats) return launch_layout<kLossStats, 0>(p, t, sms, s);
+    if (p.epilogue == kLossGrad) return launch_layout<kLossGrad, 0>(p, t, sms, s);
+    if (p.b.depth_major) return launch_layout<kStore, 0>(p, t, sms, s);
+    if (p.a.depth_major) return launch_layout<kStore, 1>(p, t, sms, s);
+    return cut(p) ? launch_layout<kStore, 3>(p, t, sms, s) : launch_layout<kStore, 2>(p, t, sms, s);
 }
 
 }  // namespace uzip

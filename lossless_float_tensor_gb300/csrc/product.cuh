@@ -54,7 +54,8 @@ struct LossEpilogue {
     const int64_t* targets;
     int64_t ignore;
     uint64_t col0;     // class of column 0
-    float2* part;      // kLossStats: [column tiles][rows] maximum, sum
+    float2* part;      // kLossStats: [rows][tiles] maximum, sum of exponentials
+    uint32_t tiles;    // column tiles of the launch
     float* hit;        // kLossStats: [rows] logit of the target
     const float* lse;  // kLossGrad
     const float* g;    // kLossGrad: [rows], scaled
@@ -110,8 +111,8 @@ cudaError_t launch_act_grad(const ActGrad& a, cudaStream_t s);
 // status only, for offsets that do not cut [0, m)
 cudaError_t launch_offset_check(const int64_t* offsets, uint64_t groups, uint64_t m, int32_t* status, cudaStream_t s);
 
-cudaError_t launch_loss_join(const LossEpilogue& e, uint64_t t, uint64_t v, uint32_t tiles, float* loss, float* lse,
-                             int32_t* status, cudaStream_t s);
+cudaError_t launch_loss_join(const LossEpilogue& e, uint64_t t, uint64_t v, float* loss, float* lse, int32_t* status,
+                             cudaStream_t s);
 // scale[0] = a power of two that brings the largest |dloss| to [2^10, 2^11),
 // scale[1] = its reciprocal; g = scaled dloss, 0 for ignored tokens
 cudaError_t launch_loss_weights(const float* dloss, const int64_t* targets, int64_t ignore, uint64_t t, uint64_t v,

@@ -268,7 +268,6 @@ uzip_status backward(const uzip_linear_grad_args* a, void* ws, uint64_t bytes, i
 struct Loss {
     Product p{};
     Packed ph, pw;
-    uint32_t tiles;
 };
 
 Loss plan_loss(const uzip_cross_entropy_args& a, Work& w, int32_t* d_status) {
@@ -280,9 +279,9 @@ Loss plan_loss(const uzip_cross_entropy_args& a, Work& w, int32_t* d_status) {
     p.schedule = kDense, p.groups = 1, p.epilogue = kLossStats;
     p.dtype = a.dtype, p.status = d_status;
     const uint32_t cols = product_tile_columns(p, sm_count());
-    f.tiles = uint32_t((a.v + cols - 1) / cols);
+    p.ls.tiles = uint32_t((a.v + cols - 1) / cols);
     p.ls.targets = a.targets, p.ls.ignore = a.ignore_index;
-    p.ls.part = w.take<float2>(uint64_t(f.tiles) * a.t);
+    p.ls.part = w.take<float2>(uint64_t(p.ls.tiles) * a.t);
     p.ls.hit = w.take<float>(a.t);
     return f;
 }
@@ -460,7 +459,7 @@ uzip_status uzip_cross_entropy(const uzip_cross_entropy_args* a, void* d_workspa
     err = run_pack(f.ph, s);
     if (err == cudaSuccess) err = run_pack(f.pw, s);
     if (err == cudaSuccess) err = launch_product(f.p, sm_count(), s);
-    if (err == cudaSuccess) err = launch_loss_join(f.p.ls, a->t, a->v, f.tiles, a->loss, a->lse, d_status, s);
+    if (err == cudaSuccess) err = launch_loss_join(f.p.ls, a->t, a->v, a->loss, a->lse, d_status, s);
     return finish(err);
 }
 

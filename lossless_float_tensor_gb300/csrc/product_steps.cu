@@ -40,20 +40,20 @@ __global__ void __launch_bounds__(kThreads) fill_kernel(T* p, uint64_t ld, uint6
 }
 
 // Block (x, y, z): 128 columns, a share of the rows, one group.  A thread
-// holds 8 columns and walks every 16th row; the 16 partial column sums meet in
-// shared memory in a fixed order.
-constexpr uint32_t kGradCols = 128, kGradRows = 16;
+// holds 8 columns and walks every 16th row, four of them in flight; the 16
+// partial column sums meet in shared memory in a fixed order.
+constexpr uint32_t kGradCols = 128, kGradRows = 16, kGradAhead = 4;
 
-__device__ __forceinline__ void load8(const uint16_t* p, bool vec, uint32_t cols, int dtype, float v[8]) {
+__device__ __forceinline__ uint4 load8(const uint16_t* p, bool vec, uint32_t cols) {
+    if (vec) return *reinterpret_cast<const uint4*>(p);
     uint32_t w[4] = {};
-    if (vec) {
-        const uint4 q = *reinterpret_cast<const uint4*>(p);
-        w[0] = q.x, w[1] = q.y, w[2] = q.z, w[3] = q.w;
-    } else {
 #pragma unroll
-        for (uint32_t j = 0; j < 8; ++j)
-            if (j < cols) w[j / 2] |= uint32_t(p[j]) << (j % 2 * 16);
-    }
+    for (uint32_t j = 0; j < 8; ++j)
+        if (j < cols) w[j / 2] |= uint32_t(p[j]) << (j % 2 * 16);
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+__device__ __forceinline__ void spread8(const uint4& q, int dtype, float v[8]) {
+    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
     for (uint32_t j = 0; j < 4; ++j) {
         const float2 f = from16x2(w[j], dtype);
@@ -94,21 +94,41 @@ __global__ void __launch_bounds__(kThreads) act_grad_kernel(const __grid_constan
         uint16_t* dz = static_cast<uint16_t*>(a.dz) + col;
         const bool vy = cols == 8 && a.lddy % 8 == 0 && reinterpret_cast<uintptr_t>(a.dy) % 16 == 0;
         const bool vz = cols == 8 && a.ldz % 8 == 0 && reinterpret_cast<uintptr_t>(a.z) % 16 == 0;
-        for (uint64_t r = r0 + ty; r < r1; r += kGradRows) {
-            float d[8], f[8];
-            load8(dy + r * a.lddy, vy, cols, a.dtype, d);
-            if (a.act != UZIP_ACT_NONE) {
-                load8(z + r * a.ldz, vz, cols, a.dtype, f);
+        const bool has_act = a.act != UZIP_ACT_NONE;
+        for (uint64_t r = r0 + ty; r < r1; r += kGradAhead * kGradRows) {
+            uint4 qd[kGradAhead], qz[kGradAhead];
 #pragma unroll
-                for (uint32_t j = 0; j < 8; ++j) d[j] *= act_slope(f[j], a.act);
-            }
+            for (uint32_t i = 0; i < kGradAhead; ++i)
+                if (r + i * kGradRows < r1) {
+                    qd[i] = load8(dy + (r + i * kGradRows) * a.lddy, vy, cols);
+                    if (has_act) qz[i] = load8(z + (r + i * kGradRows) * a.ldz, vz, cols);
+                }
 #pragma unroll
-            for (uint32_t j = 0; j < 8; ++j) sum[j] += d[j];
-            if (a.dz) {  // rows of the work area: padded to 16 bytes
-                uint4 q;
-                q.x = to16x2(d[0], d[1], a.dtype), q.y = to16x2(d[2], d[3], a.dtype);
-                q.z = to16x2(d[4], d[5], a.dtype), q.w = to16x2(d[6], d[7], a.dtype);
-                *reinterpret_cast<uint4*>(dz + r * a.lddz) = q;
+            for (uint32_t i = 0; i < kGradAhead; ++i) {
+                if (r + i * kGradRows >= r1) break;
+                float d[8], f[8];
+                spread8(qd[i], a.dtype, d);
+                if (has_act) {
+                    spread8(qz[i], a.dtype, f);
+                    if (a.act == UZIP_ACT_RELU) {
+#pragma unroll
+                        for (uint32_t j = 0; j < 8; ++j) d[j] *= act_slope(f[j], UZIP_ACT_RELU);
+                    } else if (a.act == UZIP_ACT_GELU) {
+#pragma unroll
+                        for (uint32_t j = 0; j < 8; ++j) d[j] *= act_slope(f[j], UZIP_ACT_GELU);
+                    } else {
+#pragma unroll
+                        for (uint32_t j = 0; j < 8; ++j) d[j] *= act_slope(f[j], UZIP_ACT_SILU);
+                    }
+                }
+#pragma unroll
+                for (uint32_t j = 0; j < 8; ++j) sum[j] += d[j];
+                if (a.dz) {  // rows of the work area: padded to 16 bytes
+                    uint4 q;
+                    q.x = to16x2(d[0], d[1], a.dtype), q.y = to16x2(d[2], d[3], a.dtype);
+                    q.z = to16x2(d[4], d[5], a.dtype), q.w = to16x2(d[6], d[7], a.dtype);
+                    *reinterpret_cast<uint4*>(dz + (r + i * kGradRows) * a.lddz) = q;
+                }
             }
         }
     }
@@ -141,42 +161,36 @@ __global__ void __launch_bounds__(kThreads) offset_check_kernel(const int64_t* o
     if (__syncthreads_or(offsets_bad(offsets, groups, m)) && threadIdx.x == 0) *status = int(UZIP_ERR_INVALID_ARG);
 }
 
-// One row's tile maxima and sums joined in tile order: 32 rows x 8 threads
-// each, thread (x, y) takes tiles y, y + 8, ...
-__global__ void __launch_bounds__(kThreads) loss_join_kernel(LossEpilogue e, uint64_t t, uint64_t v, uint32_t tiles,
-                                                             float* loss, float* lse, int32_t* status) {
-    __shared__ float2 s[8][32];
-    const uint32_t x = threadIdx.x % 32, y = threadIdx.x / 32;
-    const uint64_t row = uint64_t(blockIdx.x) * 32 + x;
-    float top = -INFINITY, sum = 0.f;
-    bool nan = false;
-    if (row < t)
-        for (uint32_t i = y; i < tiles; i += 8) {
-            const float2 q = e.part[uint64_t(i) * t + row];
-            nan |= q.y != q.y;
-            const float next = fmaxf(top, q.x);
-            if (next == -INFINITY) continue;
-            sum = sum * exp2f((top - next) * kLog2e) + q.y * exp2f((q.x - next) * kLog2e);
-            top = next;
-        }
-    s[y][x] = make_float2(top, nan ? NAN : sum);
+// Two (maximum, sum of exponentials) pairs as one; NaN sums stay.
+__device__ __forceinline__ float2 join(float2 a, float2 b) {
+    const float top = fmaxf(a.x, b.x), base = top == -INFINITY ? 0.f : top;
+    return make_float2(top, a.y * exp2f((a.x - base) * kLog2e) + b.y * exp2f((b.x - base) * kLog2e));
+}
+
+// One block for each row joins its tiles' pairs: thread i takes tiles i,
+// i + 128, ..., then pairs of threads meet, always in the same order.
+constexpr uint32_t kJoinThreads = 128;
+__global__ void __launch_bounds__(kJoinThreads) loss_join_kernel(LossEpilogue e, uint64_t v, uint32_t tiles, float* loss,
+                                                                 float* lse, int32_t* status) {
+    __shared__ float2 s[kJoinThreads / 32];
+    const uint64_t row = blockIdx.x;
+    const float2* part = e.part + row * tiles;
+    float2 q = make_float2(-INFINITY, 0.f);
+    for (uint32_t i = threadIdx.x; i < tiles; i += kJoinThreads) q = join(q, part[i]);
+#pragma unroll
+    for (uint32_t o = 16; o; o /= 2)
+        q = join(q, make_float2(__shfl_xor_sync(0xFFFFFFFFu, q.x, o), __shfl_xor_sync(0xFFFFFFFFu, q.y, o)));
+    if (threadIdx.x % 32 == 0) s[threadIdx.x / 32] = q;
     __syncthreads();
-    if (y != 0 || row >= t) return;
-    for (uint32_t i = 1; i < 8; ++i) {
-        const float2 q = s[i][x];
-        const float next = fmaxf(top, q.x);
-        nan |= q.y != q.y;
-        if (next == -INFINITY) continue;
-        sum = sum * exp2f((top - next) * kLog2e) + q.y * exp2f((q.x - next) * kLog2e);
-        top = next;
-    }
+    if (threadIdx.x) return;
+    q = join(join(s[0], s[1]), join(s[2], s[3]));
     const int64_t target = e.targets[row];
-    const float l = nan ? NAN : top + logf(sum);
     if (target == e.ignore) {
         loss[row] = 0.f;
         lse[row] = 0.f;
         return;
     }
+    const float l = q.x + logf(q.y);
     lse[row] = l;
     if (target < 0 || target >= int64_t(v)) {
         loss[row] = NAN;
@@ -219,24 +233,31 @@ __global__ void __launch_bounds__(1024) loss_weights_kernel(const float* dloss, 
     }
 }
 
-// One block for each word of 64 tokens; a warp reads one ignored row at a time.
+// A warp for each token, a block for each byte of a word; only ignored rows
+// are read.  Rows start on 16-byte boundaries (the products need that too).
 __global__ void __launch_bounds__(kThreads) skip_words_kernel(const uint16_t* h, uint64_t ldh, const int64_t* targets,
                                                               int64_t ignore, uint64_t t, uint64_t d, int dtype,
-                                                              uint64_t* words) {
-    __shared__ uint32_t half[2];
-    if (threadIdx.x < 2) half[threadIdx.x] = 0;
+                                                              uint8_t* bytes) {
+    __shared__ uint32_t odd_rows;
+    if (threadIdx.x == 0) odd_rows = 0;
     __syncthreads();
-    const uint32_t lane = threadIdx.x % 32;
-    const uint16_t infinite = dtype == UZIP_BF16 ? 0x7F80 : 0x7C00;
-    for (uint32_t i = threadIdx.x / 32; i < 64; i += kThreads / 32) {
-        const uint64_t row = uint64_t(blockIdx.x) * 64 + i;
-        if (row >= t || targets[row] != ignore) continue;
+    const uint32_t lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+    const uint64_t row = uint64_t(blockIdx.x) * 8 + warp;
+    if (row < t && targets[row] == ignore) {
+        const uint32_t infinite = dtype == UZIP_BF16 ? 0x7F80 : 0x7C00;
+        const uint16_t* p = h + row * ldh;
         bool odd = false;
-        for (uint64_t c = lane; c < d; c += 32) odd |= (h[row * ldh + c] & infinite) == infinite;
-        if (__any_sync(0xFFFFFFFFu, odd) && lane == 0) atomicOr(&half[i / 32], 1u << (i % 32));
+#pragma unroll 4
+        for (uint64_t c = lane; c < d / 8; c += 32) {
+            const uint4 q = reinterpret_cast<const uint4*>(p)[c];
+            for (uint32_t w : {q.x, q.y, q.z, q.w})
+                odd |= (w & infinite) == infinite || (w >> 16 & infinite) == infinite;
+        }
+        if (lane < d % 8) odd |= (p[d / 8 * 8 + lane] & infinite) == infinite;
+        if (__any_sync(0xFFFFFFFFu, odd) && lane == 0) atomicOr(&odd_rows, 1u << warp);
     }
     __syncthreads();
-    if (threadIdx.x == 0) words[blockIdx.x] = uint64_t(half[0]) | uint64_t(half[1]) << 32;
+    if (threadIdx.x == 0) bytes[blockIdx.x] = uint8_t(odd_rows);
 }
 
 }  // namespace
@@ -260,10 +281,10 @@ cudaError_t launch_fill(void* p, uint64_t ld, uint64_t rows, uint64_t cols, uint
     return cudaGetLastError();
 }
 
-// Blocks enough to fill the GPU four times over, a share of at least 64 rows.
+// Eight blocks for each SM, a share of at least 64 rows.
 uint32_t act_grad_splits(uint64_t m, uint64_t n, uint64_t groups) {
     const uint64_t have = (n + kGradCols - 1) / kGradCols * groups;
-    const uint64_t want = std::max<uint64_t>(1, 152 * 4 / std::max<uint64_t>(1, have));
+    const uint64_t want = std::max<uint64_t>(1, 152 * 8 / std::max<uint64_t>(1, have));
     return uint32_t(std::max<uint64_t>(1, std::min(want, m / groups / 64)));
 }
 
@@ -287,9 +308,9 @@ cudaError_t launch_offset_check(const int64_t* offsets, uint64_t groups, uint64_
     return cudaGetLastError();
 }
 
-cudaError_t launch_loss_join(const LossEpilogue& e, uint64_t t, uint64_t v, uint32_t tiles, float* loss, float* lse,
-                             int32_t* status, cudaStream_t s) {
-    loss_join_kernel<<<uint32_t((t + 31) / 32), kThreads, 0, s>>>(e, t, v, tiles, loss, lse, status);
+cudaError_t launch_loss_join(const LossEpilogue& e, uint64_t t, uint64_t v, float* loss, float* lse, int32_t* status,
+                             cudaStream_t s) {
+    loss_join_kernel<<<uint32_t(t), kJoinThreads, 0, s>>>(e, v, e.tiles, loss, lse, status);
     return cudaGetLastError();
 }
 
@@ -301,8 +322,9 @@ cudaError_t launch_loss_weights(const float* dloss, const int64_t* targets, int6
 
 cudaError_t launch_skip_words(const void* h, uint64_t ldh, const int64_t* targets, int64_t ignore, uint64_t t,
                               uint64_t d, int dtype, uint64_t* words, cudaStream_t s) {
-    skip_words_kernel<<<uint32_t((t + 63) / 64), kThreads, 0, s>>>(static_cast<const uint16_t*>(h), ldh, targets,
-                                                                   ignore, t, d, dtype, words);
+    static_assert(kThreads / 32 == 8, "a warp for each bit of a byte");
+    skip_words_kernel<<<uint32_t((t + 63) / 64 * 8), kThreads, 0, s>>>(static_cast<const uint16_t*>(h), ldh, targets, ignore,
+                                                                       t, d, dtype, reinterpret_cast<uint8_t*>(words));
     return cudaGetLastError();
 }
 

@@ -137,19 +137,21 @@ def _dtype_code(t) -> int:
 def _matrix(t, name, shape, like):
     """Data pointer and row stride of a CUDA matrix (or batch of matrices)
     whose rows are contiguous."""
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         _refuse(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if t.dtype != like.dtype or t.device != like.device:
+    if t is not like and (t.dtype != like.dtype or t.device != like.device):
         _refuse(f"{name} is {t.dtype} on {t.device}, expected {like.dtype} on {like.device}")
-    if t.shape[-1] > 1 and t.stride(-1) != 1:
+    ld, step = t.stride()[-2:]
+    rows, cols = shape[-2:]
+    if step != 1 and cols > 1:
         _refuse(f"{name}: the last dimension must be contiguous")
-    if t.shape[-2] > 1 and t.stride(-2) < t.shape[-1]:
+    if ld < cols and rows > 1:
         _refuse(f"{name}: rows overlap")
-    return t.data_ptr() or None, t.stride(-2)
+    return t.data_ptr() or None, ld
 
 
 def _vector(t, name, shape, dtype, device):
-    if tuple(t.shape) != tuple(shape) or t.dtype != dtype or t.device != device or not t.is_contiguous():
+    if t.shape != shape or t.dtype != dtype or t.device != device or not t.is_contiguous():
         _refuse(f"{name}: expected a contiguous {dtype} tensor of shape {tuple(shape)} on {device}")
     return t.data_ptr() or None
 
@@ -197,7 +199,7 @@ def _run(name, args, device, workspace, status, check):
         status = torch.empty((), dtype=torch.int32, device=device)
     _check(call(ref, workspace.data_ptr() if workspace is not None else None,
                 workspace.numel() if workspace is not None else 0, status.data_ptr() if status is not None else None,
-                torch.cuda.current_stream(device).cuda_stream), name)
+                torch._C._cuda_getCurrentRawStream(device.index)), name)
     if check:
         st = int(status.item())
         if st != UZIP_OK:
