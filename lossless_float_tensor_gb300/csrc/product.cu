@@ -17,6 +17,7 @@
 #include <cuda.h>
 
 #include <algorithm>
+#include <array>
 #include <atomic>
 #include <cmath>
 
@@ -30,8 +31,9 @@ constexpr uint32_t kDepthTile = 64;  // depths of a stage: 128 bytes, the swizzl
 constexpr uint32_t kSliceBytes = kDepthTile * 128;  // 64 rows x 64 depths when rows are contiguous
 constexpr uint32_t kAStage = kRowsTile * kDepthTile * 2;
 constexpr uint32_t kMaxStages = 24;
-constexpr uint32_t kThreads = 192;  // TMA warp, MMA warp, four epilogue warps
+constexpr uint32_t kThreads = 224;  // a TMA warp for A, the MMA warp, four epilogue warps, a TMA warp for B
 constexpr uint32_t kPatchBytes = 32 * 128, kEpilogueBytes = kPatchBytes + 256 * 4;  // an epilogue warp's shared memory
+constexpr uint32_t kMaxSplits = 8;  // blocks of a portable cluster
 constexpr uint32_t kHeights = 6;    // boxes of 1 to 32 lines for depths that are cut
 constexpr int64_t kWaitLimit = 8000000000;  // clock cycles: a wait gives up after about four seconds,
 constexpr int64_t kDrainLimit = 100000000;  // one for copies or products in flight then after 50 ms
@@ -675,7 +677,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (threadIdx.x == 0) {
         for (uint32_t i = 0; i < t.stages; ++i) {
-            mbar_init(smem_u32(&ctl->full[i]), 1);
+            mbar_init(smem_u32(&ctl->full[i]), 2);  // A's and B's bytes announced
             mbar_init(smem_u32(&ctl->empty[i]), 1);
         }
         for (uint32_t i = 0; i < 2; ++i) {
@@ -694,21 +696,25 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tmem = ctl->tmem;
     const uint32_t buffer_cols = t.tmem_cols / 2;
 
-    if (warp == 0) {
+    if (warp == 0 || warp == 6) {
+        // One thread fetches A, another B: issuing a copy takes about 100 cycles, and four to a stage (a slice of 64
+        // rows each where rows are contiguous) would take longer than the stage's products.
         if (elect_one()) {
+            const bool is_a = warp == 0;
             Walk walk(p, t, offsets, first);
             Tile o;
             Ring ring{t.stages};
             bool ok = true;
-            const uint32_t b_cols = t.bn / (PAIR ? 2 : 1), b_slices = (b_cols + 63) / 64;
+            const uint32_t b_cols = t.bn / (PAIR ? 2 : 1), slices = is_a ? 2 : (b_cols + 63) / 64;
             const uint64_t* const skip = p.skip_depth;
-            const bool by_group = walk.schedule == kRows;
-            const uint32_t a_box = t.a_box, a_stage = t.a_stage, stage_bytes = t.stage_bytes, depth = walk.depth;
-            const uint32_t base = smem_u32(smem);
+            const bool by_group = walk.schedule == kRows && !is_a;
+            const uint32_t a_box = t.a_box, stage_bytes = t.stage_bytes, depth = walk.depth;
+            const uint32_t base = smem_u32(smem) + (is_a ? 0 : t.a_stage);
+            const CUtensorMap* const map = is_a ? &maps.a : &maps.b;
             while (ok && walk.take(o)) {
-                const uint32_t row0 = o.row0 + rank * kRowsTile, col0 = o.col0 + rank * b_cols;
+                const uint32_t row0 = is_a ? o.row0 + rank * kRowsTile : o.col0 + rank * b_cols;
                 const uint32_t a_rows = PAIR ? kRowsTile : min(kRowsTile, (o.row_end - row0 + a_box - 1) / a_box * a_box);
-                const uint32_t bytes = ((A_DEEP ? a_rows * 128 : kAStage) + (B_DEEP ? b_cols * 128 : b_slices * kSliceBytes)) *
+                const uint32_t bytes = (is_a ? (A_DEEP ? a_rows * 128 : kAStage) : (B_DEEP ? b_cols * 128 : slices * kSliceBytes)) *
                                        (PAIR ? 2 : 1);
                 const int gb = by_group ? int(o.group) : 0;
                 uint32_t d = o.d0;
@@ -718,7 +724,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (CUT && skip && i + 1 < o.blocks) skip_next = skip[d / 64 + 1];
                     if (!(ok = wait<PAIR>(ctl, &ctl->empty[ring.s], ring.phase ^ 1))) break;
                     uint32_t bar = smem_u32(&ctl->full[ring.s]);
-                    const uint32_t a = base + ring.s * stage_bytes, b = a + a_stage;
+                    const uint32_t to = base + ring.s * stage_bytes;
                     if constexpr (CUT) {
                         const uint32_t left = o.depth_end - d;
                         uint32_t lines = kDepthTile;
@@ -732,18 +738,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                             // Depths past the group's end belong to its neighbour, and skipped ones may hold anything:
                             // their lines are read from beyond the tensor's end, where TMA gives zeros.  (Both operands
                             // have contiguous rows here: a depth is one line of each slice.)
-                            if (rank == 0) mbar_expect_tx(bar, (2 + b_slices) * 128 * lines * (PAIR ? 2 : 1));
+                            if (rank == 0) mbar_expect_tx(bar, slices * 128 * lines * (PAIR ? 2 : 1));
                             if (PAIR) bar = cluster_address(bar, 0);
+                            const CUtensorMap* const heights = is_a ? maps.a_lines : maps.b_lines;
                             for (uint32_t l = 0; l < lines;) {  // runs of kept or cleared lines, in powers of two
                                 const bool kept = keep >> l & 1;
                                 const uint64_t other = (kept ? ~keep : keep) >> l;
                                 const uint32_t run = min(other ? uint32_t(__ffsll(other)) - 1 : 64u, lines - l);
                                 const uint32_t h = min(31u - __clz(run), kHeights - 1);
                                 const int from = int(kept ? d + l : depth);
-                                for (uint32_t r = 0; r < 2; ++r)
-                                    tma_load<PAIR>(a + r * kSliceBytes + l * 128, &maps.a_lines[h], int(row0 + 64 * r), from, 0, bar);
-                                for (uint32_t r = 0; r < b_slices; ++r)
-                                    tma_load<PAIR>(b + r * kSliceBytes + l * 128, &maps.b_lines[h], int(col0 + 64 * r), from, 0, bar);
+                                for (uint32_t r = 0; r < slices; ++r)
+                                    tma_load<PAIR>(to + r * kSliceBytes + l * 128, &heights[h], int(row0 + 64 * r), from, 0, bar);
                                 l += 1u << h;
                             }
                             continue;
@@ -751,22 +756,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     if (rank == 0) mbar_expect_tx(bar, bytes);
                     if (PAIR) bar = cluster_address(bar, 0);
-                    if (A_DEEP) {
-                        for (uint32_t r = 0; r < a_rows; r += a_box)
-                            tma_load<PAIR>(a + r * 128, &maps.a, int(d), int(row0 + r), 0, bar);
+                    if (is_a ? A_DEEP : B_DEEP) {
+                        if (PAIR || !is_a)
+                            tma_load<PAIR>(to, map, int(d), int(row0), gb, bar);
+                        else
+                            for (uint32_t r = 0; r < a_rows; r += a_box)
+                                tma_load<PAIR>(to + r * 128, map, int(d), int(row0 + r), 0, bar);
                     } else {
-                        tma_load<PAIR>(a, &maps.a, int(row0), int(d), 0, bar);
-                        tma_load<PAIR>(a + kSliceBytes, &maps.a, int(row0 + 64), int(d), 0, bar);
-                    }
-                    if (B_DEEP) {
-                        tma_load<PAIR>(b, &maps.b, int(d), int(col0), gb, bar);
-                    } else {
-                        for (uint32_t r = 0; r < b_slices; ++r)
-                            tma_load<PAIR>(b + r * kSliceBytes, &maps.b, int(col0 + 64 * r), int(d), gb, bar);
+                        for (uint32_t r = 0; r < slices; ++r)
+                            tma_load<PAIR>(to + r * kSliceBytes, map, int(row0 + 64 * r), int(d), gb, bar);
                     }
                 }
             }
-            if (ctl->abort && rank == 0)  // copies in flight (a pair's: both blocks') land before the block ends
+            // copies in flight (a pair's: both blocks') land before the block ends
+            if (ctl->abort && rank == 0 && is_a)
                 for (uint32_t i = 0; i < min(ring.used, t.stages); ++i) {
                     const uint32_t back = ring.s > i ? ring.s - 1 - i : ring.s + t.stages - 1 - i;
                     drain(&ctl->full[back], ring.s > i ? ring.phase : ring.phase ^ 1);
@@ -894,12 +897,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const uint32_t r = i / wide, c = i % wide * 8;
                 if (o.col0 + c >= p.n) continue;
                 const uint32_t at = base + (r * (t.bn + 4) + c) * 4;
+                float4 lo[kMaxSplits], hi[kMaxSplits];
+#pragma unroll
+                for (uint32_t s = 0; s < kMaxSplits; ++s)  // all in flight at once
+                    if (s < t.splits) {
+                        const uint32_t from = cluster_address(at, s);
+                        lo[s] = cluster_load4(from), hi[s] = cluster_load4(from + 16);
+                    }
                 float v[8] = {};
-                for (uint32_t s = 0; s < t.splits; ++s) {
-                    const uint32_t from = cluster_address(at, s);
-                    const float4 lo = cluster_load4(from), hi = cluster_load4(from + 16);
-                    v[0] += lo.x, v[1] += lo.y, v[2] += lo.z, v[3] += lo.w, v[4] += hi.x, v[5] += hi.y, v[6] += hi.z, v[7] += hi.w;
-                }
+#pragma unroll
+                for (uint32_t s = 0; s < kMaxSplits; ++s)
+                    if (s < t.splits) {
+                        v[0] += lo[s].x, v[1] += lo[s].y, v[2] += lo[s].z, v[3] += lo[s].w;
+                        v[4] += hi[s].x, v[5] += hi[s].y, v[6] += hi[s].z, v[7] += hi[s].w;
+                    }
                 store8(p, t.vec, 0, uint64_t(o.row0) + r, o.col0 + c, min(8u, uint32_t(p.n) - o.col0 - c), alpha, v);
             }
         }
@@ -957,11 +968,6 @@ bool aligned16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0;
 
 constexpr uint32_t kSmemMost = 227 * 1024;
 
-// Tile width, split of the depth and stages for a product: the smallest
-// estimate in clock cycles.  A stage costs the longest of its multiplication
-// (2 cycles a column), its way into shared memory (about 64 bytes a cycle) and
-// the HBM share of the operand that is read once (about 3500 bytes a cycle
-// for the whole GPU); tiles come in waves of one block per SM.
 bool cut(const Product& p) { return p.schedule == kDepth || p.skip_depth; }  // depths left out, at a group's end or for skipped tokens
 uint64_t row_tiles_of(const Product& p, uint32_t pair) {
     const uint64_t unit = kRowsTile * pair;
@@ -976,49 +982,54 @@ uint64_t most_tiles(const Product& p, const Tiling& t) {
     return row_tiles_of(p, t.pair) * ((p.n + t.bn - 1) / t.bn) * (p.schedule == kDepth ? p.groups : 1);
 }
 
+// Blocks that run at once in clusters of `size` (a GPC's odd SMs stay idle).
+uint32_t cluster_blocks(uint32_t size, int sms);
+
+// Tile width, split of the depth and pairing: the smallest estimate in clock
+// cycles, from rates measured on a GB300 (1.9 GHz).  A stage of 64 depths
+// costs the longest of its multiplication (2.15 cycles a column), its way
+// into shared memory (78 bytes a cycle for a block, 62 where only four stages
+// fit: 128-column tiles of a single block ran at 385 to 410 cycles a stage,
+// 256-column tiles at 640 to 770, pairs of 256 x 256 at 523), the issue of its
+// copies (370 cycles) and its share of
+// HBM, where the operand B is streamed once (3500 bytes a cycle for the whole
+// GPU).  A wave of tiles costs its stages or, where that is longer, its
+// epilogue; the last epilogue is not hidden, and joining the splits took 3.5 us
+// and half a microsecond for every 12 KB of partial sums a block.
 Tiling choose(const Product& p, int sms) {
     Tiling best{};
     double best_cost = 1e300;
-    const uint64_t rows = p.m;
-    const double row_tiles = mean_row_tiles(p, 1);
-    best.pair = 1;
-    const uint64_t groups = p.schedule == kDepth ? p.groups : 1;
+    const uint64_t rows = p.m, groups = p.schedule == kDepth ? p.groups : 1;
     const double blocks = std::max(1.0, double(p.depth) / (p.schedule == kDepth ? p.groups : 1) / kDepthTile);
     const uint32_t low = uint32_t(std::min<uint64_t>(kRowsTile, (rows + 7) / 8 * 8));
     const uint32_t unit = p.b.depth_major ? 16 : 64;  // whole slices where rows are contiguous
     const uint32_t widest = uint32_t(std::min<uint64_t>(256, (p.n + unit - 1) / unit * unit));
     const bool may_split = p.epilogue == kStore && p.schedule == kDense && !p.skip_depth;
+    const double column = (p.st.ldo % 8 ? 40.0 : 14.0) * (p.st.z ? 2 : 1);  // epilogue cycles a column
+    // row tiles that take the same columns of B share what HBM delivers
+    auto shared = [&](double row_tiles) { return p.schedule == kRows ? std::max(1.0, row_tiles / p.groups) : std::min(16.0, row_tiles); };
+    auto consider = [&](uint32_t bn, uint32_t splits, uint32_t pair) {
+        const double row_tiles = mean_row_tiles(p, pair), tiles = row_tiles * double((p.n + bn - 1) / bn * groups);
+        const double at_once = double(splits > 1 ? cluster_blocks(splits, sms) / splits : sms / pair);
+        const double waves = std::ceil(tiles / at_once), running = std::min(tiles, at_once) * splits * pair;
+        const double bytes = ((pair == 2 ? kRowsTile : low) + bn / pair) * 128.0;
+        const double hbm = p.schedule == kDepth ? 0 : bn / pair * 128.0 * running / 3500 / shared(row_tiles);
+        const double stage = std::max({2.15 * bn, bytes / (bytes > 40960 ? 62 : 78), hbm, 370.0});
+        double last = column * bn;
+        if (splits > 1) last = std::ceil(low * bn / 8.0 / (kThreads * splits)) * (1000 + 2 * column) + 6500;
+        const double cost = (waves - 1) * std::max(blocks * stage, last) + std::ceil(blocks / splits) * stage + last + 1000.0 * pair;
+        if (cost >= best_cost) return;
+        best_cost = cost;
+        best.bn = bn, best.splits = splits, best.pair = pair;
+    };
     for (uint32_t bn = widest; bn >= unit; bn -= unit) {
         if (bn < 32 && bn < widest) break;
-        const double tiles = row_tiles * double((p.n + bn - 1) / bn * groups);
-        for (uint32_t splits = 1; splits <= (may_split ? 8u : 1u); ++splits) {
-            if (splits > 1 && blocks / splits < 4) break;
-            const double running = std::min<double>(tiles * splits, sms);
-            const double waves = std::ceil(tiles * splits / sms);
-            const double fill = (low * 128.0 + bn * 128.0) / 64;
-            const double hbm = p.schedule == kDense ? bn * 128.0 * running / 3500 / std::min(16.0, row_tiles) : 0;
-            const double stage = std::max({2.0 * bn, fill, hbm, 128.0});
-            const double cost = waves * (blocks / splits * stage + 4.0 * bn + (splits > 1 ? 1500 : 0)) + 2000;
-            if (cost < best_cost * 0.999) {
-                best_cost = cost;
-                best.bn = bn;
-                best.splits = splits;
-            }
-        }
+        consider(bn, 1, 1);
+        if (may_split)
+            for (uint32_t splits = 2; splits <= kMaxSplits && blocks / splits >= 4; ++splits) consider(bn, splits, 1);
     }
-    // pairs: half of B's bytes a block, at full rate from 7 stages
-    if (p.m > kRowsTile)
-        for (uint32_t bn : {256u, 128u}) {
-            const double tiles = mean_row_tiles(p, 2) * double((p.n + bn - 1) / bn * groups);
-            const double waves = std::ceil(tiles / (sms / 2));
-            const double cost = waves * (blocks * std::max(1.6 * bn, 300.0) + 4.0 * bn) + 2500;
-            if (cost < best_cost) {
-                best_cost = cost;
-                best.bn = bn;
-                best.splits = 1;
-                best.pair = 2;
-            }
-        }
+    if (rows > kRowsTile)
+        for (uint32_t bn : {256u, 128u}) consider(bn, 1, 2);
     Tiling& t = best;
     const uint32_t b_cols = t.bn / t.pair;
     const uint32_t b_bytes = p.b.depth_major ? b_cols * 128 : (b_cols + 63) / 64 * kSliceBytes;
@@ -1092,6 +1103,33 @@ cudaError_t launch_layout(const Product& p, const Tiling& t, int sms, cudaStream
     if (t.pair == 2) return launch<EPI, 2, LAYOUT>(p, t, sms, maps, s);
     if (kMaySplit && t.splits > 1) return launch<EPI, kMaySplit ? 1 : 0, LAYOUT>(p, t, sms, maps, s);
     return launch<EPI, 0, LAYOUT>(p, t, sms, maps, s);
+}
+
+uint32_t cluster_blocks(uint32_t size, int sms) {
+    static const std::array<uint32_t, kMaxSplits + 1> most = [sms] {
+        std::array<uint32_t, kMaxSplits + 1> v{};
+        auto kern = product_kernel<kStore, 1, 0>;
+        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kSmemMost));
+        for (uint32_t size = 1; size <= kMaxSplits; ++size) {
+            cudaLaunchConfig_t cfg{};
+            cfg.gridDim = dim3(size * 64);
+            cfg.blockDim = dim3(kThreads);
+            cfg.dynamicSmemBytes = kSmemMost;
+            cudaLaunchAttribute attr[1];
+            attr[0].id = cudaLaunchAttributeClusterDimension;
+            attr[0].val.clusterDim.x = size, attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+            cfg.attrs = attr;
+            cfg.numAttrs = 1;
+            int n = 0;
+            if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess || n < 1) {
+                cudaGetLastError();
+                n = std::max(1, sms / int(size));
+            }
+            v[size] = uint32_t(n) * size;
+        }
+        return v;
+    }();
+    return most[size];
 }
 
 }  // namespace

@@ -83,9 +83,17 @@ cudaError_t launch_product(const Product& p, int sms, cudaStream_t s);
 
 // ---- steps around the products (product_steps.cu) ---------------------------
 
-// rows x cols values of each of `groups` matrices copied to rows ld_to apart
-cudaError_t launch_pack_rows(const void* from, uint64_t ld, uint64_t group, void* to, uint64_t ld_to, uint64_t rows,
-                             uint64_t cols, uint64_t groups, cudaStream_t s);
+// matrices whose rows are copied to rows ld_to apart
+struct PackJob {
+    const void* from;
+    void* to;
+    uint64_t ld, group, ld_to, rows, cols, groups;
+};
+struct PackJobs {
+    PackJob job[3];
+    uint32_t count;
+};
+cudaError_t launch_pack(const PackJobs& jobs, cudaStream_t s);
 
 // dz = dy act'(z) into dz (nullable) and its column sums into db (nullable); db
 // is NaN where the offsets do not cut [0, m)

@@ -55,22 +55,15 @@ struct Matrix {
 
 // Operand of a product from matrix `a`, packed in the workspace where needed.
 // as_rows: a row of `a` is a row of the operand, else a depth index.
-struct Packed {
-    Matrix from;
-    void* to = nullptr;
-    uint64_t ld = 0;
-};
-Operand operand(const Matrix& a, bool as_rows, Work& w, Packed* pack) {
-    if (!a.packed()) return Operand{a.p, uint64_t(a.step()), a.groups > 1 ? uint64_t(a.group) : 0, as_rows};
-    pack->from = a;
-    pack->ld = round_to(a.cols, 8);
-    pack->to = w.take<uint16_t>(pack->ld * a.rows * a.groups);
-    return Operand{pack->to, pack->ld, pack->ld * a.rows, as_rows};
-}
-cudaError_t run_pack(const Packed& p, cudaStream_t s) {
-    if (!p.to) return cudaSuccess;
-    return launch_pack_rows(p.from.p, p.from.step(), p.from.groups > 1 ? p.from.group : 0, p.to, p.ld, p.from.rows,
-                            p.from.cols, p.from.groups, s);
+Operand operand(const Matrix& a, bool as_rows, Work& w, PackJobs* packs) {
+    const uint64_t group = a.groups > 1 ? a.group : 0;
+    if (!a.packed()) return Operand{a.p, uint64_t(a.step()), group, as_rows};
+    PackJob& j = packs->job[packs->count++];
+    j.from = a.p, j.ld = a.step(), j.group = group;
+    j.rows = a.rows, j.cols = a.cols, j.groups = a.groups;
+    j.ld_to = round_to(a.cols, 8);
+    j.to = w.take<uint16_t>(j.ld_to * j.rows * j.groups);
+    return Operand{j.to, j.ld_to, j.ld_to * j.rows, as_rows};
 }
 
 int sm_count() {
@@ -118,7 +111,7 @@ uzip_status check_common(int32_t dtype, int32_t act, int64_t m, int64_t n, int64
 
 struct Forward {
     Product p{};
-    Packed px, pw;
+    PackJobs packs{};
 };
 
 Matrix w_of(const void* w, int64_t ldw, int64_t w_group, int64_t n, int64_t k, int64_t groups) {
@@ -128,8 +121,8 @@ Matrix w_of(const void* w, int64_t ldw, int64_t w_group, int64_t n, int64_t k, i
 Forward plan_forward(const uzip_linear_args& a, Work& w, int32_t* d_status) {
     Forward f;
     Product& p = f.p;
-    p.a = operand(Matrix{a.x, a.ldx, 0, a.m, a.k, 1}, true, w, &f.px);
-    p.b = operand(w_of(a.w, a.ldw, a.w_group, a.n, a.k, a.groups), true, w, &f.pw);
+    p.a = operand(Matrix{a.x, a.ldx, 0, a.m, a.k, 1}, true, w, &f.packs);
+    p.b = operand(w_of(a.w, a.ldw, a.w_group, a.n, a.k, a.groups), true, w, &f.packs);
     p.m = a.m, p.n = a.n, p.depth = a.k;
     p.schedule = a.groups ? kRows : kDense;
     p.groups = a.groups ? uint32_t(a.groups) : 1;
@@ -166,8 +159,7 @@ uzip_status forward(const uzip_linear_args* a, void* ws, uint64_t bytes, int32_t
     cudaError_t err = cudaSuccess;
     if (d_status) err = cudaMemsetAsync(d_status, 0, sizeof(int32_t), s);
     if (err == cudaSuccess && some) {
-        err = run_pack(f.px, s);
-        if (err == cudaSuccess) err = run_pack(f.pw, s);
+        err = launch_pack(f.packs, s);
         if (err == cudaSuccess) err = launch_product(f.p, sm_count(), s);
     } else if (err == cudaSuccess && grouped)
         err = launch_offset_check(a->offsets, g, a->m, d_status, s);
@@ -177,7 +169,7 @@ uzip_status forward(const uzip_linear_args* a, void* ws, uint64_t bytes, int32_t
 struct Backward {
     ActGrad grad{};
     Product dx{}, dw{};
-    Packed pdy, px, pw;
+    PackJobs packs{};
     bool need_grad;
 };
 
@@ -206,13 +198,13 @@ Backward plan_backward(const uzip_linear_grad_args& a, Work& w, int32_t* d_statu
             dz_rows = Operand{q.dz, q.lddz, 0, 1};
         }
     }
-    if (products && !dz_rows.ld) dz_rows = operand(dy, true, w, &f.pdy);
+    if (products && !dz_rows.ld) dz_rows = operand(dy, true, w, &f.packs);
     dz_depth = dz_rows;
     dz_depth.depth_major = 0;
     if (a.dx) {
         Product& p = f.dx;
         p.a = dz_rows;
-        p.b = operand(w_of(a.w, a.ldw, a.w_group, a.n, a.k, a.groups), false, w, &f.pw);
+        p.b = operand(w_of(a.w, a.ldw, a.w_group, a.n, a.k, a.groups), false, w, &f.packs);
         p.m = a.m, p.n = a.k, p.depth = a.n;
         p.schedule = a.groups ? kRows : kDense;
         p.groups = groups, p.offsets = a.offsets;
@@ -222,7 +214,7 @@ Backward plan_backward(const uzip_linear_grad_args& a, Work& w, int32_t* d_statu
     if (a.dw) {
         Product& p = f.dw;
         p.a = dz_depth;
-        p.b = operand(Matrix{a.x, a.ldx, 0, a.m, a.k, 1}, false, w, &f.px);
+        p.b = operand(Matrix{a.x, a.ldx, 0, a.m, a.k, 1}, false, w, &f.packs);
         p.m = a.n, p.n = a.k, p.depth = a.m;
         p.schedule = a.groups ? kDepth : kDense;
         p.groups = groups, p.offsets = a.offsets;
@@ -253,8 +245,7 @@ uzip_status backward(const uzip_linear_grad_args* a, void* ws, uint64_t bytes, i
     cudaError_t err = cudaSuccess;
     if (d_status) err = cudaMemsetAsync(d_status, 0, sizeof(int32_t), s);
     if (err == cudaSuccess && f.need_grad) err = launch_act_grad(f.grad, s);
-    for (const Packed* p : {&f.pdy, &f.pw, &f.px})
-        if (err == cudaSuccess) err = run_pack(*p, s);
+    if (err == cudaSuccess) err = launch_pack(f.packs, s);
     if (err == cudaSuccess && a->dx) err = launch_product(f.dx, sm_count(), s);
     if (err == cudaSuccess && a->dw) err = launch_product(f.dw, sm_count(), s);
     // the products and the bias gradient check the offsets themselves
@@ -267,14 +258,14 @@ uzip_status backward(const uzip_linear_grad_args* a, void* ws, uint64_t bytes, i
 
 struct Loss {
     Product p{};
-    Packed ph, pw;
+    PackJobs packs{};
 };
 
 Loss plan_loss(const uzip_cross_entropy_args& a, Work& w, int32_t* d_status) {
     Loss f;
     Product& p = f.p;
-    p.a = operand(Matrix{a.h, a.ldh, 0, a.t, a.d, 1}, true, w, &f.ph);
-    p.b = operand(Matrix{a.w, a.ldw, 0, a.v, a.d, 1}, true, w, &f.pw);
+    p.a = operand(Matrix{a.h, a.ldh, 0, a.t, a.d, 1}, true, w, &f.packs);
+    p.b = operand(Matrix{a.w, a.ldw, 0, a.v, a.d, 1}, true, w, &f.packs);
     p.m = a.t, p.n = a.v, p.depth = a.d;
     p.schedule = kDense, p.groups = 1, p.epilogue = kLossStats;
     p.dtype = a.dtype, p.status = d_status;
@@ -293,7 +284,7 @@ struct LossGradPlan {
     uint64_t* skip;
     void* dl;
     Operand h_rows, w_rows;
-    Packed ph, pw;
+    PackJobs packs;
 };
 
 LossGradPlan plan_loss_grad(const uzip_cross_entropy_grad_args& a, Work& w) {
@@ -309,8 +300,8 @@ LossGradPlan plan_loss_grad(const uzip_cross_entropy_grad_args& a, Work& w) {
     f.scale = w.take<float>(2);
     f.g = w.take<float>(t);
     f.skip = w.take<uint64_t>((t + 63) / 64);
-    f.h_rows = operand(Matrix{a.h, a.ldh, 0, a.t, a.d, 1}, true, w, &f.ph);
-    f.w_rows = operand(Matrix{a.w, a.ldw, 0, a.v, a.d, 1}, true, w, &f.pw);
+    f.h_rows = operand(Matrix{a.h, a.ldh, 0, a.t, a.d, 1}, true, w, &f.packs);
+    f.w_rows = operand(Matrix{a.w, a.ldw, 0, a.v, a.d, 1}, true, w, &f.packs);
     f.dl = w.take<uint16_t>(t * f.ld_piece);
     f.ld_sum = round_to(a.d, 4);
     if (a.dh && f.pieces > 1) f.sum = w.take<float>(t * f.ld_sum);
@@ -319,8 +310,7 @@ LossGradPlan plan_loss_grad(const uzip_cross_entropy_grad_args& a, Work& w) {
 
 cudaError_t run_loss_grad(const uzip_cross_entropy_grad_args& a, const LossGradPlan& f, int32_t* d_status,
                           cudaStream_t s) {
-    cudaError_t err = run_pack(f.ph, s);
-    if (err == cudaSuccess) err = run_pack(f.pw, s);
+    cudaError_t err = launch_pack(f.packs, s);
     if (err == cudaSuccess)
         err = launch_loss_weights(a.dloss, a.targets, a.ignore_index, a.t, a.v, f.scale, f.g, d_status, s);
     if (err == cudaSuccess && a.dw)
@@ -456,8 +446,7 @@ uzip_status uzip_cross_entropy(const uzip_cross_entropy_args* a, void* d_workspa
     if (err != cudaSuccess || a->t == 0) return finish(err);
     Work work{static_cast<uint8_t*>(d_workspace)};
     const Loss f = plan_loss(*a, work, d_status);
-    err = run_pack(f.ph, s);
-    if (err == cudaSuccess) err = run_pack(f.pw, s);
+    err = launch_pack(f.packs, s);
     if (err == cudaSuccess) err = launch_product(f.p, sm_count(), s);
     if (err == cudaSuccess) err = launch_loss_join(f.p.ls, a->t, a->v, a->loss, a->lse, d_status, s);
     return finish(err);

@@ -17,19 +17,21 @@ uint32_t blocks_for(uint64_t items, uint64_t most) {
 
 // Rows copied to rows on 16-byte boundaries; the last values of a padded row
 // are zero.  One thread makes one 16-byte store from eight 2-byte loads.
-__global__ void __launch_bounds__(kThreads) pack_kernel(const uint16_t* from, uint64_t ld, uint64_t group, uint4* to,
-                                                        uint64_t vecs, uint64_t rows, uint64_t cols, uint64_t total) {
+// blockIdx.y is the matrix.
+__global__ void __launch_bounds__(kThreads) pack_kernel(const __grid_constant__ PackJobs jobs) {
+    const PackJob& j = jobs.job[blockIdx.y];
+    const uint64_t vecs = j.ld_to / 8, total = vecs * j.rows * j.groups;
     for (uint64_t i = blockIdx.x * uint64_t(kThreads) + threadIdx.x; i < total; i += uint64_t(gridDim.x) * kThreads) {
-        const uint64_t v = i % vecs, r = i / vecs, g = r / rows, row = r - g * rows;
-        const uint16_t* src = from + g * group + row * ld + 8 * v;
+        const uint64_t v = i % vecs, r = i / vecs, g = r / j.rows, row = r - g * j.rows;
+        const uint16_t* src = static_cast<const uint16_t*>(j.from) + g * j.group + row * j.ld + 8 * v;
         uint32_t w[4];
 #pragma unroll
-        for (uint32_t j = 0; j < 4; ++j) {
-            const uint32_t lo = 8 * v + 2 * j < cols ? src[2 * j] : 0u;
-            const uint32_t hi = 8 * v + 2 * j + 1 < cols ? src[2 * j + 1] : 0u;
-            w[j] = lo | hi << 16;
+        for (uint32_t k = 0; k < 4; ++k) {
+            const uint32_t lo = 8 * v + 2 * k < j.cols ? src[2 * k] : 0u;
+            const uint32_t hi = 8 * v + 2 * k + 1 < j.cols ? src[2 * k + 1] : 0u;
+            w[k] = lo | hi << 16;
         }
-        to[i] = make_uint4(w[0], w[1], w[2], w[3]);
+        static_cast<uint4*>(j.to)[i] = make_uint4(w[0], w[1], w[2], w[3]);
     }
 }
 
@@ -262,12 +264,12 @@ __global__ void __launch_bounds__(kThreads) skip_words_kernel(const uint16_t* h,
 
 }  // namespace
 
-cudaError_t launch_pack_rows(const void* from, uint64_t ld, uint64_t group, void* to, uint64_t ld_to, uint64_t rows,
-                             uint64_t cols, uint64_t groups, cudaStream_t s) {
-    const uint64_t vecs = ld_to / 8, total = vecs * rows * groups;
-    if (total == 0) return cudaSuccess;
-    pack_kernel<<<blocks_for(total, 152 * 32), kThreads, 0, s>>>(static_cast<const uint16_t*>(from), ld, group,
-                                                                 static_cast<uint4*>(to), vecs, rows, cols, total);
+cudaError_t launch_pack(const PackJobs& jobs, cudaStream_t s) {
+    uint64_t most = 0;
+    for (uint32_t i = 0; i < jobs.count; ++i)
+        most = std::max(most, jobs.job[i].ld_to / 8 * jobs.job[i].rows * jobs.job[i].groups);
+    if (most == 0) return cudaSuccess;
+    pack_kernel<<<dim3(blocks_for(most, 152 * 32), jobs.count), kThreads, 0, s>>>(jobs);
     return cudaGetLastError();
 }
 
