@@ -158,29 +158,21 @@ __device__ __forceinline__ uint32_t cluster_address(uint32_t addr, uint32_t rank
     asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
     return r;
 }
+// Barriers between the pair's blocks order only TMEM (by the tcgen05 fences)
+// and copies, no ordinary memory: without a cluster scope an arrival does not
+// wait for the warp's stores to global memory.
 __device__ __forceinline__ void cluster_arrive(uint32_t bar) {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
-// CLUSTER: arrivals may come from the other block of the pair
-template <bool CLUSTER>
 __device__ __forceinline__ bool try_wait(uint32_t bar, uint32_t parity) {
     uint32_t done;
-    if (CLUSTER)
-        asm volatile(
-            "{\n\t.reg .pred p;\n\t"
-            "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-            "selp.u32 %0, 1, 0, p;\n\t}"
-            : "=r"(done)
-            : "r"(bar), "r"(parity)
-            : "memory");
-    else
-        asm volatile(
-            "{\n\t.reg .pred p;\n\t"
-            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-            "selp.u32 %0, 1, 0, p;\n\t}"
-            : "=r"(done)
-            : "r"(bar), "r"(parity)
-            : "memory");
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(done)
+        : "r"(bar), "r"(parity)
+        : "memory");
     return done != 0;
 }
 __device__ __forceinline__ float4 cluster_load4(uint32_t addr) {
@@ -212,15 +204,14 @@ struct Control {
 // first row tile of each group, int32 [groups + 1]
 
 // (the clock is read only after 64 tries: reading a timer costs more than most waits)
-template <bool PAIR>
 __device__ __forceinline__ bool wait(Control* c, uint64_t* bar, uint32_t parity) {
     const uint32_t b = smem_u32(bar);
     for (uint32_t i = 0; i < 64; ++i)
-        if (try_wait<PAIR>(b, parity)) return true;
+        if (try_wait(b, parity)) return true;
     const int64_t start = clock64();
     do {
         for (uint32_t i = 0; i < 64; ++i)
-            if (try_wait<PAIR>(b, parity)) return true;
+            if (try_wait(b, parity)) return true;
         if (c->abort) return false;
     } while (clock64() - start < kWaitLimit);
     c->abort = 1;
@@ -228,7 +219,7 @@ __device__ __forceinline__ bool wait(Control* c, uint64_t* bar, uint32_t parity)
 }
 __device__ __forceinline__ void drain(uint64_t* bar, uint32_t parity) {
     const int64_t start = clock64();
-    while (!try_wait<true>(smem_u32(bar), parity) && clock64() - start < kDrainLimit) {
+    while (!try_wait(smem_u32(bar), parity) && clock64() - start < kDrainLimit) {
     }
 }
 
@@ -467,9 +458,11 @@ struct Patch {
 
 // One finished accumulator of a block: 128 rows, one in each lane of the four
 // warps.  `scratch` is this warp's patch, `bias` its copy of the tile's bias.
-template <int EPI>
+// `release` gives the accumulator back once its last column is read.
+template <int EPI, typename Release>
 __device__ __forceinline__ void finish_tile(const Product& p, const Tiling& t, const Tile& o, uint32_t acc, uint32_t warp_row,
-                                            uint32_t lane, float alpha, uint4* scratch, const float* bias, const uint4 ahead[8]) {
+                                            uint32_t lane, float alpha, uint4* scratch, const float* bias, const uint4 ahead[8],
+                                            Release release) {
     const uint64_t row0 = uint64_t(o.row0) + warp_row, row = row0 + lane;
     const bool live = row < o.row_end, empty = o.blocks == 0;
     const uint32_t rows = row0 < o.row_end ? uint32_t(min(uint64_t(32), o.row_end - row0)) : 0;
@@ -509,6 +502,7 @@ __device__ __forceinline__ void finish_tile(const Product& p, const Tiling& t, c
             top = next;
             __syncwarp();
         }
+        release();
         if (live) p.ls.part[row * p.ls.tiles + o.col_tile] = make_float2(top, sum);
         return;
     }
@@ -528,7 +522,7 @@ __device__ __forceinline__ void finish_tile(const Product& p, const Tiling& t, c
                 if (c + 8 * j < cols)
                     store8(p, t.vec, o.group, row, o.col0 + c + 8 * j, min(8u, cols - c - 8 * j), alpha, v + 8 * j);
         }
-        __syncwarp();
+        release();
         return;
     }
     int64_t target = -1;
@@ -567,6 +561,7 @@ __device__ __forceinline__ void finish_tile(const Product& p, const Tiling& t, c
             } else {
                 tmem_load32(acc + c + 32 * half, v);
             }
+            if (c + 32 * half + 32 >= cols) release();
             if (EPI == kLossGrad) {
 #pragma unroll
                 for (uint32_t i = 0; i < 32; ++i) {
@@ -722,7 +717,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (uint32_t i = 0; i < o.blocks; ++i, d += kDepthTile, ring.advance()) {
                     const uint64_t skip_now = skip_next;
                     if (CUT && skip && i + 1 < o.blocks) skip_next = skip[d / 64 + 1];
-                    if (!(ok = wait<PAIR>(ctl, &ctl->empty[ring.s], ring.phase ^ 1))) break;
+                    if (!(ok = wait(ctl, &ctl->empty[ring.s], ring.phase ^ 1))) break;
                     uint32_t bar = smem_u32(&ctl->full[ring.s]);
                     const uint32_t to = base + ring.s * stage_bytes;
                     if constexpr (CUT) {
@@ -793,11 +788,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint64_t desc_b = matrix_descriptor(smem_u32(smem) + t.a_stage, B_DEEP);
             while (ok && walk.take(o)) {
                 const uint32_t buf = tiles & 1;
-                if (!(ok = wait<PAIR>(ctl, &ctl->acc_empty[buf], (tiles >> 1 & 1) ^ 1))) break;
+                if (!(ok = wait(ctl, &ctl->acc_empty[buf], (tiles >> 1 & 1) ^ 1))) break;
                 tmem_fence_after();
                 const uint32_t acc = tmem + buf * buffer_cols;
                 for (uint32_t i = 0; i < o.blocks; ++i, ring.advance()) {
-                    if (!(ok = wait<PAIR>(ctl, &ctl->full[ring.s], ring.phase))) break;
+                    if (!(ok = wait(ctl, &ctl->full[ring.s], ring.phase))) break;
                     tmem_fence_after();
                     const uint64_t a = desc_a + ring.s * stage_step, b = desc_b + ring.s * stage_step;
                     const uint32_t steps = CUT ? (o.depth_end - (o.d0 + i * kDepthTile) + 15) / 16 : 4;
@@ -851,11 +846,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 __syncwarp();
             }
-            if (!__all_sync(0xFFFFFFFFu, wait<PAIR>(ctl, &ctl->acc_full[buf], tiles >> 1 & 1))) break;
+            if (!__all_sync(0xFFFFFFFFu, wait(ctl, &ctl->acc_full[buf], tiles >> 1 & 1))) break;
             tmem_fence_after();
             const uint32_t acc = tmem + buf * buffer_cols + (quarter * 32 << 16);
+            const auto release = [&] {
+                tmem_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    if (PAIR) cluster_arrive(cluster_address(smem_u32(&ctl->acc_empty[buf]), 0));
+                    else mbar_arrive(smem_u32(&ctl->acc_empty[buf]));
+                }
+            };
             if (!SPLIT) {
-                finish_tile<EPI>(p, t, o, acc, quarter * 32, lane, alpha, scratch, bias, ahead);
+                finish_tile<EPI>(p, t, o, acc, quarter * 32, lane, alpha, scratch, bias, ahead, release);
             } else {
                 const uint32_t lane_row = quarter * 32 + lane;
                 // partial sums to shared memory, rows bn + 4 floats apart (no bank conflicts for 16-byte access)
@@ -873,12 +876,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (c + i < t.bn && lane_row < o.row_end - o.row0)
                             *reinterpret_cast<float4*>(part + c + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
                 }
-            }
-            tmem_fence_before();
-            __syncwarp();
-            if (lane == 0) {
-                if (PAIR) cluster_arrive(cluster_address(smem_u32(&ctl->acc_empty[buf]), 0));
-                else mbar_arrive(smem_u32(&ctl->acc_empty[buf]));
             }
             ++tiles;
         }
