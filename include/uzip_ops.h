@@ -139,8 +139,8 @@ uzip_status uzip_cross_entropy(const uzip_cross_entropy_args* a, void* d_workspa
  *   dh_i = dloss_i (sum_j p_ij w_j - w_{t_i}),  dw_j = sum_i dloss_i (p_ij - [j = t_i]) h_i.
  * The vocabulary is taken `piece` classes at a time: their logits are computed
  * again and p - [j = t] is rounded to the dtype in the workspace (t x piece
- * values).  piece 0 takes the default: as many classes as 512 MiB hold, all of
- * them where they fit. */
+ * values).  piece 0 takes the default: as many classes as 512 MiB hold, at most
+ * 32768. */
 typedef struct {
     int32_t dtype;
     int32_t reserved; /* 0 */

@@ -32,6 +32,12 @@ constexpr uint32_t kSliceBytes = kDepthTile * 128;  // 64 rows x 64 depths when 
 constexpr uint32_t kAStage = kRowsTile * kDepthTile * 2;
 constexpr uint32_t kMaxStages = 24;
 constexpr uint32_t kThreads = 224;  // a TMA warp for A, the MMA warp, four epilogue warps, a TMA warp for B
+constexpr uint32_t kStatsThreads = 352;  // and four more epilogue warps, for the second 128 columns
+// The tensor core cuts each addition to 24 bits toward zero, which adds up to a
+// bias of half a unit an addition: at 4096 depths logits were 1e-5 off and the
+// loss 1.4e-6 of itself.  The loss statistics take the products of 1024 depths
+// at a time into registers, where they are added with rounding.
+constexpr uint32_t kStatsChunk = 16;  // stages
 constexpr uint32_t kPatchBytes = 32 * 128, kEpilogueBytes = kPatchBytes + 256 * 4;  // an epilogue warp's shared memory
 constexpr uint32_t kMaxSplits = 8;  // blocks of a portable cluster
 constexpr uint32_t kHeights = 6;    // boxes of 1 to 32 lines for depths that are cut
@@ -456,6 +462,31 @@ struct Patch {
     }
 };
 
+// The loss statistics of a row's logits in one half (128 columns) of a tile.
+__device__ __forceinline__ void finish_stats(const Product& p, const Tile& o, uint64_t row, uint32_t half, float v[128]) {
+    if (row >= o.row_end) return;
+    const uint32_t col0 = o.col0 + half * 128, cols = min(128u, uint32_t(p.n) - col0);
+    const int64_t target = p.ls.targets[row] - int64_t(col0);
+    if (target >= 0 && target < int64_t(cols)) {
+#pragma unroll
+        for (uint32_t i = 0; i < 128; ++i)
+            if (target == int64_t(i)) p.ls.hit[row] = v[i];
+    }
+    if (cols < 128) {
+#pragma unroll
+        for (uint32_t i = 0; i < 128; ++i)
+            if (i >= cols) v[i] = -INFINITY;
+    }
+    float most[4] = {v[0], v[1], v[2], v[3]};
+#pragma unroll
+    for (uint32_t i = 4; i < 128; ++i) most[i % 4] = fmaxf(most[i % 4], v[i]);
+    const float top = fmaxf(fmaxf(most[0], most[1]), fmaxf(most[2], most[3])), base = top == -INFINITY ? 0.f : top;
+    float add[4] = {};
+#pragma unroll
+    for (uint32_t i = 0; i < 128; ++i) add[i % 4] += fast_exp2((v[i] - base) * kLog2e);
+    p.ls.part[row * p.ls.tiles + col0 / 128] = make_float2(top, (add[0] + add[1]) + (add[2] + add[3]));
+}
+
 // One finished accumulator of a block: 128 rows, one in each lane of the four
 // warps.  `scratch` is this warp's patch, `bias` its copy of the tile's bias.
 // `release` gives the accumulator back once its last column is read.
@@ -469,43 +500,6 @@ __device__ __forceinline__ void finish_tile(const Product& p, const Tiling& t, c
     const uint32_t cols = min(t.bn, uint32_t(p.n) - o.col0);
     const Patch patch{scratch, lane};
     const int dtype = p.dtype;
-    if (EPI == kLossStats) {
-        float top = -INFINITY, sum = 0.f;
-        const int64_t target = live ? p.ls.targets[row] - int64_t(o.col0) : -1;
-        for (uint32_t c = 0; c < cols; c += 32) {
-            float v[32];
-            if (empty) {
-#pragma unroll
-                for (uint32_t i = 0; i < 32; ++i) v[i] = 0.f;
-            } else {
-                tmem_load32(acc + c, v);
-            }
-            const uint32_t here = min(32u, cols - c);
-            if (target >= c && target < int64_t(c + here)) {
-#pragma unroll
-                for (uint32_t i = 0; i < 32; ++i)
-                    if (target == int64_t(c + i)) p.ls.hit[row] = v[i];
-            }
-            if (here < 32) {
-#pragma unroll
-                for (uint32_t i = 0; i < 32; ++i)
-                    if (i >= here) v[i] = -INFINITY;
-            }
-            float most = v[0];
-#pragma unroll
-            for (uint32_t i = 1; i < 32; ++i) most = fmaxf(most, v[i]);
-            const float next = fmaxf(top, most), base = next == -INFINITY ? 0.f : next * kLog2e;
-            float add[4] = {};
-#pragma unroll
-            for (uint32_t i = 0; i < 32; ++i) add[i % 4] += fast_exp2(fmaf(v[i], kLog2e, -base));
-            sum = sum * fast_exp2(fmaf(top, kLog2e, -base)) + ((add[0] + add[1]) + (add[2] + add[3]));
-            top = next;
-            __syncwarp();
-        }
-        release();
-        if (live) p.ls.part[row * p.ls.tiles + o.col_tile] = make_float2(top, sum);
-        return;
-    }
     if (EPI == kStore && (p.st.out_fp32 || p.st.sum_in)) {  // partial results in 32 bits: few, after long depths
         for (uint32_t c = 0; c < cols; c += 32) {
             float v[32];
@@ -620,10 +614,11 @@ __device__ __forceinline__ void finish_tile(const Product& p, const Tiling& t, c
 // LAYOUT: 0 both operands contiguous along the depth, 1 only A, 2 neither, 3
 // neither, with the depth cut by groups or skipped tokens.
 template <int EPI, int MODE, int LAYOUT>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(EPI == kLossStats ? kStatsThreads : kThreads, 1)
     product_kernel(const __grid_constant__ Product p, const __grid_constant__ Tiling t,
                    const __grid_constant__ Maps<LAYOUT == 3> maps) {
-    constexpr bool SPLIT = MODE == 1, PAIR = MODE == 2;
+    constexpr bool SPLIT = MODE == 1, PAIR = MODE == 2, STATS = EPI == kLossStats;
+    constexpr uint32_t kBlock = STATS ? kStatsThreads : kThreads;
     constexpr bool A_DEEP = LAYOUT < 2, B_DEEP = LAYOUT == 0, CUT = LAYOUT == 3;
     extern __shared__ uint8_t raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
@@ -637,7 +632,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (p.schedule != kDense) {
         const int64_t end = p.schedule == kRows ? p.m : p.depth;
         bool bad = false;
-        for (uint32_t i = threadIdx.x; i <= p.groups; i += kThreads) {
+        for (uint32_t i = threadIdx.x; i <= p.groups; i += kBlock) {
             const int64_t v = p.offsets[i];
             bad |= v < 0 || v > end || (i == 0 && v != 0) || (i == p.groups ? v != end : v > p.offsets[i + 1]);
             offsets[i] = int32_t(v);
@@ -646,7 +641,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (blockIdx.x == 0 && threadIdx.x == 0 && p.status) atomicCAS(p.status, 0, int(UZIP_ERR_INVALID_ARG));
             const uint16_t nan = p.dtype == UZIP_BF16 ? 0x7FC0 : 0x7E00;
             const uint64_t total = p.m * p.n * (p.schedule == kDepth ? p.groups : 1);
-            for (uint64_t i = blockIdx.x * uint64_t(kThreads) + threadIdx.x; i < total; i += uint64_t(gridDim.x) * kThreads) {
+            for (uint64_t i = blockIdx.x * uint64_t(kBlock) + threadIdx.x; i < total; i += uint64_t(gridDim.x) * kBlock) {
                 const uint64_t r = i / p.n, g = r / p.m;
                 static_cast<uint16_t*>(p.st.out)[g * p.st.out_group + (r - g * p.m) * p.st.ldo + i % p.n] = nan;
                 if (p.st.z) static_cast<uint16_t*>(p.st.z)[r * p.st.ldz + i % p.n] = nan;
@@ -677,7 +672,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         for (uint32_t i = 0; i < 2; ++i) {
             mbar_init(smem_u32(&ctl->acc_full[i]), 1);
-            mbar_init(smem_u32(&ctl->acc_empty[i]), 4 * t.pair);
+            mbar_init(smem_u32(&ctl->acc_empty[i]), (STATS ? 8 : 4) * t.pair);  // an arrival for each epilogue warp
         }
         mbar_init(smem_u32(&ctl->drain), 1);
         ctl->abort = 0;
@@ -776,7 +771,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             Walk walk(p, t, offsets, first);
             Tile o;
             Ring ring{t.stages};
-            uint32_t tiles = 0;
+            uint32_t used = 0;  // accumulators
             bool ok = true;
             // 16 depths further: 32 bytes along the depth, or 16 lines
             constexpr uint32_t kStepA = A_DEEP ? 2 : 128, kStepB = B_DEEP ? 2 : 128;
@@ -787,30 +782,35 @@ __global__ void __launch_bounds__(kThreads, 1)
             // this block)
             const uint64_t desc_b = matrix_descriptor(smem_u32(smem) + t.a_stage, B_DEEP);
             while (ok && walk.take(o)) {
-                const uint32_t buf = tiles & 1;
-                if (!(ok = wait(ctl, &ctl->acc_empty[buf], (tiles >> 1 & 1) ^ 1))) break;
-                tmem_fence_after();
-                const uint32_t acc = tmem + buf * buffer_cols;
-                for (uint32_t i = 0; i < o.blocks; ++i, ring.advance()) {
-                    if (!(ok = wait(ctl, &ctl->full[ring.s], ring.phase))) break;
+                for (uint32_t i = 0; ok && (i < o.blocks || i == 0); ++used) {
+                    const uint32_t buf = used & 1;
+                    if (!(ok = wait(ctl, &ctl->acc_empty[buf], (used >> 1 & 1) ^ 1))) break;
                     tmem_fence_after();
-                    const uint64_t a = desc_a + ring.s * stage_step, b = desc_b + ring.s * stage_step;
-                    const uint32_t steps = CUT ? (o.depth_end - (o.d0 + i * kDepthTile) + 15) / 16 : 4;
-                    mma<PAIR>(acc, a, b, idesc, i);
-                    if (!CUT || steps > 1) mma<PAIR>(acc, a + kStepA, b + kStepB, idesc, 1);
-                    if (!CUT || steps > 2) mma<PAIR>(acc, a + 2 * kStepA, b + 2 * kStepB, idesc, 1);
-                    if (!CUT || steps > 3) mma<PAIR>(acc, a + 3 * kStepA, b + 3 * kStepB, idesc, 1);
-                    mma_commit<PAIR>(smem_u32(&ctl->empty[ring.s]));
-                }
-                if (o.blocks) {
+                    const uint32_t acc = tmem + buf * buffer_cols;
+                    const uint32_t first_block = i, end = STATS ? min(o.blocks, i + kStatsChunk) : o.blocks;
+                    if (end == 0) {  // nothing to add up: the epilogues take zeros
+                        if (PAIR) {
+                            cluster_arrive(cluster_address(smem_u32(&ctl->acc_full[buf]), 0));
+                            cluster_arrive(cluster_address(smem_u32(&ctl->acc_full[buf]), 1));
+                        } else {
+                            mbar_arrive(smem_u32(&ctl->acc_full[buf]));
+                        }
+                        ++i;
+                        continue;
+                    }
+                    for (; i < end; ++i, ring.advance()) {
+                        if (!(ok = wait(ctl, &ctl->full[ring.s], ring.phase))) break;
+                        tmem_fence_after();
+                        const uint64_t a = desc_a + ring.s * stage_step, b = desc_b + ring.s * stage_step;
+                        const uint32_t steps = CUT ? (o.depth_end - (o.d0 + i * kDepthTile) + 15) / 16 : 4;
+                        mma<PAIR>(acc, a, b, idesc, i != first_block);
+                        if (!CUT || steps > 1) mma<PAIR>(acc, a + kStepA, b + kStepB, idesc, 1);
+                        if (!CUT || steps > 2) mma<PAIR>(acc, a + 2 * kStepA, b + 2 * kStepB, idesc, 1);
+                        if (!CUT || steps > 3) mma<PAIR>(acc, a + 3 * kStepA, b + 3 * kStepB, idesc, 1);
+                        mma_commit<PAIR>(smem_u32(&ctl->empty[ring.s]));
+                    }
                     mma_commit<PAIR>(smem_u32(&ctl->acc_full[buf]));
-                } else if (PAIR) {  // nothing to add up: the epilogues take zeros
-                    cluster_arrive(cluster_address(smem_u32(&ctl->acc_full[buf]), 0));
-                    cluster_arrive(cluster_address(smem_u32(&ctl->acc_full[buf]), 1));
-                } else {
-                    mbar_arrive(smem_u32(&ctl->acc_full[buf]));
                 }
-                ++tiles;
             }
             if (ctl->abort) {  // products in flight end before TMEM is freed
                 mma_commit<PAIR>(smem_u32(&ctl->drain));
@@ -818,6 +818,40 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         }
         __syncwarp();
+    } else if (STATS) {
+        Walk walk(p, t, offsets, first);
+        Tile o;
+        uint32_t used = 0;
+        bool ok = true;
+        const uint32_t quarter = warp % 4, half = warp > 6;
+        while (ok && walk.take(o)) {
+            const uint32_t cols = min(t.bn, uint32_t(p.n) - o.col0), mine = cols > half * 128 ? cols - half * 128 : 0;
+            float v[128];
+#pragma unroll
+            for (uint32_t i = 0; i < 128; ++i) v[i] = 0.f;
+            for (uint32_t i = 0; i < max(o.blocks, 1u); i += kStatsChunk, ++used) {
+                const uint32_t buf = used & 1;
+                if (!(ok = __all_sync(0xFFFFFFFFu, wait(ctl, &ctl->acc_full[buf], used >> 1 & 1)))) break;
+                tmem_fence_after();
+                const uint32_t acc = tmem + buf * buffer_cols + half * 128 + (quarter * 32 << 16);
+#pragma unroll
+                for (uint32_t c = 0; c < 4; ++c)
+                    if (32 * c < mine && o.blocks) {
+                        float add[32];
+                        tmem_load32(acc + 32 * c, add);
+#pragma unroll
+                        for (uint32_t k = 0; k < 32; ++k) v[32 * c + k] += add[k];
+                    }
+                tmem_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    if (PAIR) cluster_arrive(cluster_address(smem_u32(&ctl->acc_empty[buf]), 0));
+                    else mbar_arrive(smem_u32(&ctl->acc_empty[buf]));
+                }
+            }
+            if (ok && mine) finish_stats(p, o, uint64_t(o.row0) + rank * kRowsTile + quarter * 32 + lane, half, v);
+            __syncwarp();
+        }
     } else {
         Walk walk(p, t, offsets, first);
         Tile o;
@@ -970,10 +1004,12 @@ uint64_t row_tiles_of(const Product& p, uint32_t pair) {
     const uint64_t unit = kRowsTile * pair;
     return p.schedule == kRows ? p.m / unit + p.groups : (p.m + unit - 1) / unit;  // grouped: at most
 }
-// grouped: what ragged groups take on average
+// grouped: what ragged groups take on average, with rows spread at random
 double mean_row_tiles(const Product& p, uint32_t pair) {
     const uint64_t unit = kRowsTile * pair;
-    return p.schedule == kRows ? double(p.m) / unit + 0.5 * double(std::min<uint64_t>(p.groups, p.m)) : double((p.m + unit - 1) / unit);
+    if (p.schedule != kRows) return double((p.m + unit - 1) / unit);
+    const double used = p.groups * (1 - std::exp(-double(p.m) / p.groups));
+    return std::max(used, double(p.m) / unit + 0.5 * used);
 }
 uint64_t most_tiles(const Product& p, const Tiling& t) {
     return row_tiles_of(p, t.pair) * ((p.n + t.bn - 1) / t.bn) * (p.schedule == kDepth ? p.groups : 1);
@@ -984,11 +1020,11 @@ uint32_t cluster_blocks(uint32_t size, int sms);
 
 // Tile width, split of the depth and pairing: the smallest estimate in clock
 // cycles, from rates measured on a GB300 (1.9 GHz).  A stage of 64 depths
-// costs the longest of its multiplication (2.15 cycles a column), its way
+// costs the longest of its multiplication (2 cycles a column and 35), its way
 // into shared memory (78 bytes a cycle for a block, 62 where only four stages
 // fit: 128-column tiles of a single block ran at 385 to 410 cycles a stage,
 // 256-column tiles at 640 to 770, pairs of 256 x 256 at 523), the issue of its
-// copies (370 cycles) and its share of
+// copies (350 cycles) and its share of
 // HBM, where the operand B is streamed once (3500 bytes a cycle for the whole
 // GPU).  A wave of tiles costs its stages or, where that is longer, its
 // epilogue; the last epilogue is not hidden, and joining the splits took 3.5 us
@@ -1011,7 +1047,7 @@ Tiling choose(const Product& p, int sms) {
         const double waves = std::ceil(tiles / at_once), running = std::min(tiles, at_once) * splits * pair;
         const double bytes = ((pair == 2 ? kRowsTile : low) + bn / pair) * 128.0;
         const double hbm = p.schedule == kDepth ? 0 : bn / pair * 128.0 * running / 3500 / shared(row_tiles);
-        const double stage = std::max({2.15 * bn, bytes / (bytes > 40960 ? 62 : 78), hbm, 370.0});
+        const double stage = std::max({2.0 * bn + 35, bytes / (bytes > 40960 ? 62 : 78), hbm, 350.0});
         double last = column * bn;
         if (splits > 1) last = std::ceil(low * bn / 8.0 / (kThreads * splits)) * (1000 + 2 * column) + 6500;
         const double cost = (waves - 1) * std::max(blocks * stage, last) + std::ceil(blocks / splits) * stage + last + 1000.0 * pair;
@@ -1021,12 +1057,14 @@ Tiling choose(const Product& p, int sms) {
     };
     for (uint32_t bn = widest; bn >= unit; bn -= unit) {
         if (bn < 32 && bn < widest) break;
+        if (p.epilogue == kLossStats && bn % 128 && bn < widest) continue;  // statistics are kept for every 128 columns
         consider(bn, 1, 1);
         if (may_split)
             for (uint32_t splits = 2; splits <= kMaxSplits && blocks / splits >= 4; ++splits) consider(bn, splits, 1);
     }
     if (rows > kRowsTile)
-        for (uint32_t bn : {256u, 128u}) consider(bn, 1, 2);
+        for (uint32_t bn = 256; bn >= 96; bn -= 32)
+            if (p.epilogue != kLossStats || bn % 128 == 0) consider(bn, 1, 2);
     Tiling& t = best;
     const uint32_t b_cols = t.bn / t.pair;
     const uint32_t b_bytes = p.b.depth_major ? b_cols * 128 : (b_cols + 63) / 64 * kSliceBytes;
@@ -1071,7 +1109,7 @@ cudaError_t launch(const Product& p, const Tiling& t, int sms, const Maps<LAYOUT
     cfg.gridDim = dim3(uint32_t(MODE == 1   ? tiles * t.splits
                                 : MODE == 2 ? 2 * std::min<uint64_t>(tiles, sms / 2)
                                             : std::min<uint64_t>(tiles, sms)));
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3(EPI == kLossStats ? kStatsThreads : kThreads);
     cfg.dynamicSmemBytes = t.smem;
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
@@ -1130,8 +1168,6 @@ uint32_t cluster_blocks(uint32_t size, int sms) {
 }
 
 }  // namespace
-
-uint32_t product_tile_columns(const Product& p, int sms) { return choose(p, sms).bn; }
 
 cudaError_t launch_product(const Product& p, int sms, cudaStream_t s) {
     if (p.m == 0 || p.n == 0) return cudaSuccess;

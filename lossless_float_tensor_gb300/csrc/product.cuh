@@ -55,7 +55,7 @@ struct LossEpilogue {
     int64_t ignore;
     uint64_t col0;     // class of column 0
     float2* part;      // kLossStats: [rows][tiles] maximum, sum of exponentials
-    uint32_t tiles;    // column tiles of the launch
+    uint32_t tiles;    // of kStatsCols columns
     float* hit;        // kLossStats: [rows] logit of the target
     const float* lse;  // kLossGrad
     const float* g;    // kLossGrad: [rows], scaled
@@ -77,8 +77,7 @@ struct Product {
     int32_t* status;
 };
 
-// columns of the tiles in which launch_product takes p (kLossStats partials)
-uint32_t product_tile_columns(const Product& p, int sms);
+constexpr uint32_t kStatsCols = 128;  // columns of one kLossStats partial result
 cudaError_t launch_product(const Product& p, int sms, cudaStream_t s);
 
 // ---- steps around the products (product_steps.cu) ---------------------------

@@ -14,7 +14,9 @@ namespace {
 using namespace uzip;
 
 constexpr int64_t kMaxLength = (int64_t(1) << 31) - 1;
-constexpr uint64_t kPieceBytes = 512ull << 20;
+// A piece of the vocabulary: at most 512 MiB of softmax gradient, and at most
+// 32768 classes, whose products the tensor core adds with a bias below 2^-14.
+constexpr uint64_t kPieceBytes = 512ull << 20, kPieceMost = 32768;
 
 uint64_t round_to(uint64_t v, uint64_t a) { return (v + a - 1) / a * a; }
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
@@ -269,8 +271,7 @@ Loss plan_loss(const uzip_cross_entropy_args& a, Work& w, int32_t* d_status) {
     p.m = a.t, p.n = a.v, p.depth = a.d;
     p.schedule = kDense, p.groups = 1, p.epilogue = kLossStats;
     p.dtype = a.dtype, p.status = d_status;
-    const uint32_t cols = product_tile_columns(p, sm_count());
-    p.ls.tiles = uint32_t((a.v + cols - 1) / cols);
+    p.ls.tiles = uint32_t((a.v + kStatsCols - 1) / kStatsCols);
     p.ls.targets = a.targets, p.ls.ignore = a.ignore_index;
     p.ls.part = w.take<float2>(uint64_t(p.ls.tiles) * a.t);
     p.ls.hit = w.take<float>(a.t);
@@ -291,7 +292,7 @@ LossGradPlan plan_loss_grad(const uzip_cross_entropy_grad_args& a, Work& w) {
     LossGradPlan f{};
     const uint64_t t = a.t, v = a.v;
     uint64_t piece = a.piece;
-    if (piece == 0) piece = std::max<uint64_t>(256, kPieceBytes / 2 / std::max<uint64_t>(1, t) / 256 * 256);
+    if (piece == 0) piece = std::min(kPieceMost, std::max<uint64_t>(256, kPieceBytes / 2 / std::max<uint64_t>(1, t) / 256 * 256));
     if (piece >= v) piece = v;
     else piece = round_to(piece, 8);  // every piece starts on a 16-byte boundary of a gradient row
     f.piece = piece;

@@ -343,8 +343,8 @@ def cross_entropy_backward(dloss, h, w, targets, lse, *, ignore_index=-100, need
                            workspace=None, status=None, check=False, stream=None):
     """(dh, dw) of cross_entropy() for the fp32 gradient dloss [t] of each
     token's loss.  The vocabulary is taken `piece` classes at a time (0: as
-    many as fit 512 MiB), whose softmax gradient is the only workspace of that
-    size."""
+    many as fit 512 MiB, at most 32768), whose softmax gradient is the only
+    workspace of that size."""
     import torch
 
     _operand(h, "h", 2)
