@@ -31,14 +31,15 @@ constexpr uint32_t kDepthTile = 64;  // depths of a stage: 128 bytes, the swizzl
 constexpr uint32_t kSliceBytes = kDepthTile * 128;  // 64 rows x 64 depths when rows are contiguous
 constexpr uint32_t kAStage = kRowsTile * kDepthTile * 2;
 constexpr uint32_t kMaxStages = 24;
-constexpr uint32_t kThreads = 224;  // a TMA warp for A, the MMA warp, four epilogue warps, a TMA warp for B
-constexpr uint32_t kStatsThreads = 352;  // and four more epilogue warps, for the second 128 columns
+constexpr uint32_t kThreads = 352;  // TMA warp for A, MMA warp, 4 epilogue warps, TMA warp for B, 4 epilogue warps
 // The tensor core cuts each addition to 24 bits toward zero, which adds up to a
 // bias of half a unit an addition: at 4096 depths logits were 1e-5 off and the
 // loss 1.4e-6 of itself.  The loss statistics take the products of 1024 depths
 // at a time into registers, where they are added with rounding.
 constexpr uint32_t kStatsChunk = 16;  // stages
-constexpr uint32_t kPatchBytes = 32 * 128, kEpilogueBytes = kPatchBytes + 256 * 4;  // an epilogue warp's shared memory
+constexpr uint32_t kEpilogueWarps = 8;
+constexpr uint32_t kPatchCols = 32;  // columns that an epilogue warp takes at a time
+constexpr uint32_t kPatchBytes = 32 * kPatchCols * 2, kEpilogueBytes = kPatchBytes + 128 * 4;  // a warp's shared memory
 constexpr uint32_t kMaxSplits = 8;  // blocks of a portable cluster
 constexpr uint32_t kHeights = 6;    // boxes of 1 to 32 lines for depths that are cut
 constexpr int64_t kWaitLimit = 8000000000;  // clock cycles: a wait gives up after about four seconds,
@@ -131,13 +132,14 @@ __device__ __forceinline__ void tmem_load32(uint32_t addr, float v[32]) {
     uint32_t r[32];
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
         : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
           "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
           "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
           "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-        : "r"(addr));
-    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+        : "r"(addr)
+        : "memory");
 #pragma unroll
     for (uint32_t i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
 }
@@ -396,68 +398,68 @@ __device__ __forceinline__ float fast_exp2(float v) {
 }
 
 // An epilogue warp holds a row in each lane, which would read and write memory
-// 16 bytes a row apart.  32 rows x 64 columns of 16-bit values go through 4 KB
+// 16 bytes a row apart.  32 rows x 32 columns of 16-bit values go through 2 KB
 // of shared memory instead (16-byte pieces swizzled by the row, free of bank
-// conflicts both ways), so that 8 lanes touch 128 contiguous bytes of a row.
-constexpr uint32_t kPatchCols = 64;
+// conflicts both ways), so that 4 lanes touch 64 contiguous bytes of a row.
+// Rows that do not start on 16-byte boundaries go a value a lane, a row at a
+// time.
 struct Patch {
-    uint4* s;  // [32][8]
+    uint4* s;  // [32][4]
     uint32_t lane;
-    __device__ __forceinline__ uint4& at(uint32_t row, uint32_t piece) const { return s[row * 8 + (piece ^ (row & 7))]; }
-    __device__ __forceinline__ void put_row(const uint32_t w[32]) const {
-        __syncwarp();
-#pragma unroll
-        for (uint32_t i = 0; i < 8; ++i) at(lane, i) = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
-        __syncwarp();
+    __device__ __forceinline__ uint4& at(uint32_t row, uint32_t piece) const { return s[row * 4 + (piece ^ (row >> 1 & 3))]; }
+    __device__ __forceinline__ uint16_t& value(uint32_t row, uint32_t col) const {
+        return reinterpret_cast<uint16_t*>(&at(row, col / 8))[col % 8];
     }
-    __device__ __forceinline__ void take_row(uint32_t w[32]) const {
-        __syncwarp();
+    // rows x cols values on their way from p, rows ld apart; vec: 16-byte access
+    __device__ __forceinline__ void fetch(const uint16_t* p, uint64_t ld, uint32_t rows, uint32_t cols, bool vec, uint4 q[4]) const {
+        if (vec) {
 #pragma unroll
-        for (uint32_t i = 0; i < 8; ++i) {
-            const uint4 q = at(lane, i);
-            w[4 * i] = q.x, w[4 * i + 1] = q.y, w[4 * i + 2] = q.z, w[4 * i + 3] = q.w;
-        }
-        __syncwarp();
-    }
-    // rows x cols values from (or to) p, rows ld apart; vec: 16-byte access
-    __device__ __forceinline__ void load(const uint16_t* p, uint64_t ld, uint32_t rows, uint32_t cols, bool vec, uint4 q[8]) const {
-        if (vec && cols % 8 == 0) {
-#pragma unroll
-            for (uint32_t i = 0; i < 8; ++i) {
-                const uint32_t r = 4 * i + lane / 8;
+            for (uint32_t i = 0; i < 4; ++i) {
+                const uint32_t r = 8 * i + lane / 4;
                 q[i] = make_uint4(0, 0, 0, 0);
-                if (r < rows && lane % 8 * 8 < cols) q[i] = *reinterpret_cast<const uint4*>(p + r * ld + lane % 8 * 8);
+                if (r < rows && lane % 4 * 8 < cols) q[i] = *reinterpret_cast<const uint4*>(p + r * ld + lane % 4 * 8);
             }
+        } else {  // column `lane`, two rows in a word
+            uint32_t w[16];
+#pragma unroll
+            for (uint32_t i = 0; i < 16; ++i) {
+                uint32_t lo = 0, hi = 0;
+                if (lane < cols && 2 * i < rows) lo = p[2 * i * ld + lane];
+                if (lane < cols && 2 * i + 1 < rows) hi = p[(2 * i + 1) * ld + lane];
+                w[i] = lo | hi << 16;
+            }
+#pragma unroll
+            for (uint32_t i = 0; i < 4; ++i) q[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+        }
+    }
+    __device__ __forceinline__ void place(const uint4 q[4], bool vec) const {
+        if (vec) {
+#pragma unroll
+            for (uint32_t i = 0; i < 4; ++i) at(8 * i + lane / 4, lane % 4) = q[i];
         } else {
 #pragma unroll
-            for (uint32_t i = 0; i < 8; ++i) {
-                const uint32_t r = 4 * i + lane / 8, c = lane % 8 * 8;
-                uint32_t w[4] = {};
+            for (uint32_t i = 0; i < 4; ++i) {
+                const uint32_t w[4] = {q[i].x, q[i].y, q[i].z, q[i].w};
 #pragma unroll
-                for (uint32_t j = 0; j < 8; ++j)
-                    if (r < rows && c + j < cols) w[j / 2] |= uint32_t(p[r * ld + c + j]) << (j % 2 * 16);
-                q[i] = make_uint4(w[0], w[1], w[2], w[3]);
+                for (uint32_t j = 0; j < 4; ++j) {
+                    value(8 * i + 2 * j, lane) = uint16_t(w[j]);
+                    value(8 * i + 2 * j + 1, lane) = uint16_t(w[j] >> 16);
+                }
             }
         }
-    }
-    __device__ __forceinline__ void put_loaded(const uint4 q[8]) const {
-        __syncwarp();
-#pragma unroll
-        for (uint32_t i = 0; i < 8; ++i) at(4 * i + lane / 8, lane % 8) = q[i];
     }
     __device__ __forceinline__ void store(uint16_t* p, uint64_t ld, uint32_t rows, uint32_t cols, bool vec) const {
-        if (vec && cols % 8 == 0) {
+        if (vec) {
 #pragma unroll
-            for (uint32_t i = 0; i < 8; ++i) {
-                const uint32_t r = 4 * i + lane / 8;
-                if (r < rows && lane % 8 * 8 < cols) *reinterpret_cast<uint4*>(p + r * ld + lane % 8 * 8) = at(r, lane % 8);
+            for (uint32_t i = 0; i < 4; ++i) {
+                const uint32_t r = 8 * i + lane / 4;
+                if (r < rows && lane % 4 * 8 < cols) *reinterpret_cast<uint4*>(p + r * ld + lane % 4 * 8) = at(r, lane % 4);
             }
-        } else {
+        } else if (lane < cols) {
+            p += lane;
 #pragma unroll 8
-            for (uint32_t r = 0; r < 32; ++r)
-#pragma unroll
-                for (uint32_t c = lane; c < kPatchCols; c += 32)
-                    if (r < rows && c < cols) p[r * ld + c] = reinterpret_cast<const uint16_t*>(&at(r, c / 8))[c % 8];
+            for (uint32_t r = 0; r < 32; ++r, p += ld)
+                if (r < rows) *p = value(r, lane);
         }
     }
 };
@@ -488,37 +490,22 @@ __device__ __forceinline__ void finish_stats(const Product& p, const Tile& o, ui
 }
 
 // One finished accumulator of a block: 128 rows, one in each lane of the four
-// warps.  `scratch` is this warp's patch, `bias` its copy of the tile's bias.
-// `release` gives the accumulator back once its last column is read.
+// warps of a column half; warps of half 0 take the patches 0, 2, ... of 32
+// columns, those of half 1 the others.  `bias` is the warp's copy of its
+// columns' bias.  `release` gives the accumulator back once the warp has read
+// its last column.  The loops over patches stay rolled: the code of one patch
+// fits the instruction cache, four of them did not.
 template <int EPI, typename Release>
 __device__ __forceinline__ void finish_tile(const Product& p, const Tiling& t, const Tile& o, uint32_t acc, uint32_t warp_row,
-                                            uint32_t lane, float alpha, uint4* scratch, const float* bias, const uint4 ahead[8],
+                                            uint32_t half, float alpha, const Patch& patch, const float* bias, uint4 ahead[4],
                                             Release release) {
+    const uint32_t lane = patch.lane;
     const uint64_t row0 = uint64_t(o.row0) + warp_row, row = row0 + lane;
     const bool live = row < o.row_end, empty = o.blocks == 0;
     const uint32_t rows = row0 < o.row_end ? uint32_t(min(uint64_t(32), o.row_end - row0)) : 0;
     const uint32_t cols = min(t.bn, uint32_t(p.n) - o.col0);
-    const Patch patch{scratch, lane};
     const int dtype = p.dtype;
-    if (EPI == kStore && (p.st.out_fp32 || p.st.sum_in)) {  // partial results in 32 bits: few, after long depths
-        for (uint32_t c = 0; c < cols; c += 32) {
-            float v[32];
-            __syncwarp();
-            if (empty) {
-#pragma unroll
-                for (uint32_t i = 0; i < 32; ++i) v[i] = 0.f;
-            } else {
-                tmem_load32(acc + c, v);
-            }
-            if (!live) continue;
-#pragma unroll
-            for (uint32_t j = 0; j < 4; ++j)
-                if (c + 8 * j < cols)
-                    store8(p, t.vec, o.group, row, o.col0 + c + 8 * j, min(8u, cols - c - 8 * j), alpha, v + 8 * j);
-        }
-        release();
-        return;
-    }
+    const StoreEpilogue& e = p.st;
     int64_t target = -1;
     float lse2 = 0.f, weight = 0.f;
     if (EPI == kLossGrad && live) {
@@ -526,84 +513,99 @@ __device__ __forceinline__ void finish_tile(const Product& p, const Tiling& t, c
         lse2 = p.ls.lse[row] * kLog2e;
         weight = p.ls.g[row];
     }
-    const StoreEpilogue& e = p.st;
-    const bool has_bias = EPI == kStore && e.bias, has_z = EPI == kStore && e.z, has_res = EPI == kStore && e.residual;
+    const bool wide = EPI == kStore && (e.out_fp32 || e.sum_in);  // partial results in 32 bits: few, after long depths
+    const bool has_bias = EPI == kStore && e.bias, has_res = EPI == kStore && e.residual && !wide;
     const uint32_t act = EPI == kStore ? e.act : uint32_t(UZIP_ACT_NONE);
     uint16_t* const out = EPI == kStore ? static_cast<uint16_t*>(e.out) + o.group * e.out_group + row0 * e.ldo + o.col0
                                         : static_cast<uint16_t*>(p.ls.out) + row0 * p.ls.ldo + o.col0;
     const uint64_t ldo = EPI == kStore ? e.ldo : p.ls.ldo;
-    uint4 q[8];
-#pragma unroll
-    for (uint32_t i = 0; i < 8; ++i) q[i] = ahead[i];
-    for (uint32_t c = 0; c < cols; c += kPatchCols) {
+    const uint16_t* const res = static_cast<const uint16_t*>(e.residual) + row0 * e.ldr + o.col0;
+    uint16_t* const z = EPI == kStore && e.z ? static_cast<uint16_t*>(e.z) + row0 * e.ldz + o.col0 : nullptr;
+    if (cols <= half * kPatchCols) release();  // nothing of this tile is this warp's
+#pragma unroll 1
+    for (uint32_t c = half * kPatchCols; c < cols; c += 2 * kPatchCols) {
         const uint32_t here = min(kPatchCols, cols - c);
-        uint32_t res[32], zw[32], yw[32];
-        if (has_res) {
-            patch.put_loaded(q);
-            patch.take_row(res);
-            if (c + kPatchCols < cols)
-                patch.load(static_cast<const uint16_t*>(e.residual) + row0 * e.ldr + o.col0 + c + kPatchCols, e.ldr, rows,
-                           min(kPatchCols, cols - c - kPatchCols), t.vec & 4, q);
+        float v[32];
+        if (empty) {
+#pragma unroll
+            for (uint32_t i = 0; i < 32; ++i) v[i] = 0.f;
+        } else {
+            tmem_load32(acc + c, v);
         }
+        if (c + 2 * kPatchCols >= cols) release();
+        if (wide) {
+            if (live) {
 #pragma unroll
-        for (uint32_t half = 0; half < 2; ++half) {
-            if (half && here <= 32) break;
-            float v[32];
-            if (empty) {
-#pragma unroll
-                for (uint32_t i = 0; i < 32; ++i) v[i] = 0.f;
-            } else {
-                tmem_load32(acc + c + 32 * half, v);
+                for (uint32_t j = 0; j < 4; ++j)
+                    if (8 * j < here) store8(p, t.vec, o.group, row, o.col0 + c + 8 * j, min(8u, here - 8 * j), alpha, v + 8 * j);
             }
-            if (c + 32 * half + 32 >= cols) release();
-            if (EPI == kLossGrad) {
+            __syncwarp();
+            continue;
+        }
+        if (EPI == kLossGrad) {
 #pragma unroll
-                for (uint32_t i = 0; i < 32; ++i) {
-                    float d = fast_exp2(fmaf(v[i], kLog2e, -lse2));
-                    if (target == int64_t(c + 32 * half + i)) d -= 1.f;
-                    v[i] = weight == 0.f ? 0.f : weight * d;
-                }
-            } else {
+            for (uint32_t i = 0; i < 32; ++i) {
+                float d = fast_exp2(fmaf(v[i], kLog2e, -lse2));
+                if (target == int64_t(c + i)) d -= 1.f;
+                v[i] = weight == 0.f ? 0.f : weight * d;
+            }
+        } else {
 #pragma unroll
-                for (uint32_t i = 0; i < 32; ++i) v[i] *= alpha;
-                if (has_bias) {
+            for (uint32_t i = 0; i < 32; ++i) v[i] *= alpha;
+            if (has_bias) {
+                const float* const b = bias + c / 2 - half * (kPatchCols / 2);  // this warp's patches one after the other
 #pragma unroll
-                    for (uint32_t i = 0; i < 32; i += 4) {
-                        const float4 f = *reinterpret_cast<const float4*>(bias + c + 32 * half + i);
-                        v[i] += f.x, v[i + 1] += f.y, v[i + 2] += f.z, v[i + 3] += f.w;
-                    }
-                }
-                if (has_z) {
-#pragma unroll
-                    for (uint32_t i = 0; i < 16; ++i) zw[16 * half + i] = to16x2(v[2 * i], v[2 * i + 1], dtype);
-                }
-                if (act == UZIP_ACT_RELU) {
-#pragma unroll
-                    for (uint32_t i = 0; i < 32; ++i) v[i] = act_value(v[i], UZIP_ACT_RELU);
-                } else if (act == UZIP_ACT_GELU) {
-#pragma unroll
-                    for (uint32_t i = 0; i < 32; ++i) v[i] = act_value(v[i], UZIP_ACT_GELU);
-                } else if (act == UZIP_ACT_SILU) {
-#pragma unroll
-                    for (uint32_t i = 0; i < 32; ++i) v[i] = act_value(v[i], UZIP_ACT_SILU);
-                }
-                if (has_res) {
-#pragma unroll
-                    for (uint32_t i = 0; i < 16; ++i) {
-                        const float2 f = from16x2(res[16 * half + i], dtype);
-                        v[2 * i] += f.x, v[2 * i + 1] += f.y;
-                    }
+                for (uint32_t i = 0; i < 32; i += 4) {
+                    const float4 f = *reinterpret_cast<const float4*>(b + i);
+                    v[i] += f.x, v[i + 1] += f.y, v[i + 2] += f.z, v[i + 3] += f.w;
                 }
             }
+            if (z) {
+                __syncwarp();
 #pragma unroll
-            for (uint32_t i = 0; i < 16; ++i) yw[16 * half + i] = to16x2(v[2 * i], v[2 * i + 1], dtype);
+                for (uint32_t i = 0; i < 4; ++i)
+                    patch.at(lane, i) = make_uint4(to16x2(v[8 * i], v[8 * i + 1], dtype), to16x2(v[8 * i + 2], v[8 * i + 3], dtype),
+                                                   to16x2(v[8 * i + 4], v[8 * i + 5], dtype), to16x2(v[8 * i + 6], v[8 * i + 7], dtype));
+                __syncwarp();
+                patch.store(z + c, e.ldz, rows, here, (t.vec & 8) && here % 8 == 0);
+            }
+            if (act == UZIP_ACT_RELU) {
+#pragma unroll
+                for (uint32_t i = 0; i < 32; ++i) v[i] = act_value(v[i], UZIP_ACT_RELU);
+            } else if (act == UZIP_ACT_GELU) {
+#pragma unroll
+                for (uint32_t i = 0; i < 32; ++i) v[i] = act_value(v[i], UZIP_ACT_GELU);
+            } else if (act == UZIP_ACT_SILU) {
+#pragma unroll
+                for (uint32_t i = 0; i < 32; ++i) v[i] = act_value(v[i], UZIP_ACT_SILU);
+            }
+            if (has_res) {
+                __syncwarp();
+                patch.place(ahead, (t.vec & 4) && here % 8 == 0);
+                __syncwarp();
+                if (c + 2 * kPatchCols < cols) {
+                    const uint32_t next = min(kPatchCols, cols - c - 2 * kPatchCols);
+                    patch.fetch(res + c + 2 * kPatchCols, e.ldr, rows, next, (t.vec & 4) && next % 8 == 0, ahead);
+                }
+#pragma unroll
+                for (uint32_t i = 0; i < 4; ++i) {
+                    const uint4 q = patch.at(lane, i);
+                    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+                    for (uint32_t j = 0; j < 4; ++j) {
+                        const float2 f = from16x2(w[j], dtype);
+                        v[8 * i + 2 * j] += f.x, v[8 * i + 2 * j + 1] += f.y;
+                    }
+                }
+            }
         }
-        if (has_z) {
-            patch.put_row(zw);
-            patch.store(static_cast<uint16_t*>(e.z) + row0 * e.ldz + o.col0 + c, e.ldz, rows, here, t.vec & 8);
-        }
-        patch.put_row(yw);
-        patch.store(out + c, ldo, rows, here, t.vec & 1);
+        __syncwarp();
+#pragma unroll
+        for (uint32_t i = 0; i < 4; ++i)
+            patch.at(lane, i) = make_uint4(to16x2(v[8 * i], v[8 * i + 1], dtype), to16x2(v[8 * i + 2], v[8 * i + 3], dtype),
+                                           to16x2(v[8 * i + 4], v[8 * i + 5], dtype), to16x2(v[8 * i + 6], v[8 * i + 7], dtype));
+        __syncwarp();
+        patch.store(out + c, ldo, rows, here, (t.vec & 1) && here % 8 == 0);
     }
     __syncwarp();
 }
@@ -614,15 +616,14 @@ __device__ __forceinline__ void finish_tile(const Product& p, const Tiling& t, c
 // LAYOUT: 0 both operands contiguous along the depth, 1 only A, 2 neither, 3
 // neither, with the depth cut by groups or skipped tokens.
 template <int EPI, int MODE, int LAYOUT>
-__global__ void __launch_bounds__(EPI == kLossStats ? kStatsThreads : kThreads, 1)
+__global__ void __launch_bounds__(kThreads, 1)
     product_kernel(const __grid_constant__ Product p, const __grid_constant__ Tiling t,
                    const __grid_constant__ Maps<LAYOUT == 3> maps) {
     constexpr bool SPLIT = MODE == 1, PAIR = MODE == 2, STATS = EPI == kLossStats;
-    constexpr uint32_t kBlock = STATS ? kStatsThreads : kThreads;
     constexpr bool A_DEEP = LAYOUT < 2, B_DEEP = LAYOUT == 0, CUT = LAYOUT == 3;
     extern __shared__ uint8_t raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
-    Control* ctl = reinterpret_cast<Control*>(smem + t.stages * t.stage_bytes + 4 * kEpilogueBytes);
+    Control* ctl = reinterpret_cast<Control*>(smem + t.stages * t.stage_bytes + kEpilogueWarps * kEpilogueBytes);
     int32_t* offsets = reinterpret_cast<int32_t*>(ctl + 1);
     int32_t* first = offsets + p.groups + 1;
     const uint32_t warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x / 32, 0), lane = threadIdx.x % 32;
@@ -632,7 +633,7 @@ __global__ void __launch_bounds__(EPI == kLossStats ? kStatsThreads : kThreads, 
     if (p.schedule != kDense) {
         const int64_t end = p.schedule == kRows ? p.m : p.depth;
         bool bad = false;
-        for (uint32_t i = threadIdx.x; i <= p.groups; i += kBlock) {
+        for (uint32_t i = threadIdx.x; i <= p.groups; i += kThreads) {
             const int64_t v = p.offsets[i];
             bad |= v < 0 || v > end || (i == 0 && v != 0) || (i == p.groups ? v != end : v > p.offsets[i + 1]);
             offsets[i] = int32_t(v);
@@ -641,7 +642,7 @@ __global__ void __launch_bounds__(EPI == kLossStats ? kStatsThreads : kThreads, 
             if (blockIdx.x == 0 && threadIdx.x == 0 && p.status) atomicCAS(p.status, 0, int(UZIP_ERR_INVALID_ARG));
             const uint16_t nan = p.dtype == UZIP_BF16 ? 0x7FC0 : 0x7E00;
             const uint64_t total = p.m * p.n * (p.schedule == kDepth ? p.groups : 1);
-            for (uint64_t i = blockIdx.x * uint64_t(kBlock) + threadIdx.x; i < total; i += uint64_t(gridDim.x) * kBlock) {
+            for (uint64_t i = blockIdx.x * uint64_t(kThreads) + threadIdx.x; i < total; i += uint64_t(gridDim.x) * kThreads) {
                 const uint64_t r = i / p.n, g = r / p.m;
                 static_cast<uint16_t*>(p.st.out)[g * p.st.out_group + (r - g * p.m) * p.st.ldo + i % p.n] = nan;
                 if (p.st.z) static_cast<uint16_t*>(p.st.z)[r * p.st.ldz + i % p.n] = nan;
@@ -672,7 +673,7 @@ __global__ void __launch_bounds__(EPI == kLossStats ? kStatsThreads : kThreads, 
         }
         for (uint32_t i = 0; i < 2; ++i) {
             mbar_init(smem_u32(&ctl->acc_full[i]), 1);
-            mbar_init(smem_u32(&ctl->acc_empty[i]), (STATS ? 8 : 4) * t.pair);  // an arrival for each epilogue warp
+            mbar_init(smem_u32(&ctl->acc_empty[i]), kEpilogueWarps * t.pair);
         }
         mbar_init(smem_u32(&ctl->drain), 1);
         ctl->abort = 0;
@@ -856,27 +857,30 @@ __global__ void __launch_bounds__(EPI == kLossStats ? kStatsThreads : kThreads, 
         Walk walk(p, t, offsets, first);
         Tile o;
         uint32_t tiles = 0;
-        const uint32_t quarter = warp % 4;  // the TMEM lanes that this warp may read
+        const uint32_t quarter = warp % 4, half = warp > 6;  // the TMEM lanes that this warp may read, its columns
         const float alpha = EPI == kStore && p.st.alpha ? *p.st.alpha : 1.f;
-        uint8_t* const mine = reinterpret_cast<uint8_t*>(ctl) - (4 - quarter) * kEpilogueBytes;
-        uint4* const scratch = reinterpret_cast<uint4*>(mine);
+        uint8_t* const mine = reinterpret_cast<uint8_t*>(ctl) - (kEpilogueWarps - 4 * half - quarter) * kEpilogueBytes;
+        const Patch patch{reinterpret_cast<uint4*>(mine), lane};
         float* const bias = reinterpret_cast<float*>(mine + kPatchBytes);
         while (walk.take(o)) {
             const uint32_t buf = tiles & 1;
-            uint4 ahead[8] = {};
+            uint4 ahead[4] = {};
             if (!SPLIT) {
                 // what the epilogue reads besides the products is fetched while they run
                 o.row0 += rank * kRowsTile;
+                const uint32_t cols = min(t.bn, uint32_t(p.n) - o.col0), c0 = half * kPatchCols;
                 if (EPI == kStore && p.st.bias) {
-                    const uint16_t* from = static_cast<const uint16_t*>(p.st.bias) + o.group * p.n + o.col0;
-                    const uint32_t cols = min(t.bn, uint32_t(p.n) - o.col0);
-                    for (uint32_t c = lane; c < cols; c += 32) bias[c] = from16(from[c], p.dtype);
+                    const uint16_t* from = static_cast<const uint16_t*>(p.st.bias) + o.group * p.n + o.col0 + c0 + lane;
+#pragma unroll
+                    for (uint32_t i = 0; i < 4; ++i)
+                        if (c0 + 2 * kPatchCols * i + lane < cols) bias[kPatchCols * i + lane] = from16(from[2 * kPatchCols * i], p.dtype);
                 }
-                if (EPI == kStore && p.st.residual && !p.st.out_fp32) {
+                if (EPI == kStore && p.st.residual && c0 < cols) {
                     const uint64_t row0 = uint64_t(o.row0) + quarter * 32;
                     const uint32_t rows = row0 < o.row_end ? uint32_t(min(uint64_t(32), o.row_end - row0)) : 0;
-                    Patch{scratch, lane}.load(static_cast<const uint16_t*>(p.st.residual) + row0 * p.st.ldr + o.col0, p.st.ldr,
-                                              rows, min(min(kPatchCols, t.bn), uint32_t(p.n) - o.col0), t.vec & 4, ahead);
+                    const uint32_t some = min(kPatchCols, cols - c0);
+                    patch.fetch(static_cast<const uint16_t*>(p.st.residual) + row0 * p.st.ldr + o.col0 + c0, p.st.ldr, rows, some,
+                                (t.vec & 4) && some % 8 == 0, ahead);
                 }
                 __syncwarp();
             }
@@ -892,12 +896,12 @@ __global__ void __launch_bounds__(EPI == kLossStats ? kStatsThreads : kThreads, 
                 }
             };
             if (!SPLIT) {
-                finish_tile<EPI>(p, t, o, acc, quarter * 32, lane, alpha, scratch, bias, ahead, release);
+                finish_tile<EPI>(p, t, o, acc, quarter * 32, half, alpha, patch, bias, ahead, release);
             } else {
                 const uint32_t lane_row = quarter * 32 + lane;
                 // partial sums to shared memory, rows bn + 4 floats apart (no bank conflicts for 16-byte access)
                 float* part = reinterpret_cast<float*>(smem) + lane_row * (t.bn + 4);
-                for (uint32_t c = 0; c < t.bn; c += 32) {
+                for (uint32_t c = 32 * half; c < t.bn; c += 64) {
                     float v[32];
                     if (o.blocks) {
                         tmem_load32(acc + c, v);
@@ -1073,7 +1077,7 @@ Tiling choose(const Product& p, int sms) {
     t.a_stage = few ? (low + t.a_box - 1) / t.a_box * t.a_box * 128 : kAStage;
     t.stage_bytes = t.a_stage + b_bytes;
     const uint32_t tables = p.schedule == kDense ? 0 : (2 * p.groups + 2) * 4;
-    const uint32_t rest = 1024 + 4 * kEpilogueBytes + sizeof(Control) + tables;
+    const uint32_t rest = 1024 + kEpilogueWarps * kEpilogueBytes + sizeof(Control) + tables;
     t.stages = std::min<uint32_t>(kMaxStages, (kSmemMost - rest) / t.stage_bytes);
     // (with splits the partial sums, 512 bn + 2 KiB bytes, take the stages' place: always less)
     t.smem = rest + t.stages * t.stage_bytes;
@@ -1109,7 +1113,7 @@ cudaError_t launch(const Product& p, const Tiling& t, int sms, const Maps<LAYOUT
     cfg.gridDim = dim3(uint32_t(MODE == 1   ? tiles * t.splits
                                 : MODE == 2 ? 2 * std::min<uint64_t>(tiles, sms / 2)
                                             : std::min<uint64_t>(tiles, sms)));
-    cfg.blockDim = dim3(EPI == kLossStats ? kStatsThreads : kThreads);
+    cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = t.smem;
     cfg.stream = s;
     cudaLaunchAttribute attr[1];

@@ -41,25 +41,32 @@ __global__ void __launch_bounds__(kThreads) fill_kernel(T* p, uint64_t ld, uint6
         p[i / cols * ld + i % cols] = value;
 }
 
-// Block (x, y, z): 128 columns, a share of the rows, one group.  A thread
-// holds 8 columns and walks every 16th row, four of them in flight; the 16
-// partial column sums meet in shared memory in a fixed order.
-constexpr uint32_t kGradCols = 128, kGradRows = 16, kGradAhead = 4;
+// Block (x, y, z): 128 columns, a share of the rows, one group.  Where rows
+// start on 16-byte boundaries a thread holds 8 neighbouring columns and walks
+// every 16th row; elsewhere it holds columns 32 apart, so that a warp still
+// reads neighbouring values, and walks every 8th row.  Four rows are in
+// flight; the partial column sums meet in shared memory in a fixed order.
+constexpr uint32_t kGradCols = 128, kGradAhead = 4;
 
-__device__ __forceinline__ uint4 load8(const uint16_t* p, bool vec, uint32_t cols) {
-    if (vec) return *reinterpret_cast<const uint4*>(p);
-    uint32_t w[4] = {};
-#pragma unroll
-    for (uint32_t j = 0; j < 8; ++j)
-        if (j < cols) w[j / 2] |= uint32_t(p[j]) << (j % 2 * 16);
-    return make_uint4(w[0], w[1], w[2], w[3]);
-}
 __device__ __forceinline__ void spread8(const uint4& q, int dtype, float v[8]) {
     const uint32_t w[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
     for (uint32_t j = 0; j < 4; ++j) {
         const float2 f = from16x2(w[j], dtype);
         v[2 * j] = f.x, v[2 * j + 1] = f.y;
+    }
+}
+template <int N>
+__device__ __forceinline__ void times_slope(float d[N], const float z[N], uint32_t act) {
+    if (act == UZIP_ACT_RELU) {
+#pragma unroll
+        for (int j = 0; j < N; ++j) d[j] *= act_slope(z[j], UZIP_ACT_RELU);
+    } else if (act == UZIP_ACT_GELU) {
+#pragma unroll
+        for (int j = 0; j < N; ++j) d[j] *= act_slope(z[j], UZIP_ACT_GELU);
+    } else if (act == UZIP_ACT_SILU) {
+#pragma unroll
+        for (int j = 0; j < N; ++j) d[j] *= act_slope(z[j], UZIP_ACT_SILU);
     }
 }
 
@@ -73,10 +80,12 @@ __device__ __forceinline__ bool offsets_bad(const int64_t* offsets, uint32_t gro
     return bad;
 }
 
+template <bool VEC>
 __global__ void __launch_bounds__(kThreads) act_grad_kernel(const __grid_constant__ ActGrad a) {
-    __shared__ float sums[kGradRows][kGradCols + 4];
-    const uint32_t tx = threadIdx.x % 16, ty = threadIdx.x / 16, g = blockIdx.z;
-    const uint64_t col = uint64_t(blockIdx.x) * kGradCols + 8 * tx;
+    constexpr uint32_t kAcross = VEC ? 16 : 32, kRows = kThreads / kAcross, kHeld = kGradCols / kAcross;
+    __shared__ float sums[kRows][kGradCols + 4];
+    const uint32_t tx = threadIdx.x % kAcross, ty = threadIdx.x / kAcross, g = blockIdx.z;
+    const uint64_t col0 = uint64_t(blockIdx.x) * kGradCols;
     uint64_t r0 = 0, r1 = a.m;
     bool bad = false;
     if (a.offsets) {
@@ -88,61 +97,68 @@ __global__ void __launch_bounds__(kThreads) act_grad_kernel(const __grid_constan
     const uint64_t share = (r1 - r0 + a.splits - 1) / a.splits;
     r0 = min(r0 + blockIdx.y * share, r1);
     r1 = min(r0 + share, r1);
-    float sum[8] = {};
-    if (col < a.n) {
-        const uint32_t cols = uint32_t(min(uint64_t(8), a.n - col));
-        const uint16_t* dy = static_cast<const uint16_t*>(a.dy) + col;
-        const uint16_t* z = static_cast<const uint16_t*>(a.z) + col;
-        uint16_t* dz = static_cast<uint16_t*>(a.dz) + col;
-        const bool vy = cols == 8 && a.lddy % 8 == 0 && reinterpret_cast<uintptr_t>(a.dy) % 16 == 0;
-        const bool vz = cols == 8 && a.ldz % 8 == 0 && reinterpret_cast<uintptr_t>(a.z) % 16 == 0;
-        const bool has_act = a.act != UZIP_ACT_NONE;
-        for (uint64_t r = r0 + ty; r < r1; r += kGradAhead * kGradRows) {
+    const bool has_act = a.act != UZIP_ACT_NONE;
+    float sum[kHeld] = {};
+    const uint16_t* const dy = static_cast<const uint16_t*>(a.dy) + col0;
+    const uint16_t* const z = static_cast<const uint16_t*>(a.z) + col0;
+    uint16_t* const dz = static_cast<uint16_t*>(a.dz) + col0;
+    const uint32_t cols = uint32_t(min(uint64_t(kGradCols), a.n - col0));
+    if (!VEC || tx * 8 < cols)
+        for (uint64_t r = r0 + ty; r < r1; r += kGradAhead * kRows) {
             uint4 qd[kGradAhead], qz[kGradAhead];
-#pragma unroll
-            for (uint32_t i = 0; i < kGradAhead; ++i)
-                if (r + i * kGradRows < r1) {
-                    qd[i] = load8(dy + (r + i * kGradRows) * a.lddy, vy, cols);
-                    if (has_act) qz[i] = load8(z + (r + i * kGradRows) * a.ldz, vz, cols);
-                }
+            uint16_t ud[kGradAhead][kHeld], uz[kGradAhead][kHeld];
 #pragma unroll
             for (uint32_t i = 0; i < kGradAhead; ++i) {
-                if (r + i * kGradRows >= r1) break;
-                float d[8], f[8];
-                spread8(qd[i], a.dtype, d);
-                if (has_act) {
-                    spread8(qz[i], a.dtype, f);
-                    if (a.act == UZIP_ACT_RELU) {
+                const uint64_t row = r + i * kRows;
+                if (row >= r1) break;
+                if (VEC) {
+                    qd[i] = *reinterpret_cast<const uint4*>(dy + row * a.lddy + 8 * tx);
+                    if (has_act) qz[i] = *reinterpret_cast<const uint4*>(z + row * a.ldz + 8 * tx);
+                } else {
 #pragma unroll
-                        for (uint32_t j = 0; j < 8; ++j) d[j] *= act_slope(f[j], UZIP_ACT_RELU);
-                    } else if (a.act == UZIP_ACT_GELU) {
-#pragma unroll
-                        for (uint32_t j = 0; j < 8; ++j) d[j] *= act_slope(f[j], UZIP_ACT_GELU);
-                    } else {
-#pragma unroll
-                        for (uint32_t j = 0; j < 8; ++j) d[j] *= act_slope(f[j], UZIP_ACT_SILU);
+                    for (uint32_t j = 0; j < kHeld; ++j) {
+                        const uint32_t c = tx + j * kAcross;
+                        ud[i][j] = c < cols ? dy[row * a.lddy + c] : 0;
+                        uz[i][j] = c < cols && has_act ? z[row * a.ldz + c] : 0;
                     }
                 }
+            }
 #pragma unroll
-                for (uint32_t j = 0; j < 8; ++j) sum[j] += d[j];
-                if (a.dz) {  // rows of the work area: padded to 16 bytes
-                    uint4 q;
-                    q.x = to16x2(d[0], d[1], a.dtype), q.y = to16x2(d[2], d[3], a.dtype);
-                    q.z = to16x2(d[4], d[5], a.dtype), q.w = to16x2(d[6], d[7], a.dtype);
-                    *reinterpret_cast<uint4*>(dz + (r + i * kGradRows) * a.lddz) = q;
+            for (uint32_t i = 0; i < kGradAhead; ++i) {
+                const uint64_t row = r + i * kRows;
+                if (row >= r1) break;
+                float d[kHeld], f[kHeld];
+                if constexpr (VEC) {
+                    spread8(qd[i], a.dtype, d);
+                    spread8(qz[i], a.dtype, f);
+                } else {
+#pragma unroll
+                    for (uint32_t j = 0; j < kHeld; ++j) d[j] = from16(ud[i][j], a.dtype), f[j] = from16(uz[i][j], a.dtype);
+                }
+                times_slope<kHeld>(d, f, a.act);
+#pragma unroll
+                for (uint32_t j = 0; j < kHeld; ++j) sum[j] += d[j];
+                if (!a.dz) continue;
+                if constexpr (VEC) {
+                    *reinterpret_cast<uint4*>(dz + row * a.lddz + 8 * tx) =
+                        make_uint4(to16x2(d[0], d[1], a.dtype), to16x2(d[2], d[3], a.dtype), to16x2(d[4], d[5], a.dtype),
+                                   to16x2(d[6], d[7], a.dtype));
+                } else {  // the work area's rows are padded to 16 bytes: the padding is written too
+#pragma unroll
+                    for (uint32_t j = 0; j < kHeld; ++j)
+                        if (col0 + tx + j * kAcross < a.lddz) dz[row * a.lddz + tx + j * kAcross] = to16(d[j], a.dtype);
                 }
             }
         }
-    }
     if (!a.db) return;
 #pragma unroll
-    for (uint32_t j = 0; j < 8; ++j) sums[ty][8 * tx + j] = sum[j];
+    for (uint32_t j = 0; j < kHeld; ++j) sums[ty][VEC ? kHeld * tx + j : tx + j * kAcross] = sum[j];
     __syncthreads();
-    const uint64_t c = uint64_t(blockIdx.x) * kGradCols + threadIdx.x;
-    if (threadIdx.x < kGradCols && c < a.n) {
+    if (threadIdx.x < cols) {
         float total = bad ? NAN : 0.f;
 #pragma unroll
-        for (uint32_t i = 0; i < kGradRows; ++i) total += sums[i][threadIdx.x];
+        for (uint32_t i = 0; i < kRows; ++i) total += sums[i][threadIdx.x];
+        const uint64_t c = col0 + threadIdx.x;
         if (a.splits > 1) a.part[(uint64_t(g) * a.splits + blockIdx.y) * a.n + c] = total;
         else static_cast<uint16_t*>(a.db)[g * a.n + c] = to16(total, a.dtype);
     }
@@ -293,7 +309,10 @@ uint32_t act_grad_splits(uint64_t m, uint64_t n, uint64_t groups) {
 cudaError_t launch_act_grad(const ActGrad& a, cudaStream_t s) {
     if (a.n == 0) return cudaSuccess;
     const dim3 grid(uint32_t((a.n + kGradCols - 1) / kGradCols), a.splits, a.groups);
-    act_grad_kernel<<<grid, kThreads, 0, s>>>(a);
+    const bool vec = a.n % 8 == 0 && a.lddy % 8 == 0 && reinterpret_cast<uintptr_t>(a.dy) % 16 == 0 &&
+                     (a.act == UZIP_ACT_NONE || (a.ldz % 8 == 0 && reinterpret_cast<uintptr_t>(a.z) % 16 == 0));
+    if (vec) act_grad_kernel<true><<<grid, kThreads, 0, s>>>(a);
+    else act_grad_kernel<false><<<grid, kThreads, 0, s>>>(a);
     cudaError_t err = cudaGetLastError();
     if (err == cudaSuccess && a.db && a.splits > 1) {
         const uint64_t total = uint64_t(a.groups) * a.n;
