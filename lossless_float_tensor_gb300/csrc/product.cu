@@ -57,6 +57,7 @@ struct Tiling {
     uint32_t tmem_cols;
     uint32_t idesc;
     uint32_t smem;
+    uint32_t out_width, z_width;  // values that rows of 16-bit results are aligned to: 8, 4, 2 or 1
     uint32_t vec;      // bit flags: 16-byte access to out 1, bias 2, residual 4, z 8, sums 16
 };
 
@@ -391,18 +392,11 @@ __device__ __forceinline__ void store8(const Product& p, uint32_t vec, uint32_t 
     }
 }
 
-__device__ __forceinline__ float fast_exp2(float v) {
-    float r;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
-    return r;
-}
-
 // An epilogue warp holds a row in each lane, which would read and write memory
 // 16 bytes a row apart.  32 rows x 32 columns of 16-bit values go through 2 KB
 // of shared memory instead (16-byte pieces swizzled by the row, free of bank
 // conflicts both ways), so that 4 lanes touch 64 contiguous bytes of a row.
-// Rows that do not start on 16-byte boundaries go a value a lane, a row at a
-// time.
+// Rows that do not start on 16-byte boundaries go in smaller pieces.
 struct Patch {
     uint4* s;  // [32][4]
     uint32_t lane;
@@ -448,19 +442,22 @@ struct Patch {
             }
         }
     }
-    __device__ __forceinline__ void store(uint16_t* p, uint64_t ld, uint32_t rows, uint32_t cols, bool vec) const {
-        if (vec) {
-#pragma unroll
-            for (uint32_t i = 0; i < 4; ++i) {
-                const uint32_t r = 8 * i + lane / 4;
-                if (r < rows && lane % 4 * 8 < cols) *reinterpret_cast<uint4*>(p + r * ld + lane % 4 * 8) = at(r, lane % 4);
-            }
-        } else if (lane < cols) {
-            p += lane;
+    // W values a lane: 32 / W lanes to a row, W rows at once
+    template <typename T>
+    __device__ __forceinline__ void store_by(uint16_t* p, uint64_t ld, uint32_t rows, uint32_t cols) const {
+        constexpr uint32_t W = sizeof(T) / 2, kLanes = 32 / W;
+        const uint32_t c = lane % kLanes * W, r0 = lane / kLanes;
+        if (c >= cols) return;
+        p += r0 * ld + c;
 #pragma unroll 8
-            for (uint32_t r = 0; r < 32; ++r, p += ld)
-                if (r < rows) *p = value(r, lane);
-        }
+        for (uint32_t r = r0; r < 32; r += W, p += W * ld)
+            if (r < rows) *reinterpret_cast<T*>(p) = *reinterpret_cast<const T*>(&value(r, c));
+    }
+    __device__ __forceinline__ void store(uint16_t* p, uint64_t ld, uint32_t rows, uint32_t cols, uint32_t width) const {
+        if (width == 8 && cols % 8 == 0) store_by<uint4>(p, ld, rows, cols);
+        else if (width >= 4 && cols % 4 == 0) store_by<uint2>(p, ld, rows, cols);
+        else if (width >= 2 && cols % 2 == 0) store_by<uint32_t>(p, ld, rows, cols);
+        else store_by<uint16_t>(p, ld, rows, cols);
     }
 };
 
@@ -567,7 +564,7 @@ __device__ __forceinline__ void finish_tile(const Product& p, const Tiling& t, c
                     patch.at(lane, i) = make_uint4(to16x2(v[8 * i], v[8 * i + 1], dtype), to16x2(v[8 * i + 2], v[8 * i + 3], dtype),
                                                    to16x2(v[8 * i + 4], v[8 * i + 5], dtype), to16x2(v[8 * i + 6], v[8 * i + 7], dtype));
                 __syncwarp();
-                patch.store(z + c, e.ldz, rows, here, (t.vec & 8) && here % 8 == 0);
+                patch.store(z + c, e.ldz, rows, here, t.z_width);
             }
             if (act == UZIP_ACT_RELU) {
 #pragma unroll
@@ -605,7 +602,7 @@ __device__ __forceinline__ void finish_tile(const Product& p, const Tiling& t, c
             patch.at(lane, i) = make_uint4(to16x2(v[8 * i], v[8 * i + 1], dtype), to16x2(v[8 * i + 2], v[8 * i + 3], dtype),
                                            to16x2(v[8 * i + 4], v[8 * i + 5], dtype), to16x2(v[8 * i + 6], v[8 * i + 7], dtype));
         __syncwarp();
-        patch.store(out + c, ldo, rows, here, (t.vec & 1) && here % 8 == 0);
+        patch.store(out + c, ldo, rows, here, t.out_width);
     }
     __syncwarp();
 }
@@ -999,6 +996,10 @@ cudaError_t make_map(CUtensorMap* map, const Operand& o, uint64_t rows, uint64_t
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
+uint32_t row_width(const void* p, uint64_t ld) {
+    const uint64_t bits = reinterpret_cast<uintptr_t>(p) / 2 | ld;
+    return bits % 8 == 0 ? 8 : bits % 4 == 0 ? 4 : bits % 2 == 0 ? 2 : 1;
+}
 bool aligned16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
 
 constexpr uint32_t kSmemMost = 227 * 1024;
@@ -1048,7 +1049,9 @@ Tiling choose(const Product& p, int sms) {
     auto consider = [&](uint32_t bn, uint32_t splits, uint32_t pair) {
         const double row_tiles = mean_row_tiles(p, pair), tiles = row_tiles * double((p.n + bn - 1) / bn * groups);
         const double at_once = double(splits > 1 ? cluster_blocks(splits, sms) / splits : sms / pair);
-        const double waves = std::ceil(tiles / at_once), running = std::min(tiles, at_once) * splits * pair;
+        // (how many tiles ragged rows make is not known: half a wave more on average)
+        const double waves = p.schedule == kRows ? std::max(1.0, tiles / at_once + 0.5) : std::ceil(tiles / at_once);
+        const double running = std::min(tiles, at_once) * splits * pair;
         const double bytes = ((pair == 2 ? kRowsTile : low) + bn / pair) * 128.0;
         const double hbm = p.schedule == kDepth ? 0 : bn / pair * 128.0 * running / 3500 / shared(row_tiles);
         const double stage = std::max({2.0 * bn + 35, bytes / (bytes > 40960 ? 62 : 78), hbm, 350.0});
@@ -1089,6 +1092,8 @@ Tiling choose(const Product& p, int sms) {
     t.idesc = 1u << 4 | fmt << 7 | fmt << 10 | (p.a.depth_major ? 0u : 1u << 15) | (p.b.depth_major ? 0u : 1u << 16) |
               (t.bn >> 3) << 17 | (kRowsTile * t.pair >> 4) << 24;
     const StoreEpilogue& e = p.st;
+    t.out_width = p.epilogue == kLossGrad ? 8 : row_width(e.out, e.ldo | e.out_group);
+    t.z_width = row_width(e.z, e.ldz);
     const uint32_t out_unit = e.out_fp32 ? 4 : 8;
     t.vec = (aligned16(e.out) && e.ldo % out_unit == 0 && e.out_group % out_unit == 0 ? 1 : 0) |
             (aligned16(e.bias) && (p.n % 8 == 0 || p.groups == 1) ? 2 : 0) | (aligned16(e.residual) && e.ldr % 8 == 0 ? 4 : 0) |

@@ -154,32 +154,52 @@ __device__ __forceinline__ uint32_t to16x2(float lo, float hi, int dtype) {
     return dtype == UZIP_BF16 ? *reinterpret_cast<const uint32_t*>(&b) : *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// erf by the rational approximation 7.1.26 of Abramowitz and Stegun, Handbook
-// of Mathematical Functions (error below 1.5e-7, a unit in the last place of a
-// value near one); a third of erff's instructions, without its branch
-__device__ __forceinline__ float erf_as(float x) {
-    const float a = fabsf(x), t = __fdividef(1.f, fmaf(0.3275911f, a, 1.f));
-    float s = fmaf(1.061405429f, t, -1.453152027f);
-    s = fmaf(s, t, 1.421413741f);
-    s = fmaf(s, t, -0.284496736f);
-    s = fmaf(s, t, 0.254829592f);
-    return copysignf(fmaf(-s * t, __expf(-a * a), 1.f), x);
+__device__ __forceinline__ float fast_exp2(float v) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
+__device__ __forceinline__ float fast_reciprocal(float v) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
+
+// 1 - Phi(|z|) exp(z^2 / 2) by the rational approximation 7.1.26 of Abramowitz
+// and Stegun, Handbook of Mathematical Functions: erfc(x) = (a1 t + ... + a5
+// t^5) exp(-x^2), t = 1 / (1 + 0.3275911 x), off by less than 1.5e-7 (a unit
+// in the last place of a value near one).  Its 14 instructions a value, the
+// exponential included, are a third of erff's.
+__device__ __forceinline__ float gauss_tail(float a) {
+    const float t = fast_reciprocal(fmaf(0.3275911f * kSqrtHalf, a, 1.f));
+    float s = fmaf(0.5f * 1.061405429f, t, 0.5f * -1.453152027f);
+    s = fmaf(s, t, 0.5f * 1.421413741f);
+    s = fmaf(s, t, 0.5f * -0.284496736f);
+    s = fmaf(s, t, 0.5f * 0.254829592f);
+    return s * t;
 }
 
 __device__ __forceinline__ float act_value(float z, uint32_t act) {
     switch (act) {
-        case UZIP_ACT_RELU: return z > 0.f || z != z ? z : 0.f;
-        case UZIP_ACT_GELU: return 0.5f * z * (1.f + erf_as(z * kSqrtHalf));
-        case UZIP_ACT_SILU: return __fdividef(z, 1.f + __expf(-z));
+        case UZIP_ACT_RELU: return z <= 0.f ? 0.f : z;
+        case UZIP_ACT_GELU: {  // z Phi(z) = max(z, 0) - |z| (1 - Phi(|z|)); past 40 the tail is zero
+            const float a = fminf(fabsf(z), 40.f), e = fast_exp2(a * (a * (-0.5f * kLog2e)));
+            return (z <= 0.f ? 0.f : z) - a * (gauss_tail(a) * e);
+        }
+        case UZIP_ACT_SILU: return z * fast_reciprocal(1.f + fast_exp2(-z * kLog2e));
         default: return z;
     }
 }
 __device__ __forceinline__ float act_slope(float z, uint32_t act) {
     switch (act) {
-        case UZIP_ACT_RELU: return z > 0.f ? 1.f : (z != z ? z : 0.f);
-        case UZIP_ACT_GELU: return 0.5f * (1.f + erf_as(z * kSqrtHalf)) + z * __expf(-0.5f * z * z) * kInvSqrt2Pi;
+        case UZIP_ACT_RELU: return z <= 0.f ? 0.f : (z > 0.f ? 1.f : z);
+        case UZIP_ACT_GELU: {  // Phi(z) + z phi(z)
+            const float a = fminf(fabsf(z), 40.f), e = fast_exp2(a * (a * (-0.5f * kLog2e)));
+            const float tail = gauss_tail(a) * e, odd = a * e * kInvSqrt2Pi;
+            return z <= 0.f ? tail - odd : (z > 0.f ? 1.f - tail + odd : z);
+        }
         case UZIP_ACT_SILU: {
-            const float q = __fdividef(1.f, 1.f + __expf(-z));
+            const float q = fast_reciprocal(1.f + fast_exp2(-z * kLog2e));
             return q * (1.f + z * (1.f - q));
         }
         default: return 1.f;

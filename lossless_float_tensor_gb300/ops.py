@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import functools
 
 from . import UZIP_BF16, UZIP_ERR_INVALID_ARG, UZIP_ERR_UNSUPPORTED_DTYPE, UZIP_FP16, UZIP_OK, UzipError, _check, library
 
@@ -18,6 +19,7 @@ UZIP_MAX_GROUPS = 1024
 ACTIVATIONS = {"none": UZIP_ACT_NONE, "relu": UZIP_ACT_RELU, "gelu": UZIP_ACT_GELU, "silu": UZIP_ACT_SILU}
 
 _i32, _i64, _u64, _vp = ctypes.c_int32, ctypes.c_int64, ctypes.c_uint64, ctypes.c_void_p
+_byref = ctypes.byref
 
 
 class LinearArgs(ctypes.Structure):
@@ -124,13 +126,17 @@ def _refuse(what: str):
     raise UzipError(UZIP_ERR_INVALID_ARG, what)
 
 
-def _dtype_code(t) -> int:
+@functools.cache
+def _dtypes():
     import torch
 
-    if t.dtype == torch.bfloat16:
-        return UZIP_BF16
-    if t.dtype == torch.float16:
-        return UZIP_FP16
+    return {torch.bfloat16: UZIP_BF16, torch.float16: UZIP_FP16}
+
+
+def _dtype_code(t) -> int:
+    code = _dtypes().get(t.dtype)
+    if code is not None:
+        return code
     raise UzipError(UZIP_ERR_UNSUPPORTED_DTYPE, f"dtype {t.dtype}")
 
 
@@ -139,10 +145,10 @@ def _matrix(t, name, shape, like):
     whose rows are contiguous."""
     if t.shape != shape:
         _refuse(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if t is not like and (t.dtype != like.dtype or t.device != like.device):
+    if t is not like and (t.dtype != like.dtype or t.get_device() != like.get_device()):
         _refuse(f"{name} is {t.dtype} on {t.device}, expected {like.dtype} on {like.device}")
-    ld, step = t.stride()[-2:]
-    rows, cols = shape[-2:]
+    *_, ld, step = t.stride()
+    rows, cols = shape[-2], shape[-1]
     if step != 1 and cols > 1:
         _refuse(f"{name}: the last dimension must be contiguous")
     if ld < cols and rows > 1:
@@ -150,9 +156,9 @@ def _matrix(t, name, shape, like):
     return t.data_ptr() or None, ld
 
 
-def _vector(t, name, shape, dtype, device):
-    if t.shape != shape or t.dtype != dtype or t.device != device or not t.is_contiguous():
-        _refuse(f"{name}: expected a contiguous {dtype} tensor of shape {tuple(shape)} on {device}")
+def _vector(t, name, shape, dtype, like):
+    if t.shape != shape or t.dtype != dtype or t.get_device() != like.get_device() or not t.is_contiguous():
+        _refuse(f"{name}: expected a contiguous {dtype} tensor of shape {tuple(shape)} on {like.device}")
     return t.data_ptr() or None
 
 
@@ -178,11 +184,14 @@ def _on(device, stream):
         yield
 
 
+_AS_IS = contextlib.nullcontext()
+
+
 def _here(device, stream):
     import torch
 
-    if stream is None and device.index == torch.cuda.current_device():
-        return contextlib.nullcontext()
+    if stream is None and device.index == torch._C._cuda_getDevice():
+        return _AS_IS
     return _on(device, stream)
 
 
@@ -191,7 +200,7 @@ def _run(name, args, device, workspace, status, check):
     import torch
 
     size, call = _calls[name]
-    ref = ctypes.byref(args)
+    ref = _byref(args)
     need = size(ref)
     if need and workspace is None:
         workspace = torch.empty(need, dtype=torch.uint8, device=device)
@@ -215,19 +224,23 @@ def _forward(name, x, w, offsets, bias, activation, residual, save_preact, out, 
     n = w.shape[-2]
     groups = 0 if offsets is None else w.shape[0]
     dev = x.device
-    a = LinearArgs(dtype=_dtype_code(x), act=_activation(activation), m=m, n=n, k=k, groups=groups)
+    a = LinearArgs(_dtype_code(x), _activation(activation), m, n, k, groups)
     a.x, a.ldx = _matrix(x, "x", (m, k), x)
     a.w, a.ldw = _matrix(w, "w", w.shape[:-1] + (k,), x)
     if offsets is not None:
         a.w_group = w.stride(0)
-        a.offsets = _vector(offsets, "offsets", (groups + 1,), torch.int64, dev)
+        a.offsets = _vector(offsets, "offsets", (groups + 1,), torch.int64, x)
     if bias is not None:
-        a.bias = _vector(bias, "bias", w.shape[:-1], x.dtype, dev)
+        a.bias = _vector(bias, "bias", w.shape[:-1], x.dtype, x)
     if residual is not None:
         a.residual, a.ldr = _matrix(residual, "residual", (m, n), x)
     with _here(dev, stream):
-        y = torch.empty((m, n), dtype=x.dtype, device=dev) if out is None else out
-        a.y, a.ldy = _matrix(y, "out", (m, n), x)
+        if out is None:
+            y = torch.empty((m, n), dtype=x.dtype, device=dev)
+            a.y, a.ldy = y.data_ptr() or None, n
+        else:
+            y = out
+            a.y, a.ldy = _matrix(y, "out", (m, n), x)
         z = torch.empty((m, n), dtype=x.dtype, device=dev) if save_preact else None
         if z is not None:
             a.z, a.ldz = z.data_ptr() or None, n
@@ -244,13 +257,13 @@ def _backward(name, dy, x, w, offsets, preact, activation, need_dx, need_dw, nee
     n = w.shape[-2]
     groups = 0 if offsets is None else w.shape[0]
     dev = x.device
-    a = LinearGradArgs(dtype=_dtype_code(x), act=_activation(activation), m=m, n=n, k=k, groups=groups)
+    a = LinearGradArgs(_dtype_code(x), _activation(activation), m, n, k, groups)
     a.dy, a.lddy = _matrix(dy, "dy", (m, n), x)
     a.x, a.ldx = _matrix(x, "x", (m, k), x)
     a.w, a.ldw = _matrix(w, "w", w.shape[:-1] + (k,), x)
     if offsets is not None:
         a.w_group = w.stride(0)
-        a.offsets = _vector(offsets, "offsets", (groups + 1,), torch.int64, dev)
+        a.offsets = _vector(offsets, "offsets", (groups + 1,), torch.int64, x)
     if a.act != UZIP_ACT_NONE:
         if preact is None:
             _refuse(f"activation {activation!r} needs the values before it (save_preact in the forward call)")
@@ -330,7 +343,7 @@ def cross_entropy(h, w, targets, *, ignore_index=-100, workspace=None, status=No
     a = CrossEntropyArgs(dtype=_dtype_code(h), t=t, v=v, d=d, ignore_index=ignore_index)
     a.h, a.ldh = _matrix(h, "h", (t, d), h)
     a.w, a.ldw = _matrix(w, "w", (v, d), h)
-    a.targets = _vector(targets, "targets", (t,), torch.int64, dev)
+    a.targets = _vector(targets, "targets", (t,), torch.int64, h)
     with _here(dev, stream):
         loss = torch.empty(t, dtype=torch.float32, device=dev)
         lse = torch.empty(t, dtype=torch.float32, device=dev)
@@ -354,9 +367,9 @@ def cross_entropy_backward(dloss, h, w, targets, lse, *, ignore_index=-100, need
     a = CrossEntropyGradArgs(dtype=_dtype_code(h), t=t, v=v, d=d, piece=piece, ignore_index=ignore_index)
     a.h, a.ldh = _matrix(h, "h", (t, d), h)
     a.w, a.ldw = _matrix(w, "w", (v, d), h)
-    a.targets = _vector(targets, "targets", (t,), torch.int64, dev)
-    a.lse = _vector(lse, "lse", (t,), torch.float32, dev)
-    a.dloss = _vector(dloss, "dloss", (t,), torch.float32, dev)
+    a.targets = _vector(targets, "targets", (t,), torch.int64, h)
+    a.lse = _vector(lse, "lse", (t,), torch.float32, h)
+    a.dloss = _vector(dloss, "dloss", (t,), torch.float32, h)
     with _here(dev, stream):
         dh = torch.empty((t, d), dtype=h.dtype, device=dev) if need_dh else None
         dw = torch.empty((v, d), dtype=h.dtype, device=dev) if need_dw else None
