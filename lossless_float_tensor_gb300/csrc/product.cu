@@ -52,7 +52,7 @@ struct Tiling {
     uint32_t stage_bytes;
     uint32_t splits;   // blocks of a cluster that share a tile's depth
     uint32_t pair;     // 2: two blocks share a tile of 256 rows, else 1
-    uint32_t a_box;    // rows of one TMA box of A (depth-major)
+    uint32_t a_box, b_box;  // rows of one TMA box (depth-major)
     uint32_t raster;   // row tiles taken together for the sake of L2
     uint32_t tmem_cols;
     uint32_t idesc;
@@ -243,7 +243,7 @@ struct Ring {
 
 // A tile of C: its group, first row and column, the end of its rows, and its depths.
 struct Tile {
-    uint32_t group, row0, row_end, col0, col_tile;
+    uint32_t group, row0, row_end, col0, cols, width;  // width: cols up to what the MMA takes
     uint32_t d0, blocks, depth_end;
 };
 
@@ -252,14 +252,17 @@ struct Tile {
 struct Walk {
     const int32_t *offsets, *first;  // shared memory
     uint32_t schedule, rows, depth, bn, splits, raster;
-    uint32_t tile_rows, row_tiles, col_tiles, total, step, next, group, split;
+    uint32_t tile_rows, row_tiles, col_tiles, total, step, next, group, split, columns, unit;
 
     __device__ __forceinline__ Walk(const Product& p, const Tiling& t, const int32_t* offsets, const int32_t* first)
         : offsets(offsets), first(first), schedule(p.schedule), rows(uint32_t(p.m)), depth(uint32_t(p.depth)), bn(t.bn),
           splits(t.splits), raster(t.raster) {
         tile_rows = kRowsTile * t.pair;
         col_tiles = (uint32_t(p.n) + bn - 1) / bn;
+        columns = uint32_t(p.n);
+        unit = 16 * t.pair;
         row_tiles = schedule == kRows ? uint32_t(first[p.groups]) : (rows + tile_rows - 1) / tile_rows;
+        if (schedule == kColumns) col_tiles = uint32_t(first[p.groups]);
         total = row_tiles * col_tiles * (schedule == kDepth ? p.groups : 1);
         const uint32_t cluster = splits * t.pair;  // one of the two is 1
         step = gridDim.x / cluster;
@@ -274,12 +277,28 @@ struct Walk {
         o.group = 0;
         o.d0 = 0;
         o.depth_end = depth;
+        if (schedule == kColumns) {
+            // a group's columns in tiles of equal width, all of them before the next rows of A
+            while (uint32_t(first[group + 1]) * row_tiles <= id) ++group;
+            const uint32_t some = first[group + 1] - first[group], count = offsets[group + 1] - offsets[group];
+            id -= first[group] * row_tiles;
+            o.group = group;
+            o.row0 = id / some * tile_rows;
+            o.row_end = rows;
+            o.width = ((count + some - 1) / some + unit - 1) / unit * unit;
+            const uint32_t c = id % some * o.width;
+            o.col0 = offsets[group] + c;
+            o.cols = min(o.width, count - c);
+            o.blocks = (depth + kDepthTile - 1) / kDepthTile;
+            return true;
+        }
+        uint32_t col_tile;
         if (schedule == kRows) {
             while (uint32_t(first[group + 1]) * col_tiles <= id) ++group;
             const uint32_t some = first[group + 1] - first[group];
             id -= first[group] * col_tiles;
             o.group = group;
-            o.col_tile = id / some;
+            col_tile = id / some;
             o.row0 = offsets[group] + id % some * tile_rows;
             o.row_end = offsets[group + 1];
         } else {
@@ -293,10 +312,12 @@ struct Walk {
             const uint32_t band = id / (raster * col_tiles), in = id - band * raster * col_tiles;
             const uint32_t some = min(raster, row_tiles - band * raster);
             o.row0 = (band * raster + in % some) * tile_rows;
-            o.col_tile = in / some;
+            col_tile = in / some;
             o.row_end = rows;
         }
-        o.col0 = o.col_tile * bn;
+        o.col0 = col_tile * bn;
+        o.cols = min(bn, columns - o.col0);
+        o.width = bn;
         o.blocks = (o.depth_end - o.d0 + kDepthTile - 1) / kDepthTile;
         if (splits > 1) {
             const uint32_t lo = o.blocks * split / splits, hi = o.blocks * (split + 1) / splits;
@@ -461,6 +482,61 @@ struct Patch {
     }
 };
 
+// An accumulator of the transposed product: lanes are output columns (features)
+// and accumulator columns are output rows (tokens), so a patch is written a
+// token a step, 32 neighbouring features at once.
+template <typename Release>
+__device__ __forceinline__ void finish_transposed(const Product& p, const Tiling& t, const Tile& o, uint32_t acc, uint32_t warp_row,
+                                                  uint32_t half, const Patch& patch, Release release) {
+    const uint32_t lane = patch.lane, feature0 = o.row0 + warp_row;
+    const uint32_t features = feature0 < o.row_end ? min(32u, o.row_end - feature0) : 0;
+    const bool empty = o.blocks == 0;
+    const int dtype = p.dtype;
+    const StoreEpilogue& e = p.st;
+    float bias = 0.f;
+    if (e.bias && lane < features) bias = from16(static_cast<const uint16_t*>(e.bias)[o.group * p.m + feature0 + lane], dtype);
+    uint16_t* const out = static_cast<uint16_t*>(e.out) + uint64_t(o.col0) * e.ldo + feature0;
+    uint16_t* const z = e.z ? static_cast<uint16_t*>(e.z) + uint64_t(o.col0) * e.ldz + feature0 : nullptr;
+    if (o.cols <= half * kPatchCols) release();
+#pragma unroll 1
+    for (uint32_t c = half * kPatchCols; c < o.cols; c += 2 * kPatchCols) {
+        const uint32_t tokens = min(32u, o.cols - c);
+        float v[32];
+        if (empty) {
+#pragma unroll
+            for (uint32_t i = 0; i < 32; ++i) v[i] = 0.f;
+        } else {
+            tmem_load32(acc + c, v);
+        }
+        if (c + 2 * kPatchCols >= o.cols) release();
+#pragma unroll
+        for (uint32_t i = 0; i < 32; ++i) v[i] += bias;
+        if (z) {
+            __syncwarp();
+#pragma unroll
+            for (uint32_t i = 0; i < 32; ++i) patch.value(i, lane) = to16(v[i], dtype);
+            __syncwarp();
+            patch.store(z + uint64_t(c) * e.ldz, e.ldz, tokens, features, t.z_width);
+        }
+        if (e.act == UZIP_ACT_RELU) {
+#pragma unroll
+            for (uint32_t i = 0; i < 32; ++i) v[i] = act_value(v[i], UZIP_ACT_RELU);
+        } else if (e.act == UZIP_ACT_GELU) {
+#pragma unroll
+            for (uint32_t i = 0; i < 32; ++i) v[i] = act_value(v[i], UZIP_ACT_GELU);
+        } else if (e.act == UZIP_ACT_SILU) {
+#pragma unroll
+            for (uint32_t i = 0; i < 32; ++i) v[i] = act_value(v[i], UZIP_ACT_SILU);
+        }
+        __syncwarp();
+#pragma unroll
+        for (uint32_t i = 0; i < 32; ++i) patch.value(i, lane) = to16(v[i], dtype);
+        __syncwarp();
+        patch.store(out + uint64_t(c) * e.ldo, e.ldo, tokens, features, t.out_width);
+    }
+    __syncwarp();
+}
+
 // The loss statistics of a row's logits in one half (128 columns) of a tile.
 __device__ __forceinline__ void finish_stats(const Product& p, const Tile& o, uint64_t row, uint32_t half, float v[128]) {
     if (row >= o.row_end) return;
@@ -500,7 +576,7 @@ __device__ __forceinline__ void finish_tile(const Product& p, const Tiling& t, c
     const uint64_t row0 = uint64_t(o.row0) + warp_row, row = row0 + lane;
     const bool live = row < o.row_end, empty = o.blocks == 0;
     const uint32_t rows = row0 < o.row_end ? uint32_t(min(uint64_t(32), o.row_end - row0)) : 0;
-    const uint32_t cols = min(t.bn, uint32_t(p.n) - o.col0);
+    const uint32_t cols = o.cols;
     const int dtype = p.dtype;
     const StoreEpilogue& e = p.st;
     int64_t target = -1;
@@ -611,13 +687,14 @@ __device__ __forceinline__ void finish_tile(const Product& p, const Tiling& t, c
 
 // MODE: 0 a block by itself, 1 a cluster splits the depth, 2 a pair of blocks.
 // LAYOUT: 0 both operands contiguous along the depth, 1 only A, 2 neither, 3
-// neither, with the depth cut by groups or skipped tokens.
+// neither, with the depth cut by groups or skipped tokens, 4 and 5 the
+// transposed product with ragged columns, A contiguous along the depth or not.
 template <int EPI, int MODE, int LAYOUT>
 __global__ void __launch_bounds__(kThreads, 1)
     product_kernel(const __grid_constant__ Product p, const __grid_constant__ Tiling t,
                    const __grid_constant__ Maps<LAYOUT == 3> maps) {
     constexpr bool SPLIT = MODE == 1, PAIR = MODE == 2, STATS = EPI == kLossStats;
-    constexpr bool A_DEEP = LAYOUT < 2, B_DEEP = LAYOUT == 0, CUT = LAYOUT == 3;
+    constexpr bool A_DEEP = LAYOUT < 2 || LAYOUT == 4, B_DEEP = LAYOUT == 0 || LAYOUT > 3, CUT = LAYOUT == 3, TURNED = LAYOUT > 3;
     extern __shared__ uint8_t raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
     Control* ctl = reinterpret_cast<Control*>(smem + t.stages * t.stage_bytes + kEpilogueWarps * kEpilogueBytes);
@@ -628,7 +705,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     // the cut of the rows or depths, checked whole
     if (p.schedule != kDense) {
-        const int64_t end = p.schedule == kRows ? p.m : p.depth;
+        const int64_t end = p.schedule == kRows ? p.m : p.schedule == kColumns ? p.n : p.depth;
         bool bad = false;
         for (uint32_t i = threadIdx.x; i <= p.groups; i += kThreads) {
             const int64_t v = p.offsets[i];
@@ -638,20 +715,22 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (__syncthreads_or(bad)) {
             if (blockIdx.x == 0 && threadIdx.x == 0 && p.status) atomicCAS(p.status, 0, int(UZIP_ERR_INVALID_ARG));
             const uint16_t nan = p.dtype == UZIP_BF16 ? 0x7FC0 : 0x7E00;
+            const uint64_t out_rows = TURNED ? p.n : p.m, out_cols = TURNED ? p.m : p.n;
             const uint64_t total = p.m * p.n * (p.schedule == kDepth ? p.groups : 1);
             for (uint64_t i = blockIdx.x * uint64_t(kThreads) + threadIdx.x; i < total; i += uint64_t(gridDim.x) * kThreads) {
-                const uint64_t r = i / p.n, g = r / p.m;
-                static_cast<uint16_t*>(p.st.out)[g * p.st.out_group + (r - g * p.m) * p.st.ldo + i % p.n] = nan;
-                if (p.st.z) static_cast<uint16_t*>(p.st.z)[r * p.st.ldz + i % p.n] = nan;
+                const uint64_t r = i / out_cols, g = r / out_rows;
+                static_cast<uint16_t*>(p.st.out)[g * p.st.out_group + (r - g * out_rows) * p.st.ldo + i % out_cols] = nan;
+                if (p.st.z) static_cast<uint16_t*>(p.st.z)[r * p.st.ldz + i % out_cols] = nan;
             }
             return;
         }
-        if (p.schedule == kRows && warp == 0) {
+        if (p.schedule != kDepth && warp == 0) {
+            const uint32_t unit = TURNED ? t.bn : kRowsTile * t.pair;
             int32_t before = 0;
             for (uint32_t i = 0; i < p.groups; i += 32) {
                 const uint32_t g = i + lane;
                 int32_t v = 0;
-                if (g < p.groups) v = int32_t((uint32_t(offsets[g + 1] - offsets[g]) + kRowsTile * t.pair - 1) / (kRowsTile * t.pair));
+                if (g < p.groups) v = int32_t((uint32_t(offsets[g + 1] - offsets[g]) + unit - 1) / unit);
 #pragma unroll
                 for (uint32_t d = 1; d < 32; d *= 2) {
                     const int32_t u = __shfl_up_sync(0xFFFFFFFFu, v, d);
@@ -695,14 +774,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             bool ok = true;
             const uint32_t b_cols = t.bn / (PAIR ? 2 : 1), slices = is_a ? 2 : (b_cols + 63) / 64;
             const uint64_t* const skip = p.skip_depth;
-            const bool by_group = walk.schedule == kRows && !is_a;
-            const uint32_t a_box = t.a_box, stage_bytes = t.stage_bytes, depth = walk.depth;
+            const bool by_group = TURNED ? is_a : walk.schedule == kRows && !is_a;
+            const uint32_t a_box = t.a_box, b_box = t.b_box, stage_bytes = t.stage_bytes, depth = walk.depth;
             const uint32_t base = smem_u32(smem) + (is_a ? 0 : t.a_stage);
             const CUtensorMap* const map = is_a ? &maps.a : &maps.b;
             while (ok && walk.take(o)) {
-                const uint32_t row0 = is_a ? o.row0 + rank * kRowsTile : o.col0 + rank * b_cols;
+                const uint32_t half_width = o.width / (PAIR ? 2 : 1), b_rows = (half_width + b_box - 1) / b_box * b_box;
+                const uint32_t row0 = is_a ? o.row0 + rank * kRowsTile : o.col0 + rank * (TURNED ? half_width : b_cols);
                 const uint32_t a_rows = PAIR ? kRowsTile : min(kRowsTile, (o.row_end - row0 + a_box - 1) / a_box * a_box);
-                const uint32_t bytes = (is_a ? (A_DEEP ? a_rows * 128 : kAStage) : (B_DEEP ? b_cols * 128 : slices * kSliceBytes)) *
+                const uint32_t bytes = (is_a ? (A_DEEP ? a_rows * 128 : kAStage) : (B_DEEP ? b_rows * 128 : slices * kSliceBytes)) *
                                        (PAIR ? 2 : 1);
                 const int gb = by_group ? int(o.group) : 0;
                 uint32_t d = o.d0;
@@ -745,11 +825,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (rank == 0) mbar_expect_tx(bar, bytes);
                     if (PAIR) bar = cluster_address(bar, 0);
                     if (is_a ? A_DEEP : B_DEEP) {
-                        if (PAIR || !is_a)
-                            tma_load<PAIR>(to, map, int(d), int(row0), gb, bar);
-                        else
-                            for (uint32_t r = 0; r < a_rows; r += a_box)
-                                tma_load<PAIR>(to + r * 128, map, int(d), int(row0 + r), 0, bar);
+                        const uint32_t box = is_a ? a_box : b_box, some = is_a ? a_rows : b_rows;
+                        for (uint32_t r = 0; r < some; r += box) tma_load<PAIR>(to + r * 128, map, int(d), int(row0 + r), gb, bar);
                     } else {
                         for (uint32_t r = 0; r < slices; ++r)
                             tma_load<PAIR>(to + r * kSliceBytes, map, int(row0 + 64 * r), int(d), gb, bar);
@@ -780,6 +857,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // this block)
             const uint64_t desc_b = matrix_descriptor(smem_u32(smem) + t.a_stage, B_DEEP);
             while (ok && walk.take(o)) {
+                const uint32_t shape = TURNED ? idesc | o.width >> 3 << 17 : idesc;
                 for (uint32_t i = 0; ok && (i < o.blocks || i == 0); ++used) {
                     const uint32_t buf = used & 1;
                     if (!(ok = wait(ctl, &ctl->acc_empty[buf], (used >> 1 & 1) ^ 1))) break;
@@ -801,10 +879,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                         tmem_fence_after();
                         const uint64_t a = desc_a + ring.s * stage_step, b = desc_b + ring.s * stage_step;
                         const uint32_t steps = CUT ? (o.depth_end - (o.d0 + i * kDepthTile) + 15) / 16 : 4;
-                        mma<PAIR>(acc, a, b, idesc, i != first_block);
-                        if (!CUT || steps > 1) mma<PAIR>(acc, a + kStepA, b + kStepB, idesc, 1);
-                        if (!CUT || steps > 2) mma<PAIR>(acc, a + 2 * kStepA, b + 2 * kStepB, idesc, 1);
-                        if (!CUT || steps > 3) mma<PAIR>(acc, a + 3 * kStepA, b + 3 * kStepB, idesc, 1);
+                        mma<PAIR>(acc, a, b, shape, i != first_block);
+                        if (!CUT || steps > 1) mma<PAIR>(acc, a + kStepA, b + kStepB, shape, 1);
+                        if (!CUT || steps > 2) mma<PAIR>(acc, a + 2 * kStepA, b + 2 * kStepB, shape, 1);
+                        if (!CUT || steps > 3) mma<PAIR>(acc, a + 3 * kStepA, b + 3 * kStepB, shape, 1);
                         mma_commit<PAIR>(smem_u32(&ctl->empty[ring.s]));
                     }
                     mma_commit<PAIR>(smem_u32(&ctl->acc_full[buf]));
@@ -823,7 +901,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         bool ok = true;
         const uint32_t quarter = warp % 4, half = warp > 6;
         while (ok && walk.take(o)) {
-            const uint32_t cols = min(t.bn, uint32_t(p.n) - o.col0), mine = cols > half * 128 ? cols - half * 128 : 0;
+            const uint32_t cols = o.cols, mine = cols > half * 128 ? cols - half * 128 : 0;
             float v[128];
 #pragma unroll
             for (uint32_t i = 0; i < 128; ++i) v[i] = 0.f;
@@ -865,14 +943,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!SPLIT) {
                 // what the epilogue reads besides the products is fetched while they run
                 o.row0 += rank * kRowsTile;
-                const uint32_t cols = min(t.bn, uint32_t(p.n) - o.col0), c0 = half * kPatchCols;
-                if (EPI == kStore && p.st.bias) {
+                const uint32_t cols = o.cols, c0 = half * kPatchCols;
+                if (EPI == kStore && !TURNED && p.st.bias) {
                     const uint16_t* from = static_cast<const uint16_t*>(p.st.bias) + o.group * p.n + o.col0 + c0 + lane;
 #pragma unroll
                     for (uint32_t i = 0; i < 4; ++i)
                         if (c0 + 2 * kPatchCols * i + lane < cols) bias[kPatchCols * i + lane] = from16(from[2 * kPatchCols * i], p.dtype);
                 }
-                if (EPI == kStore && p.st.residual && c0 < cols) {
+                if (EPI == kStore && !TURNED && p.st.residual && c0 < cols) {
                     const uint64_t row0 = uint64_t(o.row0) + quarter * 32;
                     const uint32_t rows = row0 < o.row_end ? uint32_t(min(uint64_t(32), o.row_end - row0)) : 0;
                     const uint32_t some = min(kPatchCols, cols - c0);
@@ -892,7 +970,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     else mbar_arrive(smem_u32(&ctl->acc_empty[buf]));
                 }
             };
-            if (!SPLIT) {
+            if constexpr (TURNED) {
+                finish_transposed(p, t, o, acc, quarter * 32, half, patch, release);
+            } else if constexpr (!SPLIT) {
                 finish_tile<EPI>(p, t, o, acc, quarter * 32, half, alpha, patch, bias, ahead, release);
             } else {
                 const uint32_t lane_row = quarter * 32 + lane;
@@ -1005,6 +1085,9 @@ bool aligned16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0;
 constexpr uint32_t kSmemMost = 227 * 1024;
 
 bool cut(const Product& p) { return p.schedule == kDepth || p.skip_depth; }  // depths left out, at a group's end or for skipped tokens
+uint64_t col_tiles_of(const Product& p, uint32_t bn) {
+    return p.schedule == kColumns ? p.n / bn + p.groups : (p.n + bn - 1) / bn;  // grouped: at most
+}
 uint64_t row_tiles_of(const Product& p, uint32_t pair) {
     const uint64_t unit = kRowsTile * pair;
     return p.schedule == kRows ? p.m / unit + p.groups : (p.m + unit - 1) / unit;  // grouped: at most
@@ -1017,7 +1100,7 @@ double mean_row_tiles(const Product& p, uint32_t pair) {
     return std::max(used, double(p.m) / unit + 0.5 * used);
 }
 uint64_t most_tiles(const Product& p, const Tiling& t) {
-    return row_tiles_of(p, t.pair) * ((p.n + t.bn - 1) / t.bn) * (p.schedule == kDepth ? p.groups : 1);
+    return row_tiles_of(p, t.pair) * col_tiles_of(p, t.bn) * (p.schedule == kDepth ? p.groups : 1);
 }
 
 // Blocks that run at once in clusters of `size` (a GPC's odd SMs stay idle).
@@ -1034,7 +1117,12 @@ uint32_t cluster_blocks(uint32_t size, int sms);
 // GPU).  A wave of tiles costs its stages or, where that is longer, its
 // epilogue; the last epilogue is not hidden, and joining the splits took 3.5 us
 // and half a microsecond for every 12 KB of partial sums a block.
-Tiling choose(const Product& p, int sms) {
+struct Choice {
+    Tiling t;
+    double cost;
+};
+
+Choice choose(const Product& p, int sms) {
     Tiling best{};
     double best_cost = 1e300;
     const uint64_t rows = p.m, groups = p.schedule == kDepth ? p.groups : 1;
@@ -1062,6 +1150,25 @@ Tiling choose(const Product& p, int sms) {
         best_cost = cost;
         best.bn = bn, best.splits = splits, best.pair = pair;
     };
+    // Ragged columns: a group's columns go in tiles of equal width up to bn, so a tile costs what it holds.
+    const double used = p.groups * (1 - std::exp(-double(p.n) / p.groups)), mean = p.n / std::max(1.0, used);
+    auto consider_turned = [&](uint32_t bn, uint32_t pair) {
+        const double each = mean <= 0.8 * bn ? 1.0 : mean / bn + 0.5, width = std::min<double>(bn, mean / each + 8 * pair);
+        const double tiles = used * each * double(row_tiles_of(p, pair)), at_once = double(sms / pair);
+        const double waves = std::max(1.0, tiles / at_once + 0.5), running = std::min(tiles, at_once) * pair;
+        const double bytes = (kRowsTile + width / pair) * 128.0, hbm = kRowsTile * 128.0 * running / 3500 / each;
+        const double stage = std::max({2.0 * width + 35, bytes / (bytes > 40960 ? 62 : 78), hbm, 350.0});
+        const double last = 1.5 * column * width;
+        const double cost = (waves - 1) * std::max(blocks * stage, last) + blocks * stage + last + 1000.0 * pair;
+        if (cost >= best_cost) return;
+        best_cost = cost;
+        best.bn = bn, best.splits = 1, best.pair = pair;
+    };
+    if (p.schedule == kColumns) {
+        for (uint32_t bn : {256u, 128u, 64u, 32u})
+            if (bn <= widest || bn == 32) consider_turned(bn, 1);
+        if (rows > kRowsTile) consider_turned(256, 2);
+    } else {
     for (uint32_t bn = widest; bn >= unit; bn -= unit) {
         if (bn < 32 && bn < widest) break;
         if (p.epilogue == kLossStats && bn % 128 && bn < widest) continue;  // statistics are kept for every 128 columns
@@ -1072,8 +1179,10 @@ Tiling choose(const Product& p, int sms) {
     if (rows > kRowsTile)
         for (uint32_t bn = 256; bn >= 96; bn -= 32)
             if (p.epilogue != kLossStats || bn % 128 == 0) consider(bn, 1, 2);
+    }
     Tiling& t = best;
     const uint32_t b_cols = t.bn / t.pair;
+    t.b_box = p.schedule != kColumns ? b_cols : std::min(b_cols, mean >= 96 * t.pair ? 64u : mean >= 24 ? 32u : 16u);
     const uint32_t b_bytes = p.b.depth_major ? b_cols * 128 : (b_cols + 63) / 64 * kSliceBytes;
     const bool few = t.pair == 1 && p.a.depth_major;
     t.a_box = !few ? kRowsTile : p.schedule != kRows || low < 32 ? low : rows / p.groups >= 96 ? kRowsTile : 32;
@@ -1090,7 +1199,7 @@ Tiling choose(const Product& p, int sms) {
     t.raster = 16 / t.pair;
     const uint32_t fmt = p.dtype == UZIP_BF16 ? 1 : 0;
     t.idesc = 1u << 4 | fmt << 7 | fmt << 10 | (p.a.depth_major ? 0u : 1u << 15) | (p.b.depth_major ? 0u : 1u << 16) |
-              (t.bn >> 3) << 17 | (kRowsTile * t.pair >> 4) << 24;
+              (p.schedule == kColumns ? 0 : t.bn >> 3 << 17) | (kRowsTile * t.pair >> 4) << 24;
     const StoreEpilogue& e = p.st;
     t.out_width = p.epilogue == kLossGrad ? 8 : row_width(e.out, e.ldo | e.out_group);
     t.z_width = row_width(e.z, e.ldz);
@@ -1098,7 +1207,7 @@ Tiling choose(const Product& p, int sms) {
     t.vec = (aligned16(e.out) && e.ldo % out_unit == 0 && e.out_group % out_unit == 0 ? 1 : 0) |
             (aligned16(e.bias) && (p.n % 8 == 0 || p.groups == 1) ? 2 : 0) | (aligned16(e.residual) && e.ldr % 8 == 0 ? 4 : 0) |
             (aligned16(e.z) && e.ldz % 8 == 0 ? 8 : 0) | (aligned16(e.sum_in) && e.ld_sum % 4 == 0 ? 16 : 0);
-    return t;
+    return Choice{t, best_cost};
 }
 
 template <int EPI, int MODE, int LAYOUT>
@@ -1132,11 +1241,11 @@ cudaError_t launch(const Product& p, const Tiling& t, int sms, const Maps<LAYOUT
 
 template <int EPI, int LAYOUT>
 cudaError_t launch_layout(const Product& p, const Tiling& t, int sms, cudaStream_t s) {
-    constexpr bool kCut = LAYOUT == 3, kMaySplit = EPI == kStore && !kCut;
+    constexpr bool kCut = LAYOUT == 3, kTurned = LAYOUT > 3, kMaySplit = EPI == kStore && !kCut && !kTurned;
     Maps<kCut> maps;
-    cudaError_t err = make_map(&maps.a, p.a, p.m, p.depth, 1, LAYOUT < 2 ? t.a_box : kDepthTile, p.dtype);
+    cudaError_t err = make_map(&maps.a, p.a, p.m, p.depth, kTurned ? p.groups : 1, p.a.depth_major ? t.a_box : kDepthTile, p.dtype);
     if (err == cudaSuccess)
-        err = make_map(&maps.b, p.b, p.n, p.depth, p.schedule == kRows ? p.groups : 1, LAYOUT ? kDepthTile : t.bn / t.pair, p.dtype);
+        err = make_map(&maps.b, p.b, p.n, p.depth, p.schedule == kRows ? p.groups : 1, p.b.depth_major ? t.b_box : kDepthTile, p.dtype);
     if constexpr (kCut) {
         for (uint32_t h = 0; h < kHeights && err == cudaSuccess; ++h) {
             err = make_map(&maps.a_lines[h], p.a, p.m, p.depth, 1, 1u << h, p.dtype);
@@ -1180,9 +1289,20 @@ uint32_t cluster_blocks(uint32_t size, int sms) {
 
 cudaError_t launch_product(const Product& p, int sms, cudaStream_t s) {
     if (p.m == 0 || p.n == 0) return cudaSuccess;
-    const Tiling t = choose(p, sms);
+    const Choice c = choose(p, sms);
+    const Tiling& t = c.t;
     if (p.epilogue == kLossStats) return launch_layout<kLossStats, 0>(p, t, sms, s);
     if (p.epilogue == kLossGrad) return launch_layout<kLossGrad, 0>(p, t, sms, s);
+    if (p.schedule == kRows) {
+        // Groups' rows as the columns of the transposed product: a tile takes as many as there are instead of 128 or
+        // 256, at the price of a slower epilogue.
+        Product q = p;
+        q.a = p.b, q.b = p.a, q.m = p.n, q.n = p.m, q.schedule = kColumns;
+        const Choice turned = choose(q, sms);
+        if (turned.cost < c.cost) {
+            return q.a.depth_major ? launch_layout<kStore, 4>(q, turned.t, sms, s) : launch_layout<kStore, 5>(q, turned.t, sms, s);
+        }
+    }
     if (p.b.depth_major) return launch_layout<kStore, 0>(p, t, sms, s);
     if (p.a.depth_major) return launch_layout<kStore, 1>(p, t, sms, s);
     return cut(p) ? launch_layout<kStore, 3>(p, t, sms, s) : launch_layout<kStore, 2>(p, t, sms, s);

@@ -26,7 +26,10 @@ struct Operand {
 enum Schedule : uint32_t {
     kDense = 0,  // one product
     kRows = 1,   // the rows of A and C are cut by the offsets, B belongs to the group
-    kDepth = 2   // the depth is cut by the offsets, C[group] = A_g B_g^T
+    kDepth = 2,  // the depth is cut by the offsets, C[group] = A_g B_g^T
+    // kRows with the operands exchanged, C^T = B A^T: the columns are cut by the
+    // offsets, A belongs to the group, and the results are stored transposed
+    kColumns = 3
 };
 
 enum EpilogueKind : uint32_t {
@@ -65,7 +68,7 @@ struct LossEpilogue {
 
 struct Product {
     Operand a, b;
-    uint64_t m, n, depth;  // kRows: m over all groups; kDepth: depth over all groups
+    uint64_t m, n, depth;  // kRows: m over all groups; kDepth: depth over all groups; kColumns: n over all groups
     uint32_t schedule, epilogue;
     uint32_t groups;  // 1 for kDense
     const int64_t* offsets;
