@@ -1111,12 +1111,15 @@ uint32_t cluster_blocks(uint32_t size, int sms);
 // costs the longest of its multiplication (2 cycles a column and 35), its way
 // into shared memory (78 bytes a cycle for a block, 62 where only four stages
 // fit: 128-column tiles of a single block ran at 385 to 410 cycles a stage,
-// 256-column tiles at 640 to 770, pairs of 256 x 256 at 523), the issue of its
-// copies (350 cycles) and its share of
-// HBM, where the operand B is streamed once (3500 bytes a cycle for the whole
-// GPU).  A wave of tiles costs its stages or, where that is longer, its
-// epilogue; the last epilogue is not hidden, and joining the splits took 3.5 us
-// and half a microsecond for every 12 KB of partial sums a block.
+// 256-column tiles at 640 to 770, pairs of 256 x 256 at 523) and the issue of
+// its copies (350 cycles).  A wave of tiles costs its stages or, where that is
+// longer, its epilogue and 1500 cycles; the last epilogue is not hidden, and joining the
+// splits took 3.5 us and half a microsecond for every 12 KB of partial sums a
+// block.  All bytes pass HBM once at 3500 a cycle; an operand streamed with
+// its rows contiguous comes in lines of twice the tile's columns, and below
+// 192 columns at three quarters of that rate (16 tokens through 8 experts of
+// 4096 x 14336, transposed: 103 us at 256 columns, 132 at 128).  The two times
+// overlap, less well the closer they are: they are joined by a cubic mean.
 struct Choice {
     Tiling t;
     double cost;
@@ -1132,37 +1135,37 @@ Choice choose(const Product& p, int sms) {
     const uint32_t widest = uint32_t(std::min<uint64_t>(256, (p.n + unit - 1) / unit * unit));
     const bool may_split = p.epilogue == kStore && p.schedule == kDense && !p.skip_depth;
     const double column = (p.st.ldo % 8 ? 40.0 : 14.0) * (p.st.z ? 2 : 1);  // epilogue cycles a column
-    // row tiles that take the same columns of B share what HBM delivers
-    auto shared = [&](double row_tiles) { return p.schedule == kRows ? std::max(1.0, row_tiles / p.groups) : std::min(16.0, row_tiles); };
-    auto consider = [&](uint32_t bn, uint32_t splits, uint32_t pair) {
-        const double row_tiles = mean_row_tiles(p, pair), tiles = row_tiles * double((p.n + bn - 1) / bn * groups);
-        const double at_once = double(splits > 1 ? cluster_blocks(splits, sms) / splits : sms / pair);
-        // (how many tiles ragged rows make is not known: half a wave more on average)
-        const double waves = p.schedule == kRows ? std::max(1.0, tiles / at_once + 0.5) : std::ceil(tiles / at_once);
-        const double running = std::min(tiles, at_once) * splits * pair;
-        const double bytes = ((pair == 2 ? kRowsTile : low) + bn / pair) * 128.0;
-        const double hbm = p.schedule == kDepth ? 0 : bn / pair * 128.0 * running / 3500 / shared(row_tiles);
-        const double stage = std::max({2.0 * bn + 35, bytes / (bytes > 40960 ? 62 : 78), hbm, 350.0});
-        double last = column * bn;
-        if (splits > 1) last = std::ceil(low * bn / 8.0 / (kThreads * splits)) * (1000 + 2 * column) + 6500;
-        const double cost = (waves - 1) * std::max(blocks * stage, last) + std::ceil(blocks / splits) * stage + last + 1000.0 * pair;
+    const double used = p.schedule == kRows || p.schedule == kColumns  // groups that have rows, when these are spread at random
+                            ? p.groups * (1 - std::exp(-double(p.schedule == kRows ? p.m : p.n) / p.groups)) : groups;
+    const double a_groups = p.schedule == kColumns ? used : 1, b_groups = p.schedule == kRows ? used : 1;
+    const double traffic = 2.0 * (a_groups * p.m * p.depth + b_groups * p.n * p.depth +
+                                  groups * p.m * p.n * ((p.st.z ? 2 : 1) + (p.st.residual ? 1 : 0)));
+    auto both = [](double x, double y) { return std::cbrt(x * x * x + y * y * y); };
+    auto offer = [&](uint32_t bn, uint32_t splits, uint32_t pair, double waves, double stage, double last) {
+        const double work = (waves - 1) * std::max(blocks * stage, last + 1500) + std::ceil(blocks / splits) * stage;
+        const double rate = p.schedule != kColumns && !p.b.depth_major && bn < 192 ? 2700 : 3500;
+        const double cost = both(work, traffic / rate) + last + 1000.0 * pair;
         if (cost >= best_cost) return;
         best_cost = cost;
         best.bn = bn, best.splits = splits, best.pair = pair;
     };
+    auto stage_of = [](double width, double bytes) { return std::max({2 * width + 35, bytes / (bytes > 40960 ? 62 : 78), 350.0}); };
+    auto consider = [&](uint32_t bn, uint32_t splits, uint32_t pair) {
+        const double tiles = mean_row_tiles(p, pair) * double((p.n + bn - 1) / bn * groups);
+        const double at_once = double(splits > 1 ? cluster_blocks(splits, sms) / splits : sms / pair);
+        // (how many tiles ragged rows make is not known: half a wave more on average)
+        const double waves = p.schedule == kRows ? std::max(1.0, tiles / at_once + 0.5) : std::ceil(tiles / at_once);
+        double last = column * bn;
+        if (splits > 1) last = std::ceil(low * bn / 8.0 / (kThreads * splits)) * (1000 + 2 * column) + 6500;
+        offer(bn, splits, pair, waves, stage_of(bn, ((pair == 2 ? kRowsTile : low) + bn / pair) * 128.0), last);
+    };
     // Ragged columns: a group's columns go in tiles of equal width up to bn, so a tile costs what it holds.
-    const double used = p.groups * (1 - std::exp(-double(p.n) / p.groups)), mean = p.n / std::max(1.0, used);
+    const double mean = p.n / std::max(1.0, used);
     auto consider_turned = [&](uint32_t bn, uint32_t pair) {
         const double each = mean <= 0.8 * bn ? 1.0 : mean / bn + 0.5, width = std::min<double>(bn, mean / each + 8 * pair);
-        const double tiles = used * each * double(row_tiles_of(p, pair)), at_once = double(sms / pair);
-        const double waves = std::max(1.0, tiles / at_once + 0.5), running = std::min(tiles, at_once) * pair;
-        const double bytes = (kRowsTile + width / pair) * 128.0, hbm = kRowsTile * 128.0 * running / 3500 / each;
-        const double stage = std::max({2.0 * width + 35, bytes / (bytes > 40960 ? 62 : 78), hbm, 350.0});
-        const double last = 1.5 * column * width;
-        const double cost = (waves - 1) * std::max(blocks * stage, last) + blocks * stage + last + 1000.0 * pair;
-        if (cost >= best_cost) return;
-        best_cost = cost;
-        best.bn = bn, best.splits = 1, best.pair = pair;
+        const double tiles = used * each * double(row_tiles_of(p, pair));
+        offer(bn, 1, pair, std::max(1.0, tiles / (sms / pair) + 0.5), stage_of(width, (kRowsTile + bn / pair) * 128.0),  // as many stages as fit decide
+              1.5 * column * width);
     };
     if (p.schedule == kColumns) {
         for (uint32_t bn : {256u, 128u, 64u, 32u})
