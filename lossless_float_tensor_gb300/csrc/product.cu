@@ -1,11 +1,11 @@
 // C = A B^T on the tensor cores, with a fused epilogue.
 //
 // A block (or a pair of blocks on two SMs) owns one tile of C at a time and
-// walks the tiles of the launch.  Three roles run at once: one thread fetches
-// 64 depths of both operands at a time with TMA into a ring of shared-memory
-// stages, one thread multiplies them with tcgen05.mma into TMEM, and four
-// warps turn a finished accumulator (one TMEM lane per row) into the result
-// while the next tile is multiplied into the other half of TMEM.
+// walks the tiles of the launch.  Its roles run at once: two threads fetch 64
+// depths of A and of B at a time with TMA into a ring of shared-memory stages,
+// one thread multiplies them with tcgen05.mma into TMEM, and eight warps turn a
+// finished accumulator (one TMEM lane per row) into the result while the next
+// tile is multiplied into the other half of TMEM.
 //
 // Operands may be contiguous along the depth or along the rows: the tensor
 // core reads both from the 128-byte swizzled layout that TMA writes, so the
@@ -13,7 +13,12 @@
 //
 // A pair of blocks (tcgen05 cta_group::2) multiplies 256 rows by up to 256
 // columns: each block holds its own 128 rows of A and half of the columns of
-// B, so a stage takes 32 KB instead of 48 KB and seven of them fit.
+// B, so a stage takes 32 KB instead of 48 KB and six of them fit.
+//
+// What bounds it (GB300, bf16): large products run at the tensor cores' rate,
+// 8192 x 8192 x 8192 in 571 us, 1927 TFLOP/s in short runs, and at the power
+// limit in long ones (1676 TFLOP/s over 1.5 s at 1455 MHz); one token to a few
+// dozen stream the weights, 16 x 4096 x 14336 in 23 us, 5.1 TB/s.
 #include <cuda.h>
 
 #include <algorithm>
@@ -209,8 +214,8 @@ struct Control {
     uint32_t tmem;
     volatile uint32_t abort;
 };
-// behind it, for the grouped schedules: int32 offsets[groups + 1], then (kRows)
-// first row tile of each group, int32 [groups + 1]
+// behind it, for the grouped schedules: int32 offsets[groups + 1], then (kRows,
+// kColumns) the first row or column tile of each group, int32 [groups + 1]
 
 // (the clock is read only after 64 tries: reading a timer costs more than most waits)
 __device__ __forceinline__ bool wait(Control* c, uint64_t* bar, uint32_t parity) {
@@ -241,7 +246,7 @@ struct Ring {
     }
 };
 
-// A tile of C: its group, first row and column, the end of its rows, and its depths.
+// A tile of C: its group, first row, the end of its rows, its columns and its depths.
 struct Tile {
     uint32_t group, row0, row_end, col0, cols, width;  // width: cols up to what the MMA takes
     uint32_t d0, blocks, depth_end;
