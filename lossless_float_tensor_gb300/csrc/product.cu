@@ -105,11 +105,11 @@ __device__ __forceinline__ void mma(uint32_t tmem, uint64_t a, uint64_t b, uint3
 }
 // one arrival once the products issued so far are done (a pair: on both blocks' barriers)
 template <bool PAIR>
-__device__ __forceinline__ void mma_commit(uint32_t bar) {
+__device__ __forceinline__ void mma_commit(uint32_t bar, uint32_t leader = 0) {
     if (PAIR)
         asm volatile(
             "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
-            "h"(uint16_t(3))
+            "h"(uint16_t(3u << leader))
             : "memory");
     else
         asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
@@ -269,10 +269,10 @@ struct Walk {
         row_tiles = schedule == kRows ? uint32_t(first[p.groups]) : (rows + tile_rows - 1) / tile_rows;
         if (schedule == kColumns) col_tiles = uint32_t(first[p.groups]);
         total = row_tiles * col_tiles * (schedule == kDepth ? p.groups : 1);
-        const uint32_t cluster = splits * t.pair;  // one of the two is 1
+        const uint32_t cluster = splits * t.pair;
         step = gridDim.x / cluster;
         next = blockIdx.x / cluster;
-        split = blockIdx.x % splits;
+        split = blockIdx.x % cluster / t.pair;
         group = 0;
     }
     __device__ __forceinline__ bool take(Tile& o) {
@@ -690,7 +690,8 @@ __device__ __forceinline__ void finish_tile(const Product& p, const Tiling& t, c
 
 // ---- the kernel -------------------------------------------------------------------------
 
-// MODE: 0 a block by itself, 1 a cluster splits the depth, 2 a pair of blocks.
+// MODE: 0 a block by itself, 1 a cluster of blocks splits the depth, 2 a pair of
+// blocks, 3 a cluster of pairs splits the depth.
 // LAYOUT: 0 both operands contiguous along the depth, 1 only A, 2 neither, 3
 // neither, with the depth cut by groups or skipped tokens, 4 and 5 the
 // transposed product with ragged columns, A contiguous along the depth or not.
@@ -698,7 +699,7 @@ template <int EPI, int MODE, int LAYOUT>
 __global__ void __launch_bounds__(kThreads, 1)
     product_kernel(const __grid_constant__ Product p, const __grid_constant__ Tiling t,
                    const __grid_constant__ Maps<LAYOUT == 3> maps) {
-    constexpr bool SPLIT = MODE == 1, PAIR = MODE == 2, STATS = EPI == kLossStats;
+    constexpr bool SPLIT = MODE & 1, PAIR = MODE & 2, STATS = EPI == kLossStats;
     constexpr bool A_DEEP = LAYOUT < 2 || LAYOUT == 4, B_DEEP = LAYOUT == 0 || LAYOUT > 3, CUT = LAYOUT == 3, TURNED = LAYOUT > 3;
     extern __shared__ uint8_t raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
@@ -706,7 +707,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     int32_t* offsets = reinterpret_cast<int32_t*>(ctl + 1);
     int32_t* first = offsets + p.groups + 1;
     const uint32_t warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x / 32, 0), lane = threadIdx.x % 32;
-    const uint32_t rank = PAIR ? cluster_rank() : 0;  // the pair's block 0 issues the products
+    const uint32_t rank = PAIR ? cluster_rank() & 1 : 0;  // the pair's block 0 issues the products,
+    const uint32_t leader = MODE == 3 ? cluster_rank() & ~1u : 0;  // and has this rank in the cluster
 
     // the cut of the rows or depths, checked whole
     if (p.schedule != kDense) {
@@ -812,7 +814,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             // their lines are read from beyond the tensor's end, where TMA gives zeros.  (Both operands
                             // have contiguous rows here: a depth is one line of each slice.)
                             if (rank == 0) mbar_expect_tx(bar, slices * 128 * lines * (PAIR ? 2 : 1));
-                            if (PAIR) bar = cluster_address(bar, 0);
+                            if (PAIR) bar = cluster_address(bar, leader);
                             const CUtensorMap* const heights = is_a ? maps.a_lines : maps.b_lines;
                             for (uint32_t l = 0; l < lines;) {  // runs of kept or cleared lines, in powers of two
                                 const bool kept = keep >> l & 1;
@@ -828,7 +830,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                     }
                     if (rank == 0) mbar_expect_tx(bar, bytes);
-                    if (PAIR) bar = cluster_address(bar, 0);
+                    if (PAIR) bar = cluster_address(bar, leader);
                     if (is_a ? A_DEEP : B_DEEP) {
                         const uint32_t box = is_a ? a_box : b_box, some = is_a ? a_rows : b_rows;
                         for (uint32_t r = 0; r < some; r += box) tma_load<PAIR>(to + r * 128, map, int(d), int(row0 + r), gb, bar);
@@ -871,8 +873,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const uint32_t first_block = i, end = STATS ? min(o.blocks, i + kStatsChunk) : o.blocks;
                     if (end == 0) {  // nothing to add up: the epilogues take zeros
                         if (PAIR) {
-                            cluster_arrive(cluster_address(smem_u32(&ctl->acc_full[buf]), 0));
-                            cluster_arrive(cluster_address(smem_u32(&ctl->acc_full[buf]), 1));
+                            cluster_arrive(cluster_address(smem_u32(&ctl->acc_full[buf]), leader));
+                            cluster_arrive(cluster_address(smem_u32(&ctl->acc_full[buf]), leader + 1));
                         } else {
                             mbar_arrive(smem_u32(&ctl->acc_full[buf]));
                         }
@@ -888,13 +890,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (!CUT || steps > 1) mma<PAIR>(acc, a + kStepA, b + kStepB, shape, 1);
                         if (!CUT || steps > 2) mma<PAIR>(acc, a + 2 * kStepA, b + 2 * kStepB, shape, 1);
                         if (!CUT || steps > 3) mma<PAIR>(acc, a + 3 * kStepA, b + 3 * kStepB, shape, 1);
-                        mma_commit<PAIR>(smem_u32(&ctl->empty[ring.s]));
+                        mma_commit<PAIR>(smem_u32(&ctl->empty[ring.s]), leader);
                     }
-                    mma_commit<PAIR>(smem_u32(&ctl->acc_full[buf]));
+                    mma_commit<PAIR>(smem_u32(&ctl->acc_full[buf]), leader);
                 }
             }
             if (ctl->abort) {  // products in flight end before TMEM is freed
-                mma_commit<PAIR>(smem_u32(&ctl->drain));
+                mma_commit<PAIR>(smem_u32(&ctl->drain), leader);
                 drain(&ctl->drain, 0);
             }
         }
@@ -926,7 +928,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tmem_fence_before();
                 __syncwarp();
                 if (lane == 0) {
-                    if (PAIR) cluster_arrive(cluster_address(smem_u32(&ctl->acc_empty[buf]), 0));
+                    if (PAIR) cluster_arrive(cluster_address(smem_u32(&ctl->acc_empty[buf]), leader));
                     else mbar_arrive(smem_u32(&ctl->acc_empty[buf]));
                 }
             }
@@ -971,7 +973,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tmem_fence_before();
                 __syncwarp();
                 if (lane == 0) {
-                    if (PAIR) cluster_arrive(cluster_address(smem_u32(&ctl->acc_empty[buf]), 0));
+                    if (PAIR) cluster_arrive(cluster_address(smem_u32(&ctl->acc_empty[buf]), leader));
                     else mbar_arrive(smem_u32(&ctl->acc_empty[buf]));
                 }
             };
@@ -980,7 +982,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             } else if constexpr (!SPLIT) {
                 finish_tile<EPI>(p, t, o, acc, quarter * 32, half, alpha, patch, bias, ahead, release);
             } else {
-                const uint32_t lane_row = quarter * 32 + lane;
+                const uint32_t lane_row = quarter * 32 + lane, row0 = o.row0 + rank * kRowsTile;
                 // partial sums to shared memory, rows bn + 4 floats apart (no bank conflicts for 16-byte access)
                 float* part = reinterpret_cast<float*>(smem) + lane_row * (t.bn + 4);
                 for (uint32_t c = 32 * half; c < t.bn; c += 64) {
@@ -993,7 +995,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
 #pragma unroll
                     for (uint32_t i = 0; i < 32; i += 4)
-                        if (c + i < t.bn && lane_row < o.row_end - o.row0)
+                        if (c + i < t.bn && row0 + lane_row < o.row_end)
                             *reinterpret_cast<float4*>(part + c + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
                 }
             }
@@ -1006,8 +1008,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         cluster_sync();
         Walk walk(p, t, offsets, first);
         Tile o;
-        if (walk.take(o)) {
+        if (walk.take(o) && o.row0 + rank * kRowsTile < o.row_end) {
             const float alpha = p.st.alpha ? *p.st.alpha : 1.f;
+            o.row0 += rank * kRowsTile;
             const uint32_t rows = min(kRowsTile, o.row_end - o.row0), wide = t.bn / 8, items = rows * wide;
             const uint32_t base = smem_u32(smem);
             for (uint32_t i = walk.split * kThreads + threadIdx.x; i < items; i += t.splits * kThreads) {
@@ -1018,7 +1021,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (uint32_t s = 0; s < kMaxSplits; ++s)  // all in flight at once
                     if (s < t.splits) {
-                        const uint32_t from = cluster_address(at, s);
+                        const uint32_t from = cluster_address(at, PAIR ? 2 * s + rank : s);
                         lo[s] = cluster_load4(from), hi[s] = cluster_load4(from + 16);
                     }
                 float v[8] = {};
@@ -1145,7 +1148,11 @@ Choice choose(const Product& p, int sms) {
     const double a_groups = p.schedule == kColumns ? used : 1, b_groups = p.schedule == kRows ? used : 1;
     const double traffic = 2.0 * (a_groups * p.m * p.depth + b_groups * p.n * p.depth +
                                   groups * p.m * p.n * ((p.st.z ? 2 : 1) + (p.st.residual ? 1 : 0)));
-    auto both = [](double x, double y) { return std::cbrt(x * x * x + y * y * y); };
+    auto both = [](double x, double y) {  // close to the cube root of the sum of cubes
+        const double more = std::max(x, y), share = std::min(x, y) / more;
+        return more * (1 + 0.26 * share * share * share);
+    };
+    const double row_tiles[3] = {0, mean_row_tiles(p, 1), mean_row_tiles(p, 2)};
     auto offer = [&](uint32_t bn, uint32_t splits, uint32_t pair, double waves, double stage, double last) {
         const double work = (waves - 1) * std::max(blocks * stage, last + 1500) + std::ceil(blocks / splits) * stage;
         const double rate = p.schedule != kColumns && !p.b.depth_major && bn < 192 ? 2700 : 3500;
@@ -1156,8 +1163,8 @@ Choice choose(const Product& p, int sms) {
     };
     auto stage_of = [](double width, double bytes) { return std::max({2 * width + 35, bytes / (bytes > 40960 ? 62 : 78), 350.0}); };
     auto consider = [&](uint32_t bn, uint32_t splits, uint32_t pair) {
-        const double tiles = mean_row_tiles(p, pair) * double((p.n + bn - 1) / bn * groups);
-        const double at_once = double(splits > 1 ? cluster_blocks(splits, sms) / splits : sms / pair);
+        const double tiles = row_tiles[pair] * double((p.n + bn - 1) / bn * groups);
+        const double at_once = double(splits > 1 ? cluster_blocks(splits * pair, sms) / (splits * pair) : sms / pair);
         // (how many tiles ragged rows make is not known: half a wave more on average)
         const double waves = p.schedule == kRows ? std::max(1.0, tiles / at_once + 0.5) : std::ceil(tiles / at_once);
         double last = column * bn;
@@ -1186,7 +1193,11 @@ Choice choose(const Product& p, int sms) {
     }
     if (rows > kRowsTile)
         for (uint32_t bn = 256; bn >= 96; bn -= 32)
-            if (p.epilogue != kLossStats || bn % 128 == 0) consider(bn, 1, 2);
+            if (p.epilogue != kLossStats || bn % 128 == 0) {
+                consider(bn, 1, 2);
+                if (may_split)
+                    for (uint32_t splits = 2; splits <= kMaxSplits / 2 && blocks / splits >= 4; ++splits) consider(bn, splits, 2);
+            }
     }
     Tiling& t = best;
     const uint32_t b_cols = t.bn / t.pair;
@@ -1232,7 +1243,7 @@ cudaError_t launch(const Product& p, const Tiling& t, int sms, const Maps<LAYOUT
     }
     const uint64_t tiles = most_tiles(p, t);
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(uint32_t(MODE == 1   ? tiles * t.splits
+    cfg.gridDim = dim3(uint32_t(MODE & 1    ? tiles * t.splits * t.pair
                                 : MODE == 2 ? 2 * std::min<uint64_t>(tiles, sms / 2)
                                             : std::min<uint64_t>(tiles, sms)));
     cfg.blockDim = dim3(kThreads);
@@ -1261,6 +1272,7 @@ cudaError_t launch_layout(const Product& p, const Tiling& t, int sms, cudaStream
         }
     }
     if (err != cudaSuccess) return err;
+    if (kMaySplit && t.pair == 2 && t.splits > 1) return launch<EPI, kMaySplit ? 3 : 2, LAYOUT>(p, t, sms, maps, s);
     if (t.pair == 2) return launch<EPI, 2, LAYOUT>(p, t, sms, maps, s);
     if (kMaySplit && t.splits > 1) return launch<EPI, kMaySplit ? 1 : 0, LAYOUT>(p, t, sms, maps, s);
     return launch<EPI, 0, LAYOUT>(p, t, sms, maps, s);

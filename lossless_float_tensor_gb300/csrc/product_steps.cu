@@ -299,11 +299,12 @@ cudaError_t launch_fill(void* p, uint64_t ld, uint64_t rows, uint64_t cols, uint
     return cudaGetLastError();
 }
 
-// Eight blocks for each SM, a share of at least 64 rows.
+// Eight blocks for each SM, a share of at least 256 rows: a second kernel joins
+// the shares, which costs more than 256 rows in one block.
 uint32_t act_grad_splits(uint64_t m, uint64_t n, uint64_t groups) {
     const uint64_t have = (n + kGradCols - 1) / kGradCols * groups;
     const uint64_t want = std::max<uint64_t>(1, 152 * 8 / std::max<uint64_t>(1, have));
-    return uint32_t(std::max<uint64_t>(1, std::min(want, m / groups / 64)));
+    return uint32_t(std::max<uint64_t>(1, std::min(want, m / groups / 256)));
 }
 
 cudaError_t launch_act_grad(const ActGrad& a, cudaStream_t s) {

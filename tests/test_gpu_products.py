@@ -81,6 +81,33 @@ def test_linear_backward_whole_numbers(uz, m, k, n, dtype):
     _same(only[1], dy.double().T @ x.double(), dtype)
 
 
+# sizes at which one tile is split over its depth (long depths, few tiles), by
+# single blocks and by pairs, and at which pairs take tiles of every width
+WIDE = [(20, 9000, 130), (300, 12000, 260), (640, 16400, 513), (1100, 300, 4200), (2300, 520, 2112), (1030, 4100, 1033)]
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("m,k,n", WIDE)
+def test_linear_whole_numbers_split_and_paired(uz, m, k, n, dtype):
+    g = _gen(m + k + 13 * n)
+    x, w = _whole(g, (m, k), dtype, 2, 24.0 / k), _whole(g, (n, k), dtype, 1)
+    b, r = _whole(g, (n,), dtype, 3), _whole(g, (m, n), dtype, 3)
+    dy = _whole(g, (m, n), dtype, 2, 24.0 / max(m, n))
+    y, z = uz.linear(x, w, b, activation="relu", residual=r, save_preact=True, check=True)
+    want = x.double() @ w.double().T + b.double()
+    _same(z, want, dtype)
+    _same(y, want.clamp(min=0) + r.double(), dtype)
+    dx, dw, db = uz.linear_backward(dy, x, w, check=True)
+    _same(dx, dy.double() @ w.double(), dtype)
+    _same(dw, dy.double().T @ x.double(), dtype)
+    _same(db, dy.double().sum(0), dtype)
+    # and the transposed shapes, whose gradients sum over k and n
+    dy2, x2 = _whole(g, (k, m), dtype, 2, 24.0 / max(k, m)), _whole(g, (k, n), dtype, 1)
+    _, dw, db = uz.linear_backward(dy2, x2, torch.zeros(m, n, dtype=dtype, device="cuda"), need_dx=False, check=True)
+    _same(dw, dy2.double().T @ x2.double(), dtype)
+    _same(db, dy2.double().sum(0), dtype)
+
+
 @pytest.mark.parametrize("act", ref.ACTS)
 @pytest.mark.parametrize("dtype", DTYPES)
 @pytest.mark.parametrize("m,k,n", [(1, 1024, 512), (5, 333, 70), (40, 4096, 384), (130, 257, 264), (513, 640, 1030)])
@@ -165,7 +192,7 @@ def test_activations_far_out(uz):
 # ---- grouped ---------------------------------------------------------------------
 
 COUNTS = [[5], [0, 0, 3], [1, 0, 2, 1], [64, 64], [63, 65, 1, 0, 200], [0, 130, 0, 129, 17, 0], [300, 1, 1, 1, 40],
-          [16] * 12, [0, 0], [1] * 40]
+          [16] * 12, [0, 0], [1] * 40, [700, 0, 513, 256, 1, 900], [257] * 9]
 
 
 def _offsets(counts):
