@@ -25,6 +25,7 @@
 #include <array>
 #include <atomic>
 #include <cmath>
+#include <type_traits>
 
 #include "product.cuh"
 
@@ -58,6 +59,7 @@ struct Tiling {
     uint32_t splits;   // blocks of a cluster that share a tile's depth
     uint32_t pair;     // 2: two blocks share a tile of 256 rows, else 1
     uint32_t a_box, b_box;  // rows of one TMA box (depth-major)
+    uint32_t a_slab, b_slab;  // all slices of a stage in one box (rows contiguous)
     uint32_t raster;   // row tiles taken together for the sake of L2
     uint32_t tmem_cols;
     uint32_t idesc;
@@ -217,19 +219,21 @@ struct Control {
 // behind it, for the grouped schedules: int32 offsets[groups + 1], then (kRows,
 // kColumns) the first row or column tile of each group, int32 [groups + 1]
 
-// (the clock is read only after 64 tries: reading a timer costs more than most waits)
-__device__ __forceinline__ bool wait(Control* c, uint64_t* bar, uint32_t parity) {
-    const uint32_t b = smem_u32(bar);
-    for (uint32_t i = 0; i < 64; ++i)
-        if (try_wait(b, parity)) return true;
+// A wait that is not over at its first try goes on outside the loops of the
+// fetching and multiplying threads, whose code the epilogue's warps push out of
+// the instruction cache: each line less is felt there.
+__device__ __noinline__ bool wait_on(volatile uint32_t* abort, uint32_t bar, uint32_t parity) {
     const int64_t start = clock64();
     do {
         for (uint32_t i = 0; i < 64; ++i)
-            if (try_wait(b, parity)) return true;
-        if (c->abort) return false;
+            if (try_wait(bar, parity)) return true;
+        if (*abort) return false;
     } while (clock64() - start < kWaitLimit);
-    c->abort = 1;
+    *abort = 1;
     return false;
+}
+__device__ __forceinline__ bool wait(Control* c, uint32_t bar, uint32_t parity) {
+    return try_wait(bar, parity) || wait_on(&c->abort, bar, parity);
 }
 __device__ __forceinline__ void drain(uint64_t* bar, uint32_t parity) {
     const int64_t start = clock64();
@@ -770,83 +774,92 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tmem = ctl->tmem;
     const uint32_t buffer_cols = t.tmem_cols / 2;
 
-    if (warp == 0 || warp == 6) {
-        // One thread fetches A, another B: issuing a copy takes about 100 cycles, and four to a stage (a slice of 64
-        // rows each where rows are contiguous) would take longer than the stage's products.
-        if (elect_one()) {
-            const bool is_a = warp == 0;
-            Walk walk(p, t, offsets, first);
-            Tile o;
-            Ring ring{t.stages};
-            bool ok = true;
-            const uint32_t b_cols = t.bn / (PAIR ? 2 : 1), slices = is_a ? 2 : (b_cols + 63) / 64;
-            const uint64_t* const skip = p.skip_depth;
-            const bool by_group = TURNED ? is_a : walk.schedule == kRows && !is_a;
-            const uint32_t a_box = t.a_box, b_box = t.b_box, stage_bytes = t.stage_bytes, depth = walk.depth;
-            const uint32_t base = smem_u32(smem) + (is_a ? 0 : t.a_stage);
-            const CUtensorMap* const map = is_a ? &maps.a : &maps.b;
-            while (ok && walk.take(o)) {
-                const uint32_t half_width = o.width / (PAIR ? 2 : 1), b_rows = (half_width + b_box - 1) / b_box * b_box;
-                const uint32_t row0 = is_a ? o.row0 + rank * kRowsTile : o.col0 + rank * (TURNED ? half_width : b_cols);
-                const uint32_t a_rows = PAIR ? kRowsTile : min(kRowsTile, (o.row_end - row0 + a_box - 1) / a_box * a_box);
-                const uint32_t bytes = (is_a ? (A_DEEP ? a_rows * 128 : kAStage) : (B_DEEP ? b_rows * 128 : slices * kSliceBytes)) *
-                                       (PAIR ? 2 : 1);
-                const int gb = by_group ? int(o.group) : 0;
-                uint32_t d = o.d0;
-                uint64_t skip_next = CUT && skip && o.blocks ? skip[d / 64] : 0;
-                for (uint32_t i = 0; i < o.blocks; ++i, d += kDepthTile, ring.advance()) {
-                    const uint64_t skip_now = skip_next;
-                    if (CUT && skip && i + 1 < o.blocks) skip_next = skip[d / 64 + 1];
-                    if (!(ok = wait(ctl, &ctl->empty[ring.s], ring.phase ^ 1))) break;
-                    uint32_t bar = smem_u32(&ctl->full[ring.s]);
-                    const uint32_t to = base + ring.s * stage_bytes;
-                    if constexpr (CUT) {
-                        const uint32_t left = o.depth_end - d;
+    // One thread fetches A, another B: issuing a copy takes about 100 cycles, more while the epilogue's warps are busy,
+    // and up to four to a stage would take longer than the stage's products.
+    const auto fetch = [&](auto which) {
+        constexpr bool IS_A = decltype(which)::value, DEEP = IS_A ? A_DEEP : B_DEEP;
+        Walk walk(p, t, offsets, first);
+        Tile o;
+        Ring ring{t.stages};
+        bool ok = true;
+        const uint32_t b_cols = t.bn / (PAIR ? 2 : 1), slices = IS_A ? 2 : (b_cols + 63) / 64;
+        const uint64_t* const skip = p.skip_depth;
+        const bool by_group = TURNED ? IS_A : walk.schedule == kRows && !IS_A;
+        const bool slab = !DEEP && (IS_A ? t.a_slab : t.b_slab);
+        const uint32_t box = IS_A ? t.a_box : t.b_box, stage_bytes = t.stage_bytes;
+        [[maybe_unused]] const uint32_t depth = walk.depth;
+        const uint32_t base = smem_u32(smem) + (IS_A ? 0 : t.a_stage), full = smem_u32(ctl->full), empty = smem_u32(ctl->empty);
+        const uint32_t leader_full = PAIR ? cluster_address(full, leader) : full;
+        const CUtensorMap* const map = IS_A ? &maps.a : &maps.b;
+        while (ok && walk.take(o)) {
+            const uint32_t half_width = o.width / (PAIR ? 2 : 1);
+            const uint32_t row0 = IS_A ? o.row0 + rank * kRowsTile : o.col0 + rank * (TURNED ? half_width : b_cols);
+            // rows in whole boxes (a pair's A: always 128)
+            const uint32_t rows = IS_A ? (PAIR ? kRowsTile : min(kRowsTile, (o.row_end - row0 + box - 1) / box * box))
+                                       : (half_width + box - 1) / box * box;
+            const uint32_t bytes = (DEEP ? rows * 128 : slices * kSliceBytes) * (PAIR ? 2 : 1);
+            const int group = by_group ? int(o.group) : 0;
+            uint32_t d = o.d0;
+            [[maybe_unused]] uint64_t skip_next = CUT && skip && o.blocks ? skip[d / 64] : 0;
+            for (uint32_t i = 0; i < o.blocks; ++i, d += kDepthTile, ring.advance()) {
+                [[maybe_unused]] const uint64_t skip_now = skip_next;
+                if (CUT && skip && i + 1 < o.blocks) skip_next = skip[d / 64 + 1];
+                if (!(ok = wait(ctl, empty + 8 * ring.s, ring.phase ^ 1))) break;
+                const uint32_t mine = full + 8 * ring.s, bar = leader_full + 8 * ring.s;
+                const uint32_t to = base + ring.s * stage_bytes;
+                if constexpr (CUT) {
+                    const uint32_t left = o.depth_end - d;
+                    if (left < kDepthTile || skip_now) {
                         uint32_t lines = kDepthTile;
-                        uint64_t keep = ~0ull;
+                        uint64_t keep = ~skip_now;
                         if (left < kDepthTile) {
                             lines = (left + 15) / 16 * 16;
-                            keep >>= 64 - left;
+                            keep &= ~0ull >> (64 - left);
                         }
-                        keep &= ~skip_now;
-                        if (~keep) {
-                            // Depths past the group's end belong to its neighbour, and skipped ones may hold anything:
-                            // their lines are read from beyond the tensor's end, where TMA gives zeros.  (Both operands
-                            // have contiguous rows here: a depth is one line of each slice.)
-                            if (rank == 0) mbar_expect_tx(bar, slices * 128 * lines * (PAIR ? 2 : 1));
-                            if (PAIR) bar = cluster_address(bar, leader);
-                            const CUtensorMap* const heights = is_a ? maps.a_lines : maps.b_lines;
-                            for (uint32_t l = 0; l < lines;) {  // runs of kept or cleared lines, in powers of two
-                                const bool kept = keep >> l & 1;
-                                const uint64_t other = (kept ? ~keep : keep) >> l;
-                                const uint32_t run = min(other ? uint32_t(__ffsll(other)) - 1 : 64u, lines - l);
-                                const uint32_t h = min(31u - __clz(run), kHeights - 1);
-                                const int from = int(kept ? d + l : depth);
-                                for (uint32_t r = 0; r < slices; ++r)
-                                    tma_load<PAIR>(to + r * kSliceBytes + l * 128, &heights[h], int(row0 + 64 * r), from, 0, bar);
-                                l += 1u << h;
-                            }
-                            continue;
+                        // Depths past the group's end belong to its neighbour, and skipped ones may hold anything: their
+                        // lines are read from beyond the tensor's end, where TMA gives zeros.  (Both operands have
+                        // contiguous rows here: a depth is one line of each slice.)
+                        if (rank == 0) mbar_expect_tx(mine, slices * 128 * lines * (PAIR ? 2 : 1));
+                        const CUtensorMap* const heights = IS_A ? maps.a_lines : maps.b_lines;
+                        for (uint32_t l = 0; l < lines;) {  // runs of kept or cleared lines, in powers of two
+                            const bool kept = keep >> l & 1;
+                            const uint64_t other = (kept ? ~keep : keep) >> l;
+                            const uint32_t run = min(other ? uint32_t(__ffsll(other)) - 1 : 64u, lines - l);
+                            const uint32_t h = min(31u - __clz(run), kHeights - 1);
+                            const int from = int(kept ? d + l : depth);
+                            for (uint32_t r = 0; r < slices; ++r)
+                                tma_load<PAIR>(to + r * kSliceBytes + l * 128, &heights[h], int(row0 + 64 * r), from, 0, bar);
+                            l += 1u << h;
                         }
+                        continue;
                     }
-                    if (rank == 0) mbar_expect_tx(bar, bytes);
-                    if (PAIR) bar = cluster_address(bar, leader);
-                    if (is_a ? A_DEEP : B_DEEP) {
-                        const uint32_t box = is_a ? a_box : b_box, some = is_a ? a_rows : b_rows;
-                        for (uint32_t r = 0; r < some; r += box) tma_load<PAIR>(to + r * 128, map, int(d), int(row0 + r), gb, bar);
-                    } else {
-                        for (uint32_t r = 0; r < slices; ++r)
-                            tma_load<PAIR>(to + r * kSliceBytes, map, int(row0 + 64 * r), int(d), gb, bar);
-                    }
+                }
+                if (rank == 0) mbar_expect_tx(mine, bytes);
+                if constexpr (DEEP) {
+                    tma_load<PAIR>(to, map, int(d), int(row0), group, bar);
+                    for (uint32_t r = box; r < rows; r += box) tma_load<PAIR>(to + r * 128, map, int(d), int(row0 + r), group, bar);
+                } else if (slab) {
+                    tma_load<PAIR>(to, map, 0, int(d), int(row0 / 64), bar);
+                } else {
+                    tma_load<PAIR>(to, map, int(row0), int(d), group, bar);
+                    for (uint32_t r = 1; r < slices; ++r)
+                        tma_load<PAIR>(to + r * kSliceBytes, map, int(row0 + 64 * r), int(d), group, bar);
                 }
             }
-            // copies in flight (a pair's: both blocks') land before the block ends
-            if (ctl->abort && rank == 0 && is_a)
-                for (uint32_t i = 0; i < min(ring.used, t.stages); ++i) {
-                    const uint32_t back = ring.s > i ? ring.s - 1 - i : ring.s + t.stages - 1 - i;
-                    drain(&ctl->full[back], ring.s > i ? ring.phase : ring.phase ^ 1);
-                }
         }
+        // copies in flight (a pair's: both blocks') land before the block ends
+        if (ctl->abort && rank == 0 && IS_A)
+            for (uint32_t i = 0; i < min(ring.used, t.stages); ++i) {
+                const uint32_t back = ring.s > i ? ring.s - 1 - i : ring.s + t.stages - 1 - i;
+                drain(&ctl->full[back], ring.s > i ? ring.phase : ring.phase ^ 1);
+            }
+    };
+
+    if (warp == 0) {
+        if (elect_one()) fetch(std::true_type{});
+        __syncwarp();
+    } else if (warp == 6) {
+        if (elect_one()) fetch(std::false_type{});
         __syncwarp();
     } else if (warp == 1) {
         if (rank == 0 && elect_one()) {
@@ -857,7 +870,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             bool ok = true;
             // 16 depths further: 32 bytes along the depth, or 16 lines
             constexpr uint32_t kStepA = A_DEEP ? 2 : 128, kStepB = B_DEEP ? 2 : 128;
-            const uint32_t idesc = t.idesc, stage_step = t.stage_bytes >> 4;
+            const uint32_t idesc = t.idesc, stage_step = t.stage_bytes >> 4, full = smem_u32(ctl->full), empty = smem_u32(ctl->empty);
             const uint64_t desc_a = matrix_descriptor(smem_u32(smem), A_DEEP);
             // (the tensor core reads 128 rows of A also where a stage holds fewer: those accumulator rows are never
             // stored, and what lies there, the stage's B, later stages or the epilogue's patches, is shared memory of
@@ -867,7 +880,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const uint32_t shape = TURNED ? idesc | o.width >> 3 << 17 : idesc;
                 for (uint32_t i = 0; ok && (i < o.blocks || i == 0); ++used) {
                     const uint32_t buf = used & 1;
-                    if (!(ok = wait(ctl, &ctl->acc_empty[buf], (used >> 1 & 1) ^ 1))) break;
+                    if (!(ok = wait(ctl, smem_u32(&ctl->acc_empty[buf]), (used >> 1 & 1) ^ 1))) break;
                     tmem_fence_after();
                     const uint32_t acc = tmem + buf * buffer_cols;
                     const uint32_t first_block = i, end = STATS ? min(o.blocks, i + kStatsChunk) : o.blocks;
@@ -882,7 +895,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         continue;
                     }
                     for (; i < end; ++i, ring.advance()) {
-                        if (!(ok = wait(ctl, &ctl->full[ring.s], ring.phase))) break;
+                        if (!(ok = wait(ctl, full + 8 * ring.s, ring.phase))) break;
                         tmem_fence_after();
                         const uint64_t a = desc_a + ring.s * stage_step, b = desc_b + ring.s * stage_step;
                         const uint32_t steps = CUT ? (o.depth_end - (o.d0 + i * kDepthTile) + 15) / 16 : 4;
@@ -890,7 +903,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (!CUT || steps > 1) mma<PAIR>(acc, a + kStepA, b + kStepB, shape, 1);
                         if (!CUT || steps > 2) mma<PAIR>(acc, a + 2 * kStepA, b + 2 * kStepB, shape, 1);
                         if (!CUT || steps > 3) mma<PAIR>(acc, a + 3 * kStepA, b + 3 * kStepB, shape, 1);
-                        mma_commit<PAIR>(smem_u32(&ctl->empty[ring.s]), leader);
+                        mma_commit<PAIR>(empty + 8 * ring.s, leader);
                     }
                     mma_commit<PAIR>(smem_u32(&ctl->acc_full[buf]), leader);
                 }
@@ -914,7 +927,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (uint32_t i = 0; i < 128; ++i) v[i] = 0.f;
             for (uint32_t i = 0; i < max(o.blocks, 1u); i += kStatsChunk, ++used) {
                 const uint32_t buf = used & 1;
-                if (!(ok = __all_sync(0xFFFFFFFFu, wait(ctl, &ctl->acc_full[buf], used >> 1 & 1)))) break;
+                if (!(ok = __all_sync(0xFFFFFFFFu, wait(ctl, smem_u32(&ctl->acc_full[buf]), used >> 1 & 1)))) break;
                 tmem_fence_after();
                 const uint32_t acc = tmem + buf * buffer_cols + half * 128 + (quarter * 32 << 16);
 #pragma unroll
@@ -966,7 +979,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 __syncwarp();
             }
-            if (!__all_sync(0xFFFFFFFFu, wait(ctl, &ctl->acc_full[buf], tiles >> 1 & 1))) break;
+            if (!__all_sync(0xFFFFFFFFu, wait(ctl, smem_u32(&ctl->acc_full[buf]), tiles >> 1 & 1))) break;
             tmem_fence_after();
             const uint32_t acc = tmem + buf * buffer_cols + (quarter * 32 << 16);
             const auto release = [&] {
@@ -1065,8 +1078,10 @@ EncodeFn encode_fn() {
 }
 
 // rows x depth x groups of 16-bit values, read in swizzled boxes of 64 contiguous values
+// (outer: rows of a box along the depth, else its depths); with slices, rows are contiguous, a multiple of 64, and a box
+// holds that many slices of 64
 cudaError_t make_map(CUtensorMap* map, const Operand& o, uint64_t rows, uint64_t depth, uint64_t groups, uint32_t box_outer,
-                     int dtype) {
+                     int dtype, uint32_t slices = 0) {
     const uint64_t inner = o.depth_major ? depth : rows, outer = o.depth_major ? rows : depth;
     if (inner == 0 || outer == 0) {  // nothing to load
         *map = CUtensorMap{};
@@ -1074,10 +1089,10 @@ cudaError_t make_map(CUtensorMap* map, const Operand& o, uint64_t rows, uint64_t
     }
     EncodeFn fn = encode_fn();
     if (!fn) return cudaErrorNotSupported;
-    const cuuint64_t dims[3] = {inner, outer, groups};
-    const uint64_t group = groups > 1 ? o.group * 2 : std::min<uint64_t>(o.ld * 2 * outer, uint64_t(1) << 39);
+    const cuuint64_t dims[3] = {slices ? 64 : inner, outer, slices ? rows / 64 : groups};
+    const uint64_t group = slices ? 128 : groups > 1 ? o.group * 2 : std::min<uint64_t>(o.ld * 2 * outer, uint64_t(1) << 39);
     const cuuint64_t strides[2] = {o.ld * 2, group};
-    const cuuint32_t box[3] = {64, box_outer, 1}, ones[3] = {1, 1, 1};
+    const cuuint32_t box[3] = {64, box_outer, slices ? slices : 1}, ones[3] = {1, 1, 1};
     const CUresult r = fn(map, dtype == UZIP_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,
                           const_cast<void*>(o.p), dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
                           CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
@@ -1202,6 +1217,10 @@ Choice choose(const Product& p, int sms) {
     Tiling& t = best;
     const uint32_t b_cols = t.bn / t.pair;
     t.b_box = p.schedule != kColumns ? b_cols : std::min(b_cols, mean >= 96 * t.pair ? 64u : mean >= 24 ? 32u : 16u);
+    // the slices of a stage come in one box where they end with the rows (the third dimension is the groups' otherwise)
+    const bool one_group = p.schedule == kDense || p.schedule == kDepth;
+    t.a_slab = one_group && !p.a.depth_major && p.m % 64 == 0 ? 2 : 0;
+    t.b_slab = one_group && !p.b.depth_major && p.n % 64 == 0 && b_cols % 64 == 0 ? b_cols / 64 : 0;
     const uint32_t b_bytes = p.b.depth_major ? b_cols * 128 : (b_cols + 63) / 64 * kSliceBytes;
     const bool few = t.pair == 1 && p.a.depth_major;
     t.a_box = !few ? kRowsTile : p.schedule != kRows || low < 32 ? low : rows / p.groups >= 96 ? kRowsTile : 32;
@@ -1262,9 +1281,10 @@ template <int EPI, int LAYOUT>
 cudaError_t launch_layout(const Product& p, const Tiling& t, int sms, cudaStream_t s) {
     constexpr bool kCut = LAYOUT == 3, kTurned = LAYOUT > 3, kMaySplit = EPI == kStore && !kCut && !kTurned;
     Maps<kCut> maps;
-    cudaError_t err = make_map(&maps.a, p.a, p.m, p.depth, kTurned ? p.groups : 1, p.a.depth_major ? t.a_box : kDepthTile, p.dtype);
+    cudaError_t err = make_map(&maps.a, p.a, p.m, p.depth, kTurned ? p.groups : 1, p.a.depth_major ? t.a_box : kDepthTile, p.dtype, t.a_slab);
     if (err == cudaSuccess)
-        err = make_map(&maps.b, p.b, p.n, p.depth, p.schedule == kRows ? p.groups : 1, p.b.depth_major ? t.b_box : kDepthTile, p.dtype);
+        err = make_map(&maps.b, p.b, p.n, p.depth, p.schedule == kRows ? p.groups : 1, p.b.depth_major ? t.b_box : kDepthTile, p.dtype,
+                       t.b_slab);
     if constexpr (kCut) {
         for (uint32_t h = 0; h < kHeights && err == cudaSuccess; ++h) {
             err = make_map(&maps.a_lines[h], p.a, p.m, p.depth, 1, 1u << h, p.dtype);
