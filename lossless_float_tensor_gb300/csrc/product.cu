@@ -263,9 +263,11 @@ struct Walk {
     uint32_t schedule, rows, depth, bn, splits, raster;
     uint32_t tile_rows, row_tiles, col_tiles, total, step, next, group, split, columns, unit;
 
-    __device__ __forceinline__ Walk(const Product& p, const Tiling& t, const int32_t* offsets, const int32_t* first)
-        : offsets(offsets), first(first), schedule(p.schedule), rows(uint32_t(p.m)), depth(uint32_t(p.depth)), bn(t.bn),
-          splits(t.splits), raster(t.raster) {
+    // rows and depth: how many there are
+    __device__ __forceinline__ Walk(const Product& p, const Tiling& t, const int32_t* offsets, const int32_t* first, uint32_t rows,
+                                    uint32_t depth)
+        : offsets(offsets), first(first), schedule(p.schedule), rows(rows), depth(depth), bn(t.bn), splits(t.splits),
+          raster(t.raster) {
         tile_rows = kRowsTile * t.pair;
         col_tiles = (uint32_t(p.n) + bn - 1) / bn;
         columns = uint32_t(p.n);
@@ -697,7 +699,7 @@ __device__ __forceinline__ void finish_tile(const Product& p, const Tiling& t, c
 // MODE: 0 a block by itself, 1 a cluster of blocks splits the depth, 2 a pair of
 // blocks, 3 a cluster of pairs splits the depth.
 // LAYOUT: 0 both operands contiguous along the depth, 1 only A, 2 neither, 3
-// neither, with the depth cut by groups or skipped tokens, 4 and 5 the
+// neither, with a depth that only the device knows, 4 and 5 the
 // transposed product with ragged columns, A contiguous along the depth or not.
 template <int EPI, int MODE, int LAYOUT>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -713,6 +715,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x / 32, 0), lane = threadIdx.x % 32;
     const uint32_t rank = PAIR ? cluster_rank() & 1 : 0;  // the pair's block 0 issues the products,
     const uint32_t leader = MODE == 3 ? cluster_rank() & ~1u : 0;  // and has this rank in the cluster
+
+    const uint32_t live_rows = p.live_rows ? *p.live_rows : uint32_t(p.m), live_depth = p.live_depth ? *p.live_depth : uint32_t(p.depth);
 
     // the cut of the rows or depths, checked whole
     if (p.schedule != kDense) {
@@ -778,16 +782,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     // and up to four to a stage would take longer than the stage's products.
     const auto fetch = [&](auto which) {
         constexpr bool IS_A = decltype(which)::value, DEEP = IS_A ? A_DEEP : B_DEEP;
-        Walk walk(p, t, offsets, first);
+        Walk walk(p, t, offsets, first, live_rows, live_depth);
         Tile o;
         Ring ring{t.stages};
         bool ok = true;
         const uint32_t b_cols = t.bn / (PAIR ? 2 : 1), slices = IS_A ? 2 : (b_cols + 63) / 64;
-        const uint64_t* const skip = p.skip_depth;
         const bool by_group = TURNED ? IS_A : walk.schedule == kRows && !IS_A;
         const bool slab = !DEEP && (IS_A ? t.a_slab : t.b_slab);
         const uint32_t box = IS_A ? t.a_box : t.b_box, stage_bytes = t.stage_bytes;
-        [[maybe_unused]] const uint32_t depth = walk.depth;
+        [[maybe_unused]] const uint32_t beyond = uint32_t(p.depth);
         const uint32_t base = smem_u32(smem) + (IS_A ? 0 : t.a_stage), full = smem_u32(ctl->full), empty = smem_u32(ctl->empty);
         const uint32_t leader_full = PAIR ? cluster_address(full, leader) : full;
         const CUtensorMap* const map = IS_A ? &maps.a : &maps.b;
@@ -800,33 +803,22 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t bytes = (DEEP ? rows * 128 : slices * kSliceBytes) * (PAIR ? 2 : 1);
             const int group = by_group ? int(o.group) : 0;
             uint32_t d = o.d0;
-            [[maybe_unused]] uint64_t skip_next = CUT && skip && o.blocks ? skip[d / 64] : 0;
             for (uint32_t i = 0; i < o.blocks; ++i, d += kDepthTile, ring.advance()) {
-                [[maybe_unused]] const uint64_t skip_now = skip_next;
-                if (CUT && skip && i + 1 < o.blocks) skip_next = skip[d / 64 + 1];
                 if (!(ok = wait(ctl, empty + 8 * ring.s, ring.phase ^ 1))) break;
                 const uint32_t mine = full + 8 * ring.s, bar = leader_full + 8 * ring.s;
                 const uint32_t to = base + ring.s * stage_bytes;
                 if constexpr (CUT) {
                     const uint32_t left = o.depth_end - d;
-                    if (left < kDepthTile || skip_now) {
-                        uint32_t lines = kDepthTile;
-                        uint64_t keep = ~skip_now;
-                        if (left < kDepthTile) {
-                            lines = (left + 15) / 16 * 16;
-                            keep &= ~0ull >> (64 - left);
-                        }
-                        // Depths past the group's end belong to its neighbour, and skipped ones may hold anything: their
+                    if (left < kDepthTile) {
+                        // Depths past the end belong to the group's neighbour, or to nobody, and may hold anything: their
                         // lines are read from beyond the tensor's end, where TMA gives zeros.  (Both operands have
                         // contiguous rows here: a depth is one line of each slice.)
+                        const uint32_t lines = (left + 15) / 16 * 16;
                         if (rank == 0) mbar_expect_tx(mine, slices * 128 * lines * (PAIR ? 2 : 1));
                         const CUtensorMap* const heights = IS_A ? maps.a_lines : maps.b_lines;
-                        for (uint32_t l = 0; l < lines;) {  // runs of kept or cleared lines, in powers of two
-                            const bool kept = keep >> l & 1;
-                            const uint64_t other = (kept ? ~keep : keep) >> l;
-                            const uint32_t run = min(other ? uint32_t(__ffsll(other)) - 1 : 64u, lines - l);
-                            const uint32_t h = min(31u - __clz(run), kHeights - 1);
-                            const int from = int(kept ? d + l : depth);
+                        for (uint32_t l = 0; l < lines;) {  // kept and cleared lines, in powers of two
+                            const uint32_t run = l < left ? left - l : lines - l, h = min(31u - __clz(run), kHeights - 1);
+                            const int from = int(l < left ? d + l : beyond);
                             for (uint32_t r = 0; r < slices; ++r)
                                 tma_load<PAIR>(to + r * kSliceBytes + l * 128, &heights[h], int(row0 + 64 * r), from, 0, bar);
                             l += 1u << h;
@@ -863,7 +855,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
     } else if (warp == 1) {
         if (rank == 0 && elect_one()) {
-            Walk walk(p, t, offsets, first);
+            Walk walk(p, t, offsets, first, live_rows, live_depth);
             Tile o;
             Ring ring{t.stages};
             uint32_t used = 0;  // accumulators
@@ -915,7 +907,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         __syncwarp();
     } else if (STATS) {
-        Walk walk(p, t, offsets, first);
+        Walk walk(p, t, offsets, first, live_rows, live_depth);
         Tile o;
         uint32_t used = 0;
         bool ok = true;
@@ -949,7 +941,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
         }
     } else {
-        Walk walk(p, t, offsets, first);
+        Walk walk(p, t, offsets, first, live_rows, live_depth);
         Tile o;
         uint32_t tiles = 0;
         const uint32_t quarter = warp % 4, half = warp > 6;  // the TMEM lanes that this warp may read, its columns
@@ -1019,7 +1011,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // every block of the cluster joins and finishes its share of the tile, in the order of the splits
         __syncthreads();
         cluster_sync();
-        Walk walk(p, t, offsets, first);
+        Walk walk(p, t, offsets, first, live_rows, live_depth);
         Tile o;
         if (walk.take(o) && o.row0 + rank * kRowsTile < o.row_end) {
             const float alpha = p.st.alpha ? *p.st.alpha : 1.f;
@@ -1107,7 +1099,7 @@ bool aligned16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0;
 
 constexpr uint32_t kSmemMost = 227 * 1024;
 
-bool cut(const Product& p) { return p.schedule == kDepth || p.skip_depth; }  // depths left out, at a group's end or for skipped tokens
+bool cut(const Product& p) { return p.schedule == kDepth || p.live_depth; }  // the depths end where the device says
 uint64_t col_tiles_of(const Product& p, uint32_t bn) {
     return p.schedule == kColumns ? p.n / bn + p.groups : (p.n + bn - 1) / bn;  // grouped: at most
 }
@@ -1156,7 +1148,7 @@ Choice choose(const Product& p, int sms) {
     const uint32_t low = uint32_t(std::min<uint64_t>(kRowsTile, (rows + 7) / 8 * 8));
     const uint32_t unit = p.b.depth_major ? 16 : 64;  // whole slices where rows are contiguous
     const uint32_t widest = uint32_t(std::min<uint64_t>(256, (p.n + unit - 1) / unit * unit));
-    const bool may_split = p.epilogue == kStore && p.schedule == kDense && !p.skip_depth;
+    const bool may_split = p.epilogue == kStore && p.schedule == kDense && !p.live_depth;
     const double column = (p.st.ldo % 8 ? 40.0 : 14.0) * (p.st.z ? 2 : 1);  // epilogue cycles a column
     const double used = p.schedule == kRows || p.schedule == kColumns  // groups that have rows, when these are spread at random
                             ? p.groups * (1 - std::exp(-double(p.schedule == kRows ? p.m : p.n) / p.groups)) : groups;

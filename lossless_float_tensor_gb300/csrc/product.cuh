@@ -72,8 +72,9 @@ struct Product {
     uint32_t schedule, epilogue;
     uint32_t groups;  // 1 for kDense
     const int64_t* offsets;
-    // kDense: bit i of word j set = depth 64 j + i adds nothing, whatever the operands hold there (nullable)
-    const uint64_t* skip_depth;
+    // kDense: how many of the rows, or of the depths, there are, where only the device knows (nullable; m and depth are
+    // the most there may be, and what the operands hold beyond counts for nothing)
+    const uint32_t *live_rows, *live_depth;
     StoreEpilogue st;
     LossEpilogue ls;
     int dtype;
@@ -121,15 +122,34 @@ cudaError_t launch_act_grad(const ActGrad& a, cudaStream_t s);
 // status only, for offsets that do not cut [0, m)
 cudaError_t launch_offset_check(const int64_t* offsets, uint64_t groups, uint64_t m, int32_t* status, cudaStream_t s);
 
-cudaError_t launch_loss_join(const LossEpilogue& e, uint64_t t, uint64_t v, float* loss, float* lse, int32_t* status,
-                             cudaStream_t s);
-// scale[0] = a power of two that brings the largest |dloss| to [2^10, 2^11),
-// scale[1] = its reciprocal; g = scaled dloss, 0 for ignored tokens
-cudaError_t launch_loss_weights(const float* dloss, const int64_t* targets, int64_t ignore, uint64_t t, uint64_t v,
-                                float* scale, float* g, int32_t* status, cudaStream_t s);
-// skip word per 64 tokens: ignored tokens whose h row is not finite
-cudaError_t launch_skip_words(const void* h, uint64_t ldh, const int64_t* targets, int64_t ignore, uint64_t t,
-                              uint64_t d, int dtype, uint64_t* words, cudaStream_t s);
+// The tokens that count, moved together in their order: their h rows, targets
+// and (for the gradient) lse and scaled weights, their number, and where each
+// is from and went.  Ignored tokens get loss and lse 0.
+struct LossRows {
+    const void* h;
+    uint64_t ldh;
+    const int64_t* targets;
+    int64_t ignore;
+    uint64_t t, v, d;
+    int dtype;
+    const float *dloss, *lse;  // nullable: the forward call has none
+    void* out_h;
+    uint64_t ld_out;
+    int64_t* out_targets;
+    float *out_lse, *out_g;
+    // scale[0] = a power of two that brings the largest |dloss| to [2^10, 2^11), scale[1] = its reciprocal
+    float* scale;
+    uint32_t *token, *place, *count;  // compact row -> token, token -> compact row or ~0, rows
+    float *loss, *zero_lse;           // forward: 0 for ignored tokens
+    int32_t* status;
+};
+cudaError_t launch_loss_rows(const LossRows& a, cudaStream_t s);
+// token and count are nullable: the rows are the tokens
+cudaError_t launch_loss_join(const LossEpilogue& e, const uint32_t* token, const uint32_t* count, uint64_t t, uint64_t v,
+                             float* loss, float* lse, int32_t* status, cudaStream_t s);
+// to[i] = from[place[i]], or zeros where place[i] is ~0
+cudaError_t launch_spread_rows(const void* from, uint64_t ld, const uint32_t* place, void* to, uint64_t ld_to, uint64_t rows,
+                               uint64_t cols, cudaStream_t s);
 cudaError_t launch_fill(void* p, uint64_t ld, uint64_t rows, uint64_t cols, uint32_t elem, cudaStream_t s);
 
 // ---- arithmetic ---------------------------------------------------------------

@@ -258,21 +258,51 @@ uzip_status backward(const uzip_linear_grad_args* a, void* ws, uint64_t bytes, i
 
 // ---- cross entropy --------------------------------------------------------------
 
+// Tokens up to one tile of rows are taken as they are: leaving the ignored ones
+// out would save nothing.  More are moved together first, which costs one pass
+// over h (12 us for 4096 x 4096, against 2.3 ms of products) and saves the
+// ignored tokens' share of the products.
+constexpr int64_t kMoveAbove = 128;
+
 struct Loss {
     Product p{};
     PackJobs packs{};
+    LossRows rows{};
+    bool moved;
 };
+
+LossRows plan_rows(const void* h, int64_t ldh, const int64_t* targets, int64_t ignore, int64_t t, int64_t v, int64_t d, int dtype,
+                   Work& w, int32_t* d_status) {
+    LossRows r{};
+    r.h = h, r.ldh = t > 1 ? ldh : round_to(d, 8);
+    r.targets = targets, r.ignore = ignore;
+    r.t = t, r.v = v, r.d = d, r.dtype = dtype, r.status = d_status;
+    r.ld_out = round_to(d, 8);
+    r.out_h = w.take<uint16_t>(t * r.ld_out);
+    r.out_targets = w.take<int64_t>(t);
+    r.token = w.take<uint32_t>(t);
+    r.count = w.take<uint32_t>(1);
+    return r;
+}
 
 Loss plan_loss(const uzip_cross_entropy_args& a, Work& w, int32_t* d_status) {
     Loss f;
     Product& p = f.p;
-    p.a = operand(Matrix{a.h, a.ldh, 0, a.t, a.d, 1}, true, w, &f.packs);
+    f.moved = a.t > kMoveAbove;
+    if (f.moved) {
+        f.rows = plan_rows(a.h, a.ldh, a.targets, a.ignore_index, a.t, a.v, a.d, a.dtype, w, d_status);
+        f.rows.loss = a.loss, f.rows.zero_lse = a.lse;
+        p.a = Operand{f.rows.out_h, f.rows.ld_out, 0, 1};
+        p.live_rows = f.rows.count;
+    } else {
+        p.a = operand(Matrix{a.h, a.ldh, 0, a.t, a.d, 1}, true, w, &f.packs);
+    }
     p.b = operand(Matrix{a.w, a.ldw, 0, a.v, a.d, 1}, true, w, &f.packs);
     p.m = a.t, p.n = a.v, p.depth = a.d;
     p.schedule = kDense, p.groups = 1, p.epilogue = kLossStats;
     p.dtype = a.dtype, p.status = d_status;
     p.ls.tiles = uint32_t((a.v + kStatsCols - 1) / kStatsCols);
-    p.ls.targets = a.targets, p.ls.ignore = a.ignore_index;
+    p.ls.targets = f.moved ? f.rows.out_targets : a.targets, p.ls.ignore = a.ignore_index;
     p.ls.part = w.take<float2>(uint64_t(p.ls.tiles) * a.t);
     p.ls.hit = w.take<float>(a.t);
     return f;
@@ -280,15 +310,15 @@ Loss plan_loss(const uzip_cross_entropy_args& a, Work& w, int32_t* d_status) {
 
 struct LossGradPlan {
     uint64_t piece, pieces, ld_piece;
-    float *scale, *g, *sum;
+    LossRows rows;
+    float* sum;
     uint64_t ld_sum;
-    uint64_t* skip;
     void* dl;
     Operand h_rows, w_rows;
     PackJobs packs;
 };
 
-LossGradPlan plan_loss_grad(const uzip_cross_entropy_grad_args& a, Work& w) {
+LossGradPlan plan_loss_grad(const uzip_cross_entropy_grad_args& a, Work& w, int32_t* d_status) {
     LossGradPlan f{};
     const uint64_t t = a.t, v = a.v;
     uint64_t piece = a.piece;
@@ -298,10 +328,13 @@ LossGradPlan plan_loss_grad(const uzip_cross_entropy_grad_args& a, Work& w) {
     f.piece = piece;
     f.pieces = (v + piece - 1) / piece;
     f.ld_piece = round_to(piece, 8);
-    f.scale = w.take<float>(2);
-    f.g = w.take<float>(t);
-    f.skip = w.take<uint64_t>((t + 63) / 64);
-    f.h_rows = operand(Matrix{a.h, a.ldh, 0, a.t, a.d, 1}, true, w, &f.packs);
+    f.rows = plan_rows(a.h, a.ldh, a.targets, a.ignore_index, a.t, a.v, a.d, a.dtype, w, d_status);
+    f.rows.dloss = a.dloss, f.rows.lse = a.lse;
+    f.rows.out_lse = w.take<float>(t);
+    f.rows.out_g = w.take<float>(t);
+    f.rows.scale = w.take<float>(2);
+    f.rows.place = w.take<uint32_t>(t);
+    f.h_rows = Operand{f.rows.out_h, f.rows.ld_out, 0, 1};
     f.w_rows = operand(Matrix{a.w, a.ldw, 0, a.v, a.d, 1}, true, w, &f.packs);
     f.dl = w.take<uint16_t>(t * f.ld_piece);
     f.ld_sum = round_to(a.d, 4);
@@ -312,10 +345,7 @@ LossGradPlan plan_loss_grad(const uzip_cross_entropy_grad_args& a, Work& w) {
 cudaError_t run_loss_grad(const uzip_cross_entropy_grad_args& a, const LossGradPlan& f, int32_t* d_status,
                           cudaStream_t s) {
     cudaError_t err = launch_pack(f.packs, s);
-    if (err == cudaSuccess)
-        err = launch_loss_weights(a.dloss, a.targets, a.ignore_index, a.t, a.v, f.scale, f.g, d_status, s);
-    if (err == cudaSuccess && a.dw)
-        err = launch_skip_words(f.h_rows.p, f.h_rows.ld, a.targets, a.ignore_index, a.t, a.d, a.dtype, f.skip, s);
+    if (err == cudaSuccess) err = launch_loss_rows(f.rows, s);
     for (uint64_t i = 0; i < f.pieces && err == cudaSuccess; ++i) {
         const uint64_t col0 = i * f.piece, cols = std::min<uint64_t>(f.piece, a.v - col0);
         Operand w_rows = f.w_rows;
@@ -324,26 +354,11 @@ cudaError_t run_loss_grad(const uzip_cross_entropy_grad_args& a, const LossGradP
         p.dtype = a.dtype, p.status = d_status, p.groups = 1;
         p.a = f.h_rows, p.b = w_rows;
         p.m = a.t, p.n = cols, p.depth = a.d;
+        p.live_rows = f.rows.count;
         p.epilogue = kLossGrad;
-        p.ls.targets = a.targets, p.ls.ignore = a.ignore_index, p.ls.col0 = col0;
-        p.ls.lse = a.lse, p.ls.g = f.g, p.ls.out = f.dl, p.ls.ldo = f.ld_piece;
+        p.ls.targets = f.rows.out_targets, p.ls.ignore = a.ignore_index, p.ls.col0 = col0;
+        p.ls.lse = f.rows.out_lse, p.ls.g = f.rows.out_g, p.ls.out = f.dl, p.ls.ldo = f.ld_piece;
         err = launch_product(p, sm_count(), s);
-        if (err == cudaSuccess && a.dh) {
-            Product q{};
-            q.dtype = a.dtype, q.status = d_status, q.groups = 1;
-            q.a = Operand{f.dl, f.ld_piece, 0, 1};
-            q.b = w_rows;
-            q.b.depth_major = 0;
-            q.m = a.t, q.n = a.d, q.depth = cols;
-            q.st.sum_in = i ? f.sum : nullptr, q.st.ld_sum = f.ld_sum;
-            if (i + 1 < f.pieces) {
-                q.st.out = f.sum, q.st.ldo = f.ld_sum, q.st.out_fp32 = 1;
-            } else {
-                q.st.out = a.dh, q.st.ldo = a.t > 1 ? a.lddh : a.d;
-            }
-            q.st.alpha = f.scale + 1;
-            err = launch_product(q, sm_count(), s);
-        }
         if (err == cudaSuccess && a.dw) {
             Product q{};
             q.dtype = a.dtype, q.status = d_status, q.groups = 1;
@@ -351,13 +366,32 @@ cudaError_t run_loss_grad(const uzip_cross_entropy_grad_args& a, const LossGradP
             q.b = f.h_rows;
             q.b.depth_major = 0;
             q.m = cols, q.n = a.d, q.depth = a.t;
-            q.skip_depth = f.skip;
+            q.live_depth = f.rows.count;
             const uint64_t ldo = a.v > 1 ? a.lddw : a.d;
             q.st.out = static_cast<uint16_t*>(a.dw) + col0 * ldo, q.st.ldo = ldo;
-            q.st.alpha = f.scale + 1;
+            q.st.alpha = f.rows.scale + 1;
+            err = launch_product(q, sm_count(), s);
+        }
+        if (err == cudaSuccess && a.dh) {
+            Product q{};
+            q.dtype = a.dtype, q.status = d_status, q.groups = 1;
+            q.a = Operand{f.dl, f.ld_piece, 0, 1};
+            q.b = w_rows;
+            q.b.depth_major = 0;
+            q.m = a.t, q.n = a.d, q.depth = cols;
+            q.live_rows = f.rows.count;
+            q.st.sum_in = i ? f.sum : nullptr, q.st.ld_sum = f.ld_sum;
+            if (i + 1 < f.pieces) {
+                q.st.out = f.sum, q.st.ldo = f.ld_sum, q.st.out_fp32 = 1;
+            } else {
+                q.st.out = f.rows.out_h, q.st.ldo = f.rows.ld_out;  // h has been read for the last time
+            }
+            q.st.alpha = f.rows.scale + 1;
             err = launch_product(q, sm_count(), s);
         }
     }
+    if (err == cudaSuccess && a.dh)
+        err = launch_spread_rows(f.rows.out_h, f.rows.ld_out, f.rows.place, a.dh, a.t > 1 ? a.lddh : a.d, a.t, a.d, s);
     return err;
 }
 
@@ -448,8 +482,11 @@ uzip_status uzip_cross_entropy(const uzip_cross_entropy_args* a, void* d_workspa
     Work work{static_cast<uint8_t*>(d_workspace)};
     const Loss f = plan_loss(*a, work, d_status);
     err = launch_pack(f.packs, s);
+    if (err == cudaSuccess && f.moved) err = launch_loss_rows(f.rows, s);
     if (err == cudaSuccess) err = launch_product(f.p, sm_count(), s);
-    if (err == cudaSuccess) err = launch_loss_join(f.p.ls, a->t, a->v, a->loss, a->lse, d_status, s);
+    if (err == cudaSuccess)
+        err = launch_loss_join(f.p.ls, f.moved ? f.rows.token : nullptr, f.moved ? f.rows.count : nullptr, a->t, a->v, a->loss,
+                               a->lse, d_status, s);
     return finish(err);
 }
 
@@ -458,7 +495,7 @@ uint64_t uzip_cross_entropy_backward_workspace_size(const uzip_cross_entropy_gra
         !length_ok(a->d) || a->piece < 0)
         return 0;
     Work w{nullptr};
-    plan_loss_grad(*a, w);
+    plan_loss_grad(*a, w, nullptr);
     return w.used;
 }
 
@@ -473,7 +510,7 @@ uzip_status uzip_cross_entropy_backward(const uzip_cross_entropy_grad_args* a, v
         !floats_ok(a->lse, a->t) || !floats_ok(a->dloss, a->t))
         return UZIP_ERR_INVALID_ARG;
     Work need{nullptr};
-    if (a->t) plan_loss_grad(*a, need);
+    if (a->t) plan_loss_grad(*a, need, nullptr);
     if ((st = check_work(need, d_workspace, workspace_bytes, d_status)) != UZIP_OK) return st;
     cudaError_t err = cudaSuccess;
     if (d_status) err = cudaMemsetAsync(d_status, 0, sizeof(int32_t), s);
@@ -483,7 +520,7 @@ uzip_status uzip_cross_entropy_backward(const uzip_cross_entropy_grad_args* a, v
         return finish(err);
     }
     Work work{static_cast<uint8_t*>(d_workspace)};
-    const LossGradPlan f = plan_loss_grad(*a, work);
+    const LossGradPlan f = plan_loss_grad(*a, work, d_status);
     return finish(run_loss_grad(*a, f, d_status, s));
 }
 

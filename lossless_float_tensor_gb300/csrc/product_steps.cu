@@ -188,10 +188,12 @@ __device__ __forceinline__ float2 join(float2 a, float2 b) {
 // One block for each row joins its tiles' pairs: thread i takes tiles i,
 // i + 128, ..., then pairs of threads meet, always in the same order.
 constexpr uint32_t kJoinThreads = 128;
-__global__ void __launch_bounds__(kJoinThreads) loss_join_kernel(LossEpilogue e, uint64_t v, uint32_t tiles, float* loss,
-                                                                 float* lse, int32_t* status) {
+__global__ void __launch_bounds__(kJoinThreads) loss_join_kernel(LossEpilogue e, const uint32_t* token, const uint32_t* count,
+                                                                 uint64_t v, uint32_t tiles, float* loss, float* lse,
+                                                                 int32_t* status) {
     __shared__ float2 s[kJoinThreads / 32];
     const uint64_t row = blockIdx.x;
+    if (count && row >= *count) return;
     const float2* part = e.part + row * tiles;
     float2 q = make_float2(-INFINITY, 0.f);
     for (uint32_t i = threadIdx.x; i < tiles; i += kJoinThreads) q = join(q, part[i]);
@@ -203,79 +205,123 @@ __global__ void __launch_bounds__(kJoinThreads) loss_join_kernel(LossEpilogue e,
     if (threadIdx.x) return;
     q = join(join(s[0], s[1]), join(s[2], s[3]));
     const int64_t target = e.targets[row];
+    const uint64_t to = token ? token[row] : row;
     if (target == e.ignore) {
-        loss[row] = 0.f;
-        lse[row] = 0.f;
+        loss[to] = 0.f;
+        lse[to] = 0.f;
         return;
     }
     const float l = q.x + logf(q.y);
-    lse[row] = l;
+    lse[to] = l;
     if (target < 0 || target >= int64_t(v)) {
-        loss[row] = NAN;
+        loss[to] = NAN;
         if (status) atomicCAS(status, 0, int(UZIP_ERR_INVALID_ARG));
         return;
     }
-    loss[row] = l - e.hit[row];
+    loss[to] = l - e.hit[row];
 }
 
-// One block: the largest finite weight, then its power of two.
-__global__ void __launch_bounds__(1024) loss_weights_kernel(const float* dloss, const int64_t* targets, int64_t ignore,
-                                                            uint64_t t, uint64_t v, float* scale, float* g,
-                                                            int32_t* status) {
+// Every block counts through all targets (they are few beside the rows), a
+// thousand at a time, and copies the rows i with i % gridDim.x == blockIdx.x: the
+// places come out the same in each, without a launch in between.
+constexpr uint32_t kPickThreads = 1024, kPickList = 2048;
+__global__ void __launch_bounds__(kPickThreads) loss_rows_kernel(const __grid_constant__ LossRows a) {
+    __shared__ uint32_t list[kPickList][2];  // token, place
+    __shared__ uint32_t listed, before[32];
     __shared__ float tops[32];
-    float top = 0.f;
-    for (uint64_t i = threadIdx.x; i < t; i += 1024)
-        if (targets[i] != ignore && fabsf(dloss[i]) < INFINITY) top = fmaxf(top, fabsf(dloss[i]));
-#pragma unroll
-    for (uint32_t o = 16; o; o /= 2) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-    if (threadIdx.x % 32 == 0) tops[threadIdx.x / 32] = top;
-    __syncthreads();
-    top = tops[threadIdx.x % 32];
-#pragma unroll
-    for (uint32_t o = 16; o; o /= 2) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-    int power = top > 0.f ? 10 - ilogbf(top) : 0;
-    power = max(-110, min(110, power));
-    const float up = exp2f(float(power));
-    if (threadIdx.x == 0) {
-        scale[0] = up;
-        scale[1] = exp2f(float(-power));
-    }
-    for (uint64_t i = threadIdx.x; i < t; i += 1024) {
-        const int64_t target = targets[i];
-        float w = target == ignore ? 0.f : dloss[i] * up;
-        if (target != ignore && (target < 0 || target >= int64_t(v))) {
-            w = NAN;
-            if (status) atomicCAS(status, 0, int(UZIP_ERR_INVALID_ARG));
+    const uint32_t lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+    if (threadIdx.x == 0) listed = 0;
+    float up = 1.f;
+    if (a.dloss) {
+        float top = 0.f;
+        for (uint64_t i = threadIdx.x; i < a.t; i += kPickThreads) {
+            const float w = fabsf(a.dloss[i]);
+            if (a.targets[i] != a.ignore && w < INFINITY) top = fmaxf(top, w);
         }
-        g[i] = w;
+#pragma unroll
+        for (uint32_t o = 16; o; o /= 2) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+        if (lane == 0) tops[warp] = top;
+        __syncthreads();
+        top = tops[lane];
+#pragma unroll
+        for (uint32_t o = 16; o; o /= 2) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+        const int power = max(-110, min(110, top > 0.f ? 10 - ilogbf(top) : 0));
+        up = exp2f(float(power));
+        if (blockIdx.x == 0 && threadIdx.x == 0) {
+            a.scale[0] = up;
+            a.scale[1] = exp2f(float(-power));
+        }
     }
+    uint32_t base = 0;
+    for (uint64_t start = 0; start < a.t; start += kPickThreads) {
+        const uint64_t i = start + threadIdx.x;
+        const bool mine = i < a.t && i % gridDim.x == blockIdx.x;
+        const int64_t target = i < a.t ? a.targets[i] : a.ignore;
+        const bool used = target != a.ignore;
+        const uint32_t votes = __ballot_sync(0xFFFFFFFFu, used);
+        __syncthreads();  // the counts of the last round, and the list, are read
+        if (lane == 0) before[warp] = __popc(votes);
+        __syncthreads();
+        uint32_t sum = before[lane];
+#pragma unroll
+        for (uint32_t o = 1; o < 32; o *= 2) {
+            const uint32_t v = __shfl_up_sync(0xFFFFFFFFu, sum, o);
+            if (lane >= o) sum += v;
+        }
+        const uint32_t mine_before = warp ? __shfl_sync(0xFFFFFFFFu, sum, warp - 1) : 0;
+        const uint32_t place = base + mine_before + __popc(votes & lanemask_lt());
+        base += __shfl_sync(0xFFFFFFFFu, sum, 31);
+        if (mine && used) {
+            const uint32_t k = atomicAdd(&listed, 1);
+            list[k][0] = uint32_t(i), list[k][1] = place;
+            a.out_targets[place] = target;
+            a.token[place] = uint32_t(i);
+            if (a.dloss) {
+                const bool bad = target < 0 || target >= int64_t(a.v);
+                if (bad && a.status) atomicCAS(a.status, 0, int(UZIP_ERR_INVALID_ARG));
+                a.out_g[place] = bad ? NAN : a.dloss[i] * up;
+                a.out_lse[place] = a.lse[i];
+            }
+        }
+        if (mine) {
+            if (a.place) a.place[i] = used ? place : ~0u;
+            if (a.loss && !used) a.loss[i] = 0.f, a.zero_lse[i] = 0.f;
+        }
+        __syncthreads();
+        if (listed + kPickThreads <= kPickList && start + kPickThreads < a.t) continue;
+        // the rows' pieces in one run of the whole block: 16 bytes, or one value where rows start anywhere
+        const bool vec = a.ldh % 8 == 0 && a.d % 8 == 0 && reinterpret_cast<uintptr_t>(a.h) % 16 == 0;
+        const uint32_t pieces = uint32_t(vec ? a.d / 8 : a.d);
+        const uint64_t all = uint64_t(listed) * pieces;
+#pragma unroll 4
+        for (uint64_t k = threadIdx.x; k < all; k += kPickThreads) {
+            const uint32_t r = uint32_t(k / pieces), c = uint32_t(k - uint64_t(r) * pieces);
+            const uint16_t* from = static_cast<const uint16_t*>(a.h) + list[r][0] * a.ldh;
+            uint16_t* to = static_cast<uint16_t*>(a.out_h) + list[r][1] * a.ld_out;
+            if (vec) reinterpret_cast<uint4*>(to)[c] = reinterpret_cast<const uint4*>(from)[c];
+            else to[c] = from[c];
+        }
+        __syncthreads();
+        if (threadIdx.x == 0) listed = 0;
+    }
+    if (blockIdx.x == 0 && threadIdx.x == 0) *a.count = base;
 }
 
-// A warp for each token, a block for each byte of a word; only ignored rows
-// are read.  Rows start on 16-byte boundaries (the products need that too).
-__global__ void __launch_bounds__(kThreads) skip_words_kernel(const uint16_t* h, uint64_t ldh, const int64_t* targets,
-                                                              int64_t ignore, uint64_t t, uint64_t d, int dtype,
-                                                              uint8_t* bytes) {
-    __shared__ uint32_t odd_rows;
-    if (threadIdx.x == 0) odd_rows = 0;
-    __syncthreads();
-    const uint32_t lane = threadIdx.x % 32, warp = threadIdx.x / 32;
-    const uint64_t row = uint64_t(blockIdx.x) * 8 + warp;
-    if (row < t && targets[row] == ignore) {
-        const uint32_t infinite = dtype == UZIP_BF16 ? 0x7F80 : 0x7C00;
-        const uint16_t* p = h + row * ldh;
-        bool odd = false;
+// A warp for each row.
+__global__ void __launch_bounds__(kThreads) spread_rows_kernel(const uint16_t* from, uint64_t ld, const uint32_t* place,
+                                                               uint16_t* to, uint64_t ld_to, uint64_t rows, uint64_t cols, bool vec) {
+    const uint32_t lane = threadIdx.x % 32;
+    for (uint64_t r = blockIdx.x * uint64_t(kThreads / 32) + threadIdx.x / 32; r < rows; r += uint64_t(gridDim.x) * (kThreads / 32)) {
+        const uint32_t at = place[r];
+        const uint16_t* src = from + uint64_t(at) * ld;
+        uint16_t* dst = to + r * ld_to;
+        const uint64_t whole = vec ? cols / 8 : 0;
 #pragma unroll 4
-        for (uint64_t c = lane; c < d / 8; c += 32) {
-            const uint4 q = reinterpret_cast<const uint4*>(p)[c];
-            for (uint32_t w : {q.x, q.y, q.z, q.w})
-                odd |= (w & infinite) == infinite || (w >> 16 & infinite) == infinite;
-        }
-        if (lane < d % 8) odd |= (p[d / 8 * 8 + lane] & infinite) == infinite;
-        if (__any_sync(0xFFFFFFFFu, odd) && lane == 0) atomicOr(&odd_rows, 1u << warp);
+        for (uint64_t c = lane; c < whole; c += 32)
+            reinterpret_cast<uint4*>(dst)[c] = at == ~0u ? make_uint4(0, 0, 0, 0) : reinterpret_cast<const uint4*>(src)[c];
+#pragma unroll 4
+        for (uint64_t c = 8 * whole + lane; c < cols; c += 32) dst[c] = at == ~0u ? uint16_t(0) : src[c];
     }
-    __syncthreads();
-    if (threadIdx.x == 0) bytes[blockIdx.x] = uint8_t(odd_rows);
 }
 
 }  // namespace
@@ -330,23 +376,23 @@ cudaError_t launch_offset_check(const int64_t* offsets, uint64_t groups, uint64_
     return cudaGetLastError();
 }
 
-cudaError_t launch_loss_join(const LossEpilogue& e, uint64_t t, uint64_t v, float* loss, float* lse, int32_t* status,
-                             cudaStream_t s) {
-    loss_join_kernel<<<uint32_t(t), kJoinThreads, 0, s>>>(e, v, e.tiles, loss, lse, status);
+cudaError_t launch_loss_join(const LossEpilogue& e, const uint32_t* token, const uint32_t* count, uint64_t t, uint64_t v,
+                             float* loss, float* lse, int32_t* status, cudaStream_t s) {
+    loss_join_kernel<<<uint32_t(t), kJoinThreads, 0, s>>>(e, token, count, v, e.tiles, loss, lse, status);
     return cudaGetLastError();
 }
 
-cudaError_t launch_loss_weights(const float* dloss, const int64_t* targets, int64_t ignore, uint64_t t, uint64_t v,
-                                float* scale, float* g, int32_t* status, cudaStream_t s) {
-    loss_weights_kernel<<<1, 1024, 0, s>>>(dloss, targets, ignore, t, v, scale, g, status);
+cudaError_t launch_loss_rows(const LossRows& a, cudaStream_t s) {
+    loss_rows_kernel<<<uint32_t(std::min<uint64_t>(a.t, 304)), kPickThreads, 0, s>>>(a);
     return cudaGetLastError();
 }
 
-cudaError_t launch_skip_words(const void* h, uint64_t ldh, const int64_t* targets, int64_t ignore, uint64_t t,
-                              uint64_t d, int dtype, uint64_t* words, cudaStream_t s) {
-    static_assert(kThreads / 32 == 8, "a warp for each bit of a byte");
-    skip_words_kernel<<<uint32_t((t + 63) / 64 * 8), kThreads, 0, s>>>(static_cast<const uint16_t*>(h), ldh, targets, ignore,
-                                                                       t, d, dtype, reinterpret_cast<uint8_t*>(words));
+cudaError_t launch_spread_rows(const void* from, uint64_t ld, const uint32_t* place, void* to, uint64_t ld_to, uint64_t rows,
+                               uint64_t cols, cudaStream_t s) {
+    if (rows == 0 || cols == 0) return cudaSuccess;
+    const bool vec = ld_to % 8 == 0 && reinterpret_cast<uintptr_t>(to) % 16 == 0;
+    spread_rows_kernel<<<uint32_t(std::min<uint64_t>((rows + 7) / 8, 152 * 8)), kThreads, 0, s>>>(
+        static_cast<const uint16_t*>(from), ld, place, static_cast<uint16_t*>(to), ld_to, rows, cols, vec);
     return cudaGetLastError();
 }
 
