@@ -493,10 +493,68 @@ struct Patch {
     }
 };
 
+// The product of row `row` of A and column `col` of B (of group g) once more,
+// by one warp in rounded 32-bit additions.  Both operands lie along the depth,
+// their rows on 16-byte boundaries.
+__device__ __noinline__ float dot_again(const Product& p, uint32_t ga, uint32_t gb, uint64_t row, uint64_t col, uint32_t lane) {
+    const uint16_t* a = static_cast<const uint16_t*>(p.a.p) + ga * p.a.group + row * p.a.ld;
+    const uint16_t* b = static_cast<const uint16_t*>(p.b.p) + gb * p.b.group + col * p.b.ld;
+    float sum = 0.f;
+#pragma unroll 4
+    for (uint64_t i = 8 * lane; i + 8 <= p.depth; i += 256) {
+        float x[8], y[8];
+        read8(a, i, true, 8, p.dtype, x);
+        read8(b, i, true, 8, p.dtype, y);
+#pragma unroll
+        for (uint32_t j = 0; j < 8; ++j) sum = fmaf(x[j], y[j], sum);
+    }
+    const uint64_t rest = p.depth / 8 * 8 + lane;
+    if (rest < p.depth) sum = fmaf(from16(a[rest], p.dtype), from16(b[rest], p.dtype), sum);
+#pragma unroll
+    for (uint32_t o = 16; o; o /= 2) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+    return sum;
+}
+
+// A step in the slope, as relu's, turns a value's error into a wrong gradient
+// where the error passes zero.  The tensor core's additions cut toward zero,
+// so a sum of k products is off by about k 2^-30 of its neighbours' mean
+// size, ten times what rounded additions would leave: of 4096 x 4096 values
+// at 4096 depths 15 changed their sign, and 8 million at 14336 depths 26.
+// Where a value to be kept for the gradient is nearer to zero than twice that
+// (one in a million at 512 depths), it is summed again; 2 are left, as many
+// as rounded 32-bit sums give.  v[i] are the lane's 32 values,
+// `count` of them real; at most eight of a patch, so that no input can make
+// this the kernel's work.
+template <typename Again>
+__device__ __forceinline__ void mend_near_zero(const Product& p, float v[32], uint32_t count, bool live, uint32_t lane, Again again) {
+    float mean = 0.f;
+#pragma unroll
+    for (uint32_t i = 0; i < 32; ++i) mean += fabsf(v[i]);
+    const float near = mean * (1.f / 32) * float(p.depth) * 0x1p-29f;
+    uint32_t close = 0;
+#pragma unroll
+    for (uint32_t i = 0; i < 32; ++i)
+        if (fabsf(v[i]) < near && v[i] != 0.f) close |= 1u << i;
+    if (!live) close = 0;
+    if (count < 32) close &= (1u << count) - 1;
+    uint32_t lanes = __ballot_sync(0xFFFFFFFFu, close);
+    for (uint32_t left = 8; lanes && left; --left) {
+        const uint32_t from = __ffs(lanes) - 1, at = __ffs(__shfl_sync(0xFFFFFFFFu, close, from)) - 1;
+        const float sum = again(from, at);
+        if (lane == from) {
+            close &= close - 1;
+#pragma unroll
+            for (uint32_t i = 0; i < 32; ++i)
+                if (i == at) v[i] = sum;
+        }
+        lanes = __ballot_sync(0xFFFFFFFFu, close);
+    }
+}
+
 // An accumulator of the transposed product: lanes are output columns (features)
 // and accumulator columns are output rows (tokens), so a patch is written a
 // token a step, 32 neighbouring features at once.
-template <typename Release>
+template <bool FORWARD, typename Release>
 __device__ __forceinline__ void finish_transposed(const Product& p, const Tiling& t, const Tile& o, uint32_t acc, uint32_t warp_row,
                                                   uint32_t half, const Patch& patch, Release release) {
     const uint32_t lane = patch.lane, feature0 = o.row0 + warp_row;
@@ -522,6 +580,11 @@ __device__ __forceinline__ void finish_transposed(const Product& p, const Tiling
         if (c + 2 * kPatchCols >= o.cols) release();
 #pragma unroll
         for (uint32_t i = 0; i < 32; ++i) v[i] += bias;
+        if (FORWARD && z && e.act == UZIP_ACT_RELU)
+            mend_near_zero(p, v, tokens, lane < features, lane, [&](uint32_t from, uint32_t at) {
+                const float b = __shfl_sync(0xFFFFFFFFu, bias, from);
+                return dot_again(p, o.group, 0, feature0 + from, o.col0 + c + at, lane) + b;
+            });
         if (z) {
             __syncwarp();
 #pragma unroll
@@ -579,7 +642,7 @@ __device__ __forceinline__ void finish_stats(const Product& p, const Tile& o, ui
 // columns' bias.  `release` gives the accumulator back once the warp has read
 // its last column.  The loops over patches stay rolled: the code of one patch
 // fits the instruction cache, four of them did not.
-template <int EPI, typename Release>
+template <int EPI, bool FORWARD, typename Release>
 __device__ __forceinline__ void finish_tile(const Product& p, const Tiling& t, const Tile& o, uint32_t acc, uint32_t warp_row,
                                             uint32_t half, float alpha, const Patch& patch, const float* bias, uint4 ahead[4],
                                             Release release) {
@@ -644,6 +707,11 @@ __device__ __forceinline__ void finish_tile(const Product& p, const Tiling& t, c
                     v[i] += f.x, v[i + 1] += f.y, v[i + 2] += f.z, v[i + 3] += f.w;
                 }
             }
+            if (FORWARD && z && act == UZIP_ACT_RELU)
+                mend_near_zero(p, v, here, live, lane, [&](uint32_t from, uint32_t at) {
+                    const float b = has_bias ? bias[c / 2 - half * (kPatchCols / 2) + at] : 0.f;
+                    return dot_again(p, 0, o.group, row0 + from, uint64_t(o.col0) + c + at, lane) + b;
+                });
             if (z) {
                 __syncwarp();
 #pragma unroll
@@ -983,9 +1051,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             };
             if constexpr (TURNED) {
-                finish_transposed(p, t, o, acc, quarter * 32, half, patch, release);
+                finish_transposed<LAYOUT == 4>(p, t, o, acc, quarter * 32, half, patch, release);
             } else if constexpr (!SPLIT) {
-                finish_tile<EPI>(p, t, o, acc, quarter * 32, half, alpha, patch, bias, ahead, release);
+                finish_tile<EPI, LAYOUT == 0>(p, t, o, acc, quarter * 32, half, alpha, patch, bias, ahead, release);
             } else {
                 const uint32_t lane_row = quarter * 32 + lane, row0 = o.row0 + rank * kRowsTile;
                 // partial sums to shared memory, rows bn + 4 floats apart (no bank conflicts for 16-byte access)
@@ -1148,7 +1216,8 @@ Choice choose(const Product& p, int sms) {
     const uint32_t low = uint32_t(std::min<uint64_t>(kRowsTile, (rows + 7) / 8 * 8));
     const uint32_t unit = p.b.depth_major ? 16 : 64;  // whole slices where rows are contiguous
     const uint32_t widest = uint32_t(std::min<uint64_t>(256, (p.n + unit - 1) / unit * unit));
-    const bool may_split = p.epilogue == kStore && p.schedule == kDense && !p.live_depth;
+    // (values near zero that are kept for relu's gradient are summed again where one block holds a tile's whole depth)
+    const bool may_split = p.epilogue == kStore && p.schedule == kDense && !p.live_depth && !(p.st.z && p.st.act == UZIP_ACT_RELU);
     const double column = (p.st.ldo % 8 ? 40.0 : 14.0) * (p.st.z ? 2 : 1);  // epilogue cycles a column
     const double used = p.schedule == kRows || p.schedule == kColumns  // groups that have rows, when these are spread at random
                             ? p.groups * (1 - std::exp(-double(p.schedule == kRows ? p.m : p.n) / p.groups)) : groups;

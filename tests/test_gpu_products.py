@@ -123,6 +123,24 @@ def test_linear_bounds(uz, m, k, n, dtype, act):
         _ok(got, pair)
 
 
+def test_signs_kept_for_relu(uz):
+    """relu's slope is a step, so a value kept for its gradient has to have its
+    sign: tensor-core sums of 4096 products get about 15 of 16 million signs
+    wrong (of values below 1e-5), 32-bit sums about 4.  Over three draws at
+    most as many as twice the latter may be, by the dense and by the grouped
+    product."""
+    wrong = [0, 0]
+    for seed in range(3):
+        g = _gen(40 + seed)
+        x, w, b = _rand(g, (4096, 4096), torch.float16), _rand(g, (4096, 4096), torch.float16, 1 / 64), _rand(g, (4096,), torch.float16, 0.5)
+        sign = x.double() @ w.double().T + b.double() > 0
+        off = torch.tensor([0, 1000, 4096], device="cuda")
+        wrong[0] += int(((uz.linear(x, w, b, activation="relu", save_preact=True)[1] > 0) != sign).sum())
+        z = uz.grouped_linear(x, torch.stack([w, w]), off, torch.stack([b, b]), activation="relu", save_preact=True)[1]
+        wrong[1] += int(((z > 0) != sign).sum())
+    assert max(wrong) <= 24
+
+
 @pytest.mark.parametrize("dtype", DTYPES)
 def test_linear_strided_views_and_odd_addresses(uz, dtype):
     g = _gen(5)
