@@ -137,8 +137,7 @@ struct LossRows {
     uint64_t ld_out;
     int64_t* out_targets;
     float *out_lse, *out_g;
-    // scale[0] = a power of two that brings the largest |dloss| to [2^10, 2^11), scale[1] = its reciprocal
-    float* scale;
+    float* scale;  // what undoes the weights' scale, which brings the largest |dloss| to 2^10
     uint32_t *token, *place, *count;  // compact row -> token, token -> compact row or ~0, rows
     float *loss, *zero_lse;           // forward: 0 for ignored tokens
     int32_t* status;

@@ -332,7 +332,7 @@ LossGradPlan plan_loss_grad(const uzip_cross_entropy_grad_args& a, Work& w, int3
     f.rows.dloss = a.dloss, f.rows.lse = a.lse;
     f.rows.out_lse = w.take<float>(t);
     f.rows.out_g = w.take<float>(t);
-    f.rows.scale = w.take<float>(2);
+    f.rows.scale = w.take<float>(1);
     f.rows.place = w.take<uint32_t>(t);
     f.h_rows = Operand{f.rows.out_h, f.rows.ld_out, 0, 1};
     f.w_rows = operand(Matrix{a.w, a.ldw, 0, a.v, a.d, 1}, true, w, &f.packs);
@@ -369,7 +369,7 @@ cudaError_t run_loss_grad(const uzip_cross_entropy_grad_args& a, const LossGradP
             q.live_depth = f.rows.count;
             const uint64_t ldo = a.v > 1 ? a.lddw : a.d;
             q.st.out = static_cast<uint16_t*>(a.dw) + col0 * ldo, q.st.ldo = ldo;
-            q.st.alpha = f.rows.scale + 1;
+            q.st.alpha = f.rows.scale;
             err = launch_product(q, sm_count(), s);
         }
         if (err == cudaSuccess && a.dh) {
@@ -386,7 +386,7 @@ cudaError_t run_loss_grad(const uzip_cross_entropy_grad_args& a, const LossGradP
             } else {
                 q.st.out = f.rows.out_h, q.st.ldo = f.rows.ld_out;  // h has been read for the last time
             }
-            q.st.alpha = f.rows.scale + 1;
+            q.st.alpha = f.rows.scale;
             err = launch_product(q, sm_count(), s);
         }
     }

@@ -245,12 +245,10 @@ __global__ void __launch_bounds__(kPickThreads) loss_rows_kernel(const __grid_co
         top = tops[lane];
 #pragma unroll
         for (uint32_t o = 16; o; o /= 2) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-        const int power = max(-110, min(110, top > 0.f ? 10 - ilogbf(top) : 0));
-        up = exp2f(float(power));
-        if (blockIdx.x == 0 && threadIdx.x == 0) {
-            a.scale[0] = up;
-            a.scale[1] = exp2f(float(-power));
-        }
+        // The largest weight becomes 2^10.  Not merely something between 2^10 and 2^11: equal weights, as in a mean, then
+        // all round alike, and a target's g (p - 1), nearly g, would carry one rounding error through the whole gradient.
+        up = top > 0.f ? fminf(1024.f / top, 0x1p120f) : 1.f;
+        if (blockIdx.x == 0 && threadIdx.x == 0) *a.scale = 1.f / up;
     }
     uint32_t base = 0;
     for (uint64_t start = 0; start < a.t; start += kPickThreads) {

@@ -334,6 +334,22 @@ def test_cross_entropy_gradient_at_any_scale(uz, scale):
         _ok(a, pair)
 
 
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_cross_entropy_gradient_of_a_mean(uz, dtype):
+    """Equal weights that are no power of two: a target's gradient is nearly the
+    weight itself, so its rounding is the same for all tokens and does not
+    average out.  The results' own rounding is u / sqrt(3) of their size or
+    less; the whole error has to stay below twice that."""
+    g = _gen(28)
+    h, w = _rand(g, (600, 256), dtype), _rand(g, (20000, 256), dtype, 1 / 16)
+    targets = torch.randint(0, 20000, (600,), generator=g, device="cuda")
+    for weight in (1 / 600, 0.7, 1.3):
+        dloss = torch.full((600,), weight * (512 if dtype == torch.float16 else 1), device="cuda")
+        _, lse = uz.cross_entropy(h, w, targets)
+        for a, (want, _) in zip(uz.cross_entropy_backward(dloss, h, w, targets, lse), ref.loss_grad64(h, w, targets, dloss)):
+            assert float((a.double() - want).norm() / want.norm()) <= 2 * ref.ROUND[dtype] / 3 ** 0.5
+
+
 def test_cross_entropy_ignored_rows_may_hold_anything(uz):
     h, w, targets, dloss = _loss_inputs(200, 900, 136, torch.bfloat16, 22)
     drop = targets == -100
