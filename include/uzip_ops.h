@@ -83,7 +83,9 @@ uzip_status uzip_grouped_linear(const uzip_linear_args* a, void* d_workspace, ui
  * over its own rows; zero for one without rows), db = column sums of dz.  The
  * residual's gradient is dy itself.  Each of dx, dw, db may be NULL.  dz is
  * rounded to the dtype for the two products (tensor cores take 16-bit
- * operands); db sums it unrounded. */
+ * operands); db sums it unrounded.  z is what uzip_linear stored: values that
+ * relu's slope turns on were summed again there where the tensor core's sum
+ * came within its own error of zero. */
 typedef struct {
     int32_t dtype;
     int32_t act;
@@ -137,9 +139,11 @@ uzip_status uzip_cross_entropy(const uzip_cross_entropy_args* a, void* d_workspa
 
 /* Gradients for the upstream gradient dloss of each token's loss:
  *   dh_i = dloss_i (sum_j p_ij w_j - w_{t_i}),  dw_j = sum_i dloss_i (p_ij - [j = t_i]) h_i.
- * The vocabulary is taken `piece` classes at a time: their logits are computed
- * again and p - [j = t] is rounded to the dtype in the workspace (t x piece
- * values).  piece 0 takes the default: as many classes as 512 MiB hold, at most
+ * The tokens that are not ignored are moved together in the workspace (t x d
+ * values), so that ignored ones cost nothing.  The vocabulary is taken `piece`
+ * classes at a time: their logits are computed again and dloss (p - [j = t]),
+ * scaled so that the largest dloss is 2^10, is rounded to the dtype in the
+ * workspace (t x piece values); dh is summed over the pieces in fp32.  piece 0 takes the default: as many classes as 512 MiB hold, at most
  * 32768. */
 typedef struct {
     int32_t dtype;
