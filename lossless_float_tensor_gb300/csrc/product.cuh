@@ -190,8 +190,8 @@ __device__ __forceinline__ float fast_reciprocal(float v) {
 // 1 - Phi(|z|) exp(z^2 / 2) by the rational approximation 7.1.26 of Abramowitz
 // and Stegun, Handbook of Mathematical Functions: erfc(x) = (a1 t + ... + a5
 // t^5) exp(-x^2), t = 1 / (1 + 0.3275911 x), off by less than 1.5e-7 (a unit
-// in the last place of a value near one).  Its 14 instructions a value, the
-// exponential included, are a third of erff's.
+// in the last place of a value near one), in 14 instructions a value with the
+// exponential.
 __device__ __forceinline__ float gauss_tail(float a) {
     const float t = fast_reciprocal(fmaf(0.3275911f * kSqrtHalf, a, 1.f));
     float s = fmaf(0.5f * 1.061405429f, t, 0.5f * -1.453152027f);

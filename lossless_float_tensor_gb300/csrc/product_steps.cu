@@ -287,17 +287,20 @@ __global__ void __launch_bounds__(kPickThreads) loss_rows_kernel(const __grid_co
         }
         __syncthreads();
         if (listed + kPickThreads <= kPickList && start + kPickThreads < a.t) continue;
-        // the rows' pieces in one run of the whole block: 16 bytes, or one value where rows start anywhere
+        // four rows at once, 256 threads to each: pieces of 16 bytes, or single values where rows start anywhere
         const bool vec = a.ldh % 8 == 0 && a.d % 8 == 0 && reinterpret_cast<uintptr_t>(a.h) % 16 == 0;
-        const uint32_t pieces = uint32_t(vec ? a.d / 8 : a.d);
-        const uint64_t all = uint64_t(listed) * pieces;
+        const uint64_t pieces = vec ? a.d / 8 : a.d;
+        for (uint32_t k = threadIdx.x / 256; k < listed; k += kPickThreads / 256) {
+            const uint16_t* from = static_cast<const uint16_t*>(a.h) + list[k][0] * a.ldh;
+            uint16_t* to = static_cast<uint16_t*>(a.out_h) + list[k][1] * a.ld_out;
+            if (vec) {
 #pragma unroll 4
-        for (uint64_t k = threadIdx.x; k < all; k += kPickThreads) {
-            const uint32_t r = uint32_t(k / pieces), c = uint32_t(k - uint64_t(r) * pieces);
-            const uint16_t* from = static_cast<const uint16_t*>(a.h) + list[r][0] * a.ldh;
-            uint16_t* to = static_cast<uint16_t*>(a.out_h) + list[r][1] * a.ld_out;
-            if (vec) reinterpret_cast<uint4*>(to)[c] = reinterpret_cast<const uint4*>(from)[c];
-            else to[c] = from[c];
+                for (uint64_t c = threadIdx.x % 256; c < pieces; c += 256)
+                    reinterpret_cast<uint4*>(to)[c] = reinterpret_cast<const uint4*>(from)[c];
+            } else {
+#pragma unroll 8
+                for (uint64_t c = threadIdx.x % 256; c < pieces; c += 256) to[c] = from[c];
+            }
         }
         __syncthreads();
         if (threadIdx.x == 0) listed = 0;
