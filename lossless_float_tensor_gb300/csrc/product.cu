@@ -1208,8 +1208,23 @@ struct Choice {
     double cost;
 };
 
-Choice choose(const Product& p, int sms) {
-    Tiling best{};
+// The search takes 2 to 3 us, which a call of a few microseconds feels, so each
+// thread remembers its last choices by what they depend on: sizes and kind of
+// product, nothing of the operands.
+struct Picked {
+    uint64_t m, n, depth;
+    uint32_t groups, kind;
+    uint32_t bn, splits, pair;
+    double cost;
+};
+Picked* picked_slot(const Product& p, uint32_t kind) {
+    static thread_local Picked slots[64];  // kind 0: empty
+    const uint64_t h = (p.m * 0x9E3779B97F4A7C15ull ^ p.n * 0xC2B2AE3D27D4EB4Full ^ p.depth * 0x165667B19E3779F9ull ^ p.groups ^ kind) *
+                       0x9E3779B97F4A7C15ull;
+    return &slots[h >> 58];
+}
+
+void search_tile(const Product& p, int sms, Picked& best) {
     double best_cost = 1e300;
     const uint64_t rows = p.m, groups = p.schedule == kDepth ? p.groups : 1;
     const double blocks = std::max(1.0, double(p.depth) / (p.schedule == kDepth ? p.groups : 1) / kDepthTile);
@@ -1252,7 +1267,7 @@ Choice choose(const Product& p, int sms) {
     auto consider_turned = [&](uint32_t bn, uint32_t pair) {
         const double each = mean <= 0.8 * bn ? 1.0 : mean / bn + 0.5, width = std::min<double>(bn, mean / each + 8 * pair);
         const double tiles = used * each * double(row_tiles_of(p, pair));
-        offer(bn, 1, pair, std::max(1.0, tiles / (sms / pair) + 0.5), stage_of(width, (kRowsTile + bn / pair) * 128.0),  // as many stages as fit decide
+        offer(bn, 1, pair, std::max(1.0, tiles / (sms / pair) + 0.5), stage_of(width, (kRowsTile + bn / pair) * 128.0),
               1.5 * column * width);
     };
     if (p.schedule == kColumns) {
@@ -1260,22 +1275,39 @@ Choice choose(const Product& p, int sms) {
             if (bn <= widest || bn == 32) consider_turned(bn, 1);
         if (rows > kRowsTile) consider_turned(256, 2);
     } else {
-    for (uint32_t bn = widest; bn >= unit; bn -= unit) {
-        if (bn < 32 && bn < widest) break;
-        if (p.epilogue == kLossStats && bn % 128 && bn < widest) continue;  // statistics are kept for every 128 columns
-        consider(bn, 1, 1);
-        if (may_split)
-            for (uint32_t splits = 2; splits <= kMaxSplits && blocks / splits >= 4; ++splits) consider(bn, splits, 1);
+        for (uint32_t bn = widest; bn >= unit; bn -= unit) {
+            if (bn < 32 && bn < widest) break;
+            if (p.epilogue == kLossStats && bn % 128 && bn < widest) continue;  // statistics are kept for every 128 columns
+            consider(bn, 1, 1);
+            if (may_split)
+                for (uint32_t splits = 2; splits <= kMaxSplits && blocks / splits >= 4; ++splits) consider(bn, splits, 1);
+        }
+        if (rows > kRowsTile)
+            for (uint32_t bn = 256; bn >= 96; bn -= 32)
+                if (p.epilogue != kLossStats || bn % 128 == 0) {
+                    consider(bn, 1, 2);
+                    if (may_split)
+                        for (uint32_t splits = 2; splits <= kMaxSplits / 2 && blocks / splits >= 4; ++splits) consider(bn, splits, 2);
+                }
     }
-    if (rows > kRowsTile)
-        for (uint32_t bn = 256; bn >= 96; bn -= 32)
-            if (p.epilogue != kLossStats || bn % 128 == 0) {
-                consider(bn, 1, 2);
-                if (may_split)
-                    for (uint32_t splits = 2; splits <= kMaxSplits / 2 && blocks / splits >= 4; ++splits) consider(bn, splits, 2);
-            }
+    best.cost = best_cost;
+}
+
+Choice choose(const Product& p, int sms) {
+    const StoreEpilogue& e = p.st;
+    const uint32_t kind = 1 | p.schedule << 1 | p.epilogue << 3 | (p.a.depth_major ? 32 : 0) | (p.b.depth_major ? 64 : 0) |
+                          (e.z ? 128 : 0) | (e.residual ? 256 : 0) | (e.ldo % 8 ? 512 : 0) |
+                          (e.z && e.act == UZIP_ACT_RELU ? 1024 : 0) | (p.live_depth ? 2048 : 0);
+    Picked* const slot = picked_slot(p, kind);
+    if (slot->kind != kind || slot->m != p.m || slot->n != p.n || slot->depth != p.depth || slot->groups != p.groups) {
+        *slot = Picked{p.m, p.n, p.depth, p.groups, kind, 0, 0, 0, 0};
+        search_tile(p, sms, *slot);
     }
-    Tiling& t = best;
+    Tiling t{};
+    t.bn = slot->bn, t.splits = slot->splits, t.pair = slot->pair;
+    const uint64_t rows = p.m;
+    const uint32_t low = uint32_t(std::min<uint64_t>(kRowsTile, (rows + 7) / 8 * 8));
+    const double used = p.groups * (1 - std::exp(-double(p.n) / p.groups)), mean = p.n / std::max(1.0, used);  // kColumns
     const uint32_t b_cols = t.bn / t.pair;
     t.b_box = p.schedule != kColumns ? b_cols : std::min(b_cols, mean >= 96 * t.pair ? 64u : mean >= 24 ? 32u : 16u);
     // the slices of a stage come in one box where they end with the rows (the third dimension is the groups' otherwise)
@@ -1299,14 +1331,13 @@ Choice choose(const Product& p, int sms) {
     const uint32_t fmt = p.dtype == UZIP_BF16 ? 1 : 0;
     t.idesc = 1u << 4 | fmt << 7 | fmt << 10 | (p.a.depth_major ? 0u : 1u << 15) | (p.b.depth_major ? 0u : 1u << 16) |
               (p.schedule == kColumns ? 0 : t.bn >> 3 << 17) | (kRowsTile * t.pair >> 4) << 24;
-    const StoreEpilogue& e = p.st;
     t.out_width = p.epilogue == kLossGrad ? 8 : row_width(e.out, e.ldo | e.out_group);
     t.z_width = row_width(e.z, e.ldz);
     const uint32_t out_unit = e.out_fp32 ? 4 : 8;
     t.vec = (aligned16(e.out) && e.ldo % out_unit == 0 && e.out_group % out_unit == 0 ? 1 : 0) |
             (aligned16(e.bias) && (p.n % 8 == 0 || p.groups == 1) ? 2 : 0) | (aligned16(e.residual) && e.ldr % 8 == 0 ? 4 : 0) |
             (aligned16(e.z) && e.ldz % 8 == 0 ? 8 : 0) | (aligned16(e.sum_in) && e.ld_sum % 4 == 0 ? 16 : 0);
-    return Choice{t, best_cost};
+    return Choice{t, slot->cost};
 }
 
 template <int EPI, int MODE, int LAYOUT>

@@ -44,9 +44,9 @@ __global__ void __launch_bounds__(kThreads) fill_kernel(T* p, uint64_t ld, uint6
 // Block (x, y, z): 128 columns, a share of the rows, one group.  Where rows
 // start on 16-byte boundaries a thread holds 8 neighbouring columns and walks
 // every 16th row; elsewhere it holds columns 32 apart, so that a warp still
-// reads neighbouring values, and walks every 8th row.  Four rows are in
-// flight; the partial column sums meet in shared memory in a fixed order.
-constexpr uint32_t kGradCols = 128, kGradAhead = 4;
+// reads neighbouring values, and walks every 8th row.  64 rows of a block are
+// in flight; the partial column sums meet in shared memory in a fixed order.
+constexpr uint32_t kGradCols = 128;
 
 __device__ __forceinline__ void spread8(const uint4& q, int dtype, float v[8]) {
     const uint32_t w[4] = {q.x, q.y, q.z, q.w};
@@ -83,6 +83,7 @@ __device__ __forceinline__ bool offsets_bad(const int64_t* offsets, uint32_t gro
 template <bool VEC>
 __global__ void __launch_bounds__(kThreads) act_grad_kernel(const __grid_constant__ ActGrad a) {
     constexpr uint32_t kAcross = VEC ? 16 : 32, kRows = kThreads / kAcross, kHeld = kGradCols / kAcross;
+    constexpr uint32_t kGradAhead = 64 / kRows;
     __shared__ float sums[kRows][kGradCols + 4];
     const uint32_t tx = threadIdx.x % kAcross, ty = threadIdx.x / kAcross, g = blockIdx.z;
     const uint64_t col0 = uint64_t(blockIdx.x) * kGradCols;
@@ -346,12 +347,14 @@ cudaError_t launch_fill(void* p, uint64_t ld, uint64_t rows, uint64_t cols, uint
     return cudaGetLastError();
 }
 
-// Eight blocks for each SM, a share of at least 256 rows: a second kernel joins
-// the shares, which costs more than 256 rows in one block.
+// Eight blocks for each SM, a share of at least 64 rows: a block takes 64 rows
+// in about 2 us (777 x 1237 in 12 shares: 5.9 us, in 3: 15.1), and a second
+// kernel joins the shares.  Experts have rows unevenly: there a share is eight
+// rows of the mean.
 uint32_t act_grad_splits(uint64_t m, uint64_t n, uint64_t groups) {
     const uint64_t have = (n + kGradCols - 1) / kGradCols * groups;
     const uint64_t want = std::max<uint64_t>(1, 152 * 8 / std::max<uint64_t>(1, have));
-    return uint32_t(std::max<uint64_t>(1, std::min(want, m / groups / 256)));
+    return uint32_t(std::max<uint64_t>(1, std::min(want, m / groups / (groups > 1 ? 8 : 64))));
 }
 
 cudaError_t launch_act_grad(const ActGrad& a, cudaStream_t s) {

@@ -241,9 +241,11 @@ def _forward(name, x, w, offsets, bias, activation, residual, save_preact, out, 
         else:
             y = out
             a.y, a.ldy = _matrix(y, "out", (m, n), x)
-        z = torch.empty((m, n), dtype=x.dtype, device=dev) if save_preact else None
-        if z is not None:
-            a.z, a.ldz = z.data_ptr() or None, n
+        z = None
+        if save_preact:  # rows on 16-byte boundaries, whatever n: the gradient reads them again
+            wide = -(-n // 8) * 8
+            z = torch.empty_strided((m, n), (wide, 1), dtype=x.dtype, device=dev)
+            a.z, a.ldz = z.data_ptr() or None, wide
         _run(name, a, dev, workspace, status, check)
     return (y, z) if save_preact else y
 
@@ -288,7 +290,7 @@ def linear(x, w, bias=None, *, activation="none", residual=None, save_preact=Fal
 
     activation is "none", "relu", "gelu" (error function) or "silu".  With
     save_preact the result is (y, z), z = x @ w.T + bias, which
-    linear_backward needs.  Matrices may have any row stride; the last
+    linear_backward needs (with padded rows where n is no multiple of 8).  Matrices may have any row stride; the last
     dimension must be contiguous.  Outputs and workspace are allocated on
     `stream` (default: the current one) where they are not given; `status` is
     a 0-dim int32 CUDA tensor, and check=True reads it back (one sync) and
