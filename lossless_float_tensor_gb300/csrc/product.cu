@@ -373,6 +373,29 @@ __device__ __forceinline__ void write8(void* base, uint64_t at, bool vec, uint32
     }
 }
 
+__device__ __forceinline__ void add_sums8(const StoreEpilogue& e, uint32_t vec, uint64_t row, uint32_t col, uint32_t cols, float v[8]) {
+    const float* s = e.sum_in + row * e.ld_sum + col;
+    if ((vec & 16) && cols == 8) {
+        const float4 lo = *reinterpret_cast<const float4*>(s), hi = *reinterpret_cast<const float4*>(s + 4);
+        v[0] += lo.x, v[1] += lo.y, v[2] += lo.z, v[3] += lo.w, v[4] += hi.x, v[5] += hi.y, v[6] += hi.z, v[7] += hi.w;
+    } else {
+#pragma unroll
+        for (uint32_t j = 0; j < 8; ++j)
+            if (j < cols) v[j] += s[j];
+    }
+}
+__device__ __forceinline__ void write_fp32(const StoreEpilogue& e, uint64_t at, uint32_t vec, uint32_t cols, const float v[8]) {
+    float* o = static_cast<float*>(e.out) + at;
+    if ((vec & 1) && cols == 8) {
+        reinterpret_cast<float4*>(o)[0] = make_float4(v[0], v[1], v[2], v[3]);
+        reinterpret_cast<float4*>(o)[1] = make_float4(v[4], v[5], v[6], v[7]);
+    } else {
+#pragma unroll
+        for (uint32_t j = 0; j < 8; ++j)
+            if (j < cols) o[j] = v[j];
+    }
+}
+
 // kStore for `cols` (1 to 8) neighbouring values of a row.
 __device__ __forceinline__ void store8(const Product& p, uint32_t vec, uint32_t g, uint64_t row, uint32_t col,
                                        uint32_t cols, float alpha, float v[8]) {
@@ -382,17 +405,7 @@ __device__ __forceinline__ void store8(const Product& p, uint32_t vec, uint32_t 
 #pragma unroll
         for (uint32_t j = 0; j < 8; ++j) v[j] *= alpha;
     }
-    if (e.sum_in) {
-        const float* s = e.sum_in + row * e.ld_sum + col;
-        if ((vec & 16) && cols == 8) {
-            const float4 lo = *reinterpret_cast<const float4*>(s), hi = *reinterpret_cast<const float4*>(s + 4);
-            v[0] += lo.x, v[1] += lo.y, v[2] += lo.z, v[3] += lo.w, v[4] += hi.x, v[5] += hi.y, v[6] += hi.z, v[7] += hi.w;
-        } else {
-#pragma unroll
-            for (uint32_t j = 0; j < 8; ++j)
-                if (j < cols) v[j] += s[j];
-        }
-    }
+    if (e.sum_in) add_sums8(e, vec, row, col, cols, v);
     if (e.bias) {
         read8(e.bias, g * p.n + col, vec & 2, cols, p.dtype, q);
 #pragma unroll
@@ -413,15 +426,7 @@ __device__ __forceinline__ void store8(const Product& p, uint32_t vec, uint32_t 
         write8(e.out, at, vec & 1, cols, p.dtype, v);
         return;
     }
-    float* o = static_cast<float*>(e.out) + at;
-    if ((vec & 1) && cols == 8) {
-        reinterpret_cast<float4*>(o)[0] = make_float4(v[0], v[1], v[2], v[3]);
-        reinterpret_cast<float4*>(o)[1] = make_float4(v[4], v[5], v[6], v[7]);
-    } else {
-#pragma unroll
-        for (uint32_t j = 0; j < 8; ++j)
-            if (j < cols) o[j] = v[j];
-    }
+    write_fp32(e, at, vec, cols, v);
 }
 
 // An epilogue warp holds a row in each lane, which would read and write memory
@@ -435,6 +440,34 @@ struct Patch {
     __device__ __forceinline__ uint4& at(uint32_t row, uint32_t piece) const { return s[row * 4 + (piece ^ (row >> 1 & 3))]; }
     __device__ __forceinline__ uint16_t& value(uint32_t row, uint32_t col) const {
         return reinterpret_cast<uint16_t*>(&at(row, col / 8))[col % 8];
+    }
+    // this lane's row, rounded
+    __device__ __forceinline__ void put(const float v[32], int dtype) const {
+        __syncwarp();
+        if (dtype == UZIP_BF16) {
+#pragma unroll
+            for (uint32_t i = 0; i < 4; ++i)
+                at(lane, i) = make_uint4(to16x2(v[8 * i], v[8 * i + 1], UZIP_BF16), to16x2(v[8 * i + 2], v[8 * i + 3], UZIP_BF16),
+                                         to16x2(v[8 * i + 4], v[8 * i + 5], UZIP_BF16), to16x2(v[8 * i + 6], v[8 * i + 7], UZIP_BF16));
+        } else {
+#pragma unroll
+            for (uint32_t i = 0; i < 4; ++i)
+                at(lane, i) = make_uint4(to16x2(v[8 * i], v[8 * i + 1], UZIP_FP16), to16x2(v[8 * i + 2], v[8 * i + 3], UZIP_FP16),
+                                         to16x2(v[8 * i + 4], v[8 * i + 5], UZIP_FP16), to16x2(v[8 * i + 6], v[8 * i + 7], UZIP_FP16));
+        }
+        __syncwarp();
+    }
+    // one value for each of the 32 rows, in this lane's column, rounded
+    __device__ __forceinline__ void put_column(const float v[32], int dtype) const {
+        __syncwarp();
+        if (dtype == UZIP_BF16) {
+#pragma unroll
+            for (uint32_t i = 0; i < 32; ++i) value(i, lane) = to16(v[i], UZIP_BF16);
+        } else {
+#pragma unroll
+            for (uint32_t i = 0; i < 32; ++i) value(i, lane) = to16(v[i], UZIP_FP16);
+        }
+        __syncwarp();
     }
     // rows x cols values on their way from p, rows ld apart; vec: 16-byte access
     __device__ __forceinline__ void fetch(const uint16_t* p, uint64_t ld, uint32_t rows, uint32_t cols, bool vec, uint4 q[4]) const {
@@ -586,10 +619,7 @@ __device__ __forceinline__ void finish_transposed(const Product& p, const Tiling
                 return dot_again(p, o.group, 0, feature0 + from, o.col0 + c + at, lane) + b;
             });
         if (z) {
-            __syncwarp();
-#pragma unroll
-            for (uint32_t i = 0; i < 32; ++i) patch.value(i, lane) = to16(v[i], dtype);
-            __syncwarp();
+            patch.put_column(v, dtype);
             patch.store(z + uint64_t(c) * e.ldz, e.ldz, tokens, features, t.z_width);
         }
         if (e.act == UZIP_ACT_RELU) {
@@ -602,10 +632,7 @@ __device__ __forceinline__ void finish_transposed(const Product& p, const Tiling
 #pragma unroll
             for (uint32_t i = 0; i < 32; ++i) v[i] = act_value(v[i], UZIP_ACT_SILU);
         }
-        __syncwarp();
-#pragma unroll
-        for (uint32_t i = 0; i < 32; ++i) patch.value(i, lane) = to16(v[i], dtype);
-        __syncwarp();
+        patch.put_column(v, dtype);
         patch.store(out + uint64_t(c) * e.ldo, e.ldo, tokens, features, t.out_width);
     }
     __syncwarp();
@@ -684,7 +711,16 @@ __device__ __forceinline__ void finish_tile(const Product& p, const Tiling& t, c
             if (live) {
 #pragma unroll
                 for (uint32_t j = 0; j < 4; ++j)
-                    if (8 * j < here) store8(p, t.vec, o.group, row, o.col0 + c + 8 * j, min(8u, here - 8 * j), alpha, v + 8 * j);
+                    if (8 * j < here) {
+                        const uint32_t some = min(8u, here - 8 * j), col = o.col0 + c + 8 * j;
+                        float* const q = v + 8 * j;
+#pragma unroll
+                        for (uint32_t i = 0; i < 8; ++i) q[i] *= alpha;
+                        if (e.sum_in) add_sums8(e, t.vec, row, col, some, q);
+                        const uint64_t at = row * e.ldo + col;
+                        if (e.out_fp32) write_fp32(e, at, t.vec, some, q);
+                        else write8(e.out, at, t.vec & 1, some, dtype, q);
+                    }
             }
             __syncwarp();
             continue;
@@ -697,8 +733,10 @@ __device__ __forceinline__ void finish_tile(const Product& p, const Tiling& t, c
                 v[i] = weight == 0.f ? 0.f : weight * d;
             }
         } else {
+            if (e.alpha) {
 #pragma unroll
-            for (uint32_t i = 0; i < 32; ++i) v[i] *= alpha;
+                for (uint32_t i = 0; i < 32; ++i) v[i] *= alpha;
+            }
             if (has_bias) {
                 const float* const b = bias + c / 2 - half * (kPatchCols / 2);  // this warp's patches one after the other
 #pragma unroll
@@ -713,12 +751,7 @@ __device__ __forceinline__ void finish_tile(const Product& p, const Tiling& t, c
                     return dot_again(p, 0, o.group, row0 + from, uint64_t(o.col0) + c + at, lane) + b;
                 });
             if (z) {
-                __syncwarp();
-#pragma unroll
-                for (uint32_t i = 0; i < 4; ++i)
-                    patch.at(lane, i) = make_uint4(to16x2(v[8 * i], v[8 * i + 1], dtype), to16x2(v[8 * i + 2], v[8 * i + 3], dtype),
-                                                   to16x2(v[8 * i + 4], v[8 * i + 5], dtype), to16x2(v[8 * i + 6], v[8 * i + 7], dtype));
-                __syncwarp();
+                patch.put(v, dtype);
                 patch.store(z + c, e.ldz, rows, here, t.z_width);
             }
             if (act == UZIP_ACT_RELU) {
@@ -751,12 +784,7 @@ __device__ __forceinline__ void finish_tile(const Product& p, const Tiling& t, c
                 }
             }
         }
-        __syncwarp();
-#pragma unroll
-        for (uint32_t i = 0; i < 4; ++i)
-            patch.at(lane, i) = make_uint4(to16x2(v[8 * i], v[8 * i + 1], dtype), to16x2(v[8 * i + 2], v[8 * i + 3], dtype),
-                                           to16x2(v[8 * i + 4], v[8 * i + 5], dtype), to16x2(v[8 * i + 6], v[8 * i + 7], dtype));
-        __syncwarp();
+        patch.put(v, dtype);
         patch.store(out + c, ldo, rows, here, t.out_width);
     }
     __syncwarp();
