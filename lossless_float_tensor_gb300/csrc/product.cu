@@ -560,10 +560,10 @@ __device__ __noinline__ float dot_again(const Product& p, uint32_t ga, uint32_t 
 // this the kernel's work.
 template <typename Again>
 __device__ __forceinline__ void mend_near_zero(const Product& p, float v[32], uint32_t count, bool live, uint32_t lane, Again again) {
-    float mean = 0.f;
+    float sum = 0.f;  // (past `count` a patch holds whatever was there)
 #pragma unroll
-    for (uint32_t i = 0; i < 32; ++i) mean += fabsf(v[i]);
-    const float near = mean * (1.f / 32) * float(p.depth) * 0x1p-29f;
+    for (uint32_t i = 0; i < 32; ++i) sum += i < count ? fabsf(v[i]) : 0.f;
+    const float near = sum / float(count) * float(p.depth) * 0x1p-29f;
     uint32_t close = 0;
 #pragma unroll
     for (uint32_t i = 0; i < 32; ++i)
@@ -573,12 +573,12 @@ __device__ __forceinline__ void mend_near_zero(const Product& p, float v[32], ui
     uint32_t lanes = __ballot_sync(0xFFFFFFFFu, close);
     for (uint32_t left = 8; lanes && left; --left) {
         const uint32_t from = __ffs(lanes) - 1, at = __ffs(__shfl_sync(0xFFFFFFFFu, close, from)) - 1;
-        const float sum = again(from, at);
+        const float mended = again(from, at);
         if (lane == from) {
             close &= close - 1;
 #pragma unroll
             for (uint32_t i = 0; i < 32; ++i)
-                if (i == at) v[i] = sum;
+                if (i == at) v[i] = mended;
         }
         lanes = __ballot_sync(0xFFFFFFFFu, close);
     }

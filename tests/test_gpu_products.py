@@ -439,6 +439,25 @@ def test_same_inputs_give_the_same_bits(uz):
         assert all(torch.equal(a, b) for a, b in zip(first, out))
 
 
+@pytest.mark.parametrize("m,k,n", [(354, 1072, 1616), (586, 4280, 273), (90, 512, 1003), (21, 3600, 3176)])
+def test_same_bits_where_a_tile_ends_inside_a_patch(uz, m, k, n):
+    """Values kept for relu's gradient are compared with their neighbours' size:
+    only with neighbours that exist.  Other calls in between leave other values
+    behind in the columns past the end."""
+    g = _gen(34)
+    x, w, b = _rand(g, (m, k), torch.float16), _rand(g, (2, n, k), torch.float16, k ** -0.5), _rand(g, (2, n), torch.float16)
+    off = torch.tensor([0, m // 3, m], device="cuda")
+    other = _rand(g, (m, k), torch.float16, 1000.0), _rand(g, (2048, k), torch.float16), _rand(g, (2048,), torch.float16, 30000.0)
+    first = None
+    for i in range(6):
+        if i % 2:
+            uz.linear(other[0], other[1], other[2], activation="relu", save_preact=True)
+        out = [*uz.linear(x, w[0], b[0], activation="relu", save_preact=True),
+               *uz.grouped_linear(x, w, off, b, activation="relu", save_preact=True)]
+        first = first or out
+        assert all(torch.equal(p, q) for p, q in zip(first, out))
+
+
 def test_streams_of_their_own(uz):
     g = _gen(32)
     x, w, dy = _whole(g, (130, 201), torch.bfloat16, 1, 0.1), _whole(g, (260, 201), torch.bfloat16, 1), \
