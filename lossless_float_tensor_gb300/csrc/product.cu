@@ -812,6 +812,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t rank = PAIR ? cluster_rank() & 1 : 0;  // the pair's block 0 issues the products,
     const uint32_t leader = MODE == 3 ? cluster_rank() & ~1u : 0;  // and has this rank in the cluster
 
+    if (threadIdx.x == 0) {
+        for (uint32_t i = 0; i < t.stages; ++i) {
+            mbar_init(smem_u32(&ctl->full[i]), 2);  // A's and B's bytes announced
+            mbar_init(smem_u32(&ctl->empty[i]), 1);
+        }
+        for (uint32_t i = 0; i < 2; ++i) {
+            mbar_init(smem_u32(&ctl->acc_full[i]), 1);
+            mbar_init(smem_u32(&ctl->acc_empty[i]), kEpilogueWarps * t.pair);
+        }
+        mbar_init(smem_u32(&ctl->drain), 1);
+        ctl->abort = 0;
+        fence_mbar_init();
+    }
+    wait_for_launch_before();
     const uint32_t live_rows = p.live_rows ? *p.live_rows : uint32_t(p.m), live_depth = p.live_depth ? *p.live_depth : uint32_t(p.depth);
 
     // the cut of the rows or depths, checked whole
@@ -852,19 +866,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (lane == 0) first[0] = 0;
         }
-    }
-    if (threadIdx.x == 0) {
-        for (uint32_t i = 0; i < t.stages; ++i) {
-            mbar_init(smem_u32(&ctl->full[i]), 2);  // A's and B's bytes announced
-            mbar_init(smem_u32(&ctl->empty[i]), 1);
-        }
-        for (uint32_t i = 0; i < 2; ++i) {
-            mbar_init(smem_u32(&ctl->acc_full[i]), 1);
-            mbar_init(smem_u32(&ctl->acc_empty[i]), kEpilogueWarps * t.pair);
-        }
-        mbar_init(smem_u32(&ctl->drain), 1);
-        ctl->abort = 0;
-        fence_mbar_init();
     }
     if (warp == 1) tmem_alloc<PAIR>(smem_u32(&ctl->tmem), t.tmem_cols);
     tmem_fence_before();
@@ -1388,12 +1389,14 @@ cudaError_t launch(const Product& p, const Tiling& t, int sms, const Maps<LAYOUT
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = t.smem;
     cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = t.splits * t.pair;
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = t.splits * t.pair;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = MODE ? 1 : 0;
+    cfg.numAttrs = MODE ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, kern, p, t, maps);
 }
 

@@ -11,6 +11,18 @@
 
 namespace uzip {
 
+// ---- launches one after another ---------------------------------------------
+
+// Every kernel of the products is launched so that its blocks may be set up
+// while the blocks of the launch before it end, and calls this before it reads
+// or writes memory: the launch before has then ended and its results are there.
+// That launch waited in the same way for the one before itself, so the order is
+// the stream's.  48 x 128256 x 4096 loss: 171 us, 166; 1001 x 32003 x 1000 loss
+// and gradient: 271 us, 248; 1531 rows in 37 experts with gradients, in a graph:
+// 75.6 us, 73.9.  Setting up earlier, as soon as the launch before has begun
+// (griddepcontrol.launch_dependents), was slower: 168, 251 and 76.2 us.
+__device__ __forceinline__ void wait_for_launch_before() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // ---- one product ------------------------------------------------------------
 
 // An operand of `rows` x `depth` values (depth is the summed dimension).

@@ -11,6 +11,21 @@ namespace {
 
 constexpr uint32_t kThreads = 256;
 
+// A launch whose blocks may be set up while the one before it ends: the kernel starts with wait_for_launch_before().
+template <typename... Args, typename... Given>
+cudaError_t launch_after(void (*kernel)(Args...), dim3 grid, uint32_t threads, cudaStream_t s, Given... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, Args(args)...);
+}
+
 uint32_t blocks_for(uint64_t items, uint64_t most) {
     return uint32_t(std::max<uint64_t>(1, std::min<uint64_t>((items + kThreads - 1) / kThreads, most)));
 }
@@ -19,6 +34,7 @@ uint32_t blocks_for(uint64_t items, uint64_t most) {
 // are zero.  One thread makes one 16-byte store from eight 2-byte loads.
 // blockIdx.y is the matrix.
 __global__ void __launch_bounds__(kThreads) pack_kernel(const __grid_constant__ PackJobs jobs) {
+    wait_for_launch_before();
     const PackJob& j = jobs.job[blockIdx.y];
     const uint64_t vecs = j.ld_to / 8, total = vecs * j.rows * j.groups;
     for (uint64_t i = blockIdx.x * uint64_t(kThreads) + threadIdx.x; i < total; i += uint64_t(gridDim.x) * kThreads) {
@@ -37,6 +53,7 @@ __global__ void __launch_bounds__(kThreads) pack_kernel(const __grid_constant__ 
 
 template <typename T>
 __global__ void __launch_bounds__(kThreads) fill_kernel(T* p, uint64_t ld, uint64_t cols, uint64_t total, T value) {
+    wait_for_launch_before();
     for (uint64_t i = blockIdx.x * uint64_t(kThreads) + threadIdx.x; i < total; i += uint64_t(gridDim.x) * kThreads)
         p[i / cols * ld + i % cols] = value;
 }
@@ -82,6 +99,7 @@ __device__ __forceinline__ bool offsets_bad(const int64_t* offsets, uint32_t gro
 
 template <bool VEC>
 __global__ void __launch_bounds__(kThreads) act_grad_kernel(const __grid_constant__ ActGrad a) {
+    wait_for_launch_before();
     constexpr uint32_t kAcross = VEC ? 16 : 32, kRows = kThreads / kAcross, kHeld = kGradCols / kAcross;
     constexpr uint32_t kGradAhead = 64 / kRows;
     __shared__ float sums[kRows][kGradCols + 4];
@@ -167,6 +185,7 @@ __global__ void __launch_bounds__(kThreads) act_grad_kernel(const __grid_constan
 
 __global__ void __launch_bounds__(kThreads) join_columns_kernel(const float* part, uint32_t splits, uint64_t n,
                                                                 uint64_t total, uint16_t* db, int dtype) {
+    wait_for_launch_before();
     const uint64_t i = blockIdx.x * uint64_t(kThreads) + threadIdx.x;
     if (i >= total) return;
     const uint64_t g = i / n, c = i - g * n;
@@ -177,6 +196,7 @@ __global__ void __launch_bounds__(kThreads) join_columns_kernel(const float* par
 
 __global__ void __launch_bounds__(kThreads) offset_check_kernel(const int64_t* offsets, uint32_t groups, uint64_t m,
                                                                 int32_t* status) {
+    wait_for_launch_before();
     if (__syncthreads_or(offsets_bad(offsets, groups, m)) && threadIdx.x == 0) *status = int(UZIP_ERR_INVALID_ARG);
 }
 
@@ -192,6 +212,7 @@ constexpr uint32_t kJoinThreads = 128;
 __global__ void __launch_bounds__(kJoinThreads) loss_join_kernel(LossEpilogue e, const uint32_t* token, const uint32_t* count,
                                                                  uint64_t v, uint32_t tiles, float* loss, float* lse,
                                                                  int32_t* status) {
+    wait_for_launch_before();
     __shared__ float2 s[kJoinThreads / 32];
     const uint64_t row = blockIdx.x;
     if (count && row >= *count) return;
@@ -227,6 +248,7 @@ __global__ void __launch_bounds__(kJoinThreads) loss_join_kernel(LossEpilogue e,
 // places come out the same in each, without a launch in between.
 constexpr uint32_t kPickThreads = 1024, kPickList = 2048;
 __global__ void __launch_bounds__(kPickThreads) loss_rows_kernel(const __grid_constant__ LossRows a) {
+    wait_for_launch_before();
     __shared__ uint32_t list[kPickList][2];  // token, place
     __shared__ uint32_t listed, before[32];
     __shared__ float tops[32];
@@ -312,6 +334,7 @@ __global__ void __launch_bounds__(kPickThreads) loss_rows_kernel(const __grid_co
 // A warp for each row.
 __global__ void __launch_bounds__(kThreads) spread_rows_kernel(const uint16_t* from, uint64_t ld, const uint32_t* place,
                                                                uint16_t* to, uint64_t ld_to, uint64_t rows, uint64_t cols, bool vec) {
+    wait_for_launch_before();
     const uint32_t lane = threadIdx.x % 32;
     for (uint64_t r = blockIdx.x * uint64_t(kThreads / 32) + threadIdx.x / 32; r < rows; r += uint64_t(gridDim.x) * (kThreads / 32)) {
         const uint32_t at = place[r];
@@ -333,18 +356,16 @@ cudaError_t launch_pack(const PackJobs& jobs, cudaStream_t s) {
     for (uint32_t i = 0; i < jobs.count; ++i)
         most = std::max(most, jobs.job[i].ld_to / 8 * jobs.job[i].rows * jobs.job[i].groups);
     if (most == 0) return cudaSuccess;
-    pack_kernel<<<dim3(blocks_for(most, 152 * 32), jobs.count), kThreads, 0, s>>>(jobs);
-    return cudaGetLastError();
+    return launch_after(pack_kernel, dim3(blocks_for(most, 152 * 32), jobs.count), kThreads, s, jobs);
 }
 
 cudaError_t launch_fill(void* p, uint64_t ld, uint64_t rows, uint64_t cols, uint32_t elem, cudaStream_t s) {
     const uint64_t total = rows * cols;
     if (total == 0) return cudaSuccess;
     if (elem == 2)
-        fill_kernel<<<blocks_for(total, 152 * 32), kThreads, 0, s>>>(static_cast<uint16_t*>(p), ld, cols, total, uint16_t(0));
-    else
-        fill_kernel<<<blocks_for(total, 152 * 32), kThreads, 0, s>>>(static_cast<float*>(p), ld, cols, total, 0.f);
-    return cudaGetLastError();
+        return launch_after(fill_kernel<uint16_t>, blocks_for(total, 152 * 32), kThreads, s, static_cast<uint16_t*>(p), ld, cols, total,
+                            uint16_t(0));
+    return launch_after(fill_kernel<float>, blocks_for(total, 152 * 32), kThreads, s, static_cast<float*>(p), ld, cols, total, 0.f);
 }
 
 // Eight blocks for each SM, a share of at least 64 rows: a block takes 64 rows
@@ -362,42 +383,35 @@ cudaError_t launch_act_grad(const ActGrad& a, cudaStream_t s) {
     const dim3 grid(uint32_t((a.n + kGradCols - 1) / kGradCols), a.splits, a.groups);
     const bool vec = a.n % 8 == 0 && a.lddy % 8 == 0 && reinterpret_cast<uintptr_t>(a.dy) % 16 == 0 &&
                      (a.act == UZIP_ACT_NONE || (a.ldz % 8 == 0 && reinterpret_cast<uintptr_t>(a.z) % 16 == 0));
-    if (vec) act_grad_kernel<true><<<grid, kThreads, 0, s>>>(a);
-    else act_grad_kernel<false><<<grid, kThreads, 0, s>>>(a);
-    cudaError_t err = cudaGetLastError();
+    cudaError_t err = launch_after(vec ? act_grad_kernel<true> : act_grad_kernel<false>, grid, kThreads, s, a);
     if (err == cudaSuccess && a.db && a.splits > 1) {
         const uint64_t total = uint64_t(a.groups) * a.n;
-        join_columns_kernel<<<uint32_t((total + kThreads - 1) / kThreads), kThreads, 0, s>>>(
-            a.part, a.splits, a.n, total, static_cast<uint16_t*>(a.db), a.dtype);
-        err = cudaGetLastError();
+        err = launch_after(join_columns_kernel, uint32_t((total + kThreads - 1) / kThreads), kThreads, s, a.part, a.splits, a.n, total,
+                           static_cast<uint16_t*>(a.db), a.dtype);
     }
     return err;
 }
 
 cudaError_t launch_offset_check(const int64_t* offsets, uint64_t groups, uint64_t m, int32_t* status, cudaStream_t s) {
     if (!status) return cudaSuccess;
-    offset_check_kernel<<<1, kThreads, 0, s>>>(offsets, uint32_t(groups), m, status);
-    return cudaGetLastError();
+    return launch_after(offset_check_kernel, 1, kThreads, s, offsets, uint32_t(groups), m, status);
 }
 
 cudaError_t launch_loss_join(const LossEpilogue& e, const uint32_t* token, const uint32_t* count, uint64_t t, uint64_t v,
                              float* loss, float* lse, int32_t* status, cudaStream_t s) {
-    loss_join_kernel<<<uint32_t(t), kJoinThreads, 0, s>>>(e, token, count, v, e.tiles, loss, lse, status);
-    return cudaGetLastError();
+    return launch_after(loss_join_kernel, uint32_t(t), kJoinThreads, s, e, token, count, v, e.tiles, loss, lse, status);
 }
 
 cudaError_t launch_loss_rows(const LossRows& a, cudaStream_t s) {
-    loss_rows_kernel<<<uint32_t(std::min<uint64_t>(a.t, 304)), kPickThreads, 0, s>>>(a);
-    return cudaGetLastError();
+    return launch_after(loss_rows_kernel, uint32_t(std::min<uint64_t>(a.t, 304)), kPickThreads, s, a);
 }
 
 cudaError_t launch_spread_rows(const void* from, uint64_t ld, const uint32_t* place, void* to, uint64_t ld_to, uint64_t rows,
                                uint64_t cols, cudaStream_t s) {
     if (rows == 0 || cols == 0) return cudaSuccess;
     const bool vec = ld_to % 8 == 0 && reinterpret_cast<uintptr_t>(to) % 16 == 0;
-    spread_rows_kernel<<<uint32_t(std::min<uint64_t>((rows + 7) / 8, 152 * 8)), kThreads, 0, s>>>(
-        static_cast<const uint16_t*>(from), ld, place, static_cast<uint16_t*>(to), ld_to, rows, cols, vec);
-    return cudaGetLastError();
+    return launch_after(spread_rows_kernel, uint32_t(std::min<uint64_t>((rows + 7) / 8, 152 * 8)), kThreads, s,
+                        static_cast<const uint16_t*>(from), ld, place, static_cast<uint16_t*>(to), ld_to, rows, cols, vec);
 }
 
 }  // namespace uzip
