@@ -526,59 +526,81 @@ struct Patch {
     }
 };
 
-// The product of row `row` of A and column `col` of B (of group g) once more,
-// by one warp in rounded 32-bit additions.  Both operands lie along the depth,
-// their rows on 16-byte boundaries.
-__device__ __noinline__ float dot_again(const Product& p, uint32_t ga, uint32_t gb, uint64_t row, uint64_t col, uint32_t lane) {
+// The product of row `row` of A and column `col` of B (of group g) and a bias
+// once more, by one warp, as near as 32 bits hold it.  Two 16-bit values' product
+// is exact in 32 bits; what each addition rounds away is summed beside it (the
+// error of a sum in six additions, Knuth), and the lanes meet in 64 bits.  Both
+// operands lie along the depth, their rows on 16-byte boundaries.
+__device__ __noinline__ float dot_again(const Product& p, uint32_t ga, uint32_t gb, uint64_t row, uint64_t col, float bias, uint32_t lane) {
     const uint16_t* a = static_cast<const uint16_t*>(p.a.p) + ga * p.a.group + row * p.a.ld;
     const uint16_t* b = static_cast<const uint16_t*>(p.b.p) + gb * p.b.group + col * p.b.ld;
-    float sum = 0.f;
+    float sum = 0.f, lost = 0.f;
+    const auto add = [&](float v) {
+        const float next = __fadd_rn(sum, v), part = __fsub_rn(next, sum);
+        lost = __fadd_rn(lost, __fadd_rn(__fsub_rn(sum, __fsub_rn(next, part)), __fsub_rn(v, part)));
+        sum = next;
+    };
 #pragma unroll 4
     for (uint64_t i = 8 * lane; i + 8 <= p.depth; i += 256) {
         float x[8], y[8];
         read8(a, i, true, 8, p.dtype, x);
         read8(b, i, true, 8, p.dtype, y);
 #pragma unroll
-        for (uint32_t j = 0; j < 8; ++j) sum = fmaf(x[j], y[j], sum);
+        for (uint32_t j = 0; j < 8; ++j) add(__fmul_rn(x[j], y[j]));
     }
     const uint64_t rest = p.depth / 8 * 8 + lane;
-    if (rest < p.depth) sum = fmaf(from16(a[rest], p.dtype), from16(b[rest], p.dtype), sum);
+    if (rest < p.depth) add(__fmul_rn(from16(a[rest], p.dtype), from16(b[rest], p.dtype)));
+    double all = double(sum) + double(lost);
 #pragma unroll
-    for (uint32_t o = 16; o; o /= 2) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
-    return sum;
+    for (uint32_t o = 16; o; o /= 2) all += __shfl_xor_sync(0xFFFFFFFFu, all, o);
+    return float(all + double(bias));
 }
 
 // A step in the slope, as relu's, turns a value's error into a wrong gradient
 // where the error passes zero.  The tensor core's additions cut toward zero,
-// so a sum of k products is off by about k 2^-30 of its neighbours' mean
-// size, ten times what rounded additions would leave: of 4096 x 4096 values
-// at 4096 depths 15 changed their sign, and 8 million at 14336 depths 26.
-// Where a value to be kept for the gradient is nearer to zero than twice that
-// (one in a million at 512 depths), it is summed again; 2 are left, as many
-// as rounded 32-bit sums give.  v[i] are the lane's 32 values,
-// `count` of them real; at most eight of a patch, so that no input can make
-// this the kernel's work.
+// so a sum of k products is off by about k 2^-30 of its neighbours' mean size,
+// ten times what rounded additions would leave: of 4096 x 4096 values at 4096
+// depths 15 changed their sign (rounded 32-bit sums: 5), and of 8 million at
+// 14336 depths 26 (4).  Where a value to be kept for the gradient is nearer to
+// zero than twice that, of 1024 depths more as the products of one step are cut
+// too (6 in a million at 4096 depths), it is summed again, as good as exactly:
+// none to one is left in three such tensors.  A positive value too small for
+// fp16 is kept as its smallest.  v[i] are the lane's 32 values, `count` of them
+// real; at most kMended of a patch, so that no input can make this the kernel's
+// work.
+constexpr uint32_t kMended = 16;
 template <typename Again>
 __device__ __forceinline__ void mend_near_zero(const Product& p, float v[32], uint32_t count, bool live, uint32_t lane, Again again) {
     float sum = 0.f;  // (past `count` a patch holds whatever was there)
 #pragma unroll
     for (uint32_t i = 0; i < 32; ++i) sum += i < count ? fabsf(v[i]) : 0.f;
-    const float near = sum / float(count) * float(p.depth) * 0x1p-29f;
-    uint32_t close = 0;
+    float of = float(count);
+    if (count < 8) {  // too few say nothing of their size: the whole patch
+        if (!live) sum = 0.f;
 #pragma unroll
-    for (uint32_t i = 0; i < 32; ++i)
-        if (fabsf(v[i]) < near && v[i] != 0.f) close |= 1u << i;
+        for (uint32_t o = 16; o; o /= 2) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+        of *= float(__popc(__ballot_sync(0xFFFFFFFFu, live)));
+    }
+    const float near = sum / of * float(p.depth + 1024) * 0x1p-29f;
+    uint32_t close = 0, zero = 0;
+#pragma unroll
+    for (uint32_t i = 0; i < 32; ++i) {
+        if (fabsf(v[i]) < near) close |= 1u << i;
+        if (v[i] == 0.f) zero |= 1u << i;
+    }
     if (!live) close = 0;
     if (count < 32) close &= (1u << count) - 1;
+    if (__reduce_add_sync(0xFFFFFFFFu, __popc(close & zero)) > kMended) close &= ~zero;  // zeros of a row or a column, not of a sum
     uint32_t lanes = __ballot_sync(0xFFFFFFFFu, close);
-    for (uint32_t left = 8; lanes && left; --left) {
+    for (uint32_t left = kMended; lanes && left; --left) {
         const uint32_t from = __ffs(lanes) - 1, at = __ffs(__shfl_sync(0xFFFFFFFFu, close, from)) - 1;
-        const float mended = again(from, at);
+        float mended = again(from, at);
+        if (mended > 0.f && p.dtype == UZIP_FP16) mended = fmaxf(mended, 0x1p-24f);
         if (lane == from) {
             close &= close - 1;
 #pragma unroll
             for (uint32_t i = 0; i < 32; ++i)
-                if (i == at) v[i] = mended;
+                if (i == at && fabsf(mended) < INFINITY) v[i] = mended;  // (another order's partial sums may pass bf16's range)
         }
         lanes = __ballot_sync(0xFFFFFFFFu, close);
     }
@@ -616,7 +638,7 @@ __device__ __forceinline__ void finish_transposed(const Product& p, const Tiling
         if (FORWARD && z && e.act == UZIP_ACT_RELU)
             mend_near_zero(p, v, tokens, lane < features, lane, [&](uint32_t from, uint32_t at) {
                 const float b = __shfl_sync(0xFFFFFFFFu, bias, from);
-                return dot_again(p, o.group, 0, feature0 + from, o.col0 + c + at, lane) + b;
+                return dot_again(p, o.group, 0, feature0 + from, o.col0 + c + at, b, lane);
             });
         if (z) {
             patch.put_column(v, dtype);
@@ -748,7 +770,7 @@ __device__ __forceinline__ void finish_tile(const Product& p, const Tiling& t, c
             if (FORWARD && z && act == UZIP_ACT_RELU)
                 mend_near_zero(p, v, here, live, lane, [&](uint32_t from, uint32_t at) {
                     const float b = has_bias ? bias[c / 2 - half * (kPatchCols / 2) + at] : 0.f;
-                    return dot_again(p, 0, o.group, row0 + from, uint64_t(o.col0) + c + at, lane) + b;
+                    return dot_again(p, 0, o.group, row0 + from, uint64_t(o.col0) + c + at, b, lane);
                 });
             if (z) {
                 patch.put(v, dtype);

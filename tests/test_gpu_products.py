@@ -540,3 +540,30 @@ def test_refusals(uz):
     for f in bad:
         with pytest.raises(uz.UzipError):
             f()
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("grouped", (False, True))
+def test_relu_keeps_the_sign_of_sums_that_cancel(uz, dtype, grouped):
+    # Every fourth row against every 64th column: 64 products, then the same ones negated, sixteen times, and +-2^-26 at
+    # last.  Sums of 32 bits are off by more, and fp16 has no value that small.
+    m, n, k = 300, 512, 2048
+    g = _gen(5)
+    x = _rand(g, (m, k), dtype)
+    w = _rand(g, (3, n, k) if grouped else (n, k), dtype)
+    sign = torch.randint(0, 2, (m,), generator=g, device="cuda") * 2 - 1
+    rows, cols = slice(0, m, 4), slice(7, n, 64)
+    xs, ws = x.view(m, k // 128, 2, 64), w.view(-1, n, k // 128, 2, 64)
+    xs[rows, :, 1] = xs[rows, :, 0]
+    ws[:, cols, :, 1] = -ws[:, cols, :, 0]
+    x[rows, k - 65] = 0
+    x[rows, k - 1] = (sign[rows] * 2.0**-13).to(dtype)
+    w[..., cols, k - 1] = 2.0**-13
+    if grouped:
+        offsets = torch.tensor([0, 130, 130, m], device="cuda")
+        z = uz.grouped_linear(x, w, offsets, activation="relu", save_preact=True)[1]
+    else:
+        z = uz.linear(x, w, activation="relu", save_preact=True)[1]
+    small = z[rows, cols]
+    assert torch.equal(small > 0, (sign[rows, None] > 0).expand_as(small))
+    assert float(small.abs().max()) <= 2.0**-24
