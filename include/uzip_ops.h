@@ -85,7 +85,8 @@ uzip_status uzip_grouped_linear(const uzip_linear_args* a, void* d_workspace, ui
  * rounded to the dtype for the two products (tensor cores take 16-bit
  * operands); db sums it unrounded.  z is what uzip_linear stored: values that
  * relu's slope turns on were summed again there where the tensor core's sum
- * came within its own error of zero. */
+ * came within its own error of zero, and a positive one of those that fp16
+ * cannot hold is stored as its smallest value. */
 typedef struct {
     int32_t dtype;
     int32_t act;
