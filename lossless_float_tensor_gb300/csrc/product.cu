@@ -559,15 +559,16 @@ __device__ __noinline__ float dot_again(const Product& p, uint32_t ga, uint32_t 
 // A step in the slope, as relu's, turns a value's error into a wrong gradient
 // where the error passes zero.  The tensor core's additions cut toward zero,
 // so a sum of k products is off by about k 2^-30 of its neighbours' mean size,
-// ten times what rounded additions would leave: of 4096 x 4096 values at 4096
-// depths 15 changed their sign (rounded 32-bit sums: 5), and of 8 million at
-// 14336 depths 26 (4).  Where a value to be kept for the gradient is nearer to
-// zero than twice that, of 1024 depths more as the products of one step are cut
-// too (6 in a million at 4096 depths), it is summed again, as good as exactly:
-// none to one is left in three such tensors.  A positive value too small for
-// fp16 is kept as its smallest.  v[i] are the lane's 32 values, `count` of them
-// real; at most kMended of a patch, so that no input can make this the kernel's
-// work.
+// ten times what rounded additions would leave, and by up to twice k 2^-29
+// where the partial sums went far from zero on their way.  Where a value to be
+// kept for the gradient is nearer to zero than k 2^-28 (and 1024 depths more,
+// as the products of one step are cut too; 12 in a million at 4096 depths), it
+// is summed again, as good as exactly.  Wrong signs of 690 million values at 520
+// to 32768 depths: 17 with half that distance, none with it (32-bit sums: 5 in
+// 180 million at 520).  4096 x 4096 x 4096 takes 90 us instead of 83, 2048 x
+// 14336 x 4096 200 instead of 137.  A positive value too small for fp16 is kept
+// as its smallest.  v[i] are the lane's 32 values, `count` of them real; at most
+// kMended of a patch, so that no input can make this the kernel's work.
 constexpr uint32_t kMended = 16;
 template <typename Again>
 __device__ __forceinline__ void mend_near_zero(const Product& p, float v[32], uint32_t count, bool live, uint32_t lane, Again again) {
@@ -581,7 +582,7 @@ __device__ __forceinline__ void mend_near_zero(const Product& p, float v[32], ui
         for (uint32_t o = 16; o; o /= 2) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
         of *= float(__popc(__ballot_sync(0xFFFFFFFFu, live)));
     }
-    const float near = sum / of * float(p.depth + 1024) * 0x1p-29f;
+    const float near = sum / of * float(p.depth + 1024) * 0x1p-28f;
     uint32_t close = 0, zero = 0;
 #pragma unroll
     for (uint32_t i = 0; i < 32; ++i) {
