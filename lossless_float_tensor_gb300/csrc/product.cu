@@ -1479,9 +1479,9 @@ cudaError_t launch_product(const Product& p, int sms, cudaStream_t s) {
     const Tiling& t = c.t;
     if (p.epilogue == kLossStats) return launch_layout<kLossStats, 0>(p, t, sms, s);
     if (p.epilogue == kLossGrad) return launch_layout<kLossGrad, 0>(p, t, sms, s);
-    if (p.schedule == kRows) {
+    if (p.schedule == kRows && !p.st.residual) {
         // Groups' rows as the columns of the transposed product: a tile takes as many as there are instead of 128 or
-        // 256, at the price of a slower epilogue.
+        // 256, at the price of a slower epilogue, which adds no residual.
         Product q = p;
         q.a = p.b, q.b = p.a, q.m = p.n, q.n = p.m, q.schedule = kColumns;
         const Choice turned = choose(q, sms);

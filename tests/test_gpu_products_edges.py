@@ -55,3 +55,37 @@ def test_no_kept_sign_is_wrong_by_expert(uz):
         for i in range(e):
             rows = slice(ends[i], ends[i + 1])
             assert torch.equal(z[rows] > 0, x[rows].double() @ w[i].double().T + b[i].double() > 0)
+
+
+# ---- grouped products with a residual (C entry point) ------------------------------
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("k,n", [(72, 300), (512, 512), (201, 130)])
+@pytest.mark.parametrize("counts", [[3, 0, 2, 1], [16] * 12, [63, 65, 1, 0, 200], [700, 0, 513, 256], [257] * 9])
+def test_grouped_residual(uz, counts, k, n, dtype):
+    """The residual is added whichever way the product is taken: few rows for
+    each expert, or many."""
+    from lossless_float_tensor_gb300 import ops
+
+    g = _gen(sum(counts) + k)
+    e, m = len(counts), sum(counts)
+    off = torch.tensor([0] + list(torch.tensor(counts).cumsum(0)), dtype=torch.int64, device="cuda")
+    whole = lambda *s: torch.randint(-2, 3, s, generator=g, device="cuda").to(dtype)  # noqa: E731
+    x, w, b, r = whole(m, k), whole(e, n, k), whole(e, n), whole(m, n)
+    x *= torch.rand(m, k, generator=g, device="cuda") < 16.0 / k
+    y, z = torch.empty_like(r), torch.empty_like(r)
+    a = ops.LinearArgs(dtype=uz.UZIP_BF16 if dtype == torch.bfloat16 else uz.UZIP_FP16, act=ops.UZIP_ACT_RELU, m=m, n=n, k=k,
+                       groups=e, offsets=off.data_ptr(), x=x.data_ptr(), ldx=k, w=w.data_ptr(), ldw=k, w_group=n * k,
+                       bias=b.data_ptr(), residual=r.data_ptr(), ldr=n, y=y.data_ptr(), ldy=n, z=z.data_ptr(), ldz=n)
+    ws = torch.empty(ops.uzip_grouped_linear_workspace_size(a), dtype=torch.uint8, device="cuda")
+    status = torch.full((), -1, dtype=torch.int32, device="cuda")
+    st = ops.uzip_grouped_linear(a, ws.data_ptr() if ws.numel() else None, ws.numel(), status.data_ptr(),
+                                 torch.cuda.current_stream().cuda_stream)
+    assert st == uz.UZIP_OK and int(status.item()) == uz.UZIP_OK
+    at = 0
+    for i, c in enumerate(counts):
+        rows = slice(at, at + c)
+        at += c
+        pz = x[rows].double() @ w[i].double().T + b[i].double()
+        assert torch.equal(z[rows].double(), pz.to(dtype).double())
+        assert torch.equal(y[rows].double(), (pz.clamp(min=0) + r[rows].double()).to(dtype).double())
