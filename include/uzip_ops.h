@@ -142,7 +142,10 @@ uzip_status uzip_cross_entropy(const uzip_cross_entropy_args* a, void* d_workspa
  *   dh_i = dloss_i (sum_j p_ij w_j - w_{t_i}),  dw_j = sum_i dloss_i (p_ij - [j = t_i]) h_i.
  * The tokens that are not ignored are moved together in the workspace (t x d
  * values), so that ignored ones cost nothing.  The vocabulary is taken `piece`
- * classes at a time: their logits are computed again and dloss (p - [j = t]),
+ * classes at a time: their logits are computed again, with the same sums as
+ * the loss's (p - 1 at a target that has nearly all of the probability is then
+ * off by no more than the rounding of lse, half a unit in its last place), and
+ * dloss (p - [j = t]),
  * scaled so that the largest dloss is 2^10, is rounded to the dtype in the
  * workspace (t x piece values); dh is summed over the pieces in fp32.  piece 0 takes the default: as many classes as 512 MiB hold, at most
  * 32768. */

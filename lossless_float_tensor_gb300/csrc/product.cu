@@ -40,9 +40,13 @@ constexpr uint32_t kMaxStages = 24;
 constexpr uint32_t kThreads = 352;  // TMA warp for A, MMA warp, 4 epilogue warps, TMA warp for B, 4 epilogue warps
 // The tensor core cuts each addition to 24 bits toward zero, which adds up to a
 // bias of half a unit an addition: at 4096 depths logits were 1e-5 off and the
-// loss 1.4e-6 of itself.  The loss statistics take the products of 1024 depths
-// at a time into registers, where they are added with rounding.
-constexpr uint32_t kStatsChunk = 16;  // stages
+// loss 1.4e-6 of itself.  The loss statistics, and the logits of the loss's
+// gradient, take the products of 1024 depths at a time into registers, where
+// they are added with rounding: both have the same logits, and p - 1 of a token
+// whose target has nearly all of the probability is a difference of two near
+// numbers (p = 0.9995 at 4096 depths: that token's gradient was off by 45 % of
+// itself when its logits were summed in one go).
+constexpr uint32_t kLogitChunk = 16;  // stages
 constexpr uint32_t kEpilogueWarps = 8;
 constexpr uint32_t kPatchCols = 32;  // columns that an epilogue warp takes at a time
 constexpr uint32_t kPatchBytes = 32 * kPatchCols * 2, kEpilogueBytes = kPatchBytes + 128 * 4;  // a warp's shared memory
@@ -689,25 +693,24 @@ __device__ __forceinline__ void finish_stats(const Product& p, const Tile& o, ui
 // One finished accumulator of a block: 128 rows, one in each lane of the four
 // warps of a column half; warps of half 0 take the patches 0, 2, ... of 32
 // columns, those of half 1 the others.  `bias` is the warp's copy of its
-// columns' bias.  `release` gives the accumulator back once the warp has read
-// its last column.  The loops over patches stay rolled: the code of one patch
-// fits the instruction cache, four of them did not.
-template <int EPI, bool FORWARD, typename Release>
-__device__ __forceinline__ void finish_tile(const Product& p, const Tiling& t, const Tile& o, uint32_t acc, uint32_t warp_row,
-                                            uint32_t half, float alpha, const Patch& patch, const float* bias, uint4 ahead[4],
-                                            Release release) {
+// columns' bias.  load(c, v) brings the patch at column c into v.  The loops over
+// patches stay rolled: the code of one patch fits the instruction cache, four of
+// them did not.
+template <int EPI, bool FORWARD, typename Load>
+__device__ __forceinline__ void finish_tile(const Product& p, const Tiling& t, const Tile& o, uint32_t warp_row, uint32_t half,
+                                            float alpha, const Patch& patch, const float* bias, uint4 ahead[4], Load load) {
     const uint32_t lane = patch.lane;
     const uint64_t row0 = uint64_t(o.row0) + warp_row, row = row0 + lane;
-    const bool live = row < o.row_end, empty = o.blocks == 0;
+    const bool live = row < o.row_end;
     const uint32_t rows = row0 < o.row_end ? uint32_t(min(uint64_t(32), o.row_end - row0)) : 0;
     const uint32_t cols = o.cols;
     const int dtype = p.dtype;
     const StoreEpilogue& e = p.st;
     int64_t target = -1;
-    float lse2 = 0.f, weight = 0.f;
+    float lse = 0.f, weight = 0.f;
     if (EPI == kLossGrad && live) {
         target = p.ls.targets[row] - int64_t(p.ls.col0 + o.col0);
-        lse2 = p.ls.lse[row] * kLog2e;
+        lse = p.ls.lse[row];
         weight = p.ls.g[row];
     }
     const bool wide = EPI == kStore && (e.out_fp32 || e.sum_in);  // partial results in 32 bits: few, after long depths
@@ -718,18 +721,11 @@ __device__ __forceinline__ void finish_tile(const Product& p, const Tiling& t, c
     const uint64_t ldo = EPI == kStore ? e.ldo : p.ls.ldo;
     const uint16_t* const res = static_cast<const uint16_t*>(e.residual) + row0 * e.ldr + o.col0;
     uint16_t* const z = EPI == kStore && e.z ? static_cast<uint16_t*>(e.z) + row0 * e.ldz + o.col0 : nullptr;
-    if (cols <= half * kPatchCols) release();  // nothing of this tile is this warp's
 #pragma unroll 1
     for (uint32_t c = half * kPatchCols; c < cols; c += 2 * kPatchCols) {
         const uint32_t here = min(kPatchCols, cols - c);
         float v[32];
-        if (empty) {
-#pragma unroll
-            for (uint32_t i = 0; i < 32; ++i) v[i] = 0.f;
-        } else {
-            tmem_load32(acc + c, v);
-        }
-        if (c + 2 * kPatchCols >= cols) release();
+        load(c, v);
         if (wide) {
             if (live) {
 #pragma unroll
@@ -751,7 +747,7 @@ __device__ __forceinline__ void finish_tile(const Product& p, const Tiling& t, c
         if (EPI == kLossGrad) {
 #pragma unroll
             for (uint32_t i = 0; i < 32; ++i) {
-                float d = fast_exp2(fmaf(v[i], kLog2e, -lse2));
+                float d = fast_exp2((v[i] - lse) * kLog2e);  // (near p = 1 the difference is exact)
                 if (target == int64_t(c + i)) d -= 1.f;
                 v[i] = weight == 0.f ? 0.f : weight * d;
             }
@@ -824,7 +820,7 @@ template <int EPI, int MODE, int LAYOUT>
 __global__ void __launch_bounds__(kThreads, 1)
     product_kernel(const __grid_constant__ Product p, const __grid_constant__ Tiling t,
                    const __grid_constant__ Maps<LAYOUT == 3> maps) {
-    constexpr bool SPLIT = MODE & 1, PAIR = MODE & 2, STATS = EPI == kLossStats;
+    constexpr bool SPLIT = MODE & 1, PAIR = MODE & 2, STATS = EPI == kLossStats, CHUNKED = EPI != kStore;
     constexpr bool A_DEEP = LAYOUT < 2 || LAYOUT == 4, B_DEEP = LAYOUT == 0 || LAYOUT > 3, CUT = LAYOUT == 3, TURNED = LAYOUT > 3;
     extern __shared__ uint8_t raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
@@ -995,7 +991,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (!(ok = wait(ctl, smem_u32(&ctl->acc_empty[buf]), (used >> 1 & 1) ^ 1))) break;
                     tmem_fence_after();
                     const uint32_t acc = tmem + buf * buffer_cols;
-                    const uint32_t first_block = i, end = STATS ? min(o.blocks, i + kStatsChunk) : o.blocks;
+                    const uint32_t first_block = i, end = CHUNKED ? min(o.blocks, i + kLogitChunk) : o.blocks;
                     if (end == 0) {  // nothing to add up: the epilogues take zeros
                         if (PAIR) {
                             cluster_arrive(cluster_address(smem_u32(&ctl->acc_full[buf]), leader));
@@ -1037,7 +1033,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             float v[128];
 #pragma unroll
             for (uint32_t i = 0; i < 128; ++i) v[i] = 0.f;
-            for (uint32_t i = 0; i < max(o.blocks, 1u); i += kStatsChunk, ++used) {
+            for (uint32_t i = 0; i < max(o.blocks, 1u); i += kLogitChunk, ++used) {
                 const uint32_t buf = used & 1;
                 if (!(ok = __all_sync(0xFFFFFFFFu, wait(ctl, smem_u32(&ctl->acc_full[buf]), used >> 1 & 1)))) break;
                 tmem_fence_after();
@@ -1063,14 +1059,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else {
         Walk walk(p, t, offsets, first, live_rows, live_depth);
         Tile o;
-        uint32_t tiles = 0;
+        uint32_t used = 0;  // accumulators
         const uint32_t quarter = warp % 4, half = warp > 6;  // the TMEM lanes that this warp may read, its columns
         const float alpha = EPI == kStore && p.st.alpha ? *p.st.alpha : 1.f;
         uint8_t* const mine = reinterpret_cast<uint8_t*>(ctl) - (kEpilogueWarps - 4 * half - quarter) * kEpilogueBytes;
         const Patch patch{reinterpret_cast<uint4*>(mine), lane};
         float* const bias = reinterpret_cast<float*>(mine + kPatchBytes);
         while (walk.take(o)) {
-            const uint32_t buf = tiles & 1;
             uint4 ahead[4] = {};
             if (!SPLIT) {
                 // what the epilogue reads besides the products is fetched while they run
@@ -1091,21 +1086,59 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 __syncwarp();
             }
-            if (!__all_sync(0xFFFFFFFFu, wait(ctl, smem_u32(&ctl->acc_full[buf]), tiles >> 1 & 1))) break;
-            tmem_fence_after();
-            const uint32_t acc = tmem + buf * buffer_cols + (quarter * 32 << 16);
+            // the next accumulator, and the way to give it back once this warp has read its last column
+            const auto arrived = [&] {
+                const bool ok = __all_sync(0xFFFFFFFFu, wait(ctl, smem_u32(&ctl->acc_full[used & 1]), used >> 1 & 1));
+                tmem_fence_after();
+                return ok;
+            };
             const auto release = [&] {
                 tmem_fence_before();
                 __syncwarp();
                 if (lane == 0) {
-                    if (PAIR) cluster_arrive(cluster_address(smem_u32(&ctl->acc_empty[buf]), leader));
-                    else mbar_arrive(smem_u32(&ctl->acc_empty[buf]));
+                    if (PAIR) cluster_arrive(cluster_address(smem_u32(&ctl->acc_empty[used & 1]), leader));
+                    else mbar_arrive(smem_u32(&ctl->acc_empty[used & 1]));
                 }
             };
+            if constexpr (CHUNKED) {
+                // the chunks' accumulators added up: this warp's patches, the next one always in sum[0]
+                float sum[4][32] = {};
+                bool ok = true;
+                for (uint32_t i = 0; i < max(o.blocks, 1u); i += kLogitChunk, ++used) {
+                    if (!(ok = arrived())) break;
+                    const uint32_t acc = tmem + (used & 1) * buffer_cols + half * kPatchCols + (quarter * 32 << 16);
+#pragma unroll
+                    for (uint32_t j = 0; j < 4; ++j)
+                        if (half * kPatchCols + 2 * kPatchCols * j < o.cols && o.blocks) {
+                            float add[32];
+                            tmem_load32(acc + 2 * kPatchCols * j, add);
+#pragma unroll
+                            for (uint32_t k = 0; k < 32; ++k) sum[j][k] += add[k];
+                        }
+                    release();
+                }
+                if (!ok) break;
+                finish_tile<EPI, LAYOUT == 0>(p, t, o, quarter * 32, half, alpha, patch, bias, ahead, [&](uint32_t, float v[32]) {
+#pragma unroll
+                    for (uint32_t k = 0; k < 32; ++k) v[k] = sum[0][k], sum[0][k] = sum[1][k], sum[1][k] = sum[2][k], sum[2][k] = sum[3][k];
+                });
+                continue;
+            }
+            if (!arrived()) break;
+            const uint32_t acc = tmem + (used & 1) * buffer_cols + (quarter * 32 << 16);
             if constexpr (TURNED) {
                 finish_transposed<LAYOUT == 4>(p, t, o, acc, quarter * 32, half, patch, release);
             } else if constexpr (!SPLIT) {
-                finish_tile<EPI, LAYOUT == 0>(p, t, o, acc, quarter * 32, half, alpha, patch, bias, ahead, release);
+                if (o.cols <= half * kPatchCols) release();  // nothing of this tile is this warp's
+                finish_tile<EPI, LAYOUT == 0>(p, t, o, quarter * 32, half, alpha, patch, bias, ahead, [&](uint32_t c, float v[32]) {
+                    if (o.blocks == 0) {
+#pragma unroll
+                        for (uint32_t i = 0; i < 32; ++i) v[i] = 0.f;
+                    } else {
+                        tmem_load32(acc + c, v);
+                    }
+                    if (c + 2 * kPatchCols >= o.cols) release();
+                });
             } else {
                 const uint32_t lane_row = quarter * 32 + lane, row0 = o.row0 + rank * kRowsTile;
                 // partial sums to shared memory, rows bn + 4 floats apart (no bank conflicts for 16-byte access)
@@ -1124,7 +1157,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             *reinterpret_cast<float4*>(part + c + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
                 }
             }
-            ++tiles;
+            ++used;
         }
     }
     if (SPLIT) {

@@ -89,3 +89,38 @@ def test_grouped_residual(uz, counts, k, n, dtype):
         pz = x[rows].double() @ w[i].double().T + b[i].double()
         assert torch.equal(z[rows].double(), pz.to(dtype).double())
         assert torch.equal(y[rows].double(), (pz.clamp(min=0) + r[rows].double()).to(dtype).double())
+
+
+# ---- tokens that the model is sure of ----------------------------------------------
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_gradient_of_confident_tokens(uz, dtype):
+    """A target with p between 0.999 and 0.99999: p - 1 is the difference of two
+    near numbers, and the whole row of dh hangs on it.  Off by: the rounding of
+    lse (half a unit of a value below 32, 2^-20) and of the exponential (2^-21)
+    against 1 - p; logits whose sums of 1024 depths are cut 256 times by 2^-23 of
+    at most 8 (four of them: 2^-10); two roundings to the type."""
+    g = _gen(35)
+    d, v, t = 4096, 8192, 512
+    w = _rand(g, (v, d), dtype, d ** -0.5)
+    targets = torch.randint(0, v, (t,), generator=g, device="cuda")
+    sure = torch.linspace(14, 24, t, device="cuda")[:, None]
+    h = (w[targets].float() * sure + 0.1 * torch.randn(t, d, generator=g, device="cuda")).to(dtype)
+    s = h.double() @ w.double().T
+    p = torch.softmax(s, 1)
+    rest = p.scatter(1, targets[:, None], 0.0).sum(1)
+    want = 16384 * (p.scatter(1, targets[:, None], -rest[:, None]) @ w.double())
+    _, lse = uz.cross_entropy(h, w, targets)
+    dh, dw = uz.cross_entropy_backward(torch.full((t,), 16384.0, device="cuda"), h, w, targets, lse, check=True)
+    off = (dh.double() - want).norm(dim=1) / want.norm(dim=1)
+    bound = 2 * ref.ROUND[dtype] + 2.0 ** -10 + (2.0 ** -20 + 2.0 ** -21) / rest
+    judged = (rest < 1e-3) & (rest > 1e-5)
+    assert int(judged.sum()) > 64 and float(lse.max()) < 32
+    assert float((off / bound)[judged].max()) <= 1.0
+    # and the classes' rows, of which only confident tokens have a part
+    only = torch.where(judged, 16384.0, 0.0)
+    _, dw = uz.cross_entropy_backward(only.float(), h, w, targets, lse, need_dh=False, check=True)
+    dl = p.scatter(1, targets[:, None], -rest[:, None]) * only.double()[:, None]
+    at = torch.unique(targets[judged])
+    want, most = (dl.T @ h.double())[at], (dl.abs() * bound[:, None]).T @ h.double().abs()
+    assert float(((dw[at].double() - want).abs() / (most[at] + ref.ROUND[dtype] * want.abs() + 2.0 ** -24)).max()) <= 1.0
