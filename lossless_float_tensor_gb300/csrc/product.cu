@@ -47,6 +47,12 @@ constexpr uint32_t kThreads = 352;  // TMA warp for A, MMA warp, 4 epilogue warp
 // numbers (p = 0.9995 at 4096 depths: that token's gradient was off by 45 % of
 // itself when its logits were summed in one go).
 constexpr uint32_t kLogitChunk = 16;  // stages
+// Other products take this many stages in one go: over 32768 depths the same sign
+// all the way was 2e-4 short (2^-12, fp16's rounding), over 2^20 6e-3.  Longer
+// depths take chunks of 16384 in the same way, which leaves 1e-4.  (Chunks of
+// 8192 would leave half of that and cost 2048 x 14336 x 4096 143 us instead of
+// 139.)
+constexpr uint32_t kLongChunk = 256;
 constexpr uint32_t kEpilogueWarps = 8;
 constexpr uint32_t kPatchCols = 32;  // columns that an epilogue warp takes at a time
 constexpr uint32_t kPatchBytes = 32 * kPatchCols * 2, kEpilogueBytes = kPatchBytes + 128 * 4;  // a warp's shared memory
@@ -613,31 +619,23 @@ __device__ __forceinline__ void mend_near_zero(const Product& p, float v[32], ui
 
 // An accumulator of the transposed product: lanes are output columns (features)
 // and accumulator columns are output rows (tokens), so a patch is written a
-// token a step, 32 neighbouring features at once.
-template <bool FORWARD, typename Release>
-__device__ __forceinline__ void finish_transposed(const Product& p, const Tiling& t, const Tile& o, uint32_t acc, uint32_t warp_row,
-                                                  uint32_t half, const Patch& patch, Release release) {
+// token a step, 32 neighbouring features at once.  load(c, v) as in finish_tile.
+template <bool FORWARD, typename Load>
+__device__ __forceinline__ void finish_transposed(const Product& p, const Tiling& t, const Tile& o, uint32_t warp_row, uint32_t half,
+                                                  const Patch& patch, Load load) {
     const uint32_t lane = patch.lane, feature0 = o.row0 + warp_row;
     const uint32_t features = feature0 < o.row_end ? min(32u, o.row_end - feature0) : 0;
-    const bool empty = o.blocks == 0;
     const int dtype = p.dtype;
     const StoreEpilogue& e = p.st;
     float bias = 0.f;
     if (e.bias && lane < features) bias = from16(static_cast<const uint16_t*>(e.bias)[o.group * p.m + feature0 + lane], dtype);
     uint16_t* const out = static_cast<uint16_t*>(e.out) + uint64_t(o.col0) * e.ldo + feature0;
     uint16_t* const z = e.z ? static_cast<uint16_t*>(e.z) + uint64_t(o.col0) * e.ldz + feature0 : nullptr;
-    if (o.cols <= half * kPatchCols) release();
 #pragma unroll 1
     for (uint32_t c = half * kPatchCols; c < o.cols; c += 2 * kPatchCols) {
         const uint32_t tokens = min(32u, o.cols - c);
         float v[32];
-        if (empty) {
-#pragma unroll
-            for (uint32_t i = 0; i < 32; ++i) v[i] = 0.f;
-        } else {
-            tmem_load32(acc + c, v);
-        }
-        if (c + 2 * kPatchCols >= o.cols) release();
+        load(c, v);
 #pragma unroll
         for (uint32_t i = 0; i < 32; ++i) v[i] += bias;
         if (FORWARD && z && e.act == UZIP_ACT_RELU)
@@ -816,11 +814,13 @@ __device__ __forceinline__ void finish_tile(const Product& p, const Tiling& t, c
 // LAYOUT: 0 both operands contiguous along the depth, 1 only A, 2 neither, 3
 // neither, with a depth that only the device knows, 4 and 5 the
 // transposed product with ragged columns, A contiguous along the depth or not.
-template <int EPI, int MODE, int LAYOUT>
+// CHUNKED: a tile's depth is taken in chunks, added up in registers.
+template <int EPI, int MODE, int LAYOUT, bool CHUNKED>
 __global__ void __launch_bounds__(kThreads, 1)
     product_kernel(const __grid_constant__ Product p, const __grid_constant__ Tiling t,
                    const __grid_constant__ Maps<LAYOUT == 3> maps) {
-    constexpr bool SPLIT = MODE & 1, PAIR = MODE & 2, STATS = EPI == kLossStats, CHUNKED = EPI != kStore;
+    constexpr bool SPLIT = MODE & 1, PAIR = MODE & 2, STATS = EPI == kLossStats;
+    constexpr uint32_t kChunk = EPI == kStore ? kLongChunk : kLogitChunk;
     constexpr bool A_DEEP = LAYOUT < 2 || LAYOUT == 4, B_DEEP = LAYOUT == 0 || LAYOUT > 3, CUT = LAYOUT == 3, TURNED = LAYOUT > 3;
     extern __shared__ uint8_t raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
@@ -991,7 +991,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (!(ok = wait(ctl, smem_u32(&ctl->acc_empty[buf]), (used >> 1 & 1) ^ 1))) break;
                     tmem_fence_after();
                     const uint32_t acc = tmem + buf * buffer_cols;
-                    const uint32_t first_block = i, end = CHUNKED ? min(o.blocks, i + kLogitChunk) : o.blocks;
+                    const uint32_t first_block = i, end = CHUNKED ? min(o.blocks, i + kChunk) : o.blocks;
                     if (end == 0) {  // nothing to add up: the epilogues take zeros
                         if (PAIR) {
                             cluster_arrive(cluster_address(smem_u32(&ctl->acc_full[buf]), leader));
@@ -1033,7 +1033,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             float v[128];
 #pragma unroll
             for (uint32_t i = 0; i < 128; ++i) v[i] = 0.f;
-            for (uint32_t i = 0; i < max(o.blocks, 1u); i += kLogitChunk, ++used) {
+            for (uint32_t i = 0; i < max(o.blocks, 1u); i += kChunk, ++used) {
                 const uint32_t buf = used & 1;
                 if (!(ok = __all_sync(0xFFFFFFFFu, wait(ctl, smem_u32(&ctl->acc_full[buf]), used >> 1 & 1)))) break;
                 tmem_fence_after();
@@ -1092,19 +1092,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tmem_fence_after();
                 return ok;
             };
-            const auto release = [&] {
+            const auto release = [&](uint32_t buf) {
                 tmem_fence_before();
                 __syncwarp();
                 if (lane == 0) {
-                    if (PAIR) cluster_arrive(cluster_address(smem_u32(&ctl->acc_empty[used & 1]), leader));
-                    else mbar_arrive(smem_u32(&ctl->acc_empty[used & 1]));
+                    if (PAIR) cluster_arrive(cluster_address(smem_u32(&ctl->acc_empty[buf]), leader));
+                    else mbar_arrive(smem_u32(&ctl->acc_empty[buf]));
                 }
             };
+            [[maybe_unused]] float sum[4][32] = {};  // CHUNKED: this warp's patches, the next one always in sum[0]
             if constexpr (CHUNKED) {
-                // the chunks' accumulators added up: this warp's patches, the next one always in sum[0]
-                float sum[4][32] = {};
                 bool ok = true;
-                for (uint32_t i = 0; i < max(o.blocks, 1u); i += kLogitChunk, ++used) {
+                for (uint32_t i = 0; i < max(o.blocks, 1u); i += kChunk, ++used) {
                     if (!(ok = arrived())) break;
                     const uint32_t acc = tmem + (used & 1) * buffer_cols + half * kPatchCols + (quarter * 32 << 16);
 #pragma unroll
@@ -1115,49 +1114,47 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                             for (uint32_t k = 0; k < 32; ++k) sum[j][k] += add[k];
                         }
-                    release();
+                    release(used & 1);
                 }
                 if (!ok) break;
-                finish_tile<EPI, LAYOUT == 0>(p, t, o, quarter * 32, half, alpha, patch, bias, ahead, [&](uint32_t, float v[32]) {
+            } else {
+                if (!arrived()) break;
+                if (!SPLIT && o.cols <= half * kPatchCols) release(used & 1);  // nothing of this tile is this warp's
+            }
+            const uint32_t buf = used & 1, acc = tmem + buf * buffer_cols + (quarter * 32 << 16);
+            const bool empty = o.blocks == 0;
+            const auto load = [&, buf, acc, empty](uint32_t c, float v[32]) {
+                if constexpr (CHUNKED) {
 #pragma unroll
                     for (uint32_t k = 0; k < 32; ++k) v[k] = sum[0][k], sum[0][k] = sum[1][k], sum[1][k] = sum[2][k], sum[2][k] = sum[3][k];
-                });
-                continue;
-            }
-            if (!arrived()) break;
-            const uint32_t acc = tmem + (used & 1) * buffer_cols + (quarter * 32 << 16);
-            if constexpr (TURNED) {
-                finish_transposed<LAYOUT == 4>(p, t, o, acc, quarter * 32, half, patch, release);
-            } else if constexpr (!SPLIT) {
-                if (o.cols <= half * kPatchCols) release();  // nothing of this tile is this warp's
-                finish_tile<EPI, LAYOUT == 0>(p, t, o, quarter * 32, half, alpha, patch, bias, ahead, [&](uint32_t c, float v[32]) {
-                    if (o.blocks == 0) {
+                } else {
+                    if (empty) {
 #pragma unroll
                         for (uint32_t i = 0; i < 32; ++i) v[i] = 0.f;
                     } else {
                         tmem_load32(acc + c, v);
                     }
-                    if (c + 2 * kPatchCols >= o.cols) release();
-                });
+                    if (!SPLIT && c + 2 * kPatchCols >= o.cols) release(buf);
+                }
+            };
+            if constexpr (TURNED) {
+                finish_transposed<LAYOUT == 4>(p, t, o, quarter * 32, half, patch, load);
+            } else if constexpr (!SPLIT) {
+                finish_tile<EPI, LAYOUT == 0>(p, t, o, quarter * 32, half, alpha, patch, bias, ahead, load);
             } else {
                 const uint32_t lane_row = quarter * 32 + lane, row0 = o.row0 + rank * kRowsTile;
                 // partial sums to shared memory, rows bn + 4 floats apart (no bank conflicts for 16-byte access)
                 float* part = reinterpret_cast<float*>(smem) + lane_row * (t.bn + 4);
                 for (uint32_t c = 32 * half; c < t.bn; c += 64) {
                     float v[32];
-                    if (o.blocks) {
-                        tmem_load32(acc + c, v);
-                    } else {
-#pragma unroll
-                        for (uint32_t i = 0; i < 32; ++i) v[i] = 0.f;
-                    }
+                    load(c, v);
 #pragma unroll
                     for (uint32_t i = 0; i < 32; i += 4)
                         if (c + i < t.bn && row0 + lane_row < o.row_end)
                             *reinterpret_cast<float4*>(part + c + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
                 }
             }
-            ++used;
+            if (!CHUNKED) ++used;
         }
     }
     if (SPLIT) {
@@ -1425,9 +1422,9 @@ Choice choose(const Product& p, int sms) {
     return Choice{t, slot->cost};
 }
 
-template <int EPI, int MODE, int LAYOUT>
+template <int EPI, int MODE, int LAYOUT, bool CHUNKED>
 cudaError_t launch(const Product& p, const Tiling& t, int sms, const Maps<LAYOUT == 3>& maps, cudaStream_t s) {
-    auto kern = product_kernel<EPI, MODE, LAYOUT>;
+    auto kern = product_kernel<EPI, MODE, LAYOUT, CHUNKED>;
     static std::atomic<uint64_t> ready{0};  // devices on which the kernel may use all of the shared memory
     int dev = 0;
     cudaError_t err = cudaGetDevice(&dev);
@@ -1456,8 +1453,8 @@ cudaError_t launch(const Product& p, const Tiling& t, int sms, const Maps<LAYOUT
     return cudaLaunchKernelEx(&cfg, kern, p, t, maps);
 }
 
-template <int EPI, int LAYOUT>
-cudaError_t launch_layout(const Product& p, const Tiling& t, int sms, cudaStream_t s) {
+template <int EPI, int LAYOUT, bool CHUNKED>
+cudaError_t launch_mode(const Product& p, const Tiling& t, int sms, cudaStream_t s) {
     constexpr bool kCut = LAYOUT == 3, kTurned = LAYOUT > 3, kMaySplit = EPI == kStore && !kCut && !kTurned;
     Maps<kCut> maps;
     cudaError_t err = make_map(&maps.a, p.a, p.m, p.depth, kTurned ? p.groups : 1, p.a.depth_major ? t.a_box : kDepthTile, p.dtype, t.a_slab);
@@ -1471,16 +1468,27 @@ cudaError_t launch_layout(const Product& p, const Tiling& t, int sms, cudaStream
         }
     }
     if (err != cudaSuccess) return err;
-    if (kMaySplit && t.pair == 2 && t.splits > 1) return launch<EPI, kMaySplit ? 3 : 2, LAYOUT>(p, t, sms, maps, s);
-    if (t.pair == 2) return launch<EPI, 2, LAYOUT>(p, t, sms, maps, s);
-    if (kMaySplit && t.splits > 1) return launch<EPI, kMaySplit ? 1 : 0, LAYOUT>(p, t, sms, maps, s);
-    return launch<EPI, 0, LAYOUT>(p, t, sms, maps, s);
+    if (kMaySplit && t.pair == 2 && t.splits > 1) return launch<EPI, kMaySplit ? 3 : 2, LAYOUT, CHUNKED>(p, t, sms, maps, s);
+    if (t.pair == 2) return launch<EPI, 2, LAYOUT, CHUNKED>(p, t, sms, maps, s);
+    if (kMaySplit && t.splits > 1) return launch<EPI, kMaySplit ? 1 : 0, LAYOUT, CHUNKED>(p, t, sms, maps, s);
+    return launch<EPI, 0, LAYOUT, CHUNKED>(p, t, sms, maps, s);
+}
+
+template <int EPI, int LAYOUT>
+cudaError_t launch_layout(const Product& p, const Tiling& t, int sms, cudaStream_t s) {
+    if constexpr (EPI != kStore) {
+        return launch_mode<EPI, LAYOUT, true>(p, t, sms, s);
+    } else {
+        // the most depths that a block may meet in one tile (a group may have all of them)
+        const bool long_depth = (p.depth + kDepthTile - 1) / kDepthTile > uint64_t(kLongChunk) * t.splits;
+        return long_depth ? launch_mode<EPI, LAYOUT, true>(p, t, sms, s) : launch_mode<EPI, LAYOUT, false>(p, t, sms, s);
+    }
 }
 
 uint32_t cluster_blocks(uint32_t size, int sms) {
     static const std::array<uint32_t, kMaxSplits + 1> most = [sms] {
         std::array<uint32_t, kMaxSplits + 1> v{};
-        auto kern = product_kernel<kStore, 1, 0>;
+        auto kern = product_kernel<kStore, 1, 0, false>;
         cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kSmemMost));
         for (uint32_t size = 1; size <= kMaxSplits; ++size) {
             cudaLaunchConfig_t cfg{};

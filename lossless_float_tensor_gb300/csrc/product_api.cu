@@ -15,7 +15,7 @@ using namespace uzip;
 
 constexpr int64_t kMaxLength = (int64_t(1) << 31) - 1;
 // A piece of the vocabulary: at most 512 MiB of softmax gradient, and at most
-// 32768 classes, whose products the tensor core adds with a bias below 2^-14.
+// 32768 classes, two chunks of a product's depth (product.cu).
 constexpr uint64_t kPieceBytes = 512ull << 20, kPieceMost = 32768;
 
 uint64_t round_to(uint64_t v, uint64_t a) { return (v + a - 1) / a * a; }

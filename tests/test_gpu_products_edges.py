@@ -124,3 +124,100 @@ def test_gradient_of_confident_tokens(uz, dtype):
     at = torch.unique(targets[judged])
     want, most = (dl.T @ h.double())[at], (dl.abs() * bound[:, None]).T @ h.double().abs()
     assert float(((dw[at].double() - want).abs() / (most[at] + ref.ROUND[dtype] * want.abs() + 2.0 ** -24)).max()) <= 1.0
+
+
+# ---- depths of many thousands ------------------------------------------------------
+
+def _whole(g, shape, dtype, most=2, share=None):
+    """Whole numbers, of which a share may be kept and the others be zero."""
+    v = torch.randint(-most, most + 1, shape, generator=g, device="cuda")
+    if share is not None:
+        v = v * (torch.rand(shape, generator=g, device="cuda") < share)
+    return v.to(dtype)
+
+
+def _same(got, want, dtype):
+    assert torch.equal(got.double(), want.to(dtype).double())
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("m,k,n", [(1, 300000, 40), (20, 200001, 130), (300, 150000, 260), (1100, 70000, 1201), (2300, 17000, 4200)])
+def test_long_depths_whole_numbers(uz, m, k, n, dtype):
+    """Depths over 16384 are added up from chunks: every sum is exact here, as a
+    product of x and w, and with the same lengths as one of dy and w or x."""
+    g = _gen(m + k + n)
+    x, w = _whole(g, (m, k), dtype, 2, 24.0 / k), _whole(g, (n, k), dtype, 1)
+    b, r = _whole(g, (n,), dtype, 3), _whole(g, (m, n), dtype, 3)
+    z = x.double() @ w.double().T + b.double()
+    for act in ("relu", "none"):
+        y, pre = uz.linear(x, w, b, activation=act, residual=r, save_preact=True, check=True)
+        _same(pre, z, dtype)
+        _same(y, ref.act64(z, act) + r.double(), dtype)
+    wt, xt = _whole(g, (k, n), dtype, 1), _whole(g, (m, n), dtype, 1)  # depth k in dx
+    dx, _, _ = uz.linear_backward(x, xt, wt, need_dw=False, need_db=False, check=True)
+    _same(dx, x.double() @ wt.double(), dtype)
+    dy, xl = x.T.contiguous(), _whole(g, (k, n), dtype, 1)  # depth k in dw
+    _, dw, _ = uz.linear_backward(dy, xl, torch.zeros(m, n, dtype=dtype, device="cuda"), need_dx=False, need_db=False, check=True)
+    _same(dw, dy.double().T @ xl.double(), dtype)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("counts,k,n", [([20000, 0, 17000, 300], 136, 200), ([16, 3, 0, 40], 17001, 264), ([300, 5, 700], 17000, 520),
+                                        ([16, 3, 0, 40], 264, 17001), ([300, 5, 700], 520, 17000), ([40000, 1], 72, 64)])
+def test_long_depths_by_expert(uz, counts, k, n, dtype):
+    g = _gen(sum(counts) + k)
+    e, m = len(counts), sum(counts)
+    off = torch.tensor([0] + list(torch.tensor(counts).cumsum(0)), dtype=torch.int64, device="cuda")
+    x, w = _whole(g, (m, k), dtype, 2, 24.0 / k), _whole(g, (e, n, k), dtype, 1)
+    dy = _whole(g, (m, n), dtype, 2, 24.0 / max(n, max(counts)))
+    y = uz.grouped_linear(x, w, off, check=True)
+    dx, dw, _ = uz.grouped_linear_backward(dy, x, w, off, need_db=False, check=True)
+    at = 0
+    for i, c in enumerate(counts):
+        rows = slice(at, at + c)
+        at += c
+        _same(y[rows], x[rows].double() @ w[i].double().T, dtype)
+        _same(dx[rows], dy[rows].double() @ w[i].double(), dtype)
+        _same(dw[i], dy[rows].double().T @ x[rows].double(), dtype)
+
+
+@pytest.mark.parametrize("rows", [1 << 17, 1 << 18, 1 << 20])
+def test_long_sums_are_not_short(uz, rows):
+    """Sums of one sign.  A chunk of 16384 depths is 1024 steps of at most four
+    additions, each cut by less than 2^-23 of the sum so far, which grows evenly:
+    2^-12 at worst, and 2^-18 for up to 64 chunks added with rounding.  Beyond
+    that only the result's own rounding is left, which has no direction: its
+    mean over some thousand values is within 2^-15."""
+    g = _gen(36)
+    x = (torch.rand(rows, 64, generator=g, device="cuda") + 0.5).half()
+    dy = ((torch.rand(rows, 96, generator=g, device="cuda") + 0.5) * (2.0 ** 14 / rows)).half()
+    want = dy.double().T @ x.double()
+    worst, mean = 2.0 ** -12 + 2.0 ** -18, 2.0 ** -15
+    w = torch.zeros(1, 96, 64, device="cuda", dtype=torch.half)
+    off = torch.tensor([0, rows], device="cuda")
+    for got in (uz.linear_backward(dy, x, w[0], need_dx=False, need_db=False, check=True)[1],
+                uz.grouped_linear_backward(dy, x, w, off, need_dx=False, need_db=False, check=True)[1][0],
+                uz.linear(dy.T.contiguous(), x.T.contiguous(), check=True),
+                uz.linear_backward(dy.T.contiguous(), torch.zeros(96, 64, device="cuda", dtype=torch.half), x, need_dw=False,
+                                   need_db=False, check=True)[0]):
+        short = (got.double() - want) / want
+        assert float(short.abs().max()) <= ref.ROUND[torch.float16] + worst
+        assert abs(float(short.mean())) <= worst + mean
+
+
+def test_long_sum_over_tokens_is_not_short(uz):
+    """The same for the gradient of a loss over 2^17 tokens that all have class
+    0: every other class's row is a sum of one sign.  The softmax gradient's
+    rounding to fp16 has no direction either."""
+    t, v, d = 1 << 17, 64, 64
+    g = _gen(37)
+    h = (torch.rand(t, d, generator=g, device="cuda") + 0.5).half()
+    w = _rand(g, (v, d), torch.float16, 0.05)
+    targets = torch.zeros(t, dtype=torch.int64, device="cuda")
+    _, lse = uz.cross_entropy(h, w, targets)
+    dw = uz.cross_entropy_backward(torch.full((t,), 1.0 / 1024, device="cuda"), h, w, targets, lse, need_dh=False, check=True)[1]
+    p = torch.softmax(h.double() @ w.double().T, 1)
+    want = (p.T @ h.double() / 1024)[1:]
+    short = (dw[1:].double() - want) / want
+    assert float(short.abs().max()) <= 2 * ref.ROUND[torch.float16] + 2.0 ** -12 + 2.0 ** -18
+    assert abs(float(short.mean())) <= 2.0 ** -12 + 2.0 ** -18 + 2.0 ** -15
