@@ -13,8 +13,7 @@
  *   - Values are bf16 or fp16 (UZIP_BF16, UZIP_FP16), products are summed in
  *     32 bits and every result is rounded once; losses are fp32.  (The tensor
  *     cores cut their additions toward zero: a sum of one sign comes out short
- *     by up to 1e-4 of itself at 16384 terms, and at any number of terms above
- *     that.)  Another dtype is UZIP_ERR_UNSUPPORTED_DTYPE.
+ *     by 1e-4 of itself at 16384 terms and by 1.3e-4 at 2^20.)  Another dtype is UZIP_ERR_UNSUPPORTED_DTYPE.
  *   - Matrices are row-major with a row stride `ld` in elements, at least the
  *     row's length (a matrix of at most one row may give any).  Any element
  *     alignment and any stride are accepted; operands whose rows do not start

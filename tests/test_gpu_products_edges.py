@@ -221,3 +221,133 @@ def test_long_sum_over_tokens_is_not_short(uz):
     short = (dw[1:].double() - want) / want
     assert float(short.abs().max()) <= 2 * ref.ROUND[torch.float16] + 2.0 ** -12 + 2.0 ** -18
     assert abs(float(short.mean())) <= 2.0 ** -12 + 2.0 ** -18 + 2.0 ** -15
+
+
+# ---- tokens by the thousand --------------------------------------------------------
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("t", [1023, 1024, 1025, 2049, 5000])
+def test_cross_entropy_of_thousands_of_tokens(uz, t, dtype):
+    """Tokens are counted 1024 at a time: some thousands with runs of ignored
+    ones longer than that, at the start, in the middle or at the end."""
+    v, d = 300, 72
+    g = _gen(t)
+    h, w = _rand(g, (t, d), dtype), _rand(g, (v, d), dtype, 2 * d ** -0.5)
+    dloss = 0.5 + torch.rand(t, generator=g, device="cuda")
+    base = torch.randint(0, v, (t,), generator=g, device="cuda")
+    base[torch.rand(t, generator=g, device="cuda") < 0.3] = -100
+    for gone in (slice(0, 0), slice(0, t // 2), slice(t // 4, t // 4 + 1100), slice(t // 2, t)):
+        targets = base.clone()
+        targets[gone] = -100
+        loss, lse = uz.cross_entropy(h, w, targets, check=True)
+        want, want_lse, off = ref.loss64(h, w, targets)
+        assert ref.within(loss, want, off) <= 1.0 and ref.within(lse, want_lse, off) <= 1.0
+        assert bool((loss[targets == -100] == 0).all())
+        got = uz.cross_entropy_backward(dloss, h, w, targets, lse, check=True)
+        for a, (r, bound) in zip(got, ref.loss_grad64(h, w, targets, dloss)):
+            assert ref.within(a, r, bound) <= 1.0
+        assert bool((got[0][targets == -100] == 0).all())
+
+
+@pytest.mark.parametrize("drop", [0.0, 0.3])
+def test_cross_entropy_of_half_a_million_tokens(uz, drop):
+    """More tokens than a block lists at once before it copies their rows: each
+    token's loss and dh, and dw, against 64 bits."""
+    t, v, d = 700_001, 24, 16
+    g = _gen(38)
+    h, w = _rand(g, (t, d), torch.float16), _rand(g, (v, d), torch.float16, 2 * d ** -0.5)
+    dloss = 0.5 + torch.rand(t, generator=g, device="cuda")
+    targets = torch.randint(0, v, (t,), generator=g, device="cuda")
+    targets[torch.rand(t, generator=g, device="cuda") < drop] = -100
+    loss, lse = uz.cross_entropy(h, w, targets, check=True)
+    want, want_lse, off = ref.loss64(h, w, targets)
+    assert ref.within(loss, want, off) <= 1.0 and ref.within(lse, want_lse, off) <= 1.0
+    for a, (r, bound) in zip(uz.cross_entropy_backward(dloss, h, w, targets, lse, check=True), ref.loss_grad64(h, w, targets, dloss)):
+        assert ref.within(a, r, bound) <= 1.0
+
+
+# ---- graphs and threads ------------------------------------------------------------
+
+def test_calls_of_many_launches_in_a_graph(uz):
+    """Calls that pack, multiply several times and join, captured and replayed on
+    other values: the same bits as the calls themselves."""
+    g = _gen(39)
+    m, k, n, e, v = 300, 201, 261, 5, 1003
+    off = torch.tensor([0, 40, 40, 170, 171, m], device="cuda")
+    x, w, we, b, be = (_rand(g, s, torch.bfloat16, 0.2) for s in ((m, k), (n, k), (e, n, k), (n,), (e, n)))
+    dy, head = _rand(g, (m, n), torch.bfloat16), _rand(g, (v, k), torch.bfloat16, 0.2)
+    targets = torch.randint(0, v, (m,), generator=g, device="cuda")
+    targets[::5] = -100
+    dloss = torch.rand(m, generator=g, device="cuda")
+
+    def step():
+        y, z = uz.linear(x, w, b, activation="gelu", residual=dy, save_preact=True)
+        ye, ze = uz.grouped_linear(x, we, off, be, activation="relu", save_preact=True)
+        loss, lse = uz.cross_entropy(x, head, targets)
+        return [y, z, ye, ze, loss, lse, *uz.linear_backward(dy, x, w, z, activation="gelu"),
+                *uz.grouped_linear_backward(dy, x, we, off, ze, activation="relu"),
+                *uz.cross_entropy_backward(dloss, x, head, targets, lse, piece=256)]
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step()
+    for seed in (40, 41, 42):
+        for a in (x, w, we, b, be, dy, head):
+            a.copy_(_rand(_gen(seed), a.shape, a.dtype, 0.2))
+        targets.copy_(targets.roll(7))
+        for o in out:
+            o.fill_(7)
+        graph.replay()
+        graph.replay()  # each replay starts from the other's leavings
+        torch.cuda.synchronize()
+        got = [o.clone() for o in out]
+        assert all(torch.equal(p, q) for p, q in zip(got, step()))
+
+
+def test_calls_from_several_threads(uz):
+    """Threads with streams of their own and sizes in different orders get what
+    one thread gets."""
+    import threading
+
+    g = _gen(43)
+    sizes = [(1, 256, 96), (40, 201, 130), (300, 520, 264), (130, 72, 1003)]
+    data = []
+    for m, k, n in sizes:
+        x, w, dy = (_rand(g, s, torch.float16, 0.2) for s in ((m, k), (n, k), (m, n)))
+        off = torch.tensor([0, m // 3, m], device="cuda")
+        data.append((x, w, dy, torch.stack([w, -w]), off))
+
+    def calls(i):
+        x, w, dy, we, off = data[i]
+        y, z = uz.linear(x, w, activation="silu", save_preact=True)
+        return [y, *uz.linear_backward(dy, x, w, z, activation="silu"), uz.grouped_linear(x, we, off),
+                *uz.grouped_linear_backward(dy, x, we, off)]
+
+    want = [calls(i) for i in range(len(sizes))]
+    torch.cuda.synchronize()
+    faults = []
+
+    def work(first):
+        try:
+            stream = torch.cuda.Stream()
+            with torch.cuda.stream(stream):
+                for turn in range(12):
+                    i = (first + turn) % len(sizes)
+                    got = calls(i)
+                    stream.synchronize()
+                    if not all(torch.equal(a, b) for a, b in zip(got, want[i])):
+                        faults.append((first, turn))
+        except Exception as err:  # a thread's error would be lost
+            faults.append(err)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(4)]
+    for th in threads:
+        th.start()
+    for th in threads:
+        th.join(120)
+    assert not faults and not any(th.is_alive() for th in threads)
