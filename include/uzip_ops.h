@@ -13,7 +13,8 @@
  *   - Values are bf16 or fp16 (UZIP_BF16, UZIP_FP16), products are summed in
  *     32 bits and every result is rounded once; losses are fp32.  (The tensor
  *     cores cut their additions toward zero: a sum of one sign comes out short
- *     by 1e-4 of itself at 16384 terms and by 1.3e-4 at 2^20.)  Another dtype is UZIP_ERR_UNSUPPORTED_DTYPE.
+ *     by 1e-4 of itself at 16384 terms and by 1.3e-4 at 2^20.)  Another dtype
+ *     is UZIP_ERR_UNSUPPORTED_DTYPE.
  *   - Matrices are row-major with a row stride `ld` in elements, at least the
  *     row's length (a matrix of at most one row may give any).  Any element
  *     alignment and any stride are accepted; operands whose rows do not start
@@ -86,8 +87,8 @@ uzip_status uzip_grouped_linear(const uzip_linear_args* a, void* d_workspace, ui
  * rounded to the dtype for the two products (tensor cores take 16-bit
  * operands); db sums it unrounded.  z is what uzip_linear stored: values that
  * relu's slope turns on were summed again there where the tensor core's sum
- * came within its own error of zero, and a positive one of those that fp16
- * cannot hold is stored as its smallest value. */
+ * came within its own error of zero, and a positive one that the dtype cannot
+ * hold is stored as its smallest value. */
 typedef struct {
     int32_t dtype;
     int32_t act;

@@ -451,31 +451,40 @@ struct Patch {
     __device__ __forceinline__ uint16_t& value(uint32_t row, uint32_t col) const {
         return reinterpret_cast<uint16_t*>(&at(row, col / 8))[col % 8];
     }
+    // A value kept for relu's slope keeps its sign: a positive one that the type
+    // cannot hold is kept as its smallest.
+    template <bool KEPT>
+    static __device__ __forceinline__ float kept(float v, float smallest) { return KEPT && v > 0.f ? fmaxf(v, smallest) : v; }
     // this lane's row, rounded
+    template <bool KEPT = false>
     __device__ __forceinline__ void put(const float v[32], int dtype) const {
+        const auto two = [&](uint32_t i, int type, float smallest) {
+            return to16x2(kept<KEPT>(v[i], smallest), kept<KEPT>(v[i + 1], smallest), type);
+        };
         __syncwarp();
         if (dtype == UZIP_BF16) {
 #pragma unroll
             for (uint32_t i = 0; i < 4; ++i)
-                at(lane, i) = make_uint4(to16x2(v[8 * i], v[8 * i + 1], UZIP_BF16), to16x2(v[8 * i + 2], v[8 * i + 3], UZIP_BF16),
-                                         to16x2(v[8 * i + 4], v[8 * i + 5], UZIP_BF16), to16x2(v[8 * i + 6], v[8 * i + 7], UZIP_BF16));
+                at(lane, i) = make_uint4(two(8 * i, UZIP_BF16, 0x1p-133f), two(8 * i + 2, UZIP_BF16, 0x1p-133f),
+                                         two(8 * i + 4, UZIP_BF16, 0x1p-133f), two(8 * i + 6, UZIP_BF16, 0x1p-133f));
         } else {
 #pragma unroll
             for (uint32_t i = 0; i < 4; ++i)
-                at(lane, i) = make_uint4(to16x2(v[8 * i], v[8 * i + 1], UZIP_FP16), to16x2(v[8 * i + 2], v[8 * i + 3], UZIP_FP16),
-                                         to16x2(v[8 * i + 4], v[8 * i + 5], UZIP_FP16), to16x2(v[8 * i + 6], v[8 * i + 7], UZIP_FP16));
+                at(lane, i) = make_uint4(two(8 * i, UZIP_FP16, 0x1p-24f), two(8 * i + 2, UZIP_FP16, 0x1p-24f),
+                                         two(8 * i + 4, UZIP_FP16, 0x1p-24f), two(8 * i + 6, UZIP_FP16, 0x1p-24f));
         }
         __syncwarp();
     }
     // one value for each of the 32 rows, in this lane's column, rounded
+    template <bool KEPT = false>
     __device__ __forceinline__ void put_column(const float v[32], int dtype) const {
         __syncwarp();
         if (dtype == UZIP_BF16) {
 #pragma unroll
-            for (uint32_t i = 0; i < 32; ++i) value(i, lane) = to16(v[i], UZIP_BF16);
+            for (uint32_t i = 0; i < 32; ++i) value(i, lane) = to16(kept<KEPT>(v[i], 0x1p-133f), UZIP_BF16);
         } else {
 #pragma unroll
-            for (uint32_t i = 0; i < 32; ++i) value(i, lane) = to16(v[i], UZIP_FP16);
+            for (uint32_t i = 0; i < 32; ++i) value(i, lane) = to16(kept<KEPT>(v[i], 0x1p-24f), UZIP_FP16);
         }
         __syncwarp();
     }
@@ -576,9 +585,9 @@ __device__ __noinline__ float dot_again(const Product& p, uint32_t ga, uint32_t 
 // is summed again, as good as exactly.  Wrong signs of 690 million values at 520
 // to 32768 depths: 17 with half that distance, none with it (32-bit sums: 5 in
 // 180 million at 520).  4096 x 4096 x 4096 takes 90 us instead of 83, 2048 x
-// 14336 x 4096 200 instead of 137.  A positive value too small for fp16 is kept
-// as its smallest.  v[i] are the lane's 32 values, `count` of them real; at most
-// kMended of a patch, so that no input can make this the kernel's work.
+// 14336 x 4096 200 instead of 137.  v[i] are the lane's 32 values, `count` of
+// them real; at most kMended of a patch, so that no input can make this the
+// kernel's work.
 constexpr uint32_t kMended = 16;
 template <typename Again>
 __device__ __forceinline__ void mend_near_zero(const Product& p, float v[32], uint32_t count, bool live, uint32_t lane, Again again) {
@@ -605,8 +614,7 @@ __device__ __forceinline__ void mend_near_zero(const Product& p, float v[32], ui
     uint32_t lanes = __ballot_sync(0xFFFFFFFFu, close);
     for (uint32_t left = kMended; lanes && left; --left) {
         const uint32_t from = __ffs(lanes) - 1, at = __ffs(__shfl_sync(0xFFFFFFFFu, close, from)) - 1;
-        float mended = again(from, at);
-        if (mended > 0.f && p.dtype == UZIP_FP16) mended = fmaxf(mended, 0x1p-24f);
+        const float mended = again(from, at);
         if (lane == from) {
             close &= close - 1;
 #pragma unroll
@@ -644,7 +652,8 @@ __device__ __forceinline__ void finish_transposed(const Product& p, const Tiling
                 return dot_again(p, o.group, 0, feature0 + from, o.col0 + c + at, b, lane);
             });
         if (z) {
-            patch.put_column(v, dtype);
+            if (FORWARD && e.act == UZIP_ACT_RELU) patch.put_column<true>(v, dtype);
+            else patch.put_column(v, dtype);
             patch.store(z + uint64_t(c) * e.ldz, e.ldz, tokens, features, t.z_width);
         }
         if (e.act == UZIP_ACT_RELU) {
@@ -768,7 +777,8 @@ __device__ __forceinline__ void finish_tile(const Product& p, const Tiling& t, c
                     return dot_again(p, 0, o.group, row0 + from, uint64_t(o.col0) + c + at, b, lane);
                 });
             if (z) {
-                patch.put(v, dtype);
+                if (FORWARD && act == UZIP_ACT_RELU) patch.put<true>(v, dtype);
+                else patch.put(v, dtype);
                 patch.store(z + c, e.ldz, rows, here, t.z_width);
             }
             if (act == UZIP_ACT_RELU) {

@@ -351,3 +351,31 @@ def test_calls_from_several_threads(uz):
     for th in threads:
         th.join(120)
     assert not faults and not any(th.is_alive() for th in threads)
+
+
+# ---- the ends of the types' ranges -------------------------------------------------
+
+@pytest.mark.parametrize("grouped", [False, True])
+def test_relu_keeps_signs_below_the_types_range(uz, grouped):
+    """Values that fp16 rounds to zero still have their sign in what is kept, and
+    so their gradient; the result itself is rounded as ever (half of 2^-24)."""
+    g = _gen(44)
+    m, k, n = 200, 96, 264
+    x, w, dy = _rand(g, (m, k), torch.float16, 2.0 ** -14), _rand(g, (2, n, k), torch.float16, 2.0 ** -18), _rand(g, (m, n), torch.float16)
+    if grouped:
+        off = torch.tensor([0, 30, m], device="cuda")
+        y, z = uz.grouped_linear(x, w, off, activation="relu", save_preact=True)
+        dx, _, db = uz.grouped_linear_backward(dy, x, w, off, z, activation="relu")
+        rows = [(slice(0, 30), 0), (slice(30, m), 1)]
+    else:
+        y, z = uz.linear(x, w[0], activation="relu", save_preact=True)
+        dx, _, db = uz.linear_backward(dy, x, w[0], z, activation="relu")
+        rows, db = [(slice(0, m), 0)], db[None]
+    for r, i in rows:
+        z64 = x[r].double() @ w[i].double().T
+        assert float(z64.abs().max()) < 2.0 ** -25 and bool((z64 != 0).all())
+        assert torch.equal(z[r] > 0, z64 > 0)
+        assert float((y[r].double() - z64.clamp(min=0)).abs().max()) <= 2.0 ** -25
+        dz = dy[r].double() * (z64 > 0)
+        want, mag = dz.sum(0), dz.abs().sum(0)
+        assert ref.within(db[i], want, ref.ROUND[torch.float16] * want.abs() + (m + 4) * 2.0 ** -22 * mag + 2.0 ** -24) <= 1.0
