@@ -234,7 +234,7 @@ __device__ __forceinline__ float act_slope(float z, uint32_t act) {
         }
         case UZIP_ACT_SILU: {
             const float q = fast_reciprocal(1.f + fast_exp2(-z * kLog2e));
-            return q * (1.f + z * (1.f - q));
+            return fabsf(z) > 200.f ? q : q * (1.f + z * (1.f - q));  // (0 or 1 out there, where a kept z may be infinite)
         }
         default: return 1.f;
     }

@@ -379,3 +379,26 @@ def test_relu_keeps_signs_below_the_types_range(uz, grouped):
         dz = dy[r].double() * (z64 > 0)
         want, mag = dz.sum(0), dz.abs().sum(0)
         assert ref.within(db[i], want, ref.ROUND[torch.float16] * want.abs() + (m + 4) * 2.0 ** -22 * mag + 2.0 ** -24) <= 1.0
+
+
+@pytest.mark.parametrize("act", ("relu", "gelu", "silu"))
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_gradients_where_the_kept_value_is_infinite(uz, dtype, act):
+    """A value past the type's range is kept as infinity: the slope there is 1
+    or 0, as it is next to it.  One that is not a number stays one."""
+    inf = float("inf")
+    z = torch.tensor([[-inf, inf, 1.0, float("nan"), -inf, 0.5, inf, -2.0]], device="cuda").to(dtype)
+    for n in (8, 5):  # 16-byte rows, and others
+        dy, x, w = (torch.ones(s, device="cuda", dtype=dtype) for s in ((1, n), (1, 3), (n, 3)))
+        _, dw, db = uz.linear_backward(dy, x, w, z[:, :n].contiguous(), activation=act)
+        for got in (db, dw[:, 0]):
+            assert got[0] == 0 and got[1] == 1 and got[4] == 0 and bool(torch.isnan(got[3]))
+            assert bool(torch.isfinite(got[[2, 0, 1, 4]]).all())
+
+
+def test_silu_gradient_of_a_value_that_overflows_fp16(uz):
+    x, w = torch.full((2, 1), 300.0, device="cuda").half(), torch.tensor([[-300.0], [0.01]], device="cuda").half()
+    y, z = uz.linear(x, w, activation="silu", save_preact=True)
+    assert bool((y[:, 0] == 0).all()) and bool(torch.isinf(z[:, 0]).all())
+    dx, dw, db = uz.linear_backward(torch.ones_like(y), x, w, z, activation="silu")
+    assert float(db[0]) == 0 and float(dw[0]) == 0 and bool(torch.isfinite(dx).all())
