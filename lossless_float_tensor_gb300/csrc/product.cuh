@@ -199,17 +199,21 @@ __device__ __forceinline__ float fast_reciprocal(float v) {
     return r;
 }
 
-// 1 - Phi(|z|) exp(z^2 / 2) by the rational approximation 7.1.26 of Abramowitz
-// and Stegun, Handbook of Mathematical Functions: erfc(x) = (a1 t + ... + a5
-// t^5) exp(-x^2), t = 1 / (1 + 0.3275911 x), off by less than 1.5e-7 (a unit
-// in the last place of a value near one), in 14 instructions a value with the
-// exponential.
+// (1 - Phi(a)) exp(a^2 / 2) for a >= 0, as t P(t) with t = 1 / (1 + 0.305 a): t
+// takes [0, inf) to (0, 1], where the function over t is smooth.  P is of degree
+// 7, fitted to erfcx in 64 bits for the smallest relative error over [0, 14]
+// (least squares, reweighted until the extremes are level): 9.4e-8, and 4e-7 as
+// computed here, so gelu's negative tail keeps the type's precision however
+// small it gets (to 9e-6 of itself at z = -12, from the exponential's argument).
 __device__ __forceinline__ float gauss_tail(float a) {
-    const float t = fast_reciprocal(fmaf(0.3275911f * kSqrtHalf, a, 1.f));
-    float s = fmaf(0.5f * 1.061405429f, t, 0.5f * -1.453152027f);
-    s = fmaf(s, t, 0.5f * 1.421413741f);
-    s = fmaf(s, t, 0.5f * -0.284496736f);
-    s = fmaf(s, t, 0.5f * 0.254829592f);
+    const float t = fast_reciprocal(fmaf(0.305000007f, a, 1.f));
+    float s = fmaf(0.0366987698f, t, -0.152986616f);
+    s = fmaf(s, t, 0.185714051f);
+    s = fmaf(s, t, -0.0379742719f);
+    s = fmaf(s, t, 0.121020354f);
+    s = fmaf(s, t, 0.103421263f);
+    s = fmaf(s, t, 0.122466758f);
+    s = fmaf(s, t, 0.121639736f);
     return s * t;
 }
 

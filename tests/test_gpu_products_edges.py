@@ -402,3 +402,33 @@ def test_silu_gradient_of_a_value_that_overflows_fp16(uz):
     assert bool((y[:, 0] == 0).all()) and bool(torch.isinf(z[:, 0]).all())
     dx, dw, db = uz.linear_backward(torch.ones_like(y), x, w, z, activation="silu")
     assert float(db[0]) == 0 and float(dw[0]) == 0 and bool(torch.isfinite(dx).all())
+
+
+# ---- the tails of the activations --------------------------------------------------
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_gelu_keeps_its_precision_in_the_tail(uz, dtype):
+    """gelu and its slope for z from -12 to -2, relative to themselves: one
+    rounding, the exponential's argument (up to 104, rounded twice: 104 2^-23
+    ln 2 = 9e-6) and the fitted tail (1e-6), below 2^-16 together.  In the slope
+    Phi(z) - |z| phi(z) the errors are up to 1.6 times the difference's own."""
+    z = torch.linspace(-12, -2, 4001, device="cuda").to(dtype).unique()
+    one = torch.ones(1, 1, device="cuda", dtype=dtype)
+    y = uz.linear(one, z[:, None], activation="gelu")[0].double()
+    want = ref.act64(z.double(), "gelu")
+    u, tiny = ref.ROUND[dtype], ref.TINY[dtype]
+    assert float(((y - want).abs() / ((u + 2.0 ** -16) * want.abs() + tiny)).max()) <= 1.0
+    dx, _, db = uz.linear_backward(torch.ones(1, z.numel(), device="cuda", dtype=dtype), one, z[:, None], z[None], activation="gelu")
+    want = ref.slope64(z.double(), "gelu")
+    assert float(((db.double() - want).abs() / ((u + 2.0 ** -15) * want.abs() + tiny)).max()) <= 1.0
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_silu_keeps_its_precision_in_the_tail(uz, dtype):
+    """The same for silu from -80 to -2: exp(-z)'s argument is up to 116, rounded
+    twice (1e-5), below 2^-16 with the reciprocal."""
+    z = torch.linspace(-80, -2, 4001, device="cuda").to(dtype).unique()
+    one = torch.ones(1, 1, device="cuda", dtype=dtype)
+    y = uz.linear(one, z[:, None], activation="silu")[0].double()
+    want = ref.act64(z.double(), "silu")
+    assert float(((y - want).abs() / ((ref.ROUND[dtype] + 2.0 ** -16) * want.abs() + ref.TINY[dtype])).max()) <= 1.0
