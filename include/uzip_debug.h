@@ -37,6 +37,11 @@ int uzip_debug_model_counts(int dtype, double sigma, uint32_t* counts);
  * and the L2 working set only, never the output. */
 void uzip_debug_set_ws_jit_blocks(uint32_t blocks);
 
+/* Products launched while wait_cycles is not 0 never fetch their first operand:
+ * every wait for it runs out after that many clock cycles instead of four
+ * seconds' worth.  0 (the default) ends that. */
+void uzip_debug_starve_products(int64_t wait_cycles);
+
 /* Byte offset of the compressor's work area inside the output buffer (the
  * area is 16 + 8*C bytes long and follows the largest possible container). */
 uint64_t uzip_debug_scratch_offset(uzip_dtype dtype, uint64_t n);

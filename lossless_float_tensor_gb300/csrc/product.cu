@@ -27,6 +27,7 @@
 #include <cmath>
 #include <type_traits>
 
+#include "../../include/uzip_debug.h"
 #include "product.cuh"
 
 namespace uzip {
@@ -59,7 +60,7 @@ constexpr uint32_t kPatchBytes = 32 * kPatchCols * 2, kEpilogueBytes = kPatchByt
 constexpr uint32_t kMaxSplits = 8;  // blocks of a portable cluster
 constexpr uint32_t kHeights = 6;    // boxes of 1 to 32 lines for depths that are cut
 constexpr int64_t kWaitLimit = 8000000000;  // clock cycles: a wait gives up after about four seconds,
-constexpr int64_t kDrainLimit = 100000000;  // one for copies or products in flight then after 50 ms
+constexpr int64_t kDrainLimit = 100000000;  // one for products in flight then after 50 ms
 
 struct Tiling {
     uint32_t bn;       // columns of a tile
@@ -76,6 +77,8 @@ struct Tiling {
     uint32_t smem;
     uint32_t out_width, z_width;  // values that rows of 16-bit results are aligned to: 8, 4, 2 or 1
     uint32_t vec;      // bit flags: 16-byte access to out 1, bias 2, residual 4, z 8, sums 16
+    uint32_t starve;   // tests: A is never fetched, so that every wait for it runs out
+    int64_t wait_limit;
 };
 
 // ---- PTX ------------------------------------------------------------------------
@@ -223,6 +226,7 @@ struct Control {
     uint64_t full[kMaxStages], empty[kMaxStages];
     uint64_t acc_full[2], acc_empty[2];
     uint64_t drain;
+    int64_t wait_limit;
     uint32_t tmem;
     volatile uint32_t abort;
 };
@@ -232,23 +236,31 @@ struct Control {
 // A wait that is not over at its first try goes on outside the loops of the
 // fetching and multiplying threads, whose code the epilogue's warps push out of
 // the instruction cache: each line less is felt there.
-__device__ __noinline__ bool wait_on(volatile uint32_t* abort, uint32_t bar, uint32_t parity) {
+__device__ __noinline__ bool wait_on(Control* c, uint32_t bar, uint32_t parity) {
     const int64_t start = clock64();
     do {
         for (uint32_t i = 0; i < 64; ++i)
             if (try_wait(bar, parity)) return true;
-        if (*abort) return false;
-    } while (clock64() - start < kWaitLimit);
-    *abort = 1;
+        if (c->abort) return false;
+    } while (clock64() - start < c->wait_limit);
+    c->abort = 1;
     return false;
 }
 __device__ __forceinline__ bool wait(Control* c, uint32_t bar, uint32_t parity) {
-    return try_wait(bar, parity) || wait_on(&c->abort, bar, parity);
+    return try_wait(bar, parity) || wait_on(c, bar, parity);
 }
 __device__ __forceinline__ void drain(uint64_t* bar, uint32_t parity) {
     const int64_t start = clock64();
     while (!try_wait(smem_u32(bar), parity) && clock64() - start < kDrainLimit) {
     }
+}
+// A block that has given up lets the copies in flight land before it ends: the
+// two fetching threads of its own, and of its pair, may each have got to another
+// stage, whose barriers then never complete, so it waits for longer than any copy
+// takes (microseconds) instead.
+__device__ __noinline__ void settle() {
+    const int64_t start = clock64();
+    while (clock64() - start < kDrainLimit) __nanosleep(1000);
 }
 
 // The next stage of the ring and the parity of its use.
@@ -852,6 +864,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         mbar_init(smem_u32(&ctl->drain), 1);
         ctl->abort = 0;
+        ctl->wait_limit = t.wait_limit;
         fence_mbar_init();
     }
     wait_for_launch_before();
@@ -965,16 +978,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
         }
-        // copies in flight (a pair's: both blocks') land before the block ends
-        if (ctl->abort && rank == 0 && IS_A)
-            for (uint32_t i = 0; i < min(ring.used, t.stages); ++i) {
-                const uint32_t back = ring.s > i ? ring.s - 1 - i : ring.s + t.stages - 1 - i;
-                drain(&ctl->full[back], ring.s > i ? ring.phase : ring.phase ^ 1);
-            }
     };
 
     if (warp == 0) {
-        if (elect_one()) fetch(std::true_type{});
+        if (elect_one() && !t.starve) fetch(std::true_type{});
         __syncwarp();
     } else if (warp == 6) {
         if (elect_one()) fetch(std::false_type{});
@@ -1203,6 +1210,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     tmem_fence_before();
     __syncthreads();
+    if (ctl->abort) settle();
     if (PAIR) cluster_sync();  // no arrival reaches a block that has ended
     tmem_fence_after();
     if (warp == 1) tmem_free<PAIR>(tmem, t.tmem_cols);
@@ -1258,6 +1266,7 @@ uint32_t row_width(const void* p, uint64_t ld) {
 bool aligned16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
 
 constexpr uint32_t kSmemMost = 227 * 1024;
+std::atomic<int64_t> g_starved_wait{0};  // clock cycles (uzip_debug_starve_products)
 
 bool cut(const Product& p) { return p.schedule == kDepth || p.live_depth; }  // the depths end where the device says
 uint64_t col_tiles_of(const Product& p, uint32_t bn) {
@@ -1429,6 +1438,9 @@ Choice choose(const Product& p, int sms) {
     t.vec = (aligned16(e.out) && e.ldo % out_unit == 0 && e.out_group % out_unit == 0 ? 1 : 0) |
             (aligned16(e.bias) && (p.n % 8 == 0 || p.groups == 1) ? 2 : 0) | (aligned16(e.residual) && e.ldr % 8 == 0 ? 4 : 0) |
             (aligned16(e.z) && e.ldz % 8 == 0 ? 8 : 0) | (aligned16(e.sum_in) && e.ld_sum % 4 == 0 ? 16 : 0);
+    const int64_t starved = g_starved_wait.load(std::memory_order_relaxed);
+    t.starve = starved != 0;
+    t.wait_limit = starved ? starved : kWaitLimit;
     return Choice{t, slot->cost};
 }
 
@@ -1546,3 +1558,5 @@ cudaError_t launch_product(const Product& p, int sms, cudaStream_t s) {
 }
 
 }  // namespace uzip
+
+extern "C" void uzip_debug_starve_products(int64_t wait_cycles) { uzip::g_starved_wait = wait_cycles; }

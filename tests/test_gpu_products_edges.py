@@ -432,3 +432,37 @@ def test_silu_keeps_its_precision_in_the_tail(uz, dtype):
     y = uz.linear(one, z[:, None], activation="silu")[0].double()
     want = ref.act64(z.double(), "silu")
     assert float(((y - want).abs() / ((ref.ROUND[dtype] + 2.0 ** -16) * want.abs() + ref.TINY[dtype])).max()) <= 1.0
+
+
+# ---- waits that run out ------------------------------------------------------------
+
+STARVED = [(1, 4096, 1024), (20, 9000, 130), (300, 520, 264), (1100, 300, 4200), (640, 16400, 513)]
+
+
+def _starved(uz, call):
+    """What call() gives while no product gets its first operand, its waits 50
+    ms long, and the status that it reports."""
+    import ctypes
+
+    hook = uz.library().uzip_debug_starve_products
+    hook.argtypes, hook.restype = [ctypes.c_int64], None
+    status = torch.full((), -1, dtype=torch.int32, device="cuda")
+    hook(100_000_000)
+    try:
+        out = call(status)
+    finally:
+        hook(0)
+    torch.cuda.synchronize()
+    return out, int(status.item())
+
+
+@pytest.mark.parametrize("m,k,n", STARVED)
+def test_waits_that_run_out_are_reported(uz, m, k, n):
+    """Single blocks, pairs and clusters of both give up, and the next call is
+    as good as ever."""
+    g = _gen(45)
+    x, w = _whole(g, (m, k), torch.bfloat16, 1, 8.0 / k), _whole(g, (n, k), torch.bfloat16, 1)
+    assert _starved(uz, lambda s: uz.linear(x, w, status=s))[1] == uz.UZIP_ERR_TIMEOUT
+    with pytest.raises(uz.UzipError, match="time"):
+        _starved(uz, lambda s: uz.linear(x, w, check=True))
+    _same(uz.linear(x, w, check=True), x.double() @ w.double().T, torch.bfloat16)
