@@ -27,8 +27,8 @@
  *   - Outputs must not overlap inputs or each other.
  *   - d_status (device i32, nullable) receives 0, or a uzip_status found on
  *     the device: UZIP_ERR_INVALID_ARG for bad offsets or targets (see
- *     there), UZIP_ERR_TIMEOUT when a bounded wait ran out (the outputs are
- *     then undefined).
+ *     there), UZIP_ERR_TIMEOUT when a bounded wait ran out (what was to be
+ *     computed there is then NaN).
  *   - The same inputs give the same bits: no sum depends on the order in
  *     which blocks run.
  */

@@ -829,6 +829,37 @@ __device__ __forceinline__ void finish_tile(const Product& p, const Tiling& t, c
     __syncwarp();
 }
 
+// What a block that has given up a wait was to write becomes NaN (a caller that
+// gave no status word would not learn of it otherwise).  The next products and
+// the loss carry it on.
+template <int EPI, bool TURNED>
+__device__ __noinline__ void leave_nan(const Product& p, Walk walk, uint32_t rank) {
+    const uint16_t nan = p.dtype == UZIP_BF16 ? 0x7FC0 : 0x7E00;
+    const StoreEpilogue& e = p.st;
+    Tile o;
+    while (walk.take(o)) {
+        const uint64_t row0 = uint64_t(o.row0) + rank * kRowsTile;
+        const uint32_t rows = row0 < o.row_end ? uint32_t(min(uint64_t(kRowsTile), o.row_end - row0)) : 0;
+        for (uint32_t i = threadIdx.x; i < rows * o.cols; i += kThreads) {
+            uint64_t row = row0 + i / o.cols, col = uint64_t(o.col0) + i % o.cols;
+            if (EPI == kLossStats) {
+                if (i % o.cols % kStatsCols == 0) p.ls.part[row * p.ls.tiles + col / kStatsCols] = make_float2(0.f, NAN);
+            } else if (EPI == kLossGrad) {
+                static_cast<uint16_t*>(p.ls.out)[row * p.ls.ldo + col] = nan;
+            } else {
+                if (TURNED) {
+                    const uint64_t r = row;
+                    row = col, col = r;
+                }
+                const uint64_t at = o.group * e.out_group + row * e.ldo + col;
+                if (e.out_fp32) static_cast<float*>(e.out)[at] = NAN;
+                else static_cast<uint16_t*>(e.out)[at] = nan;
+                if (e.z) static_cast<uint16_t*>(e.z)[row * e.ldz + col] = nan;
+            }
+        }
+    }
+}
+
 // ---- the kernel -------------------------------------------------------------------------
 
 // MODE: 0 a block by itself, 1 a cluster of blocks splits the depth, 2 a pair of
@@ -1030,6 +1061,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (!CUT || steps > 3) mma<PAIR>(acc, a + 3 * kStepA, b + 3 * kStepB, shape, 1);
                         mma_commit<PAIR>(empty + 8 * ring.s, leader);
                     }
+                    if (!ok) break;  // not finished: the epilogues give up too, those of the pair's other block among them
                     mma_commit<PAIR>(smem_u32(&ctl->acc_full[buf]), leader);
                 }
             }
@@ -1210,7 +1242,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     tmem_fence_before();
     __syncthreads();
-    if (ctl->abort) settle();
+    if (ctl->abort) {
+        settle();
+        leave_nan<EPI, TURNED>(p, Walk(p, t, offsets, first, live_rows, live_depth), rank);
+    }
     if (PAIR) cluster_sync();  // no arrival reaches a block that has ended
     tmem_fence_after();
     if (warp == 1) tmem_free<PAIR>(tmem, t.tmem_cols);

@@ -466,3 +466,37 @@ def test_waits_that_run_out_are_reported(uz, m, k, n):
     with pytest.raises(uz.UzipError, match="time"):
         _starved(uz, lambda s: uz.linear(x, w, check=True))
     _same(uz.linear(x, w, check=True), x.double() @ w.double().T, torch.bfloat16)
+
+
+@pytest.mark.parametrize("m,k,n", STARVED)
+def test_waits_that_run_out_leave_nan(uz, m, k, n):
+    """What could not be computed is NaN also for a caller who asks for no
+    status, in every output and schedule."""
+    g = _gen(46)
+    x, w, dy = (_rand(g, s, torch.float16, 0.2) for s in ((m, k), (n, k), (m, n)))
+    off = torch.tensor([0, m // 3, m // 3, m], device="cuda")
+    we = torch.stack([w, w, w])
+    calls = [lambda s: uz.linear(x, w, activation="relu", save_preact=True), lambda s: [uz.linear(x, w)],
+             lambda s: uz.linear_backward(dy, x, w, need_db=False)[:2],
+             lambda s: uz.grouped_linear(x, we, off, activation="gelu", save_preact=True),
+             lambda s: [uz.grouped_linear_backward(dy, x, we, off, need_dw=False, need_db=False)[0]],
+             # (the expert in the middle has no rows: nothing of its is waited for)
+             lambda s: list(uz.grouped_linear_backward(dy, x, we, off, need_dx=False, need_db=False)[1][(2 if m < 3 else 0)::2])]
+    for call in calls:
+        for t in _starved(uz, call)[0]:
+            assert bool(torch.isnan(t).all())
+
+
+def test_waits_that_run_out_leave_nan_losses(uz):
+    g = _gen(47)
+    for t in (20, 300):
+        h, w = _rand(g, (t, 200), torch.bfloat16), _rand(g, (1003, 200), torch.bfloat16, 0.2)
+        targets = torch.randint(0, 1003, (t,), generator=g, device="cuda")
+        targets[3] = -100
+        _, lse = uz.cross_entropy(h, w, targets)
+        (loss, bad), _ = _starved(uz, lambda s: uz.cross_entropy(h, w, targets, status=s))
+        used = targets != -100
+        assert bool(torch.isnan(loss[used]).all() & torch.isnan(bad[used]).all() & (loss[~used] == 0).all())
+        (dh, dw), _ = _starved(uz, lambda s: uz.cross_entropy_backward(torch.ones(t, device="cuda"), h, w, targets, lse, piece=256))
+        assert bool(torch.isnan(dh[used]).all() & torch.isnan(dw).all() & (dh[~used] == 0).all())
+        assert bool(torch.isfinite(uz.cross_entropy(h, w, targets, check=True)[0]).all())
