@@ -5,6 +5,11 @@ cross entropy over a vocabulary, and their gradients.
 Thin ctypes layer over include/uzip_ops.h: the functions named like the C entry
 points only marshal arguments, and the torch functions allocate outputs and
 workspace and pass the stream.  All arithmetic runs in the library's kernels.
+
+The torch functions are not known to autograd: a training step calls the
+*_backward functions itself.  Tensors that require gradients are refused while
+grad mode is on, since the results would silently have none; torch.no_grad() or
+detach() says that this is meant.
 """
 from __future__ import annotations
 
@@ -140,6 +145,13 @@ def _dtype_code(t) -> int:
     raise UzipError(UZIP_ERR_UNSUPPORTED_DTYPE, f"dtype {t.dtype}")
 
 
+def _outside_autograd(t, name):
+    import torch
+
+    if torch.is_grad_enabled():
+        _refuse(f"{name} requires gradients, which autograd would not get from here: detach it, or call under torch.no_grad()")
+
+
 def _matrix(t, name, shape, like):
     """Data pointer and row stride of a CUDA matrix (or batch of matrices)
     whose rows are contiguous."""
@@ -147,6 +159,8 @@ def _matrix(t, name, shape, like):
         _refuse(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
     if t is not like and (t.dtype != like.dtype or t.get_device() != like.get_device()):
         _refuse(f"{name} is {t.dtype} on {t.device}, expected {like.dtype} on {like.device}")
+    if t.requires_grad:
+        _outside_autograd(t, name)
     *_, ld, step = t.stride()
     rows, cols = shape[-2], shape[-1]
     if step != 1 and cols > 1:
@@ -159,6 +173,8 @@ def _matrix(t, name, shape, like):
 def _vector(t, name, shape, dtype, like):
     if t.shape != shape or t.dtype != dtype or t.get_device() != like.get_device() or not t.is_contiguous():
         _refuse(f"{name}: expected a contiguous {dtype} tensor of shape {tuple(shape)} on {like.device}")
+    if t.requires_grad:
+        _outside_autograd(t, name)
     return t.data_ptr() or None
 
 

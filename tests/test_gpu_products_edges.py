@@ -500,3 +500,28 @@ def test_waits_that_run_out_leave_nan_losses(uz):
         (dh, dw), _ = _starved(uz, lambda s: uz.cross_entropy_backward(torch.ones(t, device="cuda"), h, w, targets, lse, piece=256))
         assert bool(torch.isnan(dh[used]).all() & torch.isnan(dw).all() & (dh[~used] == 0).all())
         assert bool(torch.isfinite(uz.cross_entropy(h, w, targets, check=True)[0]).all())
+
+
+# ---- what the torch functions refuse -----------------------------------------------
+
+def test_tensors_that_require_gradients_are_refused(uz):
+    """Autograd does not know these calls: a result without a gradient would be
+    a silent hole in a training step."""
+    half = lambda *s: torch.ones(*s, device="cuda", dtype=torch.float16)  # noqa: E731
+    x, w, b, y = half(4, 8), half(6, 8), half(6), half(4, 6)
+    targets, off = torch.zeros(4, dtype=torch.int64, device="cuda"), torch.tensor([0, 4], device="cuda")
+    ones = torch.ones(4, device="cuda")
+    leaf = lambda t: t.clone().requires_grad_()  # noqa: E731
+    calls = [lambda f: uz.linear(f(x), w), lambda f: uz.linear(x, f(w)), lambda f: uz.linear(x, w, f(b)),
+             lambda f: uz.linear(x, w, residual=f(y)), lambda f: uz.linear_backward(f(y), x, w),
+             lambda f: uz.linear_backward(y, f(x), f(w)), lambda f: uz.grouped_linear(x, f(w)[None], off),
+             lambda f: uz.grouped_linear(f(x), w[None], off), lambda f: uz.cross_entropy(f(x), w, targets),
+             lambda f: uz.cross_entropy(x, f(w), targets), lambda f: uz.cross_entropy_backward(f(ones), x, w, targets, ones)]
+    for call in calls:
+        with pytest.raises(uz.UzipError, match="requires gradients"):
+            call(leaf)
+        with torch.no_grad():
+            got = call(leaf)
+        want = call(lambda t: t)
+        for p, q in zip(got if isinstance(got, tuple) else [got], want if isinstance(want, tuple) else [want]):
+            assert torch.equal(p, q)
