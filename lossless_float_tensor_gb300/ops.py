@@ -218,12 +218,18 @@ def _run(name, args, device, workspace, status, check):
     size, call = _calls[name]
     ref = _byref(args)
     need = size(ref)
-    if need and workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=device)
-    if check and status is None:
-        status = torch.empty((), dtype=torch.int32, device=device)
+    if workspace is None:
+        if need:
+            workspace = torch.empty(need, dtype=torch.uint8, device=device)
+    elif not workspace.is_contiguous():
+        _refuse("workspace: the values between those of a strided tensor are not its own")
+    if status is None:
+        if check:
+            status = torch.empty((), dtype=torch.int32, device=device)
+    elif status.dtype != torch.int32 or not status.numel():
+        _refuse(f"status: expected an int32 tensor, not {status.dtype} of {status.numel()} values")
     _check(call(ref, workspace.data_ptr() if workspace is not None else None,
-                workspace.numel() if workspace is not None else 0, status.data_ptr() if status is not None else None,
+                workspace.nbytes if workspace is not None else 0, status.data_ptr() if status is not None else None,
                 torch._C._cuda_getCurrentRawStream(device.index)), name)
     if check:
         st = int(status.item())

@@ -525,3 +525,21 @@ def test_tensors_that_require_gradients_are_refused(uz):
         want = call(lambda t: t)
         for p, q in zip(got if isinstance(got, tuple) else [got], want if isinstance(want, tuple) else [want]):
             assert torch.equal(p, q)
+
+
+def test_a_workspace_or_status_that_is_not_one(uz):
+    """A strided workspace would be written between its values, a status word of
+    another type beyond its end; a workspace of wider values has all its bytes."""
+    x, w = torch.ones(9, 33, device="cuda", dtype=torch.float16), torch.ones(50, 33, device="cuda", dtype=torch.float16)
+    wide = torch.zeros(1 << 16, dtype=torch.uint8, device="cuda")
+    with pytest.raises(uz.UzipError, match="workspace"):
+        uz.linear(x, w, workspace=wide[::2])
+    assert not wide.any()
+    words = torch.zeros(8, dtype=torch.uint8, device="cuda")
+    for bad in (words[0], words.view(torch.int64)[0], torch.zeros(4, device="cuda")[0], torch.zeros(0, dtype=torch.int32, device="cuda")):
+        with pytest.raises(uz.UzipError, match="status"):
+            uz.linear(x, w, status=bad)
+    assert not words.any()
+    need = -(-(9 + 50) * 40 * 2 // 256) * 256 + 256
+    y = uz.linear(x, w, workspace=torch.empty(need // 4, dtype=torch.float32, device="cuda"), check=True)
+    assert bool((y == 33).all())
