@@ -161,7 +161,8 @@ cudaError_t launch_loss_join(const LossEpilogue& e, const uint32_t* token, const
 // to[i] = from[place[i]], or zeros where place[i] is ~0
 cudaError_t launch_spread_rows(const void* from, uint64_t ld, const uint32_t* place, void* to, uint64_t ld_to, uint64_t rows,
                                uint64_t cols, cudaStream_t s);
-cudaError_t launch_fill(void* p, uint64_t ld, uint64_t rows, uint64_t cols, uint32_t elem, cudaStream_t s);
+// 16-bit zeros
+cudaError_t launch_clear(void* p, uint64_t ld, uint64_t rows, uint64_t cols, cudaStream_t s);
 
 // ---- arithmetic ---------------------------------------------------------------
 

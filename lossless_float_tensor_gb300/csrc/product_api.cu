@@ -516,7 +516,7 @@ uzip_status uzip_cross_entropy_backward(const uzip_cross_entropy_grad_args* a, v
     if (d_status) err = cudaMemsetAsync(d_status, 0, sizeof(int32_t), s);
     if (err != cudaSuccess) return finish(err);
     if (a->t == 0) {
-        if (a->dw) err = launch_fill(a->dw, a->v > 1 ? a->lddw : a->d, a->v, a->d, 2, s);
+        if (a->dw) err = launch_clear(a->dw, a->v > 1 ? a->lddw : a->d, a->v, a->d, s);
         return finish(err);
     }
     Work work{static_cast<uint8_t*>(d_workspace)};

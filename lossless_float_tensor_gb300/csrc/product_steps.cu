@@ -10,6 +10,7 @@ namespace uzip {
 namespace {
 
 constexpr uint32_t kThreads = 256;
+constexpr uint64_t kSms = 152;  // these steps' grids are sized for a GB300; any other number would do
 
 // A launch whose blocks may be set up while the one before it ends: the kernel starts with wait_for_launch_before().
 template <typename... Args, typename... Given>
@@ -51,11 +52,10 @@ __global__ void __launch_bounds__(kThreads) pack_kernel(const __grid_constant__ 
     }
 }
 
-template <typename T>
-__global__ void __launch_bounds__(kThreads) fill_kernel(T* p, uint64_t ld, uint64_t cols, uint64_t total, T value) {
+__global__ void __launch_bounds__(kThreads) clear_kernel(uint16_t* p, uint64_t ld, uint64_t cols, uint64_t total) {
     wait_for_launch_before();
     for (uint64_t i = blockIdx.x * uint64_t(kThreads) + threadIdx.x; i < total; i += uint64_t(gridDim.x) * kThreads)
-        p[i / cols * ld + i % cols] = value;
+        p[i / cols * ld + i % cols] = 0;
 }
 
 // Block (x, y, z): 128 columns, a share of the rows, one group.  Where rows
@@ -356,16 +356,13 @@ cudaError_t launch_pack(const PackJobs& jobs, cudaStream_t s) {
     for (uint32_t i = 0; i < jobs.count; ++i)
         most = std::max(most, jobs.job[i].ld_to / 8 * jobs.job[i].rows * jobs.job[i].groups);
     if (most == 0) return cudaSuccess;
-    return launch_after(pack_kernel, dim3(blocks_for(most, 152 * 32), jobs.count), kThreads, s, jobs);
+    return launch_after(pack_kernel, dim3(blocks_for(most, kSms * 32), jobs.count), kThreads, s, jobs);
 }
 
-cudaError_t launch_fill(void* p, uint64_t ld, uint64_t rows, uint64_t cols, uint32_t elem, cudaStream_t s) {
+cudaError_t launch_clear(void* p, uint64_t ld, uint64_t rows, uint64_t cols, cudaStream_t s) {
     const uint64_t total = rows * cols;
     if (total == 0) return cudaSuccess;
-    if (elem == 2)
-        return launch_after(fill_kernel<uint16_t>, blocks_for(total, 152 * 32), kThreads, s, static_cast<uint16_t*>(p), ld, cols, total,
-                            uint16_t(0));
-    return launch_after(fill_kernel<float>, blocks_for(total, 152 * 32), kThreads, s, static_cast<float*>(p), ld, cols, total, 0.f);
+    return launch_after(clear_kernel, blocks_for(total, kSms * 32), kThreads, s, static_cast<uint16_t*>(p), ld, cols, total);
 }
 
 // Eight blocks for each SM, a share of at least 64 rows: a block takes 64 rows
@@ -374,7 +371,7 @@ cudaError_t launch_fill(void* p, uint64_t ld, uint64_t rows, uint64_t cols, uint
 // rows of the mean.
 uint32_t act_grad_splits(uint64_t m, uint64_t n, uint64_t groups) {
     const uint64_t have = (n + kGradCols - 1) / kGradCols * groups;
-    const uint64_t want = std::max<uint64_t>(1, 152 * 8 / std::max<uint64_t>(1, have));
+    const uint64_t want = std::max<uint64_t>(1, kSms * 8 / std::max<uint64_t>(1, have));
     return uint32_t(std::max<uint64_t>(1, std::min(want, m / groups / (groups > 1 ? 8 : 64))));
 }
 
@@ -403,14 +400,14 @@ cudaError_t launch_loss_join(const LossEpilogue& e, const uint32_t* token, const
 }
 
 cudaError_t launch_loss_rows(const LossRows& a, cudaStream_t s) {
-    return launch_after(loss_rows_kernel, uint32_t(std::min<uint64_t>(a.t, 304)), kPickThreads, s, a);
+    return launch_after(loss_rows_kernel, uint32_t(std::min<uint64_t>(a.t, 2 * kSms)), kPickThreads, s, a);
 }
 
 cudaError_t launch_spread_rows(const void* from, uint64_t ld, const uint32_t* place, void* to, uint64_t ld_to, uint64_t rows,
                                uint64_t cols, cudaStream_t s) {
     if (rows == 0 || cols == 0) return cudaSuccess;
     const bool vec = ld_to % 8 == 0 && reinterpret_cast<uintptr_t>(to) % 16 == 0;
-    return launch_after(spread_rows_kernel, uint32_t(std::min<uint64_t>((rows + 7) / 8, 152 * 8)), kThreads, s,
+    return launch_after(spread_rows_kernel, uint32_t(std::min<uint64_t>((rows + 7) / 8, kSms * 8)), kThreads, s,
                         static_cast<const uint16_t*>(from), ld, place, static_cast<uint16_t*>(to), ld_to, rows, cols, vec);
 }
 
