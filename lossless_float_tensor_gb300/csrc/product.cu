@@ -59,7 +59,7 @@ constexpr uint32_t kPatchCols = 32;  // columns that an epilogue warp takes at a
 constexpr uint32_t kPatchBytes = 32 * kPatchCols * 2, kEpilogueBytes = kPatchBytes + 128 * 4;  // a warp's shared memory
 constexpr uint32_t kMaxSplits = 8;  // blocks of a portable cluster
 constexpr uint32_t kHeights = 6;    // boxes of 1 to 32 lines for depths that are cut
-constexpr int64_t kWaitLimit = 8000000000;  // clock cycles: a wait gives up after about four seconds,
+constexpr uint32_t kWaitLimit = 7630;  // times 2^20 clock cycles: a wait gives up after about four seconds,
 constexpr int64_t kDrainLimit = 100000000;  // one for products in flight then after 50 ms
 
 struct Tiling {
@@ -78,7 +78,7 @@ struct Tiling {
     uint32_t out_width, z_width;  // values that rows of 16-bit results are aligned to: 8, 4, 2 or 1
     uint32_t vec;      // bit flags: 16-byte access to out 1, bias 2, residual 4, z 8, sums 16
     uint32_t starve;   // tests: A is never fetched, so that every wait for it runs out
-    int64_t wait_limit;
+    uint32_t wait_limit;  // 2^20 clock cycles
 };
 
 // ---- PTX ------------------------------------------------------------------------
@@ -226,28 +226,28 @@ struct Control {
     uint64_t full[kMaxStages], empty[kMaxStages];
     uint64_t acc_full[2], acc_empty[2];
     uint64_t drain;
-    int64_t wait_limit;
     uint32_t tmem;
-    volatile uint32_t abort;
+    volatile uint32_t abort, wait_limit;
 };
 // behind it, for the grouped schedules: int32 offsets[groups + 1], then (kRows,
 // kColumns) the first row or column tile of each group, int32 [groups + 1]
 
 // A wait that is not over at its first try goes on outside the loops of the
 // fetching and multiplying threads, whose code the epilogue's warps push out of
-// the instruction cache: each line less is felt there.
-__device__ __noinline__ bool wait_on(Control* c, uint32_t bar, uint32_t parity) {
+// the instruction cache: each line less is felt there.  (With the limit as a plain
+// 64-bit value beside `abort` the 48 x 128256 x 4096 loss took 168 us, not 166.)
+__device__ __noinline__ bool wait_on(volatile uint32_t* abort, const volatile uint32_t* limit, uint32_t bar, uint32_t parity) {
     const int64_t start = clock64();
     do {
         for (uint32_t i = 0; i < 64; ++i)
             if (try_wait(bar, parity)) return true;
-        if (c->abort) return false;
-    } while (clock64() - start < c->wait_limit);
-    c->abort = 1;
+        if (*abort) return false;
+    } while (clock64() - start < int64_t(*limit) << 20);
+    *abort = 1;
     return false;
 }
 __device__ __forceinline__ bool wait(Control* c, uint32_t bar, uint32_t parity) {
-    return try_wait(bar, parity) || wait_on(c, bar, parity);
+    return try_wait(bar, parity) || wait_on(&c->abort, &c->wait_limit, bar, parity);
 }
 __device__ __forceinline__ void drain(uint64_t* bar, uint32_t parity) {
     const int64_t start = clock64();
@@ -833,7 +833,10 @@ __device__ __forceinline__ void finish_tile(const Product& p, const Tiling& t, c
 // gave no status word would not learn of it otherwise).  The next products and
 // the loss carry it on.
 template <int EPI, bool TURNED>
-__device__ __noinline__ void leave_nan(const Product& p, Walk walk, uint32_t rank) {
+__device__ __noinline__ void leave_nan(const Product& p, const Tiling& t, const int32_t* offsets) {
+    const uint32_t rank = t.pair == 2 ? cluster_rank() & 1 : 0;
+    Walk walk(p, t, offsets, offsets + p.groups + 1, p.live_rows ? *p.live_rows : uint32_t(p.m),
+              p.live_depth ? *p.live_depth : uint32_t(p.depth));
     const uint16_t nan = p.dtype == UZIP_BF16 ? 0x7FC0 : 0x7E00;
     const StoreEpilogue& e = p.st;
     Tile o;
@@ -1244,7 +1247,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     if (ctl->abort) {
         settle();
-        leave_nan<EPI, TURNED>(p, Walk(p, t, offsets, first, live_rows, live_depth), rank);
+        leave_nan<EPI, TURNED>(p, t, offsets);
     }
     if (PAIR) cluster_sync();  // no arrival reaches a block that has ended
     tmem_fence_after();
@@ -1301,7 +1304,7 @@ uint32_t row_width(const void* p, uint64_t ld) {
 bool aligned16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
 
 constexpr uint32_t kSmemMost = 227 * 1024;
-std::atomic<int64_t> g_starved_wait{0};  // clock cycles (uzip_debug_starve_products)
+std::atomic<uint32_t> g_starved_wait{0};  // 2^20 clock cycles (uzip_debug_starve_products)
 
 bool cut(const Product& p) { return p.schedule == kDepth || p.live_depth; }  // the depths end where the device says
 uint64_t col_tiles_of(const Product& p, uint32_t bn) {
@@ -1473,7 +1476,7 @@ Choice choose(const Product& p, int sms) {
     t.vec = (aligned16(e.out) && e.ldo % out_unit == 0 && e.out_group % out_unit == 0 ? 1 : 0) |
             (aligned16(e.bias) && (p.n % 8 == 0 || p.groups == 1) ? 2 : 0) | (aligned16(e.residual) && e.ldr % 8 == 0 ? 4 : 0) |
             (aligned16(e.z) && e.ldz % 8 == 0 ? 8 : 0) | (aligned16(e.sum_in) && e.ld_sum % 4 == 0 ? 16 : 0);
-    const int64_t starved = g_starved_wait.load(std::memory_order_relaxed);
+    const uint32_t starved = g_starved_wait.load(std::memory_order_relaxed);
     t.starve = starved != 0;
     t.wait_limit = starved ? starved : kWaitLimit;
     return Choice{t, slot->cost};
@@ -1594,4 +1597,6 @@ cudaError_t launch_product(const Product& p, int sms, cudaStream_t s) {
 
 }  // namespace uzip
 
-extern "C" void uzip_debug_starve_products(int64_t wait_cycles) { uzip::g_starved_wait = wait_cycles; }
+extern "C" void uzip_debug_starve_products(int64_t wait_cycles) {
+    uzip::g_starved_wait = uint32_t(std::min<int64_t>((std::max<int64_t>(wait_cycles, 0) + (1 << 20) - 1) >> 20, uzip::kWaitLimit));
+}
