@@ -52,7 +52,7 @@ typedef enum {
 
 /* Arguments of a product and of its gradient.  Dense: groups = 0 and
  * offsets = NULL.  Grouped: w is [groups, n, k] with w_group elements from one
- * expert to the next, bias [groups, n] contiguous, offsets groups + 1 device
+ * expert to the next (at least what one extends over), bias [groups, n] contiguous, offsets groups + 1 device
  * int64 values that start at 0, never decrease and end at m.  Offsets that do
  * not are reported in d_status and every output is filled with NaN. */
 typedef struct {
@@ -147,10 +147,12 @@ uzip_status uzip_cross_entropy(const uzip_cross_entropy_args* a, void* d_workspa
  * classes at a time: their logits are computed again, with the same sums as
  * the loss's (p - 1 at a target that has nearly all of the probability is then
  * off by no more than the rounding of lse, half a unit in its last place), and
- * dloss (p - [j = t]),
- * scaled so that the largest dloss is 2^10, is rounded to the dtype in the
- * workspace (t x piece values); dh is summed over the pieces in fp32.  piece 0 takes the default: as many classes as 512 MiB hold, at most
- * 32768. */
+ * dloss (p - [j = t]), scaled so that the largest dloss is 2^10, is rounded to
+ * the dtype in the workspace (t x piece values); dh is summed over the pieces
+ * in fp32.  fp16 has no steps below 2^-24 there: a token whose dloss is far
+ * below the largest loses what is under 2^-35 of the largest (a thousandth of
+ * it keeps p down to 2^-25; bf16 has the range for any).  piece 0 takes the
+ * default: as many classes as 512 MiB hold, at most 32768. */
 typedef struct {
     int32_t dtype;
     int32_t reserved; /* 0 */

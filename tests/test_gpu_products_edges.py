@@ -543,3 +543,26 @@ def test_a_workspace_or_status_that_is_not_one(uz):
     need = -(-(9 + 50) * 40 * 2 // 256) * 256 + 256
     y = uz.linear(x, w, workspace=torch.empty(need // 4, dtype=torch.float32, device="cuda"), check=True)
     assert bool((y == 33).all())
+
+
+# ---- token weights of many sizes ---------------------------------------------------
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_cross_entropy_weights_of_many_sizes(uz, dtype):
+    """Weights from 1 to 2^-20 of the largest: each row of dh to its own size,
+    with what fp16 cannot hold beside the largest (2^-35 of it a class)."""
+    t, v, d = 210, 4000, 136
+    g = _gen(48)
+    h, w = _rand(g, (t, d), dtype), _rand(g, (v, d), dtype, 2 * d ** -0.5)
+    targets = torch.randint(0, v, (t,), generator=g, device="cuda")
+    dloss = 2.0 ** (13 - torch.arange(t, device="cuda") % 21).float()
+    _, lse = uz.cross_entropy(h, w, targets)
+    dh, _ = uz.cross_entropy_backward(dloss, h, w, targets, lse, need_dw=False, check=True)
+    s = h.double() @ w.double().T
+    dl = dloss.double()[:, None] * (torch.softmax(s, 1) - torch.nn.functional.one_hot(targets, v))
+    want, u = dl @ w.double(), ref.ROUND[dtype]
+    lost = 2.0 ** -35 * 2.0 ** 13 if dtype == torch.float16 else 0.0
+    slip = 4 * (d + 4) * 2.0 ** -23 * (h.double().abs() @ w.double().abs().T).amax(1, keepdim=True) + 2.0 ** -18 * (2 + s.abs())
+    off = (dl.abs() * (u + slip) + lost) @ w.double().abs()
+    off = off * (1 + 2.0 ** -10) + (v + 4) * 2.0 ** -23 * (dl.abs() @ w.double().abs())
+    assert float(((dh.double() - want).abs() / (off + u * want.abs() + ref.TINY[dtype])).max()) <= 1.0
