@@ -17,7 +17,7 @@
 //
 // What bounds it (GB300, bf16): large products run at the tensor cores' rate,
 // 8192 x 8192 x 8192 in 571 us, 1927 TFLOP/s in short runs, and at the power
-// limit in long ones (1676 TFLOP/s over 1.5 s at 1455 MHz); one token to a few
+// limit in long ones (1638 to 1676 TFLOP/s over 1.5 s); one token to a few
 // dozen stream the weights, 16 x 4096 x 14336 in 23 us, 5.1 TB/s.
 #include <cuda.h>
 
