@@ -256,3 +256,18 @@ from .ops import (  # noqa: E402
     linear,
     linear_backward,
 )
+
+# ---- the key-value cache ------------------------------------------------------
+
+from .cache import (  # noqa: E402
+    cache_compact,
+    cache_copy,
+    cache_fork,
+    cache_free,
+    cache_reserve,
+    paged_attention,
+    rotary,
+    rotary_append,
+    rotary_backward,
+    rotary_frequencies,
+)

@@ -1,0 +1,533 @@
+// Attention of one new token of each sequence over a paged cache.
+//
+// For a key head h, its query heads g = 0.. and the live tokens t of a sequence:
+// z_gt = scale q_g . k_t, p = softmax over t, o_g = sum_t p_gt v_t, in one pass
+// over the keys and values with a running maximum m and sum l:
+//   m' = max(m, z), l' = l 2^(m - m') + 2^(z - m'), o' = o 2^(m - m') + 2^(z - m') v.
+// Every key and value is read once and used for 4 operations a query head, 2 to 16
+// operations a byte: what bounds it is memory, and the work of a block is to keep
+// enough of it in flight.  The products still need matrix instructions (8 query
+// heads would take 54 TFLOP/s of plain ones); they run transposed, tokens or head
+// values as the rows and query heads as the 8 columns, so that heads that do not
+// exist cost no rows: S^T = K Q^T and O^T = V^T P^T by m16n8k16, which leaves the
+// tensor cores nearly idle either way.  tcgen05's rows of 128 tokens would want
+// the tokens of four warps in one step, with the barriers between them that this
+// layout does without.
+//
+// A warp takes tiles of 16 tokens, has a ring of shared memory of its own for
+// them (cp.async, 16 bytes a lane, rows 16 bytes apart from a multiple of 128 so
+// that ldmatrix finds no bank twice), and running sums of its own: no barrier but
+// where a sequence's part ends and the four warps' sums are joined.  Rows behind
+// the last token are filled with zeros and never read, so what they hold says
+// nothing.
+//
+// The tokens of all sequences and heads, in tiles, are cut into one equal piece
+// for each block, found by every block from the lengths on the device.  Where a
+// border falls inside a sequence's head the sums go to the workspace and a second
+// launch joins them, in the order of the tokens: the same bits each time.
+#include <algorithm>
+#include <atomic>
+
+#include "cache.cuh"
+
+namespace uzip {
+namespace {
+
+constexpr uint32_t kWarps = 4, kThreads = kWarps * 32;
+constexpr int kTile = 16;  // tokens of a tile: the rows of one matrix instruction
+
+template <int DP>
+struct Shape {
+    static constexpr uint32_t kPitch = DP * 2 + 16;             // bytes from token to token
+    static constexpr uint32_t kStage = 2 * kTile * kPitch;      // keys, then values
+    static constexpr uint32_t kBlocks = DP <= 128 ? 2 : 1;      // blocks on an SM
+    static constexpr uint32_t kRoom = 227 * 1024 / kBlocks - 2048;
+    static constexpr uint32_t kMost = kRoom / (kWarps * kStage);
+    static constexpr uint32_t kStages = kMost < 8 ? kMost : 8;
+    static constexpr uint32_t kSmem = kWarps * kStages * kStage;
+};
+
+__device__ __forceinline__ uint32_t smem_at(const void* p) { return uint32_t(__cvta_generic_to_shared(p)); }
+__device__ __forceinline__ void fetch16(uint32_t to, const void* from, uint32_t bytes) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void fetch_end() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void fetch_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void load4(uint32_t r[4], uint32_t at) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(at)
+                 : "memory");
+}
+__device__ __forceinline__ void load4_turned(uint32_t r[4], uint32_t at) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(at)
+                 : "memory");
+}
+__device__ __forceinline__ uint32_t turned8x8(uint32_t v) {
+    uint32_t r;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+    return r;
+}
+template <bool BF>
+__device__ __forceinline__ void multiply(float c[4], const uint32_t a[4], uint32_t b0, uint32_t b1) {
+    if constexpr (BF)
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                     : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                     : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    else
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                     : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                     : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+template <bool BF>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+    return to16x2(lo, hi, BF ? UZIP_BF16 : UZIP_FP16);
+}
+template <bool BF>
+__device__ __forceinline__ uint16_t pack1(float v) {
+    return to16(v, BF ? UZIP_BF16 : UZIP_FP16);
+}
+
+// Live tokens [lo, len) of sequence i and its tiles; a sequence without tokens
+// has one tile of none, and so has one whose length cannot be (bad).
+struct Live {
+    int lo, len, tiles;
+    bool bad;
+};
+__device__ __forceinline__ Live live_of(const Attention& a, int i) {
+    int n = a.lengths[i];
+    Live s;
+    s.bad = n < 0 || n > a.most;
+    if (s.bad) n = 0;
+    s.len = n;
+    s.lo = a.window && n > a.window ? n - a.window : 0;
+    s.tiles = max(1, (n - s.lo + kTile - 1) / kTile);
+    return s;
+}
+
+// Where a warp is: tiles [j0, j1) of row `row` of sequence i, and its tile of
+// them.  `left` counts the block's tiles from j0 on (whole rows: unused).
+struct Place {
+    int i, row, j0, j1, tile;
+    int64_t left;
+    Live s;
+};
+
+// The next part of the block's work; false at its end.
+__device__ __forceinline__ bool next_part(const Attention& a, Place& p) {
+    if (a.cut) {
+        p.left -= p.j1 - p.j0;
+        if (p.left <= 0) return false;
+        if (++p.row == a.pairs) {
+            p.row = 0;
+            p.s = live_of(a, ++p.i);
+        }
+    } else {  // whole rows, one for each block in turn
+        const int64_t at = int64_t(p.i) * a.pairs + p.row + gridDim.x;
+        if (at >= int64_t(a.seqs) * a.pairs) return false;
+        const int i = int(at / a.pairs);
+        p.row = int(at - int64_t(i) * a.pairs);
+        if (i != p.i) p.s = live_of(a, i);
+        p.i = i;
+    }
+    p.j0 = 0;
+    p.j1 = a.cut ? int(min(int64_t(p.s.tiles), p.left)) : p.s.tiles;
+    return true;
+}
+
+// The first part of this block's work, and the record of the border before it.
+// Tiles are counted through all sequences; block b has those from b * total /
+// blocks on.  Returns false if there is none.
+__device__ bool first_part(const Attention& a, Place& p, int least) {
+    if (!a.cut) {
+        const int64_t at = blockIdx.x;
+        if (at >= int64_t(a.seqs) * a.pairs) return false;
+        p.i = int(at / a.pairs), p.row = int(at - int64_t(p.i) * a.pairs);
+        p.s = live_of(a, p.i);
+        p.j0 = 0, p.j1 = p.s.tiles;
+        return true;
+    }
+    __shared__ int64_t sums[kWarps];
+    __shared__ int64_t found[2];  // sequence, tiles before it
+    const int each = (a.seqs + int(kThreads) - 1) / int(kThreads);
+    const int from = min(a.seqs, int(threadIdx.x) * each), to = min(a.seqs, from + each);
+    int64_t mine = 0;
+    for (int i = from; i < to; ++i) mine += live_of(a, i).tiles;
+    int64_t sum = mine;
+    const uint32_t lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+#pragma unroll
+    for (int o = 1; o < 32; o *= 2) {
+        const int64_t got = __shfl_up_sync(~0u, sum, o);
+        if (lane >= uint32_t(o)) sum += got;
+    }
+    if (lane == 31) sums[warp] = sum;
+    __syncthreads();
+    int64_t total = 0, before = sum - mine;
+#pragma unroll
+    for (uint32_t w = 0; w < kWarps; ++w) {
+        if (w < warp) before += sums[w];
+        total += sums[w];
+    }
+    total *= a.pairs;
+    before *= a.pairs;
+    const int64_t blocks = min(int64_t(gridDim.x), max(int64_t(1), total / least));
+    const int64_t b = blockIdx.x;
+    if (b >= blocks) {
+        if (threadIdx.x == 0) a.record[b] = make_int4(-1, 0, 0, 0);
+        return false;
+    }
+    const int64_t begin = b * total / blocks, end = (b + 1) * total / blocks;
+    if (begin >= before && begin < before + mine * a.pairs) {  // one thread's sequences hold the beginning
+        for (int i = from; i < to; ++i) {
+            const int64_t n = int64_t(live_of(a, i).tiles) * a.pairs;
+            if (begin < before + n) {
+                found[0] = i, found[1] = before;
+                break;
+            }
+            before += n;
+        }
+    }
+    __syncthreads();
+    p.i = int(found[0]);
+    p.s = live_of(a, p.i);
+    const int64_t in = begin - found[1];
+    p.row = int(in / p.s.tiles);
+    p.j0 = int(in - int64_t(p.row) * p.s.tiles);
+    p.left = end - begin;
+    p.j1 = int(min(int64_t(p.s.tiles), p.j0 + p.left));
+    if (threadIdx.x == 0) {
+        // the first border inside a row is the one that has its joining done
+        const int64_t row_begin = begin - p.j0, row_end = row_begin + p.s.tiles;
+        const bool first = p.j0 > 0 && (b - 1) * total / blocks <= row_begin;
+        a.record[b] = first ? make_int4(p.i, p.row, int(b - 1), int((row_end * blocks - 1) / total)) : make_int4(-1, 0, 0, 0);
+    }
+    return true;
+}
+
+// 2^(z - m) for z <= m: 0 for a score of -inf, also where there is none above it; what is no number stays so.
+__device__ __forceinline__ float weight(float z, float m) { return z == -INFINITY ? 0.f : fast_exp2(z - m); }
+
+template <int DP, int NT, bool BF>
+__global__ void __launch_bounds__(kThreads, Shape<DP>::kBlocks) attention_kernel(const __grid_constant__ Attention a, int least) {
+    using S = Shape<DP>;
+    constexpr int kSteps = DP / 16;
+    constexpr int kStages = int(S::kStages);
+    constexpr int kHeads = 8 * NT;
+    constexpr int kOut = DP + 4;  // floats from head to head of a warp's sums in shared memory
+    static_assert(kHeads * kOut * 4 <= int(S::kStage), "a warp's sums fit one stage");
+    extern __shared__ __align__(128) uint8_t ring[];
+    __shared__ float2 stat[kWarps][kHeads];
+    wait_for_launch_before();
+
+    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+    const uint32_t mine = smem_at(ring) + warp * kStages * S::kStage;
+    Place ahead;
+    if (!first_part(a, ahead, least)) return;  // the whole block
+    Place at = ahead;
+    bool more = true;  // `ahead` is at a tile (or at the end)
+    ahead.tile = ahead.j0 + warp;
+    auto settle = [&] {
+        while (more && ahead.tile >= ahead.j1) {
+            more = next_part(a, ahead);
+            ahead.tile = ahead.j0 + warp;
+        }
+    };
+    // the page of this lane's token of the tile that `ahead` is at; lanes 16 to 31 hold the same tokens again
+    auto page_of = [&]() -> int {
+        const int t = ahead.s.lo + ahead.tile * kTile + lane % kTile;
+        return more && t < ahead.s.len ? a.table[ahead.i * a.ldt + uint32_t(t) / uint32_t(a.page)] : 0;
+    };
+    uint32_t poison = 0;  // stages whose tile has a page that does not exist
+    // fetches the tile that `ahead` is at, whose pages are given, into a stage
+    auto fetch = [&](const Place& p, bool real, int page, int stage) {
+        if (real) {
+            const int t0 = p.s.lo + p.tile * kTile, count = min(kTile, p.s.len - t0);
+            const bool is_v = lane >= kTile, there = lane % kTile < count, bad = there && uint32_t(page) >= uint32_t(a.pages);
+            const bool any_bad = __any_sync(~0u, bad);
+            if (any_bad) {
+                poison |= 1u << stage;
+                if (a.status && lane == 0) *a.status = UZIP_ERR_INVALID_ARG;
+            } else {
+                poison &= ~(1u << stage);
+            }
+            const int live = any_bad ? 0 : count, head = p.row / a.blocks;
+            const PoolStrides& st = is_v ? a.vs : a.ks;
+            const uint32_t t = uint32_t(t0 + lane % kTile), off = t - t / uint32_t(a.page) * uint32_t(a.page);
+            const uint16_t* row = (is_v ? a.v : a.k);
+            if (there && !any_bad) row += page * st.page + head * st.head + off * st.token;
+            constexpr int kChunks = DP / 8;  // 16-byte pieces of a row
+            const uint32_t to = mine + stage * S::kStage;
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+#pragma unroll
+                for (int n = 0; n < kChunks / 2; ++n) {
+                    const int c = n * 32 + lane, r = c / kChunks, col = c % kChunks;
+                    const uint64_t base = __shfl_sync(~0u, reinterpret_cast<uint64_t>(row), half * kTile + r);
+                    const bool in = r < live && col * 8 < a.d;
+                    fetch16(to + (half * kTile + r) * S::kPitch + col * 16,
+                            reinterpret_cast<const uint8_t*>(base) + (in ? col * 16 : 0), in ? 16u : 0u);
+                }
+            }
+        }
+        fetch_end();
+    };
+
+    // the first stages; their pages are looked up together
+    settle();
+    {
+        Place p[kStages - 1];
+        bool real[kStages - 1];
+        int page[kStages - 1];
+#pragma unroll
+        for (int s = 0; s < kStages - 1; ++s) {
+            p[s] = ahead, real[s] = more, page[s] = page_of();
+            ahead.tile += kWarps;
+            settle();
+        }
+#pragma unroll
+        for (int s = 0; s < kStages - 1; ++s) fetch(p[s], real[s], page[s], s);
+    }
+    int page = page_of();
+    int stage = 0, refill = kStages - 1;  // stage to use next, stage to fetch into next: the free one
+
+    // log2 of e into the scale: exponentials are powers of 2
+    constexpr float kLog2e = 1.4426950408889634f;
+    const float scale = a.cap > 0 ? 2.f * kLog2e * a.scale / a.cap : a.scale * kLog2e;
+    const float cap = a.cap * kLog2e;
+
+    do {
+        const int blk = at.row % a.blocks, head0 = at.row / a.blocks * a.group + blk * kHeads;
+        const int heads = min(kHeads, a.group - blk * kHeads);
+        uint32_t q[NT][kSteps][2];
+        {
+            const uint16_t* row = a.q + at.i * a.q_row;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                const int h = nt * 8 + lane / 4;
+                const uint16_t* qh = row + int64_t(head0 + min(h, heads - 1)) * a.q_head;
+#pragma unroll
+                for (int ks = 0; ks < kSteps; ++ks) {
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const int col = ks * 16 + e * 8 + lane % 4 * 2;
+                        uint32_t w = 0;
+                        if (h < heads && col < a.d) w = qh[col] | uint32_t(qh[col + 1]) << 16;
+                        q[nt][ks][e] = w;
+                    }
+                }
+            }
+        }
+        float o[NT][kSteps][4] = {};
+        float m[NT][2], l[NT][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) m[nt][0] = m[nt][1] = -INFINITY, l[nt][0] = l[nt][1] = 0.f;
+        bool broken = at.s.bad;
+        if (broken && a.status && threadIdx.x == 0) *a.status = UZIP_ERR_INVALID_ARG;
+
+        for (at.tile = at.j0 + warp; at.tile < at.j1; at.tile += kWarps) {
+            fetch_wait<kStages - 2>();
+            __syncwarp();
+            fetch(ahead, more, page, refill);
+            if (more) {
+                ahead.tile += kWarps;
+                settle();
+                page = page_of();
+            }
+            const uint32_t keys = mine + stage * S::kStage, values = keys + kTile * S::kPitch;
+            const int count = at.s.len - at.s.lo - at.tile * kTile;  // live tokens of the tile, if fewer than 16
+            broken |= poison >> stage & 1;
+            refill = stage;
+            stage = stage + 1 == kStages ? 0 : stage + 1;
+
+            float z[NT][4] = {};
+            const uint32_t k_at = keys + lane % 16 * S::kPitch + lane / 16 * 16;
+#pragma unroll
+            for (int ks = 0; ks < kSteps; ++ks) {
+                uint32_t f[4];
+                load4(f, k_at + ks * 32);
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) multiply<BF>(z[nt], f, q[nt][ks][0], q[nt][ks][1]);
+            }
+            uint32_t p[NT][2];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    float s = z[nt][e] * scale;
+                    // cap tanh(x / cap) = cap - 2 cap / (exp(2 x / cap) + 1)
+                    if (a.cap > 0) s = cap - 2.f * cap / (fast_exp2(s) + 1.f);
+                    z[nt][e] = lane / 4 + e / 2 * 8 < count ? s : -INFINITY;
+                }
+                float top[2] = {fmaxf(z[nt][0], z[nt][2]), fmaxf(z[nt][1], z[nt][3])};
+#pragma unroll
+                for (int x = 4; x < 32; x *= 2) {
+                    top[0] = fmaxf(top[0], __shfl_xor_sync(~0u, top[0], x));
+                    top[1] = fmaxf(top[1], __shfl_xor_sync(~0u, top[1], x));
+                }
+                if (__any_sync(~0u, top[0] > m[nt][0] || top[1] > m[nt][1])) {
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        const float now = fmaxf(m[nt][c], top[c]), by = weight(m[nt][c], now);
+                        m[nt][c] = now;
+                        l[nt][c] *= by;
+#pragma unroll
+                        for (int ks = 0; ks < kSteps; ++ks) o[nt][ks][c] *= by, o[nt][ks][c + 2] *= by;
+                    }
+                }
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    z[nt][e] = weight(z[nt][e], m[nt][e % 2]);
+                    l[nt][e % 2] += z[nt][e];
+                }
+                // rounded to the values' type for the second product, relative to the largest: off by half a unit each,
+                // at random, which adds up to less than the one rounding of the result; the sum l keeps them unrounded
+                p[nt][0] = turned8x8(pack2<BF>(z[nt][0], z[nt][1]));
+                p[nt][1] = turned8x8(pack2<BF>(z[nt][2], z[nt][3]));
+            }
+            const uint32_t v_at = values + (lane % 8 + lane / 16 * 8) * S::kPitch + lane / 8 % 2 * 16;
+#pragma unroll
+            for (int ks = 0; ks < kSteps; ++ks) {
+                uint32_t f[4];
+                load4_turned(f, v_at + ks * 32);
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) multiply<BF>(o[nt][ks], f, p[nt][0], p[nt][1]);
+            }
+            __syncwarp();
+        }
+
+        // the four warps' sums, each in the warp's own free stage, and their maxima
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+#pragma unroll
+                for (int x = 4; x < 32; x *= 2) l[nt][c] += __shfl_xor_sync(~0u, l[nt][c], x);
+                const int h = nt * 8 + lane % 4 * 2 + c;
+                if (lane < 4) stat[warp][h] = make_float2(m[nt][c], broken ? NAN : l[nt][c]);
+                float* to = reinterpret_cast<float*>(ring + (warp * kStages + refill) * S::kStage) + h * kOut + lane / 4;
+#pragma unroll
+                for (int ks = 0; ks < kSteps; ++ks) to[ks * 16] = o[nt][ks][c], to[ks * 16 + 8] = o[nt][ks][c + 2];
+            }
+        }
+        __shared__ uint32_t where[kWarps];
+        if (lane == 0) where[warp] = (warp * kStages + refill) * S::kStage;
+        __syncthreads();
+        const bool whole = at.j0 == 0 && at.j1 == at.s.tiles;
+        const int64_t part = 2 * int64_t(blockIdx.x) + (at.j0 == 0);
+        for (int x = threadIdx.x; x < heads * DP; x += kThreads) {
+            const int h = x / DP, e = x % DP;
+            if (e >= a.d) continue;
+            float top = -INFINITY, sum = 0.f, val = 0.f;
+#pragma unroll
+            for (uint32_t w = 0; w < kWarps; ++w) top = fmaxf(top, stat[w][h].x);
+#pragma unroll
+            for (uint32_t w = 0; w < kWarps; ++w) {
+                const float by = weight(stat[w][h].x, top);
+                sum += stat[w][h].y * by;
+                val += reinterpret_cast<const float*>(ring + where[w])[h * kOut + e] * by;
+            }
+            if (whole) {
+                const bool none = at.s.len == 0 && !at.s.bad;
+                const int hq = head0 + h;
+                a.out[at.i * a.out_row + hq * a.out_head + e] = pack1<BF>(none ? 0.f : val / sum);
+                if (a.lse && e == 0)
+                    a.lse[int64_t(at.i) * a.q_heads + hq] = none ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
+            } else {
+                a.part_o[(part * kHeads + h) * a.d + e] = val;
+                if (e == 0) a.part_ml[part * kHeads + h] = make_float2(top, sum);
+            }
+        }
+        __syncthreads();
+    } while (next_part(a, at));
+    fetch_wait<0>();
+}
+
+// Joins the parts of a row that borders cut: block (border, kept head).
+template <bool BF>
+__global__ void __launch_bounds__(kThreads) join_kernel(const __grid_constant__ Attention a, int kept) {
+    wait_for_launch_before();
+    const int4 r = a.record[blockIdx.x + 1];
+    const int h = blockIdx.y;
+    if (r.x < 0) return;
+    const int blk = r.y % a.blocks, heads = min(kept, a.group - blk * kept);
+    if (h >= heads) return;
+    const int hq = r.y / a.blocks * a.group + blk * kept + h;
+    // the first part lies where its block's last one does, the others where a block's first does
+    auto part = [&](int b) { return (2 * int64_t(b) + (b == r.z)) * kept + h; };
+    float top = -INFINITY;
+    for (int b = r.z + threadIdx.x % 32; b <= r.w; b += 32) top = fmaxf(top, a.part_ml[part(b)].x);
+#pragma unroll
+    for (int x = 1; x < 32; x *= 2) top = fmaxf(top, __shfl_xor_sync(~0u, top, x));
+    float val[2] = {}, sum = 0.f;
+#pragma unroll 4
+    for (int b = r.z; b <= r.w; ++b) {
+        const float2 ml = a.part_ml[part(b)];
+        const float by = weight(ml.x, top);
+        sum += ml.y * by;
+        const float* o = a.part_o + part(b) * a.d;
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+            const int e = threadIdx.x + c * int(kThreads);
+            if (e < a.d) val[c] += o[e] * by;
+        }
+    }
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+        const int e = threadIdx.x + c * int(kThreads);
+        if (e < a.d) a.out[r.x * a.out_row + hq * a.out_head + e] = pack1<BF>(val[c] / sum);
+    }
+    if (a.lse && threadIdx.x == 0) a.lse[int64_t(r.x) * a.q_heads + hq] = (top + log2f(sum)) * 0.6931471805599453f;
+}
+
+constexpr int kLeast = 8;  // tiles that a block has at least, where rows are cut
+
+template <int DP, int NT, bool BF>
+cudaError_t launch_as(const Attention& a, const AttentionPlan& plan, cudaStream_t s) {
+    auto kern = attention_kernel<DP, NT, BF>;
+    static std::atomic<uint64_t> ready{0};  // devices on which the kernel may use its shared memory
+    int dev = 0;
+    cudaError_t err = cudaGetDevice(&dev);
+    if (err != cudaSuccess) return err;
+    if (dev >= 64 || !(ready.load(std::memory_order_relaxed) >> dev & 1)) {
+        err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(Shape<DP>::kSmem));
+        if (err != cudaSuccess) return err;
+        if (dev < 64) ready.fetch_or(uint64_t(1) << dev, std::memory_order_relaxed);
+    }
+    err = launch_next(kern, dim3(plan.grid), kThreads, Shape<DP>::kSmem, 1, s, a, kLeast);
+    if (err != cudaSuccess || !plan.cut || plan.grid < 2) return err;
+    return launch_next(join_kernel<BF>, dim3(plan.grid - 1, std::min<uint32_t>(plan.heads, a.group)), kThreads, 0, 1, s, a, int(plan.heads));
+}
+
+template <int DP>
+cudaError_t launch_wide(const Attention& a, int dtype, const AttentionPlan& plan, cudaStream_t s) {
+    if (plan.heads == 8) return dtype == UZIP_BF16 ? launch_as<DP, 1, true>(a, plan, s) : launch_as<DP, 1, false>(a, plan, s);
+    return dtype == UZIP_BF16 ? launch_as<DP, 2, true>(a, plan, s) : launch_as<DP, 2, false>(a, plan, s);
+}
+
+}  // namespace
+
+AttentionPlan plan_attention(int64_t seqs, int64_t kv_heads, int64_t group, int64_t d, int64_t most, int sms) {
+    AttentionPlan p;
+    p.heads = group <= 8 ? 8 : 16;
+    const int64_t rows = seqs * kv_heads * ((group + p.heads - 1) / p.heads);
+    const int64_t tiles = std::max<int64_t>(1, (most + kTile - 1) / kTile);
+    const int64_t room = int64_t(sms) * (d <= 128 ? 2 : 1);
+    p.cut = tiles > 32;
+    p.grid = uint32_t(std::max<int64_t>(1, std::min(room, p.cut ? rows * ((tiles + kLeast - 1) / kLeast) : rows)));
+    return p;
+}
+
+cudaError_t launch_attention(const Attention& a, int dtype, const AttentionPlan& plan, cudaStream_t s) {
+    if (a.d <= 64) return launch_wide<64>(a, dtype, plan, s);
+    if (a.d <= 96) return launch_wide<96>(a, dtype, plan, s);
+    if (a.d <= 128) return launch_wide<128>(a, dtype, plan, s);
+    if (a.d <= 192) return launch_wide<192>(a, dtype, plan, s);
+    return launch_wide<256>(a, dtype, plan, s);
+}
+
+}  // namespace uzip
