@@ -22,7 +22,9 @@
 // nothing.
 //
 // The tokens of all sequences and heads, in tiles, are cut into one equal piece
-// for each block, found by every block from the lengths on the device.  Where a
+// for each block, found by every block from the lengths on the device.  A row (a
+// sequence's tokens for one head) counts kRowCost tiles more than it has, for its
+// queries and its end, so that a block of many short rows has no more to do.  Where a
 // border falls inside a sequence's head the sums go to the workspace and a second
 // launch joins them, in the order of the tokens: the same bits each time.
 #include <algorithm>
@@ -40,16 +42,19 @@ template <int DP>
 struct Shape {
     static constexpr uint32_t kPitch = DP * 2 + 16;             // bytes from token to token
     static constexpr uint32_t kStage = 2 * kTile * kPitch;      // keys, then values
-    static constexpr uint32_t kBlocks = DP <= 128 ? 2 : 1;      // blocks on an SM
+    static constexpr uint32_t kBlocks = DP <= 128 ? 3 : 1;      // blocks on an SM
     static constexpr uint32_t kRoom = 227 * 1024 / kBlocks - 2048;
     static constexpr uint32_t kMost = kRoom / (kWarps * kStage);
     static constexpr uint32_t kStages = kMost < 8 ? kMost : 8;
     static constexpr uint32_t kSmem = kWarps * kStages * kStage;
 };
 
-__device__ __forceinline__ uint32_t smem_at(const void* p) { return uint32_t(__cvta_generic_to_shared(p)); }
-__device__ __forceinline__ void fetch16(uint32_t to, const void* from, uint32_t bytes) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(bytes) : "memory");
+// 16 bytes into shared memory; 16 zeros where not `there`
+__device__ __forceinline__ void fetch16(uint32_t to, uint64_t from, bool there) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(there ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void fetch16(uint32_t to, uint64_t from) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
 }
 __device__ __forceinline__ void fetch_end() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -110,8 +115,13 @@ __device__ __forceinline__ Live live_of(const Attention& a, int i) {
     return s;
 }
 
+constexpr int kRowCost = 8;  // what a row costs beside its tiles, in tiles
+constexpr int kLeast = 16;   // what a block has at least, where rows are cut: over kRowCost, so that it has a tile
+static_assert(kLeast > kRowCost, "");
+
 // Where a warp is: tiles [j0, j1) of row `row` of sequence i, and its tile of
-// them.  `left` counts the block's tiles from j0 on (whole rows: unused).
+// them.  `left` counts what the block has from the row's beginning on, kRowCost
+// before the first tile (whole rows: unused).
 struct Place {
     int i, row, j0, j1, tile;
     int64_t left;
@@ -121,8 +131,8 @@ struct Place {
 // The next part of the block's work; false at its end.
 __device__ __forceinline__ bool next_part(const Attention& a, Place& p) {
     if (a.cut) {
-        p.left -= p.j1 - p.j0;
-        if (p.left <= 0) return false;
+        p.left -= kRowCost + p.s.tiles;
+        if (p.left <= kRowCost) return false;
         if (++p.row == a.pairs) {
             p.row = 0;
             p.s = live_of(a, ++p.i);
@@ -136,14 +146,14 @@ __device__ __forceinline__ bool next_part(const Attention& a, Place& p) {
         p.i = i;
     }
     p.j0 = 0;
-    p.j1 = a.cut ? int(min(int64_t(p.s.tiles), p.left)) : p.s.tiles;
+    p.j1 = a.cut ? int(min(int64_t(p.s.tiles), p.left - kRowCost)) : p.s.tiles;
     return true;
 }
 
 // The first part of this block's work, and the record of the border before it.
-// Tiles are counted through all sequences; block b has those from b * total /
+// Costs are counted through all sequences; block b has those from b * total /
 // blocks on.  Returns false if there is none.
-__device__ bool first_part(const Attention& a, Place& p, int least) {
+__device__ bool first_part(const Attention& a, Place& p) {
     if (!a.cut) {
         const int64_t at = blockIdx.x;
         if (at >= int64_t(a.seqs) * a.pairs) return false;
@@ -157,7 +167,7 @@ __device__ bool first_part(const Attention& a, Place& p, int least) {
     const int each = (a.seqs + int(kThreads) - 1) / int(kThreads);
     const int from = min(a.seqs, int(threadIdx.x) * each), to = min(a.seqs, from + each);
     int64_t mine = 0;
-    for (int i = from; i < to; ++i) mine += live_of(a, i).tiles;
+    for (int i = from; i < to; ++i) mine += kRowCost + live_of(a, i).tiles;
     int64_t sum = mine;
     const uint32_t lane = threadIdx.x % 32, warp = threadIdx.x / 32;
 #pragma unroll
@@ -175,7 +185,7 @@ __device__ bool first_part(const Attention& a, Place& p, int least) {
     }
     total *= a.pairs;
     before *= a.pairs;
-    const int64_t blocks = min(int64_t(gridDim.x), max(int64_t(1), total / least));
+    const int64_t blocks = min(int64_t(gridDim.x), max(int64_t(1), total / kLeast));
     const int64_t b = blockIdx.x;
     if (b >= blocks) {
         if (threadIdx.x == 0) a.record[b] = make_int4(-1, 0, 0, 0);
@@ -184,7 +194,7 @@ __device__ bool first_part(const Attention& a, Place& p, int least) {
     const int64_t begin = b * total / blocks, end = (b + 1) * total / blocks;
     if (begin >= before && begin < before + mine * a.pairs) {  // one thread's sequences hold the beginning
         for (int i = from; i < to; ++i) {
-            const int64_t n = int64_t(live_of(a, i).tiles) * a.pairs;
+            const int64_t n = int64_t(kRowCost + live_of(a, i).tiles) * a.pairs;
             if (begin < before + n) {
                 found[0] = i, found[1] = before;
                 break;
@@ -196,14 +206,16 @@ __device__ bool first_part(const Attention& a, Place& p, int least) {
     p.i = int(found[0]);
     p.s = live_of(a, p.i);
     const int64_t in = begin - found[1];
-    p.row = int(in / p.s.tiles);
-    p.j0 = int(in - int64_t(p.row) * p.s.tiles);
-    p.left = end - begin;
-    p.j1 = int(min(int64_t(p.s.tiles), p.j0 + p.left));
+    const int span = kRowCost + p.s.tiles;
+    p.row = int(in / span);
+    const int in_row = int(in - int64_t(p.row) * span);
+    p.j0 = max(0, in_row - kRowCost);
+    p.left = end - begin + in_row;
+    p.j1 = int(min(int64_t(p.s.tiles), p.left - kRowCost));
     if (threadIdx.x == 0) {
-        // the first border inside a row is the one that has its joining done
-        const int64_t row_begin = begin - p.j0, row_end = row_begin + p.s.tiles;
-        const bool first = p.j0 > 0 && (b - 1) * total / blocks <= row_begin;
+        // the first border behind a row's first tile is the one that has its joining done
+        const int64_t tile0 = begin - in_row + kRowCost, row_end = tile0 + p.s.tiles;
+        const bool first = p.j0 > 0 && (b - 1) * total / blocks <= tile0;
         a.record[b] = first ? make_int4(p.i, p.row, int(b - 1), int((row_end * blocks - 1) / total)) : make_int4(-1, 0, 0, 0);
     }
     return true;
@@ -213,7 +225,7 @@ __device__ bool first_part(const Attention& a, Place& p, int least) {
 __device__ __forceinline__ float weight(float z, float m) { return z == -INFINITY ? 0.f : fast_exp2(z - m); }
 
 template <int DP, int NT, bool BF>
-__global__ void __launch_bounds__(kThreads, Shape<DP>::kBlocks) attention_kernel(const __grid_constant__ Attention a, int least) {
+__global__ void __launch_bounds__(kThreads, Shape<DP>::kBlocks) attention_kernel(const __grid_constant__ Attention a) {
     using S = Shape<DP>;
     constexpr int kSteps = DP / 16;
     constexpr int kStages = int(S::kStages);
@@ -225,9 +237,9 @@ __global__ void __launch_bounds__(kThreads, Shape<DP>::kBlocks) attention_kernel
     wait_for_launch_before();
 
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
-    const uint32_t mine = smem_at(ring) + warp * kStages * S::kStage;
+    const uint32_t mine = smem_u32(ring) + warp * kStages * S::kStage;
     Place ahead;
-    if (!first_part(a, ahead, least)) return;  // the whole block
+    if (!first_part(a, ahead)) return;  // the whole block
     Place at = ahead;
     bool more = true;  // `ahead` is at a tile (or at the end)
     ahead.tile = ahead.j0 + warp;
@@ -237,62 +249,82 @@ __global__ void __launch_bounds__(kThreads, Shape<DP>::kBlocks) attention_kernel
             ahead.tile = ahead.j0 + warp;
         }
     };
-    // the page of this lane's token of the tile that `ahead` is at; lanes 16 to 31 hold the same tokens again
-    auto page_of = [&]() -> int {
-        const int t = ahead.s.lo + ahead.tile * kTile + lane % kTile;
-        return more && t < ahead.s.len ? a.table[ahead.i * a.ldt + uint32_t(t) / uint32_t(a.page)] : 0;
+    // A tile to fetch: lane l (and l + 16) has token l's page and its place there.
+    struct Row {
+        int page, off, head, count;  // count: live tokens (the same in all lanes)
+    };
+    auto row_of = [&]() -> Row {
+        Row r{0, 0, 0, 0};
+        if (!more) return r;
+        const int t0 = ahead.s.lo + ahead.tile * kTile, t = t0 + lane % kTile;
+        r.count = min(kTile, ahead.s.len - t0);
+        r.head = ahead.row / a.blocks;
+        if (lane % kTile < r.count) {
+            const uint32_t col = uint32_t(uint64_t(t) * a.page_by >> a.page_shift);
+            r.page = a.table[ahead.i * a.ldt + col];
+            r.off = t - int(col) * a.page;
+        }
+        return r;
     };
     uint32_t poison = 0;  // stages whose tile has a page that does not exist
-    // fetches the tile that `ahead` is at, whose pages are given, into a stage
-    auto fetch = [&](const Place& p, bool real, int page, int stage) {
-        if (real) {
-            const int t0 = p.s.lo + p.tile * kTile, count = min(kTile, p.s.len - t0);
-            const bool is_v = lane >= kTile, there = lane % kTile < count, bad = there && uint32_t(page) >= uint32_t(a.pages);
-            const bool any_bad = __any_sync(~0u, bad);
-            if (any_bad) {
-                poison |= 1u << stage;
-                if (a.status && lane == 0) *a.status = UZIP_ERR_INVALID_ARG;
-            } else {
-                poison &= ~(1u << stage);
+    // A row's 16-byte pieces lie with neighbouring lanes, as many rows at once as fit a warp.  A lane's place in keys and
+    // values differs by a constant where their strides are the same, so one shuffle finds both.
+    constexpr int kChunks = DP / 8, kRows = kChunks < 32 ? 32 / kChunks : 1;
+    const int col = lane % kChunks * 16, first_row = lane / kChunks;
+    const uint64_t keys_from = reinterpret_cast<uint64_t>(a.k) + col, values_from = reinterpret_cast<uint64_t>(a.v) + col;
+    const uint32_t col_to = mine + first_row * S::kPitch + col;
+    auto fetch = [&](const Row& r, int stage) {
+        const bool in = lane % kTile < r.count;
+        const bool bad = __any_sync(~0u, in && uint32_t(r.page) >= uint32_t(a.pages));
+        poison = bad ? poison | 1u << stage : poison & ~(1u << stage);
+        if (bad && a.status && lane == 0) *a.status = UZIP_ERR_INVALID_ARG;
+        const int live = bad ? 0 : r.count;
+        // bytes from the pool's first value; rows that are not there: its first row, of which nothing is read
+        auto place = [&](const PoolStrides& st) -> uint64_t {
+            return in && !bad ? 2 * (r.page * st.page + r.head * st.head + r.off * st.token) : 0;
+        };
+        const uint64_t k_off = place(a.ks), v_off = a.alike ? k_off : place(a.vs);
+        const uint32_t to = col_to + stage * S::kStage;
+        if (kRows * kChunks == 32 && live == kTile && a.d == DP && a.alike) {
+#pragma unroll
+            for (int n = 0; n < kTile; n += kRows) {
+                const uint64_t off = __shfl_sync(~0u, k_off, n + first_row);
+                fetch16(to + n * S::kPitch, keys_from + off);
+                fetch16(to + (kTile + n) * S::kPitch, values_from + off);
             }
-            const int live = any_bad ? 0 : count, head = p.row / a.blocks;
-            const PoolStrides& st = is_v ? a.vs : a.ks;
-            const uint32_t t = uint32_t(t0 + lane % kTile), off = t - t / uint32_t(a.page) * uint32_t(a.page);
-            const uint16_t* row = (is_v ? a.v : a.k);
-            if (there && !any_bad) row += page * st.page + head * st.head + off * st.token;
-            constexpr int kChunks = DP / 8;  // 16-byte pieces of a row
-            const uint32_t to = mine + stage * S::kStage;
-#pragma unroll
-            for (int half = 0; half < 2; ++half) {
-#pragma unroll
-                for (int n = 0; n < kChunks / 2; ++n) {
-                    const int c = n * 32 + lane, r = c / kChunks, col = c % kChunks;
-                    const uint64_t base = __shfl_sync(~0u, reinterpret_cast<uint64_t>(row), half * kTile + r);
-                    const bool in = r < live && col * 8 < a.d;
-                    fetch16(to + (half * kTile + r) * S::kPitch + col * 16,
-                            reinterpret_cast<const uint8_t*>(base) + (in ? col * 16 : 0), in ? 16u : 0u);
+        } else {
+#pragma unroll 4
+            for (int n = 0; n < kTile; n += kRows) {
+                const int row = n + first_row;
+                const uint64_t ko = __shfl_sync(~0u, k_off, row), vo = __shfl_sync(~0u, v_off, row);
+                const bool there = row < live && col < 2 * a.d;
+                if (first_row < kRows) {
+                    fetch16(to + n * S::kPitch, there ? keys_from + ko : keys_from - col, there);
+                    fetch16(to + (kTile + n) * S::kPitch, there ? values_from + vo : values_from - col, there);
                 }
             }
         }
-        fetch_end();
     };
 
     // the first stages; their pages are looked up together
     settle();
     {
-        Place p[kStages - 1];
+        Row r[kStages - 1];
         bool real[kStages - 1];
-        int page[kStages - 1];
 #pragma unroll
-        for (int s = 0; s < kStages - 1; ++s) {
-            p[s] = ahead, real[s] = more, page[s] = page_of();
+        for (int n = 0; n < kStages - 1; ++n) {
+            real[n] = more;
+            r[n] = row_of();
             ahead.tile += kWarps;
             settle();
         }
 #pragma unroll
-        for (int s = 0; s < kStages - 1; ++s) fetch(p[s], real[s], page[s], s);
+        for (int n = 0; n < kStages - 1; ++n) {
+            if (real[n]) fetch(r[n], n);
+            fetch_end();
+        }
     }
-    int page = page_of();
+    Row row = row_of();
     int stage = 0, refill = kStages - 1;  // stage to use next, stage to fetch into next: the free one
 
     // log2 of e into the scale: exponentials are powers of 2
@@ -305,18 +337,23 @@ __global__ void __launch_bounds__(kThreads, Shape<DP>::kBlocks) attention_kernel
         const int heads = min(kHeads, a.group - blk * kHeads);
         uint32_t q[NT][kSteps][2];
         {
-            const uint16_t* row = a.q + at.i * a.q_row;
+            const uint16_t* q_row = a.q + at.i * a.q_row;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
                 const int h = nt * 8 + lane / 4;
-                const uint16_t* qh = row + int64_t(head0 + min(h, heads - 1)) * a.q_head;
+                const uint16_t* qh = q_row + int64_t(head0 + min(h, heads - 1)) * a.q_head;
 #pragma unroll
                 for (int ks = 0; ks < kSteps; ++ks) {
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
                         const int col = ks * 16 + e * 8 + lane % 4 * 2;
                         uint32_t w = 0;
-                        if (h < heads && col < a.d) w = qh[col] | uint32_t(qh[col + 1]) << 16;
+                        if (h < heads && col < a.d) {
+                            if (a.q_pairs)
+                                w = *reinterpret_cast<const uint32_t*>(qh + col);
+                            else
+                                w = qh[col] | uint32_t(qh[col + 1]) << 16;
+                        }
                         q[nt][ks][e] = w;
                     }
                 }
@@ -332,12 +369,13 @@ __global__ void __launch_bounds__(kThreads, Shape<DP>::kBlocks) attention_kernel
         for (at.tile = at.j0 + warp; at.tile < at.j1; at.tile += kWarps) {
             fetch_wait<kStages - 2>();
             __syncwarp();
-            fetch(ahead, more, page, refill);
             if (more) {
+                fetch(row, refill);
                 ahead.tile += kWarps;
                 settle();
-                page = page_of();
+                row = row_of();
             }
+            fetch_end();
             const uint32_t keys = mine + stage * S::kStage, values = keys + kTile * S::kPitch;
             const int count = at.s.len - at.s.lo - at.tile * kTile;  // live tokens of the tile, if fewer than 16
             broken |= poison >> stage & 1;
@@ -360,7 +398,7 @@ __global__ void __launch_bounds__(kThreads, Shape<DP>::kBlocks) attention_kernel
                 for (int e = 0; e < 4; ++e) {
                     float s = z[nt][e] * scale;
                     // cap tanh(x / cap) = cap - 2 cap / (exp(2 x / cap) + 1)
-                    if (a.cap > 0) s = cap - 2.f * cap / (fast_exp2(s) + 1.f);
+                    if (a.cap > 0) s = cap - 2.f * cap * fast_reciprocal(fast_exp2(s) + 1.f);
                     z[nt][e] = lane / 4 + e / 2 * 8 < count ? s : -INFINITY;
                 }
                 float top[2] = {fmaxf(z[nt][0], z[nt][2]), fmaxf(z[nt][1], z[nt][3])};
@@ -447,44 +485,51 @@ __global__ void __launch_bounds__(kThreads, Shape<DP>::kBlocks) attention_kernel
     fetch_wait<0>();
 }
 
-// Joins the parts of a row that borders cut: block (border, kept head).
+// Joins the parts of a row that borders cut, in the order of its tokens: block
+// (border, 512 of the row's results), four results a thread.
 template <bool BF>
 __global__ void __launch_bounds__(kThreads) join_kernel(const __grid_constant__ Attention a, int kept) {
     wait_for_launch_before();
     const int4 r = a.record[blockIdx.x + 1];
-    const int h = blockIdx.y;
     if (r.x < 0) return;
     const int blk = r.y % a.blocks, heads = min(kept, a.group - blk * kept);
+    const int at = 4 * (blockIdx.y * int(kThreads) + threadIdx.x), h = at / a.d, e = at - h * a.d;
     if (h >= heads) return;
-    const int hq = r.y / a.blocks * a.group + blk * kept + h;
-    // the first part lies where its block's last one does, the others where a block's first does
-    auto part = [&](int b) { return (2 * int64_t(b) + (b == r.z)) * kept + h; };
-    float top = -INFINITY;
-    for (int b = r.z + threadIdx.x % 32; b <= r.w; b += 32) top = fmaxf(top, a.part_ml[part(b)].x);
+    float top = -INFINITY, sum = 0.f, val[4] = {};
+    constexpr int kAhead = 8;
+    for (int b0 = r.z; b0 <= r.w; b0 += kAhead) {
+        float2 ml[kAhead];
+        float4 o[kAhead];
 #pragma unroll
-    for (int x = 1; x < 32; x *= 2) top = fmaxf(top, __shfl_xor_sync(~0u, top, x));
-    float val[2] = {}, sum = 0.f;
-#pragma unroll 4
-    for (int b = r.z; b <= r.w; ++b) {
-        const float2 ml = a.part_ml[part(b)];
-        const float by = weight(ml.x, top);
-        sum += ml.y * by;
-        const float* o = a.part_o + part(b) * a.d;
+        for (int n = 0; n < kAhead; ++n) {
+            const int b = b0 + n;
+            ml[n] = make_float2(-INFINITY, 0.f), o[n] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (b > r.w) continue;
+            // the first part lies where its block's last one does, the others where a block's first does
+            const int64_t part = (2 * int64_t(b) + (b == r.z)) * kept + h;
+            ml[n] = a.part_ml[part];
+            o[n] = *reinterpret_cast<const float4*>(a.part_o + part * a.d + e);
+        }
+        float now = top;
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-            const int e = threadIdx.x + c * int(kThreads);
-            if (e < a.d) val[c] += o[e] * by;
+        for (int n = 0; n < kAhead; ++n) now = fmaxf(now, ml[n].x);
+        const float by = weight(top, now);
+        top = now, sum *= by;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) val[c] *= by;
+#pragma unroll
+        for (int n = 0; n < kAhead; ++n) {
+            const float w = weight(ml[n].x, top);
+            sum += ml[n].y * w;
+            val[0] += o[n].x * w, val[1] += o[n].y * w, val[2] += o[n].z * w, val[3] += o[n].w * w;
         }
     }
+    const int hq = r.y / a.blocks * a.group + blk * kept + h;
+    uint16_t* to = a.out + r.x * a.out_row + hq * a.out_head + e;
 #pragma unroll
-    for (int c = 0; c < 2; ++c) {
-        const int e = threadIdx.x + c * int(kThreads);
-        if (e < a.d) a.out[r.x * a.out_row + hq * a.out_head + e] = pack1<BF>(val[c] / sum);
-    }
-    if (a.lse && threadIdx.x == 0) a.lse[int64_t(r.x) * a.q_heads + hq] = (top + log2f(sum)) * 0.6931471805599453f;
+    for (int c = 0; c < 4; ++c) to[c] = pack1<BF>(val[c] / sum);
+    if (a.lse && e == 0) a.lse[int64_t(r.x) * a.q_heads + hq] = (top + log2f(sum)) * 0.6931471805599453f;
 }
-
-constexpr int kLeast = 8;  // tiles that a block has at least, where rows are cut
 
 template <int DP, int NT, bool BF>
 cudaError_t launch_as(const Attention& a, const AttentionPlan& plan, cudaStream_t s) {
@@ -498,9 +543,10 @@ cudaError_t launch_as(const Attention& a, const AttentionPlan& plan, cudaStream_
         if (err != cudaSuccess) return err;
         if (dev < 64) ready.fetch_or(uint64_t(1) << dev, std::memory_order_relaxed);
     }
-    err = launch_next(kern, dim3(plan.grid), kThreads, Shape<DP>::kSmem, 1, s, a, kLeast);
+    err = launch_next(kern, dim3(plan.grid), kThreads, Shape<DP>::kSmem, 1, s, a);
     if (err != cudaSuccess || !plan.cut || plan.grid < 2) return err;
-    return launch_next(join_kernel<BF>, dim3(plan.grid - 1, std::min<uint32_t>(plan.heads, a.group)), kThreads, 0, 1, s, a, int(plan.heads));
+    const uint32_t results = std::min<uint32_t>(plan.heads, a.group) * a.d;
+    return launch_next(join_kernel<BF>, dim3(plan.grid - 1, (results + 4 * kThreads - 1) / (4 * kThreads)), kThreads, 0, 1, s, a, int(plan.heads));
 }
 
 template <int DP>
@@ -516,9 +562,9 @@ AttentionPlan plan_attention(int64_t seqs, int64_t kv_heads, int64_t group, int6
     p.heads = group <= 8 ? 8 : 16;
     const int64_t rows = seqs * kv_heads * ((group + p.heads - 1) / p.heads);
     const int64_t tiles = std::max<int64_t>(1, (most + kTile - 1) / kTile);
-    const int64_t room = int64_t(sms) * (d <= 128 ? 2 : 1);
+    const int64_t room = int64_t(sms) * (d <= 128 ? 3 : 1);
     p.cut = tiles > 32;
-    p.grid = uint32_t(std::max<int64_t>(1, std::min(room, p.cut ? rows * ((tiles + kLeast - 1) / kLeast) : rows)));
+    p.grid = uint32_t(std::max<int64_t>(1, std::min(room, p.cut ? rows * ((tiles + kRowCost + kLeast - 1) / kLeast) : rows)));
     return p;
 }
 

@@ -46,6 +46,10 @@ struct Attention {
     int32_t pairs;       // kv_heads * blocks: rows of work of a sequence
     int32_t most;        // tokens that a sequence's row of the table holds (capped to int32)
     int32_t window;      // 0: none
+    uint64_t page_by;    // t / page = t * page_by >> page_shift for t below 2^31
+    int32_t page_shift;
+    int32_t q_pairs;     // whether neighbouring values of q may be read together
+    int32_t alike;       // whether keys and values have the same strides
     int32_t cut;         // whether a sequence's tokens may be cut between blocks
     float scale, cap;
     uint16_t* out;

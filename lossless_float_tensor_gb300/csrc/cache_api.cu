@@ -297,6 +297,13 @@ uzip_status uzip_paged_attention(const uzip_paged_attention_args* a, void* d_wor
     r.table = a->table, r.ldt = ldt, r.lengths = a->lengths;
     r.seqs = int32_t(a->seqs), r.q_heads = int32_t(a->q_heads), r.group = int32_t(a->q_heads / a->kv_heads), r.d = int32_t(a->d);
     r.pages = int32_t(a->pages), r.page = int32_t(a->page);
+    // with 2^s >= page, ceil(2^(31 + s) / page) is over 2^(31 + s) / page by less than 2^s / page: nothing below 2^31 notices
+    int s2 = 0;
+    while (int64_t(1) << s2 < a->page) ++s2;
+    r.page_shift = 31 + s2;
+    r.page_by = ((uint64_t(1) << r.page_shift) + a->page - 1) / a->page;
+    r.alike = r.ks.page == r.vs.page && r.ks.head == r.vs.head && r.ks.token == r.vs.token;
+    r.q_pairs = aligned(a->q, 4) && r.q_row % 2 == 0 && r.q_head % 2 == 0;
     r.blocks = (r.group + int32_t(plan.heads) - 1) / int32_t(plan.heads);
     r.pairs = int32_t(a->kv_heads) * r.blocks;
     r.most = int32_t(most_tokens(a->width, a->page));
