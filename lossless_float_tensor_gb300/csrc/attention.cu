@@ -2,7 +2,7 @@
 //
 // For a key head h, its query heads g = 0.. and the live tokens t of a sequence:
 // z_gt = scale q_g . k_t, p = softmax over t, o_g = sum_t p_gt v_t, in one pass
-// over the keys and values with a running maximum m and sum l:
+// over the keys and values with a running maximum m (within a factor) and sum l:
 //   m' = max(m, z), l' = l 2^(m - m') + 2^(z - m'), o' = o 2^(m - m') + 2^(z - m') v.
 // Every key and value is read once and used for 4 operations a query head, 2 to 16
 // operations a byte: what bounds it is memory, and the work of a block is to keep
@@ -36,6 +36,7 @@ namespace uzip {
 namespace {
 
 constexpr uint32_t kWarps = 4, kThreads = kWarps * 32;
+constexpr float kSlack = 8.f;  // powers of two that a score may be over the maximum
 constexpr int kTile = 16;  // tokens of a tile: the rows of one matrix instruction
 
 template <int DP>
@@ -382,34 +383,33 @@ __global__ void __launch_bounds__(kThreads, Shape<DP>::kBlocks) attention_kernel
             refill = stage;
             stage = stage + 1 == kStages ? 0 : stage + 1;
 
-            float z[NT][4] = {};
+            float z[NT][4] = {}, z2[NT][4] = {};  // two chains of sums: half the wait for each product's result
             const uint32_t k_at = keys + lane % 16 * S::kPitch + lane / 16 * 16;
 #pragma unroll
             for (int ks = 0; ks < kSteps; ++ks) {
                 uint32_t f[4];
                 load4(f, k_at + ks * 32);
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) multiply<BF>(z[nt], f, q[nt][ks][0], q[nt][ks][1]);
+                for (int nt = 0; nt < NT; ++nt) multiply<BF>(ks % 2 ? z2[nt] : z[nt], f, q[nt][ks][0], q[nt][ks][1]);
             }
             uint32_t p[NT][2];
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    float s = z[nt][e] * scale;
+                    float s = (z[nt][e] + z2[nt][e]) * scale;
                     // cap tanh(x / cap) = cap - 2 cap / (exp(2 x / cap) + 1)
                     if (a.cap > 0) s = cap - 2.f * cap * fast_reciprocal(fast_exp2(s) + 1.f);
                     z[nt][e] = lane / 4 + e / 2 * 8 < count ? s : -INFINITY;
                 }
                 float top[2] = {fmaxf(z[nt][0], z[nt][2]), fmaxf(z[nt][1], z[nt][3])};
-#pragma unroll
-                for (int x = 4; x < 32; x *= 2) {
-                    top[0] = fmaxf(top[0], __shfl_xor_sync(~0u, top[0], x));
-                    top[1] = fmaxf(top[1], __shfl_xor_sync(~0u, top[1], x));
-                }
-                if (__any_sync(~0u, top[0] > m[nt][0] || top[1] > m[nt][1])) {
+                // the maximum that weights go by is moved only once a score is over it by kSlack: weights up to 2^kSlack lose
+                // nothing, and most tiles need one vote
+                if (__any_sync(~0u, top[0] > m[nt][0] + kSlack || top[1] > m[nt][1] + kSlack)) {
 #pragma unroll
                     for (int c = 0; c < 2; ++c) {
+#pragma unroll
+                        for (int x = 4; x < 32; x *= 2) top[c] = fmaxf(top[c], __shfl_xor_sync(~0u, top[c], x));
                         const float now = fmaxf(m[nt][c], top[c]), by = weight(m[nt][c], now);
                         m[nt][c] = now;
                         l[nt][c] *= by;
@@ -422,8 +422,8 @@ __global__ void __launch_bounds__(kThreads, Shape<DP>::kBlocks) attention_kernel
                     z[nt][e] = weight(z[nt][e], m[nt][e % 2]);
                     l[nt][e % 2] += z[nt][e];
                 }
-                // rounded to the values' type for the second product, relative to the largest: off by half a unit each,
-                // at random, which adds up to less than the one rounding of the result; the sum l keeps them unrounded
+                // rounded to the values' type for the second product: off by half a unit each, at random, which adds up to
+                // less than the one rounding of the result; the sum l keeps them unrounded
                 p[nt][0] = turned8x8(pack2<BF>(z[nt][0], z[nt][1]));
                 p[nt][1] = turned8x8(pack2<BF>(z[nt][2], z[nt][3]));
             }
