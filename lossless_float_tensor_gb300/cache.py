@@ -19,9 +19,10 @@ from __future__ import annotations
 
 import ctypes
 import math
+import struct
 
-from . import library
-from .ops import _calls, _dtype_code, _here, _operand, _outside_autograd, _refuse, _run, _vector
+from . import _check, library
+from .ops import _calls, _dtype_code, _on, _outside_autograd, _refuse
 
 _i32, _i64, _u64, _vp, _f32 = ctypes.c_int32, ctypes.c_int64, ctypes.c_uint64, ctypes.c_void_p, ctypes.c_float
 
@@ -110,28 +111,100 @@ uzip_cache_copy, uzip_cache_copy_workspace_size = _entry("uzip_cache_copy", Cach
 
 
 # ---- torch convenience layer (allocation and streams only) ----------------
+#
+# A step of a server makes these calls for every layer, so their host time
+# counts: arguments are packed in one go (struct, in the C structure's native
+# layout) instead of set one by one, and each tensor is asked for each thing
+# once (attention of one token 20 us of host time, 13 so).
 
-def _strided(t, name, shape, like):
-    """Data pointer and the strides of all dimensions but the last, which is
-    contiguous."""
+class _Entry:
+    """A C entry point that takes its structure as packed bytes."""
+
+    def __init__(self, name, args):
+        codes = {_i32: "i", _i64: "q", _vp: "P", _f32: "f"}
+        self.name = name
+        self.pack = struct.Struct("@" + "".join(codes[t] for _, t in args._fields_)).pack
+        self.size, self.call = _lib[name + "_workspace_size"], _lib[name]
+        self.size.argtypes, self.size.restype = [ctypes.c_char_p], _u64
+        self.call.argtypes, self.call.restype = [ctypes.c_char_p, _vp, _u64, _vp, _vp], ctypes.c_int
+
+
+_ROTARY, _APPEND = _Entry("uzip_rotary", RotaryArgs), _Entry("uzip_rotary_append", RotaryArgs)
+_ATTENTION = _Entry("uzip_paged_attention", PagedAttentionArgs)
+_RESERVE, _FORK = _Entry("uzip_cache_reserve", CacheArgs), _Entry("uzip_cache_fork", CacheArgs)
+_FREE, _COMPACT = _Entry("uzip_cache_free", CacheArgs), _Entry("uzip_cache_compact", CacheArgs)
+_COPY = _Entry("uzip_cache_copy", CacheCopyArgs)
+
+_torch = None
+
+
+def _load():
+    global _torch
+    import torch
+
+    _torch = torch
+    return torch
+
+
+def _issue(entry, args, dev, workspace, status, check):
+    """Runs an entry point on the current stream of device `dev`, the current one."""
+    torch = _torch
+    if workspace is None:
+        need = entry.size(args)
+        at = 0
+        if need:
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+            at = workspace.data_ptr()
+    else:
+        if not workspace.is_contiguous():
+            _refuse("workspace: the values between those of a strided tensor are not its own")
+        need, at = workspace.nbytes, workspace.data_ptr()
+    if status is None:
+        if check:
+            status = torch.empty((), dtype=torch.int32, device=dev)
+    elif status.dtype != torch.int32 or not status.numel():
+        _refuse(f"status: expected an int32 tensor, not {status.dtype} of {status.numel()} values")
+    st = entry.call(args, at, need, status.data_ptr() if status is not None else None, torch._C._cuda_getCurrentRawStream(dev))
+    if st:
+        _check(st, entry.name)
+    if check:
+        _check(int(status.item()), entry.name + " (device)")
+
+
+def _elsewhere(dev, stream):
+    """Whether `stream` or the tensors' device is another than the current one."""
+    return stream is not None or dev != _torch._C._cuda_getDevice()
+
+
+def _device(t, name, dims):
+    """The index of the device of a tensor of `dims` dimensions."""
+    dev = t.get_device()
+    if dev < 0 or not t.is_cuda or t.dim() != dims:
+        _refuse(f"{name}: expected a CUDA tensor of {dims} dimensions")
+    return dev
+
+
+def _strides(t, name, shape, dtype, dev):
+    """The strides of a tensor whose last dimension is contiguous."""
     if t.shape != shape:
         _refuse(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if t is not like and (t.dtype != like.dtype or t.get_device() != like.get_device()):
-        _refuse(f"{name} is {t.dtype} on {t.device}, expected {like.dtype} on {like.device}")
+    if t.dtype is not dtype or t.get_device() != dev:
+        _refuse(f"{name} is {t.dtype} on {t.device}, expected {dtype} on cuda:{dev}")
     if t.requires_grad:
         _outside_autograd(t, name)
-    *steps, last = t.stride()
-    if last != 1 and shape[-1] > 1:
+    steps = t.stride()
+    if steps[-1] != 1 and shape[-1] > 1:
         _refuse(f"{name}: the last dimension must be contiguous")
-    return (t.data_ptr() or None, *steps)
+    return steps
 
 
-def _pools(k_pages, v_pages, dims, like):
-    _operand(k_pages, "k_pages", dims)
-    if like is None:
-        like = k_pages
-    k = _strided(k_pages, "k_pages", k_pages.shape, like)
-    return k, _strided(v_pages, "v_pages", k_pages.shape, like)
+def _list(t, name, shape, dtype, dev):
+    """The address of a contiguous tensor."""
+    if t.shape != shape or t.dtype is not dtype or t.get_device() != dev or not t.is_contiguous():
+        _refuse(f"{name}: expected a contiguous {dtype} tensor of shape {tuple(shape)} on cuda:{dev}")
+    if t.requires_grad:
+        _outside_autograd(t, name)
+    return t.data_ptr()
 
 
 def rotary_frequencies(dim, *, base=10000.0, scaling="none", factor=1.0, trained=0, fast=32.0, slow=1.0, device="cuda"):
@@ -180,48 +253,43 @@ def rotary_frequencies(dim, *, base=10000.0, scaling="none", factor=1.0, trained
     return torch.tensor(freqs, dtype=torch.float64, device=device)
 
 
-def _rotary(name, q, k, v, positions, freqs, interleaved, backward, scale, out, pools, slots, workspace, status, check, stream):
-    import torch
-
+def _rotary(q, k, positions, freqs, interleaved, backward, scale, out, status, check, stream):
+    torch = _torch or _load()
     like = q if q is not None else k
     if like is None:
         _refuse("neither q nor k is given")
-    _operand(like, "q" if q is not None else "k", 3)
-    t, _, d = like.shape
-    hq = q.shape[1] if q is not None else 0
+    dev = _device(like, "q" if q is not None else "k", 3)
+    if _elsewhere(dev, stream):
+        with _on(dev, stream):
+            return _rotary(q, k, positions, freqs, interleaved, backward, scale, out, status, check, None)
+    dt, code = like.dtype, _dtype_code(like)
+    t, hq, d = like.shape
+    hk = 0
+    if q is None:
+        hq = 0
     if k is not None:
-        _operand(k, "k", 3)
-    hkv = k.shape[1] if k is not None else 0
-    _operand(freqs, "freqs", 1)
-    dev = like.device
-    a = RotaryArgs(_dtype_code(like), bool(interleaved), backward, scale, t, hq, hkv, d, 2 * freqs.shape[0])
-    a.positions = _vector(positions, "positions", (t,), torch.int64, like)
-    a.freqs = _vector(freqs, "freqs", freqs.shape, torch.float64, like)
-    if q is not None:
-        a.q, a.q_row, a.q_head = _strided(q, "q", (t, hq, d), like)
-    if k is not None:
-        a.k, a.k_row, a.k_head = _strided(k, "k", (t, hkv, d), like)
-    if v is not None:
-        a.v, a.v_row, a.v_head = _strided(v, "v", (t, hkv, d), like)
-        (a.k_pages, a.kp_page, a.kp_head, a.kp_token), (a.v_pages, a.vp_page, a.vp_head, a.vp_token) = _pools(*pools, 4, like)
-        a.pages, heads, a.page, width = pools[0].shape
-        if heads != hkv or width != d:
-            _refuse(f"k_pages has {heads} heads of {width} values, k has {hkv} of {d}")
-        a.slots = _vector(slots, "slots", (t,), torch.int64, like)
-    q_out = k_out = None
-    with _here(dev, stream):
-        if out is not None:
-            q_out, k_out = out if v is None else (out, None)
-        if q is not None:
-            if q_out is None:
-                q_out = torch.empty((t, hq, d), dtype=like.dtype, device=dev)
-            a.q_out, a.q_out_row, a.q_out_head = _strided(q_out, "out", (t, hq, d), like)
-        if k is not None and v is None:
-            if k_out is None:
-                k_out = torch.empty((t, hkv, d), dtype=like.dtype, device=dev)
-            a.k_out, a.k_out_row, a.k_out_head = _strided(k_out, "out", (t, hkv, d), like)
-        _run(name, a, dev, workspace, status, check)
-    return (q_out, k_out) if v is None else q_out
+        _device(k, "k", 3)
+        hk = k.shape[1]
+    pairs = freqs.numel()
+    at = _list(positions, "positions", (t,), torch.int64, dev), _list(freqs, "freqs", (pairs,), torch.float64, dev)
+    q_out, k_out = out if out is not None else (None, None)
+    part = []
+    for x, y, h, name in ((q, q_out, hq, "q"), (k, k_out, hk, "k")):
+        if x is None:
+            part.append((None, (0, 0, 0, 0, 0, 0)))
+            continue
+        shape = (t, h, d)
+        row, head, _ = _strides(x, name, shape, dt, dev)
+        if y is None:
+            y = torch.empty(shape, dtype=dt, device=dev)
+            steps = h * d, d, 1
+        else:
+            steps = _strides(y, "out", shape, dt, dev)
+        part.append((y, (x.data_ptr(), row, head, y.data_ptr(), steps[0], steps[1])))
+    (q_out, a), (k_out, b) = part
+    _issue(_ROTARY, _ROTARY.pack(code, 1 if interleaved else 0, backward, scale, t, hq, hk, d, 2 * pairs, *at, *a[:3], *b[:3], 0, 0, 0, *a[3:], *b[3:],
+                                 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0), dev, None, status, check)
+    return q_out, k_out
 
 
 def rotary(q, k, positions, freqs, *, interleaved=False, scale=1.0, out=None, status=None, check=False, stream=None):
@@ -232,13 +300,13 @@ def rotary(q, k, positions, freqs, *, interleaved=False, scale=1.0, out=None, st
     radians per position (rotary_frequencies); far positions lose nothing.
     Either of q and k may be None.  out: (q', k') to write to, which may be q
     and k themselves."""
-    return _rotary("uzip_rotary", q, k, None, positions, freqs, interleaved, 0, scale, out, None, None, None, status, check, stream)
+    return _rotary(q, k, positions, freqs, interleaved, 0, scale, out, status, check, stream)
 
 
 def rotary_backward(dq, dk, positions, freqs, *, interleaved=False, scale=1.0, out=None, status=None, check=False, stream=None):
     """(dq', dk'): the gradients of rotary()'s q and k for those of its results:
     the rotation by the opposite angles."""
-    return _rotary("uzip_rotary", dq, dk, None, positions, freqs, interleaved, 1, scale, out, None, None, None, status, check, stream)
+    return _rotary(dq, dk, positions, freqs, interleaved, 1, scale, out, status, check, stream)
 
 
 def rotary_append(q, k, v, positions, freqs, k_pages, v_pages, slots, *, interleaved=False, scale=1.0, out=None, status=None, check=False,
@@ -247,10 +315,38 @@ def rotary_append(q, k, v, positions, freqs, k_pages, v_pages, slots, *, interle
     token i at page slots[i] // page size, place slots[i] % page size.  slots is
     int64 [t] (cache_reserve gives them), no two equal; -1 stores nothing, others
     outside the pool store nothing and are reported in `status`."""
+    torch = _torch or _load()
     if q is None or k is None or v is None:
         _refuse("rotary_append needs q, k and v")
-    return _rotary("uzip_rotary_append", q, k, v, positions, freqs, interleaved, 0, scale, out, (k_pages, v_pages), slots, None, status, check,
-                   stream)
+    dev = _device(q, "q", 3)
+    if _elsewhere(dev, stream):
+        with _on(dev, stream):
+            return rotary_append(q, k, v, positions, freqs, k_pages, v_pages, slots, interleaved=interleaved, scale=scale, out=out, status=status,
+                                 check=check)
+    _device(k, "k", 3)
+    dt, code = q.dtype, _dtype_code(q)
+    t, hq, d = shape = q.shape
+    hk = k.shape[1]
+    q_row, q_head, _ = _strides(q, "q", shape, dt, dev)
+    k_row, k_head, _ = _strides(k, "k", (t, hk, d), dt, dev)
+    v_row, v_head, _ = _strides(v, "v", (t, hk, d), dt, dev)
+    _device(k_pages, "k_pages", 4)
+    pages, heads, page, wide = pool = k_pages.shape
+    if heads != hk or wide != d:
+        _refuse(f"k_pages has {heads} heads of {wide} values, k has {hk} of {d}")
+    kp, vp = _strides(k_pages, "k_pages", pool, dt, dev), _strides(v_pages, "v_pages", pool, dt, dev)
+    pairs = freqs.numel()
+    if out is None:
+        out = torch.empty((t, hq, d), dtype=dt, device=dev)
+        o_row, o_head = hq * d, d
+    else:
+        o_row, o_head, _ = _strides(out, "out", shape, dt, dev)
+    args = _APPEND.pack(code, 1 if interleaved else 0, 0, scale, t, hq, hk, d, 2 * pairs, _list(positions, "positions", (t,), torch.int64, dev),
+                        _list(freqs, "freqs", (pairs,), torch.float64, dev), q.data_ptr(), q_row, q_head, k.data_ptr(), k_row, k_head, v.data_ptr(),
+                        v_row, v_head, out.data_ptr(), o_row, o_head, 0, 0, 0, pages, page, k_pages.data_ptr(), kp[0], kp[1], kp[2],
+                        v_pages.data_ptr(), vp[0], vp[1], vp[2], _list(slots, "slots", (t,), torch.int64, dev))
+    _issue(_APPEND, args, dev, None, status, check)
+    return out
 
 
 def paged_attention(q, k_pages, v_pages, table, lengths, *, scale=None, softcap=0.0, window=0, with_lse=False, out=None, workspace=None,
@@ -264,49 +360,63 @@ def paged_attention(q, k_pages, v_pages, table, lengths, *, scale=None, softcap=
     log-sum-exp of each head's scores, by which results over parts of a context
     are joined.  A length or page that cannot be gives NaN for its sequence and
     is reported in `status`."""
-    import torch
-
-    _operand(q, "q", 3)
-    k, v = _pools(k_pages, v_pages, 4, q)
-    s, hq, d = q.shape
-    pages, hkv, page, width = k_pages.shape
-    if width != d:
-        _refuse(f"q has heads of {d} values, k_pages of {width}")
-    dev = q.device
-    if table.dtype != torch.int32 or table.dim() != 2 or table.shape[0] != s or table.get_device() != q.get_device() or (
-            table.shape[1] > 1 and table.stride(1) != 1):
-        _refuse(f"table: expected int32 of shape ({s}, pages of a sequence) on {dev}, its rows contiguous")
-    a = PagedAttentionArgs(_dtype_code(q), 0, s, hq, hkv, d, pages, page, table.shape[1])
-    a.q, a.q_row, a.q_head = _strided(q, "q", q.shape, q)
-    a.k_pages, a.kp_page, a.kp_head, a.kp_token = k
-    a.v_pages, a.vp_page, a.vp_head, a.vp_token = v
-    a.table, a.ldt = table.data_ptr() or None, table.stride(0)
-    a.lengths = _vector(lengths, "lengths", (s,), torch.int32, q)
-    a.scale, a.softcap, a.window = 1 / math.sqrt(d) if scale is None and d else scale or 0.0, softcap, window
-    with _here(dev, stream):
-        if out is None:
-            out = torch.empty((s, hq, d), dtype=q.dtype, device=dev)
-        a.out, a.out_row, a.out_head = _strided(out, "out", q.shape, q)
-        lse = None
-        if with_lse:
-            lse = torch.empty((s, hq), dtype=torch.float32, device=dev)
-            a.lse = lse.data_ptr() or None
-        _run("uzip_paged_attention", a, dev, workspace, status, check)
+    torch = _torch or _load()
+    dev = _device(q, "q", 3)
+    if _elsewhere(dev, stream):
+        with _on(dev, stream):
+            return paged_attention(q, k_pages, v_pages, table, lengths, scale=scale, softcap=softcap, window=window, with_lse=with_lse, out=out,
+                                   workspace=workspace, status=status, check=check)
+    dt, code = q.dtype, _dtype_code(q)
+    s, hq, d = shape = q.shape
+    q_row, q_head, _ = _strides(q, "q", shape, dt, dev)
+    _device(k_pages, "k_pages", 4)
+    pages, hk, page, wide = pool = k_pages.shape
+    if wide != d:
+        _refuse(f"q has heads of {d} values, k_pages of {wide}")
+    kp, vp = _strides(k_pages, "k_pages", pool, dt, dev), _strides(v_pages, "v_pages", pool, dt, dev)
+    ldt, width = _table(table, dev)
+    if table.shape[0] != s:
+        _refuse(f"table has {table.shape[0]} rows for {s} queries")
+    if out is None:
+        out = torch.empty((s, hq, d), dtype=dt, device=dev)
+        o_row, o_head = hq * d, d
+    else:
+        o_row, o_head, _ = _strides(out, "out", shape, dt, dev)
+    lse = torch.empty((s, hq), dtype=torch.float32, device=dev) if with_lse else None
+    if scale is None:
+        scale = d ** -0.5 if d else 0.0
+    args = _ATTENTION.pack(code, 0, s, hq, hk, d, pages, page, width, q.data_ptr(), q_row, q_head, k_pages.data_ptr(), kp[0], kp[1], kp[2],
+                           v_pages.data_ptr(), vp[0], vp[1], vp[2], table.data_ptr(), ldt, _list(lengths, "lengths", (s,), torch.int32, dev), scale,
+                           softcap, window, out.data_ptr(), o_row, o_head, lse.data_ptr() if with_lse else 0)
+    _issue(_ATTENTION, args, dev, workspace, status, check)
     return (out, lse) if with_lse else out
 
 
-def _state(refs, table, lengths, page_size):
-    import torch
+def _table(table, dev):
+    """Row stride and columns of a table."""
+    ldt, step = table.stride() if table.dim() == 2 else (0, 0)
+    width = table.shape[-1] if table.dim() == 2 else 0
+    if table.dim() != 2 or table.dtype is not _torch.int32 or table.get_device() != dev or (step != 1 and width > 1):
+        _refuse(f"table: expected int32 [sequences, pages of a sequence] on cuda:{dev}, its rows contiguous")
+    return ldt, width
 
-    _operand(table, "table", 2)
-    s, width = table.shape
-    if table.dtype != torch.int32 or (width > 1 and table.stride(1) != 1):
-        _refuse("table: expected int32 [sequences, pages of a sequence], its rows contiguous")
-    a = CacheArgs(refs.shape[0] if refs.dim() else 0, page_size, s, width)
-    a.refs = _vector(refs, "refs", (a.pages,), torch.int32, table)
-    a.table, a.ldt = table.data_ptr() or None, table.stride(0)
-    a.lengths = _vector(lengths, "lengths", (s,), torch.int32, table)
-    return a
+
+def _change(entry, state, page_size, workspace, status, check, n=0, start=0, listed=0, tokens=0, slots=0, positions=0, pairs=0):
+    """An operation on a cache's state: refs, table, lengths, what _state() gave of them."""
+    refs, table, lengths, (pages, seqs, width, ldt, dev) = state
+    args = entry.pack(pages, page_size, seqs, width, refs.data_ptr(), table.data_ptr(), ldt, lengths.data_ptr(), n, start, listed, tokens, slots,
+                      positions, pairs)
+    _issue(entry, args, dev, workspace, status, check)
+
+
+def _state(refs, table, lengths):
+    torch = _torch or _load()
+    dev = _device(table, "table", 2)
+    ldt, width = _table(table, dev)
+    pages, seqs = refs.numel(), table.shape[0]
+    _list(refs, "refs", (pages,), torch.int32, dev)
+    _list(lengths, "lengths", (seqs,), torch.int32, dev)
+    return refs, table, lengths, (pages, seqs, width, ldt, dev)
 
 
 def cache_reserve(refs, table, lengths, counts, tokens, page_size, *, out=None, workspace=None, status=None, check=False, stream=None):
@@ -318,20 +428,22 @@ def cache_reserve(refs, table, lengths, counts, tokens, page_size, *, out=None, 
     [sequences, 2] holds {old, new} for cache_copy, {-1, -1} elsewhere.  refs,
     table and lengths are updated.  Where pages or columns of the table run out
     nothing changes, slots are -1, and `status` says so."""
-    import torch
-
-    a = _state(refs, table, lengths, page_size)
-    a.list = _vector(counts, "counts", lengths.shape, torch.int32, table)
-    a.tokens = tokens
-    dev = table.device
-    with _here(dev, stream):
-        if out is None:
-            out = (torch.empty(tokens, dtype=torch.int64, device=dev), torch.empty(tokens, dtype=torch.int64, device=dev),
-                   torch.empty((a.seqs, 2), dtype=torch.int32, device=dev))
-        a.slots = _vector(out[0], "out", (tokens,), torch.int64, table)
-        a.positions = _vector(out[1], "out", (tokens,), torch.int64, table)
-        a.pairs = _vector(out[2], "out", (a.seqs, 2), torch.int32, table)
-        _run("uzip_cache_reserve", a, dev, workspace, status, check)
+    state = _state(refs, table, lengths)
+    seqs, dev, torch = state[3][1], state[3][4], _torch
+    if _elsewhere(dev, stream):
+        with _on(dev, stream):
+            return cache_reserve(refs, table, lengths, counts, tokens, page_size, out=out, workspace=workspace, status=status, check=check)
+    if tokens < 0:
+        _refuse(f"{tokens} tokens")
+    listed = _list(counts, "counts", (seqs,), torch.int32, dev)
+    if out is None:
+        out = (torch.empty(tokens, dtype=torch.int64, device=dev), torch.empty(tokens, dtype=torch.int64, device=dev),
+               torch.empty((seqs, 2), dtype=torch.int32, device=dev))
+        slots, positions, pairs = out[0].data_ptr(), out[1].data_ptr(), out[2].data_ptr()
+    else:
+        slots, positions = (_list(x, "out", (tokens,), torch.int64, dev) for x in out[:2])
+        pairs = _list(out[2], "out", (seqs, 2), torch.int32, dev)
+    _change(_RESERVE, state, page_size, workspace, status, check, listed=listed, tokens=tokens, slots=slots, positions=positions, pairs=pairs)
     return out
 
 
@@ -339,42 +451,41 @@ def cache_fork(refs, table, lengths, parents, children, page_size, *, workspace=
     """children[j] become sequences that share the pages of parents[j] (int32
     indexes, -1 in both: none).  A child must be empty, listed once and nobody's
     parent; else nothing changes, and `status` says so."""
-    import torch
-
-    a = _state(refs, table, lengths, page_size)
-    a.n = children.shape[0] if children.dim() else 0
-    a.from_ = _vector(parents, "parents", (a.n,), torch.int32, table)
-    a.list = _vector(children, "children", (a.n,), torch.int32, table)
-    with _here(table.device, stream):
-        _run("uzip_cache_fork", a, table.device, workspace, status, check)
+    state = _state(refs, table, lengths)
+    dev, torch = state[3][4], _torch
+    if _elsewhere(dev, stream):
+        with _on(dev, stream):
+            return cache_fork(refs, table, lengths, parents, children, page_size, workspace=workspace, status=status, check=check)
+    n = children.numel()
+    _change(_FORK, state, page_size, workspace, status, check, n, _list(parents, "parents", (n,), torch.int32, dev),
+            _list(children, "children", (n,), torch.int32, dev))
 
 
 def cache_free(refs, table, lengths, sequences, page_size, *, workspace=None, status=None, check=False, stream=None):
     """The sequences listed (int32 indexes, each once, -1: none) become empty;
     pages that nobody shares are free.  Where an index is wrong nothing changes,
     and `status` says so."""
-    import torch
-
-    a = _state(refs, table, lengths, page_size)
-    a.n = sequences.shape[0] if sequences.dim() else 0
-    a.list = _vector(sequences, "sequences", (a.n,), torch.int32, table)
-    with _here(table.device, stream):
-        _run("uzip_cache_free", a, table.device, workspace, status, check)
+    state = _state(refs, table, lengths)
+    dev, torch = state[3][4], _torch
+    if _elsewhere(dev, stream):
+        with _on(dev, stream):
+            return cache_free(refs, table, lengths, sequences, page_size, workspace=workspace, status=status, check=check)
+    n = sequences.numel()
+    _change(_FREE, state, page_size, workspace, status, check, n, 0, _list(sequences, "sequences", (n,), torch.int32, dev))
 
 
 def cache_compact(refs, table, lengths, page_size, *, out=None, workspace=None, status=None, check=False, stream=None):
     """Moves the used pages to the front of the pool: updates refs and table and
     returns moves, int32 [pages // 2, 2] of {from, to} for cache_copy, -1 behind
     the last."""
-    import torch
-
-    a = _state(refs, table, lengths, page_size)
-    dev = table.device
-    with _here(dev, stream):
-        if out is None:
-            out = torch.empty((a.pages // 2, 2), dtype=torch.int32, device=dev)
-        a.pairs = _vector(out, "out", (a.pages // 2, 2), torch.int32, table)
-        _run("uzip_cache_compact", a, dev, workspace, status, check)
+    state = _state(refs, table, lengths)
+    pages, dev, torch = state[3][0], state[3][4], _torch
+    if _elsewhere(dev, stream):
+        with _on(dev, stream):
+            return cache_compact(refs, table, lengths, page_size, out=out, workspace=workspace, status=status, check=check)
+    if out is None:
+        out = torch.empty((pages // 2, 2), dtype=torch.int32, device=dev)
+    _change(_COMPACT, state, page_size, workspace, status, check, pairs=_list(out, "out", (pages // 2, 2), torch.int32, dev))
     return out
 
 
@@ -385,22 +496,27 @@ def cache_copy(k_pages, v_pages, pairs, *, to=None, status=None, check=False, st
     and sent; the same cache where not given.  Where a page does not exist, is
     written twice or (within a cache) also read, nothing is copied, and `status`
     says so."""
-    import torch
+    torch = _torch or _load()
+    layered = k_pages.dim() == 5
+    dev = _device(k_pages, "k_pages", 5 if layered else 4)
+    if _elsewhere(dev, stream):
+        with _on(dev, stream):
+            return cache_copy(k_pages, v_pages, pairs, to=to, status=status, check=check)
+    dt, code = k_pages.dtype, _dtype_code(k_pages)
+    shape = k_pages.shape
+    layers, (pages, heads, page, d) = (shape[0], shape[1:]) if layered else (1, shape)
 
-    if k_pages.dim() == 4:
-        k_pages, v_pages = k_pages[None], v_pages[None]
-        if to is not None:
-            to = to[0][None], to[1][None]
-    k, v = _pools(k_pages, v_pages, 5, None)
-    layers, pages, heads, page, d = k_pages.shape
-    a = CacheCopyArgs(_dtype_code(k_pages), 0, layers, heads, page, d, pages, pages, *k, *v, *k, *v)
+    def place(t, name, shape):  # address, and strides of layers, pages, heads, tokens
+        steps = _strides(t, name, shape, dt, dev)
+        return (t.data_ptr(), *steps[:4]) if layered else (t.data_ptr(), 0, *steps[:3])
+
+    k, v = place(k_pages, "k_pages", shape), place(v_pages, "v_pages", shape)
+    k_to, v_to, to_pages = k, v, pages
     if to is not None:
-        kt, vt = to
-        shape = (layers, kt.shape[1] if kt.dim() == 5 else -1, heads, page, d)
-        a.k_to, a.kt_layer, a.kt_page, a.kt_head, a.kt_token = _strided(kt, "to", shape, k_pages)
-        a.v_to, a.vt_layer, a.vt_page, a.vt_head, a.vt_token = _strided(vt, "to", shape, k_pages)
-        a.to_pages = shape[1]
-    a.n = pairs.shape[0] if pairs.dim() else 0
-    a.pairs = _vector(pairs, "pairs", (a.n, 2), torch.int32, k_pages)
-    with _here(k_pages.device, stream):
-        _run("uzip_cache_copy", a, k_pages.device, None, status, check)
+        _device(to[0], "to", len(shape))
+        to_pages = to[0].shape[-4]
+        into = (layers, to_pages, heads, page, d) if layered else (to_pages, heads, page, d)
+        k_to, v_to = place(to[0], "to", into), place(to[1], "to", into)
+    n = pairs.numel() // 2
+    _issue(_COPY, _COPY.pack(code, 0, layers, heads, page, d, pages, to_pages, *k, *v, *k_to, *v_to, _list(pairs, "pairs", (n, 2), torch.int32, dev), n),
+           dev, None, status, check)
