@@ -115,7 +115,7 @@ uzip_cache_copy, uzip_cache_copy_workspace_size = _entry("uzip_cache_copy", Cach
 # A step of a server makes these calls for every layer, so their host time
 # counts: arguments are packed in one go (struct, in the C structure's native
 # layout) instead of set one by one, and each tensor is asked for each thing
-# once (attention of one token 20 us of host time, 13 so).
+# once (attention of one token 20 us of host time, 14 so).
 
 class _Entry:
     """A C entry point that takes its structure as packed bytes."""
@@ -196,6 +196,11 @@ def _strides(t, name, shape, dtype, dev):
     if steps[-1] != 1 and shape[-1] > 1:
         _refuse(f"{name}: the last dimension must be contiguous")
     return steps
+
+
+def _new(like, shape):
+    """A contiguous tensor of a type and device."""
+    return _torch.empty_like(like) if like.is_contiguous() else _torch.empty(shape, dtype=like.dtype, device=like.device)
 
 
 def _list(t, name, shape, dtype, dev):
@@ -281,7 +286,7 @@ def _rotary(q, k, positions, freqs, interleaved, backward, scale, out, status, c
         shape = (t, h, d)
         row, head, _ = _strides(x, name, shape, dt, dev)
         if y is None:
-            y = torch.empty(shape, dtype=dt, device=dev)
+            y = _new(x, shape)
             steps = h * d, d, 1
         else:
             steps = _strides(y, "out", shape, dt, dev)
@@ -337,7 +342,7 @@ def rotary_append(q, k, v, positions, freqs, k_pages, v_pages, slots, *, interle
     kp, vp = _strides(k_pages, "k_pages", pool, dt, dev), _strides(v_pages, "v_pages", pool, dt, dev)
     pairs = freqs.numel()
     if out is None:
-        out = torch.empty((t, hq, d), dtype=dt, device=dev)
+        out = _new(q, shape)
         o_row, o_head = hq * d, d
     else:
         o_row, o_head, _ = _strides(out, "out", shape, dt, dev)
@@ -378,7 +383,7 @@ def paged_attention(q, k_pages, v_pages, table, lengths, *, scale=None, softcap=
     if table.shape[0] != s:
         _refuse(f"table has {table.shape[0]} rows for {s} queries")
     if out is None:
-        out = torch.empty((s, hq, d), dtype=dt, device=dev)
+        out = _new(q, shape)
         o_row, o_head = hq * d, d
     else:
         o_row, o_head, _ = _strides(out, "out", shape, dt, dev)

@@ -18,13 +18,28 @@ namespace uzip {
 namespace {
 
 constexpr uint32_t kWarps = 4, kThreads = kWarps * 32;
-constexpr int kAhead = 4;  // heads whose values are in flight in a lane
+constexpr int kAhead = 2;  // heads whose values are in flight in a lane
 
-// Radians per position as a fraction of a turn, modulo 1, in units of 2^-64.
+// Radians per position as a fraction of a turn, modulo 1, in units of 2^-64: the
+// 53 bits of the number times 2^66 / (2 pi) in integers, shifted to its exponent
+// (fp64 arithmetic would take longer than the rest of a token).
 __device__ __forceinline__ uint64_t turns_of(double radians) {
-    double t = radians * 0.15915494309189533577;
-    t -= rint(t);
-    return uint64_t(__double2ll_rn(t * 18446744073709551616.0));
+    constexpr uint64_t kPerTurn = 0xA2F9836E4E44152Aull;  // 2^66 / (2 pi)
+    const uint64_t bits = uint64_t(__double_as_longlong(radians));
+    const int e = int(bits >> 52 & 0x7FF);
+    const uint64_t m = (bits & ((1ull << 52) - 1)) | (e ? 1ull << 52 : 0);
+    const uint64_t hi = __umul64hi(m, kPerTurn), lo = m * kPerTurn;
+    const int right = 1075 + 2 - max(e, 1);  // radians = m 2^(e - 1075)
+    uint64_t t = 0;
+    if (right >= 128 || right <= -64)
+        t = 0;
+    else if (right >= 64)
+        t = hi >> (right - 64);
+    else if (right > 0)
+        t = hi << (64 - right) | lo >> right;
+    else
+        t = lo << -right;
+    return bits >> 63 ? 0 - t : t;
 }
 
 template <int V>
@@ -46,22 +61,49 @@ template <int V>
 union Values {
     typename Piece<V>::T piece;
     uint16_t v[V];
+    uint32_t w[V > 1 ? V / 2 : 1];
 };
 
 template <bool BF>
-__device__ __forceinline__ float value(uint16_t v) {
-    return BF ? __uint_as_float(uint32_t(v) << 16) : __half2float(__ushort_as_half(v));
+__device__ __forceinline__ float2 two(uint32_t w) {
+    if constexpr (BF) return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+    return __half22float2(*reinterpret_cast<const __half2*>(&w));
 }
 template <bool BF>
-__device__ __forceinline__ uint16_t rounded(float v) {
-    return to16(v, BF ? UZIP_BF16 : UZIP_FP16);
+__device__ __forceinline__ uint32_t rounded(float lo, float hi) {
+    if constexpr (BF) {
+        const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
+        return *reinterpret_cast<const uint32_t*>(&b);
+    }
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-template <bool BF>
-__device__ __forceinline__ void turn(uint16_t& x, uint16_t& y, float2 cs) {
-    const float u = value<BF>(x), w = value<BF>(y);
-    x = rounded<BF>(u * cs.x - w * cs.y);
-    y = rounded<BF>(u * cs.y + w * cs.x);
+// Turns the pairs that two pieces hold; pairs from `live` on stay as they are.
+template <int V, bool INTER, bool BF>
+__device__ __forceinline__ void turn(Values<V>& x, Values<V>& y, const float2 (&t)[V], int live) {
+    if constexpr (V == 1) {
+        if (live < 1) return;
+        const float u = two<BF>(x.v[0]).x, w = two<BF>(y.v[0]).x;
+        const uint32_t r = rounded<BF>(u * t[0].x - w * t[0].y, u * t[0].y + w * t[0].x);
+        x.v[0] = uint16_t(r), y.v[0] = uint16_t(r >> 16);
+    } else if constexpr (INTER) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            if (i >= live) continue;
+            uint32_t& word = i < V / 2 ? x.w[i] : y.w[i - V / 2];
+            const float2 f = two<BF>(word);
+            word = rounded<BF>(f.x * t[i].x - f.y * t[i].y, f.x * t[i].y + f.y * t[i].x);
+        }
+    } else {
+        if (live < V) return;  // pieces are turned as a whole
+#pragma unroll
+        for (int i = 0; i < V; i += 2) {
+            const float2 u = two<BF>(x.w[i / 2]), w = two<BF>(y.w[i / 2]);
+            x.w[i / 2] = rounded<BF>(u.x * t[i].x - w.x * t[i].y, u.y * t[i + 1].x - w.y * t[i + 1].y);
+            y.w[i / 2] = rounded<BF>(u.x * t[i].y + w.x * t[i].x, u.y * t[i + 1].y + w.y * t[i + 1].x);
+        }
+    }
 }
 
 // An item is two pieces of V neighbouring values of a head with the V pairs
@@ -69,93 +111,70 @@ __device__ __forceinline__ void turn(uint16_t& x, uint16_t& y, float2 cs) {
 // (interleaved); behind the rotated part, two neighbouring pieces.
 template <int V, bool INTER, bool BF>
 __global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant__ Rotary a, int splits) {
+    using Word = typename Piece<V>::T;
     extern __shared__ float2 shared_cs[];  // [warps][half]
     wait_for_launch_before();
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+    const uint64_t job = blockIdx.x * uint64_t(kWarps) + warp;
+    if (job >= uint64_t(a.t) * splits) return;
+    const int64_t token = job / splits;
+    const int share = int(job - token * splits);
+    const uint64_t pos = uint64_t(a.positions[token]);
+    const int64_t slot = a.slots ? a.slots[token] : -1;
     float2* cs = shared_cs + warp * a.half;
+    for (int j = lane; j < a.half; j += 32) {
+        const uint64_t turns = pos * turns_of(a.freqs[j]);
+        float s, c;
+        sincospif(float(int32_t((turns + 0x80000000ull) >> 32)) * 0x1p-31f, &s, &c);
+        cs[j] = make_float2(c * a.scale, s * a.scale * a.sign);
+    }
+    int64_t page = -1, off = 0;
+    if (slot >= 0 && slot < a.slot_count) {
+        page = slot / a.page, off = slot - page * a.page;
+    } else if (slot != -1 && a.status && lane == 0) {
+        *a.status = UZIP_ERR_INVALID_ARG;
+    }
+    __syncwarp();
     const int turned_items = INTER ? 0 : a.half / V;  // halves: rotated items first
     const int items = INTER ? (a.d + 2 * V - 1) / (2 * V) : turned_items + (a.d - 2 * a.half + 2 * V - 1) / (2 * V);
-    const int across = max(1, 32 / items);  // heads that a warp takes at once
-    const uint64_t stride = uint64_t(gridDim.x) * kWarps;
-    // frequencies of this lane's first pairs are kept; heads of more than 128 pairs convert the others again
-    uint64_t freq[4];
+    const int across = max(1, 32 / items), lanes = min(items, 32);  // heads that a warp takes at once
+    if (lane >= across * lanes) return;                              // lanes that no whole head is left for
+    const int first = share * across + lane / lanes, step = splits * across;
+    for (int item = lane % lanes; item < items; item += 32) {
+        const bool plain = !INTER && item >= turned_items;
+        const int e0 = INTER ? 2 * V * item : plain ? 2 * a.half + 2 * V * (item - turned_items) : V * item;
+        const int e1 = INTER || plain ? e0 + V : a.half + V * item;
+        const bool both = e1 < a.d;
+        const int live = plain ? 0 : min(V, a.half - V * item);
+        float2 t[V];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) freq[k] = lane + 32 * k < a.half ? turns_of(a.freqs[lane + 32 * k]) : 0;
-    for (uint64_t job = blockIdx.x * uint64_t(kWarps) + warp; job < uint64_t(a.t) * splits; job += stride) {
-        const int64_t token = job / splits;
-        const int share = int(job % splits);
-        const uint64_t pos = uint64_t(a.positions[token]);
-        __syncwarp();
-        for (int k = 0; k * 32 < a.half; ++k) {
-            const int j = k * 32 + lane;
-            if (j >= a.half) break;
-            const uint64_t f = k == 0 ? freq[0] : k == 1 ? freq[1] : k == 2 ? freq[2] : k == 3 ? freq[3] : turns_of(a.freqs[j]);
-            float s, c;
-            sincospif(float(int32_t((pos * f + 0x80000000ull) >> 32)) * 0x1p-31f, &s, &c);
-            cs[j] = make_float2(c * a.scale, s * a.scale * a.sign);
-        }
-        __syncwarp();
-        int64_t page = -1, off = 0;
-        if (a.slots) {
-            const int64_t slot = a.slots[token];
-            if (slot >= 0 && slot < a.slot_count) {
-                page = slot / a.page, off = slot - page * a.page;
-            } else if (slot != -1 && a.status && lane == 0) {
-                *a.status = UZIP_ERR_INVALID_ARG;
-            }
-        }
-        for (int item = lane % min(items, 32); item < items; item += 32) {
-            if (lane >= across * items) break;  // lanes that no whole head is left for
-            const bool plain = !INTER && item >= turned_items;
-            const int e0 = INTER ? 2 * V * item : plain ? 2 * a.half + 2 * V * (item - turned_items) : V * item;
-            const int e1 = INTER || plain ? e0 + V : a.half + V * item;
-            const bool both = e1 < a.d;
-            const int pair0 = V * item;
-            float2 t[V];
+        for (int i = 0; i < V; ++i) t[i] = i < live ? cs[V * item + i] : make_float2(1.f, 0.f);
+        // kAhead heads are loaded before the first is stored (an output may be its input, so the compiler would not move
+        // a load over a store)
 #pragma unroll
-            for (int i = 0; i < V; ++i) t[i] = !plain && pair0 + i < a.half ? cs[pair0 + i] : make_float2(1.f, 0.f);
-            // heads of this warp's share, `across` of them at once; kAhead of those are loaded before the first is
-            // stored (an output may be its input, so the compiler would not move a load over a store)
-            const int step = splits * across;
-            for (int head = share * across + lane / min(items, 32); head < a.heads; head += kAhead * step) {
+        for (int n = 0; n < 3; ++n) {
+            const RotarySegment& g = a.seg[n];
+            if (g.paged && page < 0) continue;
+            const uint16_t* from = g.from + token * g.row + first * g.head;
+            uint16_t* to = g.to + (g.paged ? page * g.to_row + off * g.to_token : token * g.to_row) + first * g.to_head;
+            for (int head = first; head < g.heads; head += kAhead * step) {
                 Values<V> x[kAhead], y[kAhead];
-                uint16_t* to[kAhead];
-                bool turned[kAhead];
 #pragma unroll
                 for (int u = 0; u < kAhead; ++u) {
-                    int h = head + u * step, n = 0;
-                    to[u] = nullptr;
-                    if (h >= a.heads) continue;
-                    if (h >= a.seg[0].heads) {
-                        h -= a.seg[0].heads, n = 1;
-                        if (h >= a.seg[1].heads) h -= a.seg[1].heads, n = 2;
-                    }
-                    const RotarySegment& g = a.seg[n];
-                    if (g.paged && page < 0) continue;
-                    turned[u] = g.turned;
-                    to[u] = g.to + h * g.to_head + (g.paged ? page * g.to_row + off * g.to_token : token * g.to_row);
-                    const uint16_t* from = g.from + token * g.row + h * g.head;
-                    x[u].piece = *reinterpret_cast<const typename Piece<V>::T*>(from + e0);
-                    if (both) y[u].piece = *reinterpret_cast<const typename Piece<V>::T*>(from + e1);
+                    if (head + u * step >= g.heads) continue;
+                    const uint16_t* at = from + u * step * g.head;
+                    x[u].piece = *reinterpret_cast<const Word*>(at + e0);
+                    if (both) y[u].piece = *reinterpret_cast<const Word*>(at + e1);
                 }
 #pragma unroll
                 for (int u = 0; u < kAhead; ++u) {
-                    if (!to[u]) continue;
-                    if (turned[u] && !plain) {
-#pragma unroll
-                        for (int i = 0; i < V; ++i) {
-                            if (pair0 + i >= a.half) continue;
-                            if constexpr (!INTER || V == 1)
-                                turn<BF>(x[u].v[i], y[u].v[i], t[i]);
-                            else if (i < V / 2)
-                                turn<BF>(x[u].v[(2 * i) % V], x[u].v[(2 * i + 1) % V], t[i]);
-                            else
-                                turn<BF>(y[u].v[(2 * i) % V], y[u].v[(2 * i + 1) % V], t[i]);
-                        }
-                    }
-                    *reinterpret_cast<typename Piece<V>::T*>(to[u] + e0) = x[u].piece;
-                    if (both) *reinterpret_cast<typename Piece<V>::T*>(to[u] + e1) = y[u].piece;
+                    if (head + u * step >= g.heads) continue;
+                    if (g.turned) turn<V, INTER, BF>(x[u], y[u], t, live);
+                    uint16_t* at = to + u * step * g.to_head;
+                    *reinterpret_cast<Word*>(at + e0) = x[u].piece;
+                    if (both) *reinterpret_cast<Word*>(at + e1) = y[u].piece;
                 }
+                from += kAhead * step * g.head, to += kAhead * step * g.to_head;
             }
         }
     }
@@ -169,7 +188,7 @@ cudaError_t launch_as(const Rotary& r, int sms, cudaStream_t s) {
     // enough warps for every SM (16 each): few tokens have their heads split, down to one step of a warp
     const int64_t want = int64_t(sms) * 16;
     const int splits = int(std::max<int64_t>(1, std::min<int64_t>(most, want / std::max<int64_t>(1, r.t))));
-    const int64_t blocks = std::min<int64_t>((r.t * splits + kWarps - 1) / kWarps, int64_t(sms) * 16);
+    const int64_t blocks = (r.t * splits + kWarps - 1) / kWarps;
     return launch_next(rotary_kernel<V, INTER, BF>, dim3(uint32_t(blocks)), kThreads, uint32_t(kWarps * std::max(1, r.half) * sizeof(float2)), 1,
                        s, r, splits);
 }
