@@ -111,21 +111,23 @@ struct Reserve {
     int64_t tokens;
     int64_t *slots, *positions;
     int32_t* copies;
-    // workspace
+    // workspace, or null where reserve_keeps()
     int32_t* first;   // [seqs] new pages of the sequences before
     int64_t* begin;   // [seqs] new tokens of the sequences before
     int32_t* before;  // [seqs] length before
-    int32_t* held;    // [seqs] 2 * pages before + whether the last is copied
+    int32_t* held;    // [seqs] pages before, ~ of it where the last is copied
     int32_t* fresh;   // [list] pages taken, ascending
     int64_t list;
 };
+bool reserve_keeps(int64_t seqs, int64_t pages, int64_t tokens, int64_t list);
 cudaError_t launch_reserve(const Reserve& r, cudaStream_t s);
 struct Fork {
     CacheState c;
     const int32_t *parents, *children;  // parents null: free the children
     int64_t n;
-    int32_t* mark;  // [seqs] workspace
+    int32_t* mark;  // [seqs] workspace, or null where fork_keeps()
 };
+bool fork_keeps(int64_t seqs, int64_t n, int64_t width);
 cudaError_t launch_fork(const Fork& f, cudaStream_t s);
 struct Compact {
     CacheState c;

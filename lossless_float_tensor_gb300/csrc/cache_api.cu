@@ -219,6 +219,7 @@ CacheState state_of(const uzip_cache_args& a, int32_t* d_status) {
 Reserve plan_reserve(const uzip_cache_args& a, Work& w) {
     Reserve r{};
     r.list = std::min(a.pages, 2 * a.tokens);
+    if (reserve_keeps(a.seqs, a.pages, a.tokens, r.list)) return r;
     r.first = w.take<int32_t>(a.seqs), r.begin = w.take<int64_t>(a.seqs), r.before = w.take<int32_t>(a.seqs);
     r.held = w.take<int32_t>(a.seqs), r.fresh = w.take<int32_t>(r.list);
     return r;
@@ -234,7 +235,7 @@ uzip_status fork(const uzip_cache_args* a, void* ws, uint64_t bytes, int32_t* d_
     if (!a || !state_ok(*a, true) || !within(a->n, 0, kMost31) || !list_ok(a->list, a->n) || (with_parents && !list_ok(a->from, a->n)))
         return UZIP_ERR_INVALID_ARG;
     Work need{nullptr};
-    need.take<int32_t>(a->seqs);
+    if (!fork_keeps(a->seqs, a->n, a->width)) need.take<int32_t>(a->seqs);
     uzip_status st = check_work(need.used, ws, bytes, d_status);
     if (st != UZIP_OK) return st;
     cudaError_t err = clear_status(d_status, s);
@@ -242,7 +243,7 @@ uzip_status fork(const uzip_cache_args* a, void* ws, uint64_t bytes, int32_t* d_
     Fork f{};
     f.c = state_of(*a, d_status);
     f.parents = with_parents ? a->from : nullptr, f.children = a->list, f.n = a->n;
-    f.mark = static_cast<int32_t*>(ws);
+    f.mark = need.used ? static_cast<int32_t*>(ws) : nullptr;
     return finish(launch_fork(f, s));
 }
 
@@ -340,7 +341,7 @@ uzip_status uzip_cache_reserve(const uzip_cache_args* a, void* d_workspace, uint
 }
 
 uint64_t uzip_cache_fork_workspace_size(const uzip_cache_args* a) {
-    if (!a || !state_ok(*a, false)) return 0;
+    if (!a || !state_ok(*a, false) || a->n < 0 || fork_keeps(a->seqs, a->n, a->width)) return 0;
     Work w{nullptr};
     w.take<int32_t>(a->seqs);
     return w.used;

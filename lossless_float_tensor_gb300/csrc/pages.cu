@@ -16,6 +16,7 @@ namespace uzip {
 namespace {
 
 constexpr uint32_t kThreads = 1024, kWarps = kThreads / 32;
+static_assert(kWarps == 32, "prefix() has one warp add up the others' sums, one a lane");
 constexpr uint32_t kCluster = 8;
 
 __device__ __forceinline__ uint32_t cluster_rank() {
@@ -102,8 +103,18 @@ __device__ bool any_of(bool mine, int64_t* flag, uint32_t blocks) {
     return any;
 }
 
-__device__ __forceinline__ int pages_of(int64_t tokens, int page) { return int((tokens + page - 1) / page); }
+__device__ __forceinline__ int pages_of(int tokens, int page) { return int((uint32_t(tokens) + uint32_t(page - 1)) / uint32_t(page)); }
 __device__ __forceinline__ bool length_ok(const CacheState& c, int n) { return n >= 0 && n <= int64_t(c.width) * c.page; }
+// Whether an entry of a row, every 32nd from `col` on, is no page in use.
+__device__ __forceinline__ bool pages_bad(const CacheState& c, int64_t row, int col, int end) {
+    bool bad = false;
+#pragma unroll 4
+    for (; col < end; col += 32) {
+        const int p = c.table[row * c.ldt + col];
+        bad |= uint32_t(p) >= uint32_t(c.pages) || c.refs[p] < 1;
+    }
+    return bad;
+}
 __device__ __forceinline__ void report(const CacheState& c, int what) {
     if (c.status && cluster_rank() == 0 && threadIdx.x == 0) *c.status = what;
 }
@@ -129,9 +140,16 @@ __global__ void __launch_bounds__(kThreads) reserve_kernel(const __grid_constant
     wait_for_launch_before();
     __shared__ PrefixRoom<3> room;
     __shared__ int64_t flag;
+    extern __shared__ int64_t own[];
     const CacheState& c = a.c;
     const uint32_t blocks = gridDim.x, rank = blocks > 1 ? cluster_rank() : 0;
     const int64_t threads = int64_t(blocks) * kThreads, me = int64_t(rank) * kThreads + threadIdx.x;
+    // lists of the sequences and of the pages taken: one block keeps them to itself
+    int64_t* const begin_of = a.begin ? a.begin : own;
+    int32_t* const first_of = a.begin ? a.first : reinterpret_cast<int32_t*>(own + c.seqs);
+    int32_t* const before = a.begin ? a.before : first_of + c.seqs;
+    int32_t* const held_of = a.begin ? a.held : before + c.seqs;
+    int32_t* const fresh = a.begin ? a.fresh : held_of + c.seqs;
     const int64_t seqs_each = (c.seqs + threads - 1) / threads, pages_each = ((c.pages + threads - 1) / threads + 3) / 4 * 4;
     const int s0 = int(min(int64_t(c.seqs), me * seqs_each)), s1 = int(min(int64_t(c.seqs), s0 + seqs_each));
     const int p0 = int(min(int64_t(c.pages), me * pages_each)), p1 = int(min(int64_t(c.pages), p0 + pages_each));
@@ -161,8 +179,8 @@ __global__ void __launch_bounds__(kThreads) reserve_kernel(const __grid_constant
                 cow = c.refs[last] > 1;
         }
         mine[0] += want - have + cow;
-        a.before[i] = n;
-        a.held[i] = 2 * have + cow;
+        before[i] = n;
+        held_of[i] = cow ? ~have : have;  // pages before; ~ where the last of them is copied
     }
     for (int p = p0; p < p1; ++p) mine[2] += c.refs[p] == 0;
     const Prefix<3> sum = prefix(mine, room, rank, blocks);
@@ -179,14 +197,14 @@ __global__ void __launch_bounds__(kThreads) reserve_kernel(const __grid_constant
     {
         int64_t first = sum.before[0], begin = sum.before[1];
         for (int i = s0; i < s1; ++i) {
-            a.first[i] = int32_t(first), a.begin[i] = begin;
-            const int n = c.lengths[i], count = a.counts[i], held = a.held[i];
-            first += pages_of(int64_t(n) + count, c.page) - held / 2 + held % 2;
+            first_of[i] = int32_t(first), begin_of[i] = begin;
+            const int n = c.lengths[i], count = a.counts[i], held = held_of[i];
+            first += pages_of(n + count, c.page) - (held < 0 ? ~held - 1 : held);
             begin += count;
         }
         int64_t free = sum.before[2];
         for (int p = p0; p < p1 && free < sum.total[0]; ++p)
-            if (c.refs[p] == 0) a.fresh[free++] = p;
+            if (c.refs[p] == 0) fresh[free++] = p;
     }
     if (blocks > 1)
         cluster_meet();
@@ -194,9 +212,9 @@ __global__ void __launch_bounds__(kThreads) reserve_kernel(const __grid_constant
         __syncthreads();
     // each new page goes to its place
     for (int64_t r = me; r < sum.total[0]; r += threads) {
-        const int i = last_at_most(a.first, c.seqs, r);
-        const int p = a.fresh[r], cow = a.held[i] % 2, in = int(r - a.first[i]);
-        int32_t* place = c.table + i * c.ldt + a.held[i] / 2 + in - cow;
+        const int i = last_at_most(first_of, c.seqs, r);
+        const int p = fresh[r], held = held_of[i], cow = held < 0, in = int(r - first_of[i]);
+        int32_t* place = c.table + i * c.ldt + (cow ? ~held - 1 : held) + in;
         if (cow && in == 0) {
             const int old = *place;
             a.copies[2 * i] = old, a.copies[2 * i + 1] = p;
@@ -206,18 +224,19 @@ __global__ void __launch_bounds__(kThreads) reserve_kernel(const __grid_constant
         c.refs[p] = 1;
     }
     for (int i = s0; i < s1; ++i) {
-        c.lengths[i] = a.before[i] + a.counts[i];
-        if (a.held[i] % 2 == 0) a.copies[2 * i] = -1, a.copies[2 * i + 1] = -1;
+        c.lengths[i] = before[i] + a.counts[i];
+        if (held_of[i] >= 0) a.copies[2 * i] = -1, a.copies[2 * i + 1] = -1;
     }
     for (int64_t t = me; t < a.tokens; t += threads) {
-        int64_t slot = -1, pos = 0;
+        int64_t slot = -1;
+        int pos = 0;
         if (t < sum.total[1]) {
-            const int i = last_at_most(a.begin, c.seqs, t);
-            pos = a.before[i] + (t - a.begin[i]);
-            const int col = int(pos / c.page), have = a.held[i] / 2, cow = a.held[i] % 2;
+            const int i = last_at_most(begin_of, c.seqs, t);
+            pos = before[i] + int(t - begin_of[i]);
+            const int col = int(uint32_t(pos) / uint32_t(c.page)), held = held_of[i], kept = held < 0 ? ~held - 1 : held;
             // entries that this call writes are read from the list, the others from the table
-            const int p = col >= have - cow ? a.fresh[a.first[i] + col - have + cow] : c.table[i * c.ldt + col];
-            slot = int64_t(p) * c.page + pos % c.page;
+            const int p = col >= kept ? fresh[first_of[i] + col - kept] : c.table[i * c.ldt + col];
+            slot = int64_t(p) * c.page + (pos - col * c.page);
         }
         a.slots[t] = slot, a.positions[t] = pos;
     }
@@ -233,9 +252,11 @@ __global__ void __launch_bounds__(kThreads) fork_kernel(const __grid_constant__ 
     const uint32_t blocks = gridDim.x, rank = blocks > 1 ? cluster_rank() : 0;
     const int64_t threads = int64_t(blocks) * kThreads, me = int64_t(rank) * kThreads + threadIdx.x;
     const int lane = threadIdx.x % 32;
+    extern __shared__ int64_t own[];
+    int32_t* const mark = a.mark ? a.mark : reinterpret_cast<int32_t*>(own);  // one block keeps it to itself
     for (int64_t j = me; j < a.n; j += threads) {
         const int s = a.children[j];
-        if (s >= 0 && s < c.seqs) a.mark[s] = int32_t(j);
+        if (s >= 0 && s < c.seqs) mark[s] = int32_t(j);
     }
     if (blocks > 1)
         cluster_meet();
@@ -248,7 +269,7 @@ __global__ void __launch_bounds__(kThreads) fork_kernel(const __grid_constant__ 
             bad = true;
             continue;
         }
-        if (s >= 0) bad |= a.mark[s] != int32_t(j);
+        if (s >= 0) bad |= mark[s] != int32_t(j);
         if (a.parents) {
             const int from = a.parents[j];
             if (from < -1 || from >= c.seqs || (from < 0) != (s < 0)) {
@@ -257,7 +278,7 @@ __global__ void __launch_bounds__(kThreads) fork_kernel(const __grid_constant__ 
             }
             if (s < 0) continue;
             bad |= c.lengths[s] != 0;
-            const uint32_t listed = uint32_t(a.mark[from]);  // says something only where that entry lists it
+            const uint32_t listed = uint32_t(mark[from]);  // says something only where that entry lists it
             bad |= listed < a.n && a.children[listed] == from;
             bad |= !length_ok(c, c.lengths[from]);
         } else if (s >= 0) {
@@ -272,10 +293,7 @@ __global__ void __launch_bounds__(kThreads) fork_kernel(const __grid_constant__ 
         const int s = a.parents ? a.parents[j] : a.children[j];
         if (s < 0 || s >= c.seqs || !length_ok(c, c.lengths[s])) continue;
         const int begin = int(job % pieces) * 256, end = min(begin + 256, pages_of(c.lengths[s], c.page));
-        for (int col = begin + lane; col < end; col += 32) {
-            const int p = c.table[s * c.ldt + col];
-            bad |= uint32_t(p) >= uint32_t(c.pages) || c.refs[p] < 1;
-        }
+        bad |= pages_bad(c, s, begin + lane, end);
     }
     if (any_of(bad, &flag, blocks)) {
         report(c, UZIP_ERR_INVALID_ARG);
@@ -285,6 +303,7 @@ __global__ void __launch_bounds__(kThreads) fork_kernel(const __grid_constant__ 
             const int s = a.children[j], from = a.parents ? a.parents[j] : s;
             if (s < 0) continue;
             const int begin = int(job % pieces) * 256, used = pages_of(c.lengths[from], c.page);
+#pragma unroll 4
             for (int col = begin + lane; col < min(begin + 256, c.width); col += 32) {
                 int p = -1;
                 if (col < used) {
@@ -322,17 +341,13 @@ __global__ void __launch_bounds__(kThreads) compact_kernel(const __grid_constant
         bad |= r < 0;
         mine[0] += r > 0;
     }
-    const int64_t warps = threads / 32;
-    for (int64_t s = me / 32; s < c.seqs; s += warps) {
-        const int n = c.lengths[s];
-        if (!length_ok(c, n)) {
-            bad = true;
-            continue;
-        }
-        for (int col = lane; col < pages_of(n, c.page); col += 32) {
-            const int p = c.table[s * c.ldt + col];
-            bad |= uint32_t(p) >= uint32_t(c.pages) || c.refs[p] < 1;
-        }
+    // a warp takes 256 columns of a row at a time
+    const int pieces = (c.width + 255) / 256;
+    const int64_t jobs = int64_t(c.seqs) * pieces, warps = threads / 32;
+    for (int64_t s = me; s < c.seqs; s += threads) bad |= !length_ok(c, c.lengths[s]);
+    for (int64_t job = me / 32; job < jobs; job += warps) {
+        const int s = int(job / pieces), begin = int(job % pieces) * 256, n = c.lengths[s];
+        if (length_ok(c, n)) bad |= pages_bad(c, s, begin + lane, min(begin + 256, pages_of(n, c.page)));
     }
     const Prefix<1> used = prefix(mine, room, rank, blocks);
     const int64_t kept = used.total[0];  // pages used: they end up below this
@@ -373,9 +388,11 @@ __global__ void __launch_bounds__(kThreads) compact_kernel(const __grid_constant
         cluster_meet();
     else
         __syncthreads();
-    for (int64_t s = me / 32; s < c.seqs; s += warps) {
-        const int n = pages_of(c.lengths[s], c.page);
-        for (int col = lane; col < n; col += 32) {
+    for (int64_t job = me / 32; job < jobs; job += warps) {
+        const int64_t s = job / pieces;
+        const int begin = int(job % pieces) * 256, end = min(begin + 256, pages_of(c.lengths[s], c.page));
+#pragma unroll 4
+        for (int col = begin + lane; col < end; col += 32) {
             int32_t* place = c.table + s * c.ldt + col;
             if (*place >= kept) *place = a.to[*place];
         }
@@ -385,7 +402,7 @@ __global__ void __launch_bounds__(kThreads) compact_kernel(const __grid_constant
 
 // A chain of short steps on few values: one block has no cluster barriers to
 // wait for, eight have eight times the threads.
-uint32_t cluster_for(int64_t items) { return items <= 8 * int64_t(kThreads) ? 1 : kCluster; }
+uint32_t cluster_for(int64_t items) { return items <= 2 * int64_t(kThreads) ? 1 : kCluster; }
 
 // ---- copies -----------------------------------------------------------------------
 
@@ -465,16 +482,27 @@ __global__ void __launch_bounds__(kCopyThreads) copy_kernel(const __grid_constan
 
 }  // namespace
 
-cudaError_t launch_reserve(const Reserve& r, cudaStream_t s) {
-    const uint32_t blocks = cluster_for(std::max<int64_t>({r.c.seqs, r.c.pages / 4, r.tokens}));
-    return launch_next(reserve_kernel, dim3(blocks), kThreads, 0, blocks, s, r);
+// Lists that one block can keep in shared memory need no workspace.
+constexpr int64_t kOwn = 40 * 1024;
+
+static uint32_t reserve_blocks(int64_t seqs, int64_t pages, int64_t tokens) {
+    return cluster_for(std::max<int64_t>({seqs, pages / 8, tokens}));
 }
+bool reserve_keeps(int64_t seqs, int64_t pages, int64_t tokens, int64_t list) {
+    return reserve_blocks(seqs, pages, tokens) == 1 && 20 * seqs + 4 * list <= kOwn;
+}
+cudaError_t launch_reserve(const Reserve& r, cudaStream_t s) {
+    const uint32_t blocks = reserve_blocks(r.c.seqs, r.c.pages, r.tokens);
+    return launch_next(reserve_kernel, dim3(blocks), kThreads, r.begin ? 0 : uint32_t(20 * r.c.seqs + 4 * r.list), blocks, s, r);
+}
+static uint32_t fork_blocks(int64_t n, int64_t width) { return cluster_for(n * ((width + 255) / 256) * 32); }
+bool fork_keeps(int64_t seqs, int64_t n, int64_t width) { return fork_blocks(n, width) == 1 && 4 * seqs <= kOwn; }
 cudaError_t launch_fork(const Fork& f, cudaStream_t s) {
-    const uint32_t blocks = cluster_for(f.n * ((f.c.width + 255) / 256) * 32);
-    return launch_next(fork_kernel, dim3(blocks), kThreads, 0, blocks, s, f);
+    const uint32_t blocks = fork_blocks(f.n, f.c.width);
+    return launch_next(fork_kernel, dim3(blocks), kThreads, f.mark ? 0 : uint32_t(4 * f.c.seqs), blocks, s, f);
 }
 cudaError_t launch_compact(const Compact& m, cudaStream_t s) {
-    const uint32_t blocks = cluster_for(std::max<int64_t>(m.c.pages / 4, int64_t(m.c.seqs) * 32));
+    const uint32_t blocks = cluster_for(std::max<int64_t>(m.c.pages / 4, int64_t(m.c.seqs) * ((m.c.width + 255) / 256) * 32));
     return launch_next(compact_kernel, dim3(blocks), kThreads, 0, blocks, s, m);
 }
 

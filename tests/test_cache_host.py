@@ -142,8 +142,12 @@ def test_workspace_only_where_something_is_kept(cache):
     assert size(_attention(cache, width=1 << 20, seqs=1000)) == long
     assert size(_attention(cache, width=1 << 20, d=12)) == 0
     up = lambda v: -(-v // 256) * 256  # noqa: E731
-    assert cache.uzip_cache_reserve_workspace_size(_state(cache, seqs=1000, pages=5000, tokens=100)) == 3 * up(4000) + up(8000) + up(800)
-    assert cache.uzip_cache_fork_workspace_size(_state(cache, seqs=1000)) == up(4000)
+    reserve, fork = cache.uzip_cache_reserve_workspace_size, cache.uzip_cache_fork_workspace_size
+    assert reserve(_state(cache, seqs=1000, pages=5000, tokens=100)) == 0  # lists that one block keeps to itself
+    assert reserve(_state(cache, seqs=3000, pages=5000, tokens=100)) == 3 * up(12000) + up(24000) + up(800)
+    assert reserve(_state(cache, seqs=1000, pages=5000, tokens=100000)) == 3 * up(4000) + up(8000) + up(20000)
+    assert fork(_state(cache, seqs=1000)) == 0
+    assert fork(_state(cache, seqs=20000)) == up(80000) and fork(_state(cache, seqs=1000, n=1000)) == up(4000)
     assert cache.uzip_cache_compact_workspace_size(_state(cache, pages=5000)) == 2 * up(10000) + up(20000)
 
 
