@@ -486,49 +486,74 @@ __global__ void __launch_bounds__(kThreads, Shape<DP>::kBlocks) attention_kernel
 }
 
 // Joins the parts of a row that borders cut, in the order of its tokens: block
-// (border, 512 of the row's results), four results a thread.
-template <bool BF>
+// (border, 512 of the row's results), four results a lane.  With SPLIT, where one
+// row has dozens of parts and their loads are what this waits for: block (border,
+// 128 results), each warp a quarter of the parts, and the first the warps' sums.
+template <bool BF, bool SPLIT>
 __global__ void __launch_bounds__(kThreads) join_kernel(const __grid_constant__ Attention a, int kept) {
     wait_for_launch_before();
     const int4 r = a.record[blockIdx.x + 1];
     if (r.x < 0) return;
+    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
     const int blk = r.y % a.blocks, heads = min(kept, a.group - blk * kept);
-    const int at = 4 * (blockIdx.y * int(kThreads) + threadIdx.x), h = at / a.d, e = at - h * a.d;
-    if (h >= heads) return;
-    float top = -INFINITY, sum = 0.f, val[4] = {};
-    constexpr int kAhead = 8;
-    for (int b0 = r.z; b0 <= r.w; b0 += kAhead) {
+    const int at = 4 * int(blockIdx.y * (SPLIT ? 32 : kThreads) + (SPLIT ? lane : threadIdx.x)), h = at / a.d, e = at - h * a.d;
+    struct Sums {
+        float top, sum, val[4];
+        __device__ void scale_to(float now) {
+            const float by = weight(top, now);
+            top = now, sum *= by;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) val[c] *= by;
+        }
+        __device__ void add(float m, float l, const float (&o)[4]) {
+            const float w = weight(m, top);
+            sum += l * w;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) val[c] += o[c] * w;
+        }
+    };
+    Sums s{-INFINITY, 0.f, {}};
+    const int each = SPLIT ? (r.w - r.z + int(kWarps)) / int(kWarps) : r.w + 1 - r.z;
+    const int begin = SPLIT ? r.z + warp * each : r.z, end = min(r.w + 1, begin + each);
+    constexpr int kAhead = SPLIT ? 8 : 4;
+    for (int b0 = begin; h < heads && b0 < end; b0 += kAhead) {
         float2 ml[kAhead];
         float4 o[kAhead];
 #pragma unroll
         for (int n = 0; n < kAhead; ++n) {
             const int b = b0 + n;
             ml[n] = make_float2(-INFINITY, 0.f), o[n] = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (b > r.w) continue;
+            if (b >= end) continue;
             // the first part lies where its block's last one does, the others where a block's first does
             const int64_t part = (2 * int64_t(b) + (b == r.z)) * kept + h;
             ml[n] = a.part_ml[part];
             o[n] = *reinterpret_cast<const float4*>(a.part_o + part * a.d + e);
         }
-        float now = top;
+        float now = s.top;
 #pragma unroll
         for (int n = 0; n < kAhead; ++n) now = fmaxf(now, ml[n].x);
-        const float by = weight(top, now);
-        top = now, sum *= by;
+        s.scale_to(now);
 #pragma unroll
-        for (int c = 0; c < 4; ++c) val[c] *= by;
+        for (int n = 0; n < kAhead; ++n) s.add(ml[n].x, ml[n].y, {o[n].x, o[n].y, o[n].z, o[n].w});
+    }
+    if constexpr (SPLIT) {
+        __shared__ Sums of_warp[kWarps][32];
+        of_warp[warp][lane] = s;
+        __syncthreads();
+        if (warp) return;
 #pragma unroll
-        for (int n = 0; n < kAhead; ++n) {
-            const float w = weight(ml[n].x, top);
-            sum += ml[n].y * w;
-            val[0] += o[n].x * w, val[1] += o[n].y * w, val[2] += o[n].z * w, val[3] += o[n].w * w;
+        for (uint32_t w = 1; w < kWarps; ++w) {
+            const Sums& t = of_warp[w][lane];
+            s.scale_to(fmaxf(s.top, t.top));
+            s.add(t.top, t.sum, t.val);
         }
     }
+    if (h >= heads) return;
     const int hq = r.y / a.blocks * a.group + blk * kept + h;
     uint16_t* to = a.out + r.x * a.out_row + hq * a.out_head + e;
 #pragma unroll
-    for (int c = 0; c < 4; ++c) to[c] = pack1<BF>(val[c] / sum);
-    if (a.lse && e == 0) a.lse[int64_t(r.x) * a.q_heads + hq] = (top + log2f(sum)) * 0.6931471805599453f;
+    for (int c = 0; c < 4; ++c) to[c] = pack1<BF>(s.val[c] / s.sum);
+    if (a.lse && e == 0) a.lse[int64_t(r.x) * a.q_heads + hq] = (s.top + log2f(s.sum)) * 0.6931471805599453f;
 }
 
 template <int DP, int NT, bool BF>
@@ -546,7 +571,9 @@ cudaError_t launch_as(const Attention& a, const AttentionPlan& plan, cudaStream_
     err = launch_next(kern, dim3(plan.grid), kThreads, Shape<DP>::kSmem, 1, s, a);
     if (err != cudaSuccess || !plan.cut || plan.grid < 2) return err;
     const uint32_t results = std::min<uint32_t>(plan.heads, a.group) * a.d;
-    return launch_next(join_kernel<BF>, dim3(plan.grid - 1, (results + 4 * kThreads - 1) / (4 * kThreads)), kThreads, 0, 1, s, a, int(plan.heads));
+    if (plan.grid >= 8 * int64_t(a.seqs) * a.pairs)  // eight parts a row or more
+        return launch_next(join_kernel<BF, true>, dim3(plan.grid - 1, (results + 127) / 128), kThreads, 0, 1, s, a, int(plan.heads));
+    return launch_next(join_kernel<BF, false>, dim3(plan.grid - 1, (results + 4 * kThreads - 1) / (4 * kThreads)), kThreads, 0, 1, s, a, int(plan.heads));
 }
 
 template <int DP>
