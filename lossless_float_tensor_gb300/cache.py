@@ -135,13 +135,19 @@ _RESERVE, _FORK = _Entry("uzip_cache_reserve", CacheArgs), _Entry("uzip_cache_fo
 _FREE, _COMPACT = _Entry("uzip_cache_free", CacheArgs), _Entry("uzip_cache_compact", CacheArgs)
 _COPY = _Entry("uzip_cache_copy", CacheCopyArgs)
 
-_torch = None
+_torch = _empty = None
 
 
 def _load():
-    global _torch
+    """torch, once it is needed, and _empty(shape, strides, dtype): a tensor on
+    the current device.  torch's allocation without its dispatcher takes 3 us
+    less of 5 between other calls; where a version has it no more,
+    empty_strided does."""
+    global _torch, _empty
     import torch
 
+    _empty = getattr(getattr(getattr(torch._C, "_dynamo", None), "guards", None), "_empty_strided_cuda", None) or (
+        lambda shape, steps, dtype: torch.empty_strided(shape, steps, dtype=dtype, device="cuda"))
     _torch = torch
     return torch
 
@@ -153,7 +159,7 @@ def _issue(entry, args, dev, workspace, status, check):
         need = entry.size(args)
         at = 0
         if need:
-            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+            workspace = _empty((need,), (1,), torch.uint8)
             at = workspace.data_ptr()
     else:
         if not workspace.is_contiguous():
@@ -196,11 +202,6 @@ def _strides(t, name, shape, dtype, dev):
     if steps[-1] != 1 and shape[-1] > 1:
         _refuse(f"{name}: the last dimension must be contiguous")
     return steps
-
-
-def _new(like, shape):
-    """A contiguous tensor of a type and device."""
-    return _torch.empty_like(like) if like.is_contiguous() else _torch.empty(shape, dtype=like.dtype, device=like.device)
 
 
 def _list(t, name, shape, dtype, dev):
@@ -286,8 +287,8 @@ def _rotary(q, k, positions, freqs, interleaved, backward, scale, out, status, c
         shape = (t, h, d)
         row, head, _ = _strides(x, name, shape, dt, dev)
         if y is None:
-            y = _new(x, shape)
             steps = h * d, d, 1
+            y = _empty(shape, steps, dt)
         else:
             steps = _strides(y, "out", shape, dt, dev)
         part.append((y, (x.data_ptr(), row, head, y.data_ptr(), steps[0], steps[1])))
@@ -342,8 +343,8 @@ def rotary_append(q, k, v, positions, freqs, k_pages, v_pages, slots, *, interle
     kp, vp = _strides(k_pages, "k_pages", pool, dt, dev), _strides(v_pages, "v_pages", pool, dt, dev)
     pairs = freqs.numel()
     if out is None:
-        out = _new(q, shape)
         o_row, o_head = hq * d, d
+        out = _empty((t, hq, d), (o_row, o_head, 1), dt)
     else:
         o_row, o_head, _ = _strides(out, "out", shape, dt, dev)
     args = _APPEND.pack(code, 1 if interleaved else 0, 0, scale, t, hq, hk, d, 2 * pairs, _list(positions, "positions", (t,), torch.int64, dev),
@@ -383,11 +384,11 @@ def paged_attention(q, k_pages, v_pages, table, lengths, *, scale=None, softcap=
     if table.shape[0] != s:
         _refuse(f"table has {table.shape[0]} rows for {s} queries")
     if out is None:
-        out = _new(q, shape)
         o_row, o_head = hq * d, d
+        out = _empty((s, hq, d), (o_row, o_head, 1), dt)
     else:
         o_row, o_head, _ = _strides(out, "out", shape, dt, dev)
-    lse = torch.empty((s, hq), dtype=torch.float32, device=dev) if with_lse else None
+    lse = _empty((s, hq), (hq, 1), torch.float32) if with_lse else None
     if scale is None:
         scale = d ** -0.5 if d else 0.0
     args = _ATTENTION.pack(code, 0, s, hq, hk, d, pages, page, width, q.data_ptr(), q_row, q_head, k_pages.data_ptr(), kp[0], kp[1], kp[2],
@@ -442,8 +443,7 @@ def cache_reserve(refs, table, lengths, counts, tokens, page_size, *, out=None, 
         _refuse(f"{tokens} tokens")
     listed = _list(counts, "counts", (seqs,), torch.int32, dev)
     if out is None:
-        out = (torch.empty(tokens, dtype=torch.int64, device=dev), torch.empty(tokens, dtype=torch.int64, device=dev),
-               torch.empty((seqs, 2), dtype=torch.int32, device=dev))
+        out = _empty((tokens,), (1,), torch.int64), _empty((tokens,), (1,), torch.int64), _empty((seqs, 2), (2, 1), torch.int32)
         slots, positions, pairs = out[0].data_ptr(), out[1].data_ptr(), out[2].data_ptr()
     else:
         slots, positions = (_list(x, "out", (tokens,), torch.int64, dev) for x in out[:2])
@@ -489,7 +489,7 @@ def cache_compact(refs, table, lengths, page_size, *, out=None, workspace=None, 
         with _on(dev, stream):
             return cache_compact(refs, table, lengths, page_size, out=out, workspace=workspace, status=status, check=check)
     if out is None:
-        out = torch.empty((pages // 2, 2), dtype=torch.int32, device=dev)
+        out = _empty((pages // 2, 2), (2, 1), torch.int32)
     _change(_COMPACT, state, page_size, workspace, status, check, pairs=_list(out, "out", (pages // 2, 2), torch.int32, dev))
     return out
 
