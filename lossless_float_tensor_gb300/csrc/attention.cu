@@ -124,9 +124,14 @@ static_assert(kLeast > kRowCost, "");
 // them.  `left` counts what the block has from the row's beginning on, kRowCost
 // before the first tile (whole rows: unused).
 struct Place {
-    int i, row, j0, j1, tile;
+    int i, row, j0, j1, tile, head;
     int64_t left;
+    const int32_t* pages;  // the sequence's row of the table
     Live s;
+    __device__ __forceinline__ void enter(const Attention& a) {
+        head = a.blocks == 1 ? row : row / a.blocks;
+        pages = a.table + i * a.ldt;
+    }
 };
 
 // The next part of the block's work; false at its end.
@@ -148,6 +153,7 @@ __device__ __forceinline__ bool next_part(const Attention& a, Place& p) {
     }
     p.j0 = 0;
     p.j1 = a.cut ? int(min(int64_t(p.s.tiles), p.left - kRowCost)) : p.s.tiles;
+    p.enter(a);
     return true;
 }
 
@@ -161,6 +167,7 @@ __device__ bool first_part(const Attention& a, Place& p) {
         p.i = int(at / a.pairs), p.row = int(at - int64_t(p.i) * a.pairs);
         p.s = live_of(a, p.i);
         p.j0 = 0, p.j1 = p.s.tiles;
+        p.enter(a);
         return true;
     }
     __shared__ int64_t sums[kWarps];
@@ -213,6 +220,7 @@ __device__ bool first_part(const Attention& a, Place& p) {
     p.j0 = max(0, in_row - kRowCost);
     p.left = end - begin + in_row;
     p.j1 = int(min(int64_t(p.s.tiles), p.left - kRowCost));
+    p.enter(a);
     if (threadIdx.x == 0) {
         // the first border behind a row's first tile is the one that has its joining done
         const int64_t tile0 = begin - in_row + kRowCost, row_end = tile0 + p.s.tiles;
@@ -259,49 +267,64 @@ __global__ void __launch_bounds__(kThreads, Shape<DP>::kBlocks) attention_kernel
         if (!more) return r;
         const int t0 = ahead.s.lo + ahead.tile * kTile, t = t0 + lane % kTile;
         r.count = min(kTile, ahead.s.len - t0);
-        r.head = ahead.row / a.blocks;
+        r.head = ahead.head;
         if (lane % kTile < r.count) {
-            const uint32_t col = uint32_t(uint64_t(t) * a.page_by >> a.page_shift);
-            r.page = a.table[ahead.i * a.ldt + col];
+            const uint32_t col = uint32_t(uint64_t(uint32_t(t)) * a.page_by >> a.page_shift);
+            r.page = ahead.pages[col];
             r.off = t - int(col) * a.page;
         }
         return r;
     };
     uint32_t poison = 0;  // stages whose tile has a page that does not exist
     // A row's 16-byte pieces lie with neighbouring lanes, as many rows at once as fit a warp.  A lane's place in keys and
-    // values differs by a constant where their strides are the same, so one shuffle finds both.
+    // values differs by a constant where their strides are the same, so one shuffle finds both.  Columns behind d are zeros.
     constexpr int kChunks = DP / 8, kRows = kChunks < 32 ? 32 / kChunks : 1;
     const int col = lane % kChunks * 16, first_row = lane / kChunks;
-    const uint64_t keys_from = reinterpret_cast<uint64_t>(a.k) + col, values_from = reinterpret_cast<uint64_t>(a.v) + col;
+    const bool col_in = col < 2 * a.d;
+    const uint64_t keys_from = reinterpret_cast<uint64_t>(a.k) + (col_in ? col : 0), values_from = reinterpret_cast<uint64_t>(a.v) + (col_in ? col : 0);
     const uint32_t col_to = mine + first_row * S::kPitch + col;
     auto fetch = [&](const Row& r, int stage) {
         const bool in = lane % kTile < r.count;
-        const bool bad = __any_sync(~0u, in && uint32_t(r.page) >= uint32_t(a.pages));
-        poison = bad ? poison | 1u << stage : poison & ~(1u << stage);
-        if (bad && a.status && lane == 0) *a.status = UZIP_ERR_INVALID_ARG;
-        const int live = bad ? 0 : r.count;
+        int live = r.count;
+        poison &= ~(1u << stage);
+        if (__any_sync(~0u, in && uint32_t(r.page) >= uint32_t(a.pages))) {
+            poison |= 1u << stage;
+            if (a.status && lane == 0) *a.status = UZIP_ERR_INVALID_ARG;
+            live = 0;
+        }
         // bytes from the pool's first value; rows that are not there: its first row, of which nothing is read
         auto place = [&](const PoolStrides& st) -> uint64_t {
-            return in && !bad ? 2 * (r.page * st.page + r.head * st.head + r.off * st.token) : 0;
+            return lane % kTile < live ? uint32_t(r.page) * st.page + uint32_t(r.head) * st.head + uint32_t(r.off) * st.token : 0;
         };
-        const uint64_t k_off = place(a.ks), v_off = a.alike ? k_off : place(a.vs);
+        const uint64_t k_off = place(a.ks);
         const uint32_t to = col_to + stage * S::kStage;
-        if (kRows * kChunks == 32 && live == kTile && a.d == DP && a.alike) {
+        if (live == kTile && a.alike) {
+            if (kRows * kChunks == 32 && a.d == DP) {
 #pragma unroll
-            for (int n = 0; n < kTile; n += kRows) {
-                const uint64_t off = __shfl_sync(~0u, k_off, n + first_row);
-                fetch16(to + n * S::kPitch, keys_from + off);
-                fetch16(to + (kTile + n) * S::kPitch, values_from + off);
+                for (int n = 0; n < kTile; n += kRows) {
+                    const uint64_t off = __shfl_sync(~0u, k_off, n + first_row);
+                    fetch16(to + n * S::kPitch, keys_from + off);
+                    fetch16(to + (kTile + n) * S::kPitch, values_from + off);
+                }
+            } else {
+#pragma unroll
+                for (int n = 0; n < kTile; n += kRows) {
+                    const uint64_t off = __shfl_sync(~0u, k_off, n + first_row);
+                    if (first_row < kRows) {
+                        fetch16(to + n * S::kPitch, keys_from + off, col_in);
+                        fetch16(to + (kTile + n) * S::kPitch, values_from + off, col_in);
+                    }
+                }
             }
         } else {
-#pragma unroll 4
+            const uint64_t v_off = place(a.vs);
+#pragma unroll 2
             for (int n = 0; n < kTile; n += kRows) {
                 const int row = n + first_row;
                 const uint64_t ko = __shfl_sync(~0u, k_off, row), vo = __shfl_sync(~0u, v_off, row);
-                const bool there = row < live && col < 2 * a.d;
                 if (first_row < kRows) {
-                    fetch16(to + n * S::kPitch, there ? keys_from + ko : keys_from - col, there);
-                    fetch16(to + (kTile + n) * S::kPitch, there ? values_from + vo : values_from - col, there);
+                    fetch16(to + n * S::kPitch, keys_from + ko, row < live && col_in);
+                    fetch16(to + (kTile + n) * S::kPitch, values_from + vo, row < live && col_in);
                 }
             }
         }
@@ -397,10 +420,14 @@ __global__ void __launch_bounds__(kThreads, Shape<DP>::kBlocks) attention_kernel
             for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    float s = (z[nt][e] + z2[nt][e]) * scale;
+                    z[nt][e] = (z[nt][e] + z2[nt][e]) * scale;
                     // cap tanh(x / cap) = cap - 2 cap / (exp(2 x / cap) + 1)
-                    if (a.cap > 0) s = cap - 2.f * cap * fast_reciprocal(fast_exp2(s) + 1.f);
-                    z[nt][e] = lane / 4 + e / 2 * 8 < count ? s : -INFINITY;
+                    if (a.cap > 0) z[nt][e] = cap - 2.f * cap * fast_reciprocal(fast_exp2(z[nt][e]) + 1.f);
+                }
+                if (count < kTile) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (lane / 4 + e / 2 * 8 >= count) z[nt][e] = -INFINITY;
                 }
                 float top[2] = {fmaxf(z[nt][0], z[nt][2]), fmaxf(z[nt][1], z[nt][3])};
                 // the maximum that weights go by is moved only once a score is over it by kSlack: weights up to 2^kSlack lose
@@ -417,9 +444,11 @@ __global__ void __launch_bounds__(kThreads, Shape<DP>::kBlocks) attention_kernel
                         for (int ks = 0; ks < kSteps; ++ks) o[nt][ks][c] *= by, o[nt][ks][c + 2] *= by;
                     }
                 }
+                // nothing but -inf so far: weights of 0, by any other maximum
+                const float from[2] = {m[nt][0] == -INFINITY ? 0.f : m[nt][0], m[nt][1] == -INFINITY ? 0.f : m[nt][1]};
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    z[nt][e] = weight(z[nt][e], m[nt][e % 2]);
+                    z[nt][e] = fast_exp2(z[nt][e] - from[e % 2]);
                     l[nt][e % 2] += z[nt][e];
                 }
                 // rounded to the values' type for the second product: off by half a unit each, at random, which adds up to

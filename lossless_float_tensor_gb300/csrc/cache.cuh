@@ -37,7 +37,7 @@ struct PoolStrides {
 struct Attention {
     const uint16_t *q, *k, *v;
     int64_t q_row, q_head;
-    PoolStrides ks, vs;
+    PoolStrides ks, vs;  // in bytes
     const int32_t* table;
     int64_t ldt;
     const int32_t* lengths;
@@ -46,7 +46,7 @@ struct Attention {
     int32_t pairs;       // kv_heads * blocks: rows of work of a sequence
     int32_t most;        // tokens that a sequence's row of the table holds (capped to int32)
     int32_t window;      // 0: none
-    uint64_t page_by;    // t / page = t * page_by >> page_shift for t below 2^31
+    uint32_t page_by;    // t / page = t * page_by >> page_shift for t below 2^31
     int32_t page_shift;
     int32_t q_pairs;     // whether neighbouring values of q may be read together
     int32_t alike;       // whether keys and values have the same strides

@@ -110,7 +110,7 @@ Block pool_of(const void* p, int64_t pages, int64_t heads, int64_t page, const P
               int64_t layer = 0) {
     return Block{p, {layers, pages, heads, page}, {layer, s.page, s.head, s.token}, d};
 }
-PoolStrides strides_of(const Block& b) { return PoolStrides{b.stride(1), b.stride(2), b.stride(3)}; }
+PoolStrides bytes_of(const Block& b) { return PoolStrides{2 * b.stride(1), 2 * b.stride(2), 2 * b.stride(3)}; }
 
 template <typename T>
 bool list_ok(const T* p, int64_t n) {
@@ -293,8 +293,8 @@ uzip_status uzip_paged_attention(const uzip_paged_attention_args* a, void* d_wor
     Work work{static_cast<uint8_t*>(d_workspace)};
     Attention r = plan_work(*a, plan, work);
     r.q = static_cast<const uint16_t*>(a->q), r.q_row = q.stride(2), r.q_head = q.stride(3);
-    r.k = static_cast<const uint16_t*>(a->k_pages), r.ks = strides_of(k);
-    r.v = static_cast<const uint16_t*>(a->v_pages), r.vs = strides_of(v);
+    r.k = static_cast<const uint16_t*>(a->k_pages), r.ks = bytes_of(k);
+    r.v = static_cast<const uint16_t*>(a->v_pages), r.vs = bytes_of(v);
     r.table = a->table, r.ldt = ldt, r.lengths = a->lengths;
     r.seqs = int32_t(a->seqs), r.q_heads = int32_t(a->q_heads), r.group = int32_t(a->q_heads / a->kv_heads), r.d = int32_t(a->d);
     r.pages = int32_t(a->pages), r.page = int32_t(a->page);
@@ -302,7 +302,7 @@ uzip_status uzip_paged_attention(const uzip_paged_attention_args* a, void* d_wor
     int s2 = 0;
     while (int64_t(1) << s2 < a->page) ++s2;
     r.page_shift = 31 + s2;
-    r.page_by = ((uint64_t(1) << r.page_shift) + a->page - 1) / a->page;
+    r.page_by = uint32_t(((uint64_t(1) << r.page_shift) + a->page - 1) / a->page);
     r.alike = r.ks.page == r.vs.page && r.ks.head == r.vs.head && r.ks.token == r.vs.token;
     r.q_pairs = aligned(a->q, 4) && r.q_row % 2 == 0 && r.q_head % 2 == 0;
     r.blocks = (r.group + int32_t(plan.heads) - 1) / int32_t(plan.heads);
