@@ -125,7 +125,7 @@ static_assert(kLeast > kRowCost, "");
 // before the first tile (whole rows: unused).
 struct Place {
     int i, row, j0, j1, tile, head;
-    int64_t left;
+    int64_t left, begin;  // begin: where the row begins among all costs
     const int32_t* pages;  // the sequence's row of the table
     Live s;
     __device__ __forceinline__ void enter(const Attention& a) {
@@ -137,7 +137,7 @@ struct Place {
 // The next part of the block's work; false at its end.
 __device__ __forceinline__ bool next_part(const Attention& a, Place& p) {
     if (a.cut) {
-        p.left -= kRowCost + p.s.tiles;
+        p.left -= kRowCost + p.s.tiles, p.begin += kRowCost + p.s.tiles;
         if (p.left <= kRowCost) return false;
         if (++p.row == a.pairs) {
             p.row = 0;
@@ -160,7 +160,7 @@ __device__ __forceinline__ bool next_part(const Attention& a, Place& p) {
 // The first part of this block's work, and the record of the border before it.
 // Costs are counted through all sequences; block b has those from b * total /
 // blocks on.  Returns false if there is none.
-__device__ bool first_part(const Attention& a, Place& p) {
+__device__ bool first_part(const Attention& a, Place& p, int64_t& total, int64_t& blocks) {
     if (!a.cut) {
         const int64_t at = blockIdx.x;
         if (at >= int64_t(a.seqs) * a.pairs) return false;
@@ -185,7 +185,8 @@ __device__ bool first_part(const Attention& a, Place& p) {
     }
     if (lane == 31) sums[warp] = sum;
     __syncthreads();
-    int64_t total = 0, before = sum - mine;
+    int64_t before = sum - mine;
+    total = 0;
 #pragma unroll
     for (uint32_t w = 0; w < kWarps; ++w) {
         if (w < warp) before += sums[w];
@@ -193,7 +194,7 @@ __device__ bool first_part(const Attention& a, Place& p) {
     }
     total *= a.pairs;
     before *= a.pairs;
-    const int64_t blocks = min(int64_t(gridDim.x), max(int64_t(1), total / kLeast));
+    blocks = min(int64_t(gridDim.x), max(int64_t(1), total / kLeast));
     const int64_t b = blockIdx.x;
     if (b >= blocks) {
         if (threadIdx.x == 0) a.record[b] = make_int4(-1, 0, 0, 0);
@@ -218,12 +219,12 @@ __device__ bool first_part(const Attention& a, Place& p) {
     p.row = int(in / span);
     const int in_row = int(in - int64_t(p.row) * span);
     p.j0 = max(0, in_row - kRowCost);
-    p.left = end - begin + in_row;
+    p.left = end - begin + in_row, p.begin = begin - in_row;
     p.j1 = int(min(int64_t(p.s.tiles), p.left - kRowCost));
     p.enter(a);
     if (threadIdx.x == 0) {
         // the first border behind a row's first tile is the one that has its joining done
-        const int64_t tile0 = begin - in_row + kRowCost, row_end = tile0 + p.s.tiles;
+        const int64_t tile0 = p.begin + kRowCost, row_end = tile0 + p.s.tiles;
         const bool first = p.j0 > 0 && (b - 1) * total / blocks <= tile0;
         a.record[b] = first ? make_int4(p.i, p.row, int(b - 1), int((row_end * blocks - 1) / total)) : make_int4(-1, 0, 0, 0);
     }
@@ -248,7 +249,8 @@ __global__ void __launch_bounds__(kThreads, Shape<DP>::kBlocks) attention_kernel
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
     const uint32_t mine = smem_u32(ring) + warp * kStages * S::kStage;
     Place ahead;
-    if (!first_part(a, ahead)) return;  // the whole block
+    int64_t total = 0, blocks = 0;
+    if (!first_part(a, ahead, total, blocks)) return;  // the whole block
     Place at = ahead;
     bool more = true;  // `ahead` is at a tile (or at the end)
     ahead.tile = ahead.j0 + warp;
@@ -486,6 +488,10 @@ __global__ void __launch_bounds__(kThreads, Shape<DP>::kBlocks) attention_kernel
         __syncthreads();
         const bool whole = at.j0 == 0 && at.j1 == at.s.tiles;
         const int64_t part = 2 * int64_t(blockIdx.x) + (at.j0 == 0);
+        if (a.row_record && at.j0 == 0 && threadIdx.x == 0) {
+            const int last = int(((at.begin + kRowCost + at.s.tiles) * blocks - 1) / total);
+            a.row_record[int64_t(at.i) * a.pairs + at.row] = make_int2(whole ? -1 : int(blockIdx.x), last);
+        }
         for (int x = threadIdx.x; x < heads * DP; x += kThreads) {
             const int h = x / DP, e = x % DP;
             if (e >= a.d) continue;
@@ -515,13 +521,20 @@ __global__ void __launch_bounds__(kThreads, Shape<DP>::kBlocks) attention_kernel
 }
 
 // Joins the parts of a row that borders cut, in the order of its tokens: block
-// (border, 512 of the row's results), four results a lane.  With SPLIT, where one
-// row has dozens of parts and their loads are what this waits for: block (border,
-// 128 results), each warp a quarter of the parts, and the first the warps' sums.
+// (border, 512 of the row's results), four results a lane.  With SPLIT, where rows
+// are few, one has dozens of parts and their loads are what this waits for: block
+// (row, 128 results), each warp a quarter of the parts, and the first the warps'
+// sums.
 template <bool BF, bool SPLIT>
 __global__ void __launch_bounds__(kThreads) join_kernel(const __grid_constant__ Attention a, int kept) {
     wait_for_launch_before();
-    const int4 r = a.record[blockIdx.x + 1];
+    int4 r;  // sequence, row, first and last block
+    if constexpr (SPLIT) {
+        const int2 b = a.row_record[blockIdx.x];
+        r = make_int4(b.x < 0 ? -1 : int(blockIdx.x) / a.pairs, int(blockIdx.x) % a.pairs, b.x, b.y);
+    } else {
+        r = a.record[blockIdx.x + 1];
+    }
     if (r.x < 0) return;
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
     const int blk = r.y % a.blocks, heads = min(kept, a.group - blk * kept);
@@ -600,8 +613,8 @@ cudaError_t launch_as(const Attention& a, const AttentionPlan& plan, cudaStream_
     err = launch_next(kern, dim3(plan.grid), kThreads, Shape<DP>::kSmem, 1, s, a);
     if (err != cudaSuccess || !plan.cut || plan.grid < 2) return err;
     const uint32_t results = std::min<uint32_t>(plan.heads, a.group) * a.d;
-    if (plan.grid >= 8 * int64_t(a.seqs) * a.pairs)  // eight parts a row or more
-        return launch_next(join_kernel<BF, true>, dim3(plan.grid - 1, (results + 127) / 128), kThreads, 0, 1, s, a, int(plan.heads));
+    if (a.row_record)
+        return launch_next(join_kernel<BF, true>, dim3(a.seqs * a.pairs, (results + 127) / 128), kThreads, 0, 1, s, a, int(plan.heads));
     return launch_next(join_kernel<BF, false>, dim3(plan.grid - 1, (results + 4 * kThreads - 1) / (4 * kThreads)), kThreads, 0, 1, s, a, int(plan.heads));
 }
 
@@ -621,6 +634,7 @@ AttentionPlan plan_attention(int64_t seqs, int64_t kv_heads, int64_t group, int6
     const int64_t room = int64_t(sms) * (d <= 128 ? 3 : 1);
     p.cut = tiles > 32;
     p.grid = uint32_t(std::max<int64_t>(1, std::min(room, p.cut ? rows * ((tiles + kRowCost + kLeast - 1) / kLeast) : rows)));
+    p.by_row = p.cut && p.grid >= 8 * rows ? rows : 0;  // eight parts a row or more, where it has its full length
     return p;
 }
 

@@ -58,6 +58,7 @@ struct Attention {
     float* part_o;       // [2 grid][kept heads][d] sums over a part of a sequence's tokens
     float2* part_ml;     // [2 grid][kept heads]: largest score (times log2 e), sum of exponentials
     int4* record;        // [grid]: what a border between two blocks cuts
+    int2* row_record;    // [rows]: first (-1: not cut) and last block; null where there are many rows
     int32_t* status;
 };
 
@@ -65,6 +66,7 @@ struct AttentionPlan {
     uint32_t grid;   // blocks
     uint32_t heads;  // kept heads: 8 or 16
     bool cut;
+    int64_t by_row;  // rows, where they are few and joined one by one; else 0
 };
 // what goes by sizes alone, for the workspace and the launch
 AttentionPlan plan_attention(int64_t seqs, int64_t kv_heads, int64_t group, int64_t d, int64_t most, int sms);

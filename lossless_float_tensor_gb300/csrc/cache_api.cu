@@ -190,6 +190,7 @@ Attention plan_work(const uzip_paged_attention_args& a, const AttentionPlan& pla
         r.part_o = w.take<float>(2 * uint64_t(plan.grid) * plan.heads * a.d);
         r.part_ml = w.take<float2>(2 * uint64_t(plan.grid) * plan.heads);
         r.record = w.take<int4>(plan.grid);
+        if (plan.by_row) r.row_record = w.take<int2>(plan.by_row);
     }
     return r;
 }

@@ -138,8 +138,8 @@ def test_workspace_only_where_something_is_kept(cache):
     assert size(_attention(cache)) == 0
     assert size(_attention(cache, width=1 << 20, window=100)) == 0
     long = size(_attention(cache, width=1 << 20))
-    assert 0 < long <= 2 * 3 * 160 * 8 * (16 + 2) * 4 + 16 * 3 * 160 + 3 * 256
-    assert size(_attention(cache, width=1 << 20, seqs=1000)) == long
+    assert 0 < long <= 2 * 3 * 160 * 8 * (16 + 2) * 4 + 16 * 3 * 160 + 4 * 256
+    assert size(_attention(cache, width=1 << 20, seqs=1000)) <= long
     assert size(_attention(cache, width=1 << 20, d=12)) == 0
     up = lambda v: -(-v // 256) * 256  # noqa: E731
     reserve, fork = cache.uzip_cache_reserve_workspace_size, cache.uzip_cache_fork_workspace_size
