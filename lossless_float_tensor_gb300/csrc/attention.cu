@@ -6,27 +6,30 @@
 //   m' = max(m, z), l' = l 2^(m - m') + 2^(z - m'), o' = o 2^(m - m') + 2^(z - m') v.
 // Every key and value is read once and used for 4 operations a query head, 2 to 16
 // operations a byte: what bounds it is memory, and the work of a block is to keep
-// enough of it in flight.  The products still need matrix instructions (8 query
-// heads would take 54 TFLOP/s of plain ones); they run transposed, tokens or head
-// values as the rows and query heads as the 8 columns, so that heads that do not
-// exist cost no rows: S^T = K Q^T and O^T = V^T P^T by m16n8k16, which leaves the
-// tensor cores nearly idle either way.  tcgen05's rows of 128 tokens would want
-// the tokens of four warps in one step, with the barriers between them that this
-// layout does without.
+// enough of it in flight.  128 sequences of 1024 to 12288 tokens, 8 x 4 heads of
+// 128 in bf16: 533 us, 6.55 TB/s of 6.79 that a copy reaches; 131072 tokens of one
+// sequence: 89.7 us, 5.99 TB/s, 8 us of it start, end and joining.  The products
+// still need matrix instructions (8 query heads would take 54 TFLOP/s of plain
+// ones); they run transposed, tokens or head values as the rows and query heads as
+// the 8 columns, so that heads that do not exist cost no rows: S^T = K Q^T and
+// O^T = V^T P^T by m16n8k16, which keeps the tensor pipe busy 9 % of the time.
+// tcgen05's rows of 128 tokens would want the tokens of eight tiles in one step,
+// with the barriers between their warps that this layout does without.
 //
 // A warp takes tiles of 16 tokens, has a ring of shared memory of its own for
 // them (cp.async, 16 bytes a lane, rows 16 bytes apart from a multiple of 128 so
 // that ldmatrix finds no bank twice), and running sums of its own: no barrier but
-// where a sequence's part ends and the four warps' sums are joined.  Rows behind
-// the last token are filled with zeros and never read, so what they hold says
-// nothing.
+// where a sequence's part ends and the four warps' sums are joined.  A lane each
+// looks its token's page up, so pages may end anywhere in a tile.  (One bulk copy a
+// row instead, 256 bytes: 663 us for the 128 sequences.)  Rows behind the last
+// token are filled with zeros and never read, so what they hold says nothing.
 //
 // The tokens of all sequences and heads, in tiles, are cut into one equal piece
-// for each block, found by every block from the lengths on the device.  A row (a
-// sequence's tokens for one head) counts kRowCost tiles more than it has, for its
-// queries and its end, so that a block of many short rows has no more to do.  Where a
-// border falls inside a sequence's head the sums go to the workspace and a second
-// launch joins them, in the order of the tokens: the same bits each time.
+// for each block, found by every block from the lengths on the device (1.1 us).  A
+// row (a sequence's tokens for one head) counts kRowCost tiles more than it has, for
+// its queries and its end, so that a block of many short rows has no more to do.
+// Where a border falls inside a row the sums go to the workspace and a second launch
+// joins them, in the order of the tokens: the same bits each time.
 #include <algorithm>
 #include <atomic>
 
@@ -43,7 +46,9 @@ template <int DP>
 struct Shape {
     static constexpr uint32_t kPitch = DP * 2 + 16;             // bytes from token to token
     static constexpr uint32_t kStage = 2 * kTile * kPitch;      // keys, then values
-    static constexpr uint32_t kBlocks = DP <= 128 ? 3 : 1;      // blocks on an SM
+    // blocks on an SM, with the stages that fit: 64 sequences of 16 to 4096 tokens, d = 128, take 92.0 us on three of
+    // two stages, 102.6 on two of three
+    static constexpr uint32_t kBlocks = DP <= 128 ? 3 : 1;
     static constexpr uint32_t kRoom = 227 * 1024 / kBlocks - 2048;
     static constexpr uint32_t kMost = kRoom / (kWarps * kStage);
     static constexpr uint32_t kStages = kMost < 8 ? kMost : 8;
@@ -116,8 +121,12 @@ __device__ __forceinline__ Live live_of(const Attention& a, int i) {
     return s;
 }
 
-constexpr int kRowCost = 8;  // what a row costs beside its tiles, in tiles
-constexpr int kLeast = 16;   // what a block has at least, where rows are cut: over kRowCost, so that it has a tile
+// What a row costs beside its tiles, in tiles.  24 sequences of 0 to 6000 tokens in
+// windows of 1024, 16 heads: 51.6 us with 0, 28.2 with 4, 23.6 with 8, 23.9 with 14.
+constexpr int kRowCost = 8;
+// What a block has at least, where rows are cut: over kRowCost, so that it has a
+// tile.  37 sequences of 0 to 2777 tokens, 3 heads: 16.8 us with 16, 18.2 with 32.
+constexpr int kLeast = 16;
 static_assert(kLeast > kRowCost, "");
 
 // Where a warp is: tiles [j0, j1) of row `row` of sequence i, and its tile of
@@ -632,6 +641,7 @@ AttentionPlan plan_attention(int64_t seqs, int64_t kv_heads, int64_t group, int6
     const int64_t rows = seqs * kv_heads * ((group + p.heads - 1) / p.heads);
     const int64_t tiles = std::max<int64_t>(1, (most + kTile - 1) / kTile);
     const int64_t room = int64_t(sms) * (d <= 128 ? 3 : 1);
+    // up to 512 tokens a row stays whole: joining would take 2.2 us, as much as four tiles of a warp
     p.cut = tiles > 32;
     p.grid = uint32_t(std::max<int64_t>(1, std::min(room, p.cut ? rows * ((tiles + kRowCost + kLeast - 1) / kLeast) : rows)));
     p.by_row = p.cut && p.grid >= 8 * rows ? rows : 0;  // eight parts a row or more, where it has its full length

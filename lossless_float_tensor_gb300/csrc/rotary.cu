@@ -1,6 +1,8 @@
 // Rotary positions: y_a = s (x_a cos - x_b sin), y_b = s (x_a sin + x_b cos) for the
 // pairs (a, b) of each head, by the angle position * frequency; backward is the
-// opposite angle.  Each value is read and written once, so memory bounds it.
+// opposite angle.  Each value is read and written once, so memory bounds it: 8192
+// tokens with 32 + 8 + 8 heads of 128 into pages 35 us, 5.8 TB/s of 6.8 that a copy
+// reaches; 8191 tokens with 32 heads of 96, 48 values turned: 20.6 us, 4.9 TB/s.
 //
 // Angles are kept in turns, as 64-bit fractions: position * frequency is one
 // integer product modulo 2^64, which is the reduction modulo a full turn, exact
@@ -9,7 +11,8 @@
 //
 // A warp takes a token and a share of its heads: the cosines and sines of a token
 // are computed once a warp, exchanged through shared memory, and kept in
-// registers for all of its heads.
+// registers for all of its heads.  Two heads are in flight in a lane (four: 37.3 and
+// 46 us for the two above; eight warps a block instead of four: 39.7 and 55).
 #include <algorithm>
 
 #include "cache.cuh"
