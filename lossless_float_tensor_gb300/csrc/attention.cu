@@ -117,7 +117,7 @@ __device__ __forceinline__ Live live_of(const Attention& a, int i) {
     if (s.bad) n = 0;
     s.len = n;
     s.lo = a.window && n > a.window ? n - a.window : 0;
-    s.tiles = max(1, (n - s.lo + kTile - 1) / kTile);
+    s.tiles = max(1, int((uint32_t(n - s.lo) + kTile - 1) / kTile));
     return s;
 }
 

@@ -3,6 +3,7 @@
 // anything is enqueued.
 #include <algorithm>
 #include <array>
+#include <cmath>
 #include <limits>
 
 #include "cache.cuh"
@@ -131,6 +132,7 @@ uzip_status rotary(const uzip_rotary_args* a, void* ws, uint64_t bytes, int32_t*
         return UZIP_ERR_INVALID_ARG;
     if (append && (a->backward || !pool_sizes_ok(a->pages, a->kv_heads, a->page, a->d))) return UZIP_ERR_INVALID_ARG;
     if (!append && a->slots) return UZIP_ERR_INVALID_ARG;
+    if (append && a->pages && a->k_pages == a->v_pages) return UZIP_ERR_INVALID_ARG;
     const int64_t t = a->t, d = a->d;
     const Block q = heads_of(a->q, t, a->q_row, a->q_heads, a->q_head, d), qo = heads_of(a->q_out, t, a->q_out_row, a->q_heads, a->q_out_head, d),
                 k = heads_of(a->k, t, a->k_row, a->kv_heads, a->k_head, d),
@@ -274,6 +276,8 @@ uzip_status uzip_paged_attention(const uzip_paged_attention_args* a, void* d_wor
     uzip_status st = attention_sizes(*a);
     if (st != UZIP_OK) return st;
     if (a->window < 0 || !(a->softcap >= 0.f) || !(a->softcap < std::numeric_limits<float>::infinity())) return UZIP_ERR_INVALID_ARG;
+    // a cap so small that the scale over it is no number says nothing
+    if (a->softcap > 0.f && std::isfinite(a->scale) && !std::isfinite(4.f * a->scale / a->softcap)) return UZIP_ERR_INVALID_ARG;
     const Block q = heads_of(a->q, a->seqs, a->q_row, a->q_heads, a->q_head, a->d), out = heads_of(a->out, a->seqs, a->out_row, a->q_heads, a->out_head, a->d);
     const Block k = pool_of(a->k_pages, a->pages, a->kv_heads, a->page, {a->kp_page, a->kp_head, a->kp_token}, a->d),
                 v = pool_of(a->v_pages, a->pages, a->kv_heads, a->page, {a->vp_page, a->vp_head, a->vp_token}, a->d);
@@ -386,6 +390,7 @@ uzip_status uzip_cache_copy(const uzip_cache_copy_args* a, void* d_workspace, ui
         return UZIP_ERR_INVALID_ARG;
     const bool same = a->k == a->k_to && a->v == a->v_to;
     if (!same && (a->k == a->k_to || a->v == a->v_to)) return UZIP_ERR_INVALID_ARG;
+    if (a->to_pages && (a->k_to == a->v_to || a->k == a->v_to || a->v == a->k_to)) return UZIP_ERR_INVALID_ARG;
     if (same && a->from_pages != a->to_pages) return UZIP_ERR_INVALID_ARG;
     const Block b[4] = {pool_of(a->k, a->from_pages, a->heads, a->page, {a->k_page, a->k_head, a->k_token}, a->d, a->layers, a->k_layer),
                         pool_of(a->v, a->from_pages, a->heads, a->page, {a->v_page, a->v_head, a->v_token}, a->d, a->layers, a->v_layer),

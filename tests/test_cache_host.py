@@ -33,7 +33,7 @@ def _rotary(cache, **kw):
 
 
 def _append(cache, **kw):
-    a = _rotary(cache, v=FAKE, v_row=16, v_head=16, pages=8, page=4, k_pages=FAKE, kp_page=64, kp_head=64, kp_token=16, v_pages=FAKE, vp_page=64,
+    a = _rotary(cache, v=FAKE, v_row=16, v_head=16, pages=8, page=4, k_pages=FAKE, kp_page=64, kp_head=64, kp_token=16, v_pages=2 * FAKE, vp_page=64,
                 vp_head=64, vp_token=16, slots=FAKE)
     return _set(a, kw)
 
@@ -51,9 +51,9 @@ def _state(cache, **kw):
 
 def _copy(cache, **kw):
     a = cache.CacheCopyArgs(dtype=0, layers=2, heads=2, page=4, d=16, from_pages=8, to_pages=8, pairs=FAKE, n=3)
-    for pre in ("k", "v"):
-        _set(a, {pre: FAKE, pre + "_layer": 1024, pre + "_page": 128, pre + "_head": 64, pre + "_token": 16})
-        _set(a, {pre + "_to": FAKE, pre + "t_layer": 1024, pre + "t_page": 128, pre + "t_head": 64, pre + "t_token": 16})
+    for pre, at in (("k", FAKE), ("v", 2 * FAKE)):
+        _set(a, {pre: at, pre + "_layer": 1024, pre + "_page": 128, pre + "_head": 64, pre + "_token": 16})
+        _set(a, {pre + "_to": at, pre + "t_layer": 1024, pre + "t_page": 128, pre + "t_head": 64, pre + "t_token": 16})
     return _set(a, kw)
 
 
@@ -72,7 +72,7 @@ def test_rotary_refuses(cache, change, want):
 @pytest.mark.parametrize("change,want", [
     (dict(dtype=4), BAD_DTYPE), (dict(backward=1), BAD_ARG), (dict(kv_heads=0), BAD_ARG), (dict(d=12, rot=12), BAD_ARG), (dict(page=0), BAD_ARG),
     (dict(v=None), BAD_ARG), (dict(slots=None), BAD_ARG), (dict(slots=FAKE + 4), BAD_ARG), (dict(k_pages=None), BAD_ARG), (dict(k_pages=FAKE + 8), BAD_ARG),
-    (dict(kp_token=20), BAD_ARG), (dict(kp_token=8), BAD_ARG), (dict(vp_page=56), BAD_ARG), (dict(pages=-1), BAD_ARG), (dict(pages=1 << 31), BAD_ARG),
+    (dict(kp_token=20), BAD_ARG), (dict(v_pages=FAKE), BAD_ARG), (dict(kp_token=8), BAD_ARG), (dict(vp_page=56), BAD_ARG), (dict(pages=-1), BAD_ARG), (dict(pages=1 << 31), BAD_ARG),
 ])
 def test_rotary_append_refuses(cache, change, want):
     assert cache.uzip_rotary_append(_append(cache, **change), None, 0, None, 0) == want
@@ -81,7 +81,7 @@ def test_rotary_append_refuses(cache, change, want):
 @pytest.mark.parametrize("change,want", [
     (dict(dtype=1), BAD_DTYPE), (dict(reserved=1), BAD_ARG), (dict(seqs=-1), BAD_ARG), (dict(seqs=65537), BAD_ARG), (dict(q_heads=3), BAD_ARG),
     (dict(q_heads=0), BAD_ARG), (dict(kv_heads=0), BAD_ARG), (dict(d=12), BAD_ARG), (dict(d=264), BAD_ARG), (dict(d=0), BAD_ARG), (dict(page=0), BAD_ARG),
-    (dict(width=-1), BAD_ARG), (dict(window=-1), BAD_ARG), (dict(softcap=-1.0), BAD_ARG), (dict(softcap=math.inf), BAD_ARG), (dict(softcap=math.nan), BAD_ARG),
+    (dict(width=-1), BAD_ARG), (dict(window=-1), BAD_ARG), (dict(softcap=-1.0), BAD_ARG), (dict(softcap=math.inf), BAD_ARG), (dict(softcap=math.nan), BAD_ARG), (dict(softcap=1e-42), BAD_ARG),
     (dict(q=None), BAD_ARG), (dict(q=FAKE + 1), BAD_ARG), (dict(k_pages=FAKE + 8), BAD_ARG), (dict(kp_token=17), BAD_ARG), (dict(vp_head=-64), BAD_ARG),
     (dict(out=None), BAD_ARG), (dict(out_row=63), BAD_ARG), (dict(out_head=0), BAD_ARG), (dict(ldt=-5), BAD_ARG), (dict(table=None), BAD_ARG),
     (dict(table=FAKE + 2), BAD_ARG), (dict(lengths=None), BAD_ARG), (dict(lse=FAKE + 1), BAD_ARG),
@@ -118,7 +118,8 @@ def test_compact_refuses(cache, change):
     (dict(dtype=1), BAD_DTYPE), (dict(reserved=1), BAD_ARG), (dict(layers=-1), BAD_ARG), (dict(heads=0), BAD_ARG), (dict(d=12), BAD_ARG),
     (dict(d=512), BAD_ARG), (dict(to_pages=1572865, from_pages=1572865), BAD_ARG), (dict(to_pages=9), BAD_ARG), (dict(k_to=FAKE + 4096), BAD_ARG),
     (dict(k=FAKE + 8, k_to=FAKE + 8), BAD_ARG), (dict(kt_page=256), BAD_ARG), (dict(k_token=8, kt_token=8), BAD_ARG), (dict(pairs=None), BAD_ARG),
-    (dict(pairs=FAKE + 4), BAD_ARG), (dict(n=-1), BAD_ARG), (dict(k_layer=-1024, kt_layer=-1024), BAD_ARG),
+    (dict(pairs=FAKE + 4), BAD_ARG), (dict(n=-1), BAD_ARG), (dict(v=FAKE, v_to=FAKE), BAD_ARG), (dict(k_to=3 * FAKE, v_to=3 * FAKE), BAD_ARG),
+    (dict(k_to=3 * FAKE, v_to=FAKE), BAD_ARG), (dict(k_layer=-1024, kt_layer=-1024), BAD_ARG),
 ])
 def test_copy_refuses(cache, change, want):
     assert cache.uzip_cache_copy(_copy(cache, **change), None, 0, None, 0) == want

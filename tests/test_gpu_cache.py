@@ -292,6 +292,25 @@ def test_attention_of_pools_past_32_bits(uz):
     assert torch.equal(_bits(k[3]), _bits(k[pages - 1])) and torch.equal(_bits(v[pages - 3]), _bits(v[5]))
 
 
+def test_attention_of_2_to_31_tokens(uz):
+    """The longest sequence, of one page of 2^20 tokens again and again (a stride
+    of zero): the tokens of the page weigh as they do in one, but for the one
+    that is missing at the end."""
+    g = _gen(10)
+    page, n = 1 << 20, 2 ** 31 - 1
+    k1, v1 = ref.pools(g, 1, 1, page, 8, torch.bfloat16)
+    k, v = k1.expand(2048, -1, -1, -1), v1.expand(2048, -1, -1, -1)
+    table = torch.arange(2048, dtype=torch.int32, device="cuda")[None]
+    q = _rand(g, (1, 2, 8), torch.bfloat16)
+    out, lse = uz.paged_attention(q, k, v, table, _i32(n), with_lse=True, check=True)
+    want, want_lse, off, _ = ref.attention64(q, k1, v1, _i32([0]), _i32(page))
+    assert within(out, want, off + 2.0 ** -20) <= 1.0  # the missing token weighs less than 2^-31 e^20 of all
+    assert float((lse.double() - want_lse - math.log(2048)).abs().max()) <= 2.0 ** -16
+    short = uz.paged_attention(q, k, v, table, _i32(n), window=page - 1, check=True)
+    want, _, off, _ = ref.attention64(q, k1, v1, _i32([0]), _i32(page - 1))
+    assert within(short, want, off) <= 1.0
+
+
 def test_attention_repeats_its_bits(uz):
     q, k, v, table, n, out, lse = _attend(uz, [5000, 1, 2600, 800], 2, 8, 128, 16, torch.bfloat16)
     for _ in range(5):
