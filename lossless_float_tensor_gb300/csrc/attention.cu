@@ -99,11 +99,6 @@ template <bool BF>
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
     return to16x2(lo, hi, BF ? UZIP_BF16 : UZIP_FP16);
 }
-template <bool BF>
-__device__ __forceinline__ uint16_t pack1(float v) {
-    return to16(v, BF ? UZIP_BF16 : UZIP_FP16);
-}
-
 // Live tokens [lo, len) of sequence i and its tiles; a sequence without tokens
 // has one tile of none, and so has one whose length cannot be (bad).
 struct Live {
@@ -153,10 +148,10 @@ __device__ __forceinline__ bool next_part(const Attention& a, Place& p) {
             p.s = live_of(a, ++p.i);
         }
     } else {  // whole rows, one for each block in turn
-        const int64_t at = int64_t(p.i) * a.pairs + p.row + gridDim.x;
-        if (at >= int64_t(a.seqs) * a.pairs) return false;
-        const int i = int(at / a.pairs);
-        p.row = int(at - int64_t(i) * a.pairs);
+        p.row += a.skip_row;
+        int i = p.i + a.skip_seq;
+        if (p.row >= a.pairs) p.row -= a.pairs, ++i;
+        if (i >= a.seqs) return false;
         if (i != p.i) p.s = live_of(a, i);
         p.i = i;
     }
@@ -501,26 +496,34 @@ __global__ void __launch_bounds__(kThreads, Shape<DP>::kBlocks) attention_kernel
             const int last = int(((at.begin + kRowCost + at.s.tiles) * blocks - 1) / total);
             a.row_record[int64_t(at.i) * a.pairs + at.row] = make_int2(whole ? -1 : int(blockIdx.x), last);
         }
-        for (int x = threadIdx.x; x < heads * DP; x += kThreads) {
-            const int h = x / DP, e = x % DP;
+        for (int x = threadIdx.x; x < heads * (DP / 4); x += kThreads) {  // four results each
+            const int h = x / (DP / 4), e = x % (DP / 4) * 4;
             if (e >= a.d) continue;
-            float top = -INFINITY, sum = 0.f, val = 0.f;
+            float top = -INFINITY, sum = 0.f;
+            float4 val = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
             for (uint32_t w = 0; w < kWarps; ++w) top = fmaxf(top, stat[w][h].x);
 #pragma unroll
             for (uint32_t w = 0; w < kWarps; ++w) {
                 const float by = weight(stat[w][h].x, top);
+                const float4 v = *reinterpret_cast<const float4*>(ring + where[w] + (h * kOut + e) * 4);
                 sum += stat[w][h].y * by;
-                val += reinterpret_cast<const float*>(ring + where[w])[h * kOut + e] * by;
+                val.x += v.x * by, val.y += v.y * by, val.z += v.z * by, val.w += v.w * by;
             }
             if (whole) {
                 const bool none = at.s.len == 0 && !at.s.bad;
                 const int hq = head0 + h;
-                a.out[at.i * a.out_row + hq * a.out_head + e] = pack1<BF>(none ? 0.f : val / sum);
+                const float by = none ? 0.f : 1.f / sum;
+                const uint2 r = none ? make_uint2(0, 0) : make_uint2(pack2<BF>(val.x * by, val.y * by), pack2<BF>(val.z * by, val.w * by));
+                uint16_t* to = a.out + at.i * a.out_row + hq * a.out_head + e;
+                if (a.out_quads)
+                    *reinterpret_cast<uint2*>(to) = r;
+                else
+                    to[0] = uint16_t(r.x), to[1] = uint16_t(r.x >> 16), to[2] = uint16_t(r.y), to[3] = uint16_t(r.y >> 16);
                 if (a.lse && e == 0)
                     a.lse[int64_t(at.i) * a.q_heads + hq] = none ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
             } else {
-                a.part_o[(part * kHeads + h) * a.d + e] = val;
+                *reinterpret_cast<float4*>(a.part_o + (part * kHeads + h) * a.d + e) = val;
                 if (e == 0) a.part_ml[part * kHeads + h] = make_float2(top, sum);
             }
         }
@@ -602,8 +605,12 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const __grid_constant__ 
     if (h >= heads) return;
     const int hq = r.y / a.blocks * a.group + blk * kept + h;
     uint16_t* to = a.out + r.x * a.out_row + hq * a.out_head + e;
-#pragma unroll
-    for (int c = 0; c < 4; ++c) to[c] = pack1<BF>(s.val[c] / s.sum);
+    const float by = 1.f / s.sum;
+    const uint2 v = make_uint2(pack2<BF>(s.val[0] * by, s.val[1] * by), pack2<BF>(s.val[2] * by, s.val[3] * by));
+    if (a.out_quads)
+        *reinterpret_cast<uint2*>(to) = v;
+    else
+        to[0] = uint16_t(v.x), to[1] = uint16_t(v.x >> 16), to[2] = uint16_t(v.y), to[3] = uint16_t(v.y >> 16);
     if (a.lse && e == 0) a.lse[int64_t(r.x) * a.q_heads + hq] = (s.top + log2f(s.sum)) * 0.6931471805599453f;
 }
 

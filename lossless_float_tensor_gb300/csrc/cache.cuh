@@ -50,6 +50,8 @@ struct Attention {
     int32_t page_shift;
     int32_t q_pairs;     // whether neighbouring values of q may be read together
     int32_t alike;       // whether keys and values have the same strides
+    int32_t out_quads;   // whether four neighbouring results may be written together
+    int32_t skip_seq, skip_row;  // whole rows: from a block's row to its next, in sequences and rows of one
     int32_t cut;         // whether a sequence's tokens may be cut between blocks
     float scale, cap;
     uint16_t* out;

@@ -317,6 +317,8 @@ uzip_status uzip_paged_attention(const uzip_paged_attention_args* a, void* d_wor
     r.cut = plan.cut;
     r.scale = a->scale, r.cap = a->softcap;
     r.out = static_cast<uint16_t*>(a->out), r.out_row = out.stride(2), r.out_head = out.stride(3);
+    r.out_quads = aligned(a->out, 8) && r.out_row % 4 == 0 && r.out_head % 4 == 0;
+    r.skip_seq = int32_t(plan.grid) / r.pairs, r.skip_row = int32_t(plan.grid) % r.pairs;
     r.lse = a->lse, r.status = d_status;
     return finish(launch_attention(r, a->dtype, plan, s));
 }
