@@ -408,8 +408,8 @@ uint32_t cluster_for(int64_t items) { return items <= 2 * int64_t(kThreads) ? 1 
 
 // ---- copies -----------------------------------------------------------------------
 
-constexpr uint32_t kCopyThreads = 512;
-constexpr int kCopyAhead = 4;
+constexpr uint32_t kCopyThreads = 256;
+constexpr int kCopyAhead = 8;
 constexpr int64_t kPiece = int64_t(kCopyThreads) * kCopyAhead;  // 16-byte units of a piece
 
 // Every block first looks all pairs over, with a bit for each page that is
