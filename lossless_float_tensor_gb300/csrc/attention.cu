@@ -7,8 +7,8 @@
 // Every key and value is read once and used for 4 operations a query head, 2 to 16
 // operations a byte: what bounds it is memory, and the work of a block is to keep
 // enough of it in flight.  128 sequences of 1024 to 12288 tokens, 8 x 4 heads of
-// 128 in bf16: 533 us, 6.55 TB/s of 6.79 that a copy reaches; 131072 tokens of one
-// sequence: 89.7 us, 5.99 TB/s, 8 us of it start, end and joining.  The products
+// 128 in bf16: 527 to 535 us, 6.6 TB/s of 6.79 that a copy reaches; 131072 tokens of
+// one sequence: 89.3 us, 6.0 TB/s, 8 us of it start, end and joining.  The products
 // still need matrix instructions (8 query heads would take 54 TFLOP/s of plain
 // ones); they run transposed, tokens or head values as the rows and query heads as
 // the 8 columns, so that heads that do not exist cost no rows: S^T = K Q^T and
