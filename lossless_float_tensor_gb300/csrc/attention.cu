@@ -42,17 +42,22 @@ constexpr uint32_t kWarps = 4, kThreads = kWarps * 32;
 constexpr float kSlack = 8.f;  // powers of two that a score may be over the maximum
 constexpr int kTile = 16;  // tokens of a tile: the rows of one matrix instruction
 
-template <int DP>
+template <int DP, int NT>
 struct Shape {
-    static constexpr uint32_t kPitch = DP * 2 + 16;             // bytes from token to token
-    static constexpr uint32_t kStage = 2 * kTile * kPitch;      // keys, then values
+    static constexpr uint32_t kPitch = DP * 2 + 16;         // bytes from token to token
+    static constexpr uint32_t kStage = 2 * kTile * kPitch;  // keys, then values
     // blocks on an SM, with the stages that fit: 64 sequences of 16 to 4096 tokens, d = 128, take 92.0 us on three of
-    // two stages, 102.6 on two of three
-    static constexpr uint32_t kBlocks = DP <= 128 ? 3 : 1;
-    static constexpr uint32_t kRoom = 227 * 1024 / kBlocks - 2048;
+    // two stages, 102.6 on two of three.  Where 32 query heads' sums take the registers: two
+    static constexpr uint32_t kBlocks = NT == 4 && DP > 64 ? 2 : DP <= 128 ? 3 : DP <= 192 ? 2 : 1;
+    // queries: in registers up to 32 of them a lane, else in shared memory, read again for each tile (64 sequences of
+    // 2000 to 6000 tokens, 4 x 16 heads of 256: 221 us with spilled registers, 181)
+    static constexpr bool kShared = NT * DP > 256;
+    static constexpr uint32_t kQueries = kShared ? 8 * NT * kPitch : 0;
+    static constexpr uint32_t kRoom = 227 * 1024 / kBlocks - 2048 - kQueries;
     static constexpr uint32_t kMost = kRoom / (kWarps * kStage);
     static constexpr uint32_t kStages = kMost < 8 ? kMost : 8;
-    static constexpr uint32_t kSmem = kWarps * kStages * kStage;
+    static constexpr uint32_t kSmem = kWarps * kStages * kStage + kQueries;
+    static_assert(kStages >= 2, "one to use, one to fetch into");
 };
 
 // 16 bytes into shared memory; 16 zeros where not `there`
@@ -239,19 +244,23 @@ __device__ bool first_part(const Attention& a, Place& p, int64_t& total, int64_t
 __device__ __forceinline__ float weight(float z, float m) { return z == -INFINITY ? 0.f : fast_exp2(z - m); }
 
 template <int DP, int NT, bool BF>
-__global__ void __launch_bounds__(kThreads, Shape<DP>::kBlocks) attention_kernel(const __grid_constant__ Attention a) {
-    using S = Shape<DP>;
+__global__ void __launch_bounds__(kThreads, (Shape<DP, NT>::kBlocks)) attention_kernel(const __grid_constant__ Attention a) {
+    using S = Shape<DP, NT>;
     constexpr int kSteps = DP / 16;
     constexpr int kStages = int(S::kStages);
     constexpr int kHeads = 8 * NT;
     constexpr int kOut = DP + 4;  // floats from head to head of a warp's sums in shared memory
-    static_assert(kHeads * kOut * 4 <= int(S::kStage), "a warp's sums fit one stage");
+    constexpr int kRound = NT < 2 ? NT : 2;  // of 8 heads: those whose sums fit one stage
+    static_assert(kRound * 8 * kOut * 4 <= int(S::kStage), "a warp's sums fit one stage");
     extern __shared__ __align__(128) uint8_t ring[];
     __shared__ float2 stat[kWarps][kHeads];
+    __shared__ uint32_t where[kWarps];
     wait_for_launch_before();
 
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
     const uint32_t mine = smem_u32(ring) + warp * kStages * S::kStage;
+    uint8_t* const queries = ring + kWarps * kStages * S::kStage;
+    const uint32_t q_at = smem_u32(queries) + (lane / 16 * 8 + lane % 8) * S::kPitch + lane / 8 % 2 * 16;
     Place ahead;
     int64_t total = 0, blocks = 0;
     if (!first_part(a, ahead, total, blocks)) return;  // the whole block
@@ -365,29 +374,26 @@ __global__ void __launch_bounds__(kThreads, Shape<DP>::kBlocks) attention_kernel
     do {
         const int blk = at.row % a.blocks, head0 = at.row / a.blocks * a.group + blk * kHeads;
         const int heads = min(kHeads, a.group - blk * kHeads);
-        uint32_t q[NT][kSteps][2];
-        {
-            const uint16_t* q_row = a.q + at.i * a.q_row;
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                const int h = nt * 8 + lane / 4;
-                const uint16_t* qh = q_row + int64_t(head0 + min(h, heads - 1)) * a.q_head;
-#pragma unroll
-                for (int ks = 0; ks < kSteps; ++ks) {
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const int col = ks * 16 + e * 8 + lane % 4 * 2;
-                        uint32_t w = 0;
-                        if (h < heads && col < a.d) {
-                            if (a.q_pairs)
-                                w = *reinterpret_cast<const uint32_t*>(qh + col);
-                            else
-                                w = qh[col] | uint32_t(qh[col + 1]) << 16;
-                        }
-                        q[nt][ks][e] = w;
-                    }
-                }
+        // two neighbouring values of a query; zeros where there is no head or column
+        auto query = [&](int h, int col) -> uint32_t {
+            if (h >= heads || col >= a.d) return 0;
+            const uint16_t* at_q = a.q + at.i * a.q_row + int64_t(head0 + h) * a.q_head + col;
+            return a.q_pairs ? *reinterpret_cast<const uint32_t*>(at_q) : at_q[0] | uint32_t(at_q[1]) << 16;
+        };
+        uint32_t q[S::kShared ? 1 : NT][S::kShared ? 1 : kSteps][2];
+        if constexpr (S::kShared) {
+            for (int x = threadIdx.x; x < kHeads * DP / 2; x += kThreads) {
+                const int h = x / (DP / 2), col = x % (DP / 2) * 2;
+                *reinterpret_cast<uint32_t*>(queries + h * S::kPitch + col * 2) = query(h, col);
             }
+            __syncthreads();
+        } else {
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int ks = 0; ks < kSteps; ++ks)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) q[nt][ks][e] = query(nt * 8 + lane / 4, ks * 16 + e * 8 + lane % 4 * 2);
         }
         float o[NT][kSteps][4] = {};
         float m[NT][2], l[NT][2];
@@ -412,21 +418,35 @@ __global__ void __launch_bounds__(kThreads, Shape<DP>::kBlocks) attention_kernel
             refill = stage;
             stage = stage + 1 == kStages ? 0 : stage + 1;
 
-            float z[NT][4] = {}, z2[NT][4] = {};  // two chains of sums: half the wait for each product's result
+            // two chains of sums, where there are few heads: half the wait for each product's result
+            constexpr int kChains = NT < 4 ? 2 : 1;
+            float z[NT][4] = {}, z2[kChains == 2 ? NT : 1][4] = {};
             const uint32_t k_at = keys + lane % 16 * S::kPitch + lane / 16 * 16;
 #pragma unroll
             for (int ks = 0; ks < kSteps; ++ks) {
                 uint32_t f[4];
                 load4(f, k_at + ks * 32);
+                if constexpr (S::kShared) {
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) multiply<BF>(ks % 2 ? z2[nt] : z[nt], f, q[nt][ks][0], q[nt][ks][1]);
+                    for (int nt = 0; nt < NT; nt += 2) {
+                        uint32_t b[4];
+                        load4(b, q_at + nt * 8 * S::kPitch + ks * 32);
+#pragma unroll
+                        for (int c = 0; c < 2; ++c)
+                            multiply<BF>(kChains == 2 && ks % 2 ? z2[(nt + c) % (kChains == 2 ? NT : 1)] : z[nt + c], f, b[2 * c], b[2 * c + 1]);
+                    }
+                } else {
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+                        multiply<BF>(kChains == 2 && ks % 2 ? z2[nt % (kChains == 2 ? NT : 1)] : z[nt], f, q[nt][ks][0], q[nt][ks][1]);
+                }
             }
             uint32_t p[NT][2];
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    z[nt][e] = (z[nt][e] + z2[nt][e]) * scale;
+                    z[nt][e] = (kChains == 2 ? z[nt][e] + z2[nt % (kChains == 2 ? NT : 1)][e] : z[nt][e]) * scale;
                     // cap tanh(x / cap) = cap - 2 cap / (exp(2 x / cap) + 1)
                     if (a.cap > 0) z[nt][e] = cap - 2.f * cap * fast_reciprocal(fast_exp2(z[nt][e]) + 1.f);
                 }
@@ -473,61 +493,65 @@ __global__ void __launch_bounds__(kThreads, Shape<DP>::kBlocks) attention_kernel
             __syncwarp();
         }
 
-        // the four warps' sums, each in the warp's own free stage, and their maxima
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-#pragma unroll
-                for (int x = 4; x < 32; x *= 2) l[nt][c] += __shfl_xor_sync(~0u, l[nt][c], x);
-                const int h = nt * 8 + lane % 4 * 2 + c;
-                if (lane < 4) stat[warp][h] = make_float2(m[nt][c], broken ? NAN : l[nt][c]);
-                float* to = reinterpret_cast<float*>(ring + (warp * kStages + refill) * S::kStage) + h * kOut + lane / 4;
-#pragma unroll
-                for (int ks = 0; ks < kSteps; ++ks) to[ks * 16] = o[nt][ks][c], to[ks * 16 + 8] = o[nt][ks][c + 2];
-            }
-        }
-        __shared__ uint32_t where[kWarps];
-        if (lane == 0) where[warp] = (warp * kStages + refill) * S::kStage;
-        __syncthreads();
+        // the four warps' sums, each in the warp's own free stage, and their maxima; 16 heads at a time
         const bool whole = at.j0 == 0 && at.j1 == at.s.tiles;
         const int64_t part = 2 * int64_t(blockIdx.x) + (at.j0 == 0);
         if (a.row_record && at.j0 == 0 && threadIdx.x == 0) {
             const int last = int(((at.begin + kRowCost + at.s.tiles) * blocks - 1) / total);
             a.row_record[int64_t(at.i) * a.pairs + at.row] = make_int2(whole ? -1 : int(blockIdx.x), last);
         }
-        for (int x = threadIdx.x; x < heads * (DP / 4); x += kThreads) {  // four results each
-            const int h = x / (DP / 4), e = x % (DP / 4) * 4;
-            if (e >= a.d) continue;
-            float top = -INFINITY, sum = 0.f;
-            float4 val = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (lane == 0) where[warp] = (warp * kStages + refill) * S::kStage;
 #pragma unroll
-            for (uint32_t w = 0; w < kWarps; ++w) top = fmaxf(top, stat[w][h].x);
+        for (int first = 0; first < NT; first += kRound) {
 #pragma unroll
-            for (uint32_t w = 0; w < kWarps; ++w) {
-                const float by = weight(stat[w][h].x, top);
-                const float4 v = *reinterpret_cast<const float4*>(ring + where[w] + (h * kOut + e) * 4);
-                sum += stat[w][h].y * by;
-                val.x += v.x * by, val.y += v.y * by, val.z += v.z * by, val.w += v.w * by;
+            for (int n = 0; n < kRound; ++n) {
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    float& sum = l[first + n][c];
+#pragma unroll
+                    for (int x = 4; x < 32; x *= 2) sum += __shfl_xor_sync(~0u, sum, x);
+                    const int h = n * 8 + lane % 4 * 2 + c;
+                    if (lane < 4) stat[warp][first * 8 + h] = make_float2(m[first + n][c], broken ? NAN : sum);
+                    float* to = reinterpret_cast<float*>(ring + (warp * kStages + refill) * S::kStage) + h * kOut + lane / 4;
+#pragma unroll
+                    for (int ks = 0; ks < kSteps; ++ks) to[ks * 16] = o[first + n][ks][c], to[ks * 16 + 8] = o[first + n][ks][c + 2];
+                }
             }
-            if (whole) {
-                const bool none = at.s.len == 0 && !at.s.bad;
-                const int hq = head0 + h;
-                const float by = none ? 0.f : 1.f / sum;
-                const uint2 r = none ? make_uint2(0, 0) : make_uint2(pack2<BF>(val.x * by, val.y * by), pack2<BF>(val.z * by, val.w * by));
-                uint16_t* to = a.out + at.i * a.out_row + hq * a.out_head + e;
-                if (a.out_quads)
-                    *reinterpret_cast<uint2*>(to) = r;
-                else
-                    to[0] = uint16_t(r.x), to[1] = uint16_t(r.x >> 16), to[2] = uint16_t(r.y), to[3] = uint16_t(r.y >> 16);
-                if (a.lse && e == 0)
-                    a.lse[int64_t(at.i) * a.q_heads + hq] = none ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
-            } else {
-                *reinterpret_cast<float4*>(a.part_o + (part * kHeads + h) * a.d + e) = val;
-                if (e == 0) a.part_ml[part * kHeads + h] = make_float2(top, sum);
+            __syncthreads();
+            const int here = min(8 * kRound, heads - first * 8);
+            for (int x = threadIdx.x; x < here * (DP / 4); x += kThreads) {  // four results each
+                const int in = x / (DP / 4), e = x % (DP / 4) * 4, h = first * 8 + in;
+                if (e >= a.d) continue;
+                float top = -INFINITY, sum = 0.f;
+                float4 val = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                for (uint32_t w = 0; w < kWarps; ++w) top = fmaxf(top, stat[w][h].x);
+#pragma unroll
+                for (uint32_t w = 0; w < kWarps; ++w) {
+                    const float by = weight(stat[w][h].x, top);
+                    const float4 v = *reinterpret_cast<const float4*>(ring + where[w] + (in * kOut + e) * 4);
+                    sum += stat[w][h].y * by;
+                    val.x += v.x * by, val.y += v.y * by, val.z += v.z * by, val.w += v.w * by;
+                }
+                if (whole) {
+                    const bool none = at.s.len == 0 && !at.s.bad;
+                    const int hq = head0 + h;
+                    const float by = none ? 0.f : 1.f / sum;
+                    const uint2 r = none ? make_uint2(0, 0) : make_uint2(pack2<BF>(val.x * by, val.y * by), pack2<BF>(val.z * by, val.w * by));
+                    uint16_t* to = a.out + at.i * a.out_row + hq * a.out_head + e;
+                    if (a.out_quads)
+                        *reinterpret_cast<uint2*>(to) = r;
+                    else
+                        to[0] = uint16_t(r.x), to[1] = uint16_t(r.x >> 16), to[2] = uint16_t(r.y), to[3] = uint16_t(r.y >> 16);
+                    if (a.lse && e == 0)
+                        a.lse[int64_t(at.i) * a.q_heads + hq] = none ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
+                } else {
+                    *reinterpret_cast<float4*>(a.part_o + (part * kHeads + h) * a.d + e) = val;
+                    if (e == 0) a.part_ml[part * kHeads + h] = make_float2(top, sum);
+                }
             }
+            __syncthreads();
         }
-        __syncthreads();
     } while (next_part(a, at));
     fetch_wait<0>();
 }
@@ -622,11 +646,11 @@ cudaError_t launch_as(const Attention& a, const AttentionPlan& plan, cudaStream_
     cudaError_t err = cudaGetDevice(&dev);
     if (err != cudaSuccess) return err;
     if (dev >= 64 || !(ready.load(std::memory_order_relaxed) >> dev & 1)) {
-        err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(Shape<DP>::kSmem));
+        err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(Shape<DP, NT>::kSmem));
         if (err != cudaSuccess) return err;
         if (dev < 64) ready.fetch_or(uint64_t(1) << dev, std::memory_order_relaxed);
     }
-    err = launch_next(kern, dim3(plan.grid), kThreads, Shape<DP>::kSmem, 1, s, a);
+    err = launch_next(kern, dim3(plan.grid), kThreads, Shape<DP, NT>::kSmem, 1, s, a);
     if (err != cudaSuccess || !plan.cut || plan.grid < 2) return err;
     const uint32_t results = std::min<uint32_t>(plan.heads, a.group) * a.d;
     if (a.row_record)
@@ -634,20 +658,36 @@ cudaError_t launch_as(const Attention& a, const AttentionPlan& plan, cudaStream_
     return launch_next(join_kernel<BF, false>, dim3(plan.grid - 1, (results + 4 * kThreads - 1) / (4 * kThreads)), kThreads, 0, 1, s, a, int(plan.heads));
 }
 
+template <int DP, int NT>
+cudaError_t launch_typed(const Attention& a, int dtype, const AttentionPlan& plan, cudaStream_t s) {
+    return dtype == UZIP_BF16 ? launch_as<DP, NT, true>(a, plan, s) : launch_as<DP, NT, false>(a, plan, s);
+}
+
 template <int DP>
 cudaError_t launch_wide(const Attention& a, int dtype, const AttentionPlan& plan, cudaStream_t s) {
-    if (plan.heads == 8) return dtype == UZIP_BF16 ? launch_as<DP, 1, true>(a, plan, s) : launch_as<DP, 1, false>(a, plan, s);
-    return dtype == UZIP_BF16 ? launch_as<DP, 2, true>(a, plan, s) : launch_as<DP, 2, false>(a, plan, s);
+    if (plan.heads == 8) return launch_typed<DP, 1>(a, dtype, plan, s);
+    if constexpr (DP <= 128)
+        if (plan.heads == 32) return launch_typed<DP, 4>(a, dtype, plan, s);
+    return launch_typed<DP, 2>(a, dtype, plan, s);
+}
+
+// Blocks on an SM, by head size and query heads kept, as Shape has them.
+int blocks_on_sm(int64_t d, uint32_t heads) {
+    if (d > 192) return 1;
+    if (d > 128) return 2;
+    return heads == 32 && d > 64 ? 2 : 3;
 }
 
 }  // namespace
 
 AttentionPlan plan_attention(int64_t seqs, int64_t kv_heads, int64_t group, int64_t d, int64_t most, int sms) {
     AttentionPlan p;
-    p.heads = group <= 8 ? 8 : 16;
+    // more query heads share a key head's pass over memory, up to what registers hold of their sums (64 sequences of 2000
+    // to 6000 tokens, 4 x 32 heads of 128: 165 us in two passes, 106 in one)
+    p.heads = group <= 8 ? 8 : group <= 16 || d > 128 ? 16 : 32;
     const int64_t rows = seqs * kv_heads * ((group + p.heads - 1) / p.heads);
     const int64_t tiles = std::max<int64_t>(1, (most + kTile - 1) / kTile);
-    const int64_t room = int64_t(sms) * (d <= 128 ? 3 : 1);
+    const int64_t room = int64_t(sms) * blocks_on_sm(d, p.heads);
     // up to 512 tokens a row stays whole: joining would take 2.2 us, as much as four tiles of a warp
     p.cut = tiles > 32;
     p.grid = uint32_t(std::max<int64_t>(1, std::min(room, p.cut ? rows * ((tiles + kRowCost + kLeast - 1) / kLeast) : rows)));

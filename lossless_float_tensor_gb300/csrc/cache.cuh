@@ -42,7 +42,7 @@ struct Attention {
     int64_t ldt;
     const int32_t* lengths;
     int32_t seqs, q_heads, group, d, pages, page;
-    int32_t blocks;      // groups of kept heads: a key head's query heads are taken 8 or 16 at a time
+    int32_t blocks;      // groups of kept heads: a key head's query heads are taken 8, 16 or 32 at a time
     int32_t pairs;       // kv_heads * blocks: rows of work of a sequence
     int32_t most;        // tokens that a sequence's row of the table holds (capped to int32)
     int32_t window;      // 0: none
@@ -66,7 +66,7 @@ struct Attention {
 
 struct AttentionPlan {
     uint32_t grid;   // blocks
-    uint32_t heads;  // kept heads: 8 or 16
+    uint32_t heads;  // kept heads: 8, 16 or 32
     bool cut;
     int64_t by_row;  // rows, where they are few and joined one by one; else 0
 };

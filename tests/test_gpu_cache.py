@@ -59,7 +59,7 @@ def _attend(uz, lengths, heads, group, d, page, dtype, order="heads", seed=0, q_
 @pytest.mark.parametrize("lengths,heads,group,d,page", [
     ([1], 1, 1, 64, 16), ([1, 0, 2, 15, 16, 17], 2, 4, 128, 16), ([0, 0, 0], 2, 1, 64, 16), ([33, 500, 512, 513, 1], 4, 8, 128, 16),
     ([100, 7], 3, 5, 80, 24), ([257, 64, 65], 1, 7, 96, 32), ([40, 300], 2, 3, 8, 7), ([70, 129], 2, 2, 256, 64), ([70, 129], 2, 9, 256, 1),
-    ([19, 77], 1, 16, 192, 16), ([300, 12], 2, 12, 128, 128), ([90], 1, 33, 64, 8), ([31, 200], 2, 20, 104, 16), ([5, 9] * 40, 1, 4, 72, 16),
+    ([19, 77], 1, 16, 192, 16), ([300, 12], 2, 12, 128, 128), ([90], 1, 33, 64, 8), ([19, 200, 0], 2, 32, 128, 16), ([77, 300], 1, 24, 80, 16), ([33], 2, 64, 40, 16), ([31, 200], 2, 20, 104, 16), ([5, 9] * 40, 1, 4, 72, 16),
 ])
 def test_attention(uz, lengths, heads, group, d, page, dtype):
     _attend(uz, lengths, heads, group, d, page, dtype)
@@ -70,7 +70,8 @@ def test_attention(uz, lengths, heads, group, d, page, dtype):
 @pytest.mark.parametrize("lengths,heads,group,d,page", [
     ([5000], 1, 8, 128, 16), ([4096, 1, 0, 4097, 3000], 2, 4, 128, 16), ([20000, 3], 1, 1, 64, 64), ([2777, 0, 1, 900], 3, 5, 80, 24),
     ([1500, 6000], 2, 16, 128, 32), ([700, 1400], 1, 40, 96, 16), ([3333], 2, 3, 256, 5), ([1000, 2500], 1, 11, 192, 16),
-    ([600] * 150, 2, 2, 64, 16), ([513, 30] * 130, 1, 4, 128, 16), ([40000], 8, 4, 128, 16),
+    ([1300, 700], 2, 32, 128, 16), ([900, 2000, 5], 1, 17, 64, 16), ([800, 1], 2, 27, 96, 24), ([1100], 1, 71, 64, 16), ([1000, 30], 1, 48, 128, 7),
+    ([1200, 3], 2, 16, 256, 16), ([1200, 3], 1, 32, 192, 16), ([600] * 150, 2, 2, 64, 16), ([513, 30] * 130, 1, 4, 128, 16), ([40000], 8, 4, 128, 16),
 ])
 def test_attention_cut_between_blocks(uz, lengths, heads, group, d, page, dtype):
     _attend(uz, lengths, heads, group, d, page, dtype)
