@@ -252,6 +252,28 @@ def test_attention_views(uz, lengths, dtype):
     assert torch.equal(_bits(uz.paged_attention(one, k, v, table, n)), _bits(uz.paged_attention(one.contiguous(), k, v, table, n)))
 
 
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("lengths,heads,group,d,page", [([30, 300, 0], 3, 2, 128, 16), ([900, 1500], 2, 5, 80, 24), ([2000, 17], 2, 20, 64, 16), ([1200], 1, 16, 256, 8)])
+def test_keys_and_values_laid_out_apart(uz, lengths, heads, group, d, page, dtype):
+    """Keys by head and values by token: attention, storing and copying go by each pool's own strides."""
+    q, k, v, table, n, out, _ = _attend(uz, lengths, heads, group, d, page, dtype)
+    by_token = v.transpose(1, 2).contiguous().transpose(1, 2)
+    assert by_token.stride() != k.stride() or heads == 1 or page == 1
+    assert torch.equal(_bits(uz.paged_attention(q, k, by_token, table, n, check=True)), _bits(out))
+    assert torch.equal(_bits(uz.paged_attention(q, k.transpose(1, 2).contiguous().transpose(1, 2), v, table, n, check=True)), _bits(out))
+    t = len(lengths)
+    new = _rand(_gen(1), (t, heads, d), dtype)
+    slots = torch.arange(t, device="cuda") * page
+    want = v.clone()
+    want[:t, :, 0] = new
+    kp = k.clone()
+    uz.rotary_append(q, new, new, torch.zeros(t, dtype=torch.int64, device="cuda"), uz.rotary_frequencies(d), kp, by_token, slots, check=True)
+    assert torch.equal(_bits(by_token), _bits(want)) and torch.equal(_bits(kp[:t, :, 0]), _bits(new))
+    last = k.shape[0] - 1
+    uz.cache_copy(kp, by_token, _i32([0, last]), check=True)
+    assert torch.equal(_bits(by_token[last]), _bits(want[0])) and torch.equal(_bits(kp[last]), _bits(kp[0]))
+
+
 def test_attention_parts_join_by_lse(uz):
     """Attention over two halves of a context, joined by their log-sum-exps, is attention over the whole."""
     q, k, v, table, n, out, lse = _attend(uz, [960, 480], 2, 4, 128, 16, torch.float16)
