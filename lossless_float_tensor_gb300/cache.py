@@ -115,7 +115,7 @@ uzip_cache_copy, uzip_cache_copy_workspace_size = _entry("uzip_cache_copy", Cach
 # A step of a server makes these calls for every layer, so their host time
 # counts: arguments are packed in one go (struct, in the C structure's native
 # layout) instead of set one by one, and each tensor is asked for each thing
-# once (attention of one token 20 us of host time, 14 so).
+# once (attention of one token 20 us of host time, 12 so).
 
 class _Entry:
     """A C entry point that takes its structure as packed bytes."""
@@ -185,7 +185,7 @@ def _elsewhere(dev, stream):
 def _device(t, name, dims):
     """The index of the device of a tensor of `dims` dimensions."""
     dev = t.get_device()
-    if dev < 0 or not t.is_cuda or t.dim() != dims:
+    if dev < 0 or t.dim() != dims:
         _refuse(f"{name}: expected a CUDA tensor of {dims} dimensions")
     return dev
 
@@ -216,16 +216,15 @@ def _list(t, name, shape, dtype, dev):
 def rotary_frequencies(dim, *, base=10000.0, scaling="none", factor=1.0, trained=0, fast=32.0, slow=1.0, device="cuda"):
     """Rotary frequencies of the first `dim` (even) values of a head, for
     rotary() and rotary_append(): a float64 tensor of dim / 2 radians per
-    position, f_j = base^(-2 j / dim), stretched for contexts `factor` times as
-    long as trained:
+    position (finite), f_j = base^(-2 j / dim), stretched for contexts `factor`
+    times as long as trained:
 
     "none"    as they are
     "linear"  f_j / factor
     "ntk"     those of base factor^(dim / (dim - 2)): the fastest stays, the slowest is divided by factor
-    "yarn"    f_j / factor where a wave turns at most `slow` times over the `trained` positions, f_j where it turns at
-              least `fast` times, and between the two by a ramp linear in the index j, from the largest index whose wave
-              turns `fast` times down to the smallest whose wave turns `slow` times (rounded outward)
-    "bands"   the same with a ramp linear in the number of turns
+    "yarn"    f_j (1 - r_j) + f_j / factor r_j with r_j rising from 0 at j = floor(i(fast)) to 1 at j = ceil(i(slow)), where
+              i(n) = dim log(trained / (2 pi n)) / (2 log base) is the index whose wave turns n times over the trained positions
+    "bands"   the same with r_j falling from 1 to 0 linearly in the number of turns, from `slow` of them to `fast`
 
     "yarn" goes with an amplitude for rotary()'s scale, usually 0.1 ln(factor) + 1.
     """

@@ -475,7 +475,7 @@ __global__ void __launch_bounds__(kCopyThreads) copy_kernel(const __grid_constan
                 src = x - run * a.run + o * a.outer_step[which] + i * a.inner_step[which];
                 at[u] = x - run * a.run + o * a.outer_step[2 + which] + i * a.inner_step[2 + which];
             }
-            held[u] = __ldg(from + src);
+            held[u] = from[src];
         }
 #pragma unroll
         for (int u = 0; u < kCopyAhead; ++u)
