@@ -65,7 +65,7 @@ typedef struct {
     float scale;
     int64_t t, q_heads, kv_heads, d, rot;
     const int64_t* positions; /* [t] */
-    const double* freqs;      /* [rot / 2] */
+    const double* freqs;      /* [rot / 2], finite */
     const void* q;
     int64_t q_row, q_head;
     const void* k;
