@@ -334,6 +334,54 @@ def test_attention_of_2_to_31_tokens(uz):
     assert within(short, want, off) <= 1.0
 
 
+@pytest.mark.parametrize("wide", [False, True])
+def test_as_many_sequences_as_there_may_be(uz, wide):
+    """65536 sequences of 0 to 40 tokens (in a table for 640, where blocks cut
+    rows), reserved, attended to with equal scores, half of them freed."""
+    from lossless_float_tensor_gb300 import UzipError
+
+    seqs, page, heads, d = 65536, 8, 2, 16
+    width = 80 if wide else 5
+    g = _gen(11)
+    n = torch.randint(0, 41, (seqs,), generator=g, device="cuda").int()
+    need = (n + page - 1) // page
+    state = ref.state(int(need.sum()) + 5, seqs, width)
+    tokens = int(n.sum()) + 9
+    slots, positions, copies = uz.cache_reserve(*state, n, tokens, page, check=True)
+    assert torch.equal(state[2], n) and bool((copies == -1).all()) and bool((slots[-9:] == -1).all())
+    row = torch.repeat_interleave(torch.arange(seqs, device="cuda"), n.long())
+    first = n.long().cumsum(0) - n
+    assert torch.equal(positions[:-9], torch.arange(tokens - 9, device="cuda") - first[row])
+    # pages are taken in order, so page j of sequence i is the number of pages before
+    base = need.long().cumsum(0) - need
+    assert torch.equal(slots[:-9], (base[row] + positions[:-9] // page) * page + positions[:-9] % page)
+    k = torch.zeros(state[0].numel(), heads, page, d, dtype=torch.bfloat16, device="cuda")
+    v = torch.randint(-3, 4, k.shape, generator=g, device="cuda").to(torch.bfloat16)
+    q = _rand(g, (seqs, heads, d), torch.bfloat16)
+    out, lse = uz.paged_attention(q, k, v, state[1], state[2], with_lse=True, check=True)
+    by_token = v.transpose(1, 2).flatten(0, 1).double()[slots[:-9]]
+    total = torch.zeros(seqs, heads, d, dtype=torch.float64, device="cuda").index_add_(0, row, by_token)
+    want = total / n.clamp(min=1)[:, None, None]
+    # sums of whole numbers are exact; the quotient is the sum times a rounded reciprocal (2 roundings of 2^-24), then
+    # rounded to the type: values of 8 bits are half a step apart from the next by 2^-8 of themselves at most
+    off = want.abs() * (2.0 ** -8 + 2.0 ** -20)
+    assert bool(((out.double() - want).abs() <= off).all())
+    assert float((lse[n > 0].double() - n[n > 0].double().log()[:, None]).abs().max()) <= 2.0 ** -17
+    gone = torch.randperm(seqs, generator=g, device="cuda")[: seqs // 2].int()
+    uz.cache_free(*state, gone, page, check=True)
+    held = torch.ones(seqs, dtype=torch.bool, device="cuda")
+    held[gone.long()] = False
+    assert int(state[0].sum()) == int(need[held].sum()) and not bool(state[2][~held].any())
+    moves = uz.cache_compact(*state, page, check=True)
+    used = int(need[held].sum())
+    assert bool((state[0][:used] == 1).all()) and not bool(state[0][used:].any())
+    uz.cache_copy(k, v, moves, check=True)
+    again = uz.paged_attention(q, k, v, state[1], state[2], check=True)
+    assert bool(((again[held].double() - want[held]).abs() <= off[held]).all()) and not bool(again[~held].any())
+    with pytest.raises(UzipError):
+        uz.paged_attention(q[:1].expand(65537, -1, -1), k, v, state[1][:1].expand(65537, -1), torch.zeros(65537, dtype=torch.int32, device="cuda"))
+
+
 def test_attention_repeats_its_bits(uz):
     q, k, v, table, n, out, lse = _attend(uz, [5000, 1, 2600, 800], 2, 8, 128, 16, torch.bfloat16)
     for _ in range(5):
