@@ -173,6 +173,14 @@ def test_attention_not_a_number_stays_in_its_sequence(uz):
                 assert pool is v or bool(out[1, 4:].isnan().all())
                 out[1, 4:] = clean[1, 4:]
                 assert torch.equal(_bits(out), _bits(clean))
+        # a value that is infinite, and weighs something, makes its column so
+        at = int(table[1, 1]), 1, 3, 5
+        kept = v[at].clone()
+        for big in (math.inf, -math.inf):
+            v[at] = big
+            out = uz.paged_attention(q / 8, k, v, table, n, check=True)
+            assert bool((out[1, 4:, 5] == big).all()) and int(out.isinf().sum()) == 4 and not bool(out.isnan().any())
+        v[at] = kept
         # every key of a head without a finite score: the softmax of nothing but -inf is no number
         q2 = torch.zeros_like(q)
         q2[..., 3] = 1
