@@ -25,7 +25,7 @@ constexpr int kAhead = 2;  // heads whose values are in flight in a lane
 
 // Radians per position as a fraction of a turn, modulo 1, in units of 2^-64: the
 // 53 bits of the number times 2^66 / (2 pi) in integers, shifted to its exponent
-// (fp64 arithmetic would take longer than the rest of a token).
+// (fp64 instructions are slow here).
 __device__ __forceinline__ uint64_t turns_of(double radians) {
     constexpr uint64_t kPerTurn = 0xA2F9836E4E44152Aull;  // 2^66 / (2 pi)
     const uint64_t bits = uint64_t(__double_as_longlong(radians));
