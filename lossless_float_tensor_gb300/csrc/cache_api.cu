@@ -210,7 +210,7 @@ bool state_ok(const uzip_cache_args& a, bool memory) {
         !within(a.width, 0, kMost31 - 256) || (a.seqs > 1 && !within(a.ldt, a.width, kMostStride)))
         return false;
     if (!memory) return true;
-    const int64_t entries = a.seqs ? (a.seqs - 1) * (a.seqs > 1 ? a.ldt : 0) + a.width : 0;
+    const int64_t entries = a.seqs && a.width ? (a.seqs - 1) * (a.seqs > 1 ? a.ldt : 0) + a.width : 0;
     return list_ok(a.refs, a.pages) && list_ok(a.table, entries) && list_ok(a.lengths, a.seqs);
 }
 

@@ -783,6 +783,65 @@ def test_state_that_cannot_be(uz):
             assert int(status) == 1 and all(torch.equal(a, b) for a, b in zip(s, before))
 
 
+def test_smallest_caches(uz):
+    """No sequences, no columns, no pages, one page, no tokens."""
+    status = torch.zeros((), dtype=torch.int32, device="cuda")
+    none = _i32()
+    for pages, seqs, width, counts, tokens, code in ((5, 0, 4, [], 3, 0), (5, 0, 4, [], 0, 0), (5, 2, 0, [0, 0], 2, 0), (5, 2, 0, [0, 1], 2, 3),
+                                                     (0, 2, 3, [0, 0], 0, 0), (0, 2, 3, [1, 0], 1, 3), (1, 1, 1, [1], 1, 0), (1, 1, 1, [5], 5, 3), (1, 3, 2, [0, 4, 0], 4, 0)):
+        state = ref.state(pages, seqs, width)
+        slots, positions, copies = uz.cache_reserve(*state, _i32(*counts), tokens, 4, status=status)
+        assert int(status) == code, (pages, seqs, width, counts)
+        real = 0 if code else sum(counts)
+        assert slots.tolist() == list(range(real)) + [-1] * (tokens - real) and copies.shape == (seqs, 2)
+        assert positions.tolist() == list(range(real)) + [0] * (tokens - real)
+        moves = uz.cache_compact(*state, 4, check=True)
+        assert moves.shape == (pages // 2, 2) and bool((moves == -1).all())
+        uz.cache_fork(*state, none, none, 4, check=True)
+        uz.cache_free(*state, none, 4, check=True)
+        uz.cache_fork(*state, _i32(-1, -1), _i32(-1, -1), 4, check=True)
+        uz.cache_free(*state, _i32(-1), 4, check=True)
+        uz.cache_free(*state, _i32(0), 4, status=status)
+        assert int(status) == (0 if seqs else 1)
+        assert not bool(state[0].any()) or seqs > 1
+    k = torch.zeros(0, 1, 4, 8, dtype=torch.bfloat16, device="cuda")
+    uz.cache_copy(k, k.clone(), none.view(0, 2), check=True)
+    uz.cache_copy(k, k.clone(), _i32([-1, -1]), check=True)
+
+
+def test_pages_in_a_graph(uz):
+    """Fork, free and compact captured once and replayed on states that change in between."""
+    page, pages, seqs, width = 4, 60, 8, 10
+    lists = [ref.ListCache(pages, page, seqs, width) for _ in range(2)]
+    state, want = ref.state(pages, seqs, width), None
+    parents, children, gone = _i32(0, 1), _i32(6, 7), _i32(1, 2, -1)
+
+    def work():
+        uz.cache_fork(*state, parents, children, page)
+        uz.cache_free(*state, gone, page)
+        return uz.cache_compact(*state, page)
+
+    eager = work()
+    assert bool((eager == -1).all())
+    for x in state:
+        x.zero_()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        moves = work()
+    for n, counts in enumerate(([9, 5, 7, 1, 0, 4, 0, 0], [1, 30, 2, 0, 0, 0, 0, 0])):
+        for x in state:
+            x.zero_()
+        lists[n].reserve(counts, sum(counts))
+        uz.cache_reserve(*state, _i32(*counts), sum(counts), page, check=True)
+        graph.replay()
+        lists[n].fork([0, 1], [6, 7])
+        lists[n].free([1, 2])
+        want = lists[n].compact()
+        assert moves.tolist() == want
+        _same(lists[n], state)
+
+
 def test_pages_refusals(uz):
     from lossless_float_tensor_gb300 import UzipError
 
