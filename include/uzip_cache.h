@@ -24,8 +24,9 @@
  *
  * Common rules, as of uzip_ops.h: the caller gives every buffer; workspaces of
  * uzip_*_workspace_size(args) bytes, 256-byte aligned (NULL where that is 0),
- * used until the call's work on the stream ends; calls that share no output and
- * no workspace may overlap; the same inputs give the same bits.  d_status
+ * used until the call's work on the stream ends; outputs overlap neither inputs
+ * nor each other (but see uzip_rotary); calls that share no output and no
+ * workspace may overlap; the same inputs give the same bits.  d_status
  * (device i32, nullable) receives 0 or a uzip_status found on the device.
  */
 #ifndef UZIP_CACHE_H

@@ -282,6 +282,7 @@ uzip_status uzip_paged_attention(const uzip_paged_attention_args* a, void* d_wor
     const Block k = pool_of(a->k_pages, a->pages, a->kv_heads, a->page, {a->kp_page, a->kp_head, a->kp_token}, a->d),
                 v = pool_of(a->v_pages, a->pages, a->kv_heads, a->page, {a->vp_page, a->vp_head, a->vp_token}, a->d);
     if (!q.readable(2) || !k.readable(16) || !v.readable(16) || !out.writable(2)) return UZIP_ERR_INVALID_ARG;
+    if (a->seqs && a->out == a->q) return UZIP_ERR_INVALID_ARG;  // other blocks may still read a query when its result is written
     if (a->seqs > 1 && !within(a->ldt, 0, kMostStride)) return UZIP_ERR_INVALID_ARG;
     const int64_t ldt = a->seqs > 1 ? a->ldt : 0;
     if (a->seqs && !list_ok(a->table, a->width ? (a->seqs - 1) * ldt + a->width : 0)) return UZIP_ERR_INVALID_ARG;

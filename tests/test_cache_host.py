@@ -1,5 +1,6 @@
 """Checks of the cache operators' C entry points that need no GPU: what is
-refused before any CUDA call, what workspace is asked for, and the frequencies."""
+refused, what workspace is asked for, and the frequencies.  (Without a GPU no
+address is one of a device; the refusals run again on real ones there.)"""
 import math
 
 import pytest
@@ -39,7 +40,7 @@ def _append(cache, **kw):
 
 
 def _attention(cache, **kw):
-    return _set(cache.PagedAttentionArgs(dtype=0, seqs=3, q_heads=4, kv_heads=2, d=16, pages=8, page=4, width=5, q=FAKE, q_row=64, q_head=16,
+    return _set(cache.PagedAttentionArgs(dtype=0, seqs=3, q_heads=4, kv_heads=2, d=16, pages=8, page=4, width=5, q=3 * FAKE, q_row=64, q_head=16,
                                          k_pages=FAKE, kp_page=128, kp_head=64, kp_token=16, v_pages=FAKE, vp_page=128, vp_head=64, vp_token=16,
                                          table=FAKE, ldt=5, lengths=FAKE, scale=0.25, out=FAKE, out_row=64, out_head=16), kw)
 
@@ -57,35 +58,44 @@ def _copy(cache, **kw):
     return _set(a, kw)
 
 
-@pytest.mark.parametrize("change,want", [
+ROTARY = [
     (dict(dtype=1), BAD_DTYPE), (dict(dtype=3), BAD_DTYPE), (dict(dtype=-1), BAD_DTYPE), (dict(interleaved=2), BAD_ARG), (dict(backward=-1), BAD_ARG),
     (dict(t=-1), BAD_ARG), (dict(t=1 << 31), BAD_ARG), (dict(d=0), BAD_ARG), (dict(d=1025), BAD_ARG), (dict(rot=18), BAD_ARG), (dict(rot=7), BAD_ARG),
     (dict(rot=-2), BAD_ARG), (dict(q_heads=-1), BAD_ARG), (dict(q=None), BAD_ARG), (dict(k=None), BAD_ARG), (dict(q=FAKE + 1), BAD_ARG),
     (dict(q_row=-32), BAD_ARG), (dict(q_row=1 << 50), BAD_ARG), (dict(q_out=None), BAD_ARG), (dict(q_out_row=31), BAD_ARG), (dict(q_out_head=8), BAD_ARG),
     (dict(q_out_row=0), BAD_ARG), (dict(positions=None), BAD_ARG), (dict(positions=FAKE + 4), BAD_ARG), (dict(freqs=FAKE + 4), BAD_ARG),
     (dict(slots=FAKE), BAD_ARG),
-])
+]
+
+
+@pytest.mark.parametrize("change,want", ROTARY)
 def test_rotary_refuses(cache, change, want):
     assert cache.uzip_rotary(_rotary(cache, **change), None, 0, None, 0) == want
 
 
-@pytest.mark.parametrize("change,want", [
+APPEND = [
     (dict(dtype=4), BAD_DTYPE), (dict(backward=1), BAD_ARG), (dict(kv_heads=0), BAD_ARG), (dict(d=12, rot=12), BAD_ARG), (dict(page=0), BAD_ARG),
     (dict(v=None), BAD_ARG), (dict(slots=None), BAD_ARG), (dict(slots=FAKE + 4), BAD_ARG), (dict(k_pages=None), BAD_ARG), (dict(k_pages=FAKE + 8), BAD_ARG),
     (dict(kp_token=20), BAD_ARG), (dict(v_pages=FAKE), BAD_ARG), (dict(kp_token=8), BAD_ARG), (dict(vp_page=56), BAD_ARG), (dict(pages=-1), BAD_ARG), (dict(pages=1 << 31), BAD_ARG),
-])
+]
+
+
+@pytest.mark.parametrize("change,want", APPEND)
 def test_rotary_append_refuses(cache, change, want):
     assert cache.uzip_rotary_append(_append(cache, **change), None, 0, None, 0) == want
 
 
-@pytest.mark.parametrize("change,want", [
+ATTENTION = [
     (dict(dtype=1), BAD_DTYPE), (dict(reserved=1), BAD_ARG), (dict(seqs=-1), BAD_ARG), (dict(seqs=65537), BAD_ARG), (dict(q_heads=3), BAD_ARG),
     (dict(q_heads=0), BAD_ARG), (dict(kv_heads=0), BAD_ARG), (dict(d=12), BAD_ARG), (dict(d=264), BAD_ARG), (dict(d=0), BAD_ARG), (dict(page=0), BAD_ARG),
     (dict(width=-1), BAD_ARG), (dict(window=-1), BAD_ARG), (dict(softcap=-1.0), BAD_ARG), (dict(softcap=math.inf), BAD_ARG), (dict(softcap=math.nan), BAD_ARG), (dict(softcap=1e-42), BAD_ARG),
     (dict(q=None), BAD_ARG), (dict(q=FAKE + 1), BAD_ARG), (dict(k_pages=FAKE + 8), BAD_ARG), (dict(kp_token=17), BAD_ARG), (dict(vp_head=-64), BAD_ARG),
-    (dict(out=None), BAD_ARG), (dict(out_row=63), BAD_ARG), (dict(out_head=0), BAD_ARG), (dict(ldt=-5), BAD_ARG), (dict(table=None), BAD_ARG),
+    (dict(out=None), BAD_ARG), (dict(out=3 * FAKE), BAD_ARG), (dict(out_row=63), BAD_ARG), (dict(out_head=0), BAD_ARG), (dict(ldt=-5), BAD_ARG), (dict(table=None), BAD_ARG),
     (dict(table=FAKE + 2), BAD_ARG), (dict(lengths=None), BAD_ARG), (dict(lse=FAKE + 1), BAD_ARG),
-])
+]
+
+
+@pytest.mark.parametrize("change,want", ATTENTION)
 def test_paged_attention_refuses(cache, change, want):
     assert cache.uzip_paged_attention(_attention(cache, **change), None, 0, None, 0) == want
 
@@ -94,12 +104,16 @@ STATE = [dict(pages=-1), dict(page=0), dict(seqs=-1), dict(seqs=65537), dict(wid
          dict(table=None), dict(lengths=None)]
 
 
-@pytest.mark.parametrize("change", STATE + [dict(tokens=-1), dict(list=None), dict(slots=None), dict(positions=FAKE + 4), dict(pairs=None)])
+RESERVE = STATE + [dict(tokens=-1), dict(list=None), dict(slots=None), dict(positions=FAKE + 4), dict(pairs=None)]
+FORK = STATE + [dict(n=-1), dict(list=None)]
+
+
+@pytest.mark.parametrize("change", RESERVE)
 def test_reserve_refuses(cache, change):
     assert cache.uzip_cache_reserve(_state(cache, **change), None, 0, None, 0) == BAD_ARG
 
 
-@pytest.mark.parametrize("change", STATE + [dict(n=-1), dict(list=None)])
+@pytest.mark.parametrize("change", FORK)
 def test_fork_and_free_refuse(cache, change):
     assert cache.uzip_cache_fork(_state(cache, **change), None, 0, None, 0) == BAD_ARG
     assert cache.uzip_cache_free(_state(cache, **change), None, 0, None, 0) == BAD_ARG
@@ -114,13 +128,16 @@ def test_compact_refuses(cache, change):
     assert cache.uzip_cache_compact(_state(cache, **change), None, 0, None, 0) == BAD_ARG
 
 
-@pytest.mark.parametrize("change,want", [
+COPY = [
     (dict(dtype=1), BAD_DTYPE), (dict(reserved=1), BAD_ARG), (dict(layers=-1), BAD_ARG), (dict(heads=0), BAD_ARG), (dict(d=12), BAD_ARG),
     (dict(d=512), BAD_ARG), (dict(to_pages=1572865, from_pages=1572865), BAD_ARG), (dict(to_pages=9), BAD_ARG), (dict(k_to=FAKE + 4096), BAD_ARG),
     (dict(k=FAKE + 8, k_to=FAKE + 8), BAD_ARG), (dict(kt_page=256), BAD_ARG), (dict(k_token=8, kt_token=8), BAD_ARG), (dict(pairs=None), BAD_ARG),
     (dict(pairs=FAKE + 4), BAD_ARG), (dict(n=-1), BAD_ARG), (dict(v=FAKE, v_to=FAKE), BAD_ARG), (dict(k_to=3 * FAKE, v_to=3 * FAKE), BAD_ARG),
     (dict(k_to=3 * FAKE, v_to=FAKE), BAD_ARG), (dict(k_layer=-1024, kt_layer=-1024), BAD_ARG),
-])
+]
+
+
+@pytest.mark.parametrize("change,want", COPY)
 def test_copy_refuses(cache, change, want):
     assert cache.uzip_cache_copy(_copy(cache, **change), None, 0, None, 0) == want
 

@@ -422,7 +422,7 @@ def test_attention_refusals(uz):
         (q, k, v[:-1], table, n, {}), (q, k, v, table.long(), n, {}), (q, k, v, table[:1], n, {}), (q, k, v, table, n.long(), {}),
         (q, k, v, table, n[:1], {}), (q[:, :7], k, v, table, n, {}), (q.cpu(), k, v, table, n, {}), (q, k.cpu(), v, table, n, {}),
         (q, k, v, table.cpu(), n, {}), (q, k, v, table, n.cpu(), {}), (q, k[..., ::2], v[..., ::2], table, n, {}), (q, k, v, table, n, dict(window=-1)),
-        (q, k, v, table, n, dict(softcap=-2.0)), (q, k, v, table, n, dict(out=q[:1])), (q, k, v, table, n, dict(out=q.float())),
+        (q, k, v, table, n, dict(softcap=-2.0)), (q, k, v, table, n, dict(out=q)), (q, k, v, table, n, dict(out=q[:1])), (q, k, v, table, n, dict(out=q.float())),
         (q, k, v, table.T.contiguous().T, n, {}), (q, k, v, table, n, dict(out=q[:1].expand(2, -1, -1))),
     ]
     for i, (*args, kw) in enumerate(bad):
@@ -934,6 +934,69 @@ def test_copy_refuses_pairs_that_collide(uz):
         with pytest.raises(UzipError):
             uz.cache_copy(*args)
     uz.cache_copy(k, v, torch.empty(0, 2, dtype=torch.int32, device="cuda"), check=True)
+
+
+def test_c_entry_points_refuse_one_wrong_thing(uz):
+    """Arguments that are taken as they are, and refused with any one of the
+    changes that the tests without a GPU list."""
+    from lossless_float_tensor_gb300 import cache
+    from tests import test_cache_host as host
+
+    room = torch.zeros(1 << 20, dtype=torch.uint8, device="cuda")
+    stream = torch.cuda.current_stream().cuda_stream
+    # each pointer its own 16 KB, zeros: lengths of 0, pages and slots of 0, frequencies of 0; status behind
+    status = torch.zeros((), dtype=torch.int32, device="cuda")
+
+    def real(a):
+        for n, (name, kind) in enumerate(a._fields_):
+            if kind is cache._vp and getattr(a, name):
+                setattr(a, name, room.data_ptr() + n * 16384)
+        if isinstance(a, cache.CacheCopyArgs):  # within one pool
+            a.k_to, a.v_to = a.k, a.v
+        return a
+
+    def check(entry, build, changes):
+        size = getattr(cache, entry.__name__ + "_workspace_size")
+        a = real(build(cache))
+        assert size(a) <= 1 << 18
+        call = lambda a: entry(a, room.data_ptr() + (3 << 18), 1 << 18, status.data_ptr(), stream)  # noqa: E731
+        assert call(a) == 0, entry.__name__
+        torch.cuda.synchronize()
+        for change in changes:
+            change, want = change if isinstance(change, tuple) else (change, host.BAD_ARG)
+            a = real(build(cache))
+            for name, v in change.items():
+                if isinstance(v, int) and v >= host.FAKE:  # the same place off its boundary, or another pointer's
+                    v = (getattr(a, name) or room.data_ptr()) + v % host.FAKE if v % host.FAKE else None
+                if v is None and change[name] is not None:
+                    break
+                setattr(a, name, v)
+            else:
+                assert call(a) == want, (entry.__name__, change)
+                torch.cuda.synchronize()
+
+    check(cache.uzip_rotary, host._rotary, [c for c in host.ROTARY if "slots" not in c[0]])
+    check(cache.uzip_rotary_append, host._append, host.APPEND)
+    check(cache.uzip_paged_attention, host._attention, host.ATTENTION)
+    check(cache.uzip_cache_reserve, host._state, host.RESERVE)
+    check(cache.uzip_cache_fork, host._state, host.FORK + [dict(from_=None)])
+    check(cache.uzip_cache_free, host._state, host.FORK)
+    check(cache.uzip_cache_compact, host._state, host.STATE + [dict(pairs=None)])
+    check(cache.uzip_cache_copy, host._copy, [c for c in host.COPY if "k_to" not in c[0]])
+    # pointers that have to differ, or to agree
+    for build, entry, same in ((host._append, cache.uzip_rotary_append, ("v_pages", "k_pages")), (host._attention, cache.uzip_paged_attention, ("out", "q")),
+                               (host._copy, cache.uzip_cache_copy, ("v_to", "k_to"))):
+        a = real(build(cache))
+        setattr(a, same[0], getattr(a, same[1]))
+        assert entry(a, None, 0, status.data_ptr(), stream) == host.BAD_ARG
+    a = real(host._rotary(cache))
+    a.slots = room.data_ptr()
+    assert cache.uzip_rotary(a, None, 0, status.data_ptr(), stream) == host.BAD_ARG
+    # memory that is not the device's, or ends too early
+    for name in ("q", "k_pages", "table", "lengths", "out"):
+        a = real(host._attention(cache))
+        setattr(a, name, host.FAKE)
+        assert cache.uzip_paged_attention(a, None, 0, None, stream) == host.BAD_ARG, name
 
 
 # ---- together ---------------------------------------------------------------------
