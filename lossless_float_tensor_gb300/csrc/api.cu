@@ -41,6 +41,12 @@ namespace uzip {
 bool device_range_ok(const void* p, uint64_t bytes) {
     if (bytes == 0) return true;
     if (p == nullptr) return false;
+    AddrRangeFn fn = addr_range_fn();
+    CUdeviceptr base = 0;
+    size_t size = 0;
+    const bool plain = fn && fn(&base, &size, reinterpret_cast<CUdeviceptr>(p)) == CUDA_SUCCESS;
+    const uint64_t start = reinterpret_cast<uint64_t>(p) - uint64_t(base);
+    if (plain && start <= size && bytes <= size - start) return true;  // nearly every call ends here
     cudaPointerAttributes attr;
     if (cudaPointerGetAttributes(&attr, p) != cudaSuccess) {
         cudaGetLastError();
@@ -48,13 +54,7 @@ bool device_range_ok(const void* p, uint64_t bytes) {
     }
     if (attr.type == cudaMemoryTypeHost) return attr.devicePointer != nullptr;
     if (attr.type != cudaMemoryTypeDevice && attr.type != cudaMemoryTypeManaged) return false;
-    AddrRangeFn fn = addr_range_fn();
-    if (!fn) return true;
-    CUdeviceptr base = 0;
-    size_t size = 0;
-    if (fn(&base, &size, reinterpret_cast<CUdeviceptr>(p)) != CUDA_SUCCESS) return true;  // not a plain allocation
-    const uint64_t start = reinterpret_cast<uint64_t>(p) - uint64_t(base);
-    return start <= size && bytes <= size - start;
+    return !plain;  // a device allocation that the driver query does not know, or one that ends too early
 }
 
 namespace {
