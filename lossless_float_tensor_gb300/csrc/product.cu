@@ -1291,10 +1291,18 @@ cudaError_t make_map(CUtensorMap* map, const Operand& o, uint64_t rows, uint64_t
     const uint64_t group = slices ? 128 : groups > 1 ? o.group * 2 : std::min<uint64_t>(o.ld * 2 * outer, uint64_t(1) << 39);
     const cuuint64_t strides[2] = {o.ld * 2, group};
     const cuuint32_t box[3] = {64, box_outer, slices ? slices : 1}, ones[3] = {1, 1, 1};
-    const CUresult r = fn(map, dtype == UZIP_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,
-                          const_cast<void*>(o.p), dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                          CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+    auto encode = [&] {
+        return fn(map, dtype == UZIP_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,
+                  const_cast<void*>(o.p), dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    };
+    if (encode() == CUDA_SUCCESS) return cudaSuccess;
+    // a driver call in a thread that has made no CUDA call yet: it has no context, which setting its device gives it
+    int dev = 0;
+    cudaError_t err = cudaGetDevice(&dev);
+    if (err == cudaSuccess) err = cudaSetDevice(dev);
+    if (err != cudaSuccess) return err;
+    return encode() == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
 uint32_t row_width(const void* p, uint64_t ld) {
