@@ -115,7 +115,7 @@ uzip_cache_copy, uzip_cache_copy_workspace_size = _entry("uzip_cache_copy", Cach
 # A step of a server makes these calls for every layer, so their host time
 # counts: arguments are packed in one go (struct, in the C structure's native
 # layout) instead of set one by one, and each tensor is asked for each thing
-# once (attention of one token 20 us of host time, 12 so).
+# once (attention of one token 20 us of host time, 11 so).
 
 class _Entry:
     """A C entry point that takes its structure as packed bytes."""
