@@ -53,7 +53,8 @@ struct Attention {
     int32_t out_quads;   // whether four neighbouring results may be written together
     int32_t skip_seq, skip_row;  // whole rows: from a block's row to its next, in sequences and rows of one
     int32_t cut;         // whether a sequence's tokens may be cut between blocks
-    float scale, cap;
+    float scale, cap;    // times log2 e: exponentials are powers of 2
+    float per_cap;       // the scale over the cap
     uint16_t* out;
     int64_t out_row, out_head;
     float* lse;

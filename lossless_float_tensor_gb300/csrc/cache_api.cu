@@ -316,7 +316,9 @@ uzip_status uzip_paged_attention(const uzip_paged_attention_args* a, void* d_wor
     r.most = int32_t(most_tokens(a->width, a->page));
     r.window = a->window >= r.most ? 0 : int32_t(a->window);
     r.cut = plan.cut;
-    r.scale = a->scale, r.cap = a->softcap;
+    constexpr float kLog2e = 1.4426950408889634f;
+    r.scale = a->scale * kLog2e, r.cap = std::min(a->softcap * kLog2e, std::numeric_limits<float>::max());
+    r.per_cap = a->softcap > 0.f ? a->scale / a->softcap : 0.f;
     r.out = static_cast<uint16_t*>(a->out), r.out_row = out.stride(2), r.out_head = out.stride(3);
     r.out_quads = aligned(a->out, 8) && r.out_row % 4 == 0 && r.out_head % 4 == 0;
     r.skip_seq = int32_t(plan.grid) / r.pairs, r.skip_row = int32_t(plan.grid) % r.pairs;

@@ -1,0 +1,134 @@
+"""Attention of one token where its arithmetic could lose digits: capped scores
+of any cap.  Bounds here go by the scores and the weights themselves, so that
+none of them grows with what it is to bound."""
+import math
+
+import pytest
+import torch
+
+from tests import _cache as ref
+from tests._products import ROUND, TINY, within
+
+pytestmark = pytest.mark.gpu
+
+DTYPES = (torch.bfloat16, torch.float16)
+
+
+@pytest.fixture(scope="module")
+def uz():
+    import lossless_float_tensor_gb300 as uz
+
+    return uz
+
+
+def _gen(seed):
+    return torch.Generator(device="cuda").manual_seed(seed)
+
+
+def _f32(x):
+    """What a float argument is in 32 bits."""
+    return float(torch.tensor(x, dtype=torch.float32))
+
+
+# ---- capped scores ------------------------------------------------------------
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("cap", [1e-3, 1.0, 30.0, 50.0, 1e3, 1e4, 1e5, 1e6, 1e8, 1e20, 1e37, 3e38])
+def test_a_capped_score_keeps_its_digits(uz, cap, dtype):
+    """The log-sum-exp of one token is its score.  Keys with a single 1 give
+    products without rounding, so all that is off is the cap: the factors in 32
+    bits (scale, cap, scale over cap, log2 e, ln 2: together some 8 roundings of
+    2^-24), 2^-21 for the exponential, its reciprocal and their difference from
+    half the cap on, 2^-23 for the polynomial below.  2^-19 of the score bounds
+    them all."""
+    d, heads = 64, 8
+    u = 10.0 ** torch.linspace(-7, 1.5, 400, dtype=torch.float64)
+    u = torch.cat([u, torch.linspace(0.4, 0.6, 200, dtype=torch.float64), 10.0 ** torch.linspace(-38, -7, 200, dtype=torch.float64)])
+    x = (cap * torch.cat([u, -u])).to(dtype)
+    x = x[x.double().abs().ge(2.0 ** -24 if dtype == torch.float16 else 1e-30) & x.double().abs().le(6e4 if dtype == torch.float16 else 5e37)]
+    # scores of ordinary size, whatever the cap
+    x = torch.cat([x, torch.linspace(-40, 40, 333, dtype=torch.float64).to(dtype)])
+    x = torch.cat([x, x[: -x.numel() % heads]]).view(-1, heads).cuda()
+    q = torch.zeros(x.shape[0], heads, d, dtype=dtype, device="cuda")
+    q[..., 5] = x
+    k = torch.zeros(1, 1, 1, d, dtype=dtype, device="cuda")
+    k[..., 5] = 1
+    v = torch.randn(k.shape, generator=_gen(1), device="cuda").to(dtype)
+    table = torch.zeros(x.shape[0], 1, dtype=torch.int32, device="cuda")
+    for scale in (1.0, -0.25):
+        out, lse = uz.paged_attention(q, k, v, table, table[:, 0] + 1, scale=scale, softcap=cap, with_lse=True, check=True)
+        s = x.double() * scale
+        want = _f32(cap) * torch.tanh(s / _f32(cap))
+        assert within(lse, want, 2.0 ** -19 * want.abs() + 2.0 ** -126) <= 1.0
+        assert torch.equal(out, v[0, 0, 0].expand_as(out))
+
+
+def attention64(q, k, v, table, lengths, scale=None, softcap=0.0, least=0.0):
+    """(out, lse, bound of |out - computed|, bound of |lse - computed|).
+
+    A score is off by the 32-bit sum of d products (each addition by at most
+    2^-23 of the magnitudes so far) and by 2^-19 of itself for what is done to
+    it, capped or not.  A weight is off by that in numerator and sum, 2^-20 for
+    the exponential, and its rounding to the type, or `least` of the largest
+    weight where it lies below the type's normal range; sums over tokens run in
+    32 bits, and the result is rounded once."""
+    u, tiny = ROUND[q.dtype], TINY[q.dtype]
+    s, hq, d = q.shape
+    heads, page = k.shape[1], k.shape[2]
+    scale = d ** -0.5 if scale is None else scale
+    out, lse = torch.zeros(s, hq, d, dtype=torch.float64, device=q.device), torch.zeros(s, hq, dtype=torch.float64, device=q.device)
+    off, off_lse = torch.zeros_like(out), torch.zeros_like(lse)
+    for i, n in enumerate(lengths.tolist()):
+        t = torch.arange(n, device=q.device)
+        at = table[i].long()[t // page]
+        kk, vv = k[at, :, t % page].double(), v[at, :, t % page].double()  # [n, heads, d]
+        qq = q[i].double().view(heads, hq // heads, d)
+        z = torch.einsum("hgd,nhd->hgn", qq, kk) * scale
+        slip = (d + 4) * 2.0 ** -23 * abs(scale) * torch.einsum("hgd,nhd->hgn", qq.abs(), kk.abs())
+        if softcap:
+            z = softcap * torch.tanh(z / softcap)
+        slip = slip + 2.0 ** -19 * z.abs()
+        # the sum weighs each token's slip as the result does; one token is off by its own
+        w = torch.softmax(z, -1)
+        worst = (w * slip).sum(-1, keepdim=True)
+        each = u + 1.1 * (slip + worst) + 2.0 ** -19 + (n + 8) * 2.0 ** -23
+        err = torch.einsum("hgn,nhd->hgd", w * each, vv.abs()) + n * least * vv.abs().amax(0)[:, None]
+        o, total = torch.einsum("hgn,nhd->hgd", w, vv), torch.logsumexp(z, -1)
+        out[i], lse[i] = o.reshape(hq, d), total.reshape(hq)
+        off[i] = (u * (o.abs() + err) + err + tiny).reshape(hq, d)
+        off_lse[i] = (1.1 * worst[..., 0] + 2.0 ** -20 * (2 + total.abs()) + (n + 8) * 2.0 ** -23).reshape(hq)
+    return out, lse, off, off_lse
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("cap", [30.0, 1e3, 1e4, 1e5, 1e6, 1e8, 1e20, 3.4e38])
+@pytest.mark.parametrize("lengths,heads,group,d", [([77, 1, 300], 2, 4, 96), ([900, 2000], 1, 8, 128), ([700, 40], 1, 17, 64), ([650], 1, 12, 256)])
+def test_attention_of_large_caps(uz, lengths, heads, group, d, cap, dtype):
+    """A cap far above the scores is hardly any: no digits of them are lost."""
+    g = _gen(d)
+    pages = sum(-(-n // 16) for n in lengths) + 3
+    k, v = ref.pools(g, pages, heads, 16, d, dtype)
+    table, n = ref.tables(lengths, 16, pages)
+    q = (torch.randn(len(lengths), heads * group, d, generator=g, device="cuda") * 2).to(dtype)
+    got = uz.paged_attention(q, k, v, table, n, softcap=cap, with_lse=True, check=True)
+    want, want_lse, off, off_lse = attention64(q, k, v, table, n, softcap=_f32(cap), least=2.0 ** -25 if dtype == torch.float16 else 0.0)
+    assert within(got[0], want, off) <= 1.0 and within(got[1], want_lse, off_lse) <= 1.0
+    if cap >= 1e8:  # (x / cap)^2 is below half a step of 32 bits: nothing is left of the cap
+        plain = uz.paged_attention(q, k, v, table, n, with_lse=True)
+        assert torch.equal(got[0].view(torch.int16), plain[0].view(torch.int16)) and torch.equal(got[1], plain[1])
+
+
+def test_infinite_scores_meet_the_cap(uz):
+    """A product past 32 bits, or an infinite key, is a score of plus or minus the cap; what is no number stays none."""
+    d = 64
+    q = torch.zeros(4, 1, d, dtype=torch.bfloat16, device="cuda")
+    q[:, 0, 0] = torch.tensor([1.0, -1.0, 3e38, math.nan], device="cuda")
+    k = torch.zeros(1, 1, 1, d, dtype=torch.bfloat16, device="cuda")
+    v = torch.ones_like(k)
+    table = torch.zeros(4, 1, dtype=torch.int32, device="cuda")
+    for key, signs in ((math.inf, (1, -1, 1)), (-3e38, (-1, 1, -1))):
+        k[..., 0] = key
+        for cap in (5.0, 1e6, 1e30):
+            _, lse = uz.paged_attention(q, k, v, table, table[:, 0] + 1, scale=1.0, softcap=cap, with_lse=True)
+            want = cap * torch.tensor(signs, dtype=torch.float64, device="cuda")
+            assert float(((lse[:3, 0].double() - want) / want).abs().max()) <= 2.0 ** -20 and bool(lse[3].isnan().all())
