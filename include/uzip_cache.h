@@ -99,7 +99,9 @@ uzip_status uzip_rotary_append(const uzip_rotary_args* a, void* d_workspace, uin
  *   out = sum_t softmax(z)_t v_t,  lse = log sum_t exp(z_t).
  * The new token's own key and value are in the cache and count in its length.
  * A sequence of length 0 gives zeros and an lse of -inf.  Products are summed in
- * 32 bits; the exponentials are rounded to the dtype for the second product.
+ * 32 bits; the exponentials are rounded to the dtype for the second product, each
+ * by half a step of itself (fp16: the largest is 2^15 there, so weights down to
+ * 2^-29 of it keep all digits; those below 2^-40 of it are lost).
  * Values of a page behind a sequence's last token, or before its window, are
  * never used, whatever they hold.  A length outside [0, width * page] or a page
  * outside [0, pages) among those used gives NaN for that sequence and is

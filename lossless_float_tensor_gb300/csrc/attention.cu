@@ -103,6 +103,12 @@ template <bool BF>
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
     return to16x2(lo, hi, BF ? UZIP_BF16 : UZIP_FP16);
 }
+// Weights are held times 2^kLift: in fp16 the largest is 2^15, so that those down to 2^-29
+// of it are normal numbers and those down to 2^-39 are there (from 1 on, fp16 would lose
+// digits at 2^-14 and all at 2^-25, which is what a result consists of where one token
+// takes nearly all of the weight and its value is 0).  Sums and parts hold the factor too.
+template <bool BF>
+constexpr float kLift = BF ? 0.f : 15.f;
 // Live tokens [lo, len) of sequence i and its tiles; a sequence without tokens
 // has one tile of none, and so has one whose length cannot be (bad).
 struct Live {
@@ -483,11 +489,12 @@ __global__ void __launch_bounds__(kThreads, (Shape<DP, NT>::kBlocks)) attention_
                 const float from[2] = {m[nt][0] == -INFINITY ? 0.f : m[nt][0], m[nt][1] == -INFINITY ? 0.f : m[nt][1]};
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    z[nt][e] = fast_exp2(z[nt][e] - from[e % 2]);
+                    z[nt][e] = fast_exp2(BF ? z[nt][e] - from[e % 2] : z[nt][e] - from[e % 2] + kLift<BF>);
                     l[nt][e % 2] += z[nt][e];
                 }
-                // rounded to the values' type for the second product: off by half a unit each, at random, which adds up to
-                // less than the one rounding of the result; the sum l keeps them unrounded
+                // rounded to the values' type for the second product, each by half a step of itself at most; the sum l keeps
+                // them unrounded.  Where they differ the errors add up, at random, to less than the one rounding of the
+                // result; equal weights are off alike, which may be as much as that rounding and no more
                 p[nt][0] = turned8x8(pack2<BF>(z[nt][0], z[nt][1]));
                 p[nt][1] = turned8x8(pack2<BF>(z[nt][2], z[nt][3]));
             }
@@ -553,7 +560,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<DP, NT>::kBlocks)) attention_
                     else
                         to[0] = uint16_t(r.x), to[1] = uint16_t(r.x >> 16), to[2] = uint16_t(r.y), to[3] = uint16_t(r.y >> 16);
                     if (a.lse && e == 0)
-                        a.lse[int64_t(at.i) * a.q_heads + hq] = none ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
+                        a.lse[int64_t(at.i) * a.q_heads + hq] = none ? -INFINITY : (top + (log2f(sum) - kLift<BF>)) * 0.6931471805599453f;
                 } else {
                     *reinterpret_cast<float4*>(a.part_o + (part * kHeads + h) * a.d + e) = val;
                     if (e == 0) a.part_ml[part * kHeads + h] = make_float2(top, sum);
@@ -644,7 +651,7 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const __grid_constant__ 
         *reinterpret_cast<uint2*>(to) = v;
     else
         to[0] = uint16_t(v.x), to[1] = uint16_t(v.x >> 16), to[2] = uint16_t(v.y), to[3] = uint16_t(v.y >> 16);
-    if (a.lse && e == 0) a.lse[int64_t(r.x) * a.q_heads + hq] = (s.top + log2f(s.sum)) * 0.6931471805599453f;
+    if (a.lse && e == 0) a.lse[int64_t(r.x) * a.q_heads + hq] = (s.top + (log2f(s.sum) - kLift<BF>)) * 0.6931471805599453f;
 }
 
 template <int DP, int NT, bool BF>

@@ -59,7 +59,7 @@ struct Attention {
     int64_t out_row, out_head;
     float* lse;
     float* part_o;       // [2 grid][kept heads][d] sums over a part of a sequence's tokens
-    float2* part_ml;     // [2 grid][kept heads]: largest score (times log2 e), sum of exponentials
+    float2* part_ml;     // [2 grid][kept heads]: largest score (times log2 e), sum of exponentials (fp16: times 2^15)
     int4* record;        // [grid]: what a border between two blocks cuts
     int2* row_record;    // [rows]: first (-1: not cut) and last block; null where there are many rows
     int32_t* status;

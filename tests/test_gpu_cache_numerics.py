@@ -1,5 +1,5 @@
 """Attention of one token where its arithmetic could lose digits: capped scores
-of any cap.  Bounds here go by the scores and the weights themselves, so that
+of any cap, weights far below the largest.  Bounds here go by the scores and the weights themselves, so that
 none of them grows with what it is to bound."""
 import math
 
@@ -63,16 +63,18 @@ def test_a_capped_score_keeps_its_digits(uz, cap, dtype):
         assert torch.equal(out, v[0, 0, 0].expand_as(out))
 
 
-def attention64(q, k, v, table, lengths, scale=None, softcap=0.0, least=0.0):
+def attention64(q, k, v, table, lengths, scale=None, softcap=0.0):
     """(out, lse, bound of |out - computed|, bound of |lse - computed|).
 
     A score is off by the 32-bit sum of d products (each addition by at most
     2^-23 of the magnitudes so far) and by 2^-19 of itself for what is done to
     it, capped or not.  A weight is off by that in numerator and sum, 2^-20 for
-    the exponential, and its rounding to the type, or `least` of the largest
-    weight where it lies below the type's normal range; sums over tokens run in
-    32 bits, and the result is rounded once."""
+    the exponential, and its rounding to the type: by half a step of itself, in
+    fp16 (where the largest is 2^15 and steps are no less than 2^-24) by no less
+    than 2^-40 of the largest.  Sums over tokens run in 32 bits, and the result
+    is rounded once."""
     u, tiny = ROUND[q.dtype], TINY[q.dtype]
+    least = 2.0 ** -40 if q.dtype == torch.float16 else 0.0
     s, hq, d = q.shape
     heads, page = k.shape[1], k.shape[2]
     scale = d ** -0.5 if scale is None else scale
@@ -111,7 +113,7 @@ def test_attention_of_large_caps(uz, lengths, heads, group, d, cap, dtype):
     table, n = ref.tables(lengths, 16, pages)
     q = (torch.randn(len(lengths), heads * group, d, generator=g, device="cuda") * 2).to(dtype)
     got = uz.paged_attention(q, k, v, table, n, softcap=cap, with_lse=True, check=True)
-    want, want_lse, off, off_lse = attention64(q, k, v, table, n, softcap=_f32(cap), least=2.0 ** -25 if dtype == torch.float16 else 0.0)
+    want, want_lse, off, off_lse = attention64(q, k, v, table, n, softcap=_f32(cap))
     assert within(got[0], want, off) <= 1.0 and within(got[1], want_lse, off_lse) <= 1.0
     if cap >= 1e8:  # (x / cap)^2 is below half a step of 32 bits: nothing is left of the cap
         plain = uz.paged_attention(q, k, v, table, n, with_lse=True)
@@ -132,3 +134,66 @@ def test_infinite_scores_meet_the_cap(uz):
             _, lse = uz.paged_attention(q, k, v, table, table[:, 0] + 1, scale=1.0, softcap=cap, with_lse=True)
             want = cap * torch.tensor(signs, dtype=torch.float64, device="cuda")
             assert float(((lse[:3, 0].double() - want) / want).abs().max()) <= 2.0 ** -20 and bool(lse[3].isnan().all())
+
+
+# ---- weights far below the largest ----------------------------------------------
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("below", [(0, 0), (13, 15), (20.3, 20.3), (16, 24), (24.7, 24.7), (25, 30), (30, 34), (5, 39)])
+@pytest.mark.parametrize("group,d", [(1, 64), (8, 128), (16, 256), (32, 96)])
+def test_small_weights_keep_their_digits(uz, group, d, below, dtype):
+    """One token has a score some powers of two over all others, and a value of
+    0: the result is what the others add up to."""
+    g = _gen(d)
+    lengths = [2, 17, 40, 300, 2000, 2000, 2000]
+    sinks = [0, 16, 5, 299, 0, 1000, 1999]
+    pages = sum(-(-n // 16) for n in lengths) + 3
+    k, v = ref.pools(g, pages, 2, 16, d, dtype, scale=1024.0)  # results in the type's normal range
+    k[..., 3] = -(below[0] + (below[1] - below[0]) * torch.rand(k.shape[:-1], generator=g, device="cuda")).to(dtype)
+    table, n = ref.tables(lengths, 16, pages)
+    for i, t in enumerate(sinks):
+        at = int(table[i, t // 16]), slice(None), t % 16
+        k[at] = 0
+        v[at] = 0
+    q = torch.zeros(len(lengths), 2 * group, d, dtype=dtype, device="cuda")
+    q[..., 3] = 1
+    scale = _f32(math.log(2))
+    out, lse = uz.paged_attention(q, k, v, table, n, scale=scale, with_lse=True, check=True)
+    want, want_lse, off, off_lse = attention64(q, k, v, table, n, scale=scale)
+    assert within(out, want, off) <= 1.0 and within(lse, want_lse, off_lse) <= 1.0
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("lengths,heads,group,d,page", [
+    ([1, 0, 2, 15, 16, 17], 2, 4, 128, 16), ([33, 500, 512, 513, 1], 4, 8, 128, 16), ([100, 7], 3, 5, 80, 24), ([70, 129], 2, 9, 256, 1),
+    ([19, 200, 0], 2, 32, 128, 16), ([20000, 3], 1, 1, 64, 64), ([1500, 6000], 2, 16, 128, 32), ([900, 2000, 5], 1, 17, 64, 16), ([1000, 2500], 1, 11, 192, 16),
+])
+def test_attention_within_the_bounds_of_its_weights(uz, lengths, heads, group, d, page, dtype):
+    g = _gen(d + page)
+    pages = sum(-(-n // page) for n in lengths) + 3
+    k, v = ref.pools(g, pages, heads, page, d, dtype)
+    table, n = ref.tables(lengths, page, pages)
+    q = (torch.randn(len(lengths), heads * group, d, generator=g, device="cuda") * 6).to(dtype)
+    out, lse = uz.paged_attention(q, k, v, table, n, with_lse=True, check=True)
+    some = n > 0
+    want, want_lse, off, off_lse = attention64(q[some], k, v, table[some], n[some])
+    assert within(out[some], want, off) <= 1.0 and within(lse[some], want_lse, off_lse) <= 1.0
+
+
+def test_large_scores_and_values_in_fp16(uz):
+    """Scores up to where 32 bits step by more than one, and the largest values: the factor of the weights makes nothing infinite."""
+    d, n = 64, 1000
+    g = _gen(3)
+    k, v = ref.pools(g, 80, 1, 16, d, torch.float16)
+    v.copy_(torch.where(torch.rand(v.shape, generator=g, device="cuda") < 0.5, -1.0, 1.0) * 65504)
+    k.fill_(60000.0)
+    table, lengths = ref.tables([n], 16, 80)
+    q = torch.full((1, 4, d), 60000.0, dtype=torch.float16, device="cuda")
+    for scale in (1.0, 1e-3, -1e4):  # equal scores of 2.3e11, 2.3e8, -2.3e15
+        out, lse = uz.paged_attention(q, k, v, table, lengths, scale=scale, with_lse=True, check=True)
+        t = torch.arange(n, device="cuda")
+        want = v[table[0].long()[t // 16], 0, t % 16].double().mean(0)
+        # sums of at most 1000 terms of 65504 in 32 bits, one rounding of the result
+        assert within(out, want.expand(1, 4, d), 2.0 ** -11 * want.abs() + 65504 * 1008 * 2.0 ** -23) <= 1.0
+        score = 3.6e9 * d * scale
+        assert float((lse.double() - score).abs().max()) <= 2.0 ** -20 * abs(score)
