@@ -35,6 +35,29 @@ AddrRangeFn addr_range_fn() {
 
 namespace uzip {
 
+// Driver calls need a context, which a thread has only from its first runtime call
+// that needs one on: where this thread has none it gets its current device's.
+// Returns whether it got one here.
+bool bind_context() {
+    typedef CUresult (*CtxGetCurrentFn)(CUcontext*);
+    static const CtxGetCurrentFn get_current = [] {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuCtxGetCurrent", &p, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+            q != cudaDriverEntryPointSuccess) {
+            cudaGetLastError();
+            p = nullptr;
+        }
+        return reinterpret_cast<CtxGetCurrentFn>(p);
+    }();
+    CUcontext ctx = nullptr;
+    if (get_current && get_current(&ctx) == CUDA_SUCCESS && ctx) return false;
+    int dev = 0;
+    if (cudaGetDevice(&dev) == cudaSuccess && cudaSetDevice(dev) == cudaSuccess) return true;
+    cudaGetLastError();
+    return false;
+}
+
 // [p, p + bytes) must be device-accessible memory.  Device allocations are
 // checked against the allocation that holds p; mapped host memory is accepted
 // by type (its extent is not known to the driver query).
@@ -44,7 +67,8 @@ bool device_range_ok(const void* p, uint64_t bytes) {
     AddrRangeFn fn = addr_range_fn();
     CUdeviceptr base = 0;
     size_t size = 0;
-    const bool plain = fn && fn(&base, &size, reinterpret_cast<CUdeviceptr>(p)) == CUDA_SUCCESS;
+    auto known = [&] { return fn && fn(&base, &size, reinterpret_cast<CUdeviceptr>(p)) == CUDA_SUCCESS; };
+    const bool plain = known() || (bind_context() && known());
     const uint64_t start = reinterpret_cast<uint64_t>(p) - uint64_t(base);
     if (plain && start <= size && bytes <= size - start) return true;  // nearly every call ends here
     cudaPointerAttributes attr;

@@ -1296,13 +1296,7 @@ cudaError_t make_map(CUtensorMap* map, const Operand& o, uint64_t rows, uint64_t
                   const_cast<void*>(o.p), dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
                   CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     };
-    if (encode() == CUDA_SUCCESS) return cudaSuccess;
-    // a driver call in a thread that has made no CUDA call yet: it has no context, which setting its device gives it
-    int dev = 0;
-    cudaError_t err = cudaGetDevice(&dev);
-    if (err == cudaSuccess) err = cudaSetDevice(dev);
-    if (err != cudaSuccess) return err;
-    return encode() == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+    return encode() == CUDA_SUCCESS || (bind_context() && encode() == CUDA_SUCCESS) ? cudaSuccess : cudaErrorInvalidValue;
 }
 
 uint32_t row_width(const void* p, uint64_t ld) {

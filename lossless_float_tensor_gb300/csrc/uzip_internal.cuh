@@ -330,6 +330,10 @@ constexpr Magic33Table make_magic33_table() {
 // up once per (device, kernel, block shape) and cached (api.cu).
 cudaError_t launch_shape(const void* kern, int threads, size_t smem, int* sms, int* per_sm);
 
+// Gives this thread its current device's context where it has none, for driver
+// calls; returns whether it had none (api.cu).
+bool bind_context();
+
 // launchers (compress.cu, decompress.cu, pipeline.cu)
 // mode: 0 per-chunk choice, 1 whole message RAW, 2 gated (a one-warp kernel
 // decides from the first 64 KiB of input), 3 per-chunk choice with sampled
