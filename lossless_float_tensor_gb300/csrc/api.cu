@@ -15,19 +15,27 @@ using namespace uzip;
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
-typedef CUresult (*AddrRangeFn)(CUdeviceptr*, size_t*, CUdeviceptr);
+// A function of the driver, or null where it has none of that name.
+template <typename F>
+F driver_function(const char* name) {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion(name, &p, 12000, cudaEnableDefault, &q) == cudaSuccess && q == cudaDriverEntryPointSuccess)
+        return reinterpret_cast<F>(p);
+    cudaGetLastError();
+    return nullptr;
+}
 
+typedef CUresult (*AddrRangeFn)(CUdeviceptr*, size_t*, CUdeviceptr);
+typedef CUresult (*CtxGetCurrentFn)(CUcontext*);
+
+// Looked up once, whichever threads ask first.
 AddrRangeFn addr_range_fn() {
-    static AddrRangeFn fn = nullptr;
-    static bool tried = false;
-    if (!tried) {
-        void* p = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPointByVersion("cuMemGetAddressRange", &p, 12000, cudaEnableDefault, &q) == cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<AddrRangeFn>(p);
-        tried = true;
-    }
+    static const AddrRangeFn fn = driver_function<AddrRangeFn>("cuMemGetAddressRange");
+    return fn;
+}
+CtxGetCurrentFn ctx_get_current_fn() {
+    static const CtxGetCurrentFn fn = driver_function<CtxGetCurrentFn>("cuCtxGetCurrent");
     return fn;
 }
 
@@ -39,17 +47,7 @@ namespace uzip {
 // that needs one on: where this thread has none it gets its current device's.
 // Returns whether it got one here.
 bool bind_context() {
-    typedef CUresult (*CtxGetCurrentFn)(CUcontext*);
-    static const CtxGetCurrentFn get_current = [] {
-        void* p = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPointByVersion("cuCtxGetCurrent", &p, 12000, cudaEnableDefault, &q) != cudaSuccess ||
-            q != cudaDriverEntryPointSuccess) {
-            cudaGetLastError();
-            p = nullptr;
-        }
-        return reinterpret_cast<CtxGetCurrentFn>(p);
-    }();
+    const CtxGetCurrentFn get_current = ctx_get_current_fn();
     CUcontext ctx = nullptr;
     if (get_current && get_current(&ctx) == CUDA_SUCCESS && ctx) return false;
     int dev = 0;

@@ -5,12 +5,17 @@ Each call here is one that has nothing to do (no tokens, no sequences, no
 pairs), so that nothing is launched whatever becomes of it; it names an operand
 that its checks look at all the same.
 """
+import os
+import subprocess
+import sys
 import threading
 
 import pytest
 import torch
 
 pytestmark = pytest.mark.gpu
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 OK, BAD_ARG = 0, 1
 
@@ -81,3 +86,30 @@ def test_a_status_that_is_not_the_devices_is_refused(room, new_thread):
     for status in (torch.zeros(64, dtype=torch.int32).data_ptr(), 1 << 45):
         assert run(lambda: call(args, None, 0, status, 0)) == BAD_ARG
     assert run(lambda: call(args, None, 0, room.data_ptr(), 0)) == OK
+
+
+_AT_ONCE = """
+import threading, torch
+from tests.test_gpu_thread_checks import _calls
+room = torch.zeros(1 << 20, dtype=torch.uint8, device="cuda")
+call, args, field, far = _calls(room.data_ptr())["paged_attention"]
+setattr(args, field, far)
+torch.cuda.synchronize()
+gate, got = threading.Barrier(16), []
+def work():
+    gate.wait()
+    got.append(call(args, None, 0, None, 0))
+threads = [threading.Thread(target=work) for _ in range(16)]
+for t in threads:
+    t.start()
+for t in threads:
+    t.join(60)
+assert got == [1] * 16, got
+"""
+
+
+def test_the_first_calls_of_a_process_at_once():
+    """The driver's functions are looked up by whichever call is first: none goes by an address check that is not there yet."""
+    for _ in range(3):
+        done = subprocess.run([sys.executable, "-c", _AT_ONCE], cwd=ROOT, timeout=300, capture_output=True, text=True)
+        assert done.returncode == 0, done.stderr
