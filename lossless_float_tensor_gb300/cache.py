@@ -22,7 +22,7 @@ import math
 import struct
 
 from . import _check, library
-from .ops import _calls, _dtype_code, _on, _outside_autograd, _refuse
+from .ops import _calls, _dtype_code, _extras, _on, _outside_autograd, _refuse
 
 _i32, _i64, _u64, _vp, _f32 = ctypes.c_int32, ctypes.c_int64, ctypes.c_uint64, ctypes.c_void_p, ctypes.c_float
 
@@ -155,6 +155,8 @@ def _load():
 def _issue(entry, args, dev, workspace, status, check):
     """Runs an entry point on the current stream of device `dev`, the current one."""
     torch = _torch
+    if workspace is not None or status is not None:
+        _extras(workspace, status, dev)
     if workspace is None:
         need = entry.size(args)
         at = 0
@@ -162,14 +164,9 @@ def _issue(entry, args, dev, workspace, status, check):
             workspace = _empty((need,), (1,), torch.uint8)
             at = workspace.data_ptr()
     else:
-        if not workspace.is_contiguous():
-            _refuse("workspace: the values between those of a strided tensor are not its own")
         need, at = workspace.nbytes, workspace.data_ptr()
-    if status is None:
-        if check:
-            status = torch.empty((), dtype=torch.int32, device=dev)
-    elif status.dtype != torch.int32 or not status.numel():
-        _refuse(f"status: expected an int32 tensor, not {status.dtype} of {status.numel()} values")
+    if status is None and check:
+        status = torch.empty((), dtype=torch.int32, device=dev)
     st = entry.call(args, at, need, status.data_ptr() if status is not None else None, torch._C._cuda_getCurrentRawStream(dev))
     if st:
         _check(st, entry.name)

@@ -211,6 +211,23 @@ def _here(device, stream):
     return _on(device, stream)
 
 
+def _extras(workspace, status, index):
+    """What a call writes beside its outputs lies where it runs.  (Host memory
+    is the C entry point's to judge: what is mapped for the device will do.)"""
+    if workspace is not None:
+        if not workspace.is_contiguous():
+            _refuse("workspace: the values between those of a strided tensor are not its own")
+        if index != workspace.get_device() >= 0:
+            _refuse(f"workspace is on {workspace.device}, the call runs on cuda:{index}")
+    if status is not None:
+        import torch
+
+        if status.dtype != torch.int32 or not status.numel():
+            _refuse(f"status: expected an int32 tensor, not {status.dtype} of {status.numel()} values")
+        if index != status.get_device() >= 0:
+            _refuse(f"status is on {status.device}, the call runs on cuda:{index}")
+
+
 def _run(name, args, device, workspace, status, check):
     """Runs one entry point on the current stream."""
     import torch
@@ -218,16 +235,12 @@ def _run(name, args, device, workspace, status, check):
     size, call = _calls[name]
     ref = _byref(args)
     need = size(ref)
-    if workspace is None:
-        if need:
-            workspace = torch.empty(need, dtype=torch.uint8, device=device)
-    elif not workspace.is_contiguous():
-        _refuse("workspace: the values between those of a strided tensor are not its own")
-    if status is None:
-        if check:
-            status = torch.empty((), dtype=torch.int32, device=device)
-    elif status.dtype != torch.int32 or not status.numel():
-        _refuse(f"status: expected an int32 tensor, not {status.dtype} of {status.numel()} values")
+    if workspace is not None or status is not None:
+        _extras(workspace, status, device.index)
+    if workspace is None and need:
+        workspace = torch.empty(need, dtype=torch.uint8, device=device)
+    if status is None and check:
+        status = torch.empty((), dtype=torch.int32, device=device)
     _check(call(ref, workspace.data_ptr() if workspace is not None else None,
                 workspace.nbytes if workspace is not None else 0, status.data_ptr() if status is not None else None,
                 torch._C._cuda_getCurrentRawStream(device.index)), name)
