@@ -12,8 +12,8 @@ multiples of 8 with the last dimension contiguous; [layers, pages, ...] for
 cache_copy), and its state: refs int32 [pages], table int32 [sequences, width]
 and lengths int32 [sequences].  A new cache has zeros in all three.  Like the
 other torch functions here these are not known to autograd: rotary_backward is
-the gradient of rotary, and tensors that require gradients are refused while
-grad mode is on.
+the gradient of rotary.  Tensors that require gradients are refused while grad
+mode is on, and so are tensors with a tangent of forward-mode differentiation.
 """
 from __future__ import annotations
 
@@ -22,7 +22,7 @@ import math
 import struct
 
 from . import _check, library
-from .ops import _calls, _dtype_code, _extras, _on, _outside_autograd, _refuse
+from .ops import _calls, _dtype_code, _dual_level, _extras, _no_tangents, _on, _outside_autograd, _refuse
 
 _i32, _i64, _u64, _vp, _f32 = ctypes.c_int32, ctypes.c_int64, ctypes.c_uint64, ctypes.c_void_p, ctypes.c_float
 
@@ -264,6 +264,8 @@ def _rotary(q, k, positions, freqs, interleaved, backward, scale, out, status, c
     if _elsewhere(dev, stream):
         with _on(dev, stream):
             return _rotary(q, k, positions, freqs, interleaved, backward, scale, out, status, check, None)
+    if _dual_level() >= 0:
+        _no_tangents(q=q, k=k, freqs=freqs, **dict(zip(("out", "out's second"), out or ())))
     dt, code = like.dtype, _dtype_code(like)
     t, hq, d = like.shape
     hk = 0
@@ -325,6 +327,8 @@ def rotary_append(q, k, v, positions, freqs, k_pages, v_pages, slots, *, interle
         with _on(dev, stream):
             return rotary_append(q, k, v, positions, freqs, k_pages, v_pages, slots, interleaved=interleaved, scale=scale, out=out, status=status,
                                  check=check)
+    if _dual_level() >= 0:
+        _no_tangents(q=q, k=k, v=v, freqs=freqs, k_pages=k_pages, v_pages=v_pages, out=out)
     _device(k, "k", 3)
     dt, code = q.dtype, _dtype_code(q)
     t, hq, d = shape = q.shape
@@ -368,6 +372,8 @@ def paged_attention(q, k_pages, v_pages, table, lengths, *, scale=None, softcap=
         with _on(dev, stream):
             return paged_attention(q, k_pages, v_pages, table, lengths, scale=scale, softcap=softcap, window=window, with_lse=with_lse, out=out,
                                    workspace=workspace, status=status, check=check)
+    if _dual_level() >= 0:
+        _no_tangents(q=q, k_pages=k_pages, v_pages=v_pages, out=out)
     dt, code = q.dtype, _dtype_code(q)
     s, hq, d = shape = q.shape
     q_row, q_head, _ = _strides(q, "q", shape, dt, dev)
@@ -503,6 +509,8 @@ def cache_copy(k_pages, v_pages, pairs, *, to=None, status=None, check=False, st
     if _elsewhere(dev, stream):
         with _on(dev, stream):
             return cache_copy(k_pages, v_pages, pairs, to=to, status=status, check=check)
+    if _dual_level() >= 0:
+        _no_tangents(k_pages=k_pages, v_pages=v_pages, **dict(zip(("to", "to's second"), to or ())))
     dt, code = k_pages.dtype, _dtype_code(k_pages)
     shape = k_pages.shape
     layers, (pages, heads, page, d) = (shape[0], shape[1:]) if layered else (1, shape)

@@ -9,7 +9,8 @@ workspace and pass the stream.  All arithmetic runs in the library's kernels.
 The torch functions are not known to autograd: a training step calls the
 *_backward functions itself.  Tensors that require gradients are refused while
 grad mode is on, since the results would silently have none; torch.no_grad() or
-detach() says that this is meant.
+detach() says that this is meant.  So are tensors with a tangent of forward-mode
+differentiation; their primals are taken.
 """
 from __future__ import annotations
 
@@ -152,6 +153,26 @@ def _outside_autograd(t, name):
         _refuse(f"{name} requires gradients, which autograd would not get from here: detach it, or call under torch.no_grad()")
 
 
+@functools.cache
+def _forward_ad():
+    import torch.autograd.forward_ad
+
+    return torch.autograd.forward_ad
+
+
+def _dual_level() -> int:
+    """Below 0 outside of forward-mode differentiation, where no tensor has a
+    tangent (0 where torch does not say: then each is asked)."""
+    return getattr(_forward_ad(), "_current_level", 0)
+
+
+def _no_tangents(**tensors):
+    """Refuses dual tensors, which do not show in requires_grad."""
+    for name, t in tensors.items():
+        if t is not None and t.is_floating_point() and _forward_ad().unpack_dual(t).tangent is not None:
+            _refuse(f"{name} has a tangent, which forward-mode differentiation would not get from here: take its primal")
+
+
 def _matrix(t, name, shape, like):
     """Data pointer and row stride of a CUDA matrix (or batch of matrices)
     whose rows are contiguous."""
@@ -255,6 +276,8 @@ def _forward(name, x, w, offsets, bias, activation, residual, save_preact, out, 
 
     _operand(x, "x", 2)
     _operand(w, "w", 3 if offsets is not None else 2)
+    if _dual_level() >= 0:
+        _no_tangents(x=x, w=w, bias=bias, residual=residual, out=out)
     m, k = x.shape
     n = w.shape[-2]
     groups = 0 if offsets is None else w.shape[0]
@@ -290,6 +313,8 @@ def _backward(name, dy, x, w, offsets, preact, activation, need_dx, need_dw, nee
 
     _operand(x, "x", 2)
     _operand(w, "w", 3 if offsets is not None else 2)
+    if _dual_level() >= 0:
+        _no_tangents(dy=dy, x=x, w=w, preact=preact)
     m, k = x.shape
     n = w.shape[-2]
     groups = 0 if offsets is None else w.shape[0]
@@ -375,6 +400,8 @@ def cross_entropy(h, w, targets, *, ignore_index=-100, workspace=None, status=No
 
     _operand(h, "h", 2)
     _operand(w, "w", 2)
+    if _dual_level() >= 0:
+        _no_tangents(h=h, w=w)
     (t, d), v = h.shape, w.shape[0]
     dev = h.device
     a = CrossEntropyArgs(dtype=_dtype_code(h), t=t, v=v, d=d, ignore_index=ignore_index)
@@ -399,6 +426,8 @@ def cross_entropy_backward(dloss, h, w, targets, lse, *, ignore_index=-100, need
 
     _operand(h, "h", 2)
     _operand(w, "w", 2)
+    if _dual_level() >= 0:
+        _no_tangents(dloss=dloss, h=h, w=w, lse=lse)
     (t, d), v = h.shape, w.shape[0]
     dev = h.device
     a = CrossEntropyGradArgs(dtype=_dtype_code(h), t=t, v=v, d=d, piece=piece, ignore_index=ignore_index)
