@@ -141,15 +141,27 @@ _torch = _empty = None
 def _load():
     """torch, once it is needed, and _empty(shape, strides, dtype): a tensor on
     the current device.  torch's allocation without its dispatcher takes 3 us
-    less of 5 between other calls; where a version has it no more,
-    empty_strided does."""
+    less of 5 between other calls; it is torch's own, so where a version has it
+    no more, or it does not do this, empty_strided does."""
     global _torch, _empty
     import torch
 
-    _empty = getattr(getattr(getattr(torch._C, "_dynamo", None), "guards", None), "_empty_strided_cuda", None) or (
+    direct = getattr(getattr(getattr(torch._C, "_dynamo", None), "guards", None), "_empty_strided_cuda", None)
+    _empty = direct if direct is not None and _allocates(direct, torch) else (
         lambda shape, steps, dtype: torch.empty_strided(shape, steps, dtype=dtype, device="cuda"))
     _torch = torch
     return torch
+
+
+def _allocates(f, torch):
+    """Whether f(shape, strides, dtype) gives such a tensor on the current device."""
+    try:
+        dev = torch.cuda.current_device()  # (CUDA is set up from here on)
+        t = f((2, 3), (4, 1), torch.int16)
+        return (type(t) is torch.Tensor and t.shape == (2, 3) and t.stride() == (4, 1) and t.dtype is torch.int16 and t.get_device() == dev
+                and not t.requires_grad)
+    except Exception:  # noqa: BLE001  (whatever it takes now, it is not this)
+        return False
 
 
 def _issue(entry, args, dev, workspace, status, check):

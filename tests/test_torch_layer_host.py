@@ -64,3 +64,43 @@ def test_memory_of_this_device_and_of_the_host_is_passed_on(uz):
     for bad in ((t[::2], None), (None, t.long()), (None, t[:0])):
         with pytest.raises(uz.UzipError):
             ops._extras(*bad, 0)
+
+
+# ---- allocation ----------------------------------------------------------------
+
+def _as_it_is(shape, strides, dtype):
+    return torch.empty_strided(shape, strides, dtype=dtype)
+
+
+@pytest.mark.parametrize("change", [
+    None, lambda shape, strides, dtype, device: _as_it_is(shape, strides, dtype), lambda shape, dtype, strides: _as_it_is(shape, strides, dtype),
+    lambda *a: _as_it_is(a[0], (3, 1), a[2]), lambda *a: _as_it_is(*a[:2], torch.int32), lambda *a: None, lambda *a: 1 / 0,
+    lambda *a: _as_it_is(a[0], a[1], a[2])[:1], lambda *a: _There(_as_it_is(*a), 7),
+])
+def test_an_allocation_of_torchs_own_that_has_changed_is_not_used(uz, monkeypatch, change):
+    from lossless_float_tensor_gb300 import cache
+
+    guards = torch._C._dynamo.guards
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: -1)  # that of tensors without a GPU
+    for name in ("_torch", "_empty"):
+        monkeypatch.setattr(cache, name, None)
+    monkeypatch.setattr(guards, "_empty_strided_cuda", change, raising=False)
+    assert cache._load() is torch and cache._empty is not None and cache._empty is not change
+    monkeypatch.setattr(guards, "_empty_strided_cuda", _as_it_is, raising=False)
+    assert cache._load() is torch and cache._empty is _as_it_is
+
+
+@pytest.mark.gpu
+def test_results_without_torchs_own_allocation(uz, monkeypatch):
+    from lossless_float_tensor_gb300 import cache
+
+    g = torch.Generator(device="cuda").manual_seed(1)
+    q, k, v = (torch.randn(s, generator=g, device="cuda").to(torch.bfloat16) for s in ((3, 8, 64), (200, 2, 16, 64), (200, 2, 16, 64)))
+    table, lengths = torch.arange(180, dtype=torch.int32, device="cuda").view(3, 60), torch.tensor([900, 1, 300], dtype=torch.int32, device="cuda")
+    call = lambda: uz.paged_attention(q, k, v, table, lengths, with_lse=True, check=True)  # noqa: E731
+    want = call()
+    for name in ("_torch", "_empty"):
+        monkeypatch.setattr(cache, name, None)
+    monkeypatch.setattr(torch._C._dynamo.guards, "_empty_strided_cuda", None, raising=False)
+    got = call()
+    assert cache._empty is not None and all(torch.equal(a, b) for a, b in zip(got, want))
