@@ -197,3 +197,34 @@ def test_large_scores_and_values_in_fp16(uz):
         assert within(out, want.expand(1, 4, d), 2.0 ** -11 * want.abs() + 65504 * 1008 * 2.0 ** -23) <= 1.0
         score = 3.6e9 * d * scale
         assert float((lse.double() - score).abs().max()) <= 2.0 ** -20 * abs(score)
+
+
+# ---- sums over long contexts ----------------------------------------------------
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("lengths,group,d", [([131072], 8, 128), ([100003], 3, 64), ([40000, 7, 65536], 4, 80), ([20001], 32, 96), ([9999], 16, 256)])
+def test_long_sums_keep_32_bits(uz, lengths, group, d, dtype):
+    """Weights of 1, 1/2, 1/4 and 1/8 and values that are small whole numbers
+    of both signs: every product and every partial sum is a multiple of 1/8 (in
+    fp16 times 2^15) of at most 2^20, which 32 bits hold exactly, while the
+    result is what is left of them.  So it is off by its one rounding and by
+    what the weights are in sum: 2^-18, for the exponentials' 2^-22, the sum's
+    and the reciprocal's roundings."""
+    g = _gen(d)
+    page = 16
+    pages = sum(-(-n // page) for n in lengths) + 3
+    k, v = ref.pools(g, pages, 1, page, d, dtype)
+    table, n = ref.tables(lengths, page, pages)
+    v.copy_(torch.randint(-3, 4, v.shape, generator=g, device="cuda").to(dtype))
+    # each tile of 16 tokens has a token of the largest score: the maximum never moves, and no sum is scaled
+    k[:, 0, :, 3] = -torch.tensor([0, 1, 2, 3, 1, 0, 3, 2] * 2, device="cuda").to(dtype)
+    q = torch.zeros(len(lengths), group, d, dtype=dtype, device="cuda")
+    q[..., 3] = 1
+    out, lse = uz.paged_attention(q, k, v, table, n, scale=_f32(math.log(2)), with_lse=True, check=True)
+    for i, m in enumerate(lengths):
+        t = torch.arange(m, device="cuda")
+        at = table[i].long()[t // page]
+        w = 2.0 ** k[at, 0, t % page, 3].double()
+        want = (w[:, None] * v[at, 0, t % page].double()).sum(0) / w.sum()
+        assert within(out[i], want.expand(group, d), (ROUND[dtype] + 2.0 ** -18) * want.abs() + TINY[dtype]) <= 1.0
+        assert float((lse[i].double() - w.sum().log()).abs().max()) <= 2.0 ** -19 * (2 + math.log(m))

@@ -113,3 +113,75 @@ def test_the_first_calls_of_a_process_at_once():
     for _ in range(3):
         done = subprocess.run([sys.executable, "-c", _AT_ONCE], cwd=ROOT, timeout=300, capture_output=True, text=True)
         assert done.returncode == 0, done.stderr
+
+
+# ---- results ----------------------------------------------------------------------
+
+FIRST = ("linear", "grouped_linear", "linear_backward", "cross_entropy", "rotary", "rotary_append", "paged_attention", "cut_attention", "reserve", "fork", "free", "compact",
+         "copy", "compress")
+
+
+def _work(name, seed=1):
+    """(call, what it changes or gives) for an operator with everything allocated before."""
+    import lossless_float_tensor_gb300 as uz
+
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    rand = lambda *s: torch.randn(s, generator=g, device="cuda").to(torch.bfloat16)  # noqa: E731
+    i32 = lambda *v: torch.tensor(v, dtype=torch.int32, device="cuda")  # noqa: E731
+    x, w, offsets, targets = rand(4, 64), rand(32, 64), torch.tensor([0, 1, 4], device="cuda"), torch.tensor([0, 5, 31, 2], device="cuda")
+    q, k, pool, pool2 = rand(2, 4, 64), rand(2, 2, 64), rand(60, 2, 16, 64), rand(60, 2, 16, 64)
+    table, short, long = torch.arange(120, dtype=torch.int32, device="cuda").view(2, 60) % 60, i32(300, 3), i32(900, 3)
+    positions, slots, freqs = torch.tensor([5, 1000], device="cuda"), torch.tensor([77, 3], device="cuda"), uz.rotary_frequencies(64)
+    refs, rows, n = (torch.zeros(s, dtype=torch.int32, device="cuda") for s in (60, (3, 20), 3))
+    state = refs, rows, n
+    if name in ("fork", "free", "compact"):
+        uz.cache_reserve(*state, i32(40, 0, 50), 90, 16)
+    if name == "compact":
+        uz.cache_free(*state, i32(0), 16)
+    room, size, status = torch.zeros(1 << 22, dtype=torch.uint8, device="cuda"), torch.zeros((), dtype=torch.int64, device="cuda"), i32(9)
+    out, y, moves = torch.zeros(2, 4, 64, dtype=torch.bfloat16, device="cuda"), torch.zeros(4, 32, dtype=torch.bfloat16, device="cuda"), i32(*[[7, 7]] * 30)
+    listed = [torch.full((3,), 7, device="cuda"), torch.full((3,), 7, device="cuda"), i32(*[[7, 7]] * 3)]
+    pairs, counts, zero, one = i32([3, 9], [-1, -1], [4, 10]), i32(1, 1, 1), i32(0), i32(1)
+    kw = dict(status=status)
+    calls = {
+        "linear": (lambda: uz.linear(x, w, out=y, workspace=room, **kw), [y]),
+        "grouped_linear": (lambda: uz.grouped_linear(x, w.view(2, 16, 64), offsets, out=y[:, :16], workspace=room, **kw), [y]),
+        "linear_backward": (lambda: uz.linear_backward(y, x, w, workspace=room, **kw), []),
+        "cross_entropy": (lambda: uz.cross_entropy(x, w, targets, workspace=room, **kw), []),
+        "rotary": (lambda: uz.rotary(q, None, positions, freqs, out=(out, None), **kw), [out]),
+        "rotary_append": (lambda: uz.rotary_append(q, k, k + 0, positions, freqs, pool2, pool, slots, out=out, **kw), [out, pool, pool2]),
+        "paged_attention": (lambda: uz.paged_attention(q, pool, pool2, table[:, :20], short, out=out, **kw), [out]),
+        "cut_attention": (lambda: uz.paged_attention(q, pool, pool2, table, long, out=out, workspace=room, **kw), [out]),
+        "reserve": (lambda: uz.cache_reserve(*state, counts, 3, 16, out=listed, workspace=room, **kw), [*listed, *state]),
+        "fork": (lambda: uz.cache_fork(*state, zero, one, 16, workspace=room, **kw), [*state]),
+        "free": (lambda: uz.cache_free(*state, zero, 16, workspace=room, **kw), [*state]),
+        "compact": (lambda: uz.cache_compact(*state, 16, out=moves, workspace=room, **kw), [moves, *state]),
+        "copy": (lambda: uz.cache_copy(pool, pool2, pairs, **kw), [pool, pool2]),
+        "compress": (lambda: uz.compress(x, out=room, out_size=size), [size]),
+    }
+    y.copy_(rand(4, 32))
+    call, kept = calls[name]
+    return call, kept, status, (room, size)
+
+
+@pytest.mark.parametrize("name", FIRST)
+def test_results_of_a_threads_first_call(name):
+    """The same inputs in this thread and as the first call of a new one: the same bits of all that the call gives and changes."""
+    def run(where):
+        call, kept, status, (room, size) = _work(name)
+        before = [t.clone() for t in kept]
+        torch.cuda.synchronize()
+        got = where(call)
+        torch.cuda.synchronize()
+        given = [t for t in (got if isinstance(got, (list, tuple)) else [got]) if t is not None]
+        if name == "compress":
+            given = [room[: int(size)]]
+        else:
+            assert int(status) == 0
+            assert not kept or any(not torch.equal(a, b) for a, b in zip(before, kept))  # something was done
+        return given + kept
+
+    here, there = run(lambda f: f()), run(_in_a_thread)
+    assert len(here) == len(there) and here
+    for a, b in zip(here, there):
+        assert torch.equal(a.reshape(-1).view(torch.uint8), b.reshape(-1).view(torch.uint8))
