@@ -32,6 +32,7 @@
 // joins them, in the order of the tokens: the same bits each time.
 #include <algorithm>
 #include <atomic>
+#include <type_traits>
 
 #include "cache.cuh"
 
@@ -149,6 +150,14 @@ constexpr int kRowCost = 8;
 // tile.  37 sequences of 0 to 2777 tokens, 3 heads: 16.8 us with 16, 18.2 with 32.
 constexpr int kLeast = 16;
 static_assert(kLeast > kRowCost, "");
+
+// Tiles that a block adds up in one go.  The matrix instructions cut their 32-bit
+// additions toward zero, so a sum of one sign falls short by 6e-9 of itself for each
+// token of a warp (524288 tokens, a row for each block: results off by 8e-4, nearly
+// two of fp16's roundings); after 8192 tokens a warp (5e-5) a block's sums are
+// joined and rounded to nearest, as at a part's end.
+constexpr int kChunk = 2048;
+static_assert(kChunk % kWarps == 0, "a warp's tiles are the same whether a part is taken in chunks or not");
 
 // Where a warp is: tiles [j0, j1) of row `row` of sequence i, and its tile of
 // them.  `left` counts what the block has from the row's beginning on, kRowCost
@@ -274,7 +283,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<DP, NT>::kBlocks)) attention_
     constexpr int kRound = NT < 2 ? NT : 2;  // of 8 heads: those whose sums fit one stage
     static_assert(kRound * 8 * kOut * 4 <= int(S::kStage), "a warp's sums fit one stage");
     extern __shared__ __align__(128) uint8_t ring[];
-    __shared__ float2 stat[kWarps][kHeads];
+    __shared__ float2 stat[kWarps + 1][kHeads];  // the warps' maxima and sums, and those of the part's chunks before
     __shared__ uint32_t where[kWarps];
     wait_for_launch_before();
 
@@ -286,6 +295,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<DP, NT>::kBlocks)) attention_
     int64_t total = 0, blocks = 0;
     if (!first_part(a, ahead, total, blocks)) return;  // the whole block
     Place at = ahead;
+    int chunk = at.j0;  // where the part's next tiles to be added up begin
     bool more = true;  // `ahead` is at a tile (or at the end)
     ahead.tile = ahead.j0 + warp;
     auto settle = [&] {
@@ -418,7 +428,8 @@ __global__ void __launch_bounds__(kThreads, (Shape<DP, NT>::kBlocks)) attention_
         bool broken = at.s.bad;
         if (broken && a.status && threadIdx.x == 0) *a.status = UZIP_ERR_INVALID_ARG;
 
-        for (at.tile = at.j0 + warp; at.tile < at.j1; at.tile += kWarps) {
+        const int stop = min(at.j1, chunk + kChunk);
+        for (at.tile = chunk + warp; at.tile < stop; at.tile += kWarps) {
             fetch_wait<kStages - 2>();
             __syncwarp();
             if (more) {
@@ -517,58 +528,79 @@ __global__ void __launch_bounds__(kThreads, (Shape<DP, NT>::kBlocks)) attention_
             a.row_record[int64_t(at.i) * a.pairs + at.row] = make_int2(whole ? -1 : int(blockIdx.x), last);
         }
         if (lane == 0) where[warp] = (warp * kStages + refill) * S::kStage;
+        auto join_warps = [&](auto chunked) {
+            constexpr bool CHUNKED = decltype(chunked)::value;
+            // the sums of the chunks before lie where the part's will
+            if (CHUNKED && chunk > at.j0 && int(threadIdx.x) < heads) stat[kWarps][threadIdx.x] = a.part_ml[part * kHeads + threadIdx.x];
 #pragma unroll
-        for (int first = 0; first < NT; first += kRound) {
+            for (int first = 0; first < NT; first += kRound) {
 #pragma unroll
-            for (int n = 0; n < kRound; ++n) {
+                for (int n = 0; n < kRound; ++n) {
 #pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    float& sum = l[first + n][c];
+                    for (int c = 0; c < 2; ++c) {
+                        float& sum = l[first + n][c];
 #pragma unroll
-                    for (int x = 4; x < 32; x *= 2) sum += __shfl_xor_sync(~0u, sum, x);
-                    const int h = n * 8 + lane % 4 * 2 + c;
-                    if (lane < 4) stat[warp][first * 8 + h] = make_float2(m[first + n][c], broken ? NAN : sum);
-                    float* to = reinterpret_cast<float*>(ring + (warp * kStages + refill) * S::kStage) + h * kOut + lane / 4;
+                        for (int x = 4; x < 32; x *= 2) sum += __shfl_xor_sync(~0u, sum, x);
+                        const int h = n * 8 + lane % 4 * 2 + c;
+                        if (lane < 4) stat[warp][first * 8 + h] = make_float2(m[first + n][c], broken ? NAN : sum);
+                        float* to = reinterpret_cast<float*>(ring + (warp * kStages + refill) * S::kStage) + h * kOut + lane / 4;
 #pragma unroll
-                    for (int ks = 0; ks < kSteps; ++ks) to[ks * 16] = o[first + n][ks][c], to[ks * 16 + 8] = o[first + n][ks][c + 2];
+                        for (int ks = 0; ks < kSteps; ++ks) to[ks * 16] = o[first + n][ks][c], to[ks * 16 + 8] = o[first + n][ks][c + 2];
+                    }
                 }
+                __syncthreads();
+                const int here = min(8 * kRound, heads - first * 8);
+                for (int x = threadIdx.x; x < here * (DP / 4); x += kThreads) {  // four results each
+                    const int in = x / (DP / 4), e = x % (DP / 4) * 4, h = first * 8 + in;
+                    if (e >= a.d) continue;
+                    float top = -INFINITY, sum = 0.f;
+                    float4 val = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                    for (uint32_t w = 0; w < kWarps; ++w) top = fmaxf(top, stat[w][h].x);
+#pragma unroll
+                    for (uint32_t w = 0; w < kWarps; ++w) {
+                        const float by = weight(stat[w][h].x, top);
+                        const float4 v = *reinterpret_cast<const float4*>(ring + where[w] + (in * kOut + e) * 4);
+                        sum += stat[w][h].y * by;
+                        val.x += v.x * by, val.y += v.y * by, val.z += v.z * by, val.w += v.w * by;
+                    }
+                    float* const part_o = a.part_o + (part * kHeads + h) * a.d + e;
+                    if (CHUNKED && chunk > at.j0) {
+                        const float2 ml = stat[kWarps][h];
+                        const float4 v = *reinterpret_cast<const float4*>(part_o);
+                        const float now = fmaxf(top, ml.x), by = weight(top, now), by2 = weight(ml.x, now);
+                        top = now, sum = sum * by + ml.y * by2;
+                        val.x = val.x * by + v.x * by2, val.y = val.y * by + v.y * by2, val.z = val.z * by + v.z * by2, val.w = val.w * by + v.w * by2;
+                    }
+                    if (CHUNKED ? whole && stop == at.j1 : whole) {
+                        const bool none = at.s.len == 0 && !at.s.bad;
+                        const int hq = head0 + h;
+                        const float by = none ? 0.f : 1.f / sum;
+                        const uint2 r = none ? make_uint2(0, 0) : make_uint2(pack2<BF>(val.x * by, val.y * by), pack2<BF>(val.z * by, val.w * by));
+                        uint16_t* to = a.out + at.i * a.out_row + hq * a.out_head + e;
+                        if (a.out_quads)
+                            *reinterpret_cast<uint2*>(to) = r;
+                        else
+                            to[0] = uint16_t(r.x), to[1] = uint16_t(r.x >> 16), to[2] = uint16_t(r.y), to[3] = uint16_t(r.y >> 16);
+                        if (a.lse && e == 0)
+                            a.lse[int64_t(at.i) * a.q_heads + hq] = none ? -INFINITY : (top + (log2f(sum) - kLift<BF>)) * 0.6931471805599453f;
+                    } else {
+                        *reinterpret_cast<float4*>(part_o) = val;
+                        if (e == 0) a.part_ml[part * kHeads + h] = make_float2(top, sum);
+                    }
+                }
+                __syncthreads();
             }
-            __syncthreads();
-            const int here = min(8 * kRound, heads - first * 8);
-            for (int x = threadIdx.x; x < here * (DP / 4); x += kThreads) {  // four results each
-                const int in = x / (DP / 4), e = x % (DP / 4) * 4, h = first * 8 + in;
-                if (e >= a.d) continue;
-                float top = -INFINITY, sum = 0.f;
-                float4 val = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-                for (uint32_t w = 0; w < kWarps; ++w) top = fmaxf(top, stat[w][h].x);
-#pragma unroll
-                for (uint32_t w = 0; w < kWarps; ++w) {
-                    const float by = weight(stat[w][h].x, top);
-                    const float4 v = *reinterpret_cast<const float4*>(ring + where[w] + (in * kOut + e) * 4);
-                    sum += stat[w][h].y * by;
-                    val.x += v.x * by, val.y += v.y * by, val.z += v.z * by, val.w += v.w * by;
-                }
-                if (whole) {
-                    const bool none = at.s.len == 0 && !at.s.bad;
-                    const int hq = head0 + h;
-                    const float by = none ? 0.f : 1.f / sum;
-                    const uint2 r = none ? make_uint2(0, 0) : make_uint2(pack2<BF>(val.x * by, val.y * by), pack2<BF>(val.z * by, val.w * by));
-                    uint16_t* to = a.out + at.i * a.out_row + hq * a.out_head + e;
-                    if (a.out_quads)
-                        *reinterpret_cast<uint2*>(to) = r;
-                    else
-                        to[0] = uint16_t(r.x), to[1] = uint16_t(r.x >> 16), to[2] = uint16_t(r.y), to[3] = uint16_t(r.y >> 16);
-                    if (a.lse && e == 0)
-                        a.lse[int64_t(at.i) * a.q_heads + hq] = none ? -INFINITY : (top + (log2f(sum) - kLift<BF>)) * 0.6931471805599453f;
-                } else {
-                    *reinterpret_cast<float4*>(a.part_o + (part * kHeads + h) * a.d + e) = val;
-                    if (e == 0) a.part_ml[part * kHeads + h] = make_float2(top, sum);
-                }
-            }
-            __syncthreads();
-        }
-    } while (next_part(a, at));
+        };
+        if (chunk == at.j0 && stop == at.j1)
+            join_warps(std::false_type());
+        else
+            join_warps(std::true_type());
+        chunk = stop;
+        if (chunk < at.j1) continue;
+        if (!next_part(a, at)) break;
+        chunk = at.j0;
+    } while (true);
     fetch_wait<0>();
 }
 

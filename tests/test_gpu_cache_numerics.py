@@ -228,3 +228,70 @@ def test_long_sums_keep_32_bits(uz, lengths, group, d, dtype):
         want = (w[:, None] * v[at, 0, t % page].double()).sum(0) / w.sum()
         assert within(out[i], want.expand(group, d), (ROUND[dtype] + 2.0 ** -18) * want.abs() + TINY[dtype]) <= 1.0
         assert float((lse[i].double() - w.sum().log()).abs().max()) <= 2.0 ** -19 * (2 + math.log(m))
+
+
+def _rounds(lengths, page, pages):
+    """A table whose rows go round and round through the pool, each from another
+    page on, and how often each sequence has each of the pool's tokens."""
+    width = -(-max(lengths) // page)
+    starts = torch.arange(len(lengths)) * 5 % pages
+    table = ((starts[:, None] + torch.arange(width)) % pages).int().cuda()
+    n, all_ = torch.tensor(lengths)[:, None], pages * page
+    place = (torch.arange(all_)[None] - starts[:, None] * page) % all_  # of the pool's token in a round
+    return table, n[:, 0].int().cuda(), ((n - place + all_ - 1) // all_).clamp(min=0).double().cuda()
+
+
+# a warp's sum of 512 tiles by instructions that cut toward zero, each by less than 2^-23 of the sum so far, and as many
+# additions of two weights in 32 bits, then a few roundings: less than 2 * 2^-14 + 2^-16
+SUMS = 2.0 ** -12.5
+
+
+def _of_rounds(uz, lengths, group, d, dtype, page=16, pages=64, q_scale=2.0, positive=False):
+    g = _gen(d + group)
+    k, v = ref.pools(g, pages, 1, page, d, dtype)
+    if positive:
+        v.copy_((1 + torch.rand(v.shape, generator=g, device="cuda")).to(dtype))
+    table, n, often = _rounds(lengths, page, pages)
+    q = (torch.randn(len(lengths), group, d, generator=g, device="cuda") * q_scale).to(dtype)
+    out, lse = uz.paged_attention(q, k, v, table, n, with_lse=True, check=True)
+    kk, vv, qq = k.flatten(0, 2).double(), v.flatten(0, 2).double(), q.double()
+    z = qq @ kk.T * d ** -0.5
+    slip = (d + 4) * 2.0 ** -23 * d ** -0.5 * (qq.abs() @ kk.abs().T) + 2.0 ** -19 * z.abs()
+    z = z + often.log()[:, None]  # tokens that a sequence does not have: -inf
+    w, total = torch.softmax(z, -1), torch.logsumexp(z, -1)
+    worst = (w * slip).sum(-1, keepdim=True)
+    u, least = ROUND[dtype], 2.0 ** -40 if dtype == torch.float16 else 0.0
+    want = w @ vv
+    err = (w * (u + 1.1 * (slip + worst) + 2.0 ** -19 + SUMS)) @ vv.abs() + least * n[:, None, None] * vv.abs().max()
+    assert within(out, want, u * (want.abs() + err) + err + TINY[dtype]) <= 1.0
+    assert within(lse, total, 1.1 * worst[..., 0] + 2.0 ** -20 * (2 + total.abs()) + SUMS) <= 1.0
+    return q, k, v, table, n, out, lse, want
+
+
+# rows that a block takes more than 32768 tokens of: a row for each block, and rows that many blocks share
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("group,d", [(1, 64), (8, 128), (12, 128), (32, 128), (32, 64), (32, 96), (3, 192), (16, 256)])
+@pytest.mark.parametrize("lengths", [[32767, 32768, 32769, 32784, 65536, 65537, 98304, 99999, 5, 1] * 61, [30 * 10 ** 6], [10 ** 7, 3, 40 * 10 ** 5, 10 ** 7]])
+def test_rows_of_many_chunks(uz, lengths, group, d, dtype):
+    _of_rounds(uz, lengths, group, d, dtype)
+
+
+@pytest.mark.parametrize("group,d", [(1, 64), (8, 128), (32, 96)])
+def test_long_sums_of_one_sign_do_not_fall_short(uz, group, d):
+    """A row of 524288 tokens for each block, values between 1 and 2: the
+    results agree with 64 bits by the sums' bound and one rounding (the weights'
+    own roundings are at random here: 2^-11 over the root of some thousand)."""
+    *_, out, _, want = _of_rounds(uz, [524288] * 500, group, d, torch.float16, page=256, pages=64, q_scale=0.5, positive=True)
+    assert within(out, want, (ROUND[torch.float16] + SUMS) * want) <= 1.0
+
+
+def test_a_bad_page_of_an_early_chunk(uz):
+    q, k, v, table, n, out, lse, _ = _of_rounds(uz, [100000] * 500, 4, 64, torch.bfloat16)
+    status = torch.zeros((), dtype=torch.int32, device="cuda")
+    for col in (0, 2047, 2048, 6249):
+        t = table.clone()
+        t[250, col] = 64
+        got, got_lse = uz.paged_attention(q, k, v, t, n, with_lse=True, status=status)
+        assert int(status) == 1 and bool(got[250].isnan().all()) and bool(got_lse[250].isnan().all())
+        got[250], got_lse[250] = out[250], lse[250]
+        assert torch.equal(got, out) and torch.equal(got_lse, lse)
