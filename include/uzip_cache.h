@@ -46,8 +46,9 @@ extern "C" {
  * pairs, by the angle positions[i] * freqs[j] of token i and pair j, and
  * multiplied by `scale`; the others are copied.  Pair j is (j, j + rot / 2), or
  * (2 j, 2 j + 1) where `interleaved`.  Angles are reduced exactly in 64-bit
- * fixed point from the frequencies in fp64 (radians per position), so far
- * positions lose nothing; results are rounded once.  `backward` rotates by the
+ * fixed point from the frequencies in fp64 (radians per position): for
+ * frequencies up to a turn they are off by less than 2^-32 + |position| 2^-62 of
+ * a turn, so positions of any length of text lose nothing; results are rounded once.  `backward` rotates by the
  * opposite angle: the gradient of the rotation.
  *
  * q is [t, q_heads, d], k and v [t, kv_heads, d], each with any row and head

@@ -4,17 +4,19 @@
 // z_gt = scale q_g . k_t, p = softmax over t, o_g = sum_t p_gt v_t, in one pass
 // over the keys and values with a running maximum m and sum l:
 //   m' = max(m, z), l' = l 2^(m - m') + 2^(z - m'), o' = o 2^(m - m') + 2^(z - m') v.
-// Every key and value is read once and used for 4 operations a query head, 2 to 16
-// operations a byte: what bounds it is memory, and the work of a block is to keep
-// enough of it in flight.  128 sequences of 1024 to 12288 tokens, 8 x 4 heads of
-// 128 in bf16: 527 to 535 us, 6.6 TB/s of 6.79 that a copy reaches; 131072 tokens of
-// one sequence: 89.3 us, 6.0 TB/s, 8 us of it start, end and joining.  The products
-// still need matrix instructions (8 query heads would take 54 TFLOP/s of plain
-// ones); they run transposed, tokens or head values as the rows and query heads as
-// the 8 columns, so that heads that do not exist cost no rows: S^T = K Q^T and
-// O^T = V^T P^T by m16n8k16, which keeps the tensor pipe busy 9 % of the time.
-// tcgen05's rows of 128 tokens would want the tokens of eight tiles in one step,
-// with the barriers between their warps that this layout does without.
+// Every key and value is read once for up to 32 query heads that share it (16 where
+// heads have over 128 values), once more for each further 32.  A pair of them is 4
+// bytes and 4 operations a query head, so 1 to 32 operations a byte: what bounds it is
+// memory, and the work of a block is to keep enough of it in flight.  128 sequences of
+// 1024 to 12288 tokens, 8 x 4 heads of 128 in bf16: 519 to 533 us, 6.6 to 6.7 TB/s of
+// 6.79 that a copy reaches; 131072 tokens of one sequence: 88.7 us, 6.1 TB/s, 8 us of it
+// start, end and joining.  The products still need matrix instructions (8 query heads
+// would take 54 TFLOP/s of plain ones); they run transposed, tokens or head values as
+// the rows and query heads as the 8 columns, so that heads that do not exist cost no
+// rows: S^T = K Q^T and O^T = V^T P^T by m16n8k16, which keeps the tensor pipe busy 9 %
+// of the time.  tcgen05's rows of 128 tokens would want the tokens of eight tiles in one
+// step, two from each of four warps, with the barriers between them that this layout
+// does without.
 //
 // A warp takes tiles of 16 tokens, has a ring of shared memory of its own for
 // them (cp.async, 16 bytes a lane, rows 16 bytes apart from a multiple of 128 so
@@ -47,13 +49,14 @@ struct Shape {
     static constexpr uint32_t kPitch = DP * 2 + 16;         // bytes from token to token
     static constexpr uint32_t kStage = 2 * kTile * kPitch;  // keys, then values
     // blocks on an SM, with the stages that fit: 64 sequences of 16 to 4096 tokens, d = 128, take 92.0 us on three of
-    // two stages, 102.6 on two of three.  Where 32 query heads' sums take the registers: two
+    // two stages, 102.6 on two of three.  Where 32 query heads' sums take the registers: two; of up to 64 values they
+    // are left three, with 28 words spilled (two blocks there: not measured)
     static constexpr uint32_t kBlocks = NT == 4 && DP > 64 ? 2 : DP <= 128 ? 3 : DP <= 192 ? 2 : 1;
     // queries: in registers up to 32 of them a lane, else in shared memory, read again for each tile (64 sequences of
     // 2000 to 6000 tokens, 4 x 16 heads of 256: 221 us with spilled registers, 181)
     static constexpr bool kShared = NT * DP > 256;
     static constexpr uint32_t kQueries = kShared ? 8 * NT * kPitch : 0;
-    static constexpr uint32_t kRoom = 227 * 1024 / kBlocks - 2048 - kQueries;
+    static constexpr uint32_t kRoom = 227 * 1024 / kBlocks - 2560 - kQueries;  // 1 KB a block is the system's, 1.4 static
     static constexpr uint32_t kMost = kRoom / (kWarps * kStage);
     static constexpr uint32_t kStages = kMost < 8 ? kMost : 8;
     static constexpr uint32_t kSmem = kWarps * kStages * kStage + kQueries;
@@ -686,8 +689,16 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const __grid_constant__ 
     if (a.lse && e == 0) a.lse[int64_t(r.x) * a.q_heads + hq] = (s.top + (log2f(s.sum) - kLift<BF>)) * 0.6931471805599453f;
 }
 
+// Blocks on an SM, by head size and query heads kept, as Shape has them.
+constexpr int blocks_on_sm(int64_t d, uint32_t heads) {
+    if (d > 192) return 1;
+    if (d > 128) return 2;
+    return heads == 32 && d > 64 ? 2 : 3;
+}
+
 template <int DP, int NT, bool BF>
 cudaError_t launch_as(const Attention& a, const AttentionPlan& plan, cudaStream_t s) {
+    static_assert(blocks_on_sm(DP, 8 * NT) == int(Shape<DP, NT>::kBlocks), "the plan counts on the blocks that there are");
     auto kern = attention_kernel<DP, NT, BF>;
     static std::atomic<uint64_t> ready{0};  // devices on which the kernel may use its shared memory
     int dev = 0;
@@ -717,13 +728,6 @@ cudaError_t launch_wide(const Attention& a, int dtype, const AttentionPlan& plan
     if constexpr (DP <= 128)
         if (plan.heads == 32) return launch_typed<DP, 4>(a, dtype, plan, s);
     return launch_typed<DP, 2>(a, dtype, plan, s);
-}
-
-// Blocks on an SM, by head size and query heads kept, as Shape has them.
-int blocks_on_sm(int64_t d, uint32_t heads) {
-    if (d > 192) return 1;
-    if (d > 128) return 2;
-    return heads == 32 && d > 64 ? 2 : 3;
 }
 
 }  // namespace

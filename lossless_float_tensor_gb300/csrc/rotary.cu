@@ -6,7 +6,9 @@
 //
 // Angles are kept in turns, as 64-bit fractions: position * frequency is one
 // integer product modulo 2^64, which is the reduction modulo a full turn, exact
-// for any position; its upper 32 bits go to sincospi in 32 bits.  (In 32-bit
+// for any position (the frequency's fraction is cut to 2^-64, so an angle is off by
+// less than 2^-62 of a turn for each position); its upper 32 bits go to sincospi in
+// 32 bits.  (In 32-bit
 // floating point an angle of 10^6 radians would be off by 0.03.)
 //
 // A warp takes a token and a share of its heads: the cosines and sines of a token
